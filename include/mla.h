@@ -310,6 +310,133 @@ mla_status_t mla_extend_chunked(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe
                                 int chunk_tokens, void* workspace, size_t workspace_bytes, mla_bf16_t* out,
                                 float* lse, mla_stream_t stream);
 
+/* ---- The latent cache over a request's life: rotation with several position axes, the write
+ * of new rows, the attention weight of every cached token, and eviction by it. ---- */
+
+/* RoPE with several position axes (a token of an image or a video has a time, a height and a
+ * width): every one of the 32 adjacent pairs of a 64-value row turns by the position on its
+ * own axis,
+ *   out[n, h, 2j]     = x0 cos(a) - x1 sin(a)
+ *   out[n, h, 2j + 1] = x0 sin(a) + x1 cos(a),   x0, x1 = x[n, h, 2j], x[n, h, 2j + 1]
+ *   a = positions[axis_j][n] * rope_theta^(-2j/64),  j = 0..31
+ * (arithmetic and accuracy of mla_absorb_q_rope; one axis gives its result).  It serves q_pe --
+ * out is then q + 512 of the decode query, assembled by an absorption called without q_pe -- and
+ * the q_pe of mla_extend_chunked.
+ *  x, out      bf16, 16-byte aligned; x_row_stride / out_row_stride elements between tokens n,
+ *              x_head_stride / out_head_stride between heads h, all >= 0 and multiples of 8.  The
+ *              rows of out may not overlap one another (those of x may: 0 repeats a row).  out may
+ *              be x itself (same pointer and strides), and overlaps it in no other way
+ *  positions   int32 device, 4-byte aligned: axis a of token n at positions[a * positions_stride
+ *              + n], each in (-2^24, 2^24); positions_stride >= N
+ *  sections    [n_axes] int32 HOST: how many pairs each axis turns, each >= 0, their sum 32;
+ *              1 <= n_axes <= 4.  axis_j: the sections one after the other (interleaved = 0), or
+ *              dealt out pair by pair, axis 0 first, each axis for as long as its section lasts
+ *              (interleaved != 0)
+ *  rope_theta  finite and > 1
+ *  inverse     nonzero: turn by -a, the transpose: the gradient of x from that of out
+ * Async on stream. */
+mla_status_t mla_rope_axes(const mla_bf16_t* x, int64_t x_row_stride, int64_t x_head_stride, mla_bf16_t* out,
+                           int64_t out_row_stride, int64_t out_head_stride, const int32_t* positions,
+                           int64_t positions_stride, const int32_t* sections, int n_axes, int interleaved,
+                           float rope_theta, int inverse, int N, int H, mla_stream_t stream);
+
+/* New rows into the paged cache.  Row r of request b (of its new rows new_offsets[b] <= r <
+ * new_offsets[b + 1]) becomes the cached row of token t = seqlens[b] - (new_offsets[b + 1] - r):
+ *   kv_cache[block_table[b, t / 64], t % 64, :] = [c[r], k_pe[r] turned as in mla_rope_axes]
+ *  c, k_pe      [N, 512] and [N, 64] bf16, 16-byte aligned, c_row_stride / k_pe_row_stride
+ *               elements between rows (multiples of 8): two parts of one [N, 576] will do
+ *  kv_cache, num_blocks, block_table, max_blocks  as for mla_decode; only the entries of the new
+ *               tokens' pages are read, only the new tokens' rows written
+ *  seqlens      [B] int32 device: lengths that count the new rows, as in mla_decode
+ *  new_offsets  [B + 1] int32 device, non-decreasing, or NULL: N / B rows a request (N a multiple
+ *               of B).  Rows before new_offsets[0] and from new_offsets[B] on belong to no
+ *               request and are not used
+ *  positions    as for mla_rope_axes (with sections .. rope_theta), or NULL: k_pe is copied
+ * Two rows of one call must not go to the same cached row.  A row whose token or page is out of
+ * range is not written; it is reported as MLA_ERR_DEVICE_BOUNDS.  Async on stream. */
+mla_status_t mla_cache_append(const mla_bf16_t* c, int64_t c_row_stride, const mla_bf16_t* k_pe,
+                              int64_t k_pe_row_stride, mla_bf16_t* kv_cache, int64_t num_blocks,
+                              const int32_t* block_table, int max_blocks, const int32_t* seqlens,
+                              const int32_t* new_offsets, int N, int B, const int32_t* positions,
+                              int64_t positions_stride, const int32_t* sections, int n_axes, int interleaved,
+                              float rope_theta, mla_stream_t stream);
+
+/* mla_cache_append into an FP8 cache (as in mla_decode_fp8): each value is divided by kv_scale in
+ * float32 and rounded to E4M3, to nearest even, saturating at +-448 (infinities too; NaN stays
+ * NaN).  The turned k_pe goes from float32 to E4M3 without a rounding to bf16 between.
+ *  kv_scale  finite and > 0 */
+mla_status_t mla_cache_append_fp8(const mla_bf16_t* c, int64_t c_row_stride, const mla_bf16_t* k_pe,
+                                  int64_t k_pe_row_stride, uint8_t* kv_cache, float kv_scale, int64_t num_blocks,
+                                  const int32_t* block_table, int max_blocks, const int32_t* seqlens,
+                                  const int32_t* new_offsets, int N, int B, const int32_t* positions,
+                                  int64_t positions_stride, const int32_t* sections, int n_axes, int interleaved,
+                                  float rope_theta, mla_stream_t stream);
+
+/* The attention weight that a step gave every cached token, summed over its heads and query
+ * positions (all of them share one cached row) and added to what earlier steps left:
+ *     weights[b, t] += sum over i, h of exp(softmax_scale * <q[b,i,h,0:576], kv_t[0:576]> - lse[b,i,h]),
+ *                      for every t < seqlens[b], over the query positions i that see t
+ * with q and lse of an mla_decode over the same cache, table, lengths, scale and causal_s_q.
+ *  lse            [B, s_q, H] fp32; a row with lse = -inf gave no weight and adds nothing
+ *  weights        fp32 device, 4-byte aligned, weights_stride elements between requests
+ *                 (>= every seqlens[b]); elements from seqlens[b] on are neither read nor written
+ * Scores, exponentials and sums are in fp32; every weights[b, t] is summed in a fixed order, so
+ * that equal inputs give equal bits.  The rest as for mla_decode (no metadata, no workspace).
+ * A request with seqlens[b] outside [0, min(64 max_blocks, weights_stride)] or a page outside
+ * [0, num_blocks) is reported as MLA_ERR_DEVICE_BOUNDS (the tokens concerned add nothing).
+ * Async on stream. */
+mla_status_t mla_attn_weights(const mla_bf16_t* q, const float* lse, const mla_bf16_t* kv_cache, int64_t num_blocks,
+                              const int32_t* block_table, int max_blocks, const int32_t* seqlens, int B, int s_q, int H,
+                              float softmax_scale, int causal_s_q, float* weights, int64_t weights_stride,
+                              mla_stream_t stream);
+
+/* mla_attn_weights over an FP8 cache, as in mla_decode_fp8. */
+mla_status_t mla_attn_weights_fp8(const mla_bf16_t* q, const float* lse, const uint8_t* kv_cache, float kv_scale,
+                                  int64_t num_blocks, const int32_t* block_table, int max_blocks,
+                                  const int32_t* seqlens, int B, int s_q, int H, float softmax_scale, int causal_s_q,
+                                  float* weights, int64_t weights_stride, mla_stream_t stream);
+
+/* Eviction: of every request's n = seqlens[b] cached tokens, the m = min(n, budget) that matter
+ * most stay, in slots 0 .. m - 1 of its pages.  The order in which tokens matter:
+ *   1. guarded tokens: the request's first (arrival < sink) and its newest (arrival >= e - recent,
+ *      with e = 1 + the largest arrival number of its tokens);
+ *   2. larger weights[b, t] first (+0 and -0 are equal, NaN comes last);
+ *   3. of equals, the lower slot.
+ * A token that stays and lies below slot m does not move.  The slots below m that fall free, in
+ * ascending order, take the staying tokens from slot m on, in ascending order: attention without a
+ * causal mask does not depend on the order of the slots, and tokens that arrive later still come
+ * after all of these.
+ *  kv_cache       bf16 (mla_evict_fp8: one byte a value), changed in place; no other request of the
+ *                 call may use the same pages.  num_blocks, block_table, max_blocks as for mla_decode
+ *  seqlens        [B] int32 device, each in [0, min(64 max_blocks, weights_stride, and
+ *                 arrival_stride where arrival is given)]
+ *  weights        fp32 [B] rows of weights_stride elements (mla_attn_weights)
+ *  arrival        int32 [B] rows of arrival_stride elements: every slot's token's number in the
+ *                 order of the request's tokens, each in [0, 2^30); NULL: the slot itself
+ *  budget >= 1;  sink, recent >= 0 with sink + recent <= budget
+ *  new_seqlens    [B] int32: m.  May be seqlens
+ *  kept           int32 [B, width]: the slot (before the call) of the token that is now in slot
+ *                 j, -1 for j >= m
+ *  weights_out    fp32 [B, width]: the weights moved along, 0 for j >= m: what mla_attn_weights
+ *                 goes on adding to
+ *  arrival_out    int32 [B, width] or NULL: the numbers moved along; e + (j - m) for j >= m, the
+ *                 numbers of the tokens that mla_cache_append will put there
+ *  width          >= min(budget, 64 max_blocks, weights_stride)
+ * weights_out and arrival_out must not overlap weights or arrival.  At most 524288 slots a request:
+ * min(64 max_blocks, weights_stride) beyond that is MLA_ERR_UNSUPPORTED.  A request whose length
+ * is out of range is reported as MLA_ERR_DEVICE_BOUNDS and treated as empty; a row whose page is
+ * out of range is reported and not copied.  Two kernels on `stream`.  Async on stream. */
+mla_status_t mla_evict(mla_bf16_t* kv_cache, int64_t num_blocks, const int32_t* block_table, int max_blocks,
+                       const int32_t* seqlens, int B, const float* weights, int64_t weights_stride,
+                       const int32_t* arrival, int64_t arrival_stride, int budget, int sink, int recent,
+                       int32_t* new_seqlens, int32_t* kept, float* weights_out, int32_t* arrival_out, int64_t width,
+                       mla_stream_t stream);
+mla_status_t mla_evict_fp8(uint8_t* kv_cache, int64_t num_blocks, const int32_t* block_table, int max_blocks,
+                           const int32_t* seqlens, int B, const float* weights, int64_t weights_stride,
+                           const int32_t* arrival, int64_t arrival_stride, int budget, int sink, int recent,
+                           int32_t* new_seqlens, int32_t* kept, float* weights_out, int32_t* arrival_out, int64_t width,
+                           mla_stream_t stream);
+
 /* mla_decode without caller-provided scratch.  The paper has no counterpart:
  * this entry point exists for callers that cannot allocate device memory or pass
  * a workspace -- code inside an inference engine or plugin whose memory pool

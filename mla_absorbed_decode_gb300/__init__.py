@@ -18,6 +18,7 @@ __all__ = [
     "decode_workspace_size", "decode", "decode_sparse", "decode_fp8", "decode_sparse_fp8", "absorb_q", "unabsorb_o",
     "absorb_plan_max_batch", "absorb_q_plan",
     "bmm_fp8_workspace_size", "absorb_q_fp8", "absorb_q_fp8_plan", "unabsorb_o_fp8", "extend_workspace_size", "extend_chunked",
+    "rope_axes", "cache_append", "cache_append_fp8", "attn_weights", "attn_weights_fp8", "evict", "evict_fp8",
     "get_device_status",
     "schedule_params", "debug_withhold_first_load", "DecodeStep", "EXPORTED_SYMBOLS",
 ]
@@ -61,6 +62,20 @@ _SIGNATURES = {
                                     _p, _p, _p]),
     "mla_decode_noalloc": (_c_int, [_p, _p, _c_ll, _p, _c_int, _p, _c_int, _c_int, _c_int, _c_float, _c_int,
                                     _c_int, _p, _p, _p]),
+    "mla_rope_axes": (_c_int, [_p, _c_ll, _c_ll, _p, _c_ll, _c_ll, _p, _c_ll, _p, _c_int, _c_int, _c_float, _c_int,
+                               _c_int, _c_int, _p]),
+    "mla_cache_append": (_c_int, [_p, _c_ll, _p, _c_ll, _p, _c_ll, _p, _c_int, _p, _p, _c_int, _c_int, _p, _c_ll, _p,
+                                  _c_int, _c_int, _c_float, _p]),
+    "mla_cache_append_fp8": (_c_int, [_p, _c_ll, _p, _c_ll, _p, _c_float, _c_ll, _p, _c_int, _p, _p, _c_int, _c_int, _p,
+                                      _c_ll, _p, _c_int, _c_int, _c_float, _p]),
+    "mla_attn_weights": (_c_int, [_p, _p, _p, _c_ll, _p, _c_int, _p, _c_int, _c_int, _c_int, _c_float, _c_int, _p, _c_ll,
+                                  _p]),
+    "mla_attn_weights_fp8": (_c_int, [_p, _p, _p, _c_float, _c_ll, _p, _c_int, _p, _c_int, _c_int, _c_int, _c_float,
+                                      _c_int, _p, _c_ll, _p]),
+    "mla_evict": (_c_int, [_p, _c_ll, _p, _c_int, _p, _c_int, _p, _c_ll, _p, _c_ll, _c_int, _c_int, _c_int, _p, _p, _p,
+                           _p, _c_ll, _p]),
+    "mla_evict_fp8": (_c_int, [_p, _c_ll, _p, _c_int, _p, _c_int, _p, _c_ll, _p, _c_ll, _c_int, _c_int, _c_int, _p, _p,
+                               _p, _p, _c_ll, _p]),
     "mla_get_device_status": (_c_int, [_p]),
     "mla_debug_withhold_first_load": (None, [_c_int]),
 }
@@ -354,6 +369,236 @@ def extend_chunked(q_nope: torch.Tensor, q_pe: torch.Tensor, w_uk: torch.Tensor,
     return out, lse
 
 
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _typed(name: str, t: torch.Tensor, dtype: torch.dtype, dev: torch.device):
+    """The kernels read raw addresses: a tensor of another type or device must not reach them."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: {dtype} expected, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name}: on {t.device}, the call's tensors are on {dev}")
+
+
+def _paged(name: str, kv_cache: torch.Tensor, block_table: torch.Tensor, seqlens: torch.Tensor, fp8: bool):
+    """Checks a call's cache, table and lengths; returns (device, B)."""
+    dev = kv_cache.device
+    _need(dev.type == "cuda", f"{name}: kv_cache must be on a GPU")
+    if fp8:
+        if kv_cache.element_size() != 1:
+            raise TypeError(f"{name}: kv_cache must hold one byte per value (E4M3 codes)")
+    else:
+        _typed(f"{name}: kv_cache", kv_cache, torch.bfloat16, dev)
+    _need(kv_cache.dim() == 3 and kv_cache.shape[1:] == (64, 576) and kv_cache.is_contiguous(),
+          f"{name}: kv_cache must be a contiguous [num_blocks, 64, 576]")
+    _typed(f"{name}: block_table", block_table, torch.int32, dev)
+    _typed(f"{name}: seqlens", seqlens, torch.int32, dev)
+    _need(seqlens.dim() == 1 and seqlens.is_contiguous(), f"{name}: seqlens must be a contiguous [B]")
+    B = seqlens.shape[0]
+    _need(block_table.dim() == 2 and block_table.shape[0] == B and block_table.is_contiguous(),
+          f"{name}: block_table must be a contiguous [B, max_blocks]")
+    return dev, B
+
+
+def _rows(name: str, t: torch.Tensor, dtype: torch.dtype, dev: torch.device, B: int) -> int:
+    """Checks a [B, slots] tensor whose rows may be strided; returns the elements between rows, of
+    which a request may use as many as there are columns."""
+    _typed(name, t, dtype, dev)
+    _need(t.dim() == 2 and t.shape[0] == B and t.shape[1] >= 1 and (t.shape[1] == 1 or t.stride(1) == 1)
+          and (B == 1 or t.stride(0) >= t.shape[1]), f"{name}: [B, slots] with contiguous rows expected")
+    return t.stride(0) if B > 1 else t.shape[1]
+
+
+class _on:
+    """Makes a tensor's device current for a call (the library launches on the current device)."""
+    __slots__ = ("guard",)
+
+    def __init__(self, dev: torch.device):
+        self.guard = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _axes(name: str, positions: torch.Tensor, sections, N: int, dev: torch.device):
+    """Checks positions ([N], or [axes, N]) and sections; returns (pointer, stride, host sections, axes)."""
+    _typed(f"{name}: positions", positions, torch.int32, dev)
+    if positions.dim() == 1:
+        positions = positions[None]
+    sections = tuple(int(v) for v in sections)
+    _need(positions.dim() == 2 and positions.shape == (len(sections), N) and (N == 1 or positions.stride(1) == 1),
+          f"{name}: positions must be [axes, N] (or [N]) with as many axes as sections")
+    _need(1 <= len(sections) <= 4 and min(sections) >= 0 and sum(sections) == 32,
+          f"{name}: sections must be 1 to 4 counts of pairs that sum to 32")
+    stride = positions.stride(0) if len(sections) > 1 else N
+    return positions.data_ptr(), stride, (_c_int * len(sections))(*sections), len(sections)
+
+
+def _row_head(t: torch.Tensor) -> tuple[int, int]:
+    """Strides of [N, H, 64] (that of a dim of one element says nothing)."""
+    return t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0
+
+
+def rope_axes(x: torch.Tensor, positions: torch.Tensor, sections=(32,), out: torch.Tensor | None = None,
+              rope_theta: float = 10000.0, interleaved: bool = False, inverse: bool = False, stream=None) -> torch.Tensor:
+    """RoPE with several position axes: x [N, H, 64] bf16 (any strides that keep the last dim
+    contiguous), positions int32 [axes, N], sections = how many of the 32 adjacent pairs each axis
+    turns, one section after the other or (interleaved) dealt out in turn.  out may be x or a view such
+    as q[..., 512:] of the decode query.  inverse turns back: the gradient of x from that of out."""
+    dev = x.device
+    _need(dev.type == "cuda" and x.dim() == 3 and x.shape[2] == 64, "rope_axes: x must be [N, H, 64] on a GPU")
+    _typed("rope_axes: x", x, torch.bfloat16, dev)
+    N, H, _ = x.shape
+    if out is None:
+        out = torch.empty((N, H, 64), dtype=torch.bfloat16, device=dev)
+    _typed("rope_axes: out", out, torch.bfloat16, dev)
+    _need(out.shape == x.shape, "rope_axes: out must have x's shape")
+    _need(x.stride(2) == 1 and out.stride(2) == 1, "rope_axes: the 64 values of a row must be contiguous")
+    if N == 0 or H == 0:
+        return out
+    pos, pos_stride, sec, axes = _axes("rope_axes", positions, sections, N, dev)
+    with _on(dev):
+        _check(lib().mla_rope_axes(_ptr(x), *_row_head(x), _ptr(out), *_row_head(out), pos, pos_stride, sec, axes,
+                                   int(interleaved), float(rope_theta), int(inverse), N, H, _stream(stream)),
+               "mla_rope_axes")
+    return out
+
+
+def _append(name, c, k_pe, kv_cache, kv_scale, block_table, seqlens, new_offsets, positions, sections, rope_theta,
+            interleaved, stream):
+    dev, B = _paged(name, kv_cache, block_table, seqlens, kv_scale is not None)
+    _typed(f"{name}: c", c, torch.bfloat16, dev)
+    _typed(f"{name}: k_pe", k_pe, torch.bfloat16, dev)
+    N = c.shape[0]
+    _need(c.shape == (N, 512) and k_pe.shape == (N, 64) and c.stride(1) == 1 and k_pe.stride(1) == 1,
+          f"{name}: c [N, 512] and k_pe [N, 64] with contiguous rows expected")
+    off = None
+    if new_offsets is not None:
+        _typed(f"{name}: new_offsets", new_offsets, torch.int32, dev)
+        _need(new_offsets.shape == (B + 1,) and new_offsets.is_contiguous(), f"{name}: new_offsets must be [B + 1]")
+        off = _ptr(new_offsets)
+    if N == 0 or B == 0:
+        return kv_cache
+    rot = (None, 0, None, 0) if positions is None else _axes(name, positions, sections, N, dev)
+    scale = () if kv_scale is None else (float(kv_scale),)
+    with _on(dev):
+        _check(getattr(lib(), f"mla_{name}")(
+            _ptr(c), c.stride(0) if N > 1 else 512, _ptr(k_pe), k_pe.stride(0) if N > 1 else 64, _ptr(kv_cache), *scale,
+            kv_cache.shape[0], _ptr(block_table), block_table.shape[1], _ptr(seqlens), off, N, B, *rot, int(interleaved),
+            float(rope_theta), _stream(stream)), f"mla_{name}")
+    return kv_cache
+
+
+def cache_append(c, k_pe, kv_cache, block_table, seqlens, new_offsets=None, positions=None, sections=(32,),
+                 rope_theta: float = 10000.0, interleaved: bool = False, stream=None) -> torch.Tensor:
+    """A step's new rows [c, k_pe] (bf16 [N, 512] and [N, 64], rows may be strided) into the paged cache:
+    request b's rows are its last tokens, seqlens counts them already.  Rows are dealt to the requests
+    by new_offsets (int32 [B + 1]) or evenly.  With positions ([axes, N] or [N] int32) k_pe is turned
+    on the way, as in rope_axes.  Returns kv_cache."""
+    return _append("cache_append", c, k_pe, kv_cache, None, block_table, seqlens, new_offsets, positions, sections,
+                   rope_theta, interleaved, stream)
+
+
+def cache_append_fp8(c, k_pe, kv_cache, kv_scale: float, block_table, seqlens, new_offsets=None, positions=None,
+                     sections=(32,), rope_theta: float = 10000.0, interleaved: bool = False,
+                     stream=None) -> torch.Tensor:
+    """cache_append into an FP8 cache: E4M3 codes of value / kv_scale (round to nearest even, saturating)."""
+    return _append("cache_append_fp8", c, k_pe, kv_cache, kv_scale, block_table, seqlens, new_offsets, positions,
+                   sections, rope_theta, interleaved, stream)
+
+
+def _weights(name, q, lse, kv_cache, kv_scale, block_table, seqlens, softmax_scale, causal, weights, stream):
+    dev, B = _paged(name, kv_cache, block_table, seqlens, kv_scale is not None)
+    _typed(f"{name}: q", q, torch.bfloat16, dev)
+    _typed(f"{name}: lse", lse, torch.float32, dev)
+    _need(q.dim() == 4 and q.shape[0] == B and q.shape[3] == 576 and q.is_contiguous(),
+          f"{name}: q must be a contiguous [B, s_q, H, 576]")
+    _, s_q, H, _ = q.shape
+    _need(lse.shape == (B, s_q, H) and lse.is_contiguous(), f"{name}: lse must be a contiguous [B, s_q, H]")
+    stride = _rows(f"{name}: weights", weights, torch.float32, dev, B)
+    _need(stride == weights.shape[1] or weights.shape[1] >= 64 * block_table.shape[1],
+          f"{name}: rows of weights that are a part of wider ones must have a slot for every entry of block_table")
+    scale = () if kv_scale is None else (float(kv_scale),)
+    with _on(dev):
+        _check(getattr(lib(), f"mla_{name}")(
+            _ptr(q), _ptr(lse), _ptr(kv_cache), *scale, kv_cache.shape[0], _ptr(block_table), block_table.shape[1],
+            _ptr(seqlens), B, s_q, H, float(softmax_scale), int(causal), _ptr(weights), stride, _stream(stream)),
+            f"mla_{name}")
+    return weights
+
+
+def attn_weights(q, lse, kv_cache, block_table, seqlens, softmax_scale: float, causal: bool, weights,
+                 stream=None) -> torch.Tensor:
+    """weights[b, t] += the attention weight that the step's heads and query positions gave cached token
+    t (fp32 [B, slots], slots >= every length; q and lse as of decode).  Returns weights."""
+    return _weights("attn_weights", q, lse, kv_cache, None, block_table, seqlens, softmax_scale, causal, weights, stream)
+
+
+def attn_weights_fp8(q, lse, kv_cache, kv_scale: float, block_table, seqlens, softmax_scale: float, causal: bool,
+                     weights, stream=None) -> torch.Tensor:
+    """attn_weights over an FP8 cache (E4M3 codes scaled by kv_scale, as in decode_fp8)."""
+    return _weights("attn_weights_fp8", q, lse, kv_cache, kv_scale, block_table, seqlens, softmax_scale, causal, weights,
+                    stream)
+
+
+def _evict(name, fp8, kv_cache, block_table, seqlens, weights, budget, sink, recent, arrival, width, new_seqlens, kept,
+           weights_out, arrival_out, stream):
+    dev, B = _paged(name, kv_cache, block_table, seqlens, fp8)
+    w_stride = _rows(f"{name}: weights", weights, torch.float32, dev, B)
+    a_ptr, a_stride = None, 0
+    for t in (weights,) if arrival is None else (weights, arrival):
+        _need(B == 1 or t.stride(0) == t.shape[1] or t.shape[1] >= 64 * block_table.shape[1],
+              f"{name}: rows that are a part of wider ones must have a slot for every entry of block_table")
+    if arrival is not None:
+        a_stride = _rows(f"{name}: arrival", arrival, torch.int32, dev, B)
+        a_ptr = _ptr(arrival)
+    if width is None:
+        width = weights.shape[1]
+    outs = []
+    for what, t, dtype, shape in (("new_seqlens", new_seqlens, torch.int32, (B,)), ("kept", kept, torch.int32, (B, width)),
+                                  ("weights_out", weights_out, torch.float32, (B, width)),
+                                  ("arrival_out", arrival_out, torch.int32, (B, width))):
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=dev)
+        else:
+            _typed(f"{name}: {what}", t, dtype, dev)
+            _need(t.shape == shape and t.is_contiguous(), f"{name}: {what} must be a contiguous {list(shape)}")
+        outs.append(t)
+    with _on(dev):
+        _check(getattr(lib(), f"mla_{name}")(
+            _ptr(kv_cache), kv_cache.shape[0], _ptr(block_table), block_table.shape[1], _ptr(seqlens), B, _ptr(weights),
+            w_stride, a_ptr, a_stride, int(budget), int(sink), int(recent), *(_ptr(t) for t in outs), width,
+            _stream(stream)), f"mla_{name}")
+    return tuple(outs)
+
+
+def evict(kv_cache, block_table, seqlens, weights, budget: int, sink: int = 0, recent: int = 0, arrival=None,
+          width: int | None = None, new_seqlens=None, kept=None, weights_out=None, arrival_out=None, stream=None):
+    """Of every request's cached tokens the min(length, budget) of largest accumulated weight stay, its
+    first `sink` and newest `recent` ones (by arrival number; the slot without `arrival`) before all
+    others, ties to the lower slot; kv_cache is changed in place: slots that fall free below the new
+    length take the staying tokens from beyond it.  Returns (new_seqlens [B] int32 (may be seqlens),
+    kept [B, width] int32: the old slot of the token in each slot, weights_out, arrival_out [B, width]:
+    what belongs to the slots from now on, later tokens' included).  width: slots a request from now
+    on (default: as weights has)."""
+    return _evict("evict", False, kv_cache, block_table, seqlens, weights, budget, sink, recent, arrival, width,
+                  new_seqlens, kept, weights_out, arrival_out, stream)
+
+
+def evict_fp8(kv_cache, block_table, seqlens, weights, budget: int, sink: int = 0, recent: int = 0, arrival=None,
+              width: int | None = None, new_seqlens=None, kept=None, weights_out=None, arrival_out=None, stream=None):
+    """evict over an FP8 cache (one byte a value)."""
+    return _evict("evict_fp8", True, kv_cache, block_table, seqlens, weights, budget, sink, recent, arrival, width,
+                  new_seqlens, kept, weights_out, arrival_out, stream)
+
+
 def get_device_status(stream=None) -> int:
     """Synchronize the stream; return and clear the kernels' device status word."""
     return lib().mla_get_device_status(_stream(stream))
@@ -403,9 +648,27 @@ class DecodeStep:
         work()
         cur.wait_stream(self._plan_stream)
 
-    def absorb_and_plan(self, q_nope, q_pe, w_uk, positions=None, rope_theta: float = 10000.0, stream=None):
-        """The W_UK absorption and plan() in one launch (B <= absorb_plan_max_batch(); else the
+    def absorb(self, q_nope, q_pe, w_uk, positions=None, rope_theta: float = 10000.0, stream=None, sections=None,
+               interleaved: bool = False):
+        """The W_UK absorption and the rest of the decode query: q_pe as it is, rotated by positions
+        (int32 [B*s_q]) inside the absorption, or, with sections, by positions [axes, B*s_q] (rope_axes)."""
+        absorb_q(q_nope, w_uk, self.q, q_pe=None if sections is not None else q_pe, stream=stream,
+                 positions=None if sections is not None else positions, rope_theta=rope_theta)
+        self._rotate(q_pe, positions, rope_theta, sections, interleaved, stream)
+
+    def _rotate(self, q_pe, positions, rope_theta, sections, interleaved, stream=None):
+        if sections is not None:
+            rope_axes(q_pe, positions, sections, out=self.q.view(self.B * self.s_q, self.H, 576)[..., 512:],
+                      rope_theta=rope_theta, interleaved=interleaved, stream=stream)
+
+    def absorb_and_plan(self, q_nope, q_pe, w_uk, positions=None, rope_theta: float = 10000.0, stream=None,
+                        sections=None, interleaved: bool = False):
+        """absorb() with plan() in the absorption's launch (B <= absorb_plan_max_batch(); else the
         two calls, the schedule on a side stream beside the absorption)."""
+        if sections is not None:
+            self.absorb_and_plan(q_nope, None, w_uk, stream=stream)
+            self._rotate(q_pe, positions, rope_theta, sections, interleaved, stream)
+            return
         if self.B <= absorb_plan_max_batch():
             absorb_q_plan(q_nope, w_uk, self.q, self.seqlens, self.parts, self.metadata, q_pe=q_pe,
                           positions=positions, rope_theta=rope_theta, stream=stream)
@@ -421,32 +684,62 @@ class DecodeStep:
             decode_fp8(self.q, kv_cache, self.kv_scale, block_table, self.seqlens, self.scale, self.causal,
                        self.metadata, self.parts, workspace=self.workspace, out=self.out, lse=self.lse, stream=stream)
 
+    def append(self, c, k_pe, kv_cache, block_table, positions=None, rope_theta: float = 10000.0, sections=(32,),
+               interleaved: bool = False, stream=None):
+        """The step's new rows (c [B*s_q,512], k_pe [B*s_q,64]) into the cache as each request's last s_q
+        tokens (seqlens counts them), before `run`; k_pe rotated by positions where they are given."""
+        rot = dict(positions=positions, sections=sections, rope_theta=rope_theta, interleaved=interleaved, stream=stream)
+        if self.kv_scale is None:
+            cache_append(c, k_pe, kv_cache, block_table, self.seqlens, **rot)
+        else:
+            cache_append_fp8(c, k_pe, kv_cache, self.kv_scale, block_table, self.seqlens, **rot)
+
+    def accumulate_weights(self, kv_cache, block_table, weights, stream=None):
+        """Adds the attention weight of the step that `run` / `replay` has just done to weights [B, slots]."""
+        if self.kv_scale is None:
+            attn_weights(self.q, self.lse, kv_cache, block_table, self.seqlens, self.scale, self.causal, weights,
+                         stream=stream)
+        else:
+            attn_weights_fp8(self.q, self.lse, kv_cache, self.kv_scale, block_table, self.seqlens, self.scale,
+                             self.causal, weights, stream=stream)
+
+    def evict(self, kv_cache, block_table, weights, budget: int, sink: int = 0, recent: int = 0, arrival=None,
+              width: int | None = None, kept=None, weights_out=None, arrival_out=None, stream=None):
+        """Evicts down to `budget` tokens a request (see evict()); seqlens is changed in place and the schedule
+        recomputed.  Returns (kept, weights_out, arrival_out)."""
+        call = evict if self.kv_scale is None else evict_fp8
+        outs = call(kv_cache, block_table, self.seqlens, weights, budget, sink=sink, recent=recent, arrival=arrival,
+                    width=width, new_seqlens=self.seqlens, kept=kept, weights_out=weights_out, arrival_out=arrival_out,
+                    stream=stream)
+        self.plan(stream=stream)
+        return outs[1:]
+
     def run(self, q_nope, q_pe, w_uk, w_uv, kv_cache, block_table, stream=None, positions=None,
-            rope_theta: float = 10000.0):
+            rope_theta: float = 10000.0, sections=None, interleaved: bool = False):
         """q_nope [B*s_q,H,128], q_pe [B*s_q,H,64] -> o [B*s_q,H,128] (bf16); with positions
-        (int32 [B*s_q]) q_pe is RoPE-rotated inside the absorption."""
-        absorb_q(q_nope, w_uk, self.q, q_pe=q_pe, stream=stream, positions=positions, rope_theta=rope_theta)
+        (int32 [B*s_q]) q_pe is RoPE-rotated inside the absorption, with sections too by
+        positions [axes, B*s_q] (rope_axes)."""
+        self.absorb(q_nope, q_pe, w_uk, positions, rope_theta, stream, sections, interleaved)
         self._decode(kv_cache, block_table, stream=stream)
         unabsorb_o(self.out.view(self.B * self.s_q, self.H, 512), w_uv, o=self.o, stream=stream)
         return self.o
 
     def capture(self, q_nope, q_pe, w_uk, w_uv, kv_cache, block_table, plan=True, before=None, after=None,
-                positions=None, rope_theta: float = 10000.0):
+                positions=None, rope_theta: float = 10000.0, sections=None, interleaved: bool = False):
         """Record the step (plan() if `plan`, then run()) into a CUDA graph; `replay()` relaunches it
         with one host call.  `before` / `after` are optional callables whose stream work (for example
         copies of the step's inputs from pinned host buffers, or of its result back) is recorded in
         the same graph.  The graph holds the addresses of every buffer: refill them in place between
         replays.  The step runs once, uncaptured, first (one-time library set-up happens there)."""
-        def absorb():
-            absorb_q(q_nope, w_uk, self.q, q_pe=q_pe, positions=positions, rope_theta=rope_theta)
+        rot = dict(positions=positions, rope_theta=rope_theta, sections=sections, interleaved=interleaved)
 
         def body():
             if before is not None:
                 before()
             if plan:   # the schedule in the absorption's launch
-                self.absorb_and_plan(q_nope, q_pe, w_uk, positions=positions, rope_theta=rope_theta)
+                self.absorb_and_plan(q_nope, q_pe, w_uk, **rot)
             else:
-                absorb()
+                self.absorb(q_nope, q_pe, w_uk, **rot)
             self._decode(kv_cache, block_table)
             unabsorb_o(self.out.view(self.B * self.s_q, self.H, 512), w_uv, o=self.o)
             if after is not None:

@@ -16,6 +16,9 @@ checks), written for a reader to check against the pages by eye:
                     example with decoupled RoPE, the FP8 projections
                     (per-tensor input quantization, bmm_fp8), and the chunked
                     expanded extend (MHA_CHUNKED_KV: chunks merged by LSE).
+* ``cache.py``    -- the latent-cache operators: rotation with several position axes,
+                    the write of new rows, the attention weight of cached tokens,
+                    eviction by it.
 * ``schedule.py`` -- a restatement of the split-KV schedule rule and the
                     invariants any valid schedule must satisfy.
 
@@ -29,5 +32,8 @@ from .mla import (  # noqa: F401
     lse_merge, decode_bruteforce, tiny_full_mla, rope_interleaved,
     E4M3_MAX, e4m3_round, input_to_float8, bmm_fp8, absorb_q_fp8, assemble_q_fp8, unabsorb_o_fp8,
     expand_chunk, attend_chunk, extend_chunked_expanded,
+)
+from .cache import (  # noqa: F401
+    axis_of_pairs, rope_axes, append_slots, append_rows, attn_weights, evict,
 )
 from .schedule import schedule_reference, check_schedule  # noqa: F401
