@@ -4,9 +4,11 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 #include <stdint.h>
 
 #include <cmath>
+#include <mutex>
 
 #include "mla_kernels.h"
 #include "mla_ptx.cuh"
@@ -31,60 +33,590 @@ struct WeightsParams {
   int* status;
 };
 
-// One block per page and request; a warp takes 8 tokens of the page, lane l dims 18 l .. 18 l + 17.
+// A CTA holds one 128-row block of a request's queries (heads x query positions) in TMEM and streams
+// the cached pages past it: S = Q K^T on tcgen05 (TMEM accumulators), then for every row
+// p = exp2(S * scale - lse) and for every token the sum over the rows.  HBM-bound: a page is
+// 72 KiB (36 KiB in FP8) read once, against 9.4 MFLOP, a third of the tensor pipe's time for it.
+//  * Rows on the TMEM lanes, tokens on the columns: Q is loaded once per request, and the ring has the
+//    whole of shared memory for pages (221 KiB: what is in flight covers HBM latency).
+//  * The sum over the rows is a butterfly over the warp's lanes that halves the columns with every
+//    step (31 shuffles leave column l's sum in lane l), then four partial sums in shared memory: a
+//    fixed order, no atomics.
+//  * More than 128 rows: a cluster of ceil(rows / 128) CTAs walks the same pages, each with its row
+//    block; the others hand their 64 sums a page to CTA 0 through distributed shared memory.
+//  * Work: all requests' pages in a row, cut evenly over the clusters that fit the GPU.  Each CTA finds
+//    its own piece from the lengths (no schedule kernel, no metadata).
+constexpr int kWThreads = 320;                 // warp 0: TMA, warp 1: MMA, warps 2..9: epilogue
+constexpr int kEpiThreads = 256;
+constexpr int kSBufs = 3;                      // S accumulators in TMEM
+constexpr uint32_t kQCol = 0, kSCol0 = 320;    // TMEM columns: Q [0, 288), S at 320, 384, 448
+constexpr int kRecvSlots = 4;                  // cluster: pages of sums in flight towards CTA 0
+constexpr uint32_t kChunk = 8192;              // 64 rows x 128 bytes, 128-byte swizzle
+constexpr uint64_t kTimeoutNs = 500ull * 1000 * 1000;
+
 template <bool F8>
-__global__ void __launch_bounds__(256) mla_attn_weights_kernel(const WeightsParams p) {
+struct WCfg {
+  static constexpr uint32_t kKChunks = F8 ? 5 : 9;
+  static constexpr uint32_t kStageBytes = kKChunks * kChunk;    // a page (FP8: the RoPE codes zero-padded)
+  static constexpr int kStages = F8 ? 5 : 3;
+  static constexpr int kQItems = F8 ? 4 : 2;                    // a row block's q in ring items of kQRows rows
+  static constexpr int kQRows = 128 / kQItems;
+  static constexpr uint32_t kQItemBytes = static_cast<uint32_t>(kQRows) * kDimQK * 2;
+  static constexpr uint32_t kOffShared = kStages * kStageBytes;
+  static_assert(kQItemBytes <= kStageBytes && kQItems <= kStages, "a row block's q is resident at once");
+};
+
+struct WShared {
+  uint64_t full[5], empty[5];
+  uint64_t s_full[kSBufs], s_empty[kSBufs];
+  uint64_t q_full, drain;
+  uint64_t recv_full[kRecvSlots];              // CTA 0: the other CTAs' sums have arrived
+  uint64_t credit[kRecvSlots];                 // the other CTAs: CTA 0 has taken what was in the slot
+  uint32_t tmem_base;
+  volatile int abort;
+  int64_t scan[kWThreads / 32 + 1];
+  int64_t first_page, count;                   // this part's piece: page of request b0, pages
+  int b0;
+  float amax[2][128];                          // FP8: row maxima of the two halves of q
+  float part[2][4][kPageTokens];               // sums over the rows of one TMEM quadrant
+  float recv[kRecvSlots][kMaxPairsPerCluster - 1][kPageTokens];
+};
+template <bool F8>
+constexpr uint32_t weights_smem() { return WCfg<F8>::kOffShared + sizeof(WShared); }
+static_assert(weights_smem<false>() <= 232448 && weights_smem<true>() <= 232448, "shared memory per CTA");
+
+struct WMaps {
+  CUtensorMap kv;     // bf16: [chunk][row][64 dims], box 64 x 64 x 9; FP8: [chunk 0..3][row][128 codes], box 4 chunks
+  CUtensorMap rope;   // FP8: [row][576 codes], box 128 codes x 64 rows (read at code 512)
+  CUtensorMap q;      // [chunk 0..8][q row][64 dims], box kQRows rows
+};
+
+// ------------------------------------------------------------------ waits --
+__device__ __forceinline__ void w_abort(WShared& sh, int* status, uint32_t cl) {
+  atomicCAS(status, 0, MLA_ERR_TIMEOUT);
+  for (uint32_t r = 0; r < cl; ++r) st_cluster_u32(map_to_rank(smem_u32(const_cast<int*>(&sh.abort)), r), 1u);
+}
+__device__ __noinline__ bool w_wait_slow(WShared& sh, uint32_t bar, uint32_t parity, int* status, uint32_t cl) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_test_cluster(bar, parity)) {
+    if (sh.abort) return false;
+    if (global_timer_ns() - t0 > kTimeoutNs) {
+      w_abort(sh, status, cl);
+      return false;
+    }
+  }
+  return true;
+}
+// Bounded wait (0.5 s): false once this cluster has given up.
+__device__ __forceinline__ bool w_wait(WShared& sh, uint64_t& bar, uint32_t parity, int* status, uint32_t cl) {
+  const uint32_t a = smem_u32(&bar);
+  if (mbar_test_cluster(a, parity)) return true;
+  return w_wait_slow(sh, a, parity, status, cl);
+}
+__device__ __forceinline__ bool w_warp_wait(WShared& sh, uint64_t& bar, uint32_t parity, int* status, uint32_t cl) {
+  return __all_sync(0xffffffffu, w_wait(sh, bar, parity, status, cl));
+}
+__device__ __noinline__ void w_drain(uint64_t& bar, uint32_t parity) {   // ignores the abort flag
+  const uint32_t a = smem_u32(&bar);
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_test(a, parity))
+    if (global_timer_ns() - t0 > kTimeoutNs) return;
+}
+
+// --------------------------------------------------------------- the walk --
+__device__ __forceinline__ int length_of(const WeightsParams& p, int b) {   // 0 where it is out of range
+  const int n = __ldg(p.seqlens + b);
+  return n < 0 || n > p.slots ? 0 : n;
+}
+__device__ __forceinline__ int pages_of(int n) { return (n + kPageTokens - 1) / kPageTokens; }
+
+// The part's piece of the line of all requests' pages.  All threads of the CTA.
+__device__ void find_piece(const WeightsParams& p, WShared& sh, int part, int parts) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int each = (p.B + kWThreads - 1) / kWThreads;
+  const int b0 = min(p.B, tid * each), b1 = min(p.B, b0 + each);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int n = __ldg(p.seqlens + b);
+    if ((n < 0 || n > p.slots) && blockIdx.x == 0) atomicCAS(p.status, 0, MLA_ERR_DEVICE_BOUNDS);
+    mine += pages_of(length_of(p, b));
+  }
+  int64_t s = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
+  }
+  if (lane == 31) sh.scan[warp] = s;
+  if (tid == 0) sh.count = 0;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+  for (int w = 0; w < kWThreads / 32; ++w) {
+    if (w < warp) before += sh.scan[w];
+    total += sh.scan[w];
+  }
+  int64_t at = before + s - mine;
+  const int64_t lo = total * part / parts, hi = total * (part + 1) / parts;
+  if (lo < hi && lo >= at && lo < at + mine) {
+    int b = b0;
+    for (int nb; lo >= at + (nb = pages_of(length_of(p, b))); ++b) at += nb;
+    sh.b0 = b;
+    sh.first_page = lo - at;
+    sh.count = hi - lo;
+  }
+  __syncthreads();
+}
+
+struct WSegment {
+  int b, n, k0, k1;   // request, its length, pages [k0, k1)
+};
+struct WWalk {
+  int64_t left;
+  int b, page;
+  __device__ explicit WWalk(const WShared& sh) : left(sh.count), b(sh.b0), page(static_cast<int>(sh.first_page)) {}
+  __device__ bool next(const WeightsParams& p, WSegment& s) {
+    while (left > 0 && b < p.B) {
+      s.b = b++;
+      s.k0 = page;
+      page = 0;
+      s.n = length_of(p, s.b);
+      const int nb = pages_of(s.n);
+      if (s.k0 >= nb) continue;
+      s.k1 = left < nb - s.k0 ? s.k0 + static_cast<int>(left) : nb;
+      left -= s.k1 - s.k0;
+      return true;
+    }
+    return false;
+  }
+};
+
+__device__ __forceinline__ int block_of(const WeightsParams& p, int b, int k) {   // -1 where it is out of range
+  const int blk = __ldg(p.block_table + static_cast<int64_t>(b) * p.max_blocks + k);
+  return blk >= 0 && blk < p.num_blocks ? blk : -1;
+}
+
+// --------------------------------------------------------------- producer --
+template <bool F8>
+__device__ void w_producer(const WeightsParams& p, const WMaps& maps, WShared& sh, uint32_t smem, int rb, uint32_t cl) {
+  using C = WCfg<F8>;
+  WWalk walk(sh);
+  WSegment s;
+  uint32_t i = 0;
+  const uint64_t policy = l2_policy_evict_first();
+  bool ok = true;
+  auto stage_for = [&](uint32_t bytes, uint32_t* st) {   // a free ring stage that expects `bytes`
+    const uint32_t k = i % C::kStages;
+    if (!w_wait(sh, sh.empty[k], ((i / C::kStages) & 1) ^ 1, p.status, cl)) return false;
+    mbar_arrive_expect_tx(smem_u32(&sh.full[k]), bytes);
+    *st = k;
+    ++i;
+    return true;
+  };
+  uint32_t st = 0;
+  while (ok && walk.next(p, s)) {
+    for (int j = 0; j < C::kQItems && ok; ++j)
+      if ((ok = stage_for(C::kQItemBytes, &st)))
+        tma_load_3d(smem + st * C::kStageBytes, &maps.q, smem_u32(&sh.full[st]), 0,
+                    s.b * p.rows + rb * kRowsPerPair + C::kQRows * j, 0);
+    for (int k = s.k0; k < s.k1 && ok; ++k) {
+      int blk = block_of(p, s.b, k);
+      if (blk < 0) {   // reported; the box lies past the cache, so TMA fills it with zeros
+        atomicCAS(p.status, 0, MLA_ERR_DEVICE_BOUNDS);
+        blk = static_cast<int>(p.num_blocks);
+      }
+      if (!(ok = stage_for(C::kStageBytes, &st))) break;
+      const uint32_t dst = smem + st * C::kStageBytes, bar = smem_u32(&sh.full[st]);
+      tma_load_3d_hint(dst, &maps.kv, bar, 0, blk * kPageTokens, 0, policy);
+      if constexpr (F8) tma_load_2d_hint(dst + 4 * kChunk, &maps.rope, bar, kDimV, blk * kPageTokens, policy);
+    }
+  }
+  const uint32_t flying = i < C::kStages ? i : C::kStages;   // loads still in flight land before the CTA may exit
+  for (uint32_t j = i - flying; j < i; ++j) w_drain(sh.full[j % C::kStages], (j / C::kStages) & 1);
+}
+
+// -------------------------------------------------------------------- MMA --
+template <bool F8>
+__device__ void w_mma(const WeightsParams& p, WShared& sh, uint32_t smem, uint32_t cl) {
+  using C = WCfg<F8>;
+  constexpr uint32_t idesc = F8 ? idesc_e4m3_f32(128, 64, 0, 0) : idesc_bf16_f32(128, 64, 0, 0);
+  const uint32_t tmem = sh.tmem_base;
+  WWalk walk(sh);
+  WSegment s;
+  uint32_t i = 0, T = 0, seg = 0;
+  bool ok = true;
+  while (ok && walk.next(p, s)) {
+    i += C::kQItems;   // taken by the epilogue warps
+    if (!(ok = w_warp_wait(sh, sh.q_full, seg++ & 1, p.status, cl))) break;
+    for (int k = s.k0; k < s.k1; ++k, ++i, ++T) {
+      const uint32_t st = i % C::kStages, sb = T % kSBufs;
+      ok = w_warp_wait(sh, sh.s_empty[sb], ((T / kSBufs) & 1) ^ 1, p.status, cl) &&
+           w_warp_wait(sh, sh.full[st], (i / C::kStages) & 1, p.status, cl);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t stage = smem + st * C::kStageBytes, d = tmem + kSCol0 + sb * kPageTokens;
+      if constexpr (F8) {
+        // chunks of 128 codes, K = 32 a step; Q = hi (columns 0..143) + lo (144..287)
+#pragma unroll
+        for (int c = 0; c < 5; ++c)
+#pragma unroll
+          for (int j = 0; j < (c < 4 ? 4 : 2); ++j) {
+            const uint64_t kd = smem_desc_sw128(stage + c * kChunk + j * 32, 16, 1024);
+            mma_f8_ts_warp(d, tmem + kQCol + c * 32 + j * 8, kd, idesc, (c | j) ? 1u : 0u);
+            mma_f8_ts_warp(d, tmem + kQCol + 144 + c * 32 + j * 8, kd, idesc, 1u);
+          }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 9; ++c)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma_bf16_ts_warp(d, tmem + kQCol + c * 32 + j * 8, smem_desc_sw128(stage + c * kChunk + j * 32, 16, 1024),
+                             idesc, (c | j) ? 1u : 0u);
+      }
+      mma_commit_warp(smem_u32(&sh.empty[st]));
+      mma_commit_warp(smem_u32(&sh.s_full[sb]));
+    }
+  }
+  if (T > 0) {   // no MMA is in flight when the CTA frees its TMEM
+    mma_commit_warp(smem_u32(&sh.drain));
+    w_drain(sh.drain, 0);
+  }
+  __syncwarp();
+}
+
+// --------------------------------------------------------------- epilogue --
+// Row r's half `half` of q (288 values) into TMEM, two bf16 values a column.  `row`: the row's first
+// 128 bytes in its ring item (chunks of chunk_bytes, 16-byte units swizzled by the row).
+__device__ __forceinline__ void q_to_tmem(uint32_t row, uint32_t chunk_bytes, uint32_t lane_base, int half, int rl) {
+#pragma unroll
+  for (int c = 0; c < 9; ++c) {
+    uint32_t v[16];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int u = half * 36 + c * 4 + j;
+      const uint4 x = ld_shared_v4(row + (u >> 3) * chunk_bytes + (((u & 7) ^ (rl & 7)) << 4));
+      v[4 * j] = x.x, v[4 * j + 1] = x.y, v[4 * j + 2] = x.z, v[4 * j + 3] = x.w;
+    }
+    tmem_st16(lane_base + kQCol + half * 144 + c * 16, v);
+  }
+}
+
+// The same as two E4M3 terms, four values a column: with sc the power of two that brings the row's
+// largest magnitude into (224, 448], hi = e4m3(q sc) and lo = e4m3(q sc - hi).  A bf16 value has 8
+// significant bits, 4 of which hi holds and 4 lo, so hi + lo = q sc for values down to 2^-2 after
+// scaling and within 2^-10 below.  Returns 1 / sc.
+__device__ __forceinline__ float q_to_tmem_f8(uint32_t row, uint32_t chunk_bytes, uint32_t lane_base, int half, int rl,
+                                              float* mine, const float* other) {
+  auto unit = [&](int u) { return ld_shared_v4(row + (u >> 3) * chunk_bytes + (((u & 7) ^ (rl & 7)) << 4)); };
+  float top = 0.f;
+#pragma unroll 4
+  for (int j = 0; j < 36; ++j) {
+    const uint4 x = unit(half * 36 + j);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
+  }
+  *mine = top;
+  named_bar_sync(1, kEpiThreads);
+  top = fmaxf(top, *other);
+  const float t = top > 0.f ? fminf(448.f / top, 0x1p100f) : 1.f;
+  const float sc = __uint_as_float(__float_as_uint(t) & 0x7F800000u);
+#pragma unroll 1
+  for (int c = 0; c < 9; ++c) {
+    uint32_t hi[8], lo[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint4 x = unit(half * 36 + c * 4 + j);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float v0 = bf16_lo(w[2 * e]) * sc, v1 = bf16_hi(w[2 * e]) * sc;
+        const float v2 = bf16_lo(w[2 * e + 1]) * sc, v3 = bf16_hi(w[2 * e + 1]) * sc;
+        const uint32_t h01 = cvt_e4m3x2(v0, v1), h23 = cvt_e4m3x2(v2, v3);
+        const float2 f01 = e4m3x2_to_float2(h01), f23 = e4m3x2_to_float2(h23);
+        hi[2 * j + e] = h01 | (h23 << 16);
+        lo[2 * j + e] = cvt_e4m3x2(v0 - f01.x, v1 - f01.y) | (cvt_e4m3x2(v2 - f23.x, v3 - f23.y) << 16);
+      }
+    }
+    tmem_st8(lane_base + kQCol + 72 * half + c * 8, hi);
+    tmem_st8(lane_base + kQCol + 144 + 72 * half + c * 8, lo);
+  }
+  return 1.f / sc;
+}
+
+// Sums over the warp's lanes: lane l gets that of v[l].  Each step exchanges half of the columns a
+// lane still has with the lane `o` away, in a fixed order.
+__device__ __forceinline__ float sum_columns(float (&v)[32], int lane) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int c = 0; c < o; ++c) {
+      const float keep = up ? v[c + o] : v[c], give = up ? v[c] : v[c + o];
+      v[c] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  }
+  return v[0];
+}
+
+// Warps 2..9.  Warp quadrant q (TMEM lanes 32 q .. 32 q + 31: the rows), half `half` of the page's columns.
+template <bool F8>
+__device__ void w_epilogue(const WeightsParams& p, WShared& sh, uint32_t smem, int rb, uint32_t cl, uint32_t rank) {
+  using C = WCfg<F8>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quad = warp & 3, half = (warp - 2) >> 2;
+  const int r = quad * 32 + lane;                    // row of the block == TMEM lane
+  const int g = rb * kRowsPerPair + r;               // row of the request: i * H + h
+  const uint32_t lane_base = sh.tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+  const int cb = half * 32;
+  WWalk walk(sh);
+  WSegment s;
+  uint32_t i = 0, T = 0;
+  bool ok = true, stop = false;
+  while (!stop && walk.next(p, s)) {
+    // rows past the request's, and rows that gave no weight, see nothing
+    int vis = 0;
+    float c_hi = 0.f, c_lo = 0.f, scale_hi = p.scale_hi, scale_lo = p.scale_lo;
+    if (g < p.rows) {
+      const float lse = __ldg(p.lse + static_cast<int64_t>(s.b) * p.rows + g);
+      if (lse != -INFINITY) {
+        vis = p.causal ? s.n - p.s_q + g / p.H + 1 : s.n;
+        // -lse * log2(e) as a float pair, so that the exponent's rounding is relative to itself
+        constexpr float kL2eHi = 1.4426950216293335f, kL2eLo = 1.9259629911266175e-8f;
+        c_hi = -lse * kL2eHi;
+        if (isfinite(lse)) c_lo = fmaf(-lse, kL2eLo, fmaf(-lse, kL2eHi, -c_hi));
+      }
+    }
+    {   // Q into TMEM: every MMA of the request before is complete (its last S has been waited for)
+      const uint32_t item = i + static_cast<uint32_t>(r / C::kQRows);
+      const bool got = w_wait(sh, sh.full[item % C::kStages], (item / C::kStages) & 1, p.status, cl);
+      if (named_bar_or(1, kEpiThreads, !got || !ok)) break;
+      const int rl = r % C::kQRows;
+      const uint32_t row = smem + (item % C::kStages) * C::kStageBytes + rl * 128;
+      if constexpr (F8) {
+        const float inv = q_to_tmem_f8(row, C::kQRows * 128, lane_base, half, rl, &sh.amax[half][r], &sh.amax[half ^ 1][r]);
+        scale_hi *= inv;   // a power of two: exact
+        scale_lo *= inv;
+      } else {
+        q_to_tmem(row, C::kQRows * 128, lane_base, half, rl);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      named_bar_sync(1, kEpiThreads);
+      if (threadIdx.x == 64) {
+        mbar_arrive(smem_u32(&sh.q_full));
+        for (uint32_t j = 0; j < C::kQItems; ++j) mbar_arrive(smem_u32(&sh.empty[(i + j) % C::kStages]));
+      }
+      i += C::kQItems + static_cast<uint32_t>(s.k1 - s.k0);
+    }
+    for (int k = s.k0; k < s.k1; ++k, ++T) {
+      const uint32_t sb = T % kSBufs, buf = T & 1;
+      const bool mine = static_cast<uint32_t>(quad) == (T & 3);   // this warp adds the page's sums up
+      const int t = k * kPageTokens + cb + lane;
+      float* const w = p.weights + s.b * p.weights_stride + t;
+      float old = 0.f;
+      bool store = false;
+      if (mine && rank == 0) {
+        store = t < s.n && block_of(p, s.b, k) >= 0;
+        if (store) old = *w;
+      }
+      ok = w_wait(sh, sh.s_full[sb], (T / kSBufs) & 1, p.status, cl) && ok;
+      tc_fence_after();
+      float v[32];
+      tmem_ld32(lane_base + kSCol0 + sb * kPageTokens + cb, *reinterpret_cast<uint32_t(*)[32]>(v));
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.s_empty[sb]));
+      const int seen = vis - (k * kPageTokens + cb);   // columns c < seen are visible to this row
+#pragma unroll
+      for (int c = 0; c < 32; ++c) v[c] = fast_exp2(fmaf(v[c], scale_hi, c_hi) + fmaf(v[c], scale_lo, c_lo));
+      if (seen < 32) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) v[c] = c < seen ? v[c] : 0.f;
+      }
+      sh.part[buf][quad][cb + lane] = sum_columns(v, lane);
+      if (named_bar_or(1, kEpiThreads, !ok)) {
+        stop = true;
+        break;
+      }
+      // the next write to part[buf] comes after the next page's barrier, which this warp reaches after its reads
+      if (!mine) continue;
+      float sum = (sh.part[buf][0][cb + lane] + sh.part[buf][1][cb + lane]) +
+                  (sh.part[buf][2][cb + lane] + sh.part[buf][3][cb + lane]);
+      if (cl > 1) {
+        const uint32_t slot = T % kRecvSlots, ph = (T / kRecvSlots) & 1;
+        if (rank != 0) {
+          ok = w_warp_wait(sh, sh.credit[slot], ph ^ 1, p.status, cl) && ok;
+          if (ok) {
+            st_cluster_u32(map_to_rank(smem_u32(&sh.recv[slot][rank - 1][cb + lane]), 0), __float_as_uint(sum));
+            mbar_arrive_remote(map_to_rank(smem_u32(&sh.recv_full[slot]), 0));   // releases this lane's store
+          }
+        } else {
+          ok = w_warp_wait(sh, sh.recv_full[slot], ph, p.status, cl) && ok;
+          for (uint32_t o = 1; o < cl; ++o) sum += sh.recv[slot][o - 1][cb + lane];
+          __syncwarp();
+          if (ok && lane > 0 && static_cast<uint32_t>(lane) < cl)
+            mbar_arrive_remote(map_to_rank(smem_u32(&sh.credit[slot]), lane));
+          store = store && ok;
+        }
+      }
+      if (store) *w = old + sum;
+    }
+  }
+}
+
+template <bool F8>
+__global__ void __launch_bounds__(kWThreads, 1)
+mla_attn_weights_kernel(const __grid_constant__ WMaps maps, const __grid_constant__ WeightsParams p) {
+  using C = WCfg<F8>;
+  extern __shared__ __align__(1024) uint8_t dyn_smem[];
+  const uint32_t smem = smem_u32(dyn_smem);
+  if (smem & 1023u) {   // the swizzled layout needs it (no static shared memory is declared); every CTA alike
+    if (threadIdx.x == 0) atomicCAS(p.status, 0, MLA_ERR_UNSUPPORTED);
+    return;
+  }
+  WShared& sh = *reinterpret_cast<WShared*>(dyn_smem + C::kOffShared);
+  const int warp = threadIdx.x >> 5;
+  const uint32_t cl = static_cast<uint32_t>((p.rows + kRowsPerPair - 1) / kRowsPerPair);
+  const uint32_t rank = cl > 1 ? cluster_ctarank() : 0;
+  if (threadIdx.x == 0) {
+    prefetch_tensormap(&maps.kv);
+    prefetch_tensormap(&maps.q);
+    if (F8) prefetch_tensormap(&maps.rope);
+    sh.abort = 0;
+    for (int j = 0; j < C::kStages; ++j) {
+      mbar_init(smem_u32(&sh.full[j]), 1);
+      mbar_init(smem_u32(&sh.empty[j]), 1);
+    }
+    for (int j = 0; j < kSBufs; ++j) {
+      mbar_init(smem_u32(&sh.s_full[j]), 1);
+      mbar_init(smem_u32(&sh.s_empty[j]), kEpiThreads / 32);
+    }
+    mbar_init(smem_u32(&sh.q_full), 1);
+    mbar_init(smem_u32(&sh.drain), 1);
+    for (int j = 0; j < kRecvSlots; ++j) {
+      mbar_init(smem_u32(&sh.recv_full[j]), cl > 1 ? kPageTokens * (cl - 1) : 1);   // every lane of two warps a CTA
+      mbar_init(smem_u32(&sh.credit[j]), 2);                                       // two warps of CTA 0
+    }
+    fence_mbar_init();
+  }
+  __syncwarp();
+  if (warp == 0) tmem_alloc(smem_u32(&sh.tmem_base), 512);
+  tc_fence_before();
+  __syncthreads();
+  if (cl > 1) cluster_sync();   // every barrier of the cluster is initialised before any remote use
+  tc_fence_after();
   griddep_wait();
   griddep_launch_dependents();
-  const int b = blockIdx.y, page = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n = __ldg(p.seqlens + b);
-  if (n < 0 || n > p.slots) {
-    if (page == 0 && threadIdx.x == 0) atomicCAS(p.status, 0, MLA_ERR_DEVICE_BOUNDS);
-    return;
+  find_piece(p, sh, static_cast<int>(blockIdx.x / cl), static_cast<int>(gridDim.x / cl));
+  if (warp == 0) {
+    if ((threadIdx.x & 31) == 0) w_producer<F8>(p, maps, sh, smem, static_cast<int>(rank), cl);
+  } else if (warp == 1) {
+    w_mma<F8>(p, sh, smem, cl);
+  } else {
+    w_epilogue<F8>(p, sh, smem, static_cast<int>(rank), cl, rank);
   }
-  if (page * kPageTokens >= n) return;
-  const int blk = __ldg(p.block_table + static_cast<int64_t>(b) * p.max_blocks + page);
-  if (blk < 0 || blk >= p.num_blocks) {
-    if (threadIdx.x == 0) atomicCAS(p.status, 0, MLA_ERR_DEVICE_BOUNDS);
-    return;
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (cl > 1) cluster_sync();   // no CTA leaves while another may still touch its shared memory
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(sh.tmem_base, 512);
   }
-  for (int i = warp; i < kPageTokens; i += 8) {
-    const int t = page * kPageTokens + i;
-    if (t >= n) break;
-    const int64_t at = (static_cast<int64_t>(blk) * kPageTokens + i) * kDimQK + lane * 18;
-    float k[18];
-#pragma unroll
-    for (int d = 0; d < 9; ++d) {
-      if constexpr (F8) {
-        const uint32_t v = *reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(p.kv) + at + 2 * d);
-        const float2 f = e4m3x2_to_float2(v);
-        k[2 * d] = f.x, k[2 * d + 1] = f.y;
-      } else {
-        const uint32_t v = *reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.kv) + at + 2 * d);
-        k[2 * d] = bf16_lo(v), k[2 * d + 1] = bf16_hi(v);
+}
+
+// ------------------------------------------------------------------- host --
+constexpr int kMaxDevices = 64;
+struct WeightsDevice {
+  bool ready = false;
+  int clusters[2][kMaxPairsPerCluster + 1] = {};   // [fp8][CTAs of a cluster]: how many fit the GPU
+};
+WeightsDevice g_dev[kMaxDevices];
+std::mutex g_mutex;
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+
+const void* weights_kernel(bool fp8) {
+  return fp8 ? reinterpret_cast<const void*>(mla_attn_weights_kernel<true>)
+             : reinterpret_cast<const void*>(mla_attn_weights_kernel<false>);
+}
+cudaLaunchConfig_t weights_config(bool fp8, int clusters, int cl, cudaStream_t stream, cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg = pdl_config(dim3(static_cast<unsigned>(clusters * cl)), dim3(kWThreads),
+                                      fp8 ? weights_smem<true>() : weights_smem<false>(), stream, attr);
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cl);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.numAttrs = cl > 1 ? 2 : 1;
+  return cfg;
+}
+
+// Once per device, with that device current: kernel attributes and how many clusters fit.
+mla_status_t weights_setup(WeightsDevice** out) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MLA_ERR_CUDA;
+  std::lock_guard<std::mutex> lock(g_mutex);
+  WeightsDevice& d = g_dev[dev];
+  if (!d.ready) {
+    if (!g_encode) {
+      cudaDriverEntryPointQueryResult q;
+      void* fn = nullptr;
+      if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+          q != cudaDriverEntryPointSuccess || fn == nullptr)
+        return MLA_ERR_CUDA;
+      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    }
+    int sms = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return MLA_ERR_CUDA;
+    for (int f = 0; f < 2; ++f) {
+      if (cudaFuncSetAttribute(weights_kernel(f), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(f ? weights_smem<true>() : weights_smem<false>())) != cudaSuccess)
+        return MLA_ERR_CUDA;
+      d.clusters[f][1] = sms;
+      for (int cl = 2; cl <= kMaxPairsPerCluster; ++cl) {
+        cudaLaunchAttribute attr[2];
+        const cudaLaunchConfig_t cfg = weights_config(f, 1, cl, nullptr, attr);
+        cudaLaunchConfig_t query = cfg;
+        query.attrs = attr + 1;
+        query.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&d.clusters[f][cl], weights_kernel(f), &query) != cudaSuccess ||
+            d.clusters[f][cl] < 1) {
+          cudaGetLastError();
+          return MLA_ERR_CUDA;
+        }
       }
     }
-    float sum = 0.f;
-    for (int g = 0; g < p.rows; ++g) {
-      if (p.causal && t >= n - p.s_q + g / p.H + 1) continue;
-      const int64_t row = static_cast<int64_t>(b) * p.rows + g;
-      const float lse = __ldg(p.lse + row);
-      if (lse == -INFINITY) continue;
-      const uint32_t* q = reinterpret_cast<const uint32_t*>(p.q + row * kDimQK + lane * 18);
-      float s = 0.f;
-#pragma unroll
-      for (int d = 0; d < 9; ++d) {
-        const uint32_t v = __ldg(q + d);
-        s = fmaf(bf16_lo(v), k[2 * d], s);
-        s = fmaf(bf16_hi(v), k[2 * d + 1], s);
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      constexpr float kLog2e = 1.4426950408889634f;
-      sum += fast_exp2(fmaf(s, p.scale_hi, fmaf(s, p.scale_lo, -lse * kLog2e)));
-    }
-    if (lane == 0) p.weights[b * p.weights_stride + t] += sum;
+    d.ready = true;
   }
+  *out = &d;
+  return MLA_OK;
+}
+
+template <bool F8>
+bool encode_maps(WMaps* m, const void* kv, int64_t num_blocks, const void* q, int64_t q_rows) {
+  using C = WCfg<F8>;
+  const cuuint32_t es[3] = {1, 1, 1};
+  auto encode = [&](CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,
+                    const cuuint64_t* strides, const cuuint32_t* box) {
+    return g_encode(map, type, rank, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  const cuuint64_t rows = static_cast<cuuint64_t>(num_blocks) * kPageTokens;
+  bool ok;
+  if (F8) {
+    const cuuint64_t dims[3] = {128, rows, 4}, strides[2] = {kDimQK, 128}, rdims[2] = {kDimQK, rows}, rstrides[1] = {kDimQK};
+    const cuuint32_t box[3] = {128, kPageTokens, 4}, rbox[2] = {128, kPageTokens};
+    ok = encode(&m->kv, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, kv, dims, strides, box) &&
+         encode(&m->rope, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, kv, rdims, rstrides, rbox);
+  } else {
+    const cuuint64_t dims[3] = {64, rows, 9}, strides[2] = {kDimQK * 2, 128};
+    const cuuint32_t box[3] = {64, kPageTokens, 9};
+    ok = encode(&m->kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, kv, dims, strides, box);
+  }
+  const cuuint64_t qdims[3] = {64, static_cast<cuuint64_t>(q_rows), 9}, qstrides[2] = {kDimQK * 2, 128};
+  const cuuint32_t qbox[3] = {64, static_cast<cuuint32_t>(C::kQRows), 9};
+  return ok && encode(&m->q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, qdims, qstrides, qbox);
 }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -125,13 +657,23 @@ mla_status_t weights_impl(const mla_bf16_t* q, const float* lse, const void* kv_
   p.weights = weights;
   p.weights_stride = weights_stride;
   p.status = device_status_word();
+  WeightsDevice* d = nullptr;
   if (!p.status) return MLA_ERR_CUDA;
-  cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg =
-      pdl_config(dim3(static_cast<unsigned>((p.slots + kPageTokens - 1) / kPageTokens), static_cast<unsigned>(B)), dim3(256),
-                 0, reinterpret_cast<cudaStream_t>(stream), attr);
-  const cudaError_t e = fp8 ? cudaLaunchKernelEx(&cfg, mla_attn_weights_kernel<true>, p)
-                            : cudaLaunchKernelEx(&cfg, mla_attn_weights_kernel<false>, p);
+  const mla_status_t st = weights_setup(&d);
+  if (st != MLA_OK) return st;
+  WMaps maps = {};
+  const int64_t q_rows = static_cast<int64_t>(B) * p.rows;
+  if (!(fp8 ? encode_maps<true>(&maps, kv_cache, num_blocks, q, q_rows)
+            : encode_maps<false>(&maps, kv_cache, num_blocks, q, q_rows)))
+    return MLA_ERR_CUDA;
+  const int cl = (p.rows + kRowsPerPair - 1) / kRowsPerPair;
+  // no more clusters than pages there can be
+  const int64_t most = static_cast<int64_t>(B) * ((p.slots + kPageTokens - 1) / kPageTokens);
+  const int clusters = static_cast<int>(most < d->clusters[fp8][cl] ? most : d->clusters[fp8][cl]);
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = weights_config(fp8, clusters, cl, reinterpret_cast<cudaStream_t>(stream), attr);
+  const cudaError_t e = fp8 ? cudaLaunchKernelEx(&cfg, mla_attn_weights_kernel<true>, maps, p)
+                            : cudaLaunchKernelEx(&cfg, mla_attn_weights_kernel<false>, maps, p);
   return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
