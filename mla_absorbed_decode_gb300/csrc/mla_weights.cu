@@ -40,15 +40,16 @@ struct WeightsParams {
 //  * Rows on the TMEM lanes, tokens on the columns: Q is loaded once per request, and the ring has the
 //    whole of shared memory for pages (221 KiB: what is in flight covers HBM latency).
 //  * The sum over the rows is a butterfly over the warp's lanes that halves the columns with every
-//    step (31 shuffles leave column l's sum in lane l), then four partial sums in shared memory: a
-//    fixed order, no atomics.
+//    step (31 shuffles leave column l's sum in lane l), then four partial sums in shared memory, which
+//    a warp of its own adds to the weights: a fixed order, no atomics.
 //  * More than 128 rows: a cluster of ceil(rows / 128) CTAs walks the same pages, each with its row
 //    block; the others hand their 64 sums a page to CTA 0 through distributed shared memory.
-//  * Work: all requests' pages in a row, cut evenly over the clusters that fit the GPU.  Each CTA finds
-//    its own piece from the lengths (no schedule kernel, no metadata).
-constexpr int kWThreads = 320;                 // warp 0: TMA, warp 1: MMA, warps 2..9: epilogue
-constexpr int kEpiThreads = 256;
+//  * Work: all requests' pages in a row, with kSwitchPages for each request's start, cut evenly over the
+//    clusters that fit the GPU.  Each CTA finds its own piece from the lengths (no schedule, no metadata).
+constexpr int kWThreads = 352;                 // warp 0: TMA, 1: MMA, 2..9: exponentials, 10: sums
+constexpr int kEpiWarps = 8;
 constexpr int kSBufs = 3;                      // S accumulators in TMEM
+constexpr int kPartBufs = 4;                   // pages of partial sums between the epilogue and the sum warp
 constexpr uint32_t kQCol = 0, kSCol0 = 320;    // TMEM columns: Q [0, 288), S at 320, 384, 448
 constexpr int kRecvSlots = 4;                  // cluster: pages of sums in flight towards CTA 0
 constexpr uint32_t kChunk = 8192;              // 64 rows x 128 bytes, 128-byte swizzle
@@ -62,6 +63,8 @@ struct WCfg {
   static constexpr int kQItems = F8 ? 4 : 2;                    // a row block's q in ring items of kQRows rows
   static constexpr int kQRows = 128 / kQItems;
   static constexpr uint32_t kQItemBytes = static_cast<uint32_t>(kQRows) * kDimQK * 2;
+  // what a switch of requests costs (Q's load and its way into TMEM), in pages: the split charges it
+  static constexpr int kSwitchPages = F8 ? 3 : 2;
   static constexpr uint32_t kOffShared = kStages * kStageBytes;
   static_assert(kQItemBytes <= kStageBytes && kQItems <= kStages, "a row block's q is resident at once");
 };
@@ -69,16 +72,17 @@ struct WCfg {
 struct WShared {
   uint64_t full[5], empty[5];
   uint64_t s_full[kSBufs], s_empty[kSBufs];
-  uint64_t q_full, drain;
+  uint64_t part_full[kPartBufs], part_empty[kPartBufs];
+  uint64_t amax_full, q_full, drain;
   uint64_t recv_full[kRecvSlots];              // CTA 0: the other CTAs' sums have arrived
   uint64_t credit[kRecvSlots];                 // the other CTAs: CTA 0 has taken what was in the slot
   uint32_t tmem_base;
   volatile int abort;
   int64_t scan[kWThreads / 32 + 1];
-  int64_t first_page, count;                   // this part's piece: page of request b0, pages
+  int64_t offset, count;                       // this part's piece: from `offset` positions into request b0 on
   int b0;
   float amax[2][128];                          // FP8: row maxima of the two halves of q
-  float part[2][4][kPageTokens];               // sums over the rows of one TMEM quadrant
+  float part[kPartBufs][4][kPageTokens];       // sums over the rows of one TMEM quadrant
   float recv[kRecvSlots][kMaxPairsPerCluster - 1][kPageTokens];
 };
 template <bool F8>
@@ -130,8 +134,14 @@ __device__ __forceinline__ int length_of(const WeightsParams& p, int b) {   // 0
 }
 __device__ __forceinline__ int pages_of(int n) { return (n + kPageTokens - 1) / kPageTokens; }
 
-// The part's piece of the line of all requests' pages.  All threads of the CTA.
+// All requests lie on a line, each with kSwitch positions for its start and one for each of its pages; the
+// line is cut evenly.  This finds the part's piece.  All threads of the CTA.
+template <int kSwitch>
 __device__ void find_piece(const WeightsParams& p, WShared& sh, int part, int parts) {
+  auto length_on_line = [&](int b) {
+    const int nb = pages_of(length_of(p, b));
+    return nb ? nb + kSwitch : 0;
+  };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int each = (p.B + kWThreads - 1) / kWThreads;
   const int b0 = min(p.B, tid * each), b1 = min(p.B, b0 + each);
@@ -139,7 +149,7 @@ __device__ void find_piece(const WeightsParams& p, WShared& sh, int part, int pa
   for (int b = b0; b < b1; ++b) {
     const int n = __ldg(p.seqlens + b);
     if ((n < 0 || n > p.slots) && blockIdx.x == 0) atomicCAS(p.status, 0, MLA_ERR_DEVICE_BOUNDS);
-    mine += pages_of(length_of(p, b));
+    mine += length_on_line(b);
   }
   int64_t s = mine;
 #pragma unroll
@@ -159,9 +169,9 @@ __device__ void find_piece(const WeightsParams& p, WShared& sh, int part, int pa
   const int64_t lo = total * part / parts, hi = total * (part + 1) / parts;
   if (lo < hi && lo >= at && lo < at + mine) {
     int b = b0;
-    for (int nb; lo >= at + (nb = pages_of(length_of(p, b))); ++b) at += nb;
+    for (int on; lo >= at + (on = length_on_line(b)); ++b) at += on;
     sh.b0 = b;
-    sh.first_page = lo - at;
+    sh.offset = lo - at;
     sh.count = hi - lo;
   }
   __syncthreads();
@@ -170,21 +180,23 @@ __device__ void find_piece(const WeightsParams& p, WShared& sh, int part, int pa
 struct WSegment {
   int b, n, k0, k1;   // request, its length, pages [k0, k1)
 };
+template <int kSwitch>
 struct WWalk {
-  int64_t left;
-  int b, page;
-  __device__ explicit WWalk(const WShared& sh) : left(sh.count), b(sh.b0), page(static_cast<int>(sh.first_page)) {}
+  int64_t left;     // positions of the piece still to walk
+  int b, offset;    // from `offset` positions into request b on
+  __device__ explicit WWalk(const WShared& sh) : left(sh.count), b(sh.b0), offset(static_cast<int>(sh.offset)) {}
   __device__ bool next(const WeightsParams& p, WSegment& s) {
     while (left > 0 && b < p.B) {
       s.b = b++;
-      s.k0 = page;
-      page = 0;
       s.n = length_of(p, s.b);
-      const int nb = pages_of(s.n);
-      if (s.k0 >= nb) continue;
-      s.k1 = left < nb - s.k0 ? s.k0 + static_cast<int>(left) : nb;
-      left -= s.k1 - s.k0;
-      return true;
+      const int nb = pages_of(s.n), from = offset;
+      if (nb == 0) continue;
+      offset = 0;
+      const int64_t take = left < nb + kSwitch - from ? left : nb + kSwitch - from;
+      left -= take;
+      s.k0 = max(0, from - kSwitch);
+      s.k1 = from + static_cast<int>(take) - kSwitch;
+      if (s.k1 > s.k0) return true;   // (a piece may end in a request's start)
     }
     return false;
   }
@@ -199,7 +211,7 @@ __device__ __forceinline__ int block_of(const WeightsParams& p, int b, int k) { 
 template <bool F8>
 __device__ void w_producer(const WeightsParams& p, const WMaps& maps, WShared& sh, uint32_t smem, int rb, uint32_t cl) {
   using C = WCfg<F8>;
-  WWalk walk(sh);
+  WWalk<C::kSwitchPages> walk(sh);
   WSegment s;
   uint32_t i = 0;
   const uint64_t policy = l2_policy_evict_first();
@@ -240,13 +252,14 @@ __device__ void w_mma(const WeightsParams& p, WShared& sh, uint32_t smem, uint32
   using C = WCfg<F8>;
   constexpr uint32_t idesc = F8 ? idesc_e4m3_f32(128, 64, 0, 0) : idesc_bf16_f32(128, 64, 0, 0);
   const uint32_t tmem = sh.tmem_base;
-  WWalk walk(sh);
+  WWalk<C::kSwitchPages> walk(sh);
   WSegment s;
   uint32_t i = 0, T = 0, seg = 0;
   bool ok = true;
   while (ok && walk.next(p, s)) {
-    i += C::kQItems;   // taken by the epilogue warps
     if (!(ok = w_warp_wait(sh, sh.q_full, seg++ & 1, p.status, cl))) break;
+    for (int j = 0; j < C::kQItems; ++j, ++i)   // read by the epilogue warps: q_full says that they are done
+      if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&sh.empty[i % C::kStages]));
     for (int k = s.k0; k < s.k1; ++k, ++i, ++T) {
       const uint32_t st = i % C::kStages, sb = T % kSBufs;
       ok = w_warp_wait(sh, sh.s_empty[sb], ((T / kSBufs) & 1) ^ 1, p.status, cl) &&
@@ -300,27 +313,40 @@ __device__ __forceinline__ void q_to_tmem(uint32_t row, uint32_t chunk_bytes, ui
   }
 }
 
-// The same as two E4M3 terms, four values a column: with sc the power of two that brings the row's
-// largest magnitude into (224, 448], hi = e4m3(q sc) and lo = e4m3(q sc - hi).  A bf16 value has 8
-// significant bits, 4 of which hi holds and 4 lo, so hi + lo = q sc for values down to 2^-2 after
-// scaling and within 2^-10 below.  Returns 1 / sc.
+// Two bf16 values (x0 in the low half) as two pairs of E4M3 codes, hi in bits 0..15 of the result and lo in
+// 16..31: hi = x cut to its top four significant bits (0 below 2^-6, E4M3's smallest normal number), lo = x - hi,
+// which the low four of bf16's eight significant bits fit.  Exact down to |x| = 2^-2, within 2^-10 below.
+__device__ __forceinline__ uint32_t split_e4m3x2(uint32_t x) {
+  const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&x);
+  const uint32_t normal = __hge2_mask(__habs2(v), __float2bfloat162_rn(0.015625f));
+  const uint32_t h = x & 0xFFF0FFF0u & normal;
+  const __nv_bfloat162 l2 = __hsub2(v, *reinterpret_cast<const __nv_bfloat162*>(&h));
+  const uint32_t l = *reinterpret_cast<const uint32_t*>(&l2);
+  return cvt_e4m3x2(bf16_lo(h), bf16_hi(h)) | (cvt_e4m3x2(bf16_lo(l), bf16_hi(l)) << 16);
+}
+
+// The same as two E4M3 terms, four values a column, of q sc, with sc the power of two that brings the row's
+// largest magnitude into (224, 448].  The two halves of a row agree on it through `mine` and `other`
+// (the caller's wait `meet` in between).  Returns 1 / sc, or -1 if the wait failed.
+template <typename Meet>
 __device__ __forceinline__ float q_to_tmem_f8(uint32_t row, uint32_t chunk_bytes, uint32_t lane_base, int half, int rl,
-                                              float* mine, const float* other) {
+                                              float* mine, const volatile float* other, Meet meet) {
   auto unit = [&](int u) { return ld_shared_v4(row + (u >> 3) * chunk_bytes + (((u & 7) ^ (rl & 7)) << 4)); };
-  float top = 0.f;
+  __nv_bfloat162 top2 = __float2bfloat162_rn(0.f);
 #pragma unroll 4
   for (int j = 0; j < 36; ++j) {
     const uint4 x = unit(half * 36 + j);
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
+    for (int e = 0; e < 4; ++e) top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[e])));
   }
-  *mine = top;
-  named_bar_sync(1, kEpiThreads);
-  top = fmaxf(top, *other);
+  *mine = fmaxf(__low2float(top2), __high2float(top2));
+  if (!meet()) return -1.f;
+  const float top = fmaxf(*mine, *other);
   const float t = top > 0.f ? fminf(448.f / top, 0x1p100f) : 1.f;
   const float sc = __uint_as_float(__float_as_uint(t) & 0x7F800000u);
-#pragma unroll 1
+  const __nv_bfloat162 sc2 = __float2bfloat162_rn(sc);   // a power of two: exact, and so are the products
+#pragma unroll 3
   for (int c = 0; c < 9; ++c) {
     uint32_t hi[8], lo[8];
 #pragma unroll
@@ -329,12 +355,14 @@ __device__ __forceinline__ float q_to_tmem_f8(uint32_t row, uint32_t chunk_bytes
       const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float v0 = bf16_lo(w[2 * e]) * sc, v1 = bf16_hi(w[2 * e]) * sc;
-        const float v2 = bf16_lo(w[2 * e + 1]) * sc, v3 = bf16_hi(w[2 * e + 1]) * sc;
-        const uint32_t h01 = cvt_e4m3x2(v0, v1), h23 = cvt_e4m3x2(v2, v3);
-        const float2 f01 = e4m3x2_to_float2(h01), f23 = e4m3x2_to_float2(h23);
-        hi[2 * j + e] = h01 | (h23 << 16);
-        lo[2 * j + e] = cvt_e4m3x2(v0 - f01.x, v1 - f01.y) | (cvt_e4m3x2(v2 - f23.x, v3 - f23.y) << 16);
+        uint32_t s[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[2 * e + i]), sc2);
+          s[i] = split_e4m3x2(*reinterpret_cast<const uint32_t*>(&v));
+        }
+        hi[2 * j + e] = __byte_perm(s[0], s[1], 0x5410);
+        lo[2 * j + e] = __byte_perm(s[0], s[1], 0x7632);
       }
     }
     tmem_st8(lane_base + kQCol + 72 * half + c * 8, hi);
@@ -359,8 +387,9 @@ __device__ __forceinline__ float sum_columns(float (&v)[32], int lane) {
 }
 
 // Warps 2..9.  Warp quadrant q (TMEM lanes 32 q .. 32 q + 31: the rows), half `half` of the page's columns.
+// All waits are on bounded barriers (no bar.sync), so a warp that gives up leaves no other hanging.
 template <bool F8>
-__device__ void w_epilogue(const WeightsParams& p, WShared& sh, uint32_t smem, int rb, uint32_t cl, uint32_t rank) {
+__device__ void w_epilogue(const WeightsParams& p, WShared& sh, uint32_t smem, int rb, uint32_t cl) {
   using C = WCfg<F8>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = warp & 3, half = (warp - 2) >> 2;
@@ -368,11 +397,10 @@ __device__ void w_epilogue(const WeightsParams& p, WShared& sh, uint32_t smem, i
   const int g = rb * kRowsPerPair + r;               // row of the request: i * H + h
   const uint32_t lane_base = sh.tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
   const int cb = half * 32;
-  WWalk walk(sh);
+  WWalk<C::kSwitchPages> walk(sh);
   WSegment s;
-  uint32_t i = 0, T = 0;
-  bool ok = true, stop = false;
-  while (!stop && walk.next(p, s)) {
+  uint32_t i = 0, T = 0, seg = 0;
+  while (walk.next(p, s)) {
     // rows past the request's, and rows that gave no weight, see nothing
     int vis = 0;
     float c_hi = 0.f, c_lo = 0.f, scale_hi = p.scale_hi, scale_lo = p.scale_lo;
@@ -388,12 +416,17 @@ __device__ void w_epilogue(const WeightsParams& p, WShared& sh, uint32_t smem, i
     }
     {   // Q into TMEM: every MMA of the request before is complete (its last S has been waited for)
       const uint32_t item = i + static_cast<uint32_t>(r / C::kQRows);
-      const bool got = w_wait(sh, sh.full[item % C::kStages], (item / C::kStages) & 1, p.status, cl);
-      if (named_bar_or(1, kEpiThreads, !got || !ok)) break;
+      if (!w_warp_wait(sh, sh.full[item % C::kStages], (item / C::kStages) & 1, p.status, cl)) return;
       const int rl = r % C::kQRows;
       const uint32_t row = smem + (item % C::kStages) * C::kStageBytes + rl * 128;
       if constexpr (F8) {
-        const float inv = q_to_tmem_f8(row, C::kQRows * 128, lane_base, half, rl, &sh.amax[half][r], &sh.amax[half ^ 1][r]);
+        const float inv = q_to_tmem_f8(row, C::kQRows * 128, lane_base, half, rl, &sh.amax[half][r],
+                                       &sh.amax[half ^ 1][r], [&] {
+                                         __syncwarp();
+                                         if (lane == 0) mbar_arrive(smem_u32(&sh.amax_full));
+                                         return w_warp_wait(sh, sh.amax_full, seg & 1, p.status, cl);
+                                       });
+        if (inv < 0.f) return;
         scale_hi *= inv;   // a power of two: exact
         scale_lo *= inv;
       } else {
@@ -401,25 +434,14 @@ __device__ void w_epilogue(const WeightsParams& p, WShared& sh, uint32_t smem, i
       }
       tmem_wait_st();
       tc_fence_before();
-      named_bar_sync(1, kEpiThreads);
-      if (threadIdx.x == 64) {
-        mbar_arrive(smem_u32(&sh.q_full));
-        for (uint32_t j = 0; j < C::kQItems; ++j) mbar_arrive(smem_u32(&sh.empty[(i + j) % C::kStages]));
-      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.q_full));
+      ++seg;
       i += C::kQItems + static_cast<uint32_t>(s.k1 - s.k0);
     }
     for (int k = s.k0; k < s.k1; ++k, ++T) {
-      const uint32_t sb = T % kSBufs, buf = T & 1;
-      const bool mine = static_cast<uint32_t>(quad) == (T & 3);   // this warp adds the page's sums up
-      const int t = k * kPageTokens + cb + lane;
-      float* const w = p.weights + s.b * p.weights_stride + t;
-      float old = 0.f;
-      bool store = false;
-      if (mine && rank == 0) {
-        store = t < s.n && block_of(p, s.b, k) >= 0;
-        if (store) old = *w;
-      }
-      ok = w_wait(sh, sh.s_full[sb], (T / kSBufs) & 1, p.status, cl) && ok;
+      const uint32_t sb = T % kSBufs, buf = T % kPartBufs;
+      if (!w_warp_wait(sh, sh.s_full[sb], (T / kSBufs) & 1, p.status, cl)) return;
       tc_fence_after();
       float v[32];
       tmem_ld32(lane_base + kSCol0 + sb * kPageTokens + cb, *reinterpret_cast<uint32_t(*)[32]>(v));
@@ -434,33 +456,66 @@ __device__ void w_epilogue(const WeightsParams& p, WShared& sh, uint32_t smem, i
 #pragma unroll
         for (int c = 0; c < 32; ++c) v[c] = c < seen ? v[c] : 0.f;
       }
-      sh.part[buf][quad][cb + lane] = sum_columns(v, lane);
-      if (named_bar_or(1, kEpiThreads, !ok)) {
-        stop = true;
-        break;
-      }
-      // the next write to part[buf] comes after the next page's barrier, which this warp reaches after its reads
-      if (!mine) continue;
-      float sum = (sh.part[buf][0][cb + lane] + sh.part[buf][1][cb + lane]) +
-                  (sh.part[buf][2][cb + lane] + sh.part[buf][3][cb + lane]);
-      if (cl > 1) {
-        const uint32_t slot = T % kRecvSlots, ph = (T / kRecvSlots) & 1;
-        if (rank != 0) {
-          ok = w_warp_wait(sh, sh.credit[slot], ph ^ 1, p.status, cl) && ok;
-          if (ok) {
-            st_cluster_u32(map_to_rank(smem_u32(&sh.recv[slot][rank - 1][cb + lane]), 0), __float_as_uint(sum));
-            mbar_arrive_remote(map_to_rank(smem_u32(&sh.recv_full[slot]), 0));   // releases this lane's store
-          }
-        } else {
-          ok = w_warp_wait(sh, sh.recv_full[slot], ph, p.status, cl) && ok;
-          for (uint32_t o = 1; o < cl; ++o) sum += sh.recv[slot][o - 1][cb + lane];
-          __syncwarp();
-          if (ok && lane > 0 && static_cast<uint32_t>(lane) < cl)
-            mbar_arrive_remote(map_to_rank(smem_u32(&sh.credit[slot]), lane));
-          store = store && ok;
+      const float sum = sum_columns(v, lane);
+      if (!w_warp_wait(sh, sh.part_empty[buf], ((T / kPartBufs) & 1) ^ 1, p.status, cl)) return;
+      sh.part[buf][quad][cb + lane] = sum;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.part_full[buf]));
+    }
+  }
+}
+
+// Warp 10: adds the four quadrants' sums of a page up and takes them to the weights, or, in the other CTAs of a
+// cluster, to CTA 0.  Lane l has tokens l and l + 32.
+template <bool F8>
+__device__ void w_sum(const WeightsParams& p, WShared& sh, uint32_t cl, uint32_t rank) {
+  using C = WCfg<F8>;
+  const int lane = threadIdx.x & 31;
+  WWalk<C::kSwitchPages> walk(sh);
+  WSegment s;
+  uint32_t T = 0;
+  while (walk.next(p, s)) {
+    for (int k = s.k0; k < s.k1; ++k, ++T) {
+      const uint32_t buf = T % kPartBufs, slot = T % kRecvSlots, ph = (T / kRecvSlots) & 1;
+      float* const w = p.weights + s.b * p.weights_stride + k * kPageTokens;
+      float old[2] = {0.f, 0.f};
+      bool store[2] = {false, false};
+      if (rank == 0) {   // read ahead of the page's sums
+        const bool page = block_of(p, s.b, k) >= 0;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          store[j] = page && k * kPageTokens + 32 * j + lane < s.n;
+          if (store[j]) old[j] = w[32 * j + lane];
         }
       }
-      if (store) *w = old + sum;
+      if (!w_warp_wait(sh, sh.part_full[buf], (T / kPartBufs) & 1, p.status, cl)) return;
+      float sum[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int c = 32 * j + lane;
+        sum[j] = (sh.part[buf][0][c] + sh.part[buf][1][c]) + (sh.part[buf][2][c] + sh.part[buf][3][c]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.part_empty[buf]));
+      if (cl > 1) {
+        if (rank != 0) {
+          if (!w_warp_wait(sh, sh.credit[slot], ph ^ 1, p.status, cl)) return;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            st_cluster_u32(map_to_rank(smem_u32(&sh.recv[slot][rank - 1][32 * j + lane]), 0), __float_as_uint(sum[j]));
+          mbar_arrive_remote(map_to_rank(smem_u32(&sh.recv_full[slot]), 0));   // releases this lane's two sums
+        } else {
+          if (!w_warp_wait(sh, sh.recv_full[slot], ph, p.status, cl)) return;
+          for (uint32_t o = 1; o < cl; ++o)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) sum[j] += sh.recv[slot][o - 1][32 * j + lane];
+          __syncwarp();
+          if (lane > 0 && static_cast<uint32_t>(lane) < cl) mbar_arrive_remote(map_to_rank(smem_u32(&sh.credit[slot]), lane));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (store[j]) w[32 * j + lane] = old[j] + sum[j];
     }
   }
 }
@@ -490,13 +545,18 @@ mla_attn_weights_kernel(const __grid_constant__ WMaps maps, const __grid_constan
     }
     for (int j = 0; j < kSBufs; ++j) {
       mbar_init(smem_u32(&sh.s_full[j]), 1);
-      mbar_init(smem_u32(&sh.s_empty[j]), kEpiThreads / 32);
+      mbar_init(smem_u32(&sh.s_empty[j]), kEpiWarps);
     }
-    mbar_init(smem_u32(&sh.q_full), 1);
+    for (int j = 0; j < kPartBufs; ++j) {
+      mbar_init(smem_u32(&sh.part_full[j]), kEpiWarps);
+      mbar_init(smem_u32(&sh.part_empty[j]), 1);
+    }
+    mbar_init(smem_u32(&sh.amax_full), kEpiWarps);
+    mbar_init(smem_u32(&sh.q_full), kEpiWarps);
     mbar_init(smem_u32(&sh.drain), 1);
     for (int j = 0; j < kRecvSlots; ++j) {
-      mbar_init(smem_u32(&sh.recv_full[j]), cl > 1 ? kPageTokens * (cl - 1) : 1);   // every lane of two warps a CTA
-      mbar_init(smem_u32(&sh.credit[j]), 2);                                       // two warps of CTA 0
+      mbar_init(smem_u32(&sh.recv_full[j]), cl > 1 ? 32 * (cl - 1) : 1);   // every lane of the others' sum warps
+      mbar_init(smem_u32(&sh.credit[j]), 1);
     }
     fence_mbar_init();
   }
@@ -508,13 +568,15 @@ mla_attn_weights_kernel(const __grid_constant__ WMaps maps, const __grid_constan
   tc_fence_after();
   griddep_wait();
   griddep_launch_dependents();
-  find_piece(p, sh, static_cast<int>(blockIdx.x / cl), static_cast<int>(gridDim.x / cl));
+  find_piece<C::kSwitchPages>(p, sh, static_cast<int>(blockIdx.x / cl), static_cast<int>(gridDim.x / cl));
   if (warp == 0) {
     if ((threadIdx.x & 31) == 0) w_producer<F8>(p, maps, sh, smem, static_cast<int>(rank), cl);
   } else if (warp == 1) {
     w_mma<F8>(p, sh, smem, cl);
+  } else if (warp < 2 + kEpiWarps) {
+    w_epilogue<F8>(p, sh, smem, static_cast<int>(rank), cl);
   } else {
-    w_epilogue<F8>(p, sh, smem, static_cast<int>(rank), cl, rank);
+    w_sum<F8>(p, sh, cl, rank);
   }
   __syncwarp();
   tc_fence_before();
