@@ -43,7 +43,8 @@ struct WeightsParams {
 //    step (31 shuffles leave column l's sum in lane l), then four partial sums in shared memory, which
 //    a warp of its own adds to the weights: a fixed order, no atomics.
 //  * More than 128 rows: a cluster of ceil(rows / 128) CTAs walks the same pages, each with its row
-//    block; the others hand their 64 sums a page to CTA 0 through distributed shared memory.
+//    block, and shares their loads (multicast); the others hand their 64 sums a page to CTA 0 through
+//    distributed shared memory.
 //  * Work: all requests' pages in a row, with kSwitchPages for each request's start, cut evenly over the
 //    clusters that fit the GPU.  Each CTA finds its own piece from the lengths (no schedule, no metadata).
 constexpr int kWThreads = 352;                 // warp 0: TMA, 1: MMA, 2..9: exponentials, 10: sums
@@ -90,7 +91,8 @@ constexpr uint32_t weights_smem() { return WCfg<F8>::kOffShared + sizeof(WShared
 static_assert(weights_smem<false>() <= 232448 && weights_smem<true>() <= 232448, "shared memory per CTA");
 
 struct WMaps {
-  CUtensorMap kv;     // bf16: [chunk][row][64 dims], box 64 x 64 x 9; FP8: [chunk 0..3][row][128 codes], box 4 chunks
+  CUtensorMap kv;     // bf16: [chunk 0..8][row][64 dims]; FP8: [chunk 0..3][row][128 codes]; box: 64 rows of all
+                      // chunks, or of one where a cluster shares the page
   CUtensorMap rope;   // FP8: [row][576 codes], box 128 codes x 64 rows (read at code 512)
   CUtensorMap q;      // [chunk 0..8][q row][64 dims], box kQRows rows
 };
@@ -208,38 +210,75 @@ __device__ __forceinline__ int block_of(const WeightsParams& p, int b, int k) { 
 }
 
 // --------------------------------------------------------------- producer --
+// The loads of a cluster: every CTA fetches its share of a page's chunks for all of them, so that a page
+// crosses from L2 to the SMs once a cluster.
+__device__ __forceinline__ void tma_load_3d_multicast(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y,
+                                                      int z, uint16_t mask, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5}], [%2], %6, %7;"
+      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "h"(mask), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_multicast(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y,
+                                                      uint16_t mask, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint"
+      " [%0], [%1, {%3, %4}], [%2], %5, %6;"
+      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "h"(mask), "l"(policy) : "memory");
+}
+// Arrives on the barrier at this offset in every CTA of the mask once the MMAs issued so far are done.
+__device__ __forceinline__ void mma_commit_warp_multicast(uint32_t bar, uint16_t mask) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}"
+      :: "r"(bar), "h"(mask) : "memory");
+}
+
 template <bool F8>
-__device__ void w_producer(const WeightsParams& p, const WMaps& maps, WShared& sh, uint32_t smem, int rb, uint32_t cl) {
+__device__ void w_producer(const WeightsParams& p, const WMaps& maps, WShared& sh, uint32_t smem, uint32_t rank,
+                           uint32_t cl) {
   using C = WCfg<F8>;
   WWalk<C::kSwitchPages> walk(sh);
   WSegment s;
   uint32_t i = 0;
-  const uint64_t policy = l2_policy_evict_first();
+  const uint64_t policy = l2_policy_evict_first();   // read once, by one SM or one cluster
+  const uint16_t mask = static_cast<uint16_t>((1u << cl) - 1);
   bool ok = true;
-  auto stage_for = [&](uint32_t bytes, uint32_t* st) {   // a free ring stage that expects `bytes`
-    const uint32_t k = i % C::kStages;
-    if (!w_wait(sh, sh.empty[k], ((i / C::kStages) & 1) ^ 1, p.status, cl)) return false;
-    mbar_arrive_expect_tx(smem_u32(&sh.full[k]), bytes);
-    *st = k;
-    ++i;
-    return true;
+  auto stage_for = [&](uint32_t bytes) {   // waits for the next ring stage, which then expects `bytes`
+    const uint32_t st = i % C::kStages;
+    ok = w_wait(sh, sh.empty[st], ((i / C::kStages) & 1) ^ 1, p.status, cl);
+    if (ok) mbar_arrive_expect_tx(smem_u32(&sh.full[st]), bytes), ++i;
+    return st;
   };
-  uint32_t st = 0;
   while (ok && walk.next(p, s)) {
-    for (int j = 0; j < C::kQItems && ok; ++j)
-      if ((ok = stage_for(C::kQItemBytes, &st)))
+    for (int j = 0; j < C::kQItems && ok; ++j) {
+      const uint32_t st = stage_for(C::kQItemBytes);
+      if (ok)
         tma_load_3d(smem + st * C::kStageBytes, &maps.q, smem_u32(&sh.full[st]), 0,
-                    s.b * p.rows + rb * kRowsPerPair + C::kQRows * j, 0);
+                    s.b * p.rows + static_cast<int>(rank) * kRowsPerPair + C::kQRows * j, 0);
+    }
     for (int k = s.k0; k < s.k1 && ok; ++k) {
       int blk = block_of(p, s.b, k);
       if (blk < 0) {   // reported; the box lies past the cache, so TMA fills it with zeros
         atomicCAS(p.status, 0, MLA_ERR_DEVICE_BOUNDS);
         blk = static_cast<int>(p.num_blocks);
       }
-      if (!(ok = stage_for(C::kStageBytes, &st))) break;
+      const uint32_t st = stage_for(C::kStageBytes);
+      if (!ok) break;
       const uint32_t dst = smem + st * C::kStageBytes, bar = smem_u32(&sh.full[st]);
-      tma_load_3d_hint(dst, &maps.kv, bar, 0, blk * kPageTokens, 0, policy);
-      if constexpr (F8) tma_load_2d_hint(dst + 4 * kChunk, &maps.rope, bar, kDimV, blk * kPageTokens, policy);
+      const int row = blk * kPageTokens;
+      if (cl == 1) {
+        tma_load_3d_hint(dst, &maps.kv, bar, 0, row, 0, policy);
+        if constexpr (F8) tma_load_2d_hint(dst + 4 * kChunk, &maps.rope, bar, kDimV, row, policy);
+      } else {
+        for (uint32_t c = rank; c < C::kKChunks; c += cl) {
+          if (F8 && c == 4)
+            tma_load_2d_multicast(dst + c * kChunk, &maps.rope, bar, kDimV, row, mask, policy);
+          else
+            tma_load_3d_multicast(dst + c * kChunk, &maps.kv, bar, 0, row, static_cast<int>(c), mask, policy);
+        }
+      }
     }
   }
   const uint32_t flying = i < C::kStages ? i : C::kStages;   // loads still in flight land before the CTA may exit
@@ -258,8 +297,12 @@ __device__ void w_mma(const WeightsParams& p, WShared& sh, uint32_t smem, uint32
   bool ok = true;
   while (ok && walk.next(p, s)) {
     if (!(ok = w_warp_wait(sh, sh.q_full, seg++ & 1, p.status, cl))) break;
-    for (int j = 0; j < C::kQItems; ++j, ++i)   // read by the epilogue warps: q_full says that they are done
-      if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&sh.empty[i % C::kStages]));
+    for (int j = 0; j < C::kQItems; ++j, ++i)   // the epilogue warps have read them: free, for every CTA's next load
+      if ((threadIdx.x & 31) < cl) {
+        const uint32_t bar = smem_u32(&sh.empty[i % C::kStages]);
+        if (cl == 1) mbar_arrive(bar);
+        else mbar_arrive_remote(map_to_rank(bar, threadIdx.x & 31));
+      }
     for (int k = s.k0; k < s.k1; ++k, ++i, ++T) {
       const uint32_t st = i % C::kStages, sb = T % kSBufs;
       ok = w_warp_wait(sh, sh.s_empty[sb], ((T / kSBufs) & 1) ^ 1, p.status, cl) &&
@@ -285,7 +328,10 @@ __device__ void w_mma(const WeightsParams& p, WShared& sh, uint32_t smem, uint32
             mma_bf16_ts_warp(d, tmem + kQCol + c * 32 + j * 8, smem_desc_sw128(stage + c * kChunk + j * 32, 16, 1024),
                              idesc, (c | j) ? 1u : 0u);
       }
-      mma_commit_warp(smem_u32(&sh.empty[st]));
+      if (cl == 1)
+        mma_commit_warp(smem_u32(&sh.empty[st]));
+      else   // the next load into this stage of any CTA writes all of them
+        mma_commit_warp_multicast(smem_u32(&sh.empty[st]), static_cast<uint16_t>((1u << cl) - 1));
       mma_commit_warp(smem_u32(&sh.s_full[sb]));
     }
   }
@@ -297,79 +343,75 @@ __device__ void w_mma(const WeightsParams& p, WShared& sh, uint32_t smem, uint32
 }
 
 // --------------------------------------------------------------- epilogue --
-// Row r's half `half` of q (288 values) into TMEM, two bf16 values a column.  `row`: the row's first
-// 128 bytes in its ring item (chunks of chunk_bytes, 16-byte units swizzled by the row).
-__device__ __forceinline__ void q_to_tmem(uint32_t row, uint32_t chunk_bytes, uint32_t lane_base, int half, int rl) {
+// A thread's half row of q (288 values, 36 units of 16 bytes) in its ring item: chunks of chunk_bytes, a
+// row's units swizzled.
+struct QHalf {
+  uint32_t row, chunk_bytes;
+  int u0, swizzle;
+  __device__ __forceinline__ uint4 unit(int j) const {
+    const int u = u0 + j;
+    return ld_shared_v4(row + (u >> 3) * chunk_bytes + (((u & 7) ^ swizzle) << 4));
+  }
+  // into TMEM, two bf16 values a column, from column `col` on
+  __device__ __forceinline__ void store(uint32_t col) const {
 #pragma unroll
-  for (int c = 0; c < 9; ++c) {
-    uint32_t v[16];
+    for (int c = 0; c < 9; ++c) {
+      uint32_t v[16];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int u = half * 36 + c * 4 + j;
-      const uint4 x = ld_shared_v4(row + (u >> 3) * chunk_bytes + (((u & 7) ^ (rl & 7)) << 4));
-      v[4 * j] = x.x, v[4 * j + 1] = x.y, v[4 * j + 2] = x.z, v[4 * j + 3] = x.w;
+      for (int j = 0; j < 4; ++j) {
+        const uint4 x = unit(4 * c + j);
+        v[4 * j] = x.x, v[4 * j + 1] = x.y, v[4 * j + 2] = x.z, v[4 * j + 3] = x.w;
+      }
+      tmem_st16(col + c * 16, v);
     }
-    tmem_st16(lane_base + kQCol + half * 144 + c * 16, v);
   }
-}
-
-// Two bf16 values (x0 in the low half) as two pairs of E4M3 codes, hi in bits 0..15 of the result and lo in
-// 16..31: hi = x cut to its top four significant bits (0 below 2^-6, E4M3's smallest normal number), lo = x - hi,
-// which the low four of bf16's eight significant bits fit.  Exact down to |x| = 2^-2, within 2^-10 below.
-__device__ __forceinline__ uint32_t split_e4m3x2(uint32_t x) {
-  const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&x);
-  const uint32_t normal = __hge2_mask(__habs2(v), __float2bfloat162_rn(0.015625f));
-  const uint32_t h = x & 0xFFF0FFF0u & normal;
-  const __nv_bfloat162 l2 = __hsub2(v, *reinterpret_cast<const __nv_bfloat162*>(&h));
-  const uint32_t l = *reinterpret_cast<const uint32_t*>(&l2);
-  return cvt_e4m3x2(bf16_lo(h), bf16_hi(h)) | (cvt_e4m3x2(bf16_lo(l), bf16_hi(l)) << 16);
-}
-
-// The same as two E4M3 terms, four values a column, of q sc, with sc the power of two that brings the row's
-// largest magnitude into (224, 448].  The two halves of a row agree on it through `mine` and `other`
-// (the caller's wait `meet` in between).  Returns 1 / sc, or -1 if the wait failed.
-template <typename Meet>
-__device__ __forceinline__ float q_to_tmem_f8(uint32_t row, uint32_t chunk_bytes, uint32_t lane_base, int half, int rl,
-                                              float* mine, const volatile float* other, Meet meet) {
-  auto unit = [&](int u) { return ld_shared_v4(row + (u >> 3) * chunk_bytes + (((u & 7) ^ (rl & 7)) << 4)); };
-  __nv_bfloat162 top2 = __float2bfloat162_rn(0.f);
-#pragma unroll 4
-  for (int j = 0; j < 36; ++j) {
-    const uint4 x = unit(half * 36 + j);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[e])));
-  }
-  *mine = fmaxf(__low2float(top2), __high2float(top2));
-  if (!meet()) return -1.f;
-  const float top = fmaxf(*mine, *other);
-  const float t = top > 0.f ? fminf(448.f / top, 0x1p100f) : 1.f;
-  const float sc = __uint_as_float(__float_as_uint(t) & 0x7F800000u);
-  const __nv_bfloat162 sc2 = __float2bfloat162_rn(sc);   // a power of two: exact, and so are the products
-#pragma unroll 3
-  for (int c = 0; c < 9; ++c) {
-    uint32_t hi[8], lo[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint4 x = unit(half * 36 + c * 4 + j);
+  // the largest magnitude; NaN where a value is NaN
+  __device__ __forceinline__ float largest() const {
+    __nv_bfloat162 top = __float2bfloat162_rn(0.f);
+#pragma unroll 6
+    for (int j = 0; j < 36; ++j) {
+      const uint4 x = unit(j);
       const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        uint32_t s[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[2 * e + i]), sc2);
-          s[i] = split_e4m3x2(*reinterpret_cast<const uint32_t*>(&v));
-        }
-        hi[2 * j + e] = __byte_perm(s[0], s[1], 0x5410);
-        lo[2 * j + e] = __byte_perm(s[0], s[1], 0x7632);
-      }
+      for (int e = 0; e < 4; ++e) top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[e])));
     }
-    tmem_st8(lane_base + kQCol + 72 * half + c * 8, hi);
-    tmem_st8(lane_base + kQCol + 144 + 72 * half + c * 8, lo);
+    const float lo = __low2float(top), hi = __high2float(top);
+    return isnan(lo) || isnan(hi) ? NAN : fmaxf(lo, hi);
   }
-  return 1.f / sc;
-}
+  // into TMEM as two E4M3 terms, four values a column, of q 2^k: hi = e4m3(q 2^k) from column `col` on and
+  // lo = e4m3(q 2^k - hi) 144 columns further.  A bf16 value has 8 significant bits, of which hi holds 4
+  // and lo the rest, so hi + lo is exact for values down to 2^-2 after scaling and within 2^-10 below.  It
+  // goes through fp16 pairs, two values an instruction (conversions of single floats bound it
+  // otherwise): with the magnitude's exponent rebased (112 = 127 - 15, less k; smaller ones become 0,
+  // below 2^-15) a bf16 pattern shifted left by three bits is the fp16 one.
+  __device__ __forceinline__ void store_e4m3(uint32_t col, int k) const {
+    const uint32_t base = static_cast<uint32_t>(112 - k) << 7, base2 = base | (base << 16);
+    auto split = [&](uint32_t w) {   // hi of the pair in bits 0..15, lo in 16..31
+      const __nv_bfloat162 m = __hmax2(__habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)),
+                                       *reinterpret_cast<const __nv_bfloat162*>(&base2));
+      const uint32_t v = ((*reinterpret_cast<const uint32_t*>(&m) - base2) << 3) | (w & 0x80008000u);
+      uint32_t both;
+      asm("{\n\t.reg .b16 h, l;\n\t.reg .b32 b, d;\n\t"
+          "cvt.rn.satfinite.e4m3x2.f16x2 h, %1;\n\tcvt.rn.f16x2.e4m3x2 b, h;\n\tsub.rn.f16x2 d, %1, b;\n\t"
+          "cvt.rn.satfinite.e4m3x2.f16x2 l, d;\n\tmov.b32 %0, {h, l};\n\t}"
+          : "=r"(both) : "r"(v));
+      return both;
+    };
+#pragma unroll
+    for (int c = 0; c < 9; ++c) {
+      uint32_t hi[8], lo[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint4 x = unit(4 * c + j);
+        const uint32_t a = split(x.x), b = split(x.y), d = split(x.z), e = split(x.w);
+        hi[2 * j] = __byte_perm(a, b, 0x5410), lo[2 * j] = __byte_perm(a, b, 0x7632);
+        hi[2 * j + 1] = __byte_perm(d, e, 0x5410), lo[2 * j + 1] = __byte_perm(d, e, 0x7632);
+      }
+      tmem_st8(col + c * 8, hi);
+      tmem_st8(col + 144 + c * 8, lo);
+    }
+  }
+};
 
 // Sums over the warp's lanes: lane l gets that of v[l].  Each step exchanges half of the columns a
 // lane still has with the lane `o` away, in a fixed order.
@@ -414,31 +456,34 @@ __device__ void w_epilogue(const WeightsParams& p, WShared& sh, uint32_t smem, i
         if (isfinite(lse)) c_lo = fmaf(-lse, kL2eLo, fmaf(-lse, kL2eHi, -c_hi));
       }
     }
-    {   // Q into TMEM: every MMA of the request before is complete (its last S has been waited for)
-      const uint32_t item = i + static_cast<uint32_t>(r / C::kQRows);
-      if (!w_warp_wait(sh, sh.full[item % C::kStages], (item / C::kStages) & 1, p.status, cl)) return;
-      const int rl = r % C::kQRows;
-      const uint32_t row = smem + (item % C::kStages) * C::kStageBytes + rl * 128;
-      if constexpr (F8) {
-        const float inv = q_to_tmem_f8(row, C::kQRows * 128, lane_base, half, rl, &sh.amax[half][r],
-                                       &sh.amax[half ^ 1][r], [&] {
-                                         __syncwarp();
-                                         if (lane == 0) mbar_arrive(smem_u32(&sh.amax_full));
-                                         return w_warp_wait(sh, sh.amax_full, seg & 1, p.status, cl);
-                                       });
-        if (inv < 0.f) return;
-        scale_hi *= inv;   // a power of two: exact
-        scale_lo *= inv;
-      } else {
-        q_to_tmem(row, C::kQRows * 128, lane_base, half, rl);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.q_full));
-      ++seg;
-      i += C::kQItems + static_cast<uint32_t>(s.k1 - s.k0);
+    // Q into TMEM: every MMA of the request before is complete (its last S has been waited for)
+    const uint32_t item = i + static_cast<uint32_t>(r / C::kQRows);
+    i += C::kQItems + static_cast<uint32_t>(s.k1 - s.k0);
+    if (!w_warp_wait(sh, sh.full[item % C::kStages], (item / C::kStages) & 1, p.status, cl)) return;
+    const int rl = r % C::kQRows;
+    const QHalf q{smem + (item % C::kStages) * C::kStageBytes + rl * 128, C::kQRows * 128, 36 * half, rl & 7};
+    if constexpr (F8) {
+      sh.amax[half][r] = q.largest();
+      __syncwarp();   // the row's two halves agree on its scale
+      if (lane == 0) mbar_arrive(smem_u32(&sh.amax_full));
+      if (!w_warp_wait(sh, sh.amax_full, seg & 1, p.status, cl)) return;
+      const float a = sh.amax[0][r], b = sh.amax[1][r];
+      // 2^e brings the largest magnitude into (224, 448]; a row with an infinity or a NaN gives NaN
+      const bool finite = a <= 3.4e38f && b <= 3.4e38f;
+      const float top = fmaxf(a, b), t = finite && top > 0.f ? fminf(448.f / top, 0x1p100f) : 1.f;
+      const int e = static_cast<int>(__float_as_uint(t) >> 23) - 127;
+      q.store_e4m3(lane_base + kQCol + 72 * half, e);
+      const float inv = finite ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : NAN;
+      scale_hi *= inv;   // a power of two: exact
+      scale_lo *= inv;
+    } else {
+      q.store(lane_base + kQCol + 144 * half);
     }
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sh.q_full));
+    ++seg;
     for (int k = s.k0; k < s.k1; ++k, ++T) {
       const uint32_t sb = T % kSBufs, buf = T % kPartBufs;
       if (!w_warp_wait(sh, sh.s_full[sb], (T / kSBufs) & 1, p.status, cl)) return;
@@ -541,7 +586,7 @@ mla_attn_weights_kernel(const __grid_constant__ WMaps maps, const __grid_constan
     sh.abort = 0;
     for (int j = 0; j < C::kStages; ++j) {
       mbar_init(smem_u32(&sh.full[j]), 1);
-      mbar_init(smem_u32(&sh.empty[j]), 1);
+      mbar_init(smem_u32(&sh.empty[j]), cl);
     }
     for (int j = 0; j < kSBufs; ++j) {
       mbar_init(smem_u32(&sh.s_full[j]), 1);
@@ -570,7 +615,7 @@ mla_attn_weights_kernel(const __grid_constant__ WMaps maps, const __grid_constan
   griddep_launch_dependents();
   find_piece<C::kSwitchPages>(p, sh, static_cast<int>(blockIdx.x / cl), static_cast<int>(gridDim.x / cl));
   if (warp == 0) {
-    if ((threadIdx.x & 31) == 0) w_producer<F8>(p, maps, sh, smem, static_cast<int>(rank), cl);
+    if ((threadIdx.x & 31) == 0) w_producer<F8>(p, maps, sh, smem, rank, cl);
   } else if (warp == 1) {
     w_mma<F8>(p, sh, smem, cl);
   } else if (warp < 2 + kEpiWarps) {
@@ -655,7 +700,7 @@ mla_status_t weights_setup(WeightsDevice** out) {
 }
 
 template <bool F8>
-bool encode_maps(WMaps* m, const void* kv, int64_t num_blocks, const void* q, int64_t q_rows) {
+bool encode_maps(WMaps* m, const void* kv, int64_t num_blocks, const void* q, int64_t q_rows, int cl) {
   using C = WCfg<F8>;
   const cuuint32_t es[3] = {1, 1, 1};
   auto encode = [&](CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,
@@ -668,12 +713,12 @@ bool encode_maps(WMaps* m, const void* kv, int64_t num_blocks, const void* q, in
   bool ok;
   if (F8) {
     const cuuint64_t dims[3] = {128, rows, 4}, strides[2] = {kDimQK, 128}, rdims[2] = {kDimQK, rows}, rstrides[1] = {kDimQK};
-    const cuuint32_t box[3] = {128, kPageTokens, 4}, rbox[2] = {128, kPageTokens};
+    const cuuint32_t box[3] = {128, kPageTokens, cl > 1 ? 1u : 4u}, rbox[2] = {128, kPageTokens};
     ok = encode(&m->kv, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, kv, dims, strides, box) &&
          encode(&m->rope, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, kv, rdims, rstrides, rbox);
   } else {
     const cuuint64_t dims[3] = {64, rows, 9}, strides[2] = {kDimQK * 2, 128};
-    const cuuint32_t box[3] = {64, kPageTokens, 9};
+    const cuuint32_t box[3] = {64, kPageTokens, cl > 1 ? 1u : 9u};
     ok = encode(&m->kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, kv, dims, strides, box);
   }
   const cuuint64_t qdims[3] = {64, static_cast<cuuint64_t>(q_rows), 9}, qstrides[2] = {kDimQK * 2, 128};
@@ -724,11 +769,11 @@ mla_status_t weights_impl(const mla_bf16_t* q, const float* lse, const void* kv_
   const mla_status_t st = weights_setup(&d);
   if (st != MLA_OK) return st;
   WMaps maps = {};
-  const int64_t q_rows = static_cast<int64_t>(B) * p.rows;
-  if (!(fp8 ? encode_maps<true>(&maps, kv_cache, num_blocks, q, q_rows)
-            : encode_maps<false>(&maps, kv_cache, num_blocks, q, q_rows)))
-    return MLA_ERR_CUDA;
   const int cl = (p.rows + kRowsPerPair - 1) / kRowsPerPair;
+  const int64_t q_rows = static_cast<int64_t>(B) * p.rows;
+  if (!(fp8 ? encode_maps<true>(&maps, kv_cache, num_blocks, q, q_rows, cl)
+            : encode_maps<false>(&maps, kv_cache, num_blocks, q, q_rows, cl)))
+    return MLA_ERR_CUDA;
   // no more clusters than pages there can be
   const int64_t most = static_cast<int64_t>(B) * ((p.slots + kPageTokens - 1) / kPageTokens);
   const int clusters = static_cast<int>(most < d->clusters[fp8][cl] ? most : d->clusters[fp8][cl]);
