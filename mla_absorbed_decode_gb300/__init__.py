@@ -9,6 +9,7 @@ There is no fallback: if the library is not built, calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -369,81 +370,81 @@ def extend_chunked(q_nope: torch.Tensor, q_pe: torch.Tensor, w_uk: torch.Tensor,
     return out, lse
 
 
-def _need(ok: bool, what: str):
-    if not ok:
-        raise ValueError(what)
-
-
-def _typed(name: str, t: torch.Tensor, dtype: torch.dtype, dev: torch.device):
-    """The kernels read raw addresses: a tensor of another type or device must not reach them."""
+# The latent-cache calls.  The kernels read raw addresses, so a tensor of another type, shape or device must
+# not reach them; the checks are plain ifs (a decode step makes these calls for every layer).
+def _typed(name: str, what: str, t: torch.Tensor, dtype: torch.dtype, dev: int):
     if t.dtype != dtype:
-        raise TypeError(f"{name}: {dtype} expected, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name}: on {t.device}, the call's tensors are on {dev}")
+        raise TypeError(f"{name}: {what}: {dtype} expected, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: {what}: on {t.device}, the call's first tensor is on GPU {dev}")
 
 
 def _paged(name: str, kv_cache: torch.Tensor, block_table: torch.Tensor, seqlens: torch.Tensor, fp8: bool):
-    """Checks a call's cache, table and lengths; returns (device, B)."""
-    dev = kv_cache.device
-    _need(dev.type == "cuda", f"{name}: kv_cache must be on a GPU")
-    if fp8:
-        if kv_cache.element_size() != 1:
-            raise TypeError(f"{name}: kv_cache must hold one byte per value (E4M3 codes)")
+    """Checks a call's cache, table and lengths; returns (device index, B, num_blocks, max_blocks)."""
+    dev = kv_cache.get_device()
+    if dev < 0:
+        raise ValueError(f"{name}: kv_cache must be on a GPU")
+    if kv_cache.element_size() != 1 if fp8 else kv_cache.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: kv_cache must hold " + ("one byte per value (E4M3 codes)" if fp8 else "bfloat16"))
+    shape = kv_cache.shape
+    if len(shape) != 3 or shape[1] != 64 or shape[2] != 576 or not kv_cache.is_contiguous():
+        raise ValueError(f"{name}: kv_cache must be a contiguous [num_blocks, 64, 576]")
+    _typed(name, "block_table", block_table, torch.int32, dev)
+    _typed(name, "seqlens", seqlens, torch.int32, dev)
+    if seqlens.dim() != 1 or not seqlens.is_contiguous():
+        raise ValueError(f"{name}: seqlens must be a contiguous [B]")
+    B = seqlens.numel()
+    if block_table.dim() != 2 or block_table.size(0) != B or not block_table.is_contiguous():
+        raise ValueError(f"{name}: block_table must be a contiguous [B, max_blocks]")
+    return dev, B, shape[0], block_table.size(1)
+
+
+def _rows(name: str, what: str, t: torch.Tensor, dtype: torch.dtype, dev: int, B: int, max_blocks: int) -> int:
+    """Checks a [B, slots] tensor whose rows may be strided; returns the elements between rows, of which a request may
+    use as many as there are columns."""
+    _typed(name, what, t, dtype, dev)
+    if t.dim() != 2 or t.size(0) != B or t.size(1) < 1 or (t.size(1) > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: {what}: [B, slots] with contiguous rows expected")
+    slots = t.size(1)
+    stride = t.stride(0) if B > 1 else slots
+    if stride != slots and (stride < slots or slots < 64 * max_blocks):
+        raise ValueError(f"{name}: {what}: rows that are a part of wider ones must have a slot for every entry of block_table")
+    return stride
+
+
+def _launch(dev: int, fn: str, args, stream):
+    """Calls the library with tensors' device current (it launches on the current device) and that device's current
+    stream unless one is given."""
+    if stream is not None:
+        raw = stream.cuda_stream
     else:
-        _typed(f"{name}: kv_cache", kv_cache, torch.bfloat16, dev)
-    _need(kv_cache.dim() == 3 and kv_cache.shape[1:] == (64, 576) and kv_cache.is_contiguous(),
-          f"{name}: kv_cache must be a contiguous [num_blocks, 64, 576]")
-    _typed(f"{name}: block_table", block_table, torch.int32, dev)
-    _typed(f"{name}: seqlens", seqlens, torch.int32, dev)
-    _need(seqlens.dim() == 1 and seqlens.is_contiguous(), f"{name}: seqlens must be a contiguous [B]")
-    B = seqlens.shape[0]
-    _need(block_table.dim() == 2 and block_table.shape[0] == B and block_table.is_contiguous(),
-          f"{name}: block_table must be a contiguous [B, max_blocks]")
-    return dev, B
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    if dev == torch._C._cuda_getDevice():
+        status = getattr(_lib or lib(), fn)(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            status = getattr(_lib or lib(), fn)(*args, raw)
+    if status != MLA_OK:
+        raise MLAError(status, fn)
 
 
-def _rows(name: str, t: torch.Tensor, dtype: torch.dtype, dev: torch.device, B: int) -> int:
-    """Checks a [B, slots] tensor whose rows may be strided; returns the elements between rows, of
-    which a request may use as many as there are columns."""
-    _typed(name, t, dtype, dev)
-    _need(t.dim() == 2 and t.shape[0] == B and t.shape[1] >= 1 and (t.shape[1] == 1 or t.stride(1) == 1)
-          and (B == 1 or t.stride(0) >= t.shape[1]), f"{name}: [B, slots] with contiguous rows expected")
-    return t.stride(0) if B > 1 else t.shape[1]
+@functools.lru_cache(maxsize=None)
+def _sections(sections: tuple):
+    """Host array of a rotation's sections."""
+    if not 1 <= len(sections) <= 4 or min(sections) < 0 or sum(sections) != 32:
+        raise ValueError("sections must be 1 to 4 counts of pairs that sum to 32")
+    return (_c_int * len(sections))(*sections)
 
 
-class _on:
-    """Makes a tensor's device current for a call (the library launches on the current device)."""
-    __slots__ = ("guard",)
-
-    def __init__(self, dev: torch.device):
-        self.guard = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-
-def _axes(name: str, positions: torch.Tensor, sections, N: int, dev: torch.device):
+def _axes(name: str, positions: torch.Tensor, sections, N: int, dev: int):
     """Checks positions ([N], or [axes, N]) and sections; returns (pointer, stride, host sections, axes)."""
-    _typed(f"{name}: positions", positions, torch.int32, dev)
-    if positions.dim() == 1:
-        positions = positions[None]
-    sections = tuple(int(v) for v in sections)
-    _need(positions.dim() == 2 and positions.shape == (len(sections), N) and (N == 1 or positions.stride(1) == 1),
-          f"{name}: positions must be [axes, N] (or [N]) with as many axes as sections")
-    _need(1 <= len(sections) <= 4 and min(sections) >= 0 and sum(sections) == 32,
-          f"{name}: sections must be 1 to 4 counts of pairs that sum to 32")
-    stride = positions.stride(0) if len(sections) > 1 else N
-    return positions.data_ptr(), stride, (_c_int * len(sections))(*sections), len(sections)
-
-
-def _row_head(t: torch.Tensor) -> tuple[int, int]:
-    """Strides of [N, H, 64] (that of a dim of one element says nothing)."""
-    return t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0
+    host = _sections(tuple(sections))
+    axes = len(host)
+    _typed(name, "positions", positions, torch.int32, dev)
+    one = positions.dim() == 1
+    if tuple(positions.shape) != ((N,) if one else (axes, N)) or (one and axes != 1) or (N > 1 and positions.stride(-1) != 1):
+        raise ValueError(f"{name}: positions must be [axes, N] (or [N]) with as many axes as sections")
+    return positions.data_ptr(), positions.stride(0) if axes > 1 else N, host, axes
 
 
 def rope_axes(x: torch.Tensor, positions: torch.Tensor, sections=(32,), out: torch.Tensor | None = None,
@@ -452,47 +453,52 @@ def rope_axes(x: torch.Tensor, positions: torch.Tensor, sections=(32,), out: tor
     contiguous), positions int32 [axes, N], sections = how many of the 32 adjacent pairs each axis
     turns, one section after the other or (interleaved) dealt out in turn.  out may be x or a view such
     as q[..., 512:] of the decode query.  inverse turns back: the gradient of x from that of out."""
-    dev = x.device
-    _need(dev.type == "cuda" and x.dim() == 3 and x.shape[2] == 64, "rope_axes: x must be [N, H, 64] on a GPU")
-    _typed("rope_axes: x", x, torch.bfloat16, dev)
-    N, H, _ = x.shape
+    dev = x.get_device()
+    shape = x.shape
+    if dev < 0 or len(shape) != 3 or shape[2] != 64:
+        raise ValueError("rope_axes: x must be [N, H, 64] on a GPU")
+    _typed("rope_axes", "x", x, torch.bfloat16, dev)
+    N, H, _ = shape
     if out is None:
-        out = torch.empty((N, H, 64), dtype=torch.bfloat16, device=dev)
-    _typed("rope_axes: out", out, torch.bfloat16, dev)
-    _need(out.shape == x.shape, "rope_axes: out must have x's shape")
-    _need(x.stride(2) == 1 and out.stride(2) == 1, "rope_axes: the 64 values of a row must be contiguous")
+        out = torch.empty((N, H, 64), dtype=torch.bfloat16, device=x.device)
+    else:
+        _typed("rope_axes", "out", out, torch.bfloat16, dev)
+        if out.shape != shape:
+            raise ValueError("rope_axes: out must have x's shape")
+    if x.stride(2) != 1 or out.stride(2) != 1:
+        raise ValueError("rope_axes: the 64 values of a row must be contiguous")
     if N == 0 or H == 0:
         return out
-    pos, pos_stride, sec, axes = _axes("rope_axes", positions, sections, N, dev)
-    with _on(dev):
-        _check(lib().mla_rope_axes(_ptr(x), *_row_head(x), _ptr(out), *_row_head(out), pos, pos_stride, sec, axes,
-                                   int(interleaved), float(rope_theta), int(inverse), N, H, _stream(stream)),
-               "mla_rope_axes")
+    pos, pos_stride, host, axes = _axes("rope_axes", positions, sections, N, dev)
+    many, heads = N > 1, H > 1   # the stride of a dim of one element says nothing
+    _launch(dev, "mla_rope_axes", (
+        x.data_ptr(), x.stride(0) if many else 0, x.stride(1) if heads else 0, out.data_ptr(),
+        out.stride(0) if many else 0, out.stride(1) if heads else 0, pos, pos_stride, host, axes, interleaved, rope_theta,
+        inverse, N, H), stream)
     return out
 
 
 def _append(name, c, k_pe, kv_cache, kv_scale, block_table, seqlens, new_offsets, positions, sections, rope_theta,
             interleaved, stream):
-    dev, B = _paged(name, kv_cache, block_table, seqlens, kv_scale is not None)
-    _typed(f"{name}: c", c, torch.bfloat16, dev)
-    _typed(f"{name}: k_pe", k_pe, torch.bfloat16, dev)
-    N = c.shape[0]
-    _need(c.shape == (N, 512) and k_pe.shape == (N, 64) and c.stride(1) == 1 and k_pe.stride(1) == 1,
-          f"{name}: c [N, 512] and k_pe [N, 64] with contiguous rows expected")
+    dev, B, num_blocks, max_blocks = _paged(name, kv_cache, block_table, seqlens, kv_scale is not None)
+    _typed(name, "c", c, torch.bfloat16, dev)
+    _typed(name, "k_pe", k_pe, torch.bfloat16, dev)
+    N = c.size(0)
+    if tuple(c.shape) != (N, 512) or tuple(k_pe.shape) != (N, 64) or c.stride(1) != 1 or k_pe.stride(1) != 1:
+        raise ValueError(f"{name}: c [N, 512] and k_pe [N, 64] with contiguous rows expected")
     off = None
     if new_offsets is not None:
-        _typed(f"{name}: new_offsets", new_offsets, torch.int32, dev)
-        _need(new_offsets.shape == (B + 1,) and new_offsets.is_contiguous(), f"{name}: new_offsets must be [B + 1]")
-        off = _ptr(new_offsets)
+        _typed(name, "new_offsets", new_offsets, torch.int32, dev)
+        if tuple(new_offsets.shape) != (B + 1,) or not new_offsets.is_contiguous():
+            raise ValueError(f"{name}: new_offsets must be a contiguous [B + 1]")
+        off = new_offsets.data_ptr()
     if N == 0 or B == 0:
         return kv_cache
     rot = (None, 0, None, 0) if positions is None else _axes(name, positions, sections, N, dev)
-    scale = () if kv_scale is None else (float(kv_scale),)
-    with _on(dev):
-        _check(getattr(lib(), f"mla_{name}")(
-            _ptr(c), c.stride(0) if N > 1 else 512, _ptr(k_pe), k_pe.stride(0) if N > 1 else 64, _ptr(kv_cache), *scale,
-            kv_cache.shape[0], _ptr(block_table), block_table.shape[1], _ptr(seqlens), off, N, B, *rot, int(interleaved),
-            float(rope_theta), _stream(stream)), f"mla_{name}")
+    pool = (kv_cache.data_ptr(),) if kv_scale is None else (kv_cache.data_ptr(), kv_scale)
+    _launch(dev, "mla_" + name, (
+        c.data_ptr(), c.stride(0) if N > 1 else 512, k_pe.data_ptr(), k_pe.stride(0) if N > 1 else 64, *pool, num_blocks,
+        block_table.data_ptr(), max_blocks, seqlens.data_ptr(), off, N, B, *rot, interleaved, rope_theta), stream)
     return kv_cache
 
 
@@ -515,22 +521,19 @@ def cache_append_fp8(c, k_pe, kv_cache, kv_scale: float, block_table, seqlens, n
 
 
 def _weights(name, q, lse, kv_cache, kv_scale, block_table, seqlens, softmax_scale, causal, weights, stream):
-    dev, B = _paged(name, kv_cache, block_table, seqlens, kv_scale is not None)
-    _typed(f"{name}: q", q, torch.bfloat16, dev)
-    _typed(f"{name}: lse", lse, torch.float32, dev)
-    _need(q.dim() == 4 and q.shape[0] == B and q.shape[3] == 576 and q.is_contiguous(),
-          f"{name}: q must be a contiguous [B, s_q, H, 576]")
-    _, s_q, H, _ = q.shape
-    _need(lse.shape == (B, s_q, H) and lse.is_contiguous(), f"{name}: lse must be a contiguous [B, s_q, H]")
-    stride = _rows(f"{name}: weights", weights, torch.float32, dev, B)
-    _need(stride == weights.shape[1] or weights.shape[1] >= 64 * block_table.shape[1],
-          f"{name}: rows of weights that are a part of wider ones must have a slot for every entry of block_table")
-    scale = () if kv_scale is None else (float(kv_scale),)
-    with _on(dev):
-        _check(getattr(lib(), f"mla_{name}")(
-            _ptr(q), _ptr(lse), _ptr(kv_cache), *scale, kv_cache.shape[0], _ptr(block_table), block_table.shape[1],
-            _ptr(seqlens), B, s_q, H, float(softmax_scale), int(causal), _ptr(weights), stride, _stream(stream)),
-            f"mla_{name}")
+    dev, B, num_blocks, max_blocks = _paged(name, kv_cache, block_table, seqlens, kv_scale is not None)
+    _typed(name, "q", q, torch.bfloat16, dev)
+    _typed(name, "lse", lse, torch.float32, dev)
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != B or shape[3] != 576 or not q.is_contiguous():
+        raise ValueError(f"{name}: q must be a contiguous [B, s_q, H, 576]")
+    if lse.shape != shape[:3] or not lse.is_contiguous():
+        raise ValueError(f"{name}: lse must be a contiguous [B, s_q, H]")
+    stride = _rows(name, "weights", weights, torch.float32, dev, B, max_blocks)
+    pool = (kv_cache.data_ptr(),) if kv_scale is None else (kv_cache.data_ptr(), kv_scale)
+    _launch(dev, "mla_" + name, (
+        q.data_ptr(), lse.data_ptr(), *pool, num_blocks, block_table.data_ptr(), max_blocks, seqlens.data_ptr(), B,
+        shape[1], shape[2], softmax_scale, causal, weights.data_ptr(), stride), stream)
     return weights
 
 
@@ -550,33 +553,31 @@ def attn_weights_fp8(q, lse, kv_cache, kv_scale: float, block_table, seqlens, so
 
 def _evict(name, fp8, kv_cache, block_table, seqlens, weights, budget, sink, recent, arrival, width, new_seqlens, kept,
            weights_out, arrival_out, stream):
-    dev, B = _paged(name, kv_cache, block_table, seqlens, fp8)
-    w_stride = _rows(f"{name}: weights", weights, torch.float32, dev, B)
+    dev, B, num_blocks, max_blocks = _paged(name, kv_cache, block_table, seqlens, fp8)
+    w_stride = _rows(name, "weights", weights, torch.float32, dev, B, max_blocks)
     a_ptr, a_stride = None, 0
-    for t in (weights,) if arrival is None else (weights, arrival):
-        _need(B == 1 or t.stride(0) == t.shape[1] or t.shape[1] >= 64 * block_table.shape[1],
-              f"{name}: rows that are a part of wider ones must have a slot for every entry of block_table")
     if arrival is not None:
-        a_stride = _rows(f"{name}: arrival", arrival, torch.int32, dev, B)
-        a_ptr = _ptr(arrival)
+        a_stride = _rows(name, "arrival", arrival, torch.int32, dev, B, max_blocks)
+        a_ptr = arrival.data_ptr()
     if width is None:
-        width = weights.shape[1]
-    outs = []
-    for what, t, dtype, shape in (("new_seqlens", new_seqlens, torch.int32, (B,)), ("kept", kept, torch.int32, (B, width)),
-                                  ("weights_out", weights_out, torch.float32, (B, width)),
-                                  ("arrival_out", arrival_out, torch.int32, (B, width))):
+        width = weights.size(1)
+
+    def given(what, t, dtype, shape):
         if t is None:
-            t = torch.empty(shape, dtype=dtype, device=dev)
-        else:
-            _typed(f"{name}: {what}", t, dtype, dev)
-            _need(t.shape == shape and t.is_contiguous(), f"{name}: {what} must be a contiguous {list(shape)}")
-        outs.append(t)
-    with _on(dev):
-        _check(getattr(lib(), f"mla_{name}")(
-            _ptr(kv_cache), kv_cache.shape[0], _ptr(block_table), block_table.shape[1], _ptr(seqlens), B, _ptr(weights),
-            w_stride, a_ptr, a_stride, int(budget), int(sink), int(recent), *(_ptr(t) for t in outs), width,
-            _stream(stream)), f"mla_{name}")
-    return tuple(outs)
+            return torch.empty(shape, dtype=dtype, device=weights.device)
+        _typed(name, what, t, dtype, dev)
+        if tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{name}: {what} must be a contiguous {list(shape)}")
+        return t
+
+    outs = (given("new_seqlens", new_seqlens, torch.int32, (B,)), given("kept", kept, torch.int32, (B, width)),
+            given("weights_out", weights_out, torch.float32, (B, width)),
+            given("arrival_out", arrival_out, torch.int32, (B, width)))
+    _launch(dev, "mla_" + name, (
+        kv_cache.data_ptr(), num_blocks, block_table.data_ptr(), max_blocks, seqlens.data_ptr(), B, weights.data_ptr(),
+        w_stride, a_ptr, a_stride, budget, sink, recent, outs[0].data_ptr(), outs[1].data_ptr(), outs[2].data_ptr(),
+        outs[3].data_ptr(), width), stream)
+    return outs
 
 
 def evict(kv_cache, block_table, seqlens, weights, budget: int, sink: int = 0, recent: int = 0, arrival=None,

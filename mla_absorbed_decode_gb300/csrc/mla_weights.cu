@@ -43,8 +43,7 @@ struct WeightsParams {
 //    step (31 shuffles leave column l's sum in lane l), then four partial sums in shared memory, which
 //    a warp of its own adds to the weights: a fixed order, no atomics.
 //  * More than 128 rows: a cluster of ceil(rows / 128) CTAs walks the same pages, each with its row
-//    block, and shares their loads (multicast); the others hand their 64 sums a page to CTA 0 through
-//    distributed shared memory.
+//    block; the others hand their 64 sums a page to CTA 0 through distributed shared memory.
 //  * Work: all requests' pages in a row, with kSwitchPages for each request's start, cut evenly over the
 //    clusters that fit the GPU.  Each CTA finds its own piece from the lengths (no schedule, no metadata).
 constexpr int kWThreads = 352;                 // warp 0: TMA, 1: MMA, 2..9: exponentials, 10: sums
@@ -91,8 +90,7 @@ constexpr uint32_t weights_smem() { return WCfg<F8>::kOffShared + sizeof(WShared
 static_assert(weights_smem<false>() <= 232448 && weights_smem<true>() <= 232448, "shared memory per CTA");
 
 struct WMaps {
-  CUtensorMap kv;     // bf16: [chunk 0..8][row][64 dims]; FP8: [chunk 0..3][row][128 codes]; box: 64 rows of all
-                      // chunks, or of one where a cluster shares the page
+  CUtensorMap kv;     // bf16: [chunk 0..8][row][64 dims]; FP8: [chunk 0..3][row][128 codes]; box: all chunks of 64 rows
   CUtensorMap rope;   // FP8: [row][576 codes], box 128 codes x 64 rows (read at code 512)
   CUtensorMap q;      // [chunk 0..8][q row][64 dims], box kQRows rows
 };
@@ -102,9 +100,11 @@ __device__ __forceinline__ void w_abort(WShared& sh, int* status, uint32_t cl) {
   atomicCAS(status, 0, MLA_ERR_TIMEOUT);
   for (uint32_t r = 0; r < cl; ++r) st_cluster_u32(map_to_rank(smem_u32(const_cast<int*>(&sh.abort)), r), 1u);
 }
+// kCluster: arrivals come from other CTAs' threads, whose stores are read after the wait.
+template <bool kCluster>
 __device__ __noinline__ bool w_wait_slow(WShared& sh, uint32_t bar, uint32_t parity, int* status, uint32_t cl) {
   const uint64_t t0 = global_timer_ns();
-  while (!mbar_test_cluster(bar, parity)) {
+  while (!(kCluster ? mbar_test_cluster(bar, parity) : mbar_test(bar, parity))) {
     if (sh.abort) return false;
     if (global_timer_ns() - t0 > kTimeoutNs) {
       w_abort(sh, status, cl);
@@ -114,13 +114,15 @@ __device__ __noinline__ bool w_wait_slow(WShared& sh, uint32_t bar, uint32_t par
   return true;
 }
 // Bounded wait (0.5 s): false once this cluster has given up.
+template <bool kCluster = false>
 __device__ __forceinline__ bool w_wait(WShared& sh, uint64_t& bar, uint32_t parity, int* status, uint32_t cl) {
   const uint32_t a = smem_u32(&bar);
-  if (mbar_test_cluster(a, parity)) return true;
-  return w_wait_slow(sh, a, parity, status, cl);
+  if (kCluster ? mbar_test_cluster(a, parity) : mbar_test(a, parity)) return true;
+  return w_wait_slow<kCluster>(sh, a, parity, status, cl);
 }
+template <bool kCluster = false>
 __device__ __forceinline__ bool w_warp_wait(WShared& sh, uint64_t& bar, uint32_t parity, int* status, uint32_t cl) {
-  return __all_sync(0xffffffffu, w_wait(sh, bar, parity, status, cl));
+  return __all_sync(0xffffffffu, w_wait<kCluster>(sh, bar, parity, status, cl));
 }
 __device__ __noinline__ void w_drain(uint64_t& bar, uint32_t parity) {   // ignores the abort flag
   const uint32_t a = smem_u32(&bar);
@@ -210,29 +212,10 @@ __device__ __forceinline__ int block_of(const WeightsParams& p, int b, int k) { 
 }
 
 // --------------------------------------------------------------- producer --
-// The loads of a cluster: every CTA fetches its share of a page's chunks for all of them, so that a page
-// crosses from L2 to the SMs once a cluster.
-__device__ __forceinline__ void tma_load_3d_multicast(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y,
-                                                      int z, uint16_t mask, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint"
-      " [%0], [%1, {%3, %4, %5}], [%2], %6, %7;"
-      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "h"(mask), "l"(policy)
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_2d_multicast(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y,
-                                                      uint16_t mask, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint"
-      " [%0], [%1, {%3, %4}], [%2], %5, %6;"
-      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "h"(mask), "l"(policy) : "memory");
-}
-// Arrives on the barrier at this offset in every CTA of the mask once the MMAs issued so far are done.
-__device__ __forceinline__ void mma_commit_warp_multicast(uint32_t bar, uint16_t mask) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}"
-      :: "r"(bar), "h"(mask) : "memory");
+__device__ __forceinline__ uint64_t l2_policy_evict_normal() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
 }
 
 template <bool F8>
@@ -242,8 +225,10 @@ __device__ void w_producer(const WeightsParams& p, const WMaps& maps, WShared& s
   WWalk<C::kSwitchPages> walk(sh);
   WSegment s;
   uint32_t i = 0;
-  const uint64_t policy = l2_policy_evict_first();   // read once, by one SM or one cluster
-  const uint16_t mask = static_cast<uint16_t>((1u << cl) - 1);
+  // A page that one SM reads need not stay in L2 (50.5 us against 53.7 for 64 requests of 4096 tokens); one that the
+  // CTAs of a cluster read, each by itself, has to until the last of them (145 us against 176 for two
+  // query positions over 8192 tokens; 163 where they shared the loads by multicast).
+  const uint64_t policy = cl == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
   bool ok = true;
   auto stage_for = [&](uint32_t bytes) {   // waits for the next ring stage, which then expects `bytes`
     const uint32_t st = i % C::kStages;
@@ -268,17 +253,8 @@ __device__ void w_producer(const WeightsParams& p, const WMaps& maps, WShared& s
       if (!ok) break;
       const uint32_t dst = smem + st * C::kStageBytes, bar = smem_u32(&sh.full[st]);
       const int row = blk * kPageTokens;
-      if (cl == 1) {
-        tma_load_3d_hint(dst, &maps.kv, bar, 0, row, 0, policy);
-        if constexpr (F8) tma_load_2d_hint(dst + 4 * kChunk, &maps.rope, bar, kDimV, row, policy);
-      } else {
-        for (uint32_t c = rank; c < C::kKChunks; c += cl) {
-          if (F8 && c == 4)
-            tma_load_2d_multicast(dst + c * kChunk, &maps.rope, bar, kDimV, row, mask, policy);
-          else
-            tma_load_3d_multicast(dst + c * kChunk, &maps.kv, bar, 0, row, static_cast<int>(c), mask, policy);
-        }
-      }
+      tma_load_3d_hint(dst, &maps.kv, bar, 0, row, 0, policy);
+      if constexpr (F8) tma_load_2d_hint(dst + 4 * kChunk, &maps.rope, bar, kDimV, row, policy);
     }
   }
   const uint32_t flying = i < C::kStages ? i : C::kStages;   // loads still in flight land before the CTA may exit
@@ -297,12 +273,8 @@ __device__ void w_mma(const WeightsParams& p, WShared& sh, uint32_t smem, uint32
   bool ok = true;
   while (ok && walk.next(p, s)) {
     if (!(ok = w_warp_wait(sh, sh.q_full, seg++ & 1, p.status, cl))) break;
-    for (int j = 0; j < C::kQItems; ++j, ++i)   // the epilogue warps have read them: free, for every CTA's next load
-      if ((threadIdx.x & 31) < cl) {
-        const uint32_t bar = smem_u32(&sh.empty[i % C::kStages]);
-        if (cl == 1) mbar_arrive(bar);
-        else mbar_arrive_remote(map_to_rank(bar, threadIdx.x & 31));
-      }
+    for (int j = 0; j < C::kQItems; ++j, ++i)   // the epilogue warps have read them: q_full says so
+      if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&sh.empty[i % C::kStages]));
     for (int k = s.k0; k < s.k1; ++k, ++i, ++T) {
       const uint32_t st = i % C::kStages, sb = T % kSBufs;
       ok = w_warp_wait(sh, sh.s_empty[sb], ((T / kSBufs) & 1) ^ 1, p.status, cl) &&
@@ -328,10 +300,7 @@ __device__ void w_mma(const WeightsParams& p, WShared& sh, uint32_t smem, uint32
             mma_bf16_ts_warp(d, tmem + kQCol + c * 32 + j * 8, smem_desc_sw128(stage + c * kChunk + j * 32, 16, 1024),
                              idesc, (c | j) ? 1u : 0u);
       }
-      if (cl == 1)
-        mma_commit_warp(smem_u32(&sh.empty[st]));
-      else   // the next load into this stage of any CTA writes all of them
-        mma_commit_warp_multicast(smem_u32(&sh.empty[st]), static_cast<uint16_t>((1u << cl) - 1));
+      mma_commit_warp(smem_u32(&sh.empty[st]));
       mma_commit_warp(smem_u32(&sh.s_full[sb]));
     }
   }
@@ -522,17 +491,7 @@ __device__ void w_sum(const WeightsParams& p, WShared& sh, uint32_t cl, uint32_t
   while (walk.next(p, s)) {
     for (int k = s.k0; k < s.k1; ++k, ++T) {
       const uint32_t buf = T % kPartBufs, slot = T % kRecvSlots, ph = (T / kRecvSlots) & 1;
-      float* const w = p.weights + s.b * p.weights_stride + k * kPageTokens;
-      float old[2] = {0.f, 0.f};
-      bool store[2] = {false, false};
-      if (rank == 0) {   // read ahead of the page's sums
-        const bool page = block_of(p, s.b, k) >= 0;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          store[j] = page && k * kPageTokens + 32 * j + lane < s.n;
-          if (store[j]) old[j] = w[32 * j + lane];
-        }
-      }
+      const bool page = rank == 0 && block_of(p, s.b, k) >= 0;
       if (!w_warp_wait(sh, sh.part_full[buf], (T / kPartBufs) & 1, p.status, cl)) return;
       float sum[2];
 #pragma unroll
@@ -544,13 +503,13 @@ __device__ void w_sum(const WeightsParams& p, WShared& sh, uint32_t cl, uint32_t
       if (lane == 0) mbar_arrive(smem_u32(&sh.part_empty[buf]));
       if (cl > 1) {
         if (rank != 0) {
-          if (!w_warp_wait(sh, sh.credit[slot], ph ^ 1, p.status, cl)) return;
+          if (!w_warp_wait<true>(sh, sh.credit[slot], ph ^ 1, p.status, cl)) return;
 #pragma unroll
           for (int j = 0; j < 2; ++j)
             st_cluster_u32(map_to_rank(smem_u32(&sh.recv[slot][rank - 1][32 * j + lane]), 0), __float_as_uint(sum[j]));
           mbar_arrive_remote(map_to_rank(smem_u32(&sh.recv_full[slot]), 0));   // releases this lane's two sums
         } else {
-          if (!w_warp_wait(sh, sh.recv_full[slot], ph, p.status, cl)) return;
+          if (!w_warp_wait<true>(sh, sh.recv_full[slot], ph, p.status, cl)) return;
           for (uint32_t o = 1; o < cl; ++o)
 #pragma unroll
             for (int j = 0; j < 2; ++j) sum[j] += sh.recv[slot][o - 1][32 * j + lane];
@@ -558,9 +517,13 @@ __device__ void w_sum(const WeightsParams& p, WShared& sh, uint32_t cl, uint32_t
           if (lane > 0 && static_cast<uint32_t>(lane) < cl) mbar_arrive_remote(map_to_rank(smem_u32(&sh.credit[slot]), lane));
         }
       }
+      // one addition a token and call, so the order of the calls alone decides the result; as a reduction at L2
+      // it costs this warp no round trip to memory (which had set the period of a page)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        if (store[j]) w[32 * j + lane] = old[j] + sum[j];
+      for (int j = 0; j < 2; ++j) {
+        const int t = k * kPageTokens + 32 * j + lane;
+        if (page && t < s.n) atomicAdd(p.weights + s.b * p.weights_stride + t, sum[j]);
+      }
     }
   }
 }
@@ -586,7 +549,7 @@ mla_attn_weights_kernel(const __grid_constant__ WMaps maps, const __grid_constan
     sh.abort = 0;
     for (int j = 0; j < C::kStages; ++j) {
       mbar_init(smem_u32(&sh.full[j]), 1);
-      mbar_init(smem_u32(&sh.empty[j]), cl);
+      mbar_init(smem_u32(&sh.empty[j]), 1);
     }
     for (int j = 0; j < kSBufs; ++j) {
       mbar_init(smem_u32(&sh.s_full[j]), 1);
@@ -700,7 +663,7 @@ mla_status_t weights_setup(WeightsDevice** out) {
 }
 
 template <bool F8>
-bool encode_maps(WMaps* m, const void* kv, int64_t num_blocks, const void* q, int64_t q_rows, int cl) {
+bool encode_maps(WMaps* m, const void* kv, int64_t num_blocks, const void* q, int64_t q_rows) {
   using C = WCfg<F8>;
   const cuuint32_t es[3] = {1, 1, 1};
   auto encode = [&](CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,
@@ -713,12 +676,12 @@ bool encode_maps(WMaps* m, const void* kv, int64_t num_blocks, const void* q, in
   bool ok;
   if (F8) {
     const cuuint64_t dims[3] = {128, rows, 4}, strides[2] = {kDimQK, 128}, rdims[2] = {kDimQK, rows}, rstrides[1] = {kDimQK};
-    const cuuint32_t box[3] = {128, kPageTokens, cl > 1 ? 1u : 4u}, rbox[2] = {128, kPageTokens};
+    const cuuint32_t box[3] = {128, kPageTokens, 4}, rbox[2] = {128, kPageTokens};
     ok = encode(&m->kv, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, kv, dims, strides, box) &&
          encode(&m->rope, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, kv, rdims, rstrides, rbox);
   } else {
     const cuuint64_t dims[3] = {64, rows, 9}, strides[2] = {kDimQK * 2, 128};
-    const cuuint32_t box[3] = {64, kPageTokens, cl > 1 ? 1u : 9u};
+    const cuuint32_t box[3] = {64, kPageTokens, 9};
     ok = encode(&m->kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, kv, dims, strides, box);
   }
   const cuuint64_t qdims[3] = {64, static_cast<cuuint64_t>(q_rows), 9}, qstrides[2] = {kDimQK * 2, 128};
@@ -771,8 +734,8 @@ mla_status_t weights_impl(const mla_bf16_t* q, const float* lse, const void* kv_
   WMaps maps = {};
   const int cl = (p.rows + kRowsPerPair - 1) / kRowsPerPair;
   const int64_t q_rows = static_cast<int64_t>(B) * p.rows;
-  if (!(fp8 ? encode_maps<true>(&maps, kv_cache, num_blocks, q, q_rows, cl)
-            : encode_maps<false>(&maps, kv_cache, num_blocks, q, q_rows, cl)))
+  if (!(fp8 ? encode_maps<true>(&maps, kv_cache, num_blocks, q, q_rows)
+            : encode_maps<false>(&maps, kv_cache, num_blocks, q, q_rows)))
     return MLA_ERR_CUDA;
   // no more clusters than pages there can be
   const int64_t most = static_cast<int64_t>(B) * ((p.slots + kPageTokens - 1) / kPageTokens);
