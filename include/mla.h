@@ -422,7 +422,7 @@ mla_status_t mla_attn_weights_fp8(const mla_bf16_t* q, const float* lse, const u
  *  arrival_out    int32 [B, width] or NULL: the numbers moved along; e + (j - m) for j >= m, the
  *                 numbers of the tokens that mla_cache_append will put there
  *  width          >= min(budget, 64 max_blocks, weights_stride)
- * weights_out and arrival_out must not overlap weights or arrival.  At most 524288 slots a request:
+ * weights_out and arrival_out must not overlap weights or arrival.  At most 262144 slots a request:
  * min(64 max_blocks, weights_stride) beyond that is MLA_ERR_UNSUPPORTED.  A request whose length
  * is out of range is reported as MLA_ERR_DEVICE_BOUNDS and treated as empty; a row whose page is
  * out of range is reported and not copied.  Two kernels on `stream`.  Async on stream. */

@@ -181,9 +181,13 @@ __global__ void __launch_bounds__(128) mla_append_kernel(const __grid_constant__
 }
 
 // ------------------------------------------------------------------ evict --
-constexpr int kEvictMaxSlots = 524288;  // a request's keep mask and its prefix counts fit shared memory
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelDigitBits = 11, kSelBins = 1 << kSelDigitBits;   // three digits: 11, 11 and 10 bits
+constexpr int kSelMaxCtas = 8;          // CTAs of a request's cluster
+constexpr int kSelSlotsPerCta = 4096;   // a request gets another CTA for every so many slots
+constexpr int kEvictMaxSlots = 262144;  // 32768 keys a CTA: 128 KiB of shared memory
+constexpr int kMoveSlots = 16;          // slots of one warp of the move kernel
 
 struct EvictParams {
   void* kv;
@@ -196,6 +200,7 @@ struct EvictParams {
   const int32_t* arrival;
   int64_t arrival_stride;
   int budget, sink, recent, slots;
+  int sel_ctas, sel_slice;  // selection: CTAs a request and their slots (a multiple of 32)
   int32_t* new_seqlens;
   int32_t* kept;
   float* weights_out;
@@ -212,146 +217,218 @@ __device__ __forceinline__ uint32_t weight_order(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// One block per request.  The m-th largest key is found by a radix selection (four passes of 8
-// bits over the keys), ties are taken from the lowest slot on, and the keep mask and its prefix
-// counts (one bit and 1/32 word a slot, in shared memory) give every free slot its source.
-__global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const __grid_constant__ EvictParams p) {
-  extern __shared__ uint32_t sel_smem[];          // mask [words], then prefix [words + 1]
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t warp_sum[kSelWarps + 1];
-  __shared__ uint32_t s_key, s_left;
-  __shared__ int s_max;
+__device__ __forceinline__ uint32_t ld_cluster_u32(const uint32_t* p, uint32_t rank) {   // CTA `rank`'s copy of *p
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(map_to_rank(smem_u32(p), rank)) : "memory");
+  return v;
+}
+
+struct SelShared {
+  uint32_t hist[3][kSelBins];
+  uint32_t warp_sum[kSelWarps];
+  uint32_t digit, need;         // of the digit in which the m-th largest key lies
+  uint32_t kept, below;         // this CTA's kept slots; those of them below slot m
+  int newest;                   // this CTA's largest arrival number
+};
+// Dynamic shared memory of a CTA with `slice` slots: keys (later the list of sources), keep mask, prefix counts.
+__host__ __device__ constexpr size_t sel_smem(int slice) {
+  return sizeof(SelShared) + sizeof(uint32_t) * (static_cast<size_t>(slice) + 2 * (static_cast<size_t>(slice) / 32));
+}
+
+// Exclusive sum of v over the CTA's threads; *total gets the sum of all.
+__device__ __forceinline__ uint32_t scan_cta(uint32_t v, uint32_t* warp_sum, uint32_t* total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
+  }
+  if (lane == 31) warp_sum[warp] = s;
+  __syncthreads();
+  uint32_t w = warp_sum[lane], ws = w;   // kSelWarps == 32: every warp scans the warps' sums for itself
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, ws, o);
+    if (lane >= o) ws += y;
+  }
+  *total = __shfl_sync(0xffffffffu, ws, 31);
+  const uint32_t before = __shfl_sync(0xffffffffu, ws - w, warp);
+  __syncthreads();
+  return before + s - v;
+}
+static_assert(kSelWarps == 32, "scan_cta");
+
+// One cluster of `cl` CTAs per request, each with a slice of its slots, whose keys stay in shared memory.  The m-th
+// largest key is found by a radix selection of three digits (the CTAs' histograms are added up through
+// distributed shared memory), ties are taken from the lowest slot on, and from the keep mask every staying
+// token past slot m is written into a list in rank order, from which the free slots below m take theirs.
+// Latency-bound (a few KB a CTA): what counts is the number of barriers, one of the cluster a digit and
+// four more.
+__global__ void __launch_bounds__(kSelThreads, 1) mla_evict_select_kernel(const __grid_constant__ EvictParams p) {
+  extern __shared__ __align__(16) uint8_t sel_dyn[];
+  SelShared& sh = *reinterpret_cast<SelShared*>(sel_dyn);
+  uint32_t* keys = reinterpret_cast<uint32_t*>(sel_dyn + sizeof(SelShared));
+  const int cl = p.sel_ctas, slice_max = p.sel_slice, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint32_t* mask = keys + slice_max;
+  uint32_t* prefix = mask + slice_max / 32;
+  const int b = static_cast<int>(blockIdx.x) / cl;
+  const uint32_t rank = cl > 1 ? cluster_ctarank() : 0;
+  auto sync = [&] {
+    if (cl > 1) cluster_sync();
+    else __syncthreads();
+  };
+  for (int i = tid; i < 3 * kSelBins; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
+  if (tid == 0) sh.newest = -1;
   griddep_wait();
   griddep_launch_dependents();
-  const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int n = p.seqlens[b];   // (new_seqlens may be the same array: not through the read-only path)
   if (n < 0 || n > p.slots) {
-    if (tid == 0) atomicCAS(p.status, 0, MLA_ERR_DEVICE_BOUNDS);
+    if (tid == 0 && rank == 0) atomicCAS(p.status, 0, MLA_ERR_DEVICE_BOUNDS);
     n = 0;
   }
   const int m = min(n, p.budget);
   const float* w = p.weights + b * p.weights_stride;
   const int32_t* arr = p.arrival ? p.arrival + b * p.arrival_stride : nullptr;
-  const int words = (n + 31) / 32;
-  uint32_t* mask = sel_smem;
-  uint32_t* prefix = sel_smem + (p.slots + 31) / 32;
+  // slices of whole 32-slot words, as even as that allows
+  const int slice = min(slice_max, (n + 32 * cl - 1) / (32 * cl) * 32);
+  const int t0 = min(n, static_cast<int>(rank) * slice), count = min(n, t0 + slice) - t0;
+  const int words = (count + 31) / 32;
   auto arrival_of = [&](int t) { return arr ? __ldg(arr + t) : t; };
 
   // e = 1 + the largest arrival number
-  if (tid == 0) s_max = -1;
-  __syncthreads();
+  int64_t e = n;
   if (arr) {
+    __syncthreads();
     int top = -1;
-    for (int t = tid; t < n; t += kSelThreads) top = max(top, __ldg(arr + t));
-    top = __reduce_max_sync(0xffffffffu, top);
-    if (lane == 0) atomicMax(&s_max, top);
-  } else if (tid == 0) {
-    s_max = n - 1;
-  }
-  __syncthreads();
-  const int64_t e = static_cast<int64_t>(s_max) + 1;
-  auto key_of = [&](int t) {
-    const int a = arrival_of(t);
-    return (a < p.sink || a >= e - p.recent) ? 0xffffffffu : weight_order(__ldg(w + t));
-  };
-
-  uint32_t cut = 0, ties = 0;   // keep key > cut, and the first `ties` slots with key == cut
-  if (m < n) {
-    uint32_t left = static_cast<uint32_t>(m);
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
-      const uint32_t high = shift == 24 ? 0u : ~0u << (shift + 8);
-      for (int t = tid; t < n; t += kSelThreads) {
-        const uint32_t k = key_of(t);
-        if (((k ^ cut) & high) == 0) atomicAdd(&hist[(k >> shift) & 255u], 1u);
-      }
-      __syncthreads();
-      if (tid == 0) {   // the digit in which the m-th largest key lies
-        uint32_t need = left;
-        int d = 255;
-        while (d > 0 && hist[d] < need) need -= hist[d--];
-        s_key = cut | (static_cast<uint32_t>(d) << shift);
-        s_left = need;
-      }
-      __syncthreads();
-      cut = s_key;
-      left = s_left;
+    for (int i = tid; i < count; i += kSelThreads) {
+      const int a = __ldg(arr + t0 + i);
+      keys[i] = static_cast<uint32_t>(a);
+      top = max(top, a);
     }
-    ties = left;
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) atomicMax(&sh.newest, top);
+    sync();
+    int newest = -1;
+    for (int r = 0; r < cl; ++r)
+      newest = max(newest, cl > 1 ? static_cast<int>(ld_cluster_u32(reinterpret_cast<uint32_t*>(&sh.newest), r)) : sh.newest);
+    e = static_cast<int64_t>(newest) + 1;
+  }
+  uint32_t cut = 0, ties = 0;   // keep key > cut, and the first `ties` slots with key == cut
+  uint32_t tie_first = 0;       // ties in the CTAs before this one
+  if (m < n) {
+    for (int i = tid; i < count; i += kSelThreads) {
+      const int a = arr ? static_cast<int>(keys[i]) : t0 + i;
+      const uint32_t k = (a < p.sink || a >= e - p.recent) ? 0xffffffffu : weight_order(__ldg(w + t0 + i));
+      keys[i] = k;
+    }
+    uint32_t need = static_cast<uint32_t>(m);
+    int shift = 32;
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+      const int bits = pass < 2 ? kSelDigitBits : 32 - 2 * kSelDigitBits;
+      const uint32_t high = pass == 0 ? 0u : ~0u << shift;   // the digits found so far
+      shift -= bits;
+      uint32_t* hist = sh.hist[pass];
+      __syncthreads();   // (the first digit: keys and zeros are in place)
+      for (int i = tid; i < count; i += kSelThreads) {
+        const uint32_t k = keys[i];
+        if (((k ^ cut) & high) == 0) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
+      }
+      sync();
+      // bins in descending order, two a thread
+      uint32_t bin[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int d = kSelBins - 1 - (2 * tid + j);
+        bin[j] = 0;
+        for (int r = 0; r < cl; ++r) bin[j] += cl > 1 ? ld_cluster_u32(&hist[d], r) : hist[d];
+      }
+      uint32_t all;
+      uint32_t above = scan_cta(bin[0] + bin[1], sh.warp_sum, &all);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (above < need && need <= above + bin[j]) {
+          sh.digit = static_cast<uint32_t>(kSelBins - 1 - (2 * tid + j));
+          sh.need = need - above;
+        }
+        above += bin[j];
+      }
+      __syncthreads();
+      cut |= sh.digit << shift;
+      need = sh.need;
+    }
+    ties = need;
+    for (uint32_t r = 0; r < rank; ++r) tie_first += ld_cluster_u32(&sh.hist[2][cut & ((1u << (32 - 2 * kSelDigitBits)) - 1u)], r);
   }
 
-  // keep mask: each warp walks a run of words; ties before its run are counted first
+  // keep mask: a warp walks a run of words; ties before the run are counted first
   const int run = (words + kSelWarps - 1) / kSelWarps;
   const int w0 = min(words, warp * run), w1 = min(words, w0 + run);
-  auto scan_warps = [&](uint32_t v) {   // exclusive sum over the warps of lane 0's v; total in warp_sum[kSelWarps]
-    if (lane == 0) warp_sum[warp] = v;
-    __syncthreads();
-    if (warp == 0) {
-      const uint32_t x = warp_sum[lane];
-      uint32_t s = x;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += y;
-      }
-      warp_sum[lane] = s - x;
-      if (lane == 31) warp_sum[kSelWarps] = s;
-    }
-    __syncthreads();
-    const uint32_t r = warp_sum[warp];
-    __syncthreads();
-    return r;
-  };
-  uint32_t tie_rank = 0;
+  uint32_t tie_rank = tie_first, all;
   if (m < n) {
     uint32_t mine = 0;
-    for (int i = w0; i < w1; ++i) {
-      const int t = i * 32 + lane;
-      mine += __popc(__ballot_sync(0xffffffffu, t < n && key_of(t) == cut));
-    }
-    tie_rank = scan_warps(mine);
+    for (int i = w0 * 32 + lane; i < w1 * 32; i += 32) mine += i < count && keys[i] == cut;
+    tie_rank += scan_cta(mine, sh.warp_sum, &all);
+    tie_rank = __shfl_sync(0xffffffffu, tie_rank, 0);   // that of the run's first lane: ties before the run
   }
-  uint32_t kept_mine = 0;
+  uint32_t kept = 0;
   for (int i = w0; i < w1; ++i) {
     const int t = i * 32 + lane;
-    bool keep = t < n;
+    bool keep = t < count;
     if (m < n) {
-      const uint32_t k = t < n ? key_of(t) : 0u;
-      const bool tie = t < n && k == cut;
+      const uint32_t k = t < count ? keys[t] : 0u;
+      const bool tie = t < count && k == cut;
       const uint32_t tied = __ballot_sync(0xffffffffu, tie);
-      keep = t < n && (k > cut || (tie && tie_rank + __popc(tied & ((1u << lane) - 1u)) < ties));
+      keep = t < count && (k > cut || (tie && tie_rank + __popc(tied & ((1u << lane) - 1u)) < ties));
       tie_rank += __popc(tied);
     }
-    const uint32_t bits = __ballot_sync(0xffffffffu, keep);
-    if (lane == 0) {
-      mask[i] = bits;
-      prefix[i] = kept_mine;   // within the warp's run
-    }
-    kept_mine += __popc(bits);
+    const uint32_t word = __ballot_sync(0xffffffffu, keep);
+    if (lane == 0) mask[i] = word, prefix[i] = kept;   // prefix: within the run so far
+    kept += __popc(word);
   }
-  const uint32_t before = scan_warps(kept_mine);
-  for (int i = w0 + lane; i < w1; i += 32) prefix[i] += before;
+  const uint32_t before_run = __shfl_sync(0xffffffffu, scan_cta(lane == 0 ? kept : 0u, sh.warp_sum, &all), 0);
+  for (int i = w0 + lane; i < w1; i += 32) prefix[i] += before_run;
   __syncthreads();
-
-  // outputs: slot j keeps its token, or takes that of the next source
-  auto kept_before = [&](int t) {   // kept slots below t
-    return t >= words * 32 ? static_cast<uint32_t>(m) : prefix[t >> 5] + __popc(mask[t >> 5] & ((1u << (t & 31)) - 1u));
+  auto kept_before = [&](int t) {   // of this CTA's slots, below its slot t
+    return t >= words * 32 ? all : prefix[t >> 5] + __popc(mask[t >> 5] & ((1u << (t & 31)) - 1u));
   };
-  const uint32_t below = kept_before(m);
-  for (int64_t j = tid; j < p.width; j += kSelThreads) {
+  const int m_here = max(0, min(count, m - t0));   // slots below m of this CTA
+  if (tid == 0) sh.kept = all, sh.below = kept_before(m_here);
+  sync();
+  uint32_t first = 0, below = 0;   // kept slots of the CTAs before this one; kept slots below m
+  for (int r = 0; r < cl; ++r) {
+    if (r < static_cast<int>(rank)) first += ld_cluster_u32(&sh.kept, r);
+    below += cl > 1 ? ld_cluster_u32(&sh.below, r) : sh.below;
+  }
+  // sources in rank order: entry i of the list lies in CTA i / slice_max (the keys are no longer needed)
+  for (int i = (m_here / 32 + warp) * 32 + lane; i < words * 32; i += kSelThreads) {
+    if (i >= m_here && ((mask[i >> 5] >> (i & 31)) & 1u)) {
+      const uint32_t at = first + kept_before(i) - below;
+      uint32_t* entry = keys + at % slice_max;
+      if (cl > 1) st_cluster_u32(map_to_rank(smem_u32(entry), at / slice_max), static_cast<uint32_t>(t0 + i));
+      else *entry = static_cast<uint32_t>(i);
+    }
+  }
+  if (cl > 1) {
+    if (tid == 0) sh.need = first;   // the CTA's first kept slot's rank, for the outputs below
+  }
+  sync();
+
+  // outputs, spread over the cluster: slot j keeps its token, or takes that of the next source
+  for (int64_t j = static_cast<int64_t>(rank) * kSelThreads + tid; j < p.width; j += static_cast<int64_t>(cl) * kSelThreads) {
     int src = -1;
     if (j < m) {
       const int t = static_cast<int>(j);
       src = t;
-      if (!((mask[t >> 5] >> (t & 31)) & 1u)) {
-        const uint32_t rank = below + (static_cast<uint32_t>(t) - kept_before(t));   // the rank-th kept slot
-        int lo = m >> 5, hi = words - 1;   // the last word with prefix <= rank
-        while (lo < hi) {
-          const int mid = (lo + hi + 1) >> 1;
-          if (prefix[mid] <= rank) lo = mid; else hi = mid - 1;
-        }
-        src = lo * 32 + static_cast<int>(__fns(mask[lo], 0, static_cast<int>(rank - prefix[lo]) + 1));
+      const uint32_t r = cl > 1 ? static_cast<uint32_t>(t / slice) : 0u;
+      const int at = t - static_cast<int>(r) * slice;
+      const uint32_t word = cl > 1 ? ld_cluster_u32(&mask[at >> 5], r) : mask[at >> 5];
+      if (!((word >> (at & 31)) & 1u)) {
+        const uint32_t kept_below = (cl > 1 ? ld_cluster_u32(&sh.need, r) + ld_cluster_u32(&prefix[at >> 5], r)
+                                            : prefix[at >> 5]) + __popc(word & ((1u << (at & 31)) - 1u));
+        const uint32_t hole = static_cast<uint32_t>(t) - kept_below;
+        src = static_cast<int>(cl > 1 ? ld_cluster_u32(&keys[hole % slice_max], hole / slice_max) : keys[hole]);
       }
     }
     const int64_t at = b * p.width + j;
@@ -359,21 +436,22 @@ __global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const __g
     p.weights_out[at] = src >= 0 ? __ldg(w + src) : 0.f;
     if (p.arrival_out) p.arrival_out[at] = src >= 0 ? arrival_of(src) : static_cast<int32_t>(e + (j - m));
   }
-  if (tid == 0) p.new_seqlens[b] = m;   // last: it may be the array that the lengths came from
+  if (cl > 1) cluster_sync();   // no CTA leaves while another reads its shared memory
+  if (tid == 0 && rank == 0) p.new_seqlens[b] = m;   // last: it may be the array that the lengths came from
 }
 
-// Copies the rows of moved tokens.  A warp takes 32 slots; sources lie at or past the new length
-// and targets below it, so no row is both.
+// Copies the rows of moved tokens: 16-byte units, two rows in flight a warp.  A warp takes kMoveSlots slots; sources
+// lie at or past the new length and targets below it, so no row is both.
 template <int kRowBytes>
 __global__ void __launch_bounds__(256) mla_evict_move_kernel(const __grid_constant__ EvictParams p) {
   griddep_wait();
   griddep_launch_dependents();
-  constexpr int kUnits = kRowBytes / 16;
+  constexpr int kUnits = kRowBytes / 16, kEach = (kUnits + 31) / 32;
   const int b = blockIdx.y, lane = threadIdx.x & 31;
-  const int64_t j = (static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * 32 + lane;
+  const int64_t j = (static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * kMoveSlots + lane;
   const int top = min(p.budget, p.slots);
   int src = -1;
-  if (j < top) src = p.kept[b * p.width + j];
+  if (lane < kMoveSlots && j < top) src = p.kept[b * p.width + j];
   auto row_of = [&](int t) -> int64_t {
     const int blk = __ldg(p.block_table + static_cast<int64_t>(b) * p.max_blocks + t / kPageTokens);
     return blk >= 0 && blk < p.num_blocks ? static_cast<int64_t>(blk) * kPageTokens + t % kPageTokens : -1;
@@ -388,13 +466,27 @@ __global__ void __launch_bounds__(256) mla_evict_move_kernel(const __grid_consta
     }
   }
   uint32_t todo = __ballot_sync(0xffffffffu, from >= 0);
+  uint8_t* kv = static_cast<uint8_t*>(p.kv);
   while (todo) {
-    const int l = __ffs(todo) - 1;
-    todo &= todo - 1;
-    const int64_t f = __shfl_sync(0xffffffffu, from, l), t = __shfl_sync(0xffffffffu, to, l);
-    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.kv) + f * kRowBytes);
-    uint4* d = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.kv) + t * kRowBytes);
-    for (int u = lane; u < kUnits; u += 32) d[u] = s[u];
+    uint4 v[2][kEach];
+    int64_t t[2];
+    bool have[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      have[r] = todo != 0;
+      const int l = have[r] ? __ffs(todo) - 1 : 0;
+      todo &= todo - 1;
+      const int64_t f = __shfl_sync(0xffffffffu, from, l);
+      t[r] = __shfl_sync(0xffffffffu, to, l);
+#pragma unroll
+      for (int u = 0; u < kEach; ++u)
+        if (have[r] && u * 32 + lane < kUnits) v[r][u] = *reinterpret_cast<const uint4*>(kv + f * kRowBytes + (u * 32 + lane) * 16);
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int u = 0; u < kEach; ++u)
+        if (have[r] && u * 32 + lane < kUnits) *reinterpret_cast<uint4*>(kv + t[r] * kRowBytes + (u * 32 + lane) * 16) = v[r][u];
   }
 }
 
@@ -527,18 +619,27 @@ mla_status_t evict_impl(void* kv_cache, bool fp8, int64_t num_blocks, const int3
   p.width = width;
   p.status = device_status_word();
   if (!p.status) return MLA_ERR_CUDA;
-  const size_t smem = (2 * ((static_cast<size_t>(slots) + 31) / 32) + 1) * sizeof(uint32_t);
-  if (smem > 40 * 1024 &&
-      cudaFuncSetAttribute(mla_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>((2 * (kEvictMaxSlots / 32) + 1) * sizeof(uint32_t))) != cudaSuccess)
+  int cl = 1;
+  while (cl < kSelMaxCtas && static_cast<int64_t>(cl) * kSelSlotsPerCta < slots) cl *= 2;
+  p.sel_ctas = cl;
+  p.sel_slice = static_cast<int>((slots + 32 * cl - 1) / (32 * cl) * 32);
+  const size_t smem = sel_smem(p.sel_slice);
+  if (smem > 48 * 1024 && cudaFuncSetAttribute(mla_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(sel_smem(kEvictMaxSlots / kSelMaxCtas))) != cudaSuccess)
     return MLA_ERR_CUDA;
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t sel = pdl_config(dim3(static_cast<unsigned>(B)), dim3(kSelThreads), smem, cs, attr);
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t sel = pdl_config(dim3(static_cast<unsigned>(B * cl)), dim3(kSelThreads), smem, cs, attr);
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cl);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  sel.numAttrs = cl > 1 ? 2 : 1;
   if (cudaLaunchKernelEx(&sel, mla_evict_select_kernel, p) != cudaSuccess) return MLA_ERR_CUDA;
   const int64_t top = budget < slots ? budget : slots;
-  const cudaLaunchConfig_t mv =
-      pdl_config(dim3(static_cast<unsigned>((top + 255) / 256), static_cast<unsigned>(B)), dim3(256), 0, cs, attr);
+  constexpr int kMoveBlock = 8 * kMoveSlots;   // slots of a block's 8 warps
+  const cudaLaunchConfig_t mv = pdl_config(dim3(static_cast<unsigned>((top + kMoveBlock - 1) / kMoveBlock), static_cast<unsigned>(B)),
+                                           dim3(256), 0, cs, attr);
   const cudaError_t e = fp8 ? cudaLaunchKernelEx(&mv, mla_evict_move_kernel<kDimQK>, p)
                             : cudaLaunchKernelEx(&mv, mla_evict_move_kernel<kDimQK * 2>, p);
   return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
