@@ -214,7 +214,7 @@ struct EvictParams {
   const int32_t* arrival;
   int64_t arrival_stride;
   int budget, sink, recent, slots;
-  int sel_ctas, sel_slice;  // selection: CTAs a request and their slots (a multiple of 32)
+  int sel_slice;            // selection: slots of a CTA (a multiple of 32)
   int32_t* new_seqlens;
   int32_t* kept;
   float* weights_out;
@@ -237,8 +237,18 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(const uint32_t* p, uint32_t r
   return v;
 }
 
+__device__ __forceinline__ uint2 ld_cluster_v2(const uint32_t* p, uint32_t rank) {
+  uint2 v;
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(map_to_rank(smem_u32(p), rank)) : "memory");
+  return v;
+}
+// Asynchronous copy of 4 bytes global -> shared.
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
 struct SelShared {
-  uint32_t hist[3][kSelBins];
+  uint32_t hist[3][kSelBins];   // bins in descending order of their digit
   uint32_t warp_sum[kSelWarps];
   uint32_t digit, need;         // of the digit in which the m-th largest key lies
   uint32_t kept, below;         // this CTA's kept slots; those of them below slot m
@@ -279,11 +289,12 @@ static_assert(kSelWarps == 32, "scan_cta");
 // token past slot m is written into a list in rank order, from which the free slots below m take theirs.
 // Latency-bound (a few KB a CTA): what counts is the number of barriers, one of the cluster a digit and
 // four more.
+template <int cl>
 __global__ void __launch_bounds__(kSelThreads, 1) mla_evict_select_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ __align__(16) uint8_t sel_dyn[];
   SelShared& sh = *reinterpret_cast<SelShared*>(sel_dyn);
   uint32_t* keys = reinterpret_cast<uint32_t*>(sel_dyn + sizeof(SelShared));
-  const int cl = p.sel_ctas, slice_max = p.sel_slice, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int slice_max = p.sel_slice, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t* mask = keys + slice_max;
   uint32_t* prefix = mask + slice_max / 32;
   const int b = static_cast<int>(blockIdx.x) / cl;
@@ -315,15 +326,14 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_evict_select_kernel(const 
   if (arr) {
     __syncthreads();
     int top = -1;
-    for (int i = tid; i < count; i += kSelThreads) {
-      const int a = __ldg(arr + t0 + i);
-      keys[i] = static_cast<uint32_t>(a);
-      top = max(top, a);
-    }
+    for (int i = tid; i < count; i += kSelThreads) cp_async4(keys + i, w + t0 + i);   // each for the same thread below
+#pragma unroll 8
+    for (int i = tid; i < count; i += kSelThreads) top = max(top, __ldg(arr + t0 + i));
     top = __reduce_max_sync(0xffffffffu, top);
     if (lane == 0) atomicMax(&sh.newest, top);
     sync();
     int newest = -1;
+#pragma unroll
     for (int r = 0; r < cl; ++r)
       newest = max(newest, cl > 1 ? static_cast<int>(ld_cluster_u32(reinterpret_cast<uint32_t*>(&sh.newest), r)) : sh.newest);
     e = static_cast<int64_t>(newest) + 1;
@@ -331,10 +341,12 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_evict_select_kernel(const 
   uint32_t cut = 0, ties = 0;   // keep key > cut, and the first `ties` slots with key == cut
   uint32_t tie_first = 0;       // ties in the CTAs before this one
   if (m < n) {
+    cp_async_wait_all();
+#pragma unroll 8
     for (int i = tid; i < count; i += kSelThreads) {
-      const int a = arr ? static_cast<int>(keys[i]) : t0 + i;
-      const uint32_t k = (a < p.sink || a >= e - p.recent) ? 0xffffffffu : weight_order(__ldg(w + t0 + i));
-      keys[i] = k;
+      const int a = arrival_of(t0 + i);
+      const float weight = arr ? __uint_as_float(keys[i]) : __ldg(w + t0 + i);
+      keys[i] = (a < p.sink || a >= e - p.recent) ? 0xffffffffu : weight_order(weight);
     }
     uint32_t need = static_cast<uint32_t>(m);
     int shift = 32;
@@ -347,16 +359,18 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_evict_select_kernel(const 
       __syncthreads();   // (the first digit: keys and zeros are in place)
       for (int i = tid; i < count; i += kSelThreads) {
         const uint32_t k = keys[i];
-        if (((k ^ cut) & high) == 0) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
+        if (((k ^ cut) & high) == 0) atomicAdd(&hist[kSelBins - 1 - ((k >> shift) & ((1u << bits) - 1u))], 1u);
       }
       sync();
       // bins in descending order, two a thread
-      uint32_t bin[2];
+      uint32_t bin[2] = {hist[2 * tid], hist[2 * tid + 1]};
+      if (cl > 1) {
+        uint2 part[cl];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int d = kSelBins - 1 - (2 * tid + j);
-        bin[j] = 0;
-        for (int r = 0; r < cl; ++r) bin[j] += cl > 1 ? ld_cluster_u32(&hist[d], r) : hist[d];
+        for (int r = 0; r < cl; ++r) part[r] = ld_cluster_v2(&hist[2 * tid], r);
+        bin[0] = bin[1] = 0;
+#pragma unroll
+        for (int r = 0; r < cl; ++r) bin[0] += part[r].x, bin[1] += part[r].y;
       }
       uint32_t all;
       uint32_t above = scan_cta(bin[0] + bin[1], sh.warp_sum, &all);
@@ -373,7 +387,14 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_evict_select_kernel(const 
       need = sh.need;
     }
     ties = need;
-    for (uint32_t r = 0; r < rank; ++r) tie_first += ld_cluster_u32(&sh.hist[2][cut & ((1u << (32 - 2 * kSelDigitBits)) - 1u)], r);
+    if (cl > 1) {
+      const uint32_t* bin = &sh.hist[2][kSelBins - 1 - (cut & ((1u << (32 - 2 * kSelDigitBits)) - 1u))];
+#pragma unroll
+      for (int r = 0; r < cl; ++r) {
+        const uint32_t k = ld_cluster_u32(bin, r);
+        tie_first += r < static_cast<int>(rank) ? k : 0u;
+      }
+    }
   }
 
   // keep mask: a warp walks a run of words; ties before the run are counted first
@@ -411,8 +432,10 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_evict_select_kernel(const 
   if (tid == 0) sh.kept = all, sh.below = kept_before(m_here);
   sync();
   uint32_t first = 0, below = 0;   // kept slots of the CTAs before this one; kept slots below m
+#pragma unroll
   for (int r = 0; r < cl; ++r) {
-    if (r < static_cast<int>(rank)) first += ld_cluster_u32(&sh.kept, r);
+    const uint32_t k = cl > 1 ? ld_cluster_u32(&sh.kept, r) : 0u;
+    first += r < static_cast<int>(rank) ? k : 0u;
     below += cl > 1 ? ld_cluster_u32(&sh.below, r) : sh.below;
   }
   // sources in rank order: entry i of the list lies in CTA i / slice_max (the keys are no longer needed)
@@ -639,10 +662,11 @@ mla_status_t evict_impl(void* kv_cache, bool fp8, int64_t num_blocks, const int3
   if (!p.status) return MLA_ERR_CUDA;
   int cl = 1;
   while (cl < kSelMaxCtas && static_cast<int64_t>(cl) * kSelSlotsPerCta < slots) cl *= 2;
-  p.sel_ctas = cl;
   p.sel_slice = static_cast<int>((slots + 32 * cl - 1) / (32 * cl) * 32);
   const size_t smem = sel_smem(p.sel_slice);
-  if (smem > 48 * 1024 && cudaFuncSetAttribute(mla_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const auto select = cl == 1 ? mla_evict_select_kernel<1> : cl == 2 ? mla_evict_select_kernel<2>
+                      : cl == 4 ? mla_evict_select_kernel<4> : mla_evict_select_kernel<8>;
+  if (smem > 48 * 1024 && cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(sel_smem(kEvictMaxSlots / kSelMaxCtas))) != cudaSuccess)
     return MLA_ERR_CUDA;
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
@@ -653,7 +677,7 @@ mla_status_t evict_impl(void* kv_cache, bool fp8, int64_t num_blocks, const int3
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   sel.numAttrs = cl > 1 ? 2 : 1;
-  if (cudaLaunchKernelEx(&sel, mla_evict_select_kernel, p) != cudaSuccess) return MLA_ERR_CUDA;
+  if (cudaLaunchKernelEx(&sel, select, p) != cudaSuccess) return MLA_ERR_CUDA;
   const int64_t top = budget < slots ? budget : slots;
   constexpr int kMoveBlock = 8 * kMoveSlots;   // slots of a block's 8 warps
   const cudaLaunchConfig_t mv = pdl_config(dim3(static_cast<unsigned>((top + kMoveBlock - 1) / kMoveBlock), static_cast<unsigned>(B)),
