@@ -200,7 +200,7 @@ constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelDigitBits = 11, kSelBins = 1 << kSelDigitBits;   // three digits: 11, 11 and 10 bits
 constexpr int kSelMaxCtas = 8;          // CTAs of a request's cluster
 constexpr int kSelSlotsPerCta = 4096;   // a request gets another CTA for every so many slots
-constexpr int kEvictMaxSlots = 262144;  // 32768 keys a CTA: 128 KiB of shared memory
+constexpr int kEvictMaxSlots = 262144;  // 32768 keys a CTA: 128 KiB of shared memory, and 16 bits a count
 constexpr int kMoveSlots = 16;          // slots of one warp of the move kernel
 
 struct EvictParams {
@@ -214,7 +214,7 @@ struct EvictParams {
   const int32_t* arrival;
   int64_t arrival_stride;
   int budget, sink, recent, slots;
-  int sel_slice;            // selection: slots of a CTA (a multiple of 32)
+  int sel_log_slice;        // selection: log2 of the slots of a CTA
   int32_t* new_seqlens;
   int32_t* kept;
   float* weights_out;
@@ -237,20 +237,15 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(const uint32_t* p, uint32_t r
   return v;
 }
 
-__device__ __forceinline__ uint2 ld_cluster_v2(const uint32_t* p, uint32_t rank) {
-  uint2 v;
-  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(map_to_rank(smem_u32(p), rank)) : "memory");
-  return v;
-}
 // Asynchronous copy of 4 bytes global -> shared.
 __device__ __forceinline__ void cp_async4(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
-struct SelShared {
-  uint32_t hist[3][kSelBins];   // bins in descending order of their digit
+struct alignas(16) SelShared {
+  uint32_t hist[3][kSelBins / 2];   // bins in descending order of their digit, two 16-bit counts a word
   uint32_t warp_sum[kSelWarps];
-  uint32_t digit, need;         // of the digit in which the m-th largest key lies
+  uint32_t digit, need, here;   // the digit in which the m-th largest key lies; keys wanted of it, keys there
   uint32_t kept, below;         // this CTA's kept slots; those of them below slot m
   int newest;                   // this CTA's largest arrival number
 };
@@ -258,6 +253,7 @@ struct SelShared {
 __host__ __device__ constexpr size_t sel_smem(int slice) {
   return sizeof(SelShared) + sizeof(uint32_t) * (static_cast<size_t>(slice) + 2 * (static_cast<size_t>(slice) / 32));
 }
+static_assert(sel_smem(kEvictMaxSlots / kSelMaxCtas) <= 232448, "shared memory per CTA");
 
 // Exclusive sum of v over the CTA's threads; *total gets the sum of all.
 __device__ __forceinline__ uint32_t scan_cta(uint32_t v, uint32_t* warp_sum, uint32_t* total) {
@@ -294,16 +290,16 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_evict_select_kernel(const 
   extern __shared__ __align__(16) uint8_t sel_dyn[];
   SelShared& sh = *reinterpret_cast<SelShared*>(sel_dyn);
   uint32_t* keys = reinterpret_cast<uint32_t*>(sel_dyn + sizeof(SelShared));
-  const int slice_max = p.sel_slice, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  uint32_t* mask = keys + slice_max;
-  uint32_t* prefix = mask + slice_max / 32;
+  const int log_slice = p.sel_log_slice, slice = 1 << log_slice, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint32_t* mask = keys + slice;
+  uint32_t* prefix = mask + slice / 32;
   const int b = static_cast<int>(blockIdx.x) / cl;
   const uint32_t rank = cl > 1 ? cluster_ctarank() : 0;
   auto sync = [&] {
     if (cl > 1) cluster_sync();
     else __syncthreads();
   };
-  for (int i = tid; i < 3 * kSelBins; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
+  for (int i = tid; i < 3 * kSelBins / 2; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
   if (tid == 0) sh.newest = -1;
   griddep_wait();
   griddep_launch_dependents();
@@ -315,20 +311,30 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_evict_select_kernel(const 
   const int m = min(n, p.budget);
   const float* w = p.weights + b * p.weights_stride;
   const int32_t* arr = p.arrival ? p.arrival + b * p.arrival_stride : nullptr;
-  // slices of whole 32-slot words, as even as that allows
-  const int slice = min(slice_max, (n + 32 * cl - 1) / (32 * cl) * 32);
-  const int t0 = min(n, static_cast<int>(rank) * slice), count = min(n, t0 + slice) - t0;
+  const int t0 = min(n, static_cast<int>(rank) << log_slice), count = min(n, t0 + slice) - t0;
   const int words = (count + 31) / 32;
   auto arrival_of = [&](int t) { return arr ? __ldg(arr + t) : t; };
 
-  // e = 1 + the largest arrival number
+  // e = 1 + the largest arrival number; four slots a load where both rows are 16-byte aligned
   int64_t e = n;
+  const int step = arr && ((reinterpret_cast<uintptr_t>(w) | reinterpret_cast<uintptr_t>(arr)) & 15u) == 0 ? 4 : 1;
   if (arr) {
     __syncthreads();
     int top = -1;
-    for (int i = tid; i < count; i += kSelThreads) cp_async4(keys + i, w + t0 + i);   // each for the same thread below
-#pragma unroll 8
-    for (int i = tid; i < count; i += kSelThreads) top = max(top, __ldg(arr + t0 + i));
+    // the weights on their way into shared memory, each for the thread that uses it below
+    for (int i = step * tid; i < count; i += step * kSelThreads) {
+      if (step == 4 && i + 4 <= count) cp_async16(smem_u32(keys + i), w + t0 + i);
+      else for (int j = i; j < min(count, i + step); ++j) cp_async4(keys + j, w + t0 + j);
+    }
+#pragma unroll 4
+    for (int i = step * tid; i < count; i += step * kSelThreads) {
+      if (step == 4 && i + 4 <= count) {
+        const int4 a = __ldg(reinterpret_cast<const int4*>(arr + t0 + i));
+        top = max(top, max(max(a.x, a.y), max(a.z, a.w)));
+      } else {
+        for (int j = i; j < min(count, i + step); ++j) top = max(top, __ldg(arr + t0 + j));
+      }
+    }
     top = __reduce_max_sync(0xffffffffu, top);
     if (lane == 0) atomicMax(&sh.newest, top);
     sync();
@@ -340,13 +346,23 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_evict_select_kernel(const 
   }
   uint32_t cut = 0, ties = 0;   // keep key > cut, and the first `ties` slots with key == cut
   uint32_t tie_first = 0;       // ties in the CTAs before this one
+  bool all_ties = true;         // every key == cut stays (distinct weights: no ranks among them are needed)
   if (m < n) {
+    auto key = [&](int a, float weight) {
+      return (a < p.sink || a >= e - p.recent) ? 0xffffffffu : weight_order(weight);
+    };
     cp_async_wait_all();
-#pragma unroll 8
-    for (int i = tid; i < count; i += kSelThreads) {
-      const int a = arrival_of(t0 + i);
-      const float weight = arr ? __uint_as_float(keys[i]) : __ldg(w + t0 + i);
-      keys[i] = (a < p.sink || a >= e - p.recent) ? 0xffffffffu : weight_order(weight);
+#pragma unroll 4
+    for (int i = step * tid; i < count; i += step * kSelThreads) {
+      if (step == 4 && i + 4 <= count) {
+        const int4 a = __ldg(reinterpret_cast<const int4*>(arr + t0 + i));
+        uint4& k = *reinterpret_cast<uint4*>(keys + i);
+        k = make_uint4(key(a.x, __uint_as_float(k.x)), key(a.y, __uint_as_float(k.y)), key(a.z, __uint_as_float(k.z)),
+                       key(a.w, __uint_as_float(k.w)));
+      } else {
+        for (int j = i; j < min(count, i + step); ++j)
+          keys[j] = key(arrival_of(t0 + j), arr ? __uint_as_float(keys[j]) : __ldg(w + t0 + j));
+      }
     }
     uint32_t need = static_cast<uint32_t>(m);
     int shift = 32;
@@ -359,19 +375,18 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_evict_select_kernel(const 
       __syncthreads();   // (the first digit: keys and zeros are in place)
       for (int i = tid; i < count; i += kSelThreads) {
         const uint32_t k = keys[i];
-        if (((k ^ cut) & high) == 0) atomicAdd(&hist[kSelBins - 1 - ((k >> shift) & ((1u << bits) - 1u))], 1u);
+        if (((k ^ cut) & high) == 0) {
+          const uint32_t d = kSelBins - 1 - ((k >> shift) & ((1u << bits) - 1u));
+          atomicAdd(&hist[d >> 1], 1u << (16 * (d & 1)));
+        }
       }
       sync();
       // bins in descending order, two a thread
-      uint32_t bin[2] = {hist[2 * tid], hist[2 * tid + 1]};
-      if (cl > 1) {
-        uint2 part[cl];
+      uint32_t part[cl], bin[2] = {0, 0};
 #pragma unroll
-        for (int r = 0; r < cl; ++r) part[r] = ld_cluster_v2(&hist[2 * tid], r);
-        bin[0] = bin[1] = 0;
+      for (int r = 0; r < cl; ++r) part[r] = cl > 1 ? ld_cluster_u32(&hist[tid], r) : hist[tid];
 #pragma unroll
-        for (int r = 0; r < cl; ++r) bin[0] += part[r].x, bin[1] += part[r].y;
-      }
+      for (int r = 0; r < cl; ++r) bin[0] += part[r] & 0xffffu, bin[1] += part[r] >> 16;
       uint32_t all;
       uint32_t above = scan_cta(bin[0] + bin[1], sh.warp_sum, &all);
 #pragma unroll
@@ -379,6 +394,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_evict_select_kernel(const 
         if (above < need && need <= above + bin[j]) {
           sh.digit = static_cast<uint32_t>(kSelBins - 1 - (2 * tid + j));
           sh.need = need - above;
+          sh.here = bin[j];
         }
         above += bin[j];
       }
@@ -387,11 +403,12 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_evict_select_kernel(const 
       need = sh.need;
     }
     ties = need;
-    if (cl > 1) {
-      const uint32_t* bin = &sh.hist[2][kSelBins - 1 - (cut & ((1u << (32 - 2 * kSelDigitBits)) - 1u))];
+    all_ties = need == sh.here;
+    if (cl > 1 && !all_ties) {
+      const uint32_t d = kSelBins - 1 - (cut & ((1u << (32 - 2 * kSelDigitBits)) - 1u));
 #pragma unroll
       for (int r = 0; r < cl; ++r) {
-        const uint32_t k = ld_cluster_u32(bin, r);
+        const uint32_t k = ld_cluster_u32(&sh.hist[2][d >> 1], r) >> (16 * (d & 1)) & 0xffffu;
         tie_first += r < static_cast<int>(rank) ? k : 0u;
       }
     }
@@ -401,7 +418,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_evict_select_kernel(const 
   const int run = (words + kSelWarps - 1) / kSelWarps;
   const int w0 = min(words, warp * run), w1 = min(words, w0 + run);
   uint32_t tie_rank = tie_first, all;
-  if (m < n) {
+  if (!all_ties) {
     uint32_t mine = 0;
     for (int i = w0 * 32 + lane; i < w1 * 32; i += 32) mine += i < count && keys[i] == cut;
     tie_rank += scan_cta(mine, sh.warp_sum, &all);
@@ -411,7 +428,9 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_evict_select_kernel(const 
   for (int i = w0; i < w1; ++i) {
     const int t = i * 32 + lane;
     bool keep = t < count;
-    if (m < n) {
+    if (m < n && all_ties) {
+      keep = t < count && keys[t] >= cut;
+    } else if (m < n) {
       const uint32_t k = t < count ? keys[t] : 0u;
       const bool tie = t < count && k == cut;
       const uint32_t tied = __ballot_sync(0xffffffffu, tie);
@@ -438,12 +457,12 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_evict_select_kernel(const 
     first += r < static_cast<int>(rank) ? k : 0u;
     below += cl > 1 ? ld_cluster_u32(&sh.below, r) : sh.below;
   }
-  // sources in rank order: entry i of the list lies in CTA i / slice_max (the keys are no longer needed)
+  // sources in rank order: entry i of the list lies in CTA i / slice (the keys are no longer needed)
   for (int i = (m_here / 32 + warp) * 32 + lane; i < words * 32; i += kSelThreads) {
     if (i >= m_here && ((mask[i >> 5] >> (i & 31)) & 1u)) {
       const uint32_t at = first + kept_before(i) - below;
-      uint32_t* entry = keys + at % slice_max;
-      if (cl > 1) st_cluster_u32(map_to_rank(smem_u32(entry), at / slice_max), static_cast<uint32_t>(t0 + i));
+      uint32_t* entry = keys + (at & (slice - 1));
+      if (cl > 1) st_cluster_u32(map_to_rank(smem_u32(entry), at >> log_slice), static_cast<uint32_t>(t0 + i));
       else *entry = static_cast<uint32_t>(i);
     }
   }
@@ -458,14 +477,14 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_evict_select_kernel(const 
     if (j < m) {
       const int t = static_cast<int>(j);
       src = t;
-      const uint32_t r = cl > 1 ? static_cast<uint32_t>(t / slice) : 0u;
-      const int at = t - static_cast<int>(r) * slice;
+      const uint32_t r = static_cast<uint32_t>(t >> log_slice);
+      const int at = t & (slice - 1);
       const uint32_t word = cl > 1 ? ld_cluster_u32(&mask[at >> 5], r) : mask[at >> 5];
       if (!((word >> (at & 31)) & 1u)) {
         const uint32_t kept_below = (cl > 1 ? ld_cluster_u32(&sh.need, r) + ld_cluster_u32(&prefix[at >> 5], r)
                                             : prefix[at >> 5]) + __popc(word & ((1u << (at & 31)) - 1u));
         const uint32_t hole = static_cast<uint32_t>(t) - kept_below;
-        src = static_cast<int>(cl > 1 ? ld_cluster_u32(&keys[hole % slice_max], hole / slice_max) : keys[hole]);
+        src = static_cast<int>(cl > 1 ? ld_cluster_u32(&keys[hole & (slice - 1)], hole >> log_slice) : keys[hole]);
       }
     }
     const int64_t at = b * p.width + j;
@@ -662,8 +681,9 @@ mla_status_t evict_impl(void* kv_cache, bool fp8, int64_t num_blocks, const int3
   if (!p.status) return MLA_ERR_CUDA;
   int cl = 1;
   while (cl < kSelMaxCtas && static_cast<int64_t>(cl) * kSelSlotsPerCta < slots) cl *= 2;
-  p.sel_slice = static_cast<int>((slots + 32 * cl - 1) / (32 * cl) * 32);
-  const size_t smem = sel_smem(p.sel_slice);
+  p.sel_log_slice = 5;
+  while (static_cast<int64_t>(cl) << p.sel_log_slice < slots) ++p.sel_log_slice;
+  const size_t smem = sel_smem(1 << p.sel_log_slice);
   const auto select = cl == 1 ? mla_evict_select_kernel<1> : cl == 2 ? mla_evict_select_kernel<2>
                       : cl == 4 ? mla_evict_select_kernel<4> : mla_evict_select_kernel<8>;
   if (smem > 48 * 1024 && cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize,
