@@ -373,6 +373,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_evict_select_kernel(const 
       shift -= bits;
       uint32_t* hist = sh.hist[pass];
       __syncthreads();   // (the first digit: keys and zeros are in place)
+#pragma unroll 4
       for (int i = tid; i < count; i += kSelThreads) {
         const uint32_t k = keys[i];
         if (((k ^ cut) & high) == 0) {
@@ -401,6 +402,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_evict_select_kernel(const 
       __syncthreads();
       cut |= sh.digit << shift;
       need = sh.need;
+      if (need == sh.here) break;   // all of the digit's keys stay: key >= cut, whatever the digits further on
     }
     ties = need;
     all_ties = need == sh.here;
@@ -425,6 +427,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_evict_select_kernel(const 
     tie_rank = __shfl_sync(0xffffffffu, tie_rank, 0);   // that of the run's first lane: ties before the run
   }
   uint32_t kept = 0;
+#pragma unroll 4
   for (int i = w0; i < w1; ++i) {
     const int t = i * 32 + lane;
     bool keep = t < count;
@@ -458,9 +461,11 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_evict_select_kernel(const 
     below += cl > 1 ? ld_cluster_u32(&sh.below, r) : sh.below;
   }
   // sources in rank order: entry i of the list lies in CTA i / slice (the keys are no longer needed)
+#pragma unroll 4
   for (int i = (m_here / 32 + warp) * 32 + lane; i < words * 32; i += kSelThreads) {
-    if (i >= m_here && ((mask[i >> 5] >> (i & 31)) & 1u)) {
-      const uint32_t at = first + kept_before(i) - below;
+    const uint32_t word = mask[i >> 5], lower = (1u << (i & 31)) - 1u;
+    if (i >= m_here && (word & (lower + 1u))) {
+      const uint32_t at = first + prefix[i >> 5] + __popc(word & lower) - below;
       uint32_t* entry = keys + (at & (slice - 1));
       if (cl > 1) st_cluster_u32(map_to_rank(smem_u32(entry), at >> log_slice), static_cast<uint32_t>(t0 + i));
       else *entry = static_cast<uint32_t>(i);
@@ -471,26 +476,46 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_evict_select_kernel(const 
   }
   sync();
 
-  // outputs, spread over the cluster: slot j keeps its token, or takes that of the next source
-  for (int64_t j = static_cast<int64_t>(rank) * kSelThreads + tid; j < p.width; j += static_cast<int64_t>(cl) * kSelThreads) {
-    int src = -1;
-    if (j < m) {
-      const int t = static_cast<int>(j);
-      src = t;
-      const uint32_t r = static_cast<uint32_t>(t >> log_slice);
-      const int at = t & (slice - 1);
-      const uint32_t word = cl > 1 ? ld_cluster_u32(&mask[at >> 5], r) : mask[at >> 5];
-      if (!((word >> (at & 31)) & 1u)) {
-        const uint32_t kept_below = (cl > 1 ? ld_cluster_u32(&sh.need, r) + ld_cluster_u32(&prefix[at >> 5], r)
-                                            : prefix[at >> 5]) + __popc(word & ((1u << (at & 31)) - 1u));
-        const uint32_t hole = static_cast<uint32_t>(t) - kept_below;
-        src = static_cast<int>(cl > 1 ? ld_cluster_u32(&keys[hole & (slice - 1)], hole >> log_slice) : keys[hole]);
+  // outputs, spread over the cluster, four slots a thread at a time (each is a chain of reads): slot j keeps its
+  // token, or takes that of the next source
+  constexpr int kEach = 4;
+  const int64_t stride = static_cast<int64_t>(cl) * kSelThreads;
+  for (int64_t j0 = static_cast<int64_t>(rank) * kSelThreads + tid; j0 < p.width; j0 += kEach * stride) {
+    int src[kEach];
+    uint32_t word[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int64_t j = j0 + i * stride;
+      src[i] = j < m ? static_cast<int>(j) : -1;
+      const int at = src[i] & (slice - 1);
+      word[i] = src[i] < 0 ? ~0u : cl > 1 ? ld_cluster_u32(&mask[at >> 5], src[i] >> log_slice) : mask[at >> 5];
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const uint32_t bit = 1u << (src[i] & 31);
+      if (!(word[i] & bit)) {
+        const uint32_t r = src[i] >> log_slice, at = (src[i] & (slice - 1)) >> 5;
+        const uint32_t kept_below = (cl > 1 ? ld_cluster_u32(&sh.need, r) + ld_cluster_u32(&prefix[at], r) : prefix[at]) +
+                                    __popc(word[i] & (bit - 1u));
+        const uint32_t hole = static_cast<uint32_t>(src[i]) - kept_below;
+        src[i] = static_cast<int>(cl > 1 ? ld_cluster_u32(&keys[hole & (slice - 1)], hole >> log_slice) : keys[hole]);
       }
     }
-    const int64_t at = b * p.width + j;
-    p.kept[at] = src;
-    p.weights_out[at] = src >= 0 ? __ldg(w + src) : 0.f;
-    if (p.arrival_out) p.arrival_out[at] = src >= 0 ? arrival_of(src) : static_cast<int32_t>(e + (j - m));
+    float weight[kEach];
+    int number[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      weight[i] = src[i] >= 0 ? __ldg(w + src[i]) : 0.f;
+      number[i] = src[i] >= 0 ? arrival_of(src[i]) : static_cast<int>(e + (j0 + i * stride - m));
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int64_t j = j0 + i * stride;
+      if (j >= p.width) break;
+      p.kept[b * p.width + j] = src[i];
+      p.weights_out[b * p.width + j] = weight[i];
+      if (p.arrival_out) p.arrival_out[b * p.width + j] = number[i];
+    }
   }
   if (cl > 1) cluster_sync();   // no CTA leaves while another reads its shared memory
   if (tid == 0 && rank == 0) p.new_seqlens[b] = m;   // last: it may be the array that the lengths came from
