@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include <cmath>
+#include <cstddef>
 #include <mutex>
 
 #include "mla_kernels.h"
@@ -51,9 +52,19 @@ constexpr int kEpiWarps = 8;
 constexpr int kSBufs = 3;                      // S accumulators in TMEM
 constexpr int kPartBufs = 4;                   // pages of partial sums between the epilogue and the sum warp
 constexpr uint32_t kQCol = 0, kSCol0 = 320;    // TMEM columns: Q [0, 288), S at 320, 384, 448
-constexpr int kRecvSlots = 4;                  // cluster: pages of sums in flight towards CTA 0
+constexpr int kRecvRows = 12;                  // cluster: 64-token sums in flight towards CTA 0: a slot takes cl - 1
 constexpr uint32_t kChunk = 8192;              // 64 rows x 128 bytes, 128-byte swizzle
 constexpr uint64_t kTimeoutNs = 500ull * 1000 * 1000;
+
+// 16 consecutive 32-bit columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
 
 template <bool F8>
 struct WCfg {
@@ -64,7 +75,7 @@ struct WCfg {
   static constexpr int kQRows = 128 / kQItems;
   static constexpr uint32_t kQItemBytes = static_cast<uint32_t>(kQRows) * kDimQK * 2;
   // what a switch of requests costs (Q's load and its way into TMEM), in pages: the split charges it
-  static constexpr int kSwitchPages = F8 ? 3 : 2;
+  static constexpr int kSwitchPages = F8 ? 5 : 2;
   static constexpr uint32_t kOffShared = kStages * kStageBytes;
   static_assert(kQItemBytes <= kStageBytes && kQItems <= kStages, "a row block's q is resident at once");
 };
@@ -73,18 +84,21 @@ struct WShared {
   uint64_t full[5], empty[5];
   uint64_t s_full[kSBufs], s_empty[kSBufs];
   uint64_t part_full[kPartBufs], part_empty[kPartBufs];
-  uint64_t amax_full, q_full, drain;
-  uint64_t recv_full[kRecvSlots];              // CTA 0: the other CTAs' sums have arrived
-  uint64_t credit[kRecvSlots];                 // the other CTAs: CTA 0 has taken what was in the slot
+  uint64_t q_read;                             // FP8: raw q is in TMEM, and the rows' maxima are in amax
+  uint64_t q_full, drain;
+  uint64_t recv_full[kRecvRows];               // CTA 0: the other CTAs' sums have arrived
+  uint64_t credit[kRecvRows];                  // the other CTAs: CTA 0 has taken what was in the slot
   uint32_t tmem_base;
   volatile int abort;
   int64_t scan[kWThreads / 32 + 1];
   int64_t offset, count;                       // this part's piece: from `offset` positions into request b0 on
   int b0;
   float amax[2][128];                          // FP8: row maxima of the two halves of q
-  float part[kPartBufs][4][kPageTokens];       // sums over the rows of one TMEM quadrant
-  float recv[kRecvSlots][kMaxPairsPerCluster - 1][kPageTokens];
+  alignas(16) float part[kPartBufs][4][kPageTokens];   // sums over the rows of one TMEM quadrant
+  alignas(16) float recv[kRecvRows][kPageTokens];
 };
+// pairs of sums are read, written and sent as 8 bytes
+static_assert(offsetof(WShared, part) % 16 == 0 && offsetof(WShared, recv) % 16 == 0 && alignof(WShared) == 16, "alignment");
 template <bool F8>
 constexpr uint32_t weights_smem() { return WCfg<F8>::kOffShared + sizeof(WShared); }
 static_assert(weights_smem<false>() <= 232448 && weights_smem<true>() <= 232448, "shared memory per CTA");
@@ -100,11 +114,9 @@ __device__ __forceinline__ void w_abort(WShared& sh, int* status, uint32_t cl) {
   atomicCAS(status, 0, MLA_ERR_TIMEOUT);
   for (uint32_t r = 0; r < cl; ++r) st_cluster_u32(map_to_rank(smem_u32(const_cast<int*>(&sh.abort)), r), 1u);
 }
-// kCluster: arrivals come from other CTAs' threads, whose stores are read after the wait.
-template <bool kCluster>
 __device__ __noinline__ bool w_wait_slow(WShared& sh, uint32_t bar, uint32_t parity, int* status, uint32_t cl) {
   const uint64_t t0 = global_timer_ns();
-  while (!(kCluster ? mbar_test_cluster(bar, parity) : mbar_test(bar, parity))) {
+  while (!mbar_test(bar, parity)) {
     if (sh.abort) return false;
     if (global_timer_ns() - t0 > kTimeoutNs) {
       w_abort(sh, status, cl);
@@ -114,15 +126,13 @@ __device__ __noinline__ bool w_wait_slow(WShared& sh, uint32_t bar, uint32_t par
   return true;
 }
 // Bounded wait (0.5 s): false once this cluster has given up.
-template <bool kCluster = false>
 __device__ __forceinline__ bool w_wait(WShared& sh, uint64_t& bar, uint32_t parity, int* status, uint32_t cl) {
   const uint32_t a = smem_u32(&bar);
-  if (kCluster ? mbar_test_cluster(a, parity) : mbar_test(a, parity)) return true;
-  return w_wait_slow<kCluster>(sh, a, parity, status, cl);
+  if (mbar_test(a, parity)) return true;
+  return w_wait_slow(sh, a, parity, status, cl);
 }
-template <bool kCluster = false>
 __device__ __forceinline__ bool w_warp_wait(WShared& sh, uint64_t& bar, uint32_t parity, int* status, uint32_t cl) {
-  return __all_sync(0xffffffffu, w_wait<kCluster>(sh, bar, parity, status, cl));
+  return __all_sync(0xffffffffu, w_wait(sh, bar, parity, status, cl));
 }
 __device__ __noinline__ void w_drain(uint64_t& bar, uint32_t parity) {   // ignores the abort flag
   const uint32_t a = smem_u32(&bar);
@@ -272,9 +282,11 @@ __device__ void w_mma(const WeightsParams& p, WShared& sh, uint32_t smem, uint32
   uint32_t i = 0, T = 0, seg = 0;
   bool ok = true;
   while (ok && walk.next(p, s)) {
-    if (!(ok = w_warp_wait(sh, sh.q_full, seg++ & 1, p.status, cl))) break;
-    for (int j = 0; j < C::kQItems; ++j, ++i)   // the epilogue warps have read them: q_full says so
+    if (!(ok = w_warp_wait(sh, F8 ? sh.q_read : sh.q_full, seg & 1, p.status, cl))) break;
+    for (int j = 0; j < C::kQItems; ++j, ++i)   // the epilogue warps have read the ring's q
       if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&sh.empty[i % C::kStages]));
+    if (F8 && !(ok = w_warp_wait(sh, sh.q_full, seg & 1, p.status, cl))) break;
+    ++seg;
     for (int k = s.k0; k < s.k1; ++k, ++i, ++T) {
       const uint32_t st = i % C::kStages, sb = T % kSBufs;
       ok = w_warp_wait(sh, sh.s_empty[sb], ((T / kSBufs) & 1) ^ 1, p.status, cl) &&
@@ -283,14 +295,15 @@ __device__ void w_mma(const WeightsParams& p, WShared& sh, uint32_t smem, uint32
       tc_fence_after();
       const uint32_t stage = smem + st * C::kStageBytes, d = tmem + kSCol0 + sb * kPageTokens;
       if constexpr (F8) {
-        // chunks of 128 codes, K = 32 a step; Q = hi (columns 0..143) + lo (144..287)
+        // chunks of 128 codes, K = 32 a step; the half of q that a step lies in holds its hi, then its lo
 #pragma unroll
         for (int c = 0; c < 5; ++c)
 #pragma unroll
           for (int j = 0; j < (c < 4 ? 4 : 2); ++j) {
             const uint64_t kd = smem_desc_sw128(stage + c * kChunk + j * 32, 16, 1024);
-            mma_f8_ts_warp(d, tmem + kQCol + c * 32 + j * 8, kd, idesc, (c | j) ? 1u : 0u);
-            mma_f8_ts_warp(d, tmem + kQCol + 144 + c * 32 + j * 8, kd, idesc, 1u);
+            const int step = 4 * c + j, col = 144 * (step / 9) + 8 * (step % 9);
+            mma_f8_ts_warp(d, tmem + kQCol + col, kd, idesc, (c | j) ? 1u : 0u);
+            mma_f8_ts_warp(d, tmem + kQCol + col + 72, kd, idesc, 1u);
           }
       } else {
 #pragma unroll
@@ -321,8 +334,11 @@ struct QHalf {
     const int u = u0 + j;
     return ld_shared_v4(row + (u >> 3) * chunk_bytes + (((u & 7) ^ swizzle) << 4));
   }
-  // into TMEM, two bf16 values a column, from column `col` on
-  __device__ __forceinline__ void store(uint32_t col) const {
+  // Into TMEM, two bf16 values a column, from column `col` on.  Returns the largest magnitude, NaN where a value is
+  // NaN (asked for by kLargest).
+  template <bool kLargest>
+  __device__ __forceinline__ float store(uint32_t col) const {
+    __nv_bfloat162 top = __float2bfloat162_rn(0.f);
 #pragma unroll
     for (int c = 0; c < 9; ++c) {
       uint32_t v[16];
@@ -332,55 +348,55 @@ struct QHalf {
         v[4 * j] = x.x, v[4 * j + 1] = x.y, v[4 * j + 2] = x.z, v[4 * j + 3] = x.w;
       }
       tmem_st16(col + c * 16, v);
-    }
-  }
-  // the largest magnitude; NaN where a value is NaN
-  __device__ __forceinline__ float largest() const {
-    __nv_bfloat162 top = __float2bfloat162_rn(0.f);
-#pragma unroll 6
-    for (int j = 0; j < 36; ++j) {
-      const uint4 x = unit(j);
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      if (kLargest)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[e])));
+        for (int j = 0; j < 16; ++j) top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&v[j])));
     }
     const float lo = __low2float(top), hi = __high2float(top);
     return isnan(lo) || isnan(hi) ? NAN : fmaxf(lo, hi);
   }
-  // into TMEM as two E4M3 terms, four values a column, of q 2^k: hi = e4m3(q 2^k) from column `col` on and
-  // lo = e4m3(q 2^k - hi) 144 columns further.  A bf16 value has 8 significant bits, of which hi holds 4
-  // and lo the rest, so hi + lo is exact for values down to 2^-2 after scaling and within 2^-10 below.  It
-  // goes through fp16 pairs, two values an instruction (conversions of single floats bound it
-  // otherwise): with the magnitude's exponent rebased (112 = 127 - 15, less k; smaller ones become 0,
-  // below 2^-15) a bf16 pattern shifted left by three bits is the fp16 one.
-  __device__ __forceinline__ void store_e4m3(uint32_t col, int k) const {
-    const uint32_t base = static_cast<uint32_t>(112 - k) << 7, base2 = base | (base << 16);
-    auto split = [&](uint32_t w) {   // hi of the pair in bits 0..15, lo in 16..31
-      const __nv_bfloat162 m = __hmax2(__habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)),
-                                       *reinterpret_cast<const __nv_bfloat162*>(&base2));
-      const uint32_t v = ((*reinterpret_cast<const uint32_t*>(&m) - base2) << 3) | (w & 0x80008000u);
-      uint32_t both;
-      asm("{\n\t.reg .b16 h, l;\n\t.reg .b32 b, d;\n\t"
-          "cvt.rn.satfinite.e4m3x2.f16x2 h, %1;\n\tcvt.rn.f16x2.e4m3x2 b, h;\n\tsub.rn.f16x2 d, %1, b;\n\t"
-          "cvt.rn.satfinite.e4m3x2.f16x2 l, d;\n\tmov.b32 %0, {h, l};\n\t}"
-          : "=r"(both) : "r"(v));
-      return both;
-    };
-#pragma unroll
-    for (int c = 0; c < 9; ++c) {
-      uint32_t hi[8], lo[8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint4 x = unit(4 * c + j);
-        const uint32_t a = split(x.x), b = split(x.y), d = split(x.z), e = split(x.w);
-        hi[2 * j] = __byte_perm(a, b, 0x5410), lo[2 * j] = __byte_perm(a, b, 0x7632);
-        hi[2 * j + 1] = __byte_perm(d, e, 0x5410), lo[2 * j + 1] = __byte_perm(d, e, 0x7632);
-      }
-      tmem_st8(col + c * 8, hi);
-      tmem_st8(col + 144 + c * 8, lo);
-    }
-  }
 };
+
+// FP8: a thread's half row in TMEM (144 columns of two bf16 values from `col` on), turned in place into two E4M3
+// terms of q 2^k, four values a column: hi = e4m3(q 2^k) in the first 72 columns, lo = e4m3(q 2^k - hi) in the
+// others.  A bf16 value has 8 significant bits, of which hi holds 4 and lo the rest, so hi + lo is exact for
+// values down to 2^-2 after scaling and within 2^-10 below.  It goes through fp16 pairs, two values an
+// instruction (conversions of single floats, which bound it, take 3.7 us a row block, these 2.4): with the
+// magnitude's exponent rebased (112 = 127 - 15, less k; smaller ones become 0, below 2^-15) a bf16 pattern
+// shifted left by three bits is the fp16 one.
+__device__ __forceinline__ void split_q(uint32_t col, int k) {
+  const uint32_t base = static_cast<uint32_t>(112 - k) << 7, base2 = base | (base << 16);
+  auto split = [&](uint32_t w) {   // hi of the pair in bits 0..15, lo in 16..31
+    const __nv_bfloat162 m = __hmax2(__habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&base2));
+    const uint32_t v = ((*reinterpret_cast<const uint32_t*>(&m) - base2) << 3) | (w & 0x80008000u);
+    uint32_t both;
+    asm("{\n\t.reg .b16 h, l;\n\t.reg .b32 b, d;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 h, %1;\n\tcvt.rn.f16x2.e4m3x2 b, h;\n\tsub.rn.f16x2 d, %1, b;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 l, d;\n\tmov.b32 %0, {h, l};\n\t}"
+        : "=r"(both) : "r"(v));
+    return both;
+  };
+  // 16 columns a step: raw columns [16 c, 16 c + 16) give hi and lo columns [8 c, 8 c + 8).  Columns are written
+  // once they have been read: hi at once (8 c + 8 <= 16 c + 16), lo from the step on that has read past it.
+  uint32_t lo[9][8];
+#pragma unroll
+  for (int c = 0; c < 9; ++c) {
+    uint32_t v[16], hi[8];
+    tmem_ld16(col + 16 * c, v);
+    tmem_wait_ld();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t a = split(v[2 * j]), b = split(v[2 * j + 1]);
+      hi[j] = __byte_perm(a, b, 0x5410);
+      lo[c][j] = __byte_perm(a, b, 0x7632);
+    }
+    tmem_st8(col + 8 * c, hi);
+#pragma unroll
+    for (int l = 0; l < 9; ++l)   // 72 + 8 l + 8 <= 16 c + 16, and not yet so a step before
+      if (2 * c - 8 >= l && 2 * c - 10 < l) tmem_st8(col + 72 + 8 * l, lo[l]);
+  }
+}
 
 // Sums over the warp's lanes: lane l gets that of v[l].  Each step exchanges half of the columns a
 // lane still has with the lane `o` away, in a fixed order.
@@ -431,22 +447,24 @@ __device__ void w_epilogue(const WeightsParams& p, WShared& sh, uint32_t smem, i
     if (!w_warp_wait(sh, sh.full[item % C::kStages], (item / C::kStages) & 1, p.status, cl)) return;
     const int rl = r % C::kQRows;
     const QHalf q{smem + (item % C::kStages) * C::kStageBytes + rl * 128, C::kQRows * 128, 36 * half, rl & 7};
+    const uint32_t col = lane_base + kQCol + 144 * half;
     if constexpr (F8) {
-      sh.amax[half][r] = q.largest();
-      __syncwarp();   // the row's two halves agree on its scale
-      if (lane == 0) mbar_arrive(smem_u32(&sh.amax_full));
-      if (!w_warp_wait(sh, sh.amax_full, seg & 1, p.status, cl)) return;
-      const float a = sh.amax[0][r], b = sh.amax[1][r];
+      sh.amax[half][r] = q.store<true>(col);
+      tmem_wait_st();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.q_read));
+      if (!w_warp_wait(sh, sh.q_read, seg & 1, p.status, cl)) return;
+      const float a = sh.amax[0][r], b = sh.amax[1][r];   // the row's two halves agree on its scale:
       // 2^e brings the largest magnitude into (224, 448]; a row with an infinity or a NaN gives NaN
       const bool finite = a <= 3.4e38f && b <= 3.4e38f;
       const float top = fmaxf(a, b), t = finite && top > 0.f ? fminf(448.f / top, 0x1p100f) : 1.f;
       const int e = static_cast<int>(__float_as_uint(t) >> 23) - 127;
-      q.store_e4m3(lane_base + kQCol + 72 * half, e);
+      split_q(col, e);
       const float inv = finite ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : NAN;
       scale_hi *= inv;   // a power of two: exact
       scale_lo *= inv;
     } else {
-      q.store(lane_base + kQCol + 144 * half);
+      q.store<false>(col);
     }
     tmem_wait_st();
     tc_fence_before();
@@ -479,53 +497,69 @@ __device__ void w_epilogue(const WeightsParams& p, WShared& sh, uint32_t smem, i
   }
 }
 
+// Two floats into another CTA's shared memory; its barrier counts their 8 bytes.
+__device__ __forceinline__ void st_async_v2(uint32_t cluster_addr, float a, float b, uint32_t cluster_bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];"
+               :: "r"(cluster_addr), "f"(a), "f"(b), "r"(cluster_bar) : "memory");
+}
+// Arrival in another CTA that releases nothing beyond this CTA (it says that a slot has been read): a release to
+// the cluster would wait for the warp's reductions at L2, page by page (sums then set the period: 145 us for
+// two query positions over 8192 tokens).
+__device__ __forceinline__ void mbar_arrive_other(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_bar) : "memory");
+}
+
 // Warp 10: adds the four quadrants' sums of a page up and takes them to the weights, or, in the other CTAs of a
-// cluster, to CTA 0.  Lane l has tokens l and l + 32.
+// cluster, to CTA 0.  Lane l has tokens 2 l and 2 l + 1.
 template <bool F8>
 __device__ void w_sum(const WeightsParams& p, WShared& sh, uint32_t cl, uint32_t rank) {
   using C = WCfg<F8>;
   const int lane = threadIdx.x & 31;
+  const uint32_t others = cl - 1, slots = cl > 1 ? kRecvRows / others : 1;
   WWalk<C::kSwitchPages> walk(sh);
   WSegment s;
   uint32_t T = 0;
+  // CTA 0: each slot's barrier waits for one arrival, here, and the bytes of the other CTAs' sums
+  auto expect = [&](uint32_t slot) { mbar_arrive_expect_tx(smem_u32(&sh.recv_full[slot]), others * kPageTokens * 4); };
+  if (rank == 0 && static_cast<uint32_t>(lane) < slots && cl > 1) expect(lane);
   while (walk.next(p, s)) {
     for (int k = s.k0; k < s.k1; ++k, ++T) {
-      const uint32_t buf = T % kPartBufs, slot = T % kRecvSlots, ph = (T / kRecvSlots) & 1;
+      const uint32_t buf = T % kPartBufs, slot = T % slots, ph = (T / slots) & 1;
       const bool page = rank == 0 && block_of(p, s.b, k) >= 0;
       if (!w_warp_wait(sh, sh.part_full[buf], (T / kPartBufs) & 1, p.status, cl)) return;
-      float sum[2];
+      float2 sum = {0.f, 0.f};
+      float2 q[4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int c = 32 * j + lane;
-        sum[j] = (sh.part[buf][0][c] + sh.part[buf][1][c]) + (sh.part[buf][2][c] + sh.part[buf][3][c]);
-      }
+      for (int j = 0; j < 4; ++j) q[j] = *reinterpret_cast<const float2*>(&sh.part[buf][j][2 * lane]);
+      sum.x = (q[0].x + q[1].x) + (q[2].x + q[3].x);
+      sum.y = (q[0].y + q[1].y) + (q[2].y + q[3].y);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.part_empty[buf]));
-      if (cl > 1) {
-        if (rank != 0) {
-          if (!w_warp_wait<true>(sh, sh.credit[slot], ph ^ 1, p.status, cl)) return;
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            st_cluster_u32(map_to_rank(smem_u32(&sh.recv[slot][rank - 1][32 * j + lane]), 0), __float_as_uint(sum[j]));
-          mbar_arrive_remote(map_to_rank(smem_u32(&sh.recv_full[slot]), 0));   // releases this lane's two sums
-        } else {
-          if (!w_warp_wait<true>(sh, sh.recv_full[slot], ph, p.status, cl)) return;
-          for (uint32_t o = 1; o < cl; ++o)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) sum[j] += sh.recv[slot][o - 1][32 * j + lane];
-          __syncwarp();
-          if (lane > 0 && static_cast<uint32_t>(lane) < cl) mbar_arrive_remote(map_to_rank(smem_u32(&sh.credit[slot]), lane));
+      if (cl > 1 && rank != 0) {
+        if (!w_warp_wait(sh, sh.credit[slot], ph ^ 1, p.status, cl)) return;
+        st_async_v2(map_to_rank(smem_u32(&sh.recv[slot * others + rank - 1][2 * lane]), 0), sum.x, sum.y,
+                    map_to_rank(smem_u32(&sh.recv_full[slot]), 0));
+      } else if (cl > 1) {
+        if (!w_warp_wait(sh, sh.recv_full[slot], ph, p.status, cl)) return;
+        for (uint32_t o = 0; o < others; ++o) {
+          const float2 r = *reinterpret_cast<const float2*>(&sh.recv[slot * others + o][2 * lane]);
+          sum.x += r.x, sum.y += r.y;
         }
+        __syncwarp();
+        if (lane == 0) expect(slot);   // before the other CTAs may send the slot's next sums
+        __syncwarp();
+        if (lane > 0 && static_cast<uint32_t>(lane) < cl) mbar_arrive_other(map_to_rank(smem_u32(&sh.credit[slot]), lane));
       }
-      // one addition a token and call, so the order of the calls alone decides the result; as a reduction at L2
-      // it costs this warp no round trip to memory (which had set the period of a page)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int t = k * kPageTokens + 32 * j + lane;
-        if (page && t < s.n) atomicAdd(p.weights + s.b * p.weights_stride + t, sum[j]);
-      }
+      // One addition a token and call, so the order of the calls alone decides the result; as a reduction at L2 it
+      // costs this warp no round trip to memory.
+      const int t = k * kPageTokens + 2 * lane;
+      float* const w = p.weights + s.b * p.weights_stride + t;
+      if (page && t < s.n) atomicAdd(w, sum.x);
+      if (page && t + 1 < s.n) atomicAdd(w + 1, sum.y);
     }
   }
+  // sums on their way to CTA 0 land before it may leave: it has waited for all of them above; where it gave up, the
+  // others' bounded waits have ended too, and the cluster's last barrier holds every CTA until then
 }
 
 template <bool F8>
@@ -559,11 +593,11 @@ mla_attn_weights_kernel(const __grid_constant__ WMaps maps, const __grid_constan
       mbar_init(smem_u32(&sh.part_full[j]), kEpiWarps);
       mbar_init(smem_u32(&sh.part_empty[j]), 1);
     }
-    mbar_init(smem_u32(&sh.amax_full), kEpiWarps);
+    mbar_init(smem_u32(&sh.q_read), kEpiWarps);
     mbar_init(smem_u32(&sh.q_full), kEpiWarps);
     mbar_init(smem_u32(&sh.drain), 1);
-    for (int j = 0; j < kRecvSlots; ++j) {
-      mbar_init(smem_u32(&sh.recv_full[j]), cl > 1 ? 32 * (cl - 1) : 1);   // every lane of the others' sum warps
+    for (int j = 0; j < kRecvRows; ++j) {
+      mbar_init(smem_u32(&sh.recv_full[j]), 1);
       mbar_init(smem_u32(&sh.credit[j]), 1);
     }
     fence_mbar_init();
