@@ -40,9 +40,10 @@ struct WeightsParams {
 // 72 KiB (36 KiB in FP8) read once, against 9.4 MFLOP, a third of the tensor pipe's time for it.
 //  * Rows on the TMEM lanes, tokens on the columns: Q is loaded once per request, and the ring has the
 //    whole of shared memory for pages (221 KiB: what is in flight covers HBM latency).
-//  * The sum over the rows is a butterfly over the warp's lanes that halves the columns with every
-//    step (31 shuffles leave column l's sum in lane l), then four partial sums in shared memory, which
-//    a warp of its own adds to the weights: a fixed order, no atomics.
+//  * S is read with four of the rows in a lane, so that the sum over the rows is three additions in the
+//    lane, a butterfly over eight lanes that halves the columns with every step (7 shuffles; 31 where a
+//    lane has one row: their issue slots slow the MMAs down, 120 -> 110 us for two query positions), and four partial sums in shared memory,
+//    which a warp of its own adds to the weights: a fixed order.
 //  * More than 128 rows: a cluster of ceil(rows / 128) CTAs walks the same pages, each with its row
 //    block; the others hand their 64 sums a page to CTA 0 through distributed shared memory.
 //  * Work: all requests' pages in a row, with kSwitchPages for each request's start, cut evenly over the
@@ -398,20 +399,50 @@ __device__ __forceinline__ void split_q(uint32_t col, int k) {
   }
 }
 
-// Sums over the warp's lanes: lane l gets that of v[l].  Each step exchanges half of the columns a
-// lane still has with the lane `o` away, in a fixed order.
-__device__ __forceinline__ float sum_columns(float (&v)[32], int lane) {
+// 32 columns of 16 TMEM lanes: lane l of the warp gets, in r[4 n + 2 h + e], row 8 h + l / 4, column 8 n + 2 (l % 4) + e.
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, float (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+        "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+      : "r"(taddr));
+}
+// Two floats an instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// Sums over the lanes that share l % 4: lane l gets that of v[4 (l / 16) + 2 (l / 8 % 2) + l / 4 % 2].  Each step
+// exchanges half of the values a lane still has with the lane `o` away, in a fixed order.
+__device__ __forceinline__ float sum_lanes(float (&v)[8], int lane) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+  for (int o = 16, half = 4; o >= 4; o >>= 1, half >>= 1) {
     const bool up = lane & o;
 #pragma unroll
-    for (int c = 0; c < o; ++c) {
-      const float keep = up ? v[c + o] : v[c], give = up ? v[c] : v[c + o];
+    for (int c = 0; c < half; ++c) {
+      const float keep = up ? v[c + half] : v[c], give = up ? v[c] : v[c + half];
       v[c] = keep + __shfl_xor_sync(0xffffffffu, give, o);
     }
   }
   return v[0];
 }
+
+struct Row {   // of the scores: p = exp2(s scale + c), both as float pairs
+  float c_hi, c_lo, scale_hi, scale_lo;
+  int vis;     // tokens it sees
+};
 
 // Warps 2..9.  Warp quadrant q (TMEM lanes 32 q .. 32 q + 31: the rows), half `half` of the page's columns.
 // All waits are on bounded barriers (no bar.sync), so a warp that gives up leaves no other hanging.
@@ -424,6 +455,8 @@ __device__ void w_epilogue(const WeightsParams& p, WShared& sh, uint32_t smem, i
   const int g = rb * kRowsPerPair + r;               // row of the request: i * H + h
   const uint32_t lane_base = sh.tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
   const int cb = half * 32;
+  // the column whose sum sum_lanes leaves to this lane: 8 n + 2 (lane % 4) + e
+  const int column = 16 * (lane >> 4) + 8 * (lane >> 3 & 1) + 2 * (lane & 3) + (lane >> 2 & 1);
   WWalk<C::kSwitchPages> walk(sh);
   WSegment s;
   uint32_t i = 0, T = 0, seg = 0;
@@ -471,26 +504,56 @@ __device__ void w_epilogue(const WeightsParams& p, WShared& sh, uint32_t smem, i
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sh.q_full));
     ++seg;
+    // the constants of the four rows 8 j + lane / 4 whose scores this lane gets
+    Row row[4];
+    int least = 0x7fffffff;   // of their numbers of visible tokens
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int from = 8 * j + (lane >> 2);
+      row[j].c_hi = __shfl_sync(0xffffffffu, c_hi, from);
+      row[j].c_lo = __shfl_sync(0xffffffffu, c_lo, from);
+      row[j].scale_hi = F8 ? __shfl_sync(0xffffffffu, scale_hi, from) : scale_hi;
+      row[j].scale_lo = F8 ? __shfl_sync(0xffffffffu, scale_lo, from) : scale_lo;
+      row[j].vis = __shfl_sync(0xffffffffu, vis, from);
+      least = min(least, row[j].vis);
+    }
     for (int k = s.k0; k < s.k1; ++k, ++T) {
       const uint32_t sb = T % kSBufs, buf = T % kPartBufs;
       if (!w_warp_wait(sh, sh.s_full[sb], (T / kSBufs) & 1, p.status, cl)) return;
       tc_fence_after();
-      float v[32];
-      tmem_ld32(lane_base + kSCol0 + sb * kPageTokens + cb, *reinterpret_cast<uint32_t(*)[32]>(v));
+      float v[2][16];   // rows 16 h .. 16 h + 15 of the quadrant
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        tmem_ld_16x256(lane_base + (static_cast<uint32_t>(16 * h) << 16) + kSCol0 + sb * kPageTokens + cb, v[h]);
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.s_empty[sb]));
-      const int seen = vis - (k * kPageTokens + cb);   // columns c < seen are visible to this row
+      const int c0 = k * kPageTokens + cb;   // token of the columns' first
+      const bool whole = least - c0 >= 32;   // all 32 columns are visible to the four rows
+      float total[8];
 #pragma unroll
-      for (int c = 0; c < 32; ++c) v[c] = fast_exp2(fmaf(v[c], scale_hi, c_hi) + fmaf(v[c], scale_lo, c_lo));
-      if (seen < 32) {
+      for (int n = 0; n < 4; ++n) {
+        float2 e[4];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) v[c] = c < seen ? v[c] : 0.f;
+        for (int j = 0; j < 4; ++j) {
+          const float2 x = {v[j >> 1][4 * n + 2 * (j & 1)], v[j >> 1][4 * n + 2 * (j & 1) + 1]};
+          const Row& r4 = row[j];
+          const float2 y = add2(fma2(x, {r4.scale_hi, r4.scale_hi}, {r4.c_hi, r4.c_hi}),
+                                fma2(x, {r4.scale_lo, r4.scale_lo}, {r4.c_lo, r4.c_lo}));
+          e[j] = {fast_exp2(y.x), fast_exp2(y.y)};
+          if (!whole) {
+            const int seen = r4.vis - (c0 + 8 * n + 2 * (lane & 3));
+            e[j].x = seen > 0 ? e[j].x : 0.f;
+            e[j].y = seen > 1 ? e[j].y : 0.f;
+          }
+        }
+        const float2 sum2 = add2(add2(e[0], e[1]), add2(e[2], e[3]));
+        total[2 * n] = sum2.x, total[2 * n + 1] = sum2.y;
       }
-      const float sum = sum_columns(v, lane);
+      const float sum = sum_lanes(total, lane);
       if (!w_warp_wait(sh, sh.part_empty[buf], ((T / kPartBufs) & 1) ^ 1, p.status, cl)) return;
-      sh.part[buf][quad][cb + lane] = sum;
+      sh.part[buf][quad][cb + column] = sum;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.part_full[buf]));
     }
