@@ -371,54 +371,53 @@ def extend_chunked(q_nope: torch.Tensor, q_pe: torch.Tensor, w_uk: torch.Tensor,
 
 
 # The latent-cache calls.  The kernels read raw addresses, so a tensor of another type, shape or device must
-# not reach them; the checks are plain ifs (a decode step makes these calls for every layer).
-def _typed(name: str, what: str, t: torch.Tensor, dtype: torch.dtype, dev: int):
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: {what}: {dtype} expected, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name}: {what}: on {t.device}, the call's first tensor is on GPU {dev}")
+# not reach them; the checks are plain conditions (a decode step makes these calls for every layer).
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def _bad(name: str, what: str, wanted: str, t: torch.Tensor, dtype=None) -> Exception:
+    kind = TypeError if dtype is not None and t.dtype is not dtype else ValueError
+    return kind(f"{name}: {what} must be {wanted} on one GPU with the call's other tensors; got {t.dtype} "
+                f"{list(t.shape)} with strides {list(t.stride())} on {t.device}")
 
 
 def _paged(name: str, kv_cache: torch.Tensor, block_table: torch.Tensor, seqlens: torch.Tensor, fp8: bool):
     """Checks a call's cache, table and lengths; returns (device index, B, num_blocks, max_blocks)."""
     dev = kv_cache.get_device()
-    if dev < 0:
-        raise ValueError(f"{name}: kv_cache must be on a GPU")
-    if kv_cache.element_size() != 1 if fp8 else kv_cache.dtype != torch.bfloat16:
-        raise TypeError(f"{name}: kv_cache must hold " + ("one byte per value (E4M3 codes)" if fp8 else "bfloat16"))
     shape = kv_cache.shape
-    if len(shape) != 3 or shape[1] != 64 or shape[2] != 576 or not kv_cache.is_contiguous():
-        raise ValueError(f"{name}: kv_cache must be a contiguous [num_blocks, 64, 576]")
-    _typed(name, "block_table", block_table, torch.int32, dev)
-    _typed(name, "seqlens", seqlens, torch.int32, dev)
-    if seqlens.dim() != 1 or not seqlens.is_contiguous():
-        raise ValueError(f"{name}: seqlens must be a contiguous [B]")
+    if fp8 and kv_cache.element_size() != 1:
+        raise TypeError(f"{name}: kv_cache must hold one byte per value (E4M3 codes)")
+    if (dev < 0 or not (fp8 or kv_cache.dtype is _BF16) or len(shape) != 3 or shape[1] != 64 or shape[2] != 576
+            or not kv_cache.is_contiguous()):
+        raise _bad(name, "kv_cache", "a contiguous [num_blocks, 64, 576]", kv_cache, None if fp8 else _BF16)
+    if seqlens.dtype is not _I32 or seqlens.get_device() != dev or seqlens.dim() != 1 or not seqlens.is_contiguous():
+        raise _bad(name, "seqlens", "a contiguous int32 [B]", seqlens, _I32)
     B = seqlens.numel()
-    if block_table.dim() != 2 or block_table.size(0) != B or not block_table.is_contiguous():
-        raise ValueError(f"{name}: block_table must be a contiguous [B, max_blocks]")
-    return dev, B, shape[0], block_table.size(1)
+    table = block_table.shape
+    if (block_table.dtype is not _I32 or block_table.get_device() != dev or len(table) != 2 or table[0] != B
+            or not block_table.is_contiguous()):
+        raise _bad(name, "block_table", "a contiguous int32 [B, max_blocks]", block_table, _I32)
+    return dev, B, shape[0], table[1]
 
 
 def _rows(name: str, what: str, t: torch.Tensor, dtype: torch.dtype, dev: int, B: int, max_blocks: int) -> int:
     """Checks a [B, slots] tensor whose rows may be strided; returns the elements between rows, of which a request may
     use as many as there are columns."""
-    _typed(name, what, t, dtype, dev)
-    if t.dim() != 2 or t.size(0) != B or t.size(1) < 1 or (t.size(1) > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name}: {what}: [B, slots] with contiguous rows expected")
-    slots = t.size(1)
-    stride = t.stride(0) if B > 1 else slots
+    shape, strides = t.shape, t.stride()
+    if (t.dtype is not dtype or t.get_device() != dev or len(shape) != 2 or shape[0] != B or shape[1] < 1
+            or (shape[1] > 1 and strides[1] != 1)):
+        raise _bad(name, what, f"{dtype} [B, slots] with contiguous rows", t, dtype)
+    slots = shape[1]
+    stride = strides[0] if B > 1 else slots
     if stride != slots and (stride < slots or slots < 64 * max_blocks):
         raise ValueError(f"{name}: {what}: rows that are a part of wider ones must have a slot for every entry of block_table")
     return stride
 
 
 def _launch(dev: int, fn: str, args, stream):
-    """Calls the library with tensors' device current (it launches on the current device) and that device's current
+    """Calls the library with the tensors' device current (it launches on the current device) and that device's current
     stream unless one is given."""
-    if stream is not None:
-        raw = stream.cuda_stream
-    else:
-        raw = torch._C._cuda_getCurrentRawStream(dev)
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     if dev == torch._C._cuda_getDevice():
         status = getattr(_lib or lib(), fn)(*args, raw)
     else:
@@ -433,18 +432,17 @@ def _sections(sections: tuple):
     """Host array of a rotation's sections."""
     if not 1 <= len(sections) <= 4 or min(sections) < 0 or sum(sections) != 32:
         raise ValueError("sections must be 1 to 4 counts of pairs that sum to 32")
-    return (_c_int * len(sections))(*sections)
+    return (_c_int * len(sections))(*sections), len(sections)
 
 
 def _axes(name: str, positions: torch.Tensor, sections, N: int, dev: int):
     """Checks positions ([N], or [axes, N]) and sections; returns (pointer, stride, host sections, axes)."""
-    host = _sections(tuple(sections))
-    axes = len(host)
-    _typed(name, "positions", positions, torch.int32, dev)
-    one = positions.dim() == 1
-    if tuple(positions.shape) != ((N,) if one else (axes, N)) or (one and axes != 1) or (N > 1 and positions.stride(-1) != 1):
-        raise ValueError(f"{name}: positions must be [axes, N] (or [N]) with as many axes as sections")
-    return positions.data_ptr(), positions.stride(0) if axes > 1 else N, host, axes
+    host, axes = _sections(sections if type(sections) is tuple else tuple(sections))
+    shape, strides = positions.shape, positions.stride()
+    if (positions.dtype is not _I32 or positions.get_device() != dev or not 1 <= len(shape) <= 2 or shape[-1] != N
+            or (shape[0] if len(shape) == 2 else 1) != axes or (N > 1 and strides[-1] != 1)):
+        raise _bad(name, "positions", f"int32 [{axes} axes, N] (or [N] for one axis) with contiguous rows", positions, _I32)
+    return positions.data_ptr(), strides[0] if axes > 1 else N, host, axes
 
 
 def rope_axes(x: torch.Tensor, positions: torch.Tensor, sections=(32,), out: torch.Tensor | None = None,
@@ -454,50 +452,46 @@ def rope_axes(x: torch.Tensor, positions: torch.Tensor, sections=(32,), out: tor
     turns, one section after the other or (interleaved) dealt out in turn.  out may be x or a view such
     as q[..., 512:] of the decode query.  inverse turns back: the gradient of x from that of out."""
     dev = x.get_device()
-    shape = x.shape
-    if dev < 0 or len(shape) != 3 or shape[2] != 64:
-        raise ValueError("rope_axes: x must be [N, H, 64] on a GPU")
-    _typed("rope_axes", "x", x, torch.bfloat16, dev)
+    shape, xs = x.shape, x.stride()
+    if dev < 0 or x.dtype is not _BF16 or len(shape) != 3 or shape[2] != 64 or xs[2] != 1:
+        raise _bad("rope_axes", "x", "a bfloat16 [N, H, 64] with contiguous rows", x, _BF16)
     N, H, _ = shape
     if out is None:
-        out = torch.empty((N, H, 64), dtype=torch.bfloat16, device=x.device)
-    else:
-        _typed("rope_axes", "out", out, torch.bfloat16, dev)
-        if out.shape != shape:
-            raise ValueError("rope_axes: out must have x's shape")
-    if x.stride(2) != 1 or out.stride(2) != 1:
-        raise ValueError("rope_axes: the 64 values of a row must be contiguous")
+        out = torch.empty((N, H, 64), dtype=_BF16, device=x.device)
+    os_ = out.stride()
+    if out.dtype is not _BF16 or out.get_device() != dev or out.shape != shape or os_[2] != 1:
+        raise _bad("rope_axes", "out", "a bfloat16 of x's shape with contiguous rows", out, _BF16)
     if N == 0 or H == 0:
         return out
     pos, pos_stride, host, axes = _axes("rope_axes", positions, sections, N, dev)
     many, heads = N > 1, H > 1   # the stride of a dim of one element says nothing
     _launch(dev, "mla_rope_axes", (
-        x.data_ptr(), x.stride(0) if many else 0, x.stride(1) if heads else 0, out.data_ptr(),
-        out.stride(0) if many else 0, out.stride(1) if heads else 0, pos, pos_stride, host, axes, interleaved, rope_theta,
-        inverse, N, H), stream)
+        x.data_ptr(), xs[0] if many else 0, xs[1] if heads else 0, out.data_ptr(), os_[0] if many else 0,
+        os_[1] if heads else 0, pos, pos_stride, host, axes, interleaved, rope_theta, inverse, N, H), stream)
     return out
 
 
 def _append(name, c, k_pe, kv_cache, kv_scale, block_table, seqlens, new_offsets, positions, sections, rope_theta,
             interleaved, stream):
     dev, B, num_blocks, max_blocks = _paged(name, kv_cache, block_table, seqlens, kv_scale is not None)
-    _typed(name, "c", c, torch.bfloat16, dev)
-    _typed(name, "k_pe", k_pe, torch.bfloat16, dev)
-    N = c.size(0)
-    if tuple(c.shape) != (N, 512) or tuple(k_pe.shape) != (N, 64) or c.stride(1) != 1 or k_pe.stride(1) != 1:
-        raise ValueError(f"{name}: c [N, 512] and k_pe [N, 64] with contiguous rows expected")
+    shape, cs, ps = c.shape, c.stride(), k_pe.stride()
+    if c.dtype is not _BF16 or c.get_device() != dev or len(shape) != 2 or shape[1] != 512 or cs[1] != 1:
+        raise _bad(name, "c", "a bfloat16 [N, 512] with contiguous rows", c, _BF16)
+    N = shape[0]
+    if k_pe.dtype is not _BF16 or k_pe.get_device() != dev or k_pe.shape != (N, 64) or ps[1] != 1:
+        raise _bad(name, "k_pe", f"a bfloat16 [{N}, 64] with contiguous rows", k_pe, _BF16)
     off = None
     if new_offsets is not None:
-        _typed(name, "new_offsets", new_offsets, torch.int32, dev)
-        if tuple(new_offsets.shape) != (B + 1,) or not new_offsets.is_contiguous():
-            raise ValueError(f"{name}: new_offsets must be a contiguous [B + 1]")
+        if (new_offsets.dtype is not _I32 or new_offsets.get_device() != dev or new_offsets.shape != (B + 1,)
+                or not new_offsets.is_contiguous()):
+            raise _bad(name, "new_offsets", "a contiguous int32 [B + 1]", new_offsets, _I32)
         off = new_offsets.data_ptr()
     if N == 0 or B == 0:
         return kv_cache
     rot = (None, 0, None, 0) if positions is None else _axes(name, positions, sections, N, dev)
     pool = (kv_cache.data_ptr(),) if kv_scale is None else (kv_cache.data_ptr(), kv_scale)
     _launch(dev, "mla_" + name, (
-        c.data_ptr(), c.stride(0) if N > 1 else 512, k_pe.data_ptr(), k_pe.stride(0) if N > 1 else 64, *pool, num_blocks,
+        c.data_ptr(), cs[0] if N > 1 else 512, k_pe.data_ptr(), ps[0] if N > 1 else 64, *pool, num_blocks,
         block_table.data_ptr(), max_blocks, seqlens.data_ptr(), off, N, B, *rot, interleaved, rope_theta), stream)
     return kv_cache
 
@@ -522,14 +516,13 @@ def cache_append_fp8(c, k_pe, kv_cache, kv_scale: float, block_table, seqlens, n
 
 def _weights(name, q, lse, kv_cache, kv_scale, block_table, seqlens, softmax_scale, causal, weights, stream):
     dev, B, num_blocks, max_blocks = _paged(name, kv_cache, block_table, seqlens, kv_scale is not None)
-    _typed(name, "q", q, torch.bfloat16, dev)
-    _typed(name, "lse", lse, torch.float32, dev)
     shape = q.shape
-    if len(shape) != 4 or shape[0] != B or shape[3] != 576 or not q.is_contiguous():
-        raise ValueError(f"{name}: q must be a contiguous [B, s_q, H, 576]")
-    if lse.shape != shape[:3] or not lse.is_contiguous():
-        raise ValueError(f"{name}: lse must be a contiguous [B, s_q, H]")
-    stride = _rows(name, "weights", weights, torch.float32, dev, B, max_blocks)
+    if (q.dtype is not _BF16 or q.get_device() != dev or len(shape) != 4 or shape[0] != B or shape[3] != 576
+            or not q.is_contiguous()):
+        raise _bad(name, "q", "a contiguous bfloat16 [B, s_q, H, 576]", q, _BF16)
+    if lse.dtype is not _F32 or lse.get_device() != dev or lse.shape != shape[:3] or not lse.is_contiguous():
+        raise _bad(name, "lse", "a contiguous float32 [B, s_q, H]", lse, _F32)
+    stride = _rows(name, "weights", weights, _F32, dev, B, max_blocks)
     pool = (kv_cache.data_ptr(),) if kv_scale is None else (kv_cache.data_ptr(), kv_scale)
     _launch(dev, "mla_" + name, (
         q.data_ptr(), lse.data_ptr(), *pool, num_blocks, block_table.data_ptr(), max_blocks, seqlens.data_ptr(), B,
@@ -554,25 +547,24 @@ def attn_weights_fp8(q, lse, kv_cache, kv_scale: float, block_table, seqlens, so
 def _evict(name, fp8, kv_cache, block_table, seqlens, weights, budget, sink, recent, arrival, width, new_seqlens, kept,
            weights_out, arrival_out, stream):
     dev, B, num_blocks, max_blocks = _paged(name, kv_cache, block_table, seqlens, fp8)
-    w_stride = _rows(name, "weights", weights, torch.float32, dev, B, max_blocks)
+    w_stride = _rows(name, "weights", weights, _F32, dev, B, max_blocks)
     a_ptr, a_stride = None, 0
     if arrival is not None:
-        a_stride = _rows(name, "arrival", arrival, torch.int32, dev, B, max_blocks)
+        a_stride = _rows(name, "arrival", arrival, _I32, dev, B, max_blocks)
         a_ptr = arrival.data_ptr()
     if width is None:
-        width = weights.size(1)
+        width = weights.shape[1]
 
     def given(what, t, dtype, shape):
         if t is None:
             return torch.empty(shape, dtype=dtype, device=weights.device)
-        _typed(name, what, t, dtype, dev)
-        if tuple(t.shape) != shape or not t.is_contiguous():
-            raise ValueError(f"{name}: {what} must be a contiguous {list(shape)}")
+        if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+            raise _bad(name, what, f"a contiguous {dtype} {list(shape)}", t, dtype)
         return t
 
-    outs = (given("new_seqlens", new_seqlens, torch.int32, (B,)), given("kept", kept, torch.int32, (B, width)),
-            given("weights_out", weights_out, torch.float32, (B, width)),
-            given("arrival_out", arrival_out, torch.int32, (B, width)))
+    wide = (B, width)
+    outs = (given("new_seqlens", new_seqlens, _I32, (B,)), given("kept", kept, _I32, wide),
+            given("weights_out", weights_out, _F32, wide), given("arrival_out", arrival_out, _I32, wide))
     _launch(dev, "mla_" + name, (
         kv_cache.data_ptr(), num_blocks, block_table.data_ptr(), max_blocks, seqlens.data_ptr(), B, weights.data_ptr(),
         w_stride, a_ptr, a_stride, budget, sink, recent, outs[0].data_ptr(), outs[1].data_ptr(), outs[2].data_ptr(),

@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include <cmath>
+#include <cstring>
 
 #include "mla_kernels.h"
 #include "mla_ptx.cuh"
@@ -604,11 +605,19 @@ bool rope_table(const int32_t* sections, int n_axes, int interleaved, float thet
       a = (a + 1) % n_axes;
     }
   }
-  for (int j = 0; j < kPairs; ++j) {
-    const double inv = std::pow(static_cast<double>(theta), -2.0 * j / 64.0);
-    t->hi[j] = static_cast<float>(inv);
-    t->lo[j] = static_cast<float>(inv - static_cast<double>(t->hi[j]));
+  // theta is a constant of the model: its 32 powers are kept from the thread's last call with the same one
+  thread_local float kept_theta = 0.f;
+  thread_local float kept[2][kPairs];
+  if (kept_theta != theta) {
+    for (int j = 0; j < kPairs; ++j) {
+      const double inv = std::pow(static_cast<double>(theta), -2.0 * j / 64.0);
+      kept[0][j] = static_cast<float>(inv);
+      kept[1][j] = static_cast<float>(inv - static_cast<double>(kept[0][j]));
+    }
+    kept_theta = theta;
   }
+  std::memcpy(t->hi, kept[0], sizeof(t->hi));
+  std::memcpy(t->lo, kept[1], sizeof(t->lo));
   const double two_pi = 6.283185307179586476925286766559;
   t->two_pi_hi = static_cast<float>(two_pi);
   t->two_pi_lo = static_cast<float>(two_pi - static_cast<double>(t->two_pi_hi));
