@@ -10,6 +10,7 @@
 #include <cmath>
 #include <cstddef>
 #include <mutex>
+#include <type_traits>
 
 #include "mla_kernels.h"
 #include "mla_ptx.cuh"
@@ -273,6 +274,15 @@ __device__ void w_producer(const WeightsParams& p, const WMaps& maps, WShared& s
 }
 
 // -------------------------------------------------------------------- MMA --
+// Whether a phase is complete; unlike a wait it never suspends the thread.
+__device__ __forceinline__ bool mbar_peek(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+
 template <bool F8>
 __device__ void w_mma(const WeightsParams& p, WShared& sh, uint32_t smem, uint32_t cl) {
   using C = WCfg<F8>;
@@ -288,32 +298,36 @@ __device__ void w_mma(const WeightsParams& p, WShared& sh, uint32_t smem, uint32
       if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&sh.empty[i % C::kStages]));
     if (F8 && !(ok = w_warp_wait(sh, sh.q_full, seg & 1, p.status, cl))) break;
     ++seg;
+    bool ready = false;   // the page's stage and S buffer have been seen free during the page before
     for (int k = s.k0; k < s.k1; ++k, ++i, ++T) {
       const uint32_t st = i % C::kStages, sb = T % kSBufs;
-      ok = w_warp_wait(sh, sh.s_empty[sb], ((T / kSBufs) & 1) ^ 1, p.status, cl) &&
-           w_warp_wait(sh, sh.full[st], (i / C::kStages) & 1, p.status, cl);
+      if (!ready) ok = w_warp_wait(sh, sh.s_empty[sb], ((T / kSBufs) & 1) ^ 1, p.status, cl) &&
+                       w_warp_wait(sh, sh.full[st], (i / C::kStages) & 1, p.status, cl);
       if (!ok) break;
       tc_fence_after();
       const uint32_t stage = smem + st * C::kStageBytes, d = tmem + kSCol0 + sb * kPageTokens;
-      if constexpr (F8) {
-        // chunks of 128 codes, K = 32 a step; the half of q that a step lies in holds its hi, then its lo
+      auto chunks = [&](auto first, auto last) {   // the MMAs of the page's chunks [first, last)
 #pragma unroll
-        for (int c = 0; c < 5; ++c)
+        for (int c = first; c < last; ++c)
 #pragma unroll
-          for (int j = 0; j < (c < 4 ? 4 : 2); ++j) {
+          for (int j = 0; j < (F8 && c == 4 ? 2 : 4); ++j) {
             const uint64_t kd = smem_desc_sw128(stage + c * kChunk + j * 32, 16, 1024);
-            const int step = 4 * c + j, col = 144 * (step / 9) + 8 * (step % 9);
-            mma_f8_ts_warp(d, tmem + kQCol + col, kd, idesc, (c | j) ? 1u : 0u);
-            mma_f8_ts_warp(d, tmem + kQCol + col + 72, kd, idesc, 1u);
+            if constexpr (F8) {   // chunks of 128 codes, K = 32 a step; the half of q that it lies in holds hi, then lo
+              const int step = 4 * c + j, col = 144 * (step / 9) + 8 * (step % 9);
+              mma_f8_ts_warp(d, tmem + kQCol + col, kd, idesc, (c | j) ? 1u : 0u);
+              mma_f8_ts_warp(d, tmem + kQCol + col + 72, kd, idesc, 1u);
+            } else {
+              mma_bf16_ts_warp(d, tmem + kQCol + c * 32 + j * 8, kd, idesc, (c | j) ? 1u : 0u);
+            }
           }
-      } else {
-#pragma unroll
-        for (int c = 0; c < 9; ++c)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma_bf16_ts_warp(d, tmem + kQCol + c * 32 + j * 8, smem_desc_sw128(stage + c * kChunk + j * 32, 16, 1024),
-                             idesc, (c | j) ? 1u : 0u);
-      }
+      };
+      constexpr int kAll = static_cast<int>(C::kKChunks), kFirst = F8 ? 4 : 7;
+      chunks(std::integral_constant<int, 0>(), std::integral_constant<int, kFirst>());
+      // a look at the next page's barriers while MMAs are queued, not between two pages where the pipe would drain
+      ready = k + 1 < s.k1 &&
+              __all_sync(0xffffffffu, mbar_peek(smem_u32(&sh.s_empty[(T + 1) % kSBufs]), (((T + 1) / kSBufs) & 1) ^ 1) &&
+                                          mbar_peek(smem_u32(&sh.full[(i + 1) % C::kStages]), ((i + 1) / C::kStages) & 1));
+      chunks(std::integral_constant<int, kFirst>(), std::integral_constant<int, kAll>());
       mma_commit_warp(smem_u32(&sh.empty[st]));
       mma_commit_warp(smem_u32(&sh.s_full[sb]));
     }
