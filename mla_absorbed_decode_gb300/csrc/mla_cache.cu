@@ -249,6 +249,11 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(const uint32_t* p, uint32_t r
   return v;
 }
 
+__device__ __forceinline__ uint2 ld_cluster_v2(const uint2* p, uint32_t rank) {
+  uint2 v;
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(map_to_rank(smem_u32(p), rank)) : "memory");
+  return v;
+}
 // Asynchronous copy of 4 bytes global -> shared.
 __device__ __forceinline__ void cp_async4(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(smem_u32(dst)), "l"(src) : "memory");
@@ -303,8 +308,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_evict_select_kernel(const 
   SelShared& sh = *reinterpret_cast<SelShared*>(sel_dyn);
   uint32_t* keys = reinterpret_cast<uint32_t*>(sel_dyn + sizeof(SelShared));
   const int log_slice = p.sel_log_slice, slice = 1 << log_slice, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  uint32_t* mask = keys + slice;
-  uint32_t* prefix = mask + slice / 32;
+  uint2* words_of = reinterpret_cast<uint2*>(keys + slice);   // 32 slots each: keep mask, kept slots before
   const int b = static_cast<int>(blockIdx.x) / cl;
   const uint32_t rank = cl > 1 ? cluster_ctarank() : 0;
   auto sync = [&] {
@@ -453,14 +457,14 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_evict_select_kernel(const 
       tie_rank += __popc(tied);
     }
     const uint32_t word = __ballot_sync(0xffffffffu, keep);
-    if (lane == 0) mask[i] = word, prefix[i] = kept;   // prefix: within the run so far
+    if (lane == 0) words_of[i] = make_uint2(word, kept);   // (before: within the run so far)
     kept += __popc(word);
   }
   const uint32_t before_run = __shfl_sync(0xffffffffu, scan_cta(lane == 0 ? kept : 0u, sh.warp_sum, &all), 0);
-  for (int i = w0 + lane; i < w1; i += 32) prefix[i] += before_run;
+  for (int i = w0 + lane; i < w1; i += 32) words_of[i].y += before_run;
   __syncthreads();
   auto kept_before = [&](int t) {   // of this CTA's slots, below its slot t
-    return t >= words * 32 ? all : prefix[t >> 5] + __popc(mask[t >> 5] & ((1u << (t & 31)) - 1u));
+    return t >= words * 32 ? all : words_of[t >> 5].y + __popc(words_of[t >> 5].x & ((1u << (t & 31)) - 1u));
   };
   const int m_here = max(0, min(count, m - t0));   // slots below m of this CTA
   if (tid == 0) sh.kept = all, sh.below = kept_before(m_here);
@@ -475,16 +479,18 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_evict_select_kernel(const 
   // sources in rank order: entry i of the list lies in CTA i / slice (the keys are no longer needed)
 #pragma unroll 4
   for (int i = (m_here / 32 + warp) * 32 + lane; i < words * 32; i += kSelThreads) {
-    const uint32_t word = mask[i >> 5], lower = (1u << (i & 31)) - 1u;
-    if (i >= m_here && (word & (lower + 1u))) {
-      const uint32_t at = first + prefix[i >> 5] + __popc(word & lower) - below;
+    const uint2 word = words_of[i >> 5];
+    const uint32_t lower = (1u << (i & 31)) - 1u;
+    if (i >= m_here && (word.x & (lower + 1u))) {
+      const uint32_t at = first + word.y + __popc(word.x & lower) - below;
       uint32_t* entry = keys + (at & (slice - 1));
       if (cl > 1) st_cluster_u32(map_to_rank(smem_u32(entry), at >> log_slice), static_cast<uint32_t>(t0 + i));
       else *entry = static_cast<uint32_t>(i);
     }
   }
   if (cl > 1) {
-    if (tid == 0) sh.need = first;   // the CTA's first kept slot's rank, for the outputs below
+    __syncthreads();   // every thread has its words' counts; from here on they are the request's
+    for (int i = tid; i < words; i += kSelThreads) words_of[i].y += first;
   }
   sync();
 
@@ -494,22 +500,19 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_evict_select_kernel(const 
   const int64_t stride = static_cast<int64_t>(cl) * kSelThreads;
   for (int64_t j0 = static_cast<int64_t>(rank) * kSelThreads + tid; j0 < p.width; j0 += kEach * stride) {
     int src[kEach];
-    uint32_t word[kEach];
+    uint2 word[kEach];
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       const int64_t j = j0 + i * stride;
       src[i] = j < m ? static_cast<int>(j) : -1;
-      const int at = src[i] & (slice - 1);
-      word[i] = src[i] < 0 ? ~0u : cl > 1 ? ld_cluster_u32(&mask[at >> 5], src[i] >> log_slice) : mask[at >> 5];
+      const uint2* at = words_of + ((src[i] & (slice - 1)) >> 5);
+      word[i] = src[i] < 0 ? make_uint2(~0u, 0) : cl > 1 ? ld_cluster_v2(at, src[i] >> log_slice) : *at;
     }
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       const uint32_t bit = 1u << (src[i] & 31);
-      if (!(word[i] & bit)) {
-        const uint32_t r = src[i] >> log_slice, at = (src[i] & (slice - 1)) >> 5;
-        const uint32_t kept_below = (cl > 1 ? ld_cluster_u32(&sh.need, r) + ld_cluster_u32(&prefix[at], r) : prefix[at]) +
-                                    __popc(word[i] & (bit - 1u));
-        const uint32_t hole = static_cast<uint32_t>(src[i]) - kept_below;
+      if (!(word[i].x & bit)) {
+        const uint32_t hole = static_cast<uint32_t>(src[i]) - word[i].y - __popc(word[i].x & (bit - 1u));
         src[i] = static_cast<int>(cl > 1 ? ld_cluster_u32(&keys[hole & (slice - 1)], hole >> log_slice) : keys[hole]);
       }
     }
