@@ -311,7 +311,9 @@ mla_status_t mla_extend_chunked(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe
                                 float* lse, mla_stream_t stream);
 
 /* ---- The latent cache over a request's life: rotation with several position axes, the write
- * of new rows, the attention weight of every cached token, and eviction by it. ---- */
+ * of new rows, the attention weight of every cached token, and eviction by it.  None of the calls
+ * keeps anything between calls or needs a workspace; a device's one-time set-up happens in its
+ * first call, which is to be made before a stream capture. ---- */
 
 /* RoPE with several position axes (a token of an image or a video has a time, a height and a
  * width): every one of the 32 adjacent pairs of a 64-value row turns by the position on its
@@ -380,8 +382,10 @@ mla_status_t mla_cache_append_fp8(const mla_bf16_t* c, int64_t c_row_stride, con
  *  lse            [B, s_q, H] fp32; a row with lse = -inf gave no weight and adds nothing
  *  weights        fp32 device, 4-byte aligned, weights_stride elements between requests
  *                 (>= every seqlens[b]); elements from seqlens[b] on are neither read nor written
- * Scores, exponentials and sums are in fp32; every weights[b, t] is summed in a fixed order, so
- * that equal inputs give equal bits.  The rest as for mla_decode (no metadata, no workspace).
+ * softmax_scale (times kv_scale) times log2(e) has to be a normal float32.  Scores,
+ * exponentials and sums are in fp32; every weights[b, t] is summed in a fixed order and added to
+ * once, so that equal inputs give equal bits (a sum below 2^-126 may become 0).  The rest as for
+ * mla_decode (no metadata, no workspace).
  * A request with seqlens[b] outside [0, min(64 max_blocks, weights_stride)] or a page outside
  * [0, num_blocks) is reported as MLA_ERR_DEVICE_BOUNDS (the tokens concerned add nothing).
  * Async on stream. */
@@ -422,7 +426,7 @@ mla_status_t mla_attn_weights_fp8(const mla_bf16_t* q, const float* lse, const u
  *  arrival_out    int32 [B, width] or NULL: the numbers moved along; e + (j - m) for j >= m, the
  *                 numbers of the tokens that mla_cache_append will put there
  *  width          >= min(budget, 64 max_blocks, weights_stride)
- * weights_out and arrival_out must not overlap weights or arrival.  At most 262144 slots a request:
+ * kept, weights_out and arrival_out must overlap neither one another nor weights or arrival.  At most 262144 slots a request:
  * min(64 max_blocks, weights_stride) beyond that is MLA_ERR_UNSUPPORTED.  A request whose length
  * is out of range is reported as MLA_ERR_DEVICE_BOUNDS and treated as empty; a row whose page is
  * out of range is reported and not copied.  Two kernels on `stream`.  Async on stream. */

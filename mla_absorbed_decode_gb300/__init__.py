@@ -523,6 +523,8 @@ def _weights(name, q, lse, kv_cache, kv_scale, block_table, seqlens, softmax_sca
     if lse.dtype is not _F32 or lse.get_device() != dev or lse.shape != shape[:3] or not lse.is_contiguous():
         raise _bad(name, "lse", "a contiguous float32 [B, s_q, H]", lse, _F32)
     stride = _rows(name, "weights", weights, _F32, dev, B, max_blocks)
+    if q.numel() == 0:
+        return weights
     pool = (kv_cache.data_ptr(),) if kv_scale is None else (kv_cache.data_ptr(), kv_scale)
     _launch(dev, "mla_" + name, (
         q.data_ptr(), lse.data_ptr(), *pool, num_blocks, block_table.data_ptr(), max_blocks, seqlens.data_ptr(), B,
@@ -565,6 +567,8 @@ def _evict(name, fp8, kv_cache, block_table, seqlens, weights, budget, sink, rec
     wide = (B, width)
     outs = (given("new_seqlens", new_seqlens, _I32, (B,)), given("kept", kept, _I32, wide),
             given("weights_out", weights_out, _F32, wide), given("arrival_out", arrival_out, _I32, wide))
+    if B == 0:
+        return outs
     _launch(dev, "mla_" + name, (
         kv_cache.data_ptr(), num_blocks, block_table.data_ptr(), max_blocks, seqlens.data_ptr(), B, weights.data_ptr(),
         w_stride, a_ptr, a_stride, budget, sink, recent, outs[0].data_ptr(), outs[1].data_ptr(), outs[2].data_ptr(),

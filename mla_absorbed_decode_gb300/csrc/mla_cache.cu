@@ -697,12 +697,16 @@ mla_status_t evict_impl(void* kv_cache, bool fp8, int64_t num_blocks, const int3
   int64_t slots = static_cast<int64_t>(max_blocks) * kPageTokens;
   slots = slots < weights_stride ? slots : weights_stride;
   if (width < (budget < slots ? budget : slots)) return MLA_ERR_INVALID_ARG;
-  const uint64_t in_w = (static_cast<uint64_t>(B) - 1) * weights_stride + slots;
-  const uint64_t out = static_cast<uint64_t>(B) * width;
-  const uint64_t in_a = arrival ? (static_cast<uint64_t>(B) - 1) * arrival_stride + slots : 0;
-  for (const void* o : {static_cast<const void*>(weights_out), static_cast<const void*>(arrival_out)})
-    if (o && (overlap(o, out * 4, weights, in_w * 4) || (arrival && overlap(o, out * 4, arrival, in_a * 4))))
-      return MLA_ERR_INVALID_ARG;
+  // what is written may overlap neither the rows that are read nor one another
+  const uint64_t out_bytes = static_cast<uint64_t>(B) * width * 4;
+  const struct { const void* at; uint64_t bytes; } span[] = {
+      {kept, out_bytes}, {weights_out, out_bytes}, {arrival_out, out_bytes},
+      {weights, ((static_cast<uint64_t>(B) - 1) * weights_stride + slots) * 4},
+      {arrival, ((static_cast<uint64_t>(B) - 1) * arrival_stride + slots) * 4}};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 5; ++j)
+      if (span[i].at && span[j].at && overlap(span[i].at, span[i].bytes, span[j].at, span[j].bytes))
+        return MLA_ERR_INVALID_ARG;
   if (slots > kEvictMaxSlots || num_blocks * kPageTokens > (int64_t(1) << 31) - kPageTokens || B > kScheduleMaxB)
     return MLA_ERR_UNSUPPORTED;
   if (arrival && arrival_stride < slots) slots = arrival_stride;

@@ -835,6 +835,7 @@ mla_status_t weights_impl(const mla_bf16_t* q, const float* lse, const void* kv_
   const double scale = static_cast<double>(softmax_scale) * 1.4426950408889634074 * (fp8 ? kv_scale : 1.0);
   p.scale_hi = static_cast<float>(scale);
   p.scale_lo = static_cast<float>(scale - static_cast<double>(p.scale_hi));
+  if (!std::isnormal(p.scale_hi)) return MLA_ERR_INVALID_ARG;
   p.weights = weights;
   p.weights_stride = weights_stride;
   p.status = device_status_word();

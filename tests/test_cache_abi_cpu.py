@@ -83,11 +83,12 @@ def test_evict_checks(mla, fp8):
     call = L.mla_evict_fp8 if fp8 else L.mla_evict
     # (kv, num_blocks, table, max_blocks, seqlens, B, weights, w_stride, arrival, a_stride, budget, sink, recent,
     #  new_seqlens, kept, weights_out, arrival_out, width, stream)
-    ok = [A, 4, A, 2, A, 3, A, 128, 2 * A, 128, 100, 4, 16, A, A, 1 << 40, 1 << 41, 100, None]
+    ok = [A, 4, A, 2, A, 3, A, 128, 2 * A, 128, 100, 4, 16, A, 1 << 42, 1 << 40, 1 << 41, 100, None]
     _broken(call, ok, 1, _0=(None, A + 8), _1=(0,), _2=(None, A + 2), _3=(0,), _4=(None, A + 2), _5=(0,), _6=(None, A + 2),
             _7=(0,), _8=(2 * A + 2,), _9=(0,), _10=(0, -1, 19), _11=(-1, 85), _12=(-1, 97, 2 ** 31 - 1),
             _13=(None, A + 2), _14=(None, A + 2), _15=(None, A + 2), _16=(A + 2,), _17=(99, 0))
-    _broken(call, ok, 1, _15=(A, A + 4, A - 4 * 299, 2 * A + 4), _16=(A, 2 * A, 2 * A + 4 * 383))   # over the inputs
+    _broken(call, ok, 1, _14=(A, 1 << 40, (1 << 41) + 1196), _15=(A, A + 4, A - 4 * 299, 2 * A + 4, (1 << 42) - 4),
+            _16=(A, 2 * A, 2 * A + 4 * 383))   # over the inputs or one another
     wide = list(ok)
     wide[3], wide[7], wide[8], wide[9], wide[16] = 8193, 524352, None, 0, None
     assert call(*wide) == 2
@@ -106,3 +107,10 @@ def test_tensors_that_are_not_on_a_gpu_are_refused(mla):
                          torch.zeros(1, 128))
     with pytest.raises(ValueError):
         mla.evict(kv, table, lens, torch.zeros(1, 128), 4)
+
+
+def test_scales_that_leave_the_normal_numbers_are_refused(mla):
+    L = mla.lib()
+    # softmax_scale * kv_scale * log2(e) against [2^-126 = 1.18e-38, 3.4e38]
+    for scale, kv_scale in ((1e-39, 1.0), (3e38, 1.0), (1.0, 1e-39), (1e30, 1e30)):
+        assert L.mla_attn_weights_fp8(A, A, A, kv_scale, 4, A, 2, A, 3, 1, 16, scale, 0, A, 128, None) == 1, scale
