@@ -427,6 +427,14 @@ def _launch(dev: int, fn: str, args, stream):
         raise MLAError(status, fn)
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """An output of a call on `stream`, from that stream's memory."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 @functools.lru_cache(maxsize=None)
 def _sections(sections: tuple):
     """Host array of a rotation's sections."""
@@ -457,7 +465,7 @@ def rope_axes(x: torch.Tensor, positions: torch.Tensor, sections=(32,), out: tor
         raise _bad("rope_axes", "x", "a bfloat16 [N, H, 64] with contiguous rows", x, _BF16)
     N, H, _ = shape
     if out is None:
-        out = torch.empty((N, H, 64), dtype=_BF16, device=x.device)
+        out = _empty((N, H, 64), _BF16, x.device, stream)
     os_ = out.stride()
     if out.dtype is not _BF16 or out.get_device() != dev or out.shape != shape or os_[2] != 1:
         raise _bad("rope_axes", "out", "a bfloat16 of x's shape with contiguous rows", out, _BF16)
@@ -559,7 +567,7 @@ def _evict(name, fp8, kv_cache, block_table, seqlens, weights, budget, sink, rec
 
     def given(what, t, dtype, shape):
         if t is None:
-            return torch.empty(shape, dtype=dtype, device=weights.device)
+            return _empty(shape, dtype, weights.device, stream)
         if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
             raise _bad(name, what, f"a contiguous {dtype} {list(shape)}", t, dtype)
         return t

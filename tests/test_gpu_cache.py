@@ -704,3 +704,23 @@ def test_calls_on_two_streams_at_once():
         assert torch.equal(w.cpu(), want_w)
         for x, y in zip(ev, want_ev):
             assert torch.equal(x, y)
+
+
+def test_outputs_made_for_a_given_stream_are_that_stream_s_memory():
+    """`stream=` without an output: the output is free for other work only when that stream has passed."""
+    import mla_absorbed_decode_gb300 as mla
+    side = torch.cuda.Stream()
+    x = torch.randn(33, 2, 64, generator=torch.Generator().manual_seed(31)).to(torch.bfloat16).cuda()
+    pos = torch.arange(33, dtype=torch.int32).repeat(1, 1).cuda()
+    want = mla.rope_axes(x, pos)
+    e = {k: v.cuda() for k, v in _evict_inputs([70, 9], 128, False, seed=32).items()}
+    torch.cuda.synchronize()
+    out = mla.rope_axes(x, pos, stream=side)
+    left = mla.evict(e["kv"], e["table"], e["lens"], e["w"], 64, arrival=e["a"], stream=side)
+    before = [t.data_ptr() for t in (out, *left)]
+    del left
+    on_main = torch.empty_like(out)
+    assert on_main.data_ptr() not in before      # the side stream's pool is not the current stream's
+    side.synchronize()
+    assert torch.equal(out, want)
+    assert mla.get_device_status() == 0
