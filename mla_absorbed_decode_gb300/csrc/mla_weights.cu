@@ -37,14 +37,23 @@ struct WeightsParams {
 
 // A CTA holds one 128-row block of a request's queries (heads x query positions) in TMEM and streams
 // the cached pages past it: S = Q K^T on tcgen05 (TMEM accumulators), then for every row
-// p = exp2(S * scale - lse) and for every token the sum over the rows.  HBM-bound: a page is
-// 72 KiB (36 KiB in FP8) read once, against 9.4 MFLOP, a third of the tensor pipe's time for it.
+// p = exp2(S * scale - lse) and for every token the sum over the rows.  A page is 72 KiB (36 KiB in
+// FP8) read once, against 9.4 MFLOP.  Measured (GPU time of a call, B = 64, H = 128):
+//     bf16, 4096 tokens                       48-49 us  6.4 TB/s, 0.95 of the copy rate: HBM-bound
+//     FP8, 4096 tokens                        33 us     4.9 TB/s, 0.73: the MMAs (q is two E4M3 terms, so bf16's
+//                                                       MMA time for half the bytes), 8 us of start and end
+//     bf16, two query positions, 8192 tokens  113 us    5.5 TB/s, 0.82: the MMAs (45 clk each where 32 is the
+//                                                       pipe's: their operands share shared memory with the loads)
 //  * Rows on the TMEM lanes, tokens on the columns: Q is loaded once per request, and the ring has the
-//    whole of shared memory for pages (221 KiB: what is in flight covers HBM latency).
+//    whole of shared memory for pages (221 KiB: what is in flight covers HBM latency).  Q comes through the ring
+//    too: read from global memory by its threads, 1152 bytes apart, it took 9.5 us instead of 2.4.
+//  * One TMA box a page: boxes of three chunks with a barrier pair each refill the ring earlier, but cost more
+//    (54 us against 51 at 4096 tokens).
 //  * S is read with four of the rows in a lane, so that the sum over the rows is three additions in the
-//    lane, a butterfly over eight lanes that halves the columns with every step (7 shuffles; 31 where a
-//    lane has one row: their issue slots slow the MMAs down, 120 -> 110 us for two query positions), and four partial sums in shared memory,
-//    which a warp of its own adds to the weights: a fixed order.
+//    lane, a butterfly over eight lanes that halves the columns with every step (7 shuffles; with one row a
+//    lane it is 31, whose issue slots the MMA warp misses: 120 us against 113 for two query
+//    positions), and four partial sums in shared memory, which a warp of its own adds to the weights:
+//    a fixed order.
 //  * More than 128 rows: a cluster of ceil(rows / 128) CTAs walks the same pages, each with its row
 //    block; the others hand their 64 sums a page to CTA 0 through distributed shared memory.
 //  * Work: all requests' pages in a row, with kSwitchPages for each request's start, cut evenly over the
@@ -831,7 +840,8 @@ mla_status_t weights_impl(const mla_bf16_t* q, const float* lse, const void* kv_
   p.causal = causal_s_q ? 1 : 0;
   int64_t slots = static_cast<int64_t>(max_blocks) * kPageTokens;
   slots = slots < weights_stride ? slots : weights_stride;
-  p.slots = static_cast<int>(slots < INT32_MAX ? slots : INT32_MAX);
+  constexpr int64_t kMostSlots = INT32_MAX / kPageTokens * kPageTokens;   // token numbers are ints
+  p.slots = static_cast<int>(slots < kMostSlots ? slots : kMostSlots);
   // The MMAs add each step's products to the accumulator by truncation towards zero, so that over the 36 steps a
   // score comes out short: measured, by 8.7 * 2^-24 of itself on average for a bf16 cache and 2.8 * 2^-24 for an
   // FP8 one (N(0, 1) q and k, 131072 scores; 7.3 to 8.7 with k scaled by 0.1 to 2.8), 0.5e-6 beside a spread of the

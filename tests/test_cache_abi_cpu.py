@@ -114,3 +114,12 @@ def test_scales_that_leave_the_normal_numbers_are_refused(mla):
     # softmax_scale * kv_scale * log2(e) against [2^-126 = 1.18e-38, 3.4e38]
     for scale, kv_scale in ((1e-39, 1.0), (3e38, 1.0), (1.0, 1e-39), (1e30, 1e30)):
         assert L.mla_attn_weights_fp8(A, A, A, kv_scale, 4, A, 2, A, 3, 1, 16, scale, 0, A, 128, None) == 1, scale
+
+
+def test_more_rows_than_row_numbers_count_are_refused(mla):
+    L = mla.lib()
+    far = 1 << 44
+    n = (1 << 30) + 1
+    assert L.mla_rope_axes(A, 128, 64, far, 128, 64, 2 * far, n, _sections(32), 1, 0, 10000.0, 0, n, 2, None) == 2
+    assert L.mla_cache_append(A, 576, 2 * far, 576, far, 4, 3 * far, 2, 4 * far, 5 * far, n, 3, 6 * far, n,
+                              _sections(32), 1, 0, 10000.0, None) == 2
