@@ -40,10 +40,11 @@ struct WeightsParams {
 // p = exp2(S * scale - lse) and for every token the sum over the rows.  A page is 72 KiB (36 KiB in
 // FP8) read once, against 9.4 MFLOP.  Measured (GPU time of a call, B = 64, H = 128):
 //     bf16, 4096 tokens                       48-49 us  6.4 TB/s, 0.95 of the copy rate: HBM-bound
-//     FP8, 4096 tokens                        33 us     4.9 TB/s, 0.73: the MMAs (q is two E4M3 terms, so bf16's
-//                                                       MMA time for half the bytes), 8 us of start and end
-//     bf16, two query positions, 8192 tokens  113 us    5.5 TB/s, 0.82: the MMAs (45 clk each where 32 is the
-//                                                       pipe's: their operands share shared memory with the loads)
+//     FP8, 4096 tokens                        31-32 us  5.2 TB/s, 0.77: the MMAs (q is two E4M3 terms, so bf16's
+//                                                       MMA time for half the bytes; 1290 clk a page, 1152 of
+//                                                       them the tensor pipe's), 7 us of start and end
+//     bf16, two query positions, 8192 tokens  109-113 us  5.7 TB/s, 0.84: 1430 clk a page, 1152 of them the
+//                                                       tensor pipe's, 150 waits for a page that two CTAs load
 //  * Rows on the TMEM lanes, tokens on the columns: Q is loaded once per request, and the ring has the
 //    whole of shared memory for pages (221 KiB: what is in flight covers HBM latency).  Q comes through the ring
 //    too: read from global memory by its threads, 1152 bytes apart, it took 9.5 us instead of 2.4.
@@ -52,7 +53,7 @@ struct WeightsParams {
 //  * S is read with four of the rows in a lane, so that the sum over the rows is three additions in the
 //    lane, a butterfly over eight lanes that halves the columns with every step (7 shuffles; with one row a
 //    lane it is 31, whose issue slots the MMA warp misses: 120 us against 113 for two query
-//    positions), and four partial sums in shared memory, which a warp of its own adds to the weights:
+//    positions, before the steps got shorter), and four partial sums in shared memory, which a warp of its own adds to the weights:
 //    a fixed order.
 //  * More than 128 rows: a cluster of ceil(rows / 128) CTAs walks the same pages, each with its row
 //    block; the others hand their 64 sums a page to CTA 0 through distributed shared memory.
@@ -292,10 +293,35 @@ __device__ __forceinline__ bool mbar_peek(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// One lane of the warp, the same every time.
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e;
+}
+// An MMA step by the lane that has `lead`, all lanes with the same operands: A in TMEM, B at shared-memory address
+// 16 k_lo, 128-byte swizzle.  The lane is elected once a page, not a step, and a step's address is one 32-bit addition: the
+// issue slots that a step takes are what the epilogue warps leave of an SM's quarter (FP8: 33.0 -> 31.6 us, two query
+// positions: 116.6 -> 112.0; alone beside warps of FMAs, a step every 34 clk where it was 55).
+template <bool F8>
+__device__ __forceinline__ void mma_step(uint32_t d_tmem, uint32_t a_tmem, uint32_t k_lo, uint32_t accumulate, uint32_t lead) {
+  constexpr uint32_t idesc = F8 ? idesc_e4m3_f32(128, 64, 0, 0) : idesc_bf16_f32(128, 64, 0, 0);
+  constexpr uint32_t k_hi = (1024u >> 4) | (1u << 14) | (2u << 29);   // 8 rows are 1024 bytes; version 1, 128-byte swizzle
+  if constexpr (F8)
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 k;\n\tmov.b64 k, {%2, %3};\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 e, %6, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], k, %4, p;\n\t}"
+        :: "r"(d_tmem), "r"(a_tmem), "r"(k_lo), "r"(k_hi), "r"(idesc), "r"(accumulate), "r"(lead) : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 k;\n\tmov.b64 k, {%2, %3};\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 e, %6, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], k, %4, p;\n\t}"
+        :: "r"(d_tmem), "r"(a_tmem), "r"(k_lo), "r"(k_hi), "r"(idesc), "r"(accumulate), "r"(lead) : "memory");
+}
+
 template <bool F8>
 __device__ void w_mma(const WeightsParams& p, WShared& sh, uint32_t smem, uint32_t cl) {
   using C = WCfg<F8>;
-  constexpr uint32_t idesc = F8 ? idesc_e4m3_f32(128, 64, 0, 0) : idesc_bf16_f32(128, 64, 0, 0);
   const uint32_t tmem = sh.tmem_base;
   WWalk<C::kSwitchPages> walk(sh);
   WSegment s;
@@ -314,25 +340,27 @@ __device__ void w_mma(const WeightsParams& p, WShared& sh, uint32_t smem, uint32
                        w_warp_wait(sh, sh.full[st], (i / C::kStages) & 1, p.status, cl);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t stage = smem + st * C::kStageBytes, d = tmem + kSCol0 + sb * kPageTokens;
+      const uint32_t d = tmem + kSCol0 + sb * kPageTokens, lead = elect_lane();
+      const uint32_t page = (((smem + st * C::kStageBytes) >> 4) & 0x3FFF) | (1u << 16);   // (16 bytes: unused with a swizzle)
       auto chunks = [&](auto first, auto last) {   // the MMAs of the page's chunks [first, last)
 #pragma unroll
         for (int c = first; c < last; ++c)
 #pragma unroll
           for (int j = 0; j < (F8 && c == 4 ? 2 : 4); ++j) {
-            const uint64_t kd = smem_desc_sw128(stage + c * kChunk + j * 32, 16, 1024);
+            const uint32_t at = page + (c * kChunk + j * 32) / 16;
             if constexpr (F8) {   // chunks of 128 codes, K = 32 a step; the half of q that it lies in holds hi, then lo
               const int step = 4 * c + j, col = 144 * (step / 9) + 8 * (step % 9);
-              mma_f8_ts_warp(d, tmem + kQCol + col, kd, idesc, (c | j) ? 1u : 0u);
-              mma_f8_ts_warp(d, tmem + kQCol + col + 72, kd, idesc, 1u);
+              mma_step<F8>(d, tmem + kQCol + col, at, (c | j) ? 1u : 0u, lead);
+              mma_step<F8>(d, tmem + kQCol + col + 72, at, 1u, lead);
             } else {
-              mma_bf16_ts_warp(d, tmem + kQCol + c * 32 + j * 8, kd, idesc, (c | j) ? 1u : 0u);
+              mma_step<F8>(d, tmem + kQCol + c * 32 + j * 8, at, (c | j) ? 1u : 0u, lead);
             }
           }
       };
       constexpr int kAll = static_cast<int>(C::kKChunks), kFirst = F8 ? 4 : 7;
       chunks(std::integral_constant<int, 0>(), std::integral_constant<int, kFirst>());
       // a look at the next page's barriers while MMAs are queued, not between two pages where the pipe would drain
+      // (FP8: 31.8 -> 30.9 us)
       ready = k + 1 < s.k1 &&
               __all_sync(0xffffffffu, mbar_peek(smem_u32(&sh.s_empty[(T + 1) % kSBufs]), (((T + 1) / kSBufs) & 1) ^ 1) &&
                                           mbar_peek(smem_u32(&sh.full[(i + 1) % C::kStages]), ((i + 1) / C::kStages) & 1));
