@@ -410,8 +410,8 @@ mla_status_t mla_attn_weights_fp8(const mla_bf16_t* q, const float* lse, const u
  * ascending order, take the staying tokens from slot m on, in ascending order: attention without a
  * causal mask does not depend on the order of the slots, and tokens that arrive later still come
  * after all of these.
- *  kv_cache       bf16 (mla_evict_fp8: one byte a value), changed in place; no other request of the
- *                 call may use the same pages.  num_blocks, block_table, max_blocks as for mla_decode
+ *  kv_cache       bf16 (mla_evict_fp8: one byte a value), changed in place; no page may be there twice,
+ *                 in one request or in two.  num_blocks, block_table, max_blocks as for mla_decode
  *  seqlens        [B] int32 device, each in [0, min(64 max_blocks, weights_stride, and
  *                 arrival_stride where arrival is given)]
  *  weights        fp32 [B] rows of weights_stride elements (mla_attn_weights)
@@ -426,8 +426,8 @@ mla_status_t mla_attn_weights_fp8(const mla_bf16_t* q, const float* lse, const u
  *  arrival_out    int32 [B, width] or NULL: the numbers moved along; e + (j - m) for j >= m, the
  *                 numbers of the tokens that mla_cache_append will put there
  *  width          >= min(budget, 64 max_blocks, weights_stride)
- * kept, weights_out and arrival_out must overlap neither one another nor weights or arrival.  At most 262144 slots a request:
- * min(64 max_blocks, weights_stride) beyond that is MLA_ERR_UNSUPPORTED.  A request whose length
+ * kept, weights_out and arrival_out must overlap neither one another nor weights or arrival.
+ * At most 262144 slots a request: min(64 max_blocks, weights_stride) beyond that is MLA_ERR_UNSUPPORTED.  A request whose length
  * is out of range is reported as MLA_ERR_DEVICE_BOUNDS and treated as empty; a row whose page is
  * out of range is reported and not copied.  Two kernels on `stream`.  Async on stream. */
 mla_status_t mla_evict(mla_bf16_t* kv_cache, int64_t num_blocks, const int32_t* block_table, int max_blocks,

@@ -45,6 +45,7 @@ struct WeightsParams {
 //                                                       them the tensor pipe's), 7 us of start and end
 //     bf16, two query positions, 8192 tokens  109-113 us  5.7 TB/s, 0.84: 1430 clk a page, 1152 of them the
 //                                                       tensor pipe's, 150 waits for a page that two CTAs load
+// Called for seconds on end, the last two run into the power limit (1.35 kW): 36 us at 1.70 GHz and 126 us at 1.33 GHz.
 //  * Rows on the TMEM lanes, tokens on the columns: Q is loaded once per request, and the ring has the
 //    whole of shared memory for pages (221 KiB: what is in flight covers HBM latency).  Q comes through the ring
 //    too: read from global memory by its threads, 1152 bytes apart, it took 9.5 us instead of 2.4.
