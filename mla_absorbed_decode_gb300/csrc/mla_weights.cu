@@ -43,9 +43,8 @@ struct WeightsParams {
 //     FP8, 4096 tokens                        31-32 us  5.2 TB/s, 0.77: the MMAs (q is two E4M3 terms, so bf16's
 //                                                       MMA time for half the bytes; 1290 clk a page, 1152 of
 //                                                       them the tensor pipe's), 7 us of start and end
-//     bf16, two query positions, 8192 tokens  109-113 us  5.7 TB/s, 0.84: 1430 clk a page, 1152 of them the
-//                                                       tensor pipe's, 150 waits for a page that two CTAs load
-// Called for seconds on end, the last two run into the power limit (1.35 kW): 36 us at 1.70 GHz and 126 us at 1.33 GHz.
+//     bf16, two query positions, 8192 tokens  99-103 us  6.2 TB/s, 0.92: HBM and the MMAs (81.8 us at the pipe's rate)
+// Called for seconds on end, the last two run into the power limit (1.35 kW): 36 us at 1.70 GHz and 115 us at 1.50 GHz.
 //  * Rows on the TMEM lanes, tokens on the columns: Q is loaded once per request, and the ring has the
 //    whole of shared memory for pages (221 KiB: what is in flight covers HBM latency).  Q comes through the ring
 //    too: read from global memory by its threads, 1152 bytes apart, it took 9.5 us instead of 2.4.
@@ -53,11 +52,14 @@ struct WeightsParams {
 //    (54 us against 51 at 4096 tokens).
 //  * S is read with four of the rows in a lane, so that the sum over the rows is three additions in the
 //    lane, a butterfly over eight lanes that halves the columns with every step (7 shuffles; with one row a
-//    lane it is 31, whose issue slots the MMA warp misses: 120 us against 113 for two query
-//    positions, before the steps got shorter), and four partial sums in shared memory, which a warp of its own adds to the weights:
-//    a fixed order.
+//    lane it is 31, whose issue slots the MMA warp misses), and four partial sums in shared memory, which a
+//    warp of its own adds to the weights: a fixed order.
 //  * More than 128 rows: a cluster of ceil(rows / 128) CTAs walks the same pages, each with its row
 //    block; the others hand their 64 sums a page to CTA 0 through distributed shared memory.
+//  * Two CTAs whose row blocks share pages make a pair: one MMA of 256 rows (cta_group::2), for which each
+//    loads half of a page's tokens.  That halves what a page costs in L2 reads and shared memory: 111 us before, each CTA
+//    with whole pages, and 126 us at the power limit.  Three row blocks stay single: padded to two pairs, a third fewer
+//    clusters fit (54.0 us against 43.1 for 16 requests of 8192 tokens).
 //  * Work: all requests' pages in a row, with kSwitchPages for each request's start, cut evenly over the
 //    clusters that fit the GPU.  Each CTA finds its own piece from the lengths (no schedule, no metadata).
 constexpr int kWThreads = 352;                 // warp 0: TMA, 1: MMA, 2..9: exponentials, 10: sums
@@ -66,7 +68,6 @@ constexpr int kSBufs = 3;                      // S accumulators in TMEM
 constexpr int kPartBufs = 4;                   // pages of partial sums between the epilogue and the sum warp
 constexpr uint32_t kQCol = 0, kSCol0 = 320;    // TMEM columns: Q [0, 288), S at 320, 384, 448
 constexpr int kRecvRows = 12;                  // cluster: 64-token sums in flight towards CTA 0: a slot takes cl - 1
-constexpr uint32_t kChunk = 8192;              // 64 rows x 128 bytes, 128-byte swizzle
 constexpr uint64_t kTimeoutNs = 500ull * 1000 * 1000;
 
 // 16 consecutive 32-bit columns of this thread's TMEM lane.
@@ -79,25 +80,33 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr));
 }
 
-template <bool F8>
+template <bool F8, bool Pair>
 struct WCfg {
+  static constexpr uint32_t kTokens = Pair ? 32 : 64;           // of a page that a CTA loads
+  static constexpr uint32_t kChunk = kTokens * 128;             // 128 bytes of each, 128-byte swizzle
   static constexpr uint32_t kKChunks = F8 ? 5 : 9;
-  static constexpr uint32_t kStageBytes = kKChunks * kChunk;    // a page (FP8: the RoPE codes zero-padded)
-  static constexpr int kStages = F8 ? 5 : 3;
-  static constexpr int kQItems = F8 ? 4 : 2;                    // a row block's q in ring items of kQRows rows
+  static constexpr uint32_t kStageBytes = kKChunks * kChunk;    // (FP8: the RoPE codes zero-padded)
+  static constexpr int kStages = (F8 ? 5 : 3) * (Pair ? 2 : 1);
+  static constexpr int kQItems = (F8 ? 4 : 2) * (Pair ? 2 : 1); // a row block's q in ring items of kQRows rows
   static constexpr int kQRows = 128 / kQItems;
+  static constexpr uint32_t kEpiArrivals = kEpiWarps * (Pair ? 2 : 1);   // where a pair's epilogue warps all arrive
   static constexpr uint32_t kQItemBytes = static_cast<uint32_t>(kQRows) * kDimQK * 2;
-  // what a switch of requests costs (Q's load and its way into TMEM), in pages: the split charges it
-  static constexpr int kSwitchPages = F8 ? 5 : 2;
+  // what a switch of requests costs (Q's load and its way into TMEM), in pages: the split charges it.  A pair's pages
+  // take less time (two query positions, 64 requests of up to 8192 tokens: 66.4 us with 2, 64.1 with 6, 62.0 with 8; 128
+  // of up to 400: 21.6, 22.6 and 23.5 with 4, 6 and 8).
+  static constexpr int kSwitchPages = Pair ? (F8 ? 10 : 6) : F8 ? 5 : 2;
+  static_assert(kQRows * 128 % 1024 == 0 && kStageBytes % 1024 == 0, "swizzled rows start where the swizzle does");
   static constexpr uint32_t kOffShared = kStages * kStageBytes;
   static_assert(kQItemBytes <= kStageBytes && kQItems <= kStages, "a row block's q is resident at once");
 };
 
 struct WShared {
-  uint64_t full[5], empty[5];
+  uint64_t full[10], empty[10];                // (a pair's full: in its first CTA, for both halves of a page)
+  uint64_t q_item[8];                          // a row block's q has arrived
   uint64_t s_full[kSBufs], s_empty[kSBufs];
   uint64_t part_full[kPartBufs], part_empty[kPartBufs];
   uint64_t q_read;                             // FP8: raw q is in TMEM, and the rows' maxima are in amax
+  uint64_t q_taken;                            // FP8: q has left the ring (of both CTAs of a pair)
   uint64_t q_full, drain;
   uint64_t recv_full[kRecvRows];               // CTA 0: the other CTAs' sums have arrived
   uint64_t credit[kRecvRows];                  // the other CTAs: CTA 0 has taken what was in the slot
@@ -113,8 +122,11 @@ struct WShared {
 // pairs of sums are read, written and sent as 8 bytes
 static_assert(offsetof(WShared, part) % 16 == 0 && offsetof(WShared, recv) % 16 == 0 && alignof(WShared) == 16, "alignment");
 template <bool F8>
-constexpr uint32_t weights_smem() { return WCfg<F8>::kOffShared + sizeof(WShared); }
+constexpr uint32_t weights_smem() { return WCfg<F8, false>::kOffShared + sizeof(WShared); }
 static_assert(weights_smem<false>() <= 232448 && weights_smem<true>() <= 232448, "shared memory per CTA");
+static_assert(WCfg<false, true>::kOffShared == WCfg<false, false>::kOffShared &&
+              WCfg<true, true>::kOffShared == WCfg<true, false>::kOffShared && WCfg<true, true>::kStages == 10 &&
+              WCfg<true, true>::kQItems == 8, "a pair's CTAs lay shared memory out as others do");
 
 struct WMaps {
   CUtensorMap kv;     // bf16: [chunk 0..8][row][64 dims]; FP8: [chunk 0..3][row][128 codes]; box: all chunks of 64 rows
@@ -147,11 +159,12 @@ __device__ __forceinline__ bool w_wait(WShared& sh, uint64_t& bar, uint32_t pari
 __device__ __forceinline__ bool w_warp_wait(WShared& sh, uint64_t& bar, uint32_t parity, int* status, uint32_t cl) {
   return __all_sync(0xffffffffu, w_wait(sh, bar, parity, status, cl));
 }
-__device__ __noinline__ void w_drain(uint64_t& bar, uint32_t parity) {   // ignores the abort flag
+__device__ __noinline__ bool w_drain(uint64_t& bar, uint32_t parity) {   // ignores the abort flag
   const uint32_t a = smem_u32(&bar);
   const uint64_t t0 = global_timer_ns();
   while (!mbar_test(a, parity))
-    if (global_timer_ns() - t0 > kTimeoutNs) return;
+    if (global_timer_ns() - t0 > kTimeoutNs) return false;
+  return true;
 }
 
 // --------------------------------------------------------------- the walk --
@@ -241,47 +254,94 @@ __device__ __forceinline__ uint64_t l2_policy_evict_normal() {
   return p;
 }
 
-template <bool F8>
+// Loads of a pair: the barrier may be the other CTA's (addresses of the cluster).
+__device__ __forceinline__ void pair_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
+                                             uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5}], [%2], %6;"
+      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy) : "memory");
+}
+__device__ __forceinline__ void pair_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y,
+                                             uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
+      " [%0], [%1, {%3, %4}], [%2], %5;"
+      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(policy) : "memory");
+}
+
+// A pair's CTAs load half of each page's tokens each, and the first one's barrier counts both halves.  Neither half can
+// be a use of the stage ahead: both CTAs' stages are given back together, once the first one's barrier has completed
+// (pages) or both have taken their q.
+template <bool F8, bool Pair>
 __device__ void w_producer(const WeightsParams& p, const WMaps& maps, WShared& sh, uint32_t smem, uint32_t rank,
                            uint32_t cl) {
-  using C = WCfg<F8>;
+  using C = WCfg<F8, Pair>;
   WWalk<C::kSwitchPages> walk(sh);
   WSegment s;
-  uint32_t i = 0;
-  // A page that one SM reads need not stay in L2 (50.5 us against 53.7 for 64 requests of 4096 tokens); one that the
-  // CTAs of a cluster read, each by itself, has to until the last of them (145 us against 176 for two
-  // query positions over 8192 tokens; 163 where they shared the loads by multicast).
-  const uint64_t policy = cl == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
+  uint32_t i = 0, seg = 0, q_seg = 0, q_last = 0;   // q_last: the last ring item of the latest q
+  int q_flying = 0;                                 // how many items of the latest q have been asked for
+  const bool first = !Pair || (rank & 1) == 0;
+  // A page that one CTA or pair reads need not stay in L2 (50.5 us against 53.7 for 64 requests of 4096 tokens); one that
+  // several read, each by itself, has to until the last of them (145 us against 176 for two CTAs over 64 x 8192 tokens; 163
+  // where they shared the loads by multicast).
+  const uint64_t policy = cl == (Pair ? 2 : 1) ? l2_policy_evict_first() : l2_policy_evict_normal();
   bool ok = true;
-  auto stage_for = [&](uint32_t bytes) {   // waits for the next ring stage, which then expects `bytes`
+  auto stage_free = [&]() {   // waits for the next ring stage
     const uint32_t st = i % C::kStages;
     ok = w_wait(sh, sh.empty[st], ((i / C::kStages) & 1) ^ 1, p.status, cl);
-    if (ok) mbar_arrive_expect_tx(smem_u32(&sh.full[st]), bytes), ++i;
+    if (ok) ++i;
     return st;
   };
-  while (ok && walk.next(p, s)) {
+  for (; ok && walk.next(p, s); ++seg) {
+    // the q before has been taken, so that its items' barriers are free (a stage that has come round again says so, too)
+    if (seg > 0 && i <= q_last + C::kStages &&
+        !(ok = w_wait(sh, sh.empty[q_last % C::kStages], (q_last / C::kStages) & 1, p.status, cl)))
+      break;
+    q_flying = 0;
+    q_seg = seg;
     for (int j = 0; j < C::kQItems && ok; ++j) {
-      const uint32_t st = stage_for(C::kQItemBytes);
-      if (ok)
-        tma_load_3d(smem + st * C::kStageBytes, &maps.q, smem_u32(&sh.full[st]), 0,
-                    s.b * p.rows + static_cast<int>(rank) * kRowsPerPair + C::kQRows * j, 0);
+      const uint32_t st = stage_free();
+      if (!ok) break;
+      if (first) mbar_arrive(smem_u32(&sh.full[st]));   // (nobody waits for it: the stage's phases go on)
+      mbar_arrive_expect_tx(smem_u32(&sh.q_item[j]), C::kQItemBytes);
+      tma_load_3d(smem + st * C::kStageBytes, &maps.q, smem_u32(&sh.q_item[j]), 0,
+                  s.b * p.rows + static_cast<int>(rank) * kRowsPerPair + C::kQRows * j, 0);
+      q_last = i - 1;
+      q_flying = j + 1;
     }
+    if (!ok) break;
     for (int k = s.k0; k < s.k1 && ok; ++k) {
       int blk = block_of(p, s.b, k);
       if (blk < 0) {   // reported; the box lies past the cache, so TMA fills it with zeros
         atomicCAS(p.status, 0, MLA_ERR_DEVICE_BOUNDS);
         blk = static_cast<int>(p.num_blocks);
       }
-      const uint32_t st = stage_for(C::kStageBytes);
+      const uint32_t st = stage_free();
       if (!ok) break;
-      const uint32_t dst = smem + st * C::kStageBytes, bar = smem_u32(&sh.full[st]);
-      const int row = blk * kPageTokens;
-      tma_load_3d_hint(dst, &maps.kv, bar, 0, row, 0, policy);
-      if constexpr (F8) tma_load_2d_hint(dst + 4 * kChunk, &maps.rope, bar, kDimV, row, policy);
+      const uint32_t dst = smem + st * C::kStageBytes;
+      if constexpr (Pair) {
+        if (first) mbar_arrive_expect_tx(smem_u32(&sh.full[st]), 2 * C::kStageBytes);
+        const uint32_t bar = map_to_rank(smem_u32(&sh.full[st]), rank & ~1u);
+        const int row = blk * kPageTokens + static_cast<int>(rank & 1) * static_cast<int>(C::kTokens);
+        pair_load_3d(dst, &maps.kv, bar, 0, row, 0, policy);
+        if constexpr (F8) pair_load_2d(dst + 4 * C::kChunk, &maps.rope, bar, kDimV, row, policy);
+      } else {
+        const uint32_t bar = smem_u32(&sh.full[st]);
+        const int row = blk * kPageTokens;
+        mbar_arrive_expect_tx(bar, C::kStageBytes);
+        tma_load_3d_hint(dst, &maps.kv, bar, 0, row, 0, policy);
+        if constexpr (F8) tma_load_2d_hint(dst + 4 * C::kChunk, &maps.rope, bar, kDimV, row, policy);
+      }
     }
   }
-  const uint32_t flying = i < C::kStages ? i : C::kStages;   // loads still in flight land before the CTA may exit
-  for (uint32_t j = i - flying; j < i; ++j) w_drain(sh.full[j % C::kStages], (j / C::kStages) & 1);
+  // Loads still in flight land before the CTA may exit.  A pair's second CTA sees it by its stages' coming back.
+  const uint32_t flying = i < C::kStages ? i : C::kStages;
+  for (uint32_t j = i - flying; j < i; ++j) {
+    uint64_t& bar = first ? sh.full[j % C::kStages] : sh.empty[j % C::kStages];
+    if (!w_drain(bar, (j / C::kStages) & 1)) break;
+  }
+  for (int j = 0; j < q_flying; ++j) w_drain(sh.q_item[j], q_seg & 1);
 }
 
 // -------------------------------------------------------------------- MMA --
@@ -301,37 +361,72 @@ __device__ __forceinline__ uint32_t elect_lane() {
   return e;
 }
 // An MMA step by the lane that has `lead`, all lanes with the same operands: A in TMEM, B at shared-memory address
-// 16 k_lo, 128-byte swizzle.  The lane is elected once a page, not a step, and a step's address is one 32-bit addition: the
-// issue slots that a step takes are what the epilogue warps leave of an SM's quarter (FP8: 33.0 -> 31.6 us, two query
-// positions: 116.6 -> 112.0; alone beside warps of FMAs, a step every 34 clk where it was 55).
-template <bool F8>
-__device__ __forceinline__ void mma_step(uint32_t d_tmem, uint32_t a_tmem, uint32_t k_lo, uint32_t accumulate, uint32_t lead) {
-  constexpr uint32_t idesc = F8 ? idesc_e4m3_f32(128, 64, 0, 0) : idesc_bf16_f32(128, 64, 0, 0);
+// 16 k_lo, 128-byte swizzle; for a pair, 128 rows of A and half of B's rows in each CTA.  The lane is elected once a
+// page, not a step, and a step's address is one 32-bit addition: the issue slots that a step takes are what the
+// epilogue warps leave of an SM's quarter (FP8: 33.0 -> 31.6 us; alone beside warps of FMAs, a step every 34 clk where
+// it was 55).
+template <bool F8, bool Pair>
+__device__ __forceinline__ void mma_step(uint32_t d_tmem, uint32_t a_tmem, uint32_t k_lo, uint32_t accumulate,
+                                         uint32_t lead) {
+  constexpr int M = Pair ? 256 : 128;
+  constexpr uint32_t idesc = F8 ? idesc_e4m3_f32(M, 64, 0, 0) : idesc_bf16_f32(M, 64, 0, 0);
   constexpr uint32_t k_hi = (1024u >> 4) | (1u << 14) | (2u << 29);   // 8 rows are 1024 bytes; version 1, 128-byte swizzle
-  if constexpr (F8)
+#define MLA_MMA_STEP(GROUP, KIND)                                                                                   \
+  asm volatile(                                                                                                     \
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 k;\n\tmov.b64 k, {%2, %3};\n\tsetp.ne.b32 p, %5, 0;\n\t"                   \
+      "setp.ne.b32 e, %6, 0;\n\t@e tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], [%1], k, %4, p;\n\t}"      \
+      :: "r"(d_tmem), "r"(a_tmem), "r"(k_lo), "r"(k_hi), "r"(idesc), "r"(accumulate), "r"(lead) : "memory")
+  if constexpr (F8 && Pair) MLA_MMA_STEP("2", "f8f6f4");
+  else if constexpr (F8) MLA_MMA_STEP("1", "f8f6f4");
+  else if constexpr (Pair) MLA_MMA_STEP("2", "f16");
+  else MLA_MMA_STEP("1", "f16");
+#undef MLA_MMA_STEP
+}
+// The barrier (of both CTAs of a pair, at the same place in their shared memory) gets an arrival once all MMAs so far
+// are complete.
+template <bool Pair>
+__device__ __forceinline__ void commit_step(uint32_t bar, uint32_t rank) {
+  if constexpr (Pair)
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\t.reg .b64 k;\n\tmov.b64 k, {%2, %3};\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 e, %6, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], k, %4, p;\n\t}"
-        :: "r"(d_tmem), "r"(a_tmem), "r"(k_lo), "r"(k_hi), "r"(idesc), "r"(accumulate), "r"(lead) : "memory");
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}"
+        :: "r"(bar), "h"(static_cast<uint16_t>(3u << rank)) : "memory");
   else
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t.reg .b64 k;\n\tmov.b64 k, {%2, %3};\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 e, %6, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], k, %4, p;\n\t}"
-        :: "r"(d_tmem), "r"(a_tmem), "r"(k_lo), "r"(k_hi), "r"(idesc), "r"(accumulate), "r"(lead) : "memory");
+    mma_commit_warp(bar);
+}
+template <bool Pair>
+__device__ __forceinline__ void weights_tmem_alloc(uint32_t dst_smem) {   // whole warp; a pair's two CTAs together
+  if constexpr (Pair) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(dst_smem), "r"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    tmem_alloc(dst_smem, 512);
+  }
+}
+template <bool Pair>
+__device__ __forceinline__ void weights_tmem_dealloc(uint32_t taddr) {
+  if constexpr (Pair)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(taddr), "r"(512) : "memory");
+  else
+    tmem_dealloc(taddr, 512);
 }
 
-template <bool F8>
-__device__ void w_mma(const WeightsParams& p, WShared& sh, uint32_t smem, uint32_t cl) {
-  using C = WCfg<F8>;
+// (of a pair: in its first CTA)
+template <bool F8, bool Pair>
+__device__ void w_mma(const WeightsParams& p, WShared& sh, uint32_t smem, uint32_t rank, uint32_t cl) {
+  using C = WCfg<F8, Pair>;
   const uint32_t tmem = sh.tmem_base;
   WWalk<C::kSwitchPages> walk(sh);
   WSegment s;
   uint32_t i = 0, T = 0, seg = 0;
   bool ok = true;
   while (ok && walk.next(p, s)) {
-    if (!(ok = w_warp_wait(sh, F8 ? sh.q_read : sh.q_full, seg & 1, p.status, cl))) break;
+    if (!(ok = w_warp_wait(sh, F8 ? sh.q_taken : sh.q_full, seg & 1, p.status, cl))) break;
     for (int j = 0; j < C::kQItems; ++j, ++i)   // the epilogue warps have read the ring's q
-      if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&sh.empty[i % C::kStages]));
+      if ((threadIdx.x & 31) == 0) {
+        mbar_arrive(smem_u32(&sh.empty[i % C::kStages]));
+        if (Pair) mbar_arrive_remote(map_to_rank(smem_u32(&sh.empty[i % C::kStages]), rank + 1));
+      }
     if (F8 && !(ok = w_warp_wait(sh, sh.q_full, seg & 1, p.status, cl))) break;
     ++seg;
     bool ready = false;   // the page's stage and S buffer have been seen free during the page before
@@ -348,13 +443,13 @@ __device__ void w_mma(const WeightsParams& p, WShared& sh, uint32_t smem, uint32
         for (int c = first; c < last; ++c)
 #pragma unroll
           for (int j = 0; j < (F8 && c == 4 ? 2 : 4); ++j) {
-            const uint32_t at = page + (c * kChunk + j * 32) / 16;
+            const uint32_t at = page + (c * C::kChunk + j * 32) / 16;
             if constexpr (F8) {   // chunks of 128 codes, K = 32 a step; the half of q that it lies in holds hi, then lo
               const int step = 4 * c + j, col = 144 * (step / 9) + 8 * (step % 9);
-              mma_step<F8>(d, tmem + kQCol + col, at, (c | j) ? 1u : 0u, lead);
-              mma_step<F8>(d, tmem + kQCol + col + 72, at, 1u, lead);
+              mma_step<F8, Pair>(d, tmem + kQCol + col, at, (c | j) ? 1u : 0u, lead);
+              mma_step<F8, Pair>(d, tmem + kQCol + col + 72, at, 1u, lead);
             } else {
-              mma_step<F8>(d, tmem + kQCol + c * 32 + j * 8, at, (c | j) ? 1u : 0u, lead);
+              mma_step<F8, Pair>(d, tmem + kQCol + c * 32 + j * 8, at, (c | j) ? 1u : 0u, lead);
             }
           }
       };
@@ -366,12 +461,12 @@ __device__ void w_mma(const WeightsParams& p, WShared& sh, uint32_t smem, uint32
               __all_sync(0xffffffffu, mbar_peek(smem_u32(&sh.s_empty[(T + 1) % kSBufs]), (((T + 1) / kSBufs) & 1) ^ 1) &&
                                           mbar_peek(smem_u32(&sh.full[(i + 1) % C::kStages]), ((i + 1) / C::kStages) & 1));
       chunks(std::integral_constant<int, kFirst>(), std::integral_constant<int, kAll>());
-      mma_commit_warp(smem_u32(&sh.empty[st]));
-      mma_commit_warp(smem_u32(&sh.s_full[sb]));
+      commit_step<Pair>(smem_u32(&sh.empty[st]), rank);
+      commit_step<Pair>(smem_u32(&sh.s_full[sb]), rank);
     }
   }
   if (T > 0) {   // no MMA is in flight when the CTA frees its TMEM
-    mma_commit_warp(smem_u32(&sh.drain));
+    commit_step<Pair>(smem_u32(&sh.drain), rank);
     w_drain(sh.drain, 0);
   }
   __syncwarp();
@@ -496,15 +591,28 @@ struct Row {   // of the scores: p = exp2(s scale + c), both as float pairs
   int vis;     // tokens it sees
 };
 
+// Arrival in another CTA that releases nothing beyond this CTA (it says that a slot has been read): a release to
+// the cluster would wait for the warp's reductions at L2, page by page (sums then set the period: 145 us for
+// two query positions over 8192 tokens).
+__device__ __forceinline__ void mbar_arrive_other(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_bar) : "memory");
+}
+
 // Warps 2..9.  Warp quadrant q (TMEM lanes 32 q .. 32 q + 31: the rows), half `half` of the page's columns.
 // All waits are on bounded barriers (no bar.sync), so a warp that gives up leaves no other hanging.
-template <bool F8>
-__device__ void w_epilogue(const WeightsParams& p, WShared& sh, uint32_t smem, int rb, uint32_t cl) {
-  using C = WCfg<F8>;
+template <bool F8, bool Pair>
+__device__ void w_epilogue(const WeightsParams& p, WShared& sh, uint32_t smem, uint32_t rank, uint32_t cl) {
+  using C = WCfg<F8, Pair>;
+  // an arrival for the warp that issues the MMAs: of a pair, in its first CTA.  What it orders is TMEM alone (the
+  // tcgen05 fences beside it), so it releases no further than any arrival.
+  auto tell_mma = [&](uint64_t& bar) {
+    if constexpr (Pair) mbar_arrive_other(map_to_rank(smem_u32(&bar), rank & ~1u));
+    else mbar_arrive(smem_u32(&bar));
+  };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = warp & 3, half = (warp - 2) >> 2;
   const int r = quad * 32 + lane;                    // row of the block == TMEM lane
-  const int g = rb * kRowsPerPair + r;               // row of the request: i * H + h
+  const int g = static_cast<int>(rank) * kRowsPerPair + r;   // row of the request: i * H + h
   const uint32_t lane_base = sh.tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
   const int cb = half * 32;
   // the column whose sum sum_lanes leaves to this lane: 8 n + 2 (lane % 4) + e
@@ -529,7 +637,7 @@ __device__ void w_epilogue(const WeightsParams& p, WShared& sh, uint32_t smem, i
     // Q into TMEM: every MMA of the request before is complete (its last S has been waited for)
     const uint32_t item = i + static_cast<uint32_t>(r / C::kQRows);
     i += C::kQItems + static_cast<uint32_t>(s.k1 - s.k0);
-    if (!w_warp_wait(sh, sh.full[item % C::kStages], (item / C::kStages) & 1, p.status, cl)) return;
+    if (!w_warp_wait(sh, sh.q_item[r / C::kQRows], seg & 1, p.status, cl)) return;
     const int rl = r % C::kQRows;
     const QHalf q{smem + (item % C::kStages) * C::kStageBytes + rl * 128, C::kQRows * 128, 36 * half, rl & 7};
     const uint32_t col = lane_base + kQCol + 144 * half;
@@ -537,7 +645,7 @@ __device__ void w_epilogue(const WeightsParams& p, WShared& sh, uint32_t smem, i
       sh.amax[half][r] = q.store<true>(col);
       tmem_wait_st();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.q_read));
+      if (lane == 0) mbar_arrive(smem_u32(&sh.q_read)), tell_mma(sh.q_taken);
       if (!w_warp_wait(sh, sh.q_read, seg & 1, p.status, cl)) return;
       const float a = sh.amax[0][r], b = sh.amax[1][r];   // the row's two halves agree on its scale:
       // 2^e brings the largest magnitude into (224, 448]; a row with an infinity or a NaN gives NaN
@@ -554,7 +662,7 @@ __device__ void w_epilogue(const WeightsParams& p, WShared& sh, uint32_t smem, i
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&sh.q_full));
+    if (lane == 0) tell_mma(sh.q_full);
     ++seg;
     // the constants of the four rows 8 j + lane / 4 whose scores this lane gets
     Row row[4];
@@ -580,7 +688,7 @@ __device__ void w_epilogue(const WeightsParams& p, WShared& sh, uint32_t smem, i
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.s_empty[sb]));
+      if (lane == 0) tell_mma(sh.s_empty[sb]);
       const int c0 = k * kPageTokens + cb;   // token of the columns' first
       const bool whole = least - c0 >= 32;   // all 32 columns are visible to the four rows
       float total[8];
@@ -617,18 +725,11 @@ __device__ __forceinline__ void st_async_v2(uint32_t cluster_addr, float a, floa
   asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];"
                :: "r"(cluster_addr), "f"(a), "f"(b), "r"(cluster_bar) : "memory");
 }
-// Arrival in another CTA that releases nothing beyond this CTA (it says that a slot has been read): a release to
-// the cluster would wait for the warp's reductions at L2, page by page (sums then set the period: 145 us for
-// two query positions over 8192 tokens).
-__device__ __forceinline__ void mbar_arrive_other(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_bar) : "memory");
-}
-
 // Warp 10: adds the four quadrants' sums of a page up and takes them to the weights, or, in the other CTAs of a
 // cluster, to CTA 0.  Lane l has tokens 2 l and 2 l + 1.
-template <bool F8>
+template <bool F8, bool Pair>
 __device__ void w_sum(const WeightsParams& p, WShared& sh, uint32_t cl, uint32_t rank) {
-  using C = WCfg<F8>;
+  using C = WCfg<F8, Pair>;
   const int lane = threadIdx.x & 31;
   const uint32_t others = cl - 1, slots = cl > 1 ? kRecvRows / others : 1;
   WWalk<C::kSwitchPages> walk(sh);
@@ -677,10 +778,10 @@ __device__ void w_sum(const WeightsParams& p, WShared& sh, uint32_t cl, uint32_t
   // others' bounded waits have ended too, and the cluster's last barrier holds every CTA until then
 }
 
-template <bool F8>
+template <bool F8, bool Pair>
 __global__ void __launch_bounds__(kWThreads, 1)
 mla_attn_weights_kernel(const __grid_constant__ WMaps maps, const __grid_constant__ WeightsParams p) {
-  using C = WCfg<F8>;
+  using C = WCfg<F8, Pair>;
   extern __shared__ __align__(1024) uint8_t dyn_smem[];
   const uint32_t smem = smem_u32(dyn_smem);
   if (smem & 1023u) {   // the swizzled layout needs it (no static shared memory is declared); every CTA alike
@@ -702,14 +803,16 @@ mla_attn_weights_kernel(const __grid_constant__ WMaps maps, const __grid_constan
     }
     for (int j = 0; j < kSBufs; ++j) {
       mbar_init(smem_u32(&sh.s_full[j]), 1);
-      mbar_init(smem_u32(&sh.s_empty[j]), kEpiWarps);
+      mbar_init(smem_u32(&sh.s_empty[j]), C::kEpiArrivals);
     }
     for (int j = 0; j < kPartBufs; ++j) {
       mbar_init(smem_u32(&sh.part_full[j]), kEpiWarps);
       mbar_init(smem_u32(&sh.part_empty[j]), 1);
     }
+    for (int j = 0; j < C::kQItems; ++j) mbar_init(smem_u32(&sh.q_item[j]), 1);
     mbar_init(smem_u32(&sh.q_read), kEpiWarps);
-    mbar_init(smem_u32(&sh.q_full), kEpiWarps);
+    mbar_init(smem_u32(&sh.q_taken), C::kEpiArrivals);
+    mbar_init(smem_u32(&sh.q_full), C::kEpiArrivals);
     mbar_init(smem_u32(&sh.drain), 1);
     for (int j = 0; j < kRecvRows; ++j) {
       mbar_init(smem_u32(&sh.recv_full[j]), 1);
@@ -718,7 +821,7 @@ mla_attn_weights_kernel(const __grid_constant__ WMaps maps, const __grid_constan
     fence_mbar_init();
   }
   __syncwarp();
-  if (warp == 0) tmem_alloc(smem_u32(&sh.tmem_base), 512);
+  if (warp == 0) weights_tmem_alloc<Pair>(smem_u32(&sh.tmem_base));
   tc_fence_before();
   __syncthreads();
   if (cl > 1) cluster_sync();   // every barrier of the cluster is initialised before any remote use
@@ -727,13 +830,13 @@ mla_attn_weights_kernel(const __grid_constant__ WMaps maps, const __grid_constan
   griddep_launch_dependents();
   find_piece<C::kSwitchPages>(p, sh, static_cast<int>(blockIdx.x / cl), static_cast<int>(gridDim.x / cl));
   if (warp == 0) {
-    if ((threadIdx.x & 31) == 0) w_producer<F8>(p, maps, sh, smem, rank, cl);
+    if ((threadIdx.x & 31) == 0) w_producer<F8, Pair>(p, maps, sh, smem, rank, cl);
   } else if (warp == 1) {
-    w_mma<F8>(p, sh, smem, cl);
+    if (!Pair || (rank & 1) == 0) w_mma<F8, Pair>(p, sh, smem, rank, cl);
   } else if (warp < 2 + kEpiWarps) {
-    w_epilogue<F8>(p, sh, smem, static_cast<int>(rank), cl);
+    w_epilogue<F8, Pair>(p, sh, smem, rank, cl);
   } else {
-    w_sum<F8>(p, sh, cl, rank);
+    w_sum<F8, Pair>(p, sh, cl, rank);
   }
   __syncwarp();
   tc_fence_before();
@@ -741,7 +844,7 @@ mla_attn_weights_kernel(const __grid_constant__ WMaps maps, const __grid_constan
   if (cl > 1) cluster_sync();   // no CTA leaves while another may still touch its shared memory
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(sh.tmem_base, 512);
+    weights_tmem_dealloc<Pair>(sh.tmem_base);
   }
 }
 
@@ -755,9 +858,12 @@ WeightsDevice g_dev[kMaxDevices];
 std::mutex g_mutex;
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
-const void* weights_kernel(bool fp8) {
-  return fp8 ? reinterpret_cast<const void*>(mla_attn_weights_kernel<true>)
-             : reinterpret_cast<const void*>(mla_attn_weights_kernel<false>);
+using WeightsKernel = void (*)(WMaps, WeightsParams);
+// An even number of row blocks pairs up.
+bool pairs_up(int cl) { return cl % 2 == 0; }
+WeightsKernel weights_kernel(bool fp8, int cl) {
+  return pairs_up(cl) ? (fp8 ? mla_attn_weights_kernel<true, true> : mla_attn_weights_kernel<false, true>)
+                      : (fp8 ? mla_attn_weights_kernel<true, false> : mla_attn_weights_kernel<false, false>);
 }
 cudaLaunchConfig_t weights_config(bool fp8, int clusters, int cl, cudaStream_t stream, cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t cfg = pdl_config(dim3(static_cast<unsigned>(clusters * cl)), dim3(kWThreads),
@@ -788,9 +894,10 @@ mla_status_t weights_setup(WeightsDevice** out) {
     int sms = 0;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return MLA_ERR_CUDA;
     for (int f = 0; f < 2; ++f) {
-      if (cudaFuncSetAttribute(weights_kernel(f), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(f ? weights_smem<true>() : weights_smem<false>())) != cudaSuccess)
-        return MLA_ERR_CUDA;
+      for (int cl = 1; cl <= 2; ++cl)   // both kernels
+        if (cudaFuncSetAttribute(weights_kernel(f, cl), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(f ? weights_smem<true>() : weights_smem<false>())) != cudaSuccess)
+          return MLA_ERR_CUDA;
       d.clusters[f][1] = sms;
       for (int cl = 2; cl <= kMaxPairsPerCluster; ++cl) {
         cudaLaunchAttribute attr[2];
@@ -798,7 +905,7 @@ mla_status_t weights_setup(WeightsDevice** out) {
         cudaLaunchConfig_t query = cfg;
         query.attrs = attr + 1;
         query.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&d.clusters[f][cl], weights_kernel(f), &query) != cudaSuccess ||
+        if (cudaOccupancyMaxActiveClusters(&d.clusters[f][cl], weights_kernel(f, cl), &query) != cudaSuccess ||
             d.clusters[f][cl] < 1) {
           cudaGetLastError();
           return MLA_ERR_CUDA;
@@ -811,9 +918,9 @@ mla_status_t weights_setup(WeightsDevice** out) {
   return MLA_OK;
 }
 
-template <bool F8>
+template <bool F8, bool Pair>
 bool encode_maps(WMaps* m, const void* kv, int64_t num_blocks, const void* q, int64_t q_rows) {
-  using C = WCfg<F8>;
+  using C = WCfg<F8, Pair>;
   const cuuint32_t es[3] = {1, 1, 1};
   auto encode = [&](CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,
                     const cuuint64_t* strides, const cuuint32_t* box) {
@@ -825,12 +932,12 @@ bool encode_maps(WMaps* m, const void* kv, int64_t num_blocks, const void* q, in
   bool ok;
   if (F8) {
     const cuuint64_t dims[3] = {128, rows, 4}, strides[2] = {kDimQK, 128}, rdims[2] = {kDimQK, rows}, rstrides[1] = {kDimQK};
-    const cuuint32_t box[3] = {128, kPageTokens, 4}, rbox[2] = {128, kPageTokens};
+    const cuuint32_t box[3] = {128, C::kTokens, 4}, rbox[2] = {128, C::kTokens};
     ok = encode(&m->kv, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, kv, dims, strides, box) &&
          encode(&m->rope, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, kv, rdims, rstrides, rbox);
   } else {
     const cuuint64_t dims[3] = {64, rows, 9}, strides[2] = {kDimQK * 2, 128};
-    const cuuint32_t box[3] = {64, kPageTokens, 9};
+    const cuuint32_t box[3] = {64, C::kTokens, 9};
     ok = encode(&m->kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, kv, dims, strides, box);
   }
   const cuuint64_t qdims[3] = {64, static_cast<cuuint64_t>(q_rows), 9}, qstrides[2] = {kDimQK * 2, 128};
@@ -891,17 +998,15 @@ mla_status_t weights_impl(const mla_bf16_t* q, const float* lse, const void* kv_
   WMaps maps = {};
   const int cl = (p.rows + kRowsPerPair - 1) / kRowsPerPair;
   const int64_t q_rows = static_cast<int64_t>(B) * p.rows;
-  if (!(fp8 ? encode_maps<true>(&maps, kv_cache, num_blocks, q, q_rows)
-            : encode_maps<false>(&maps, kv_cache, num_blocks, q, q_rows)))
-    return MLA_ERR_CUDA;
+  const auto encode = pairs_up(cl) ? (fp8 ? encode_maps<true, true> : encode_maps<false, true>)
+                                   : (fp8 ? encode_maps<true, false> : encode_maps<false, false>);
+  if (!encode(&maps, kv_cache, num_blocks, q, q_rows)) return MLA_ERR_CUDA;
   // no more clusters than pages there can be
   const int64_t most = static_cast<int64_t>(B) * ((p.slots + kPageTokens - 1) / kPageTokens);
   const int clusters = static_cast<int>(most < d->clusters[fp8][cl] ? most : d->clusters[fp8][cl]);
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = weights_config(fp8, clusters, cl, reinterpret_cast<cudaStream_t>(stream), attr);
-  const cudaError_t e = fp8 ? cudaLaunchKernelEx(&cfg, mla_attn_weights_kernel<true>, maps, p)
-                            : cudaLaunchKernelEx(&cfg, mla_attn_weights_kernel<false>, maps, p);
-  return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, weights_kernel(fp8, cl), maps, p) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 }  // namespace

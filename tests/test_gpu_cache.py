@@ -724,3 +724,13 @@ def test_outputs_made_for_a_given_stream_are_that_stream_s_memory():
     side.synchronize()
     assert torch.equal(out, want)
     assert mla.get_device_status() == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("B,s_q,longest", [(300, 2, 90), (150, 4, 200), (220, 3, 90)])
+def test_attn_weights_many_short_requests_of_several_row_blocks(fp8, B, s_q, longest):
+    """Requests of a page or two, one after the other on every cluster of two, three and four CTAs."""
+    w = W.Workload("weights_blocks", B=B, s_q=s_q, H=128, ragged_max=longest, causal=True, kv_fp8=fp8)
+    g = torch.Generator().manual_seed(B)
+    inp = _weights_inputs(w, seed=9, seqlens=torch.randint(0, longest, (B,), generator=g, dtype=torch.int32))
+    _check_weights(inp, _run_weights(inp))
