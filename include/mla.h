@@ -426,7 +426,8 @@ mla_status_t mla_attn_weights_fp8(const mla_bf16_t* q, const float* lse, const u
  *  arrival_out    int32 [B, width] or NULL: the numbers moved along; e + (j - m) for j >= m, the
  *                 numbers of the tokens that mla_cache_append will put there
  *  width          >= min(budget, 64 max_blocks, weights_stride)
- * kept, weights_out and arrival_out must overlap neither one another nor weights or arrival.
+ * What is written (kept, weights_out, arrival_out, new_seqlens) overlaps neither one another nor what is
+ * read (weights, arrival, block_table, seqlens but where new_seqlens is it): MLA_ERR_INVALID_ARG.
  * At most 262144 slots a request: min(64 max_blocks, weights_stride) beyond that is MLA_ERR_UNSUPPORTED.  A request whose length
  * is out of range is reported as MLA_ERR_DEVICE_BOUNDS and treated as empty; a row whose page is
  * out of range is reported and not copied.  Two kernels on `stream`.  Async on stream. */

@@ -363,6 +363,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_evict_select_kernel(const 
     for (int r = 0; r < cl; ++r)
       newest = max(newest, cl > 1 ? static_cast<int>(ld_cluster_u32(reinterpret_cast<uint32_t*>(&sh.newest), r)) : sh.newest);
     e = static_cast<int64_t>(newest) + 1;
+    cp_async_wait_all();   // (where every token stays, too: nothing is on its way when the CTA leaves)
   }
   uint32_t cut = 0, ties = 0;   // keep key > cut, and the first `ties` slots with key == cut
   uint32_t tie_first = 0;       // ties in the CTAs before this one
@@ -371,7 +372,6 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_evict_select_kernel(const 
     auto key = [&](int a, float weight) {
       return (a < p.sink || a >= e - p.recent) ? 0xffffffffu : weight_order(weight);
     };
-    cp_async_wait_all();
 #pragma unroll 4
     for (int i = step * tid; i < count; i += step * kSelThreads) {
       if (step == 4 && i + 4 <= count) {
@@ -703,18 +703,18 @@ mla_status_t evict_impl(void* kv_cache, bool fp8, int64_t num_blocks, const int3
   int64_t slots = static_cast<int64_t>(max_blocks) * kPageTokens;
   slots = slots < weights_stride ? slots : weights_stride;
   if (width < (budget < slots ? budget : slots)) return MLA_ERR_INVALID_ARG;
-  // what is written may overlap neither the rows that are read nor one another
-  const uint64_t out_bytes = static_cast<uint64_t>(B) * width * 4;
-  const struct { const void* at; uint64_t bytes; } span[] = {
-      {kept, out_bytes}, {weights_out, out_bytes}, {arrival_out, out_bytes},
-      {weights, ((static_cast<uint64_t>(B) - 1) * weights_stride + slots) * 4},
-      {arrival, ((static_cast<uint64_t>(B) - 1) * arrival_stride + slots) * 4}};
-  for (int i = 0; i < 3; ++i)
-    for (int j = i + 1; j < 5; ++j)
-      if (span[i].at && span[j].at && overlap(span[i].at, span[i].bytes, span[j].at, span[j].bytes))
-        return MLA_ERR_INVALID_ARG;
   if (slots > kEvictMaxSlots || num_blocks * kPageTokens > (int64_t(1) << 31) - kPageTokens || B > kScheduleMaxB)
     return MLA_ERR_UNSUPPORTED;
+  // what is written may overlap neither what is read nor one another (new_seqlens may be seqlens)
+  const uint64_t out_bytes = static_cast<uint64_t>(B) * width * 4, rows = static_cast<uint64_t>(B) - 1;
+  const struct { const void* at; uint64_t bytes; } span[] = {
+      {kept, out_bytes}, {weights_out, out_bytes}, {arrival_out, out_bytes}, {new_seqlens, (rows + 1) * 4},
+      {new_seqlens == seqlens ? nullptr : seqlens, (rows + 1) * 4}, {block_table, (rows + 1) * max_blocks * 4},
+      {weights, (rows * weights_stride + slots) * 4}, {arrival, (rows * arrival_stride + slots) * 4}};
+  for (int i = 0; i < 4; ++i)
+    for (int j = i + 1; j < 8; ++j)
+      if (span[i].at && span[j].at && overlap(span[i].at, span[i].bytes, span[j].at, span[j].bytes))
+        return MLA_ERR_INVALID_ARG;
   if (arrival && arrival_stride < slots) slots = arrival_stride;
   EvictParams p = {};
   p.kv = kv_cache;

@@ -123,3 +123,21 @@ def test_more_rows_than_row_numbers_count_are_refused(mla):
     assert L.mla_rope_axes(A, 128, 64, far, 128, 64, 2 * far, n, _sections(32), 1, 0, 10000.0, 0, n, 2, None) == 2
     assert L.mla_cache_append(A, 576, 2 * far, 576, far, 4, 3 * far, 2, 4 * far, 5 * far, n, 3, 6 * far, n,
                               _sections(32), 1, 0, 10000.0, None) == 2
+
+
+def test_evict_s_lengths_overlap_nothing_but_the_lengths_they_replace(mla):
+    L = mla.lib()
+    far = 1 << 40   # apart from one another
+    table, lens, weights, arrival, new, kept, w_out, a_out = ((i + 1) * far for i in range(8))
+    base = [A, 4, table, 2, lens, 3, weights, 128, arrival, 128, 100, 4, 16, new, kept, w_out, a_out, 100, None]
+    for fp8 in (False, True):
+        call = L.mla_evict_fp8 if fp8 else L.mla_evict
+        for at in (lens + 4, lens - 8, table, table + 20, weights + 4 * 383, arrival, kept, kept - 8, w_out + 1196, a_out):
+            bad = list(base)
+            bad[13] = at
+            assert call(*bad) == 1, hex(at)
+        for i in (14, 15, 16):      # an output over the lengths or the table
+            for at in (lens, table - 1196):
+                bad = list(base)
+                bad[i] = at
+                assert call(*bad) == 1, (i, hex(at))
