@@ -43,7 +43,7 @@ struct WeightsParams {
 //     FP8, 4096 tokens                        31-32 us  5.2 TB/s, 0.77: the MMAs (q is two E4M3 terms, so bf16's
 //                                                       MMA time for half the bytes; 1290 clk a page, 1152 of
 //                                                       them the tensor pipe's), 7 us of start and end
-//     bf16, two query positions, 8192 tokens  99-103 us  6.2 TB/s, 0.92: HBM and the MMAs (81.8 us at the pipe's rate)
+//     bf16, two query positions, 8192 tokens  99-101 us  6.3 TB/s, 0.93: HBM and the MMAs (81.8 us at the pipe's rate)
 // Called for seconds on end, the last two run into the power limit (1.35 kW): 36 us at 1.70 GHz and 115 us at 1.50 GHz.
 //  * Rows on the TMEM lanes, tokens on the columns: Q is loaded once per request, and the ring has the
 //    whole of shared memory for pages (221 KiB: what is in flight covers HBM latency).  Q comes through the ring
@@ -91,10 +91,10 @@ struct WCfg {
   static constexpr int kQRows = 128 / kQItems;
   static constexpr uint32_t kEpiArrivals = kEpiWarps * (Pair ? 2 : 1);   // where a pair's epilogue warps all arrive
   static constexpr uint32_t kQItemBytes = static_cast<uint32_t>(kQRows) * kDimQK * 2;
-  // what a switch of requests costs (Q's load and its way into TMEM), in pages: the split charges it.  A pair's pages
-  // take less time (two query positions, 64 requests of up to 8192 tokens: 66.4 us with 2, 64.1 with 6, 62.0 with 8; 128
-  // of up to 400: 21.6, 22.6 and 23.5 with 4, 6 and 8).
-  static constexpr int kSwitchPages = Pair ? (F8 ? 10 : 6) : F8 ? 5 : 2;
+  // what a switch of requests costs (Q's load and its way into TMEM), in pages: the split charges it (more
+  // changes little: two query positions over 64 requests of up to 8192 tokens 57.9 us with 2, 56.8 with 4, 57.8 with 8;
+  // over 128 of up to 400 16.3, 17.1 and 17.5)
+  static constexpr int kSwitchPages = F8 ? 5 : 2;
   static_assert(kQRows * 128 % 1024 == 0 && kStageBytes % 1024 == 0, "swizzled rows start where the swizzle does");
   static constexpr uint32_t kOffShared = kStages * kStageBytes;
   static_assert(kQItemBytes <= kStageBytes && kQItems <= kStages, "a row block's q is resident at once");
@@ -165,6 +165,13 @@ __device__ __noinline__ bool w_drain(uint64_t& bar, uint32_t parity) {   // igno
   while (!mbar_test(a, parity))
     if (global_timer_ns() - t0 > kTimeoutNs) return false;
   return true;
+}
+
+// Arrival in another CTA that releases nothing beyond this CTA: it says that something has been read.  A release to
+// the cluster would wait for what the thread or its warp has on its way to L2 (over a microsecond: a page's sums
+// set the period with it, 145 us for two query positions over 8192 tokens; a request's q came back 5 us late).
+__device__ __forceinline__ void mbar_arrive_other(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_bar) : "memory");
 }
 
 // --------------------------------------------------------------- the walk --
@@ -422,11 +429,13 @@ __device__ void w_mma(const WeightsParams& p, WShared& sh, uint32_t smem, uint32
   bool ok = true;
   while (ok && walk.next(p, s)) {
     if (!(ok = w_warp_wait(sh, F8 ? sh.q_taken : sh.q_full, seg & 1, p.status, cl))) break;
-    for (int j = 0; j < C::kQItems; ++j, ++i)   // the epilogue warps have read the ring's q
-      if ((threadIdx.x & 31) == 0) {
-        mbar_arrive(smem_u32(&sh.empty[i % C::kStages]));
-        if (Pair) mbar_arrive_remote(map_to_rank(smem_u32(&sh.empty[i % C::kStages]), rank + 1));
-      }
+    const uint32_t lane = threadIdx.x & 31;   // the epilogue warps have read the ring's q: an item a lane
+    if (lane < C::kQItems) {
+      const uint32_t bar = smem_u32(&sh.empty[(i + lane) % C::kStages]);
+      mbar_arrive(bar);
+      if (Pair) mbar_arrive_other(map_to_rank(bar, rank + 1));
+    }
+    i += C::kQItems;
     if (F8 && !(ok = w_warp_wait(sh, sh.q_full, seg & 1, p.status, cl))) break;
     ++seg;
     bool ready = false;   // the page's stage and S buffer have been seen free during the page before
@@ -590,13 +599,6 @@ struct Row {   // of the scores: p = exp2(s scale + c), both as float pairs
   float c_hi, c_lo, scale_hi, scale_lo;
   int vis;     // tokens it sees
 };
-
-// Arrival in another CTA that releases nothing beyond this CTA (it says that a slot has been read): a release to
-// the cluster would wait for the warp's reductions at L2, page by page (sums then set the period: 145 us for
-// two query positions over 8192 tokens).
-__device__ __forceinline__ void mbar_arrive_other(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_bar) : "memory");
-}
 
 // Warps 2..9.  Warp quadrant q (TMEM lanes 32 q .. 32 q + 31: the rows), half `half` of the page's columns.
 // All waits are on bounded barriers (no bar.sync), so a warp that gives up leaves no other hanging.
