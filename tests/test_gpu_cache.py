@@ -734,3 +734,37 @@ def test_attn_weights_many_short_requests_of_several_row_blocks(fp8, B, s_q, lon
     g = torch.Generator().manual_seed(B)
     inp = _weights_inputs(w, seed=9, seqlens=torch.randint(0, longest, (B,), generator=g, dtype=torch.int32))
     _check_weights(inp, _run_weights(inp))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("s_q", [2, 3, 4])
+def test_attn_weights_of_several_row_blocks_bad_pages_and_a_replayed_call(fp8, s_q):
+    import mla_absorbed_decode_gb300 as mla
+    w = W.Workload("weights_blocks_bad", B=4, s_q=s_q, H=128, fixed_seqlens=(100, 130, 70, 64), kv_fp8=fp8)
+    inp = _weights_inputs(w, seed=17)
+    good = _run_weights(inp)
+    lens, table = inp["seqlens"].clone(), inp["block_table"].clone()
+    lens[0], lens[2] = 193, -3
+    table[1, 1] = -1
+    dev = {k: inp[k].cuda() for k in ("q", "lse", "kv_cache")}
+    scale = (inp["kv_scale"],) if fp8 else ()
+    call = mla.attn_weights_fp8 if fp8 else mla.attn_weights
+    got = inp["before"].cuda()
+    call(dev["q"], dev["lse"], dev["kv_cache"], *scale, table.cuda(), lens.cuda(), inp["softmax_scale"], False, got)
+    assert mla.get_device_status() == 6
+    got = got.cpu()
+    for b in (0, 2):
+        assert torch.equal(got[b], inp["before"][b])
+    assert torch.equal(got[3], good[3])
+    assert torch.equal(got[1, :64], good[1, :64]) and torch.equal(got[1, 64:128], inp["before"][1, 64:128])
+    assert torch.equal(got[1, 128:], good[1, 128:])
+    # recorded once, replayed from the same weights
+    lens, table, out = inp["seqlens"].cuda(), inp["block_table"].cuda(), inp["before"].cuda()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(dev["q"], dev["lse"], dev["kv_cache"], *scale, table, lens, inp["softmax_scale"], False, out)
+    for _ in range(3):
+        out.copy_(inp["before"])
+        graph.replay()
+        assert torch.equal(out.cpu(), good)
+    assert mla.get_device_status() == 0
