@@ -380,6 +380,7 @@ mla_status_t mla_cache_append_fp8(const mla_bf16_t* c, int64_t c_row_stride, con
  *                      for every t < seqlens[b], over the query positions i that see t
  * with q and lse of an mla_decode over the same cache, table, lengths, scale and causal_s_q.
  *  lse            [B, s_q, H] fp32; a row with lse = -inf gave no weight and adds nothing
+ *                 (nor do finite scores of a row with lse = +inf, nor a score of -inf: exp(-inf) = 0)
  *  weights        fp32 device, 4-byte aligned, weights_stride elements between requests
  *                 (>= every seqlens[b]); elements from seqlens[b] on are neither read nor written
  * softmax_scale (times kv_scale) times log2(e) has to be a normal float32.  Scores,

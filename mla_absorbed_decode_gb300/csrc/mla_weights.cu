@@ -7,6 +7,7 @@
 #include <cudaTypedefs.h>
 #include <stdint.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstddef>
 #include <mutex>
@@ -29,7 +30,7 @@ struct WeightsParams {
   const int32_t* seqlens;
   int B, s_q, H, rows, causal;
   int slots;                 // largest length: min(64 max_blocks, weights_stride)
-  float scale_hi, scale_lo;  // softmax_scale * log2(e) (times kv_scale) as a float pair
+  float scale_hi, scale_lo;  // softmax_scale * log2(e) (times kv_scale) as a float pair, both > 0
   float* weights;
   int64_t weights_stride;
   int* status;
@@ -633,7 +634,7 @@ __device__ void w_epilogue(const WeightsParams& p, WShared& sh, uint32_t smem, u
         // -lse * log2(e) as a float pair, so that the exponent's rounding is relative to itself
         constexpr float kL2eHi = 1.4426950216293335f, kL2eLo = 1.9259629911266175e-8f;
         c_hi = -lse * kL2eHi;
-        if (isfinite(lse)) c_lo = fmaf(-lse, kL2eLo, fmaf(-lse, kL2eHi, -c_hi));
+        if (isfinite(c_hi)) c_lo = fmaf(-lse, kL2eLo, fmaf(-lse, kL2eHi, -c_hi));   // (lse may be finite and c_hi not)
       }
     }
     // Q into TMEM: every MMA of the request before is complete (its last S has been waited for)
@@ -987,9 +988,14 @@ mla_status_t weights_impl(const mla_bf16_t* q, const float* lse, const void* kv_
   // heads, whose larger scores all come out short.
   const double shortfall = (fp8 ? 2.8 : 8.7) * 0x1p-24;
   const double scale = static_cast<double>(softmax_scale) * 1.4426950408889634074 * (fp8 ? kv_scale : 1.0) * (1.0 + shortfall);
+  // Both floats of the pair are positive: a score of -inf times either is -inf, and its exponential 0 (with a negative
+  // or zero low part the sum of the two products would be NaN).
   p.scale_hi = static_cast<float>(scale);
-  p.scale_lo = static_cast<float>(scale - static_cast<double>(p.scale_hi));
   if (!std::isnormal(p.scale_hi)) return MLA_ERR_INVALID_ARG;
+  if (static_cast<double>(p.scale_hi) > scale) p.scale_hi = std::nextafterf(p.scale_hi, 0.f);
+  p.scale_lo = static_cast<float>(scale - static_cast<double>(p.scale_hi));
+  const float least = p.scale_hi * 0x1p-48f;   // where the residue is (nearly) 0: far below what the pair resolves
+  p.scale_lo = std::fmax(p.scale_lo, std::fmax(least, FLT_TRUE_MIN));
   p.weights = weights;
   p.weights_stride = weights_stride;
   p.status = device_status_word();
