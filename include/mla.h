@@ -385,8 +385,10 @@ mla_status_t mla_cache_append_fp8(const mla_bf16_t* c, int64_t c_row_stride, con
  *                 (>= every seqlens[b]); elements from seqlens[b] on are neither read nor written
  * softmax_scale (times kv_scale) times log2(e) has to be a normal float32.  Scores,
  * exponentials and sums are in fp32; every weights[b, t] is summed in a fixed order and added to
- * once, so that equal inputs give equal bits (a sum below 2^-126 may become 0).  The rest as for
- * mla_decode (no metadata, no workspace).
+ * once, so that equal inputs give equal bits (a sum below 2^-126 may become 0).  A score's exact
+ * products are added up on the tensor cores, as mla_decode's are, which truncates: a score is off by at
+ * most 40 * 2^-23 of softmax_scale * sum over d of |q_d kv_td|, and by nothing where it is one product.
+ * The rest as for mla_decode (no metadata, no workspace).
  * A request with seqlens[b] outside [0, min(64 max_blocks, weights_stride)] or a page outside
  * [0, num_blocks) is reported as MLA_ERR_DEVICE_BOUNDS (the tokens concerned add nothing).
  * Async on stream. */

@@ -981,13 +981,10 @@ mla_status_t weights_impl(const mla_bf16_t* q, const float* lse, const void* kv_
   slots = slots < weights_stride ? slots : weights_stride;
   constexpr int64_t kMostSlots = INT32_MAX / kPageTokens * kPageTokens;   // token numbers are ints
   p.slots = static_cast<int>(slots < kMostSlots ? slots : kMostSlots);
-  // The MMAs add each step's products to the accumulator by truncation towards zero, so that over the 36 steps a
-  // score comes out short: measured, by 8.7 * 2^-24 of itself on average for a bf16 cache and 2.8 * 2^-24 for an
-  // FP8 one (N(0, 1) q and k, 131072 scores; 7.3 to 8.7 with k scaled by 0.1 to 2.8), 0.5e-6 beside a spread of the
-  // same size.  The scale makes up for it, which leaves the spread: the shortfall does not average out over the
-  // heads, whose larger scores all come out short.
-  const double shortfall = (fp8 ? 2.8 : 8.7) * 0x1p-24;
-  const double scale = static_cast<double>(softmax_scale) * 1.4426950408889634074 * (fp8 ? kv_scale : 1.0) * (1.0 + shortfall);
+  // The scale as it was given: the tensor pipe truncates as it adds up a score's 36 steps (18 over FP8, twice), and what
+  // that leaves out depends on the partial sums (nothing, for a score of one product), so no factor makes up for it.
+  // The decode's scores, and with them lse, are formed the same way.
+  const double scale = static_cast<double>(softmax_scale) * 1.4426950408889634074 * (fp8 ? kv_scale : 1.0);
   // Both floats of the pair are positive: a score of -inf times either is -inf, and its exponential 0 (with a negative
   // or zero low part the sum of the two products would be NaN).
   p.scale_hi = static_cast<float>(scale);
