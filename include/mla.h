@@ -475,8 +475,8 @@ mla_status_t mla_decode_noalloc(const mla_bf16_t* q, const mla_bf16_t* kv_cache,
  * kernels set (MLA_OK, MLA_ERR_TIMEOUT or MLA_ERR_DEVICE_BOUNDS). */
 mla_status_t mla_get_device_status(mla_stream_t stream);
 
-/* Test hook: when nonzero, the next mla_decode launch withholds the first KV
- * page load of every part, so that each barrier wait on it runs out of time
+/* Test hook: when nonzero, the next mla_decode or mla_attn_weights launch (over either
+ * cache type) withholds the first KV page load of every part (or CTA), so that each barrier wait on it runs out of time
  * (0.5 s) and the call reports MLA_ERR_TIMEOUT through
  * mla_get_device_status.  No memory access is made out of bounds and nothing
  * traps; the flag clears itself after one launch. */

@@ -159,6 +159,12 @@ size_t max_splits(int B, int num_parts) { return static_cast<size_t>(B) + static
 
 }  // namespace
 
+int take_withheld_load() {
+  const int withheld = g_withhold_first_load;
+  g_withhold_first_load = 0;
+  return withheld;
+}
+
 int* device_status_word() {
   DeviceState* d = nullptr;
   if (current_device(&d) != MLA_OK) return nullptr;
@@ -296,8 +302,7 @@ mla_status_t decode_impl(const void* q, const void* kv_cache, int64_t num_blocks
   p.out = reinterpret_cast<__nv_bfloat16*>(out);
   p.lse = lse;
   p.status = d->status;
-  p.withhold_first_load = g_withhold_first_load;
-  g_withhold_first_load = 0;
+  p.withhold_first_load = take_withheld_load();
   p.kv_fp8 = kv_fp8 ? 1 : 0;
   p.kv_scale = kv_fp8 ? kv_scale : 1.f;
 

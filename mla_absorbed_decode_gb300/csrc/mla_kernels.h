@@ -86,6 +86,8 @@ bool encode_kv_maps_fp8(PFN_cuTensorMapEncodeTiled_v12000 encode, KvMaps* maps, 
 // Device address of the kernels' status word on the current device (set-up on
 // first use); nullptr on error.
 int* device_status_word();
+// The test hook of mla_debug_withhold_first_load, for one launch: read and cleared.
+int take_withheld_load();
 
 // Launch configuration shared by every kernel of the library: programmatic stream
 // serialisation, so that a kernel's set-up overlaps the tail of the kernel before it

@@ -34,6 +34,7 @@ struct WeightsParams {
   float* weights;
   int64_t weights_stride;
   int* status;
+  int withhold;              // test hook: every CTA's first page is not loaded
 };
 
 // A CTA holds one 128-row block of a request's queries (heads x query positions) in TMEM and streams
@@ -113,6 +114,7 @@ struct WShared {
   uint64_t credit[kRecvRows];                  // the other CTAs: CTA 0 has taken what was in the slot
   uint32_t tmem_base;
   volatile int abort;
+  uint32_t items, units;                       // what the MMA warp has given back and filled, when it ends
   int64_t scan[kWThreads / 32 + 1];
   int64_t offset, count;                       // this part's piece: from `offset` positions into request b0 on
   int b0;
@@ -160,12 +162,12 @@ __device__ __forceinline__ bool w_wait(WShared& sh, uint64_t& bar, uint32_t pari
 __device__ __forceinline__ bool w_warp_wait(WShared& sh, uint64_t& bar, uint32_t parity, int* status, uint32_t cl) {
   return __all_sync(0xffffffffu, w_wait(sh, bar, parity, status, cl));
 }
-__device__ __noinline__ bool w_drain(uint64_t& bar, uint32_t parity) {   // ignores the abort flag
+// Before a CTA leaves: waits until the phase is complete or the time is `until` (one limit for all the phases that a role
+// drains, each looked at once at least); ignores the abort flag.
+__device__ __noinline__ void w_drain(uint64_t& bar, uint32_t parity, uint64_t until) {
   const uint32_t a = smem_u32(&bar);
-  const uint64_t t0 = global_timer_ns();
   while (!mbar_test(a, parity))
-    if (global_timer_ns() - t0 > kTimeoutNs) return false;
-  return true;
+    if (global_timer_ns() > until) return;
 }
 
 // Arrival in another CTA that releases nothing beyond this CTA: it says that something has been read.  A release to
@@ -327,6 +329,7 @@ __device__ void w_producer(const WeightsParams& p, const WMaps& maps, WShared& s
       }
       const uint32_t st = stage_free();
       if (!ok) break;
+      if (p.withhold && seg == 0 && k == s.k0) continue;   // test hook: this page never arrives
       const uint32_t dst = smem + st * C::kStageBytes;
       if constexpr (Pair) {
         if (first) mbar_arrive_expect_tx(smem_u32(&sh.full[st]), 2 * C::kStageBytes);
@@ -343,13 +346,14 @@ __device__ void w_producer(const WeightsParams& p, const WMaps& maps, WShared& s
       }
     }
   }
-  // Loads still in flight land before the CTA may exit.  A pair's second CTA sees it by its stages' coming back.
+  // Loads still in flight land before the CTA may exit (a pair's second CTA sees it by its stages' coming back), and so do
+  // the arrivals that give the stages back.
+  const uint64_t until = global_timer_ns() + kTimeoutNs;
   const uint32_t flying = i < C::kStages ? i : C::kStages;
-  for (uint32_t j = i - flying; j < i; ++j) {
-    uint64_t& bar = first ? sh.full[j % C::kStages] : sh.empty[j % C::kStages];
-    if (!w_drain(bar, (j / C::kStages) & 1)) break;
-  }
-  for (int j = 0; j < q_flying; ++j) w_drain(sh.q_item[j], q_seg & 1);
+  if (first)
+    for (uint32_t j = i - flying; j < i; ++j) w_drain(sh.full[j % C::kStages], (j / C::kStages) & 1, until);
+  for (int j = 0; j < q_flying; ++j) w_drain(sh.q_item[j], q_seg & 1, until);
+  for (uint32_t j = i - flying; j < i; ++j) w_drain(sh.empty[j % C::kStages], (j / C::kStages) & 1, until);
 }
 
 // -------------------------------------------------------------------- MMA --
@@ -390,15 +394,15 @@ __device__ __forceinline__ void mma_step(uint32_t d_tmem, uint32_t a_tmem, uint3
   else MLA_MMA_STEP("1", "f16");
 #undef MLA_MMA_STEP
 }
-// The barrier (of both CTAs of a pair, at the same place in their shared memory) gets an arrival once all MMAs so far
-// are complete.
+// The barrier (of a pair: in the cluster's CTAs of `mask`, at the same place in their shared memory) gets an arrival once
+// all MMAs so far are complete.  Somebody in each of those CTAs has to wait for it before the CTA may leave.
 template <bool Pair>
-__device__ __forceinline__ void commit_step(uint32_t bar, uint32_t rank) {
+__device__ __forceinline__ void commit_step(uint32_t bar, uint32_t mask) {
   if constexpr (Pair)
     asm volatile(
         "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
         "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}"
-        :: "r"(bar), "h"(static_cast<uint16_t>(3u << rank)) : "memory");
+        :: "r"(bar), "h"(static_cast<uint16_t>(mask)) : "memory");
   else
     mma_commit_warp(bar);
 }
@@ -471,15 +475,36 @@ __device__ void w_mma(const WeightsParams& p, WShared& sh, uint32_t smem, uint32
               __all_sync(0xffffffffu, mbar_peek(smem_u32(&sh.s_empty[(T + 1) % kSBufs]), (((T + 1) / kSBufs) & 1) ^ 1) &&
                                           mbar_peek(smem_u32(&sh.full[(i + 1) % C::kStages]), ((i + 1) / C::kStages) & 1));
       chunks(std::integral_constant<int, kFirst>(), std::integral_constant<int, kAll>());
-      commit_step<Pair>(smem_u32(&sh.empty[st]), rank);
-      commit_step<Pair>(smem_u32(&sh.s_full[sb]), rank);
+      commit_step<Pair>(smem_u32(&sh.empty[st]), 3u << rank);   // waited for by the producers, at the latest when they end
+      commit_step<Pair>(smem_u32(&sh.s_full[sb]), 3u << rank);  // waited for by the epilogue warps
     }
   }
-  if (T > 0) {   // no MMA is in flight when the CTA frees its TMEM
-    commit_step<Pair>(smem_u32(&sh.drain), rank);
-    w_drain(sh.drain, 0);
+  if (T > 0) {   // no MMA is in flight when the CTAs free their TMEM: said to this CTA alone, which waits for it
+    commit_step<Pair>(smem_u32(&sh.drain), 1u << rank);
+    w_drain(sh.drain, 0, global_timer_ns() + kTimeoutNs);
+  }
+  if (elect_lane()) {   // for w_settle, across the cluster's last barrier
+    sh.items = i, sh.units = T;
+    if (Pair) {
+      st_cluster_u32(map_to_rank(smem_u32(&sh.items), rank + 1), i);
+      st_cluster_u32(map_to_rank(smem_u32(&sh.units), rank + 1), T);
+    }
   }
   __syncwarp();
+}
+
+// Where a wait has given up, the roles no longer wait for one another: after the cluster's last barrier, the commits'
+// arrivals on their way to this CTA land (their MMAs are complete), and the other CTAs' sums, for which there is no
+// barrier that would complete, get the time that a store in a cluster takes many times over.
+template <bool F8, bool Pair>
+__device__ __noinline__ void w_settle(WShared& sh) {
+  using C = WCfg<F8, Pair>;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t j = sh.items - min(sh.items, static_cast<uint32_t>(C::kStages)); j < sh.items; ++j)
+    w_drain(sh.empty[j % C::kStages], (j / C::kStages) & 1, t0 + kTimeoutNs);
+  for (uint32_t j = sh.units - min(sh.units, static_cast<uint32_t>(kSBufs)); j < sh.units; ++j)
+    w_drain(sh.s_full[j % kSBufs], (j / kSBufs) & 1, t0 + kTimeoutNs);
+  while (global_timer_ns() - t0 < 100 * 1000) {}
 }
 
 // --------------------------------------------------------------- epilogue --
@@ -777,8 +802,8 @@ __device__ void w_sum(const WeightsParams& p, WShared& sh, uint32_t cl, uint32_t
       if (page && t + 1 < s.n) atomicAdd(w + 1, sum.y);
     }
   }
-  // sums on their way to CTA 0 land before it may leave: it has waited for all of them above; where it gave up, the
-  // others' bounded waits have ended too, and the cluster's last barrier holds every CTA until then
+  // sums on their way to CTA 0 land before it may leave: it has waited for all of them above; where it gave up, w_settle
+  // waits
 }
 
 template <bool F8, bool Pair>
@@ -800,6 +825,7 @@ mla_attn_weights_kernel(const __grid_constant__ WMaps maps, const __grid_constan
     prefetch_tensormap(&maps.q);
     if (F8) prefetch_tensormap(&maps.rope);
     sh.abort = 0;
+    sh.items = sh.units = 0;
     for (int j = 0; j < C::kStages; ++j) {
       mbar_init(smem_u32(&sh.full[j]), 1);
       mbar_init(smem_u32(&sh.empty[j]), 1);
@@ -849,6 +875,7 @@ mla_attn_weights_kernel(const __grid_constant__ WMaps maps, const __grid_constan
     tc_fence_after();
     weights_tmem_dealloc<Pair>(sh.tmem_base);
   }
+  if (threadIdx.x == 32 && sh.abort) w_settle<F8, Pair>(sh);
 }
 
 // ------------------------------------------------------------------- host --
@@ -1000,6 +1027,7 @@ mla_status_t weights_impl(const mla_bf16_t* q, const float* lse, const void* kv_
   if (!p.status) return MLA_ERR_CUDA;
   const mla_status_t st = weights_setup(&d);
   if (st != MLA_OK) return st;
+  p.withhold = take_withheld_load();
   WMaps maps = {};
   const int cl = (p.rows + kRowsPerPair - 1) / kRowsPerPair;
   const int64_t q_rows = static_cast<int64_t>(B) * p.rows;

@@ -101,3 +101,62 @@ def test_attn_weights_scores_of_one_product(fp8, n, H):
     u = 2.0 ** -24
     room = (p * (3 * u * np.abs(arg) + 2.0 ** -22 + H * u)).sum(axis=0)
     assert np.all(np.abs(got - p.sum(axis=0)) <= room + 2.0 ** -126 * H), float((np.abs(got - p.sum(axis=0)) / p.sum(axis=0)).max())
+
+
+# ------------------------------------------------------------- weights: a CTA leaves nothing behind --
+def _call(inp, dev, out):
+    import mla_absorbed_decode_gb300 as mla
+    args = (dev["block_table"], dev["seqlens"], inp["softmax_scale"], inp["causal"], out)
+    if "kv_scale" in inp:
+        mla.attn_weights_fp8(dev["q"], dev["lse"], dev["kv_cache"], inp["kv_scale"], *args)
+    else:
+        mla.attn_weights(dev["q"], dev["lse"], dev["kv_cache"], *args)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("s_q", [1, 2, 3, 4])
+def test_attn_weights_calls_of_every_cluster_size_back_to_back(fp8, s_q):
+    """Short calls one straight after the other, beside calls of another kernel that starts in the shared memory they
+    have just left: an arrival that comes after its CTA has gone would be one that the next CTA's barriers count."""
+    import mla_absorbed_decode_gb300 as mla
+    w = W.Workload("weights_back", B=40, s_q=s_q, H=128, ragged_max=200, causal=True, kv_fp8=fp8)
+    g = torch.Generator().manual_seed(s_q)
+    inp = _weights_inputs(w, seed=33, seqlens=torch.randint(0, 200, (40,), generator=g, dtype=torch.int32))
+    good = _run_weights(inp)
+    dev = {k: v.cuda() for k, v in inp.items() if torch.is_tensor(v)}
+    parts = mla.num_sm_parts(s_q, 128)
+    meta = mla.decode_metadata(dev["seqlens"], s_q, 128, True, parts)
+    pool = (dev["q"], dev["kv_cache"]) + ((inp["kv_scale"],) if fp8 else ())
+    decode = lambda: (mla.decode_fp8 if fp8 else mla.decode)(*pool, dev["block_table"], dev["seqlens"],
+                                                              inp["softmax_scale"], True, meta, parts)
+    first = decode()
+    outs = [dev["before"].clone() for _ in range(60)]
+    for i, out in enumerate(outs):
+        _call(inp, dev, out)
+        if i % 3 == 2:
+            last = decode()
+    assert mla.get_device_status() == 0
+    for out in outs:
+        assert torch.equal(out.cpu(), good)
+    assert torch.equal(last[0], first[0]) and torch.equal(last[1], first[1])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("s_q", [1, 2, 3, 4])
+def test_attn_weights_gives_up_when_a_page_never_arrives(fp8, s_q):
+    """The test hook withholds every CTA's first page: the waits on it run out of time, the call reports it and ends,
+    and the calls after it are right."""
+    import mla_absorbed_decode_gb300 as mla
+    w = W.Workload("weights_timeout", B=3, s_q=s_q, H=128, fixed_seqlens=(300, 2000, 64), kv_fp8=fp8)
+    inp = _weights_inputs(w, seed=34)
+    good = _run_weights(inp)
+    dev = {k: v.cuda() for k, v in inp.items() if torch.is_tensor(v)}
+    out = dev["before"].clone()
+    mla.debug_withhold_first_load(True)
+    _call(inp, dev, out)
+    assert mla.get_device_status() == 5          # MLA_ERR_TIMEOUT
+    assert mla.get_device_status() == 0
+    for b, n in enumerate((300, 2000, 64)):
+        assert torch.equal(out[b, n:], dev["before"][b, n:])
+    for _ in range(3):
+        assert torch.equal(_run_weights(inp), good)
