@@ -11,7 +11,6 @@
 #include <cmath>
 #include <cstddef>
 #include <mutex>
-#include <type_traits>
 
 #include "mla_kernels.h"
 #include "mla_ptx.cuh"
@@ -82,7 +81,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr));
 }
 
-template <bool F8, bool Pair>
+template <bool F8, bool Pair, int Parts = 1>
 struct WCfg {
   static constexpr uint32_t kTokens = Pair ? 32 : 64;           // of a page that a CTA loads
   static constexpr uint32_t kChunk = kTokens * 128;             // 128 bytes of each, 128-byte swizzle
@@ -97,6 +96,8 @@ struct WCfg {
   // changes little: two query positions over 64 requests of up to 8192 tokens 57.9 us with 2, 56.8 with 4, 57.8 with 8;
   // over 128 of up to 400 16.3, 17.1 and 17.5)
   static constexpr int kSwitchPages = F8 ? 5 : 2;
+  static constexpr int kParts = Parts;   // accumulators that a page's scores are added up from, a run of its chunks each
+  static_assert(kParts == 1 || kKChunks % kParts == 0, "equal parts");
   static_assert(kQRows * 128 % 1024 == 0 && kStageBytes % 1024 == 0, "swizzled rows start where the swizzle does");
   static constexpr uint32_t kOffShared = kStages * kStageBytes;
   static_assert(kQItemBytes <= kStageBytes && kQItems <= kStages, "a row block's q is resident at once");
@@ -424,13 +425,13 @@ __device__ __forceinline__ void weights_tmem_dealloc(uint32_t taddr) {
 }
 
 // (of a pair: in its first CTA)
-template <bool F8, bool Pair>
+template <bool F8, bool Pair, int Parts>
 __device__ void w_mma(const WeightsParams& p, WShared& sh, uint32_t smem, uint32_t rank, uint32_t cl) {
-  using C = WCfg<F8, Pair>;
+  using C = WCfg<F8, Pair, Parts>;
   const uint32_t tmem = sh.tmem_base;
   WWalk<C::kSwitchPages> walk(sh);
   WSegment s;
-  uint32_t i = 0, T = 0, seg = 0;
+  uint32_t i = 0, T = 0, seg = 0;   // T: S accumulators filled
   bool ok = true;
   while (ok && walk.next(p, s)) {
     if (!(ok = w_warp_wait(sh, F8 ? sh.q_taken : sh.q_full, seg & 1, p.status, cl))) break;
@@ -443,40 +444,49 @@ __device__ void w_mma(const WeightsParams& p, WShared& sh, uint32_t smem, uint32
     i += C::kQItems;
     if (F8 && !(ok = w_warp_wait(sh, sh.q_full, seg & 1, p.status, cl))) break;
     ++seg;
-    bool ready = false;   // the page's stage and S buffer have been seen free during the page before
-    for (int k = s.k0; k < s.k1; ++k, ++i, ++T) {
-      const uint32_t st = i % C::kStages, sb = T % kSBufs;
-      if (!ready) ok = w_warp_wait(sh, sh.s_empty[sb], ((T / kSBufs) & 1) ^ 1, p.status, cl) &&
-                       w_warp_wait(sh, sh.full[st], (i / C::kStages) & 1, p.status, cl);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t d = tmem + kSCol0 + sb * kPageTokens, lead = elect_lane();
+    bool ready = false;   // the next part's S buffer (and stage) have been seen free during the part before
+    for (int k = s.k0; k < s.k1; ++k, ++i) {
+      const uint32_t st = i % C::kStages;
       const uint32_t page = (((smem + st * C::kStageBytes) >> 4) & 0x3FFF) | (1u << 16);   // (16 bytes: unused with a swizzle)
-      auto chunks = [&](auto first, auto last) {   // the MMAs of the page's chunks [first, last)
 #pragma unroll
-        for (int c = first; c < last; ++c)
+      for (int part = 0; part < C::kParts; ++part) {
+        const uint32_t sb = T % kSBufs;
+        if (!ready) ok = w_warp_wait(sh, sh.s_empty[sb], ((T / kSBufs) & 1) ^ 1, p.status, cl) &&
+                         (part > 0 || w_warp_wait(sh, sh.full[st], (i / C::kStages) & 1, p.status, cl));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = tmem + kSCol0 + sb * kPageTokens, lead = elect_lane();
+        const int c0 = part * (C::kKChunks / C::kParts), c1 = c0 + C::kKChunks / C::kParts;
+        auto chunks = [&](int first, int last) {   // the MMAs of the page's chunks [first, last)
 #pragma unroll
-          for (int j = 0; j < (F8 && c == 4 ? 2 : 4); ++j) {
-            const uint32_t at = page + (c * C::kChunk + j * 32) / 16;
-            if constexpr (F8) {   // chunks of 128 codes, K = 32 a step; the half of q that it lies in holds hi, then lo
-              const int step = 4 * c + j, col = 144 * (step / 9) + 8 * (step % 9);
-              mma_step<F8, Pair>(d, tmem + kQCol + col, at, (c | j) ? 1u : 0u, lead);
-              mma_step<F8, Pair>(d, tmem + kQCol + col + 72, at, 1u, lead);
-            } else {
-              mma_step<F8, Pair>(d, tmem + kQCol + c * 32 + j * 8, at, (c | j) ? 1u : 0u, lead);
+          for (int c = first; c < last; ++c)
+#pragma unroll
+            for (int j = 0; j < (F8 && c == 4 ? 2 : 4); ++j) {
+              const uint32_t at = page + (c * C::kChunk + j * 32) / 16;
+              if constexpr (F8) {   // chunks of 128 codes, K = 32 a step; the half of q that it lies in holds hi, then lo
+                const int step = 4 * c + j, col = 144 * (step / 9) + 8 * (step % 9);
+                mma_step<F8, Pair>(d, tmem + kQCol + col, at, (c | j) ? 1u : 0u, lead);
+                mma_step<F8, Pair>(d, tmem + kQCol + col + 72, at, 1u, lead);
+              } else {
+                mma_step<F8, Pair>(d, tmem + kQCol + c * 32 + j * 8, at, c > c0 || j ? 1u : 0u, lead);
+              }
             }
-          }
-      };
-      constexpr int kAll = static_cast<int>(C::kKChunks), kFirst = F8 ? 4 : 7;
-      chunks(std::integral_constant<int, 0>(), std::integral_constant<int, kFirst>());
-      // a look at the next page's barriers while MMAs are queued, not between two pages where the pipe would drain
-      // (FP8: 31.8 -> 30.9 us)
-      ready = k + 1 < s.k1 &&
-              __all_sync(0xffffffffu, mbar_peek(smem_u32(&sh.s_empty[(T + 1) % kSBufs]), (((T + 1) / kSBufs) & 1) ^ 1) &&
-                                          mbar_peek(smem_u32(&sh.full[(i + 1) % C::kStages]), ((i + 1) / C::kStages) & 1));
-      chunks(std::integral_constant<int, kFirst>(), std::integral_constant<int, kAll>());
-      commit_step<Pair>(smem_u32(&sh.empty[st]), 3u << rank);   // waited for by the producers, at the latest when they end
-      commit_step<Pair>(smem_u32(&sh.s_full[sb]), 3u << rank);  // waited for by the epilogue warps
+        };
+        const int look = c1 - (F8 || C::kParts > 1 ? 1 : 2);
+        chunks(c0, look);
+        // a look at the next part's barriers while MMAs are queued, not between two parts where the pipe would drain
+        // (FP8: 31.8 -> 30.9 us)
+        const bool more = part + 1 < C::kParts, next_page = k + 1 < s.k1;
+        ready = (more || next_page) &&
+                __all_sync(0xffffffffu,
+                           mbar_peek(smem_u32(&sh.s_empty[(T + 1) % kSBufs]), (((T + 1) / kSBufs) & 1) ^ 1) &&
+                               (more || mbar_peek(smem_u32(&sh.full[(i + 1) % C::kStages]), ((i + 1) / C::kStages) & 1)));
+        chunks(look, c1);
+        if (!more) commit_step<Pair>(smem_u32(&sh.empty[st]), 3u << rank);   // waited for by the producers, at the latest when they end
+        commit_step<Pair>(smem_u32(&sh.s_full[sb]), 3u << rank);             // waited for by the epilogue warps
+        ++T;
+      }
+      if (!ok) break;
     }
   }
   if (T > 0) {   // no MMA is in flight when the CTAs free their TMEM: said to this CTA alone, which waits for it
@@ -628,9 +638,9 @@ struct Row {   // of the scores: p = exp2(s scale + c), both as float pairs
 
 // Warps 2..9.  Warp quadrant q (TMEM lanes 32 q .. 32 q + 31: the rows), half `half` of the page's columns.
 // All waits are on bounded barriers (no bar.sync), so a warp that gives up leaves no other hanging.
-template <bool F8, bool Pair>
+template <bool F8, bool Pair, int Parts>
 __device__ void w_epilogue(const WeightsParams& p, WShared& sh, uint32_t smem, uint32_t rank, uint32_t cl) {
-  using C = WCfg<F8, Pair>;
+  using C = WCfg<F8, Pair, Parts>;
   // an arrival for the warp that issues the MMAs: of a pair, in its first CTA.  What it orders is TMEM alone (the
   // tcgen05 fences beside it), so it releases no further than any arrival.
   auto tell_mma = [&](uint64_t& bar) {
@@ -706,17 +716,29 @@ __device__ void w_epilogue(const WeightsParams& p, WShared& sh, uint32_t smem, u
       least = min(least, row[j].vis);
     }
     for (int k = s.k0; k < s.k1; ++k, ++T) {
-      const uint32_t sb = T % kSBufs, buf = T % kPartBufs;
-      if (!w_warp_wait(sh, sh.s_full[sb], (T / kSBufs) & 1, p.status, cl)) return;
-      tc_fence_after();
+      const uint32_t buf = T % kPartBufs;
       float v[2][16];   // rows 16 h .. 16 h + 15 of the quadrant
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        tmem_ld_16x256(lane_base + (static_cast<uint32_t>(16 * h) << 16) + kSCol0 + sb * kPageTokens + cb, v[h]);
-      tmem_wait_ld();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tell_mma(sh.s_empty[sb]);
+      for (int part = 0; part < C::kParts; ++part) {
+        const uint32_t unit = T * C::kParts + part, sb = unit % kSBufs;
+        if (!w_warp_wait(sh, sh.s_full[sb], (unit / kSBufs) & 1, p.status, cl)) return;
+        tc_fence_after();
+        float x[2][16];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          tmem_ld_16x256(lane_base + (static_cast<uint32_t>(16 * h) << 16) + kSCol0 + sb * kPageTokens + cb, x[h]);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tell_mma(sh.s_empty[sb]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            const float2 sum = part ? add2({v[h][e], v[h][e + 1]}, {x[h][e], x[h][e + 1]}) : make_float2(x[h][e], x[h][e + 1]);
+            v[h][e] = sum.x, v[h][e + 1] = sum.y;
+          }
+      }
       const int c0 = k * kPageTokens + cb;   // token of the columns' first
       const bool whole = least - c0 >= 32;   // all 32 columns are visible to the four rows
       float total[8];
@@ -806,7 +828,7 @@ __device__ void w_sum(const WeightsParams& p, WShared& sh, uint32_t cl, uint32_t
   // waits
 }
 
-template <bool F8, bool Pair>
+template <bool F8, bool Pair, int Parts>
 __global__ void __launch_bounds__(kWThreads, 1)
 mla_attn_weights_kernel(const __grid_constant__ WMaps maps, const __grid_constant__ WeightsParams p) {
   using C = WCfg<F8, Pair>;
@@ -861,9 +883,9 @@ mla_attn_weights_kernel(const __grid_constant__ WMaps maps, const __grid_constan
   if (warp == 0) {
     if ((threadIdx.x & 31) == 0) w_producer<F8, Pair>(p, maps, sh, smem, rank, cl);
   } else if (warp == 1) {
-    if (!Pair || (rank & 1) == 0) w_mma<F8, Pair>(p, sh, smem, rank, cl);
+    if (!Pair || (rank & 1) == 0) w_mma<F8, Pair, Parts>(p, sh, smem, rank, cl);
   } else if (warp < 2 + kEpiWarps) {
-    w_epilogue<F8, Pair>(p, sh, smem, rank, cl);
+    w_epilogue<F8, Pair, Parts>(p, sh, smem, rank, cl);
   } else {
     w_sum<F8, Pair>(p, sh, cl, rank);
   }
@@ -891,9 +913,19 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 using WeightsKernel = void (*)(WMaps, WeightsParams);
 // An even number of row blocks pairs up.
 bool pairs_up(int cl) { return cl % 2 == 0; }
+// bf16: every step that the tensor pipe adds to an accumulator truncates, which leaves a score short in proportion to the
+// steps.  One row block adds its scores up from three accumulators of 12 steps (rounded sums).  Error against 64 bits and
+// time, N(0, 1) q and k, with three accumulators and with one: 64 requests of 4096 tokens, 128 heads, 1.9e-7 and 5.6e-7,
+// 48.9 and 48.1 us; 16 heads 3.7e-7 and 1.1e-6, 48.6 and 47.5 us; 8 requests of 1000 tokens, one head, 1.2e-6 and 3.9e-6, 8.6 and
+// 8.5 us.  (Nine: 9.6e-8 and 2.5e-7, but 56 us.)  With more blocks a weight is a sum of more than 128 rows, its error 5e-7 with
+// one accumulator, and the epilogue has no time for three: two query positions over 64 x 8192 tokens 116 us and
+// 101, three over 16 x 8192 51 and 46.  FP8: an E4M3 product has 8 bits, so that one accumulator leaves out less (2.0e-7; 8.7e-7
+// for one head).
+constexpr int kBlockParts = 3;
 WeightsKernel weights_kernel(bool fp8, int cl) {
-  return pairs_up(cl) ? (fp8 ? mla_attn_weights_kernel<true, true> : mla_attn_weights_kernel<false, true>)
-                      : (fp8 ? mla_attn_weights_kernel<true, false> : mla_attn_weights_kernel<false, false>);
+  if (fp8) return pairs_up(cl) ? mla_attn_weights_kernel<true, true, 1> : mla_attn_weights_kernel<true, false, 1>;
+  if (cl == 1) return mla_attn_weights_kernel<false, false, kBlockParts>;
+  return pairs_up(cl) ? mla_attn_weights_kernel<false, true, 1> : mla_attn_weights_kernel<false, false, 1>;
 }
 cudaLaunchConfig_t weights_config(bool fp8, int clusters, int cl, cudaStream_t stream, cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t cfg = pdl_config(dim3(static_cast<unsigned>(clusters * cl)), dim3(kWThreads),
@@ -924,7 +956,7 @@ mla_status_t weights_setup(WeightsDevice** out) {
     int sms = 0;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return MLA_ERR_CUDA;
     for (int f = 0; f < 2; ++f) {
-      for (int cl = 1; cl <= 2; ++cl)   // both kernels
+      for (int cl = 1; cl <= 3; ++cl)   // every kernel
         if (cudaFuncSetAttribute(weights_kernel(f, cl), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(f ? weights_smem<true>() : weights_smem<false>())) != cudaSuccess)
           return MLA_ERR_CUDA;
