@@ -712,6 +712,7 @@ mla_status_t evict_impl(void* kv_cache, bool fp8, int64_t num_blocks, const int3
   if (width < (budget < slots ? budget : slots)) return MLA_ERR_INVALID_ARG;
   if (slots > kEvictMaxSlots || num_blocks * kPageTokens > (int64_t(1) << 31) - kPageTokens || B > kScheduleMaxB)
     return MLA_ERR_UNSUPPORTED;
+  if (arrival && arrival_stride < slots) slots = arrival_stride;   // what is read of a row
   // what is written may overlap neither what is read nor one another (new_seqlens may be seqlens)
   const uint64_t out_bytes = static_cast<uint64_t>(B) * width * 4, rows = static_cast<uint64_t>(B) - 1;
   const struct { const void* at; uint64_t bytes; } span[] = {
@@ -722,7 +723,6 @@ mla_status_t evict_impl(void* kv_cache, bool fp8, int64_t num_blocks, const int3
     for (int j = i + 1; j < 8; ++j)
       if (span[i].at && span[j].at && overlap(span[i].at, span[i].bytes, span[j].at, span[j].bytes))
         return MLA_ERR_INVALID_ARG;
-  if (arrival && arrival_stride < slots) slots = arrival_stride;
   EvictParams p = {};
   p.kv = kv_cache;
   p.num_blocks = num_blocks;
