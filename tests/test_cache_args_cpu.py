@@ -1,5 +1,7 @@
 """Argument checks of eviction that its arguments reach one by one: every pointer has an address of its own, and the call
 that each check breaks is one that passes all of them (CPU: nothing is launched, the addresses are never read)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -94,3 +96,16 @@ def test_evict_limits(mla, fp8):
                  dict(max_blocks=4097, w_stride=262208, arrival=None, a_stride=0, budget=100, width=100)):
         assert call(*_args(**more)) == 2, more
     assert call(*_args(max_blocks=4096, w_stride=262208, arrival=None, a_stride=0)) == PASSED
+
+
+def test_the_other_calls_pass_their_checks(mla):
+    """The calls that test_cache_abi_cpu.py breaks argument by argument are valid ones."""
+    L, A, sec = mla.lib(), 0x10000, (ctypes.c_int * 3)(16, 8, 8)
+    one = (ctypes.c_int * 1)(32)
+    assert L.mla_rope_axes(A, 128, 64, 2 * A, 128, 64, A, 4, sec, 3, 0, 10000.0, 0, 4, 2, None) == PASSED
+    for fp8 in (False, True):
+        scale = [1.0] if fp8 else []
+        append = [A, 576, A + 1024, 576, 2 * A] + scale + [4, A, 2, A, None, 6, 3, A, 6, one, 1, 0, 10000.0, None]
+        weights = [A, A, A] + scale + [4, A, 2, A, 3, 1, 16, 0.1, 0, A, 128, None]
+        assert (L.mla_cache_append_fp8 if fp8 else L.mla_cache_append)(*append) == PASSED
+        assert (L.mla_attn_weights_fp8 if fp8 else L.mla_attn_weights)(*weights) == PASSED
