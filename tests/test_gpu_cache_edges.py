@@ -5,9 +5,11 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 from mla_absorbed_decode_gb300 import workloads as W
 
-from test_gpu_cache import BF, _run_weights, _weights_inputs
+from _harness import to_np
+from test_gpu_cache import BF, _check_evict, _evict_inputs, _positions, _rope_room, _run_weights, _weights_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -160,3 +162,167 @@ def test_attn_weights_gives_up_when_a_page_never_arrives(fp8, s_q):
         assert torch.equal(out[b, n:], dev["before"][b, n:])
     for _ in range(3):
         assert torch.equal(_run_weights(inp), good)
+
+
+# ------------------------------------------------------------------------ every variant of a kernel --
+@pytest.mark.parametrize("N,H", [(700, 40), (611, 128), (350, 130), (305, 200), (640, 33)])
+@pytest.mark.parametrize("inverse", [False, True])
+def test_rope_axes_several_rounds_of_heads_a_block(N, H, inverse):
+    """Many tokens of more than 32 heads: a block turns up to 128 heads of a token, the last round in part."""
+    import mla_absorbed_decode_gb300 as mla
+    g = torch.Generator().manual_seed(N + H)
+    x = torch.randn((N, H, 64), generator=g).to(BF)
+    pos = _positions(3, N, g)
+    q = torch.full((N, H, 576), 5.0, dtype=BF, device="cuda")
+    got = mla.rope_axes(x.cuda(), pos.cuda(), (10, 12, 10), out=q[..., 512:], interleaved=True, inverse=inverse)
+    ref = oracle.rope_axes(to_np(x), pos.numpy(), (10, 12, 10), interleaved=True, inverse=inverse)
+    assert np.all(np.abs(to_np(got) - ref) <= 2.0 ** -8 * np.abs(ref) + _rope_room(to_np(x)))
+    assert torch.all(q[..., :512] == 5.0)
+    flat = mla.rope_axes(x[:40].cuda(), pos[:, :40].contiguous().cuda(), (10, 12, 10), interleaved=True, inverse=inverse)
+    assert torch.equal(flat, got[:40])           # a block's rounds change no bit
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("slots,lens", [(5056, [5056, 4097, 100]), (12032, [12000, 0, 8193, 4096]),
+                                        (16384, [16384, 16383]), (40000, [39999, 777])])
+def test_evict_equal_weights_over_the_ctas_of_a_cluster(fp8, slots, lens):
+    """Requests of 2, 4 and 8 CTAs whose weights have five values: the cut lies among equals that every CTA holds."""
+    for arrival in (True, False):
+        s = _evict_inputs(lens, slots, fp8, seed=slots, ties=True, arrival=arrival)
+        for budget in (slots // 3, slots - 700):
+            _check_evict(s, budget, 3, 40, budget + 9)
+    s["w"][:] = 1.5                              # nothing but equals
+    _check_evict(s, slots // 2 + 1, 0, 0, slots)
+
+
+@pytest.mark.parametrize("slots,lens", [(451, [451, 450, 3]), (5057, [5057, 4099]), (9001, [9001, 8193])])
+@pytest.mark.parametrize("ties", [False, True])
+def test_evict_rows_that_are_not_aligned(slots, lens, ties):
+    """Rows of an odd number of elements, with arrival numbers: slot by slot where 16-byte loads are not possible."""
+    s = _evict_inputs(lens, slots, False, seed=slots + ties, ties=ties)
+    _check_evict(s, slots // 2, 2, 30, slots // 2 + 65)
+
+
+@pytest.mark.parametrize("shift", [1, 2, 3])
+def test_evict_rows_that_start_anywhere(shift):
+    """Weights and arrival as parts of wider buffers, of which one row or the other is aligned."""
+    import mla_absorbed_decode_gb300 as mla
+    s = _evict_inputs([700, 90, 640], 704, False, seed=35)
+    want = _check_evict(s, 256, 4, 64, 320)
+    wide_w, wide_a = torch.full((3, 709), 9.0, device="cuda"), torch.full((3, 712), 7, dtype=torch.int32, device="cuda")
+    for ws, as_ in ((shift, 0), (0, shift), (shift, shift)):
+        wide_w[:, ws:ws + 704], wide_a[:, as_:as_ + 704] = s["w"].cuda(), s["a"].cuda()
+        kv = s["kv"].cuda()
+        got = mla.evict(kv, s["table"].cuda(), s["lens"].cuda(), wide_w[:, ws:ws + 704], 256, sink=4, recent=64,
+                        arrival=wide_a[:, as_:as_ + 704], width=320)
+        assert mla.get_device_status() == 0
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
+
+
+def test_evict_narrow_arrival_rows_bound_the_lengths():
+    import mla_absorbed_decode_gb300 as mla
+    s = _evict_inputs([60, 64], 256, False, seed=36)
+    a = s["a"][:, :64].contiguous()
+    want = _check_evict(s, 40, 2, 8, 256)
+    kv = s["kv"].cuda()
+    lens = torch.tensor([60, 64], dtype=torch.int32, device="cuda")
+    buf = torch.empty(2 * 64 + 2 * 256, dtype=torch.int32, device="cuda")       # kept right behind arrival
+    arrival, kept = buf[:128].view(2, 64), buf[128:].view(2, 256)
+    arrival.copy_(a)
+    got = mla.evict(kv, s["table"].cuda(), lens, s["w"].cuda(), 40, sink=2, recent=8, arrival=arrival, kept=kept)
+    assert mla.get_device_status() == 0
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
+    assert torch.equal(arrival.cpu(), a)
+
+
+# ------------------------------------------------------------ weights: large channels, the decode's lse --
+@pytest.mark.parametrize("factor", [30.0, 300.0, 3000.0])
+@pytest.mark.parametrize("causal", [False, True])
+def test_attn_weights_fp8_a_large_channel_of_q(factor, causal):
+    """One channel of q is `factor` times the others.  q travels as two E4M3 terms of q 2^k, its largest element in
+    (224, 448]: what they leave of another element is at most half a step of the subnormal codes, 2^-10, so at most 2^-10 / 224
+    < 2^-17 of the largest; a score moves by at most that times scale sum |k_d|, a term p by e^that - 1.  The rest as
+    in test_gpu_cache.py."""
+    w = W.Workload("weights_channel", B=2, s_q=2, H=16, fixed_seqlens=(300, 65), causal=causal, kv_fp8=True)
+    inp = W.make_inputs(w, seed=37)
+    inp["q"][..., 77] *= factor
+    kv = inp["kv_cache"].numpy()
+    q = to_np(inp["q"])
+    B, s_q, H, _ = q.shape
+    rows = [oracle.gather_request(kv, inp["block_table"][b].numpy(), int(inp["seqlens"][b]), inp["kv_scale"]) for b in range(B)]
+    lse = np.full((B, s_q, H), -np.inf)
+    for b in range(B):
+        for i in range(s_q):
+            v = oracle.mla.visible_tokens(int(inp["seqlens"][b]), s_q, i, causal)
+            s = inp["softmax_scale"] * q[b, i] @ rows[b][:v].T
+            lse[b, i] = s.max(axis=1) + np.log(np.exp(s - s.max(axis=1, keepdims=True)).sum(axis=1))
+    inp["lse"] = torch.from_numpy(lse).float()
+    inp["before"] = torch.zeros((B, inp["block_table"].shape[1] * 64))
+    got = _run_weights(inp).double().numpy()
+    for b in range(B):
+        n = int(inp["seqlens"][b])
+        want, room = np.zeros(n), np.full(n, 2.0 ** -126 * s_q * H)
+        for i in range(s_q):
+            v = oracle.mla.visible_tokens(n, s_q, i, causal)
+            for h in range(H):
+                s = inp["softmax_scale"] * rows[b][:v] @ q[b, i, h]
+                arg = s - float(inp["lse"][b, i, h])
+                p = np.exp(arg)
+                mag = inp["softmax_scale"] * np.abs(rows[b][:v])
+                off = 40 * 2.0 ** -23 * (mag @ np.abs(q[b, i, h])) + 2.0 ** -17 * np.abs(q[b, i, h]).max() * mag.sum(axis=1)
+                off += 3 * 2.0 ** -24 * np.abs(arg)
+                want[:v] += p
+                room[:v] += p * (np.expm1(off) + 2.0 ** -22 + s_q * H * 2.0 ** -24)
+        assert np.all(np.abs(got[b, :n] - want) <= room), (b, float((np.abs(got[b, :n] - want) / room).max()))
+        assert np.all(got[b, n:] == 0)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_attn_weights_a_query_row_that_is_not_finite(fp8):
+    """It gives NaN to the tokens that it sees, no other request and no slot past the length; without weight, nothing."""
+    w = W.Workload("weights_q_inf", B=3, s_q=1, H=32, fixed_seqlens=(100, 130, 70), kv_fp8=fp8)
+    inp = _weights_inputs(w, seed=38)
+    good = _run_weights(inp)
+    for v in (float("nan"), float("inf")):
+        bad = dict(inp, q=inp["q"].clone(), lse=inp["lse"].clone())
+        bad["q"][1, 0, 5, 3] = v
+        bad["lse"][1, 0, 5] = float("nan")       # what the decode gives for such a row
+        got = _run_weights(bad)
+        assert torch.isnan(got[1, :130]).all() and torch.equal(got[1, 130:], good[1, 130:])
+        assert torch.equal(got[0], good[0]) and torch.equal(got[2], good[2])
+        bad["lse"][1, 0, 5] = -float("inf")
+        left = dict(inp, lse=inp["lse"].clone())
+        left["lse"][1, 0, 5] = -float("inf")
+        assert torch.equal(_run_weights(bad), _run_weights(left))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("peak", [1.0, 6.0])
+def test_attn_weights_rows_sum_to_the_heads_with_the_decode_s_lse(fp8, peak):
+    """A row's weights sum to 1 with the lse that the library's own decode gives, for flat rows and for peaked ones: both
+    form a score to within 40 * 2^-23 of scale sum |q_d k_d| = A, so the sum is off by at most e^(2 A') - 1 for the largest such
+    A', and the lse is an fp32 number of a few fp32 roundings (2^-20 of the largest |score|)."""
+    import mla_absorbed_decode_gb300 as mla
+    w = W.Workload("weights_sum", B=3, s_q=1, H=64, fixed_seqlens=(900, 64, 333), kv_fp8=fp8)
+    inp = W.make_inputs(w, seed=39)
+    inp["q"] *= peak
+    dev = {k: (v.cuda() if torch.is_tensor(v) else v) for k, v in inp.items()}
+    parts = mla.num_sm_parts(1, 64)
+    meta = mla.decode_metadata(dev["seqlens"], 1, 64, False, parts)
+    pool = (dev["q"], dev["kv_cache"]) + ((inp["kv_scale"],) if fp8 else ())
+    _, lse = (mla.decode_fp8 if fp8 else mla.decode)(*pool, dev["block_table"], dev["seqlens"], inp["softmax_scale"],
+                                                     False, meta, parts)
+    inp["lse"], inp["before"] = lse.cpu(), torch.zeros((3, inp["block_table"].shape[1] * 64))
+    got = _run_weights(inp).double().sum(dim=1).numpy()
+    kv = inp["kv_cache"].numpy() if fp8 else inp["kv_cache"].float().numpy()
+    q = to_np(inp["q"])
+    for b in range(3):
+        rows = oracle.gather_request(kv, inp["block_table"][b].numpy(), int(inp["seqlens"][b]), inp.get("kv_scale"))
+        mag = inp["softmax_scale"] * np.abs(rows) @ np.abs(q[b, 0]).T
+        off = 2 * 40 * 2.0 ** -23 * mag.max()
+        if fp8:
+            off += 2 * 2.0 ** -17 * np.abs(q[b]).max() * inp["softmax_scale"] * np.abs(rows).sum(axis=1).max()
+        off += 2.0 ** -20 * mag.max()
+        assert abs(got[b] - 64) <= 64 * (np.expm1(off) + 2.0 ** -14), (b, got[b], off)
