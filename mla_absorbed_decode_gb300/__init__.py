@@ -657,9 +657,15 @@ class DecodeStep:
                interleaved: bool = False):
         """The W_UK absorption and the rest of the decode query: q_pe as it is, rotated by positions
         (int32 [B*s_q]) inside the absorption, or, with sections, by positions [axes, B*s_q] (rope_axes)."""
+        self._check_axes(positions, sections)
         absorb_q(q_nope, w_uk, self.q, q_pe=None if sections is not None else q_pe, stream=stream,
                  positions=None if sections is not None else positions, rope_theta=rope_theta)
         self._rotate(q_pe, positions, rope_theta, sections, interleaved, stream)
+
+    @staticmethod
+    def _check_axes(positions, sections):
+        if sections is not None and positions is None:
+            raise ValueError("sections need positions [axes, B*s_q]")
 
     def _rotate(self, q_pe, positions, rope_theta, sections, interleaved, stream=None):
         if sections is not None:
@@ -670,6 +676,7 @@ class DecodeStep:
                         sections=None, interleaved: bool = False):
         """absorb() with plan() in the absorption's launch (B <= absorb_plan_max_batch(); else the
         two calls, the schedule on a side stream beside the absorption)."""
+        self._check_axes(positions, sections)
         if sections is not None:
             self.absorb_and_plan(q_nope, None, w_uk, stream=stream)
             self._rotate(q_pe, positions, rope_theta, sections, interleaved, stream)
@@ -692,7 +699,8 @@ class DecodeStep:
     def append(self, c, k_pe, kv_cache, block_table, positions=None, rope_theta: float = 10000.0, sections=(32,),
                interleaved: bool = False, stream=None):
         """The step's new rows (c [B*s_q,512], k_pe [B*s_q,64]) into the cache as each request's last s_q
-        tokens (seqlens counts them), before `run`; k_pe rotated by positions where they are given."""
+        tokens (seqlens counts them), before `run`; k_pe rotated by positions where they are given.  In a batch
+        padded with empty requests cache_append, whose new_offsets give those no row, is the call to make."""
         rot = dict(positions=positions, sections=sections, rope_theta=rope_theta, interleaved=interleaved, stream=stream)
         if self.kv_scale is None:
             cache_append(c, k_pe, kv_cache, block_table, self.seqlens, **rot)

@@ -326,3 +326,57 @@ def test_attn_weights_rows_sum_to_the_heads_with_the_decode_s_lse(fp8, peak):
             off += 2 * 2.0 ** -17 * np.abs(q[b]).max() * inp["softmax_scale"] * np.abs(rows).sum(axis=1).max()
         off += 2.0 ** -20 * mag.max()
         assert abs(got[b] - 64) <= 64 * (np.expm1(off) + 2.0 ** -14), (b, got[b], off)
+
+
+def test_a_step_s_sections_need_positions():
+    """Refused before anything is launched: the query buffer stays as it was."""
+    import mla_absorbed_decode_gb300 as mla
+    B, H = 2, 4
+    step = mla.DecodeStep(B, 1, H, torch.tensor([3, 4], dtype=torch.int32, device="cuda"), False, 0.1)
+    z = lambda *s: torch.zeros(s, dtype=BF, device="cuda")
+    step.q.fill_(3.0)
+    kv, table = z(2, 64, 576), torch.tensor([[0], [1]], dtype=torch.int32, device="cuda")
+    ops = (z(B, H, 128), z(B, H, 64), z(H, 128, 512))
+    for call, args in ((step.absorb, ops), (step.absorb_and_plan, ops), (step.run, (*ops, z(H, 512, 128), kv, table)),
+                       (step.capture, (*ops, z(H, 512, 128), kv, table))):
+        with pytest.raises(ValueError, match="positions"):
+            call(*args, sections=(16, 8, 8))
+    torch.cuda.synchronize()
+    assert torch.all(step.q == 3.0) and mla.get_device_status() == 0
+
+
+def test_append_to_a_batch_padded_with_empty_requests():
+    """new_offsets give an empty request no row: nothing is reported, the others' rows are written."""
+    import mla_absorbed_decode_gb300 as mla
+    g = torch.Generator().manual_seed(40)
+    lens = torch.tensor([5, 0, 64, 0, 65, 0], dtype=torch.int32)
+    offsets = torch.tensor([0, 1, 1, 2, 2, 3, 3], dtype=torch.int32)
+    table = torch.tensor([[0, -1], [-1, -1], [1, -1], [-1, -1], [2, 3], [-1, -1]], dtype=torch.int32)
+    rows, kv = torch.randn((3, 576), generator=g).to(BF), torch.randn((4, 64, 576), generator=g).to(BF)
+    got = mla.cache_append(rows[:, :512].cuda(), rows[:, 512:].cuda(), kv.cuda(), table.cuda(), lens.cuda(),
+                           new_offsets=offsets.cuda())
+    assert mla.get_device_status() == 0
+    want = kv.clone()
+    want[0, 4], want[1, 63], want[3, 0] = rows[0], rows[1], rows[2]
+    assert torch.equal(got.cpu(), want)
+
+
+@pytest.mark.parametrize("plan", [False, True])
+def test_a_captured_step_with_sections(plan):
+    """capture(sections=...) and replay give what the calls one by one give, with positions changed in place."""
+    import mla_absorbed_decode_gb300 as mla
+    w = W.small_variant(W.V3, B=2, seqlen=200, H=16)
+    inp = W.make_inputs(w, seed=41)
+    dev = {k: (v.cuda() if torch.is_tensor(v) else v) for k, v in inp.items()}
+    ops = [dev[k] for k in ("q_nope", "q_pe", "w_uk", "w_uv", "kv_cache", "block_table")]
+    pos = torch.zeros((3, 2), dtype=torch.int32, device="cuda")
+    step = mla.DecodeStep(2, 1, 16, dev["seqlens"], False, w.softmax_scale)
+    step.plan()
+    step.capture(*ops, plan=plan, positions=pos, sections=(16, 8, 8), interleaved=True)
+    pos.copy_(torch.tensor([[200, 199], [3, 40], [17, 0]], dtype=torch.int32))
+    o, q = step.replay().clone(), step.q.clone()
+    turned = mla.rope_axes(dev["q_pe"], pos, (16, 8, 8), interleaved=True)
+    assert torch.equal(q.view(2, 16, 576)[..., 512:], turned)
+    step.run(dev["q_nope"], turned, *ops[2:])
+    assert torch.equal(step.o, o) and torch.equal(step.q, q)
+    assert mla.get_device_status() == 0
