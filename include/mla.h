@@ -312,8 +312,9 @@ mla_status_t mla_extend_chunked(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe
 
 /* ---- The latent cache over a request's life: rotation with several position axes, the write
  * of new rows, the attention weight of every cached token, and eviction by it.  None of the calls
- * keeps anything between calls or needs a workspace; a device's one-time set-up happens in its
- * first call, which is to be made before a stream capture. ---- */
+ * needs a workspace or keeps anything of its tensors (a thread keeps the 32 frequencies of the last
+ * rope_theta that it passed); a device's one-time set-up happens in its first call, which is to be
+ * made before a stream capture. ---- */
 
 /* RoPE with several position axes (a token of an image or a video has a time, a height and a
  * width): every one of the 32 adjacent pairs of a 64-value row turns by the position on its
@@ -382,7 +383,8 @@ mla_status_t mla_cache_append_fp8(const mla_bf16_t* c, int64_t c_row_stride, con
  *  lse            [B, s_q, H] fp32; a row with lse = -inf gave no weight and adds nothing
  *                 (nor do finite scores of a row with lse = +inf, nor a score of -inf: exp(-inf) = 0)
  *  weights        fp32 device, 4-byte aligned, weights_stride elements between requests
- *                 (>= every seqlens[b]); elements from seqlens[b] on are neither read nor written
+ *                 (>= every seqlens[b]); elements from seqlens[b] on are neither read nor written.
+ *                 It overlaps nothing else that the call reads
  * softmax_scale (times kv_scale) times log2(e) has to be a normal float32.  Scores,
  * exponentials and sums are in fp32; every weights[b, t] is summed in a fixed order and added to
  * once, so that equal inputs give equal bits (a sum below 2^-126 may become 0).  A score's exact
@@ -397,7 +399,11 @@ mla_status_t mla_attn_weights(const mla_bf16_t* q, const float* lse, const mla_b
                               float softmax_scale, int causal_s_q, float* weights, int64_t weights_stride,
                               mla_stream_t stream);
 
-/* mla_attn_weights over an FP8 cache, as in mla_decode_fp8. */
+/* mla_attn_weights over an FP8 cache, as in mla_decode_fp8.  Every query row travels as two E4M3 terms of
+ * itself times a power of two that brings its largest element into (224, 448]: exact for elements down to
+ * 1/896 of the largest, within 2^-17 of the largest below.  A score is off by at most that times
+ * softmax_scale * sum over d of |kv_td| more.  A row with an infinity or a NaN gives NaN to every token
+ * it sees (unless its lse is -inf). */
 mla_status_t mla_attn_weights_fp8(const mla_bf16_t* q, const float* lse, const uint8_t* kv_cache, float kv_scale,
                                   int64_t num_blocks, const int32_t* block_table, int max_blocks,
                                   const int32_t* seqlens, int B, int s_q, int H, float softmax_scale, int causal_s_q,

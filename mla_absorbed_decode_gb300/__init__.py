@@ -435,7 +435,7 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-@functools.lru_cache(maxsize=None)
+@functools.lru_cache(maxsize=64)   # a model has one
 def _sections(sections: tuple):
     """Host array of a rotation's sections."""
     if not 1 <= len(sections) <= 4 or min(sections) < 0 or sum(sections) != 32:
