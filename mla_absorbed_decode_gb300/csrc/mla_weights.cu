@@ -40,12 +40,12 @@ struct WeightsParams {
 // the cached pages past it: S = Q K^T on tcgen05 (TMEM accumulators), then for every row
 // p = exp2(S * scale - lse) and for every token the sum over the rows.  A page is 72 KiB (36 KiB in
 // FP8) read once, against 9.4 MFLOP.  Measured (GPU time of a call, B = 64, H = 128):
-//     bf16, 4096 tokens                       48-49 us  6.4 TB/s, 0.95 of the copy rate: HBM-bound
-//     FP8, 4096 tokens                        31-32 us  5.2 TB/s, 0.77: the MMAs (q is two E4M3 terms, so bf16's
-//                                                       MMA time for half the bytes; 1290 clk a page, 1152 of
-//                                                       them the tensor pipe's), 7 us of start and end
-//     bf16, two query positions, 8192 tokens  99-101 us  6.3 TB/s, 0.93: HBM and the MMAs (81.8 us at the pipe's rate)
-// Called for seconds on end, the last two run into the power limit (1.35 kW): 36 us at 1.70 GHz and 115 us at 1.50 GHz.
+//     bf16, 4096 tokens                       49-50 us  6.3 TB/s, 0.94 of the copy rate: HBM-bound
+//     FP8, 4096 tokens                        33 us     4.9 TB/s, 0.73: q is two E4M3 terms, so bf16's MMA time for half
+//                                                       the bytes.  27 pages a CTA of 1290 clk (1152 of them the tensor pipe's) are
+//                                                       16.8 us at 2.07 GHz, start and end 7; the other 9 have not been traced
+//     bf16, two query positions, 8192 tokens  99-106 us 5.9-6.3 TB/s: HBM and the MMAs (81.8 us at the pipe's rate)
+// Called for seconds on end, the last two run into the power limit (1.35 kW): 35 to 37 us, and 114 to 124 from board to board.
 //  * Rows on the TMEM lanes, tokens on the columns: Q is loaded once per request, and the ring has the
 //    whole of shared memory for pages (221 KiB: what is in flight covers HBM latency).  Q comes through the ring
 //    too: read from global memory by its threads, 1152 bytes apart, it took 9.5 us instead of 2.4.
@@ -58,9 +58,10 @@ struct WeightsParams {
 //  * More than 128 rows: a cluster of ceil(rows / 128) CTAs walks the same pages, each with its row
 //    block; the others hand their 64 sums a page to CTA 0 through distributed shared memory.
 //  * Two CTAs whose row blocks share pages make a pair: one MMA of 256 rows (cta_group::2), for which each
-//    loads half of a page's tokens.  That halves what a page costs in L2 reads and shared memory: 111 us before, each CTA
-//    with whole pages, and 126 us at the power limit.  Three row blocks stay single: padded to two pairs, a third fewer
-//    clusters fit (54.0 us against 43.1 for 16 requests of 8192 tokens).
+//    loads half of a page's tokens.  That halves what a page costs in L2 reads and shared memory: two query positions took 111
+//    us where they take 101, each CTA with whole pages.  Three row blocks stay single: padded to two pairs, a third
+//    fewer clusters fit (16 requests of 8192 tokens 54.0 us, where single ones took 43.1 on the same board).
+//  * bf16, one row block: a page's scores come from three accumulators of 12 MMA steps each (kBlockParts says why).
 //  * Work: all requests' pages in a row, with kSwitchPages for each request's start, cut evenly over the
 //    clusters that fit the GPU.  Each CTA finds its own piece from the lengths (no schedule, no metadata).
 constexpr int kWThreads = 352;                 // warp 0: TMA, 1: MMA, 2..9: exponentials, 10: sums
@@ -92,9 +93,9 @@ struct WCfg {
   static constexpr int kQRows = 128 / kQItems;
   static constexpr uint32_t kEpiArrivals = kEpiWarps * (Pair ? 2 : 1);   // where a pair's epilogue warps all arrive
   static constexpr uint32_t kQItemBytes = static_cast<uint32_t>(kQRows) * kDimQK * 2;
-  // what a switch of requests costs (Q's load and its way into TMEM), in pages: the split charges it (more
-  // changes little: two query positions over 64 requests of up to 8192 tokens 57.9 us with 2, 56.8 with 4, 57.8 with 8;
-  // over 128 of up to 400 16.3, 17.1 and 17.5)
+  // what a switch of requests costs (Q's load and its way into TMEM), in pages: the split charges it.  bf16: 128 requests
+  // of up to 400 tokens 12.3 us with 2 and 13.7 with 4 (two query positions 16.5 and 17.1), 64 x 4096 49.0 and 49.5; FP8: 128 of
+  // up to 8192 72.8 us with 2, 70.4 with 5, 71.2 with 8, two query positions over 64 of up to 8192 66.8, 64.0 and 64.2
   static constexpr int kSwitchPages = F8 ? 5 : 2;
   static constexpr int kParts = Parts;   // accumulators that a page's scores are added up from, a run of its chunks each
   static_assert(kParts == 1 || kKChunks % kParts == 0, "equal parts");
