@@ -380,3 +380,79 @@ def test_a_captured_step_with_sections(plan):
     step.run(dev["q_nope"], turned, *ops[2:])
     assert torch.equal(step.o, o) and torch.equal(step.q, q)
     assert mla.get_device_status() == 0
+
+
+# ------------------------------------------------------------------- replayed calls, addresses past 32 bits --
+@pytest.mark.parametrize("slots,lens", [(704, [700, 90, 640]), (40000, [39000, 40000])])
+def test_evict_recorded_and_replayed_with_lengths_in_place(slots, lens):
+    """A graph of the call with new_seqlens = seqlens, for requests of one CTA and of eight: every replay from the same
+    cache and lengths gives what the call gives."""
+    import mla_absorbed_decode_gb300 as mla
+    s = _evict_inputs(lens, slots, True, seed=42)
+    budget, width = slots // 3, slots // 3 + 64
+    want = _check_evict(s, budget, 4, 64, width)
+    dev = {k: v.cuda() for k, v in s.items()}
+    kv, n = dev["kv"].clone(), dev["lens"].clone()
+    outs = [torch.empty_like(t) for t in want[1:]]
+    call = lambda: mla.evict_fp8(kv, dev["table"], n, dev["w"], budget, sink=4, recent=64, arrival=dev["a"], width=width,
+                                 new_seqlens=n, kept=outs[0], weights_out=outs[1], arrival_out=outs[2])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    after = None
+    for _ in range(3):
+        kv.copy_(dev["kv"])
+        n.copy_(dev["lens"])
+        graph.replay()
+        assert torch.equal(n, want[0])
+        for x, y in zip(outs, want[1:]):
+            assert torch.equal(x, y)
+        after = kv.clone() if after is None else after
+        assert torch.equal(kv, after)
+    assert mla.get_device_status() == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_cache_of_more_than_4_gib(fp8):
+    """Append, attention weights and eviction on pages whose addresses and element numbers pass 32 bits give the bits that
+    they give in a small pool."""
+    import mla_absorbed_decode_gb300 as mla
+    far = 117000 if fp8 else 59000                       # pages: 4.3 GB, and more than 2^31 elements
+    w = W.Workload("weights_far", B=2, s_q=1, H=32, fixed_seqlens=(300, 129), kv_fp8=fp8)
+    inp = _weights_inputs(w, seed=43)
+    g = torch.Generator().manual_seed(44)
+    rows = torch.randn((2, 576), generator=g).to(BF).cuda()
+    small, table = inp["kv_cache"].cuda(), inp["block_table"].cuda()
+    big = torch.zeros((far + small.shape[0], 64, 576), dtype=small.dtype, device="cuda")
+    assert big.numel() > 2 ** 31 and big.numel() * big.element_size() > 2 ** 32
+    big[far:] = small
+    seqlens = inp["seqlens"].cuda()
+    scale = (inp["kv_scale"],) if fp8 else ()
+    got = []
+    for kv, bt in ((small, table), (big, torch.where(table >= 0, table + far, table))):
+        (mla.cache_append_fp8 if fp8 else mla.cache_append)(rows[:, :512], rows[:, 512:], kv, *scale, bt, seqlens)
+        weights = inp["before"].cuda()
+        (mla.attn_weights_fp8 if fp8 else mla.attn_weights)(inp["q"].cuda(), inp["lse"].cuda(), kv, *scale, bt, seqlens,
+                                                            inp["softmax_scale"], False, weights)
+        left = (mla.evict_fp8 if fp8 else mla.evict)(kv, bt, seqlens, weights, 100, sink=2, recent=20)
+        assert mla.get_device_status() == 0
+        got.append((weights, *left))
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+    bits = lambda t: t if fp8 else t.view(torch.int16)
+    assert torch.equal(bits(big[far:]), bits(small))
+    assert not bits(big[:far]).any()
+
+
+def test_rope_axes_into_a_query_of_more_than_2_31_elements():
+    import mla_absorbed_decode_gb300 as mla
+    g = torch.Generator().manual_seed(45)
+    N, H = 30000, 128
+    x, pos = torch.randn((1, H, 64), generator=g).to(BF).cuda(), _positions(3, N, g).cuda()
+    q = torch.zeros((N, H, 576), dtype=BF, device="cuda")
+    assert q.numel() > 2 ** 31
+    mla.rope_axes(x.expand(N, H, 64), pos, (16, 8, 8), out=q[..., 512:])
+    for n in (0, 1, 14563, 14564, 29127, N - 1):
+        assert torch.equal(q[n, :, 512:], mla.rope_axes(x, pos[:, n:n + 1].contiguous(), (16, 8, 8))[0])
+    assert not q[-300:, :, :512].any() and not q[:300, :, :512].any()
+    assert mla.get_device_status() == 0
