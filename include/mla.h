@@ -169,6 +169,32 @@ mla_status_t mla_decode_sparse_fp8(const mla_bf16_t* q, const uint8_t* kv_cache,
                                    int num_sm_parts, void* workspace, size_t workspace_bytes, mla_bf16_t* out,
                                    float* lse, mla_stream_t stream);
 
+/* Absorbed decode over a 4-bit latent cache.  A cached token is 352 bytes:
+ *   [0, 256)    512 E2M1 codes of the latent, dim 2i in the low half of byte i (sign, 2 exponent
+ *               bits with bias 1, 1 mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6)
+ *   [256, 288)  32 E4M3 scales, one for 16 latent dims
+ *   [288, 352)  64 E4M3 codes of the RoPE key
+ *   kv_t[d] = code[d] * scale[d / 16] * kv_scale (d < 512),  kv_t[512 + j] = code[j] * kv_scale
+ *  kv_cache  [num_blocks, 64, 352] bytes, 16-byte aligned
+ *  kv_scale  one scale for the whole cache, in [2^-116, 2^115], and softmax_scale * kv_scale * log2(e) a normal
+ *            float32 (else MLA_ERR_INVALID_ARG)
+ * The attention is that of mla_decode over these values; q stays bf16.  Other arguments, results and
+ * errors as for mla_decode, but B up to 16384 (more: MLA_ERR_UNSUPPORTED).  Async on stream. */
+mla_status_t mla_decode_fp4(const mla_bf16_t* q, const uint8_t* kv_cache, float kv_scale, int64_t num_blocks,
+                            const int32_t* block_table, int max_blocks, const int32_t* seqlens, int B, int s_q, int H,
+                            float softmax_scale, int causal_s_q, const void* metadata, int num_sm_parts,
+                            void* workspace, size_t workspace_bytes, mla_bf16_t* out, float* lse,
+                            mla_stream_t stream);
+
+/* The sparse (top-k) decode of mla_decode_sparse over a 4-bit cache as in mla_decode_fp4.  Arguments, results and
+ * errors as for those two calls.  Async on stream. */
+mla_status_t mla_decode_sparse_fp4(const mla_bf16_t* q, const uint8_t* kv_cache, float kv_scale, int64_t num_blocks,
+                                   const int32_t* block_table, int max_blocks, const int32_t* seqlens,
+                                   const int32_t* indices, int64_t index_stride, const int32_t* topk_lens, int B,
+                                   int s_q, int H, float softmax_scale, int causal_s_q, const void* metadata,
+                                   int num_sm_parts, void* workspace, size_t workspace_bytes, mla_bf16_t* out,
+                                   float* lse, mla_stream_t stream);
+
 /* W_UK absorption and assembly of the decode query ("DeepSeekV2之MLA" 4.5:
  * q_nope_out = bmm(q_nope, w_kc) goes into q[..., :kv_lora_rank], the RoPE'd
  * q_pe into the last 64 values):
@@ -374,6 +400,25 @@ mla_status_t mla_cache_append_fp8(const mla_bf16_t* c, int64_t c_row_stride, con
                                   const int32_t* new_offsets, int N, int B, const int32_t* positions,
                                   int64_t positions_stride, const int32_t* sections, int n_axes, int interleaved,
                                   float rope_theta, mla_stream_t stream);
+
+/* mla_cache_append into a 4-bit cache (as in mla_decode_fp4), with the latent's norm on the way:
+ *   y     = c[r], or with norm_weight  c[r] * rsqrt(mean(c[r]^2) + norm_eps) * norm_weight
+ *   scale = E4M3(max |y| over the 16 dims of a group / (6 kv_scale))
+ *   code  = E2M1(y / (scale kv_scale))          (0 in a group whose scale is 0 or NaN)
+ *   rope  = E4M3(turned k_pe / kv_scale)
+ * all of it in float32 from the bf16 inputs, every rounding to nearest even and saturating (infinities too).  A
+ * group with a NaN gets a NaN scale, so that its values read as NaN.
+ *  kv_cache     [num_blocks, 64, 352] bytes, 16-byte aligned
+ *  kv_scale     as for mla_decode_fp4
+ *  norm_weight  [512] bf16, 16-byte aligned, or NULL: the latent comes normalised
+ *  norm_eps     finite and >= 0 (read with norm_weight only)
+ * Other arguments, results and errors as for mla_cache_append. */
+mla_status_t mla_cache_append_fp4(const mla_bf16_t* c, int64_t c_row_stride, const mla_bf16_t* k_pe,
+                                  int64_t k_pe_row_stride, uint8_t* kv_cache, float kv_scale, int64_t num_blocks,
+                                  const int32_t* block_table, int max_blocks, const int32_t* seqlens,
+                                  const int32_t* new_offsets, int N, int B, const int32_t* positions,
+                                  int64_t positions_stride, const int32_t* sections, int n_axes, int interleaved,
+                                  float rope_theta, const mla_bf16_t* norm_weight, float norm_eps, mla_stream_t stream);
 
 /* The attention weight that a step gave every cached token, summed over its heads and query
  * positions (all of them share one cached row) and added to what earlier steps left:

@@ -16,10 +16,11 @@ import torch
 
 __all__ = [
     "MLAError", "lib", "library_path", "num_sm_parts", "metadata_size", "decode_metadata",
-    "decode_workspace_size", "decode", "decode_sparse", "decode_fp8", "decode_sparse_fp8", "absorb_q", "unabsorb_o",
+    "decode_workspace_size", "decode", "decode_sparse", "decode_fp8", "decode_sparse_fp8", "decode_fp4",
+    "decode_sparse_fp4", "absorb_q", "unabsorb_o",
     "absorb_plan_max_batch", "absorb_q_plan",
     "bmm_fp8_workspace_size", "absorb_q_fp8", "absorb_q_fp8_plan", "unabsorb_o_fp8", "extend_workspace_size", "extend_chunked",
-    "rope_axes", "cache_append", "cache_append_fp8", "attn_weights", "attn_weights_fp8", "evict", "evict_fp8",
+    "rope_axes", "cache_append", "cache_append_fp8", "cache_append_fp4", "attn_weights", "attn_weights_fp8", "evict", "evict_fp8",
     "get_device_status",
     "schedule_params", "debug_withhold_first_load", "DecodeStep", "EXPORTED_SYMBOLS",
 ]
@@ -47,6 +48,10 @@ _SIGNATURES = {
                                 _p, _c_int, _p, _c_size, _p, _p, _p]),
     "mla_decode_sparse_fp8": (_c_int, [_p, _p, _c_float, _c_ll, _p, _c_int, _p, _p, _c_ll, _p, _c_int, _c_int, _c_int,
                                        _c_float, _c_int, _p, _c_int, _p, _c_size, _p, _p, _p]),
+    "mla_decode_fp4": (_c_int, [_p, _p, _c_float, _c_ll, _p, _c_int, _p, _c_int, _c_int, _c_int, _c_float, _c_int,
+                                _p, _c_int, _p, _c_size, _p, _p, _p]),
+    "mla_decode_sparse_fp4": (_c_int, [_p, _p, _c_float, _c_ll, _p, _c_int, _p, _p, _c_ll, _p, _c_int, _c_int, _c_int,
+                                       _c_float, _c_int, _p, _c_int, _p, _c_size, _p, _p, _p]),
     "mla_absorb_q": (_c_int, [_p, _c_ll, _p, _c_ll, _p, _p, _c_int, _c_int, _p]),
     "mla_absorb_q_rope": (_c_int, [_p, _c_ll, _p, _c_ll, _p, _c_float, _p, _p, _c_int, _c_int, _p]),
     "mla_absorb_plan_max_batch": (_c_int, []),
@@ -69,6 +74,8 @@ _SIGNATURES = {
                                   _c_int, _c_int, _c_float, _p]),
     "mla_cache_append_fp8": (_c_int, [_p, _c_ll, _p, _c_ll, _p, _c_float, _c_ll, _p, _c_int, _p, _p, _c_int, _c_int, _p,
                                       _c_ll, _p, _c_int, _c_int, _c_float, _p]),
+    "mla_cache_append_fp4": (_c_int, [_p, _c_ll, _p, _c_ll, _p, _c_float, _c_ll, _p, _c_int, _p, _p, _c_int, _c_int, _p,
+                                      _c_ll, _p, _c_int, _c_int, _c_float, _p, _c_float, _p]),
     "mla_attn_weights": (_c_int, [_p, _p, _p, _c_ll, _p, _c_int, _p, _c_int, _c_int, _c_int, _c_float, _c_int, _p, _c_ll,
                                   _p]),
     "mla_attn_weights_fp8": (_c_int, [_p, _p, _p, _c_float, _c_ll, _p, _c_int, _p, _c_int, _c_int, _c_int, _c_float,
@@ -373,6 +380,7 @@ def extend_chunked(q_nope: torch.Tensor, q_pe: torch.Tensor, w_uk: torch.Tensor,
 # The latent-cache calls.  The kernels read raw addresses, so a tensor of another type, shape or device must
 # not reach them; the checks are plain conditions (a decode step makes these calls for every layer).
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_FP4_ROW = 352   # bytes of a token in a 4-bit cache
 
 
 def _bad(name: str, what: str, wanted: str, t: torch.Tensor, dtype=None) -> Exception:
@@ -381,15 +389,19 @@ def _bad(name: str, what: str, wanted: str, t: torch.Tensor, dtype=None) -> Exce
                 f"{list(t.shape)} with strides {list(t.stride())} on {t.device}")
 
 
-def _paged(name: str, kv_cache: torch.Tensor, block_table: torch.Tensor, seqlens: torch.Tensor, fp8: bool):
+def _paged(name: str, kv_cache: torch.Tensor, block_table: torch.Tensor, seqlens: torch.Tensor, fp8: bool,
+           row: int = 576):
     """Checks a call's cache, table and lengths; returns (device index, B, num_blocks, max_blocks)."""
     dev = kv_cache.get_device()
     shape = kv_cache.shape
-    if fp8 and kv_cache.element_size() != 1:
+    if row == _FP4_ROW:
+        if kv_cache.dtype is not torch.uint8:
+            raise TypeError(f"{name}: kv_cache must be uint8 (rows of {row} bytes: E2M1 codes, their scales, E4M3 codes)")
+    elif fp8 and kv_cache.element_size() != 1:
         raise TypeError(f"{name}: kv_cache must hold one byte per value (E4M3 codes)")
-    if (dev < 0 or not (fp8 or kv_cache.dtype is _BF16) or len(shape) != 3 or shape[1] != 64 or shape[2] != 576
+    if (dev < 0 or not (fp8 or kv_cache.dtype is _BF16) or len(shape) != 3 or shape[1] != 64 or shape[2] != row
             or not kv_cache.is_contiguous()):
-        raise _bad(name, "kv_cache", "a contiguous [num_blocks, 64, 576]", kv_cache, None if fp8 else _BF16)
+        raise _bad(name, "kv_cache", f"a contiguous [num_blocks, 64, {row}]", kv_cache, None if fp8 else _BF16)
     if seqlens.dtype is not _I32 or seqlens.get_device() != dev or seqlens.dim() != 1 or not seqlens.is_contiguous():
         raise _bad(name, "seqlens", "a contiguous int32 [B]", seqlens, _I32)
     B = seqlens.numel()
@@ -480,8 +492,8 @@ def rope_axes(x: torch.Tensor, positions: torch.Tensor, sections=(32,), out: tor
 
 
 def _append(name, c, k_pe, kv_cache, kv_scale, block_table, seqlens, new_offsets, positions, sections, rope_theta,
-            interleaved, stream):
-    dev, B, num_blocks, max_blocks = _paged(name, kv_cache, block_table, seqlens, kv_scale is not None)
+            interleaved, stream, row=576, norm=()):
+    dev, B, num_blocks, max_blocks = _paged(name, kv_cache, block_table, seqlens, kv_scale is not None, row)
     shape, cs, ps = c.shape, c.stride(), k_pe.stride()
     if c.dtype is not _BF16 or c.get_device() != dev or len(shape) != 2 or shape[1] != 512 or cs[1] != 1:
         raise _bad(name, "c", "a bfloat16 [N, 512] with contiguous rows", c, _BF16)
@@ -494,13 +506,18 @@ def _append(name, c, k_pe, kv_cache, kv_scale, block_table, seqlens, new_offsets
                 or not new_offsets.is_contiguous()):
             raise _bad(name, "new_offsets", "a contiguous int32 [B + 1]", new_offsets, _I32)
         off = new_offsets.data_ptr()
+    if norm and norm[0] is not None:
+        w = norm[0]
+        if w.dtype is not _BF16 or w.get_device() != dev or w.shape != (512,) or not w.is_contiguous():
+            raise _bad(name, "norm_weight", "a contiguous bfloat16 [512]", w, _BF16)
+        norm = (w.data_ptr(), norm[1])
     if N == 0 or B == 0:
         return kv_cache
     rot = (None, 0, None, 0) if positions is None else _axes(name, positions, sections, N, dev)
     pool = (kv_cache.data_ptr(),) if kv_scale is None else (kv_cache.data_ptr(), kv_scale)
     _launch(dev, "mla_" + name, (
         c.data_ptr(), cs[0] if N > 1 else 512, k_pe.data_ptr(), ps[0] if N > 1 else 64, *pool, num_blocks,
-        block_table.data_ptr(), max_blocks, seqlens.data_ptr(), off, N, B, *rot, interleaved, rope_theta), stream)
+        block_table.data_ptr(), max_blocks, seqlens.data_ptr(), off, N, B, *rot, interleaved, rope_theta, *norm), stream)
     return kv_cache
 
 
@@ -520,6 +537,16 @@ def cache_append_fp8(c, k_pe, kv_cache, kv_scale: float, block_table, seqlens, n
     """cache_append into an FP8 cache: E4M3 codes of value / kv_scale (round to nearest even, saturating)."""
     return _append("cache_append_fp8", c, k_pe, kv_cache, kv_scale, block_table, seqlens, new_offsets, positions,
                    sections, rope_theta, interleaved, stream)
+
+
+def cache_append_fp4(c, k_pe, kv_cache, kv_scale: float, block_table, seqlens, new_offsets=None, positions=None,
+                     sections=(32,), rope_theta: float = 10000.0, interleaved: bool = False, norm_weight=None,
+                     norm_eps: float = 1e-6, stream=None) -> torch.Tensor:
+    """cache_append into a 4-bit cache (uint8 [num_blocks, 64, 352], see decode_fp4): E2M1 codes of the latent with an
+    E4M3 scale for 16 values, E4M3 codes of k_pe.  With norm_weight (bf16 [512]) the latent is normalised on the way:
+    c * rsqrt(mean(c^2) + norm_eps) * norm_weight."""
+    return _append("cache_append_fp4", c, k_pe, kv_cache, kv_scale, block_table, seqlens, new_offsets, positions,
+                   sections, rope_theta, interleaved, stream, _FP4_ROW, (norm_weight, norm_eps))
 
 
 def _weights(name, q, lse, kv_cache, kv_scale, block_table, seqlens, softmax_scale, causal, weights, stream):
@@ -602,6 +629,65 @@ def evict_fp8(kv_cache, block_table, seqlens, weights, budget: int, sink: int = 
     """evict over an FP8 cache (one byte a value)."""
     return _evict("evict_fp8", True, kv_cache, block_table, seqlens, weights, budget, sink, recent, arrival, width,
                   new_seqlens, kept, weights_out, arrival_out, stream)
+
+
+def _decode_fp4(name, q, kv_cache, kv_scale, block_table, seqlens, lists, softmax_scale, causal, metadata, parts, workspace,
+                out, lse, stream):
+    dev, B, num_blocks, max_blocks = _paged(name, kv_cache, block_table, seqlens, True, _FP4_ROW)
+    shape = q.shape
+    if (q.dtype is not _BF16 or q.get_device() != dev or len(shape) != 4 or shape[0] != B or shape[3] != 576
+            or not q.is_contiguous()):
+        raise _bad(name, "q", "a contiguous bfloat16 [B, s_q, H, 576]", q, _BF16)
+    s_q, H = shape[1], shape[2]
+    if lists:
+        indices, topk_lens = lists
+        if (indices.dtype is not _I32 or indices.get_device() != dev or indices.dim() != 2 or indices.shape[0] != B
+                or (indices.shape[1] > 1 and indices.stride(1) != 1)):
+            raise _bad(name, "indices", "an int32 [B, entries] with contiguous rows", indices, _I32)
+        if topk_lens.dtype is not _I32 or topk_lens.get_device() != dev or topk_lens.shape != (B,) or not topk_lens.is_contiguous():
+            raise _bad(name, "topk_lens", "a contiguous int32 [B]", topk_lens, _I32)
+        stride = indices.stride(0) if B > 1 else indices.shape[1]
+        if stride < indices.shape[1]:
+            raise ValueError(f"{name}: the rows of indices overlap")
+        lists = (indices.data_ptr(), stride, topk_lens.data_ptr())
+    if (metadata.dtype is not _I32 or metadata.get_device() != dev or not metadata.is_contiguous()
+            or metadata.numel() * 4 < metadata_size(B, parts)):
+        raise _bad(name, "metadata", "what decode_metadata returns for these lengths and parts", metadata, _I32)
+    if out is None:
+        out = _empty((B, s_q, H, 512), _BF16, q.device, stream)
+    elif out.dtype is not _BF16 or out.get_device() != dev or out.shape != (B, s_q, H, 512) or not out.is_contiguous():
+        raise _bad(name, "out", f"a contiguous bfloat16 [{B}, {s_q}, {H}, 512]", out, _BF16)
+    if lse is None:
+        lse = _empty((B, s_q, H), _F32, q.device, stream)
+    elif lse.dtype is not _F32 or lse.get_device() != dev or lse.shape != (B, s_q, H) or not lse.is_contiguous():
+        raise _bad(name, "lse", f"a contiguous float32 [{B}, {s_q}, {H}]", lse, _F32)
+    if q.numel() == 0:
+        return out, lse
+    if workspace is None:
+        workspace = _empty((decode_workspace_size(B, s_q, H, parts),), torch.uint8, q.device, stream)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise _bad(name, "workspace", "contiguous", workspace)
+    _launch(dev, "mla_" + name, (
+        q.data_ptr(), kv_cache.data_ptr(), kv_scale, num_blocks, block_table.data_ptr(), max_blocks, seqlens.data_ptr(),
+        *lists, B, s_q, H, softmax_scale, causal, metadata.data_ptr(), parts, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), out.data_ptr(), lse.data_ptr()), stream)
+    return out, lse
+
+
+def decode_fp4(q, kv_cache, kv_scale: float, block_table, seqlens, softmax_scale: float, causal: bool, metadata, parts: int,
+               workspace=None, out=None, lse=None, stream=None):
+    """Absorbed MLA decode over a 4-bit cache, uint8 [num_blocks, 64, 352]: of every token 512 E2M1 codes of the latent
+    (256 bytes), 32 E4M3 scales of 16 values each, 64 E4M3 codes of the RoPE key; a latent value is code * scale *
+    kv_scale, a RoPE value code * kv_scale.  Returns (out, lse) as decode."""
+    return _decode_fp4("decode_fp4", q, kv_cache, kv_scale, block_table, seqlens, (), softmax_scale, causal, metadata, parts,
+                       workspace, out, lse, stream)
+
+
+def decode_sparse_fp4(q, kv_cache, kv_scale: float, block_table, seqlens, indices, topk_lens, softmax_scale: float,
+                      causal: bool, metadata, parts: int, workspace=None, out=None, lse=None, stream=None):
+    """decode_sparse over a 4-bit cache (as in decode_fp4)."""
+    return _decode_fp4("decode_sparse_fp4", q, kv_cache, kv_scale, block_table, seqlens, (indices, topk_lens), softmax_scale,
+                       causal, metadata, parts, workspace, out, lse, stream)
 
 
 def get_device_status(stream=None) -> int:

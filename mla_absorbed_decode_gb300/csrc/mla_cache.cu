@@ -1,5 +1,5 @@
 // The latent cache over a request's life: RoPE with several position axes, the write of
-// new rows into the paged cache (bf16 or E4M3), and eviction by accumulated attention
+// new rows into the paged cache (bf16, E4M3 or 4 bits), and eviction by accumulated attention
 // weight.  C entries at the end (declared in mla.h).
 
 #include <cuda.h>
@@ -10,6 +10,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "mla_fp4.cuh"
 #include "mla_kernels.h"
 #include "mla_ptx.cuh"
 
@@ -116,6 +117,8 @@ struct AppendParams {
   int64_t pos_stride;
   float kv_scale, kv_inv;
   int* status;
+  const __nv_bfloat16* norm;   // 4-bit cache: [512] weights of the latent's norm, or nullptr
+  float norm_eps;
   RopeTable table;
 };
 
@@ -133,6 +136,27 @@ __device__ __forceinline__ int request_of(const int32_t* offsets, int B, int r, 
     lo = min(nlo, hi);
   }
   return lo - 1;
+}
+
+// The cached row (page and slot) that new row r goes to: of request b, whose rows end before row `end`.  -1: it belongs to
+// no request, or its token or page is out of range (reported).  All lanes of the warp agree.
+__device__ __forceinline__ int64_t append_target(const AppendParams& p, int r, int lane) {
+  int b, end;
+  if (p.offsets != nullptr) {
+    b = request_of(p.offsets, p.B, r, lane);
+    if (b < 0 || b >= p.B) return -1;
+    end = __ldg(p.offsets + b + 1);
+  } else {
+    b = r / p.rows_each;
+    end = (b + 1) * p.rows_each;
+  }
+  const int64_t t = static_cast<int64_t>(__ldg(p.seqlens + b)) - (end - r);
+  if (t >= 0 && t < static_cast<int64_t>(p.max_blocks) * kPageTokens) {
+    const int blk = __ldg(p.block_table + static_cast<int64_t>(b) * p.max_blocks + t / kPageTokens);
+    if (blk >= 0 && blk < p.num_blocks) return static_cast<int64_t>(blk) * kPageTokens + t % kPageTokens;
+  }
+  if (lane == 0) atomicCAS(p.status, 0, MLA_ERR_DEVICE_BOUNDS);
+  return -1;
 }
 
 // One warp per new row: 64 units of 8 latent values, lane l takes units l and l + 32, and 32 pairs of k_pe, a pair a
@@ -160,25 +184,8 @@ __global__ void __launch_bounds__(128) mla_append_kernel(const __grid_constant__
   const uint32_t pe = __ldg(reinterpret_cast<const uint32_t*>(p.pe + r * p.pe_row) + lane);
   int pos = 0;
   if (p.positions != nullptr) pos = __ldg(p.positions + s_axis[lane] * p.pos_stride + r);
-  int b, end;
-  if (p.offsets != nullptr) {
-    b = request_of(p.offsets, p.B, r, lane);
-    if (b < 0 || b >= p.B) return;
-    end = __ldg(p.offsets + b + 1);
-  } else {
-    b = r / p.rows_each;
-    end = (b + 1) * p.rows_each;
-  }
-  const int64_t t = static_cast<int64_t>(__ldg(p.seqlens + b)) - (end - r);
-  int64_t row = -1;
-  if (t >= 0 && t < static_cast<int64_t>(p.max_blocks) * kPageTokens) {
-    const int blk = __ldg(p.block_table + static_cast<int64_t>(b) * p.max_blocks + t / kPageTokens);
-    if (blk >= 0 && blk < p.num_blocks) row = static_cast<int64_t>(blk) * kPageTokens + t % kPageTokens;
-  }
-  if (row < 0) {
-    if (lane == 0) atomicCAS(p.status, 0, MLA_ERR_DEVICE_BOUNDS);
-    return;
-  }
+  const int64_t row = append_target(p, r, lane);
+  if (row < 0) return;
   float x0 = bf16_lo(pe), x1 = bf16_hi(pe);
   if (p.positions != nullptr) {
     const float2 turn = rope_turn(p.table, s_hi[lane], s_lo[lane], pos);
@@ -205,6 +212,76 @@ __global__ void __launch_bounds__(128) mla_append_kernel(const __grid_constant__
     reinterpret_cast<uint4*>(dst)[32 + lane] = c1;
     reinterpret_cast<uint32_t*>(dst + kDimV)[lane] = p.positions != nullptr ? pack_bf16x2(x0, x1) : pe;
   }
+}
+
+// A row of the 4-bit cache (mla_fp4.cuh) from one new row, one warp a row: a lane has one group of 16 latent values, which
+// it normalises, scales and rounds, and one pair of k_pe.
+//   y = c, or c * rsqrt(mean(c^2) + eps) * w;  scale = E4M3(max|y| / (6 kv_scale));  code = E2M1(y / (scale kv_scale))
+// The quotients are IEEE divisions in fp32 (a reciprocal's last bit would move codes that lie halfway); values of a
+// group whose scale rounds to 0 are stored as 0.
+template <bool Norm>
+__global__ void __launch_bounds__(128) mla_append_fp4_kernel(const __grid_constant__ AppendParams p) {
+  __shared__ float s_hi[kPairs], s_lo[kPairs];
+  __shared__ int s_axis[kPairs];
+  const int lane = threadIdx.x & 31;
+  if (p.positions != nullptr && threadIdx.x < kPairs) {
+    s_hi[lane] = p.table.hi[lane];
+    s_lo[lane] = p.table.lo[lane];
+    s_axis[lane] = p.table.axis[lane];
+  }
+  __syncthreads();
+  griddep_wait();
+  griddep_launch_dependents();
+  const int r = blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (r >= p.N) return;
+  const uint4* c = reinterpret_cast<const uint4*>(p.c + r * p.c_row) + 2 * lane;
+  const uint4 c0 = __ldg(c), c1 = __ldg(c + 1);
+  const uint32_t pe = __ldg(reinterpret_cast<const uint32_t*>(p.pe + r * p.pe_row) + lane);
+  int pos = 0;
+  if (p.positions != nullptr) pos = __ldg(p.positions + s_axis[lane] * p.pos_stride + r);
+  uint4 w0 = {}, w1 = {};
+  if constexpr (Norm) {
+    w0 = __ldg(reinterpret_cast<const uint4*>(p.norm) + 2 * lane);
+    w1 = __ldg(reinterpret_cast<const uint4*>(p.norm) + 2 * lane + 1);
+  }
+  const int64_t row = append_target(p, r, lane);
+  if (row < 0) return;
+  float x0 = bf16_lo(pe), x1 = bf16_hi(pe);
+  if (p.positions != nullptr) {
+    const float2 turn = rope_turn(p.table, s_hi[lane], s_lo[lane], pos);
+    const float y0 = fmaf(x0, turn.x, -x1 * turn.y), y1 = fmaf(x0, turn.y, x1 * turn.x);
+    x0 = y0, x1 = y1;
+  }
+  const uint32_t cw[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+  float y[16];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[2 * i] = bf16_lo(cw[i]), y[2 * i + 1] = bf16_hi(cw[i]);
+  if constexpr (Norm) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) ss = fmaf(y[i], y[i], ss);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float inv = rsqrtf(ss * (1.f / kDimV) + p.norm_eps);
+    const uint32_t ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[2 * i] = y[2 * i] * inv * bf16_lo(ww[i]), y[2 * i + 1] = y[2 * i + 1] * inv * bf16_hi(ww[i]);
+  }
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) amax = max_nan(amax, fabsf(y[i]));
+  const uint32_t scale = cvt_e4m3x2(__fdiv_rn(amax, 6.f * p.kv_scale), 0.f) & 0xFFu;
+  const float step = e4m3x2_to_float2(scale).x * p.kv_scale;
+  uint32_t code[2] = {0u, 0u};
+  if (step > 0.f)   // (no group whose scale is 0 or NaN)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      code[i >> 2] |= cvt_e2m1x2(__fdiv_rn(y[2 * i], step), __fdiv_rn(y[2 * i + 1], step)) << (8 * (i & 3));
+  uint8_t* dst = static_cast<uint8_t*>(p.kv) + row * kFp4RowBytes;
+  *reinterpret_cast<uint2*>(dst + 8 * lane) = make_uint2(code[0], code[1]);
+  dst[kFp4Scales + lane] = static_cast<uint8_t>(scale);
+  *reinterpret_cast<uint16_t*>(dst + kFp4Rope + 2 * lane) =
+      static_cast<uint16_t>(cvt_e4m3x2(__fdiv_rn(x0, p.kv_scale), __fdiv_rn(x1, p.kv_scale)));
 }
 
 // ------------------------------------------------------------------ evict --
@@ -639,11 +716,15 @@ bool rope_table(const int32_t* sections, int n_axes, int interleaved, float thet
   return true;
 }
 
+enum class CacheFormat { kBf16, kFp8, kFp4 };
+
 mla_status_t append_impl(const mla_bf16_t* c, int64_t c_row_stride, const mla_bf16_t* k_pe, int64_t k_pe_row_stride,
-                         void* kv_cache, bool fp8, float kv_scale, int64_t num_blocks, const int32_t* block_table,
-                         int max_blocks, const int32_t* seqlens, const int32_t* new_offsets, int N, int B,
-                         const int32_t* positions, int64_t positions_stride, const int32_t* sections, int n_axes,
-                         int interleaved, float rope_theta, mla_stream_t stream) {
+                         void* kv_cache, CacheFormat format, float kv_scale, int64_t num_blocks,
+                         const int32_t* block_table, int max_blocks, const int32_t* seqlens, const int32_t* new_offsets,
+                         int N, int B, const int32_t* positions, int64_t positions_stride, const int32_t* sections,
+                         int n_axes, int interleaved, float rope_theta, mla_stream_t stream,
+                         const mla_bf16_t* norm_weight = nullptr, float norm_eps = 0.f) {
+  const bool fp8 = format == CacheFormat::kFp8, fp4 = format == CacheFormat::kFp4;
   if (!c || !k_pe || !kv_cache || !block_table || !seqlens || N < 1 || B < 1 || num_blocks < 1 || max_blocks < 1)
     return MLA_ERR_INVALID_ARG;
   if (!aligned(c, 16) || !aligned(k_pe, 16) || !aligned(kv_cache, 16) || !aligned(block_table, 4) ||
@@ -652,7 +733,9 @@ mla_status_t append_impl(const mla_bf16_t* c, int64_t c_row_stride, const mla_bf
   if (c_row_stride < kDimV || c_row_stride % 8 || k_pe_row_stride < 64 || k_pe_row_stride % 8)
     return MLA_ERR_INVALID_ARG;
   if (!new_offsets && N % B) return MLA_ERR_INVALID_ARG;
-  if (fp8 && (!std::isfinite(kv_scale) || !(kv_scale > 0.f))) return MLA_ERR_INVALID_ARG;
+  if ((fp8 || fp4) && (!std::isfinite(kv_scale) || !(kv_scale > 0.f))) return MLA_ERR_INVALID_ARG;
+  if (fp4 && !fp4_scale_ok(kv_scale)) return MLA_ERR_INVALID_ARG;
+  if (norm_weight && (!aligned(norm_weight, 16) || !std::isfinite(norm_eps) || !(norm_eps >= 0.f))) return MLA_ERR_INVALID_ARG;
   AppendParams p = {};
   if (positions && (positions_stride < N || !rope_table(sections, n_axes, interleaved, rope_theta, &p.table)))
     return MLA_ERR_INVALID_ARG;
@@ -677,12 +760,16 @@ mla_status_t append_impl(const mla_bf16_t* c, int64_t c_row_stride, const mla_bf
   p.kv_inv = 1.f / kv_scale;
   int exponent = 0;
   const bool divide = std::frexp(kv_scale, &exponent) != 0.5f || !std::isnormal(p.kv_inv);   // no power of two
+  p.norm = reinterpret_cast<const __nv_bfloat16*>(norm_weight);
+  p.norm_eps = norm_eps;
   p.status = device_status_word();
   if (!p.status) return MLA_ERR_CUDA;
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = pdl_config(dim3(static_cast<unsigned>((N + 3) / 4)), dim3(128), 0,
                                             reinterpret_cast<cudaStream_t>(stream), attr);
-  const cudaError_t e = !fp8    ? cudaLaunchKernelEx(&cfg, mla_append_kernel<false, false>, p)
+  const cudaError_t e = fp4      ? (norm_weight ? cudaLaunchKernelEx(&cfg, mla_append_fp4_kernel<true>, p)
+                                                : cudaLaunchKernelEx(&cfg, mla_append_fp4_kernel<false>, p))
+                        : !fp8   ? cudaLaunchKernelEx(&cfg, mla_append_kernel<false, false>, p)
                         : divide ? cudaLaunchKernelEx(&cfg, mla_append_kernel<true, true>, p)
                                  : cudaLaunchKernelEx(&cfg, mla_append_kernel<true, false>, p);
   return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
@@ -833,7 +920,7 @@ mla_status_t mla_cache_append(const mla_bf16_t* c, int64_t c_row_stride, const m
                               const int32_t* new_offsets, int N, int B, const int32_t* positions,
                               int64_t positions_stride, const int32_t* sections, int n_axes, int interleaved,
                               float rope_theta, mla_stream_t stream) {
-  return append_impl(c, c_row_stride, k_pe, k_pe_row_stride, kv_cache, false, 1.f, num_blocks, block_table, max_blocks,
+  return append_impl(c, c_row_stride, k_pe, k_pe_row_stride, kv_cache, CacheFormat::kBf16, 1.f, num_blocks, block_table, max_blocks,
                      seqlens, new_offsets, N, B, positions, positions_stride, sections, n_axes, interleaved, rope_theta,
                      stream);
 }
@@ -844,9 +931,20 @@ mla_status_t mla_cache_append_fp8(const mla_bf16_t* c, int64_t c_row_stride, con
                                   const int32_t* new_offsets, int N, int B, const int32_t* positions,
                                   int64_t positions_stride, const int32_t* sections, int n_axes, int interleaved,
                                   float rope_theta, mla_stream_t stream) {
-  return append_impl(c, c_row_stride, k_pe, k_pe_row_stride, kv_cache, true, kv_scale, num_blocks, block_table,
-                     max_blocks, seqlens, new_offsets, N, B, positions, positions_stride, sections, n_axes, interleaved,
-                     rope_theta, stream);
+  return append_impl(c, c_row_stride, k_pe, k_pe_row_stride, kv_cache, CacheFormat::kFp8, kv_scale, num_blocks,
+                     block_table, max_blocks, seqlens, new_offsets, N, B, positions, positions_stride, sections, n_axes,
+                     interleaved, rope_theta, stream);
+}
+
+mla_status_t mla_cache_append_fp4(const mla_bf16_t* c, int64_t c_row_stride, const mla_bf16_t* k_pe,
+                                  int64_t k_pe_row_stride, uint8_t* kv_cache, float kv_scale, int64_t num_blocks,
+                                  const int32_t* block_table, int max_blocks, const int32_t* seqlens,
+                                  const int32_t* new_offsets, int N, int B, const int32_t* positions,
+                                  int64_t positions_stride, const int32_t* sections, int n_axes, int interleaved,
+                                  float rope_theta, const mla_bf16_t* norm_weight, float norm_eps, mla_stream_t stream) {
+  return append_impl(c, c_row_stride, k_pe, k_pe_row_stride, kv_cache, CacheFormat::kFp4, kv_scale, num_blocks,
+                     block_table, max_blocks, seqlens, new_offsets, N, B, positions, positions_stride, sections, n_axes,
+                     interleaved, rope_theta, stream, norm_weight, norm_eps);
 }
 
 mla_status_t mla_evict(mla_bf16_t* kv_cache, int64_t num_blocks, const int32_t* block_table, int max_blocks,

@@ -19,6 +19,7 @@ checks), written for a reader to check against the pages by eye:
 * ``cache.py``    -- the latent-cache operators: rotation with several position axes,
                     the write of new rows, the attention weight of cached tokens,
                     eviction by it.
+* ``fp4.py``      -- the 4-bit latent cache: what its bytes stand for, which bytes a row becomes.
 * ``schedule.py`` -- a restatement of the split-KV schedule rule and the
                     invariants any valid schedule must satisfy.
 
@@ -35,5 +36,8 @@ from .mla import (  # noqa: F401
 )
 from .cache import (  # noqa: F401
     axis_of_pairs, rope_axes, append_slots, append_rows, attn_weights, evict,
+)
+from .fp4 import (  # noqa: F401
+    E2M1_VALUES, E2M1_MIDDLES, e2m1_round, pack_fp4, unpack_fp4, normed_latent,
 )
 from .schedule import schedule_reference, check_schedule  # noqa: F401
