@@ -120,14 +120,15 @@ mla_combine_kernel(const float* o_part, const float* lse_part, const int32_t* nu
       }
     }
   }
-  const float inv = z > 0.f ? 1.f / z : 0.f;
+  // (z is NaN where a partial lse is +inf: a row of NaN in the 4-bit decode)
+  const float inv = z == 0.f ? 0.f : 1.f / z;
   uint4 u[2];
   uint32_t* w = reinterpret_cast<uint32_t*>(u);
 #pragma unroll
   for (int j = 0; j < 8; ++j) w[j] = pack_bf16x2(acc[2 * j] * inv, acc[2 * j + 1] * inv);
   reinterpret_cast<uint4*>(orow)[0] = u[0];
   reinterpret_cast<uint4*>(orow)[1] = u[1];
-  if (lane == 0) lse[static_cast<int64_t>(b) * rows + g] = z > 0.f ? m + logf(z) : -INFINITY;
+  if (lane == 0) lse[static_cast<int64_t>(b) * rows + g] = z == 0.f ? -INFINITY : m + logf(z);
 }
 
 // -------------------------------------------------------------------- bmm --

@@ -273,10 +273,11 @@ __global__ void __launch_bounds__(128) mla_append_fp4_kernel(const __grid_consta
   const uint32_t scale = cvt_e4m3x2(__fdiv_rn(amax, 6.f * p.kv_scale), 0.f) & 0xFFu;
   const float step = e4m3x2_to_float2(scale).x * p.kv_scale;
   uint32_t code[2] = {0u, 0u};
-  if (step > 0.f)   // (no group whose scale is 0 or NaN)
+  if (step > 0.f) {   // (no group whose scale is 0 or NaN)
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       code[i >> 2] |= cvt_e2m1x2(__fdiv_rn(y[2 * i], step), __fdiv_rn(y[2 * i + 1], step)) << (8 * (i & 3));
+  }
   uint8_t* dst = static_cast<uint8_t*>(p.kv) + row * kFp4RowBytes;
   *reinterpret_cast<uint2*>(dst + 8 * lane) = make_uint2(code[0], code[1]);
   dst[kFp4Scales + lane] = static_cast<uint8_t>(scale);

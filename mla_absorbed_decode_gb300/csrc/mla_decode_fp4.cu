@@ -1,5 +1,32 @@
-// Absorbed MLA decode over the 4-bit latent cache (mla_fp4.cuh): dense and over lists of tokens.
+// Absorbed MLA decode over the 4-bit latent cache (mla_fp4.cuh): dense, and over lists of tokens.
 // C entries at the end (declared in mla.h).
+//
+//   s_t = scale * <q, kv_t>,  p_t = exp(s_t - max),  out = sum_t p_t kv_t[0:512] / sum_t p_t,  lse = ln sum_t exp(s_t)
+//
+// for every query row (head and query position) of a request, whose rows share the cached tokens.  A token is 352 bytes, and
+// 2176 FLOP per row: at 128 rows 791 FLOP/B, so the tensor pipes bound it, not HBM.  The codes become fp16 on the
+// way to them (code * scale is exact there; kv_scale goes into the scores and the output), and the work of a 128-row block is
+// split over a CTA pair, because an output accumulator of 128 x 512 takes all of one SM's TMEM:
+//   * the S-CTA (even cluster rank) computes S^T = K Q^T in tiles of 128 tokens (two pages): tokens on the TMEM lanes, so that
+//     the converted keys go from the converting threads' registers straight into TMEM as the MMA's A operand (a thread
+//     a token) and never through shared memory, whose bandwidth the operands need; Q is the B operand, in
+//     shared memory for a whole segment.  An MMA is as wide as there are heads (rounded up to 16), so few heads cost little.
+//     S^T is read with four tokens and 16 heads in a thread, which keeps the heads' running maxima and sums in registers;
+//     P^T goes to the partner with one shared-to-shared bulk copy a tile and warpgroup;
+//   * the O-CTA (odd rank) converts the latent part of the pages into shared memory (they hit L2 behind the S-CTA's loads) and
+//     accumulates O += P V, P^T and V both read by the MMA as they lie (tokens by rows: transposed operands).
+// Rows past 128 go to further pairs of the cluster, which walk the same pages.  A cluster is one part of the split schedule.
+//
+// The softmax is online, with the reference maximum of a head raised only where a score passes it by 2^8: the threads take the
+// exponentials against the old reference, and a vote (the barrier that ends a tile anyhow) tells whether one overflowed its room;
+// only then the tile is done again with new references, and O rescaled.  P is fp16 with an offset of 2^6, so that everything down to
+// 2^-20 of the reference keeps 11 bits.
+//
+// q is bf16 and K fp16, and an MMA takes one type: each row of q is multiplied by a power of two that brings its largest
+// element into [2^14, 2^15) and rounded to fp16, which is exact for elements down to 2^-31 of the largest.
+//
+// Every barrier wait is bounded; on expiry the CTA records MLA_ERR_TIMEOUT, raises an abort flag in every CTA of its cluster,
+// drains what it has in flight and leaves.
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -7,7 +34,9 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <climits>
 #include <cmath>
+#include <mutex>
 
 #include "mla_fp4.cuh"
 #include "mla_kernels.h"
@@ -16,98 +45,1218 @@
 namespace mla {
 namespace {
 
-constexpr int kTile = 32, kRowsCta = 8, kStride = kDimQK + 1;
-constexpr size_t kSmem = sizeof(float) * (kTile * kStride + kRowsCta * kDimQK + kRowsCta * kTile + kRowsCta);
+constexpr int kThreads = 640;   // warps 0..3: loads, MMAs, copies; 4..11: softmax or rescale and epilogue; 12..19: conversion
+constexpr int kTile = 128;      // tokens of a tile: two pages
+constexpr uint32_t kPageBytes = kPageTokens * kFp4RowBytes;
+constexpr uint32_t kQChunk = 128 * 128;       // 64 dims of the row block's q: up to 128 rows of 128 bytes, swizzled
+constexpr uint32_t kVChunk = 64 * 128;        // 64 dims of a page's values
+constexpr int kVSlots = 4;                    // half pages (64 tokens x 256 dims) of converted values
+constexpr uint32_t kVSlot = 4 * kVChunk;
+constexpr int kKSlots = 8;                    // TMEM slots of converted keys: 128 tokens x 64 dims, 32 columns
+constexpr int kItems = 9;                     // of them a tile
+// a packet: what one softmax warpgroup (half of the row block's heads) sends to the O-CTA for a tile
+constexpr uint32_t kPktAlpha = 128 * 128;     // after P^T (128 tokens x 64 heads): float[64], factors of a rebase
+constexpr uint32_t kPktInvL = kPktAlpha + 256;   // float[64], the output's factors (last tile of a segment)
+constexpr uint32_t kPktFlag = kPktInvL + 256;    // whether alpha counts
+constexpr uint32_t kPktBytes = kPktFlag + 16;
+constexpr uint32_t kPktStride = 17 * 1024;
+constexpr uint32_t kKCol = 256;               // S-CTA's TMEM columns: S^T of two tiles at 0 and 128, the keys from 256
+constexpr float kOffset = 6.f;                // P is taken against 2^-6 of the reference maximum
+constexpr float kTop = kOffset + 8.f;         // an exponent past this rebases its head
+constexpr uint64_t kTimeoutNs = 500ull * 1000 * 1000;
+constexpr float kLn2 = 0.69314718055994530942f;
+// registers a thread: the three kinds of warpgroups share what the launch gets (640 x 96)
+constexpr int kRegsMisc = 64, kRegsSoftmax = 120, kRegsConvert = 88;
+static_assert(128 * kRegsMisc + 256 * kRegsSoftmax + 256 * kRegsConvert <= kThreads * 96, "more would wait forever");
 
-// A CTA takes eight query rows of a request past its tokens, 32 at a time, values as fp32 in shared memory.
-__global__ void __launch_bounds__(256) mla_decode_fp4_kernel(const __grid_constant__ DecodeParams p) {
-  extern __shared__ float sm[];
-  float* k = sm;
-  float* q = k + kTile * kStride;
-  float* pr = q + kRowsCta * kDimQK;
-  float* alpha = pr + kRowsCta * kTile;
-  griddep_wait();
-  const int b = blockIdx.y, g0 = blockIdx.x * kRowsCta, tid = threadIdx.x, row = tid >> 5, lane = tid & 31;
-  const int g = g0 + row;
-  for (int i = tid; i < kRowsCta * kDimQK; i += 256) {
-    const int r = g0 + i / kDimQK;
-    q[i] = r < p.rows ? __bfloat162float(p.q[(static_cast<int64_t>(b) * p.rows + r) * kDimQK + i % kDimQK]) : 0.f;
+
+// shared memory (offsets from a 1024-byte aligned base)
+constexpr uint32_t kOffSend = 9 * kQChunk;                   // S-CTA: q first, then a packet of each warpgroup
+constexpr uint32_t kOffRaw = kOffSend + 2 * kPktStride;      // S-CTA: the two pages of a tile as cached
+constexpr uint32_t kOffV = 4 * kPktStride;                   // O-CTA: the packets of two tiles first, then values
+constexpr uint32_t kOffEpi = kOffV + kVSlots * kVSlot;       // O-CTA: 2 KiB transpose buffer per epilogue warp
+constexpr uint32_t kOffInvL = kOffEpi + 8 * 2048;            // O-CTA: output factors of the segment [2][64]
+constexpr uint32_t kOffShared = kOffRaw + 2 * kPageBytes;
+static_assert(kOffInvL + 512 <= kOffShared, "O-CTA layout");
+
+struct Shared {
+  // S-CTA
+  uint64_t raw_full[2], raw_empty[2];         // a page of the tile has landed; is in the converters' registers
+  uint64_t k_full[kKSlots], k_empty[kKSlots];
+  uint64_t s_full[2], s_empty[2];
+  uint64_t q_full;                            // the segment's q is in place (a softmax warp each)
+  uint64_t p_ready[2], st_free[2];            // a warpgroup's packet is written; has been read by its copy
+  uint64_t credit[2];                         // the partner's receive slot is free (remote)
+  // O-CTA
+  uint64_t p_full[2], p_free[2];
+  uint64_t v_full[kVSlots], v_empty[kVSlots];
+  uint64_t o_full, o_free, o_sync, corr_go, corr_done;
+  uint64_t drain;                             // both
+  uint32_t tmem_base;
+  volatile int abort;
+  int cmd, cmd_arg;                           // O-CTA: 1 = rescale (by the packets of slot cmd_arg), 2 = epilogue, 3 = leave
+  float q_scale[128];                         // S-CTA: raw score -> log2 units, by column
+  float part[2][4][64];                       // a warpgroup's maxima or sums by warp and head
+  float ref[2][64];
+  uint16_t pos[128];                          // a column's query position
+};
+constexpr uint32_t kSmemBytes = kOffShared + sizeof(Shared);
+static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+
+// ------------------------------------------------------------------ waits --
+__device__ __forceinline__ void raise_abort(Shared& sh, int* status, int code, uint32_t cl) {
+  if (!sh.abort) {
+    atomicCAS(status, 0, code);
+    for (uint32_t r = 0; r < cl; ++r) st_cluster_u32(map_to_rank(smem_u32(const_cast<int*>(&sh.abort)), r), 1u);
   }
-  const int n = p.lens[b], len = p.seqlens[b];
-  const int last = p.causal ? len - p.s_q + (g < p.rows ? g / p.H : 0) : len - 1;   // the row sees positions up to here
-  float acc[kRowsCta][2] = {};
-  float m = -INFINITY, l = 0.f;
-  for (int t0 = 0; t0 < n; t0 += kTile) {
-    __syncthreads();
-    for (int j = row; j < kTile; j += 8) {   // a warp a token
-      const int e = t0 + j;
-      int64_t at = -1;
-      if (e < n) {
-        int t = e;
-        if (p.indices) t = e < p.idx_stride ? p.indices[b * p.idx_stride + e] : -1;
-        if (t >= 0 && t < len && t / kPageTokens < p.max_blocks) {
-          const int blk = p.block_table[static_cast<int64_t>(b) * p.max_blocks + t / kPageTokens];
-          if (blk >= 0 && blk < p.num_blocks) at = static_cast<int64_t>(blk) * kPageTokens + t % kPageTokens;
-        }
-        if (at < 0 && lane == 0) atomicCAS(p.status, 0, MLA_ERR_DEVICE_BOUNDS);
-      }
-      const uint8_t* src = reinterpret_cast<const uint8_t*>(p.kv) + at * kFp4RowBytes;
-      float* dst = k + j * kStride;
-      for (int i = lane; i < kDimQK; i += 32) {
-        float v = 0.f;
-        if (at >= 0 && i < kDimV) {
-          const uint32_t pair = e2m1x2_to_f16x2<0>(src[i / 2]);
-          const __half2 h = *reinterpret_cast<const __half2*>(&pair);
-          v = (i & 1 ? __high2float(h) : __low2float(h)) * e4m3x2_to_float2(src[kFp4Scales + i / kFp4Group]).x;
-        } else if (at >= 0) {
-          v = e4m3x2_to_float2(src[kFp4Rope + i - kDimV]).x;
-        }
-        dst[i] = v;
-      }
-    }
-    __syncthreads();
-    {
-      const int e = t0 + lane;
-      float s = -INFINITY;
-      int t = e;
-      if (p.indices && e < n) t = e < p.idx_stride ? p.indices[b * p.idx_stride + e] : -1;
-      if (e < n && g < p.rows && t <= last) {
-        s = 0.f;
-        for (int i = 0; i < kDimQK; ++i) s = fmaf(q[row * kDimQK + i], k[lane * kStride + i], s);
-        s *= p.scale_log2 * p.kv_scale;
-      }
-      float mx = s;
-      for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const float m_new = fmaxf(m, mx), ref = m_new == -INFINITY ? 0.f : m_new;
-      const float e2 = exp2f(s - ref);
-      float sum = e2;
-      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      const float a = exp2f(m - ref);
-      l = l * a + sum;
-      m = m_new;
-      pr[row * kTile + lane] = e2;
-      if (lane == 0) alpha[row] = a;
-    }
-    __syncthreads();
-    for (int r = 0; r < kRowsCta; ++r) acc[r][0] *= alpha[r], acc[r][1] *= alpha[r];
-    for (int j = 0; j < min(kTile, n - t0); ++j) {
-      const float v0 = k[j * kStride + 2 * tid], v1 = k[j * kStride + 2 * tid + 1];
-      for (int r = 0; r < kRowsCta; ++r) acc[r][0] += pr[r * kTile + j] * v0, acc[r][1] += pr[r * kTile + j] * v1;
+  sh.abort = 1;
+}
+__device__ __forceinline__ bool wait_slow(Shared& sh, uint32_t bar, uint32_t parity, int* status, uint32_t cl, bool cluster) {
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    if (cluster ? mbar_test_cluster(bar, parity) : mbar_test(bar, parity)) return true;
+    if (sh.abort) return false;
+    if (global_timer_ns() - t0 > kTimeoutNs) {
+      raise_abort(sh, status, MLA_ERR_TIMEOUT, cl);
+      return false;
     }
   }
-  __syncthreads();
+}
+// Bounded wait; false on abort or timeout (after raising the abort).
+__device__ __forceinline__ bool wait_bar(Shared& sh, uint64_t& b, uint32_t parity, int* status, uint32_t cl,
+                                         bool cluster = false) {
+  const uint32_t bar = smem_u32(&b);
+  if (cluster ? mbar_test_cluster(bar, parity) : mbar_test(bar, parity)) return true;
+  return wait_slow(sh, bar, parity, status, cl, cluster);
+}
+// The same by all lanes, with one answer.
+__device__ __forceinline__ bool warp_wait(Shared& sh, uint64_t& b, uint32_t parity, int* status, uint32_t cl,
+                                          bool cluster = false) {
+  return __all_sync(0xffffffffu, wait_bar(sh, b, parity, status, cl, cluster));
+}
+// Bounded wait that ignores the abort flag: for what is in flight.
+__device__ __forceinline__ void drain_bar(uint64_t& b, uint32_t parity) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_test(smem_u32(&b), parity))
+    if (global_timer_ns() - t0 > kTimeoutNs) return;
+}
+__device__ __forceinline__ void arrive(uint64_t& b) { mbar_arrive(smem_u32(&b)); }
+__device__ __forceinline__ void arrive2(uint64_t& b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], 2;" :: "r"(smem_u32(&b)) : "memory");
+}
+
+// ------------------------------------------------------------ instructions --
+template <int R>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(R)); }
+template <int R>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(R)); }
+// `bytes` (a multiple of 16, both addresses 16-byte aligned) of global memory into shared memory.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t& bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               :: "r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(&bar)) : "memory");
+}
+// 32 (x4) or 16 (x2) columns of 16 TMEM lanes: lane l of the warp gets, in r[4 n + 2 h + e], row 8 h + l / 4, column
+// 8 n + 2 (l % 4) + e.
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, float (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+        "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, float (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+      : "r"(taddr));
+}
+// Four 8 x 8 matrices of 16-bit elements: register m of lane l has row l / 4, columns 2 (l % 4) and the next, of matrix m, whose
+// row r goes to the 16 bytes at lane 8 m + r's address.
+__device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};"
+               :: "r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+// Two floats an instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// kind::f16 with fp16 inputs and fp32 accumulation (the bf16 descriptor without its two type bits).
+__device__ __forceinline__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn, int b_mn) {
+  return idesc_bf16_f32(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
+}
+// 16 latent values (two words of codes) as fp16 pairs; `scale` twice in a word.
+__device__ __forceinline__ void values16(uint32_t w0, uint32_t w1, uint32_t scale, uint32_t* v) {
+  v[0] = mul_f16x2(e2m1x2_to_f16x2<0>(w0), scale);
+  v[1] = mul_f16x2(e2m1x2_to_f16x2<1>(w0), scale);
+  v[2] = mul_f16x2(e2m1x2_to_f16x2<2>(w0), scale);
+  v[3] = mul_f16x2(e2m1x2_to_f16x2<3>(w0), scale);
+  v[4] = mul_f16x2(e2m1x2_to_f16x2<0>(w1), scale);
+  v[5] = mul_f16x2(e2m1x2_to_f16x2<1>(w1), scale);
+  v[6] = mul_f16x2(e2m1x2_to_f16x2<2>(w1), scale);
+  v[7] = mul_f16x2(e2m1x2_to_f16x2<3>(w1), scale);
+}
+
+// ------------------------------------------------------------------- walk --
+struct Segment {
+  int b, kb, ke, split;   // request, page range, split index within the request
+};
+
+// Walks the segments of one part in order (the same walk in every role).
+struct SegmentWalker {
+  const DecodeParams* p;
+  int b_last, k_end, b, kb, split0;
+  bool first, done;
+  __device__ void init(const DecodeParams& prm, int part) {
+    p = &prm;
+    const int* m = prm.meta + part * kMetaInts;
+    b = m[0];
+    kb = m[1];
+    b_last = m[2];
+    k_end = m[3];
+    split0 = m[4];
+    first = true;
+    done = b < 0;
+    // a record that does not fit this call would send the walk past the caller's buffers: reported, and nothing walked
+    if (!done && (b >= prm.B || b_last < b || b_last >= prm.B || kb < 0 || k_end < 0 || split0 < 0)) {
+      atomicCAS(prm.status, 0, MLA_ERR_DEVICE_BOUNDS);
+      done = true;
+    }
+  }
+  __device__ bool next(Segment& s) {
+    while (!done) {
+      if (b > b_last) {
+        done = true;
+        break;
+      }
+      const int L = __ldg(p->lens + b);
+      const int nb = L > 0 ? (L - 1) / kPageTokens + 1 : 0;
+      const int k0 = first ? kb : 0;
+      const int k1 = b == b_last ? min(k_end, nb) : nb;
+      const int sp = first ? split0 : 0;
+      first = false;
+      const int cur = b++;
+      if (k1 > k0) {
+        s.b = cur, s.kb = k0, s.ke = k1, s.split = sp;
+        return true;
+      }
+    }
+    return false;
+  }
+};
+
+__device__ __forceinline__ int tiles_of(const Segment& s) { return (s.ke - s.kb + 1) >> 1; }
+// Listed tokens of the tile that starts at page k.
+__device__ __forceinline__ int tile_tokens(const DecodeParams& p, const Segment& s, int k) {
+  return min(min(kTile, (s.ke - k) * kPageTokens), __ldg(p.lens + s.b) - k * kPageTokens);
+}
+
+// Walks the pages of one part.
+struct PageIter {
+  SegmentWalker w;
+  Segment s;
+  int k;
+  bool valid;
+  __device__ void init(const DecodeParams& p, int part) {
+    w.init(p, part);
+    valid = w.next(s);
+    k = valid ? s.kb : 0;
+  }
+  __device__ void advance() {
+    if (valid && ++k >= s.ke) {
+      valid = w.next(s);
+      k = valid ? s.kb : 0;
+    }
+  }
+};
+
+// Whether split slot `slot` lies in the workspace, which holds B + num_parts; one outside (metadata that does not fit the
+// call) is reported and not written.
+__device__ __forceinline__ bool split_slot_ok(const DecodeParams& p, int slot) {
+  if (slot >= 0 && slot < p.B + p.num_parts) return true;
+  atomicCAS(p.status, 0, MLA_ERR_DEVICE_BOUNDS);
+  return false;
+}
+
+// Page number of page k of request b; one that is out of range is reported, and page 0 read in its place.
+__device__ __forceinline__ int page_of(const DecodeParams& p, int b, int k) {
+  int blk = -1;
+  if (k < p.max_blocks) blk = __ldg(p.block_table + static_cast<int64_t>(b) * p.max_blocks + k);
+  if (blk >= 0 && blk < p.num_blocks) return blk;
+  atomicCAS(p.status, 0, MLA_ERR_DEVICE_BOUNDS);
+  return 0;
+}
+// Position of list entry e of request b; -1 where the row of indices ends before it (reported).
+__device__ __forceinline__ int entry_of(const DecodeParams& p, int b, int e) {
+  if (e < p.idx_stride) return __ldg(p.indices + static_cast<int64_t>(b) * p.idx_stride + e);
+  atomicCAS(p.status, 0, MLA_ERR_DEVICE_BOUNDS);
+  return -1;
+}
+// Its page; -1 where the position is none of the request's (reported).
+__device__ __forceinline__ int entry_page(const DecodeParams& p, int b, int t) {
+  if (t >= 0 && t < __ldg(p.seqlens + b)) return page_of(p, b, t / kPageTokens);
+  atomicCAS(p.status, 0, MLA_ERR_DEVICE_BOUNDS);
+  return -1;
+}
+// The cached row of a token; row 0 for a bad one, which is always there.
+__device__ __forceinline__ const uint8_t* row_at(const DecodeParams& p, int t, int blk) {
+  const int64_t row = blk < 0 ? 0 : static_cast<int64_t>(blk) * kPageTokens + t % kPageTokens;
+  return reinterpret_cast<const uint8_t*>(p.kv) + row * kFp4RowBytes;
+}
+
+// A row block's heads: `valid` of its columns are query rows, the MMA has N (a multiple of 16), a softmax warpgroup N / 2.
+struct Block {
+  int rb, valid, N, half;
+  __device__ Block(const DecodeParams& p, int rb_) : rb(rb_) {
+    valid = min(kRowsPerPair, p.rows - rb * kRowsPerPair);
+    N = (valid + 15) & ~15;
+    half = N >> 1;
+  }
+};
+
+// ------------------------------------------------------------------ S-CTA --
+// Warp 0: the two pages of every tile.  Dense: one copy a page (as far as the request has tokens); lists: a copy a
+// row, whose addresses are looked up while the tile before is being loaded.
+template <bool Sparse>
+__device__ void s_load(const DecodeParams& p, Shared& sh, uint32_t smem, int part, uint32_t cl) {
+  const int lane = threadIdx.x & 31;
+  SegmentWalker w;
+  w.init(p, part);
+  Segment s;
+  uint32_t T = 0;
+  bool withhold = p.withhold_first_load != 0;   // test hook: the first page never arrives
+  bool ok = true, armed[2] = {false, false};
+  uint32_t phase[2] = {0, 0};                   // of the last loads into each page
+  while (ok && w.next(s)) {
+    const int L = __ldg(p.lens + s.b);
+    for (int k = s.kb; ok && k < s.ke; k += 2, ++T) {
+      for (int h = 0; h < 2; ++h) {
+        const int n = k + h < s.ke ? min(kPageTokens, L - (k + h) * kPageTokens) : 0;   // rows
+        const uint32_t dst = smem + kOffRaw + h * kPageBytes;
+        const uint8_t* row[2] = {nullptr, nullptr};
+        if constexpr (Sparse) {
+          int t[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) t[i] = lane + 32 * i < n ? entry_of(p, s.b, (k + h) * kPageTokens + lane + 32 * i) : 0;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (lane + 32 * i < n) row[i] = row_at(p, t[i], entry_page(p, s.b, t[i]));
+        } else if (n > 0) {
+          row[0] = row_at(p, 0, page_of(p, s.b, k + h));
+        }
+        if (!warp_wait(sh, sh.raw_empty[h], (T & 1) ^ 1, p.status, cl)) {
+          ok = false;
+          break;
+        }
+        if (withhold) {
+          withhold = false;
+          continue;
+        }
+        armed[h] = true;
+        phase[h] = T & 1;
+        if (lane == 0) {
+          if (n > 0) mbar_arrive_expect_tx(smem_u32(&sh.raw_full[h]), static_cast<uint32_t>(n) * kFp4RowBytes);
+          else arrive(sh.raw_full[h]);
+        }
+        __syncwarp();
+        if constexpr (Sparse) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (row[i]) bulk_load(dst + (lane + 32 * i) * kFp4RowBytes, row[i], kFp4RowBytes, sh.raw_full[h]);
+        } else if (lane == 0 && n > 0) {
+          bulk_load(dst, row[0], static_cast<uint32_t>(n) * kFp4RowBytes, sh.raw_full[h]);
+        }
+      }
+    }
+  }
+  if (lane == 0)   // loads still in flight land before the CTA may leave
+    for (int h = 0; h < 2; ++h)
+      if (armed[h]) drain_bar(sh.raw_full[h], phase[h]);
+  __syncwarp();
+}
+
+// Warps 12..19: a thread a token; warpgroup c takes latent dims [256 c, 256 c + 256) and half of the rope dims.  A tile's codes
+// are read into registers at once, which frees the page buffers for the next tile's loads.  Rows are 352 bytes: lanes 4
+// rows apart would hit the same banks, so rows with bit 2 set read each pair of units the other way round.
+__device__ void s_convert(const DecodeParams& p, Shared& sh, uint32_t smem, int part, uint32_t cl, int c) {
+  const int quad = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  const int h = quad >> 1;                                   // page of the tile
+  const int r = (quad & 1) * 32 + lane;                      // row of the page
+  const uint32_t raw = smem + kOffRaw + h * kPageBytes + r * kFp4RowBytes;
+  const bool swap = r & 4;
+  const uint32_t first = swap ? 16 : 0;
+  const uint32_t tm = sh.tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + kKCol;
+  auto pair = [&](uint32_t at, uint32_t (&w)[8]) {           // 32 bytes of the row
+    const uint4 a = ld_shared_v4(raw + at + first), b = ld_shared_v4(raw + at + (first ^ 16));
+    w[0] = swap ? b.x : a.x, w[1] = swap ? b.y : a.y, w[2] = swap ? b.z : a.z, w[3] = swap ? b.w : a.w;
+    w[4] = swap ? a.x : b.x, w[5] = swap ? a.y : b.y, w[6] = swap ? a.z : b.z, w[7] = swap ? a.w : b.w;
+  };
+  SegmentWalker w;
+  w.init(p, part);
+  Segment s;
+  uint32_t T = 0;
+  while (w.next(s)) {
+    for (int t = tiles_of(s); t > 0; --t, ++T) {
+      if (!warp_wait(sh, sh.raw_full[h], T & 1, p.status, cl)) return;
+      uint32_t code[4][8], rope[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) pair(128 * c + 32 * k, code[k]);
+      const uint4 sc = ld_shared_v4(raw + kFp4Scales + 16 * c);
+      pair(kFp4Rope + 32 * c, rope);
+      __syncwarp();
+      if (lane == 0) arrive(sh.raw_empty[h]);
+      const uint32_t scale[4] = {sc.x, sc.y, sc.z, sc.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t i = kItems * T + 2 * k + c, slot = i % kKSlots;
+        uint32_t v[32];
+        const uint32_t s01 = e4m3x2_to_f16x2<0>(scale[k]), s23 = e4m3x2_to_f16x2<1>(scale[k]);
+        values16(code[k][0], code[k][1], __byte_perm(s01, 0, 0x1010), v);
+        values16(code[k][2], code[k][3], __byte_perm(s01, 0, 0x3232), v + 8);
+        values16(code[k][4], code[k][5], __byte_perm(s23, 0, 0x1010), v + 16);
+        values16(code[k][6], code[k][7], __byte_perm(s23, 0, 0x3232), v + 24);
+        if (!warp_wait(sh, sh.k_empty[slot], ((i / kKSlots) & 1) ^ 1, p.status, cl)) return;
+        tc_fence_after();
+        tmem_st32(tm + slot * 32, v);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive2(sh.k_full[slot]);
+      }
+      const uint32_t i = kItems * T + 8, slot = i % kKSlots;
+      uint32_t v[16];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[2 * j] = e4m3x2_to_f16x2<0>(rope[j]), v[2 * j + 1] = e4m3x2_to_f16x2<1>(rope[j]);
+      if (!warp_wait(sh, sh.k_empty[slot], ((i / kKSlots) & 1) ^ 1, p.status, cl)) return;
+      tc_fence_after();
+      tmem_st16(tm + slot * 32 + 16 * c, v);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive(sh.k_full[slot]);
+    }
+  }
+}
+
+// Warp 1 (all lanes; an elected one issues): S^T = K Q^T, 36 steps of 16 dims a tile.
+__device__ void s_mma(const DecodeParams& p, Shared& sh, uint32_t smem, int part, uint32_t cl, const Block& blk) {
+  SegmentWalker w;
+  w.init(p, part);
+  Segment s;
+  uint32_t i = 0, T = 0, seg = 0;
+  const uint32_t tmem = sh.tmem_base;
+  const uint32_t idesc = idesc_f16_f32(kTile, blk.N, 0, 0);
+  bool ok = true;
+  while (ok && w.next(s)) {
+    if (!warp_wait(sh, sh.q_full, seg & 1, p.status, cl)) break;
+    for (int t = tiles_of(s); ok && t > 0; --t, ++T) {
+      const uint32_t sb = T & 1;
+      if (!warp_wait(sh, sh.s_empty[sb], ((T >> 1) & 1) ^ 1, p.status, cl)) {
+        ok = false;
+        break;
+      }
+#pragma unroll
+      for (int it = 0; it < kItems; ++it, ++i) {
+        const uint32_t slot = i % kKSlots;
+        if (!warp_wait(sh, sh.k_full[slot], (i / kKSlots) & 1, p.status, cl)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const int chunk = it < 8 ? (it >> 1) + 4 * (it & 1) : 8;   // the warpgroups' chunks in turn
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          mma_bf16_ts_warp(tmem + sb * kTile, tmem + kKCol + slot * 32 + j * 8,
+                           smem_desc_sw128(smem + chunk * kQChunk + j * 32, 16, 1024), idesc, it | j ? 1u : 0u);
+        mma_commit_warp(smem_u32(&sh.k_empty[slot]));
+      }
+      if (ok) mma_commit_warp(smem_u32(&sh.s_full[sb]));
+    }
+    ++seg;
+  }
+  mma_commit_warp(smem_u32(&sh.drain));   // behind everything issued
+  drain_bar(sh.drain, 0);
+  __syncwarp();
+}
+
+// Rows of q of warpgroup w's heads, 4 at a time a warp, into shared memory as fp16, with their scores' factors.
+__device__ void s_load_q(const DecodeParams& p, Shared& sh, uint32_t smem, int b, const Block& blk, int w, int wq, int lane) {
+  const float unit = p.scale_log2 * p.kv_scale;
+  for (int j0 = 0; j0 < blk.half; j0 += 16) {
+    uint4 v[4][3];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = w * blk.half + j0 + 4 * j + wq;
+      const bool have = j0 + 4 * j < blk.half && n < blk.valid;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          p.q + (static_cast<int64_t>(b) * p.rows + blk.rb * kRowsPerPair + (have ? n : 0)) * kDimQK);
+#pragma unroll
+      for (int u = 0; u < 3; ++u)
+        v[j][u] = have && lane + 32 * u < kDimQK / 8 ? __ldg(src + lane + 32 * u) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = w * blk.half + j0 + 4 * j + wq;
+      float top = 0.f;
+#pragma unroll
+      for (int u = 0; u < 3; ++u) {
+        const uint32_t x[4] = {v[j][u].x, v[j][u].y, v[j][u].z, v[j][u].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = max_nan(top, max_nan(fabsf(bf16_lo(x[e])), fabsf(bf16_hi(x[e]))));
+      }
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const bool finite = top <= 3.4e38f;
+      const int e = finite ? max(static_cast<int>(__float_as_uint(top) >> 23), 41) : 141;   // at most a factor 2^100
+      const float sc = finite ? __uint_as_float(static_cast<uint32_t>(268 - e) << 23) : 0.f;
+      // (a row with an infinity or a NaN gets scores of NaN; the factor is never 0, so that masks stay -inf)
+      const float back = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+      if (j0 + 4 * j >= blk.half) break;
+#pragma unroll
+      for (int u = 0; u < 3; ++u) {
+        const int unit16 = lane + 32 * u;
+        if (unit16 < kDimQK / 8) {
+          const uint32_t x[4] = {v[j][u].x, v[j][u].y, v[j][u].z, v[j][u].w};
+          uint32_t y[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) y[q] = finite ? pack_f16x2(bf16_lo(x[q]) * sc, bf16_hi(x[q]) * sc) : 0u;
+          st_shared_v4(smem + (unit16 >> 3) * kQChunk + n * 128 + (((unit16 & 7) ^ (n & 7)) << 4),
+                       make_uint4(y[0], y[1], y[2], y[3]));
+        }
+      }
+      if (lane == 0) sh.q_scale[n] = finite ? fmaxf(unit * back, 0x1p-126f) : NAN;
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) arrive(sh.q_full);
+}
+
+// Warps 4..11: warpgroup w has heads [w N/2, (w + 1) N/2) of the block.  Thread l of a warp has four of a tile's tokens (rows l / 4
+// + 8 {0..3} of the warp's TMEM quadrant) and up to 16 heads (8 i + 2 (l % 4) + {0, 1}).
+template <bool Sparse>
+__device__ void s_softmax(const DecodeParams& p, Shared& sh, uint32_t smem, int part, uint32_t cl, const Block& blk) {
+  const int t = threadIdx.x - 128, w = t >> 7, wq = (t >> 5) & 3, lane = t & 31, tr = lane >> 2, tc = lane & 3;
+  const uint32_t bar = 1 + w;                     // named barrier of the warpgroup
+  const int units = blk.half >> 3;                // of 8 heads
+  const uint32_t tm = sh.tmem_base + (static_cast<uint32_t>(wq * 32) << 16) + w * blk.half;
+  const uint32_t pkt = smem + kOffSend + w * kPktStride;
+  // stmatrix: lane 8 m + r has row r of matrix m: unit m / 2 of a pair, rows 8 (m % 2) + r of 16
+  const int st_row = 32 * wq + 8 * ((lane >> 3) & 1) + (lane & 7), st_unit = lane >> 4;
+  SegmentWalker walk;
+  walk.init(p, part);
+  Segment s;
+  uint32_t T = 0;
+  bool ok = true;
+  while (ok && walk.next(s)) {
+    const int L = __ldg(p.lens + s.b);
+    const int L_seq = Sparse ? __ldg(p.seqlens + s.b) : L;
+    s_load_q(p, sh, smem, s.b, blk, w, wq, lane);   // (every MMA of the segment before is complete: its last S was waited for)
+    named_bar_sync(bar, 128);
+    float2 sl[8], nm[8], l[8];                       // score factor, offset - reference maximum (log2), sum of the thread's tokens
+    uint32_t fresh = 0;                              // heads that have no reference yet, two bits a unit
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // (units are taken in pairs: one past the heads gives exponents of -inf)
+      sl[i] = i < units ? *reinterpret_cast<const float2*>(&sh.q_scale[w * blk.half + 8 * i + 2 * tc]) : make_float2(0.f, 0.f);
+      nm[i] = i < units ? make_float2(0.f, 0.f) : make_float2(-INFINITY, -INFINITY);
+      l[i] = make_float2(0.f, 0.f);
+      if (i < units) fresh |= 3u << (2 * i);
+    }
+    for (int k = s.kb; k < s.ke; k += 2, ++T) {
+      const uint32_t sb = T & 1;
+      const int ntok = min(min(kTile, (s.ke - k) * kPageTokens), L - k * kPageTokens);
+      const bool last = k + 2 >= s.ke;
+      // a token is seen by a head whose limit lies above its key (its position; none past the tile's tokens)
+      const bool masked = ntok < kTile || (p.causal && (Sparse || k * kPageTokens + kTile > L_seq - p.s_q + 1));
+      int key[4];
+      if (masked) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int tok = 32 * wq + 8 * j + tr, e = k * kPageTokens + tok;
+          key[j] = INT_MAX;
+          if (tok < ntok) {
+            key[j] = e;
+            if (Sparse) {   // (a bad entry is reported by the loads, and seen by nobody)
+              const int at = e < p.idx_stride ? __ldg(p.indices + static_cast<int64_t>(s.b) * p.idx_stride + e) : -1;
+              key[j] = at >= 0 && at < L_seq ? at : INT_MAX;
+            }
+          }
+        }
+      }
+      bool ok_t = wait_bar(sh, sh.s_full[sb], (T >> 1) & 1, p.status, cl);
+      if (ok_t) ok_t = wait_bar(sh, sh.st_free[w], (T & 1) ^ 1, p.status, cl);   // the last packet has been read
+      __syncwarp();
+      tc_fence_after();
+      float2 ls[8];
+      uint32_t top = 0;   // largest P, two fp16
+      auto limit = [&](int col) {
+        return p.causal ? L_seq - p.s_q + sh.pos[w * blk.half + col] + 1 : INT_MAX;
+      };
+      auto exponentials = [&] {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ls[i] = make_float2(0.f, 0.f);
+        const uint32_t at0 = tm + sb * kTile;
+        float xa[16], xb[16];   // the next 32 columns are on their way while these are worked on
+        auto work = [&](int part4, const float (&x)[16]) {   // part4: token rows 16 (part4 % 2), units from 4 (part4 / 2)
+          const int hf = part4 & 1, i0 = 4 * (part4 >> 1);
+#pragma unroll
+          for (int ii = 0; ii < 2; ++ii) {
+            if (i0 + 2 * ii >= units) break;
+            uint32_t pk[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {   // unit i0 + 2 ii + q / 2, token row q % 2
+              const int i = i0 + 2 * ii + (q >> 1), at = 8 * ii + 2 * q;
+              float2 y = fma2(make_float2(x[at], x[at + 1]), sl[i], nm[i]);
+              if (masked) {
+                const int c = 8 * i + 2 * tc, kk = key[2 * hf + (q & 1)];
+                if (!(kk < limit(c))) y.x = -INFINITY;
+                if (!(kk < limit(c + 1))) y.y = -INFINITY;
+              }
+              y.x = fast_exp2(y.x);
+              y.y = fast_exp2(y.y);
+              ls[i] = add2(ls[i], y);
+              pk[q] = pack_f16x2(y.x, y.y);
+              top = max_f16x2(top, pk[q]);
+            }
+            const int row = st_row + 16 * hf;
+            stmatrix4(pkt + row * 128 + (((i0 + 2 * ii + st_unit) ^ (row & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
+          }
+        };
+        constexpr uint32_t kRow16 = 16u << 16;
+        tmem_ld_16x256(at0, xa);
+        tmem_wait_ld();
+        tmem_ld_16x256(at0 + kRow16, xb);
+        work(0, xa);
+        tmem_wait_ld();
+        if (units > 4) tmem_ld_16x256(at0 + 32, xa);
+        work(1, xb);
+        if (units > 4) {
+          tmem_wait_ld();
+          tmem_ld_16x256(at0 + kRow16 + 32, xb);
+          work(2, xa);
+          tmem_wait_ld();
+          work(3, xb);
+        }
+      };
+      exponentials();
+      // a P past 2^14 (0x7400 in fp16), or a head without a reference: the tile again, with new references
+      const bool again = fresh != 0 || (top & 0xFFFFu) > 0x7400u || (top >> 16) > 0x7400u || !ok_t;
+      fence_proxy_async_smem();
+      tc_fence_before();
+      bool rebased = false;
+      if (named_bar_or(bar, 128, again)) {
+        if (named_bar_or(bar, 128, !ok_t)) {
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (int ii = 0; ii < 4; ++ii) {   // the heads' maxima over the warp's tokens, two units at a time
+          if (2 * ii >= units) break;
+          float2 cm[2] = {make_float2(-INFINITY, -INFINITY), make_float2(-INFINITY, -INFINITY)};
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            float x[8];
+            tmem_ld_16x256(tm + sb * kTile + 16 * ii + (static_cast<uint32_t>(16 * hf) << 16), x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int u = q >> 1, i = 2 * ii + u;
+              float2 y = make_float2(x[2 * q] * sl[i].x, x[2 * q + 1] * sl[i].y);
+              if (masked) {
+                const int c = 8 * i + 2 * tc, kk = key[2 * hf + (q & 1)];
+                if (!(kk < limit(c))) y.x = -INFINITY;
+                if (!(kk < limit(c + 1))) y.y = -INFINITY;
+              }
+              cm[u] = make_float2(fmaxf(cm[u].x, y.x), fmaxf(cm[u].y, y.y));
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int o = 4; o <= 16; o <<= 1) {
+              cm[u].x = fmaxf(cm[u].x, __shfl_xor_sync(0xffffffffu, cm[u].x, o));
+              cm[u].y = fmaxf(cm[u].y, __shfl_xor_sync(0xffffffffu, cm[u].y, o));
+            }
+            if (tr == 0) *reinterpret_cast<float2*>(&sh.part[w][wq][16 * ii + 8 * u + 2 * tc]) = cm[u];
+          }
+        }
+        named_bar_sync(bar, 128);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i < units) {
+            float alpha[2] = {1.f, 1.f};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int c = 8 * i + 2 * tc + e;
+              const float m = fmaxf(fmaxf(sh.part[w][0][c], sh.part[w][1][c]), fmaxf(sh.part[w][2][c], sh.part[w][3][c]));
+              float& n = e ? nm[i].y : nm[i].x;
+              float& sum = e ? l[i].y : l[i].x;
+              const uint32_t bit = 1u << (2 * i + e);
+              if (fresh & bit) {
+                if (m > -INFINITY) n = kOffset - m, fresh &= ~bit;
+              } else if (m + n > kTop) {
+                alpha[e] = fast_exp2(kOffset - n - m);
+                n = kOffset - m;
+                sum *= alpha[e];
+              }
+            }
+            if (wq == 0 && tr == 0)
+              asm volatile("st.shared.v2.f32 [%0], {%1, %2};" :: "r"(pkt + kPktAlpha + (8 * i + 2 * tc) * 4), "f"(alpha[0]),
+                           "f"(alpha[1]) : "memory");
+          }
+        exponentials();
+        fence_proxy_async_smem();
+        tc_fence_before();
+        rebased = true;
+      }
+      __syncwarp();
+      if (lane == 0) arrive(sh.s_empty[sb]);   // S^T has been read
+#pragma unroll
+      for (int i = 0; i < 8; ++i) l[i] = add2(l[i], ls[i]);
+      if (last) {   // the heads' sums over the warpgroup's threads
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i < units) {
+            float2 v = l[i];
+#pragma unroll
+            for (int o = 4; o <= 16; o <<= 1) {
+              v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+              v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+            }
+            if (rebased && i == 0) named_bar_sync(bar, 128);   // (part still holds the maxima)
+            if (tr == 0) {
+              *reinterpret_cast<float2*>(&sh.part[w][wq][8 * i + 2 * tc]) = v;
+              if (wq == 0) *reinterpret_cast<float2*>(&sh.ref[w][8 * i + 2 * tc]) = nm[i];
+            }
+          }
+        named_bar_sync(bar, 128);
+        const int c = t & 127;
+        if (c < blk.half) {
+          const float sum = (sh.part[w][0][c] + sh.part[w][1][c]) + (sh.part[w][2][c] + sh.part[w][3][c]);
+          asm volatile("st.shared.f32 [%0], %1;" :: "r"(pkt + kPktInvL + c * 4), "f"(sum == 0.f ? 0.f : p.kv_scale / sum)
+                       : "memory");
+          const int n = w * blk.half + c, g = blk.rb * kRowsPerPair + n;
+          if (n < blk.valid) {
+            const float lse = sum == 0.f ? -INFINITY : (log2f(sum) - sh.ref[w][c]) * kLn2;
+            const int ns0 = __ldg(p.num_splits + s.b), nsplit = __ldg(p.num_splits + s.b + 1) - ns0;
+            if (nsplit == 1) p.lse[static_cast<int64_t>(s.b) * p.rows + g] = lse;
+            else if (split_slot_ok(p, ns0 + s.split))   // (NaN travels as +inf, whose weight the merge makes NaN)
+              p.lse_part[static_cast<int64_t>(ns0 + s.split) * p.rows + g] = isnan(lse) ? INFINITY : lse;
+          }
+        }
+      }
+      if (t - 128 * w == 0) asm volatile("st.shared.u32 [%0], %1;" :: "r"(pkt + kPktFlag), "r"(rebased ? 1 : 0) : "memory");
+      if (rebased || last) {
+        fence_proxy_async_smem();
+        named_bar_sync(bar, 128);
+      } else if (t - 128 * w == 0) {
+        fence_proxy_async_smem();
+      }
+      if (t - 128 * w == 0) arrive(sh.p_ready[w]);
+    }
+  }
+}
+
+// Warps 2 and 3 (a lane each): warpgroup w's packets to the partner.
+__device__ void s_ship(const DecodeParams& p, Shared& sh, uint32_t smem, int part, uint32_t cl, uint32_t peer, int w) {
+  const uint32_t src = smem + kOffSend + w * kPktStride, dst = map_to_rank(smem + w * kPktStride, peer);
+  const uint32_t full = map_to_rank(smem_u32(&sh.p_full[0]), peer);
+  SegmentWalker walk;
+  walk.init(p, part);
+  Segment s;
+  uint32_t T = 0;
+  bool ok = true;
+  while (ok && walk.next(s)) {
+    for (int t = tiles_of(s); t > 0; --t, ++T) {
+      const uint32_t slot = T & 1;
+      if (!wait_bar(sh, sh.p_ready[w], T & 1, p.status, cl) ||
+          !wait_bar(sh, sh.credit[slot], ((T >> 1) & 1) ^ 1, p.status, cl, true)) {
+        ok = false;
+        break;
+      }
+      bulk_copy_to_cluster(dst + slot * 2 * kPktStride, src, kPktBytes, full + slot * 8);
+      bulk_commit_group();
+      bulk_wait_group_read<0>();
+      arrive(sh.st_free[w]);
+    }
+  }
+  bulk_wait_group<0>();   // copies land before the CTA may leave
+}
+
+// ------------------------------------------------------------------ O-CTA --
+// Warps 12..19: the latent dims of every page, from global memory through registers into shared memory as fp16 (64 tokens by
+// 64 dims a chunk, 128-byte swizzle).  A thread has two rows of a page, 8 warps a row group of 32, and of each row a unit of 32
+// dims in either half.  Four lanes apart two rows and a unit pair: a quarter warp reads 32 bytes of four rows and writes eight different banks.
+// Addresses are looked up two pages ahead, codes loaded one page ahead.
+template <bool Sparse>
+__device__ void o_convert(const DecodeParams& p, Shared& sh, uint32_t smem, int part, uint32_t cl) {
+  const int v = (threadIdx.x >> 5) - 12, lane = threadIdx.x & 31;
+  const int u0 = lane & 1, rr = (lane >> 1) & 3, q = lane >> 3;
+  const int r0 = 4 * v + rr;              // rows r0 and r0 + 32
+  const int unit = 2 * q + u0;            // of the 8 in a half
+  struct Tokens { int t[2]; int b, n, k; bool valid; } tok;            // n: rows of the page that hold tokens
+  struct Rows { const uint8_t* at[2]; int n; bool valid; } rows;
+  struct Codes { uint4 c[2][2]; uint32_t s[2][2]; int n; bool valid; } cur, nxt;   // by row and half
+  PageIter it;
+  it.init(p, part);
+  auto fetch_tokens = [&] {
+    tok.valid = it.valid;
+    tok.n = 0;
+    if (!it.valid) return;
+    tok.b = it.s.b;
+    tok.k = it.k;
+    tok.n = min(kPageTokens, __ldg(p.lens + it.s.b) - it.k * kPageTokens);
+    if constexpr (Sparse) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int e = it.k * kPageTokens + r0 + 32 * g;
+        tok.t[g] = r0 + 32 * g < tok.n && e < p.idx_stride ? __ldg(p.indices + static_cast<int64_t>(it.s.b) * p.idx_stride + e) : -1;
+      }
+    }
+    it.advance();
+  };
+  auto fetch_rows = [&] {   // (what is out of range is reported by the S-CTA's loads and read as row or page 0 here)
+    rows.valid = tok.valid;
+    rows.n = tok.n;
+    if (!tok.valid) return;
+    if constexpr (Sparse) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int t = tok.t[g];
+        int blk = -1;
+        if (t >= 0 && t < __ldg(p.seqlens + tok.b) && t / kPageTokens < p.max_blocks)
+          blk = __ldg(p.block_table + static_cast<int64_t>(tok.b) * p.max_blocks + t / kPageTokens);
+        rows.at[g] = row_at(p, t < 0 ? 0 : t, blk < p.num_blocks ? blk : -1);
+      }
+    } else {
+      int blk = -1;
+      if (tok.k < p.max_blocks) blk = __ldg(p.block_table + static_cast<int64_t>(tok.b) * p.max_blocks + tok.k);
+      const uint8_t* page = row_at(p, 0, blk < p.num_blocks ? blk : -1);
+      rows.at[0] = page + r0 * kFp4RowBytes;
+      rows.at[1] = page + (r0 + 32) * kFp4RowBytes;
+    }
+  };
+  auto fetch_codes = [&](Codes& d) {
+    d.valid = rows.valid;
+    d.n = rows.n;
+    if (!rows.valid) return;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      if (r0 + 32 * g < d.n) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          d.c[g][h] = __ldg(reinterpret_cast<const uint4*>(rows.at[g] + 128 * h + 16 * unit));
+          d.s[g][h] = __ldg(reinterpret_cast<const uint16_t*>(rows.at[g] + kFp4Scales + 16 * h + 2 * unit));
+        }
+      }
+    }
+  };
+  uint32_t i = 0;   // half pages
+  auto convert = [&](const Codes& d) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h, ++i) {
+      const uint32_t slot = i % kVSlots;
+      if (!warp_wait(sh, sh.v_empty[slot], ((i / kVSlots) & 1) ^ 1, p.status, cl)) return false;
+      const uint32_t base = smem + kOffV + slot * kVSlot + q * kVChunk;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int r = r0 + 32 * g;
+        uint32_t x[16];
+        if (r < d.n) {
+          const uint32_t s = e4m3x2_to_f16x2<0>(d.s[g][h]);
+          values16(d.c[g][h].x, d.c[g][h].y, __byte_perm(s, 0, 0x1010), x);
+          values16(d.c[g][h].z, d.c[g][h].w, __byte_perm(s, 0, 0x3232), x + 8);
+        } else {   // P is 0 there, and 0 times what lies in an unused row need not be 0
+#pragma unroll
+          for (int j = 0; j < 16; ++j) x[j] = 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          st_shared_v4(base + r * 128 + (((4 * u0 + j) ^ (r & 7)) << 4),
+                       make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]));
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive(sh.v_full[slot]);
+    }
+    return true;
+  };
+  fetch_tokens();
+  fetch_rows();
+  fetch_tokens();
+  fetch_codes(cur);
+  fetch_rows();
+  fetch_tokens();
+  while (cur.valid) {
+    fetch_codes(nxt);
+    fetch_rows();
+    fetch_tokens();
+    if (!convert(cur)) return;
+    cur = nxt;
+  }
+}
+
+// Warp 1 (all lanes; an elected one issues): O += P V, for every page and 256-column half of O a step per 16 tokens.
+__device__ void o_mma(const DecodeParams& p, Shared& sh, uint32_t smem, int part, uint32_t cl) {
+  const int lane = threadIdx.x & 31;
+  SegmentWalker w;
+  w.init(p, part);
+  Segment s;
+  uint32_t T = 0, i = 0, seg = 0, nresc = 0;
+  const uint32_t tmem = sh.tmem_base;
+  constexpr uint32_t idesc = idesc_f16_f32(128, 256, 1, 1);
+  bool ok = true;
+  while (ok && w.next(s)) {
+    if (seg > 0 && !warp_wait(sh, sh.o_free, (seg - 1) & 1, p.status, cl)) {
+      ok = false;
+      break;
+    }
+    for (int k = s.kb; ok && k < s.ke; k += 2, ++T) {
+      const uint32_t slot = T & 1;
+      const uint32_t pkt = smem + slot * 2 * kPktStride;
+      const bool last = k + 2 >= s.ke;
+      const int ntok = tile_tokens(p, s, k);
+      if (lane == 0) mbar_arrive_expect_tx(smem_u32(&sh.p_full[slot]), 2 * kPktBytes);
+      __syncwarp();
+      if (!warp_wait(sh, sh.p_full[slot], (T >> 1) & 1, p.status, cl, true)) {
+        ok = false;
+        break;
+      }
+      if (last)   // before the slot can be reused
+        st_shared_v4(smem + kOffInvL + lane * 16, ld_shared_v4(pkt + (lane >> 4) * kPktStride + kPktInvL + (lane & 15) * 16));
+      const float flag = ld_shared_f32(pkt + (lane & 1) * kPktStride + kPktFlag);
+      __syncwarp();
+      if (k != s.kb && __any_sync(0xffffffffu, __float_as_uint(flag) != 0)) {   // scale O before adding this tile
+        mma_commit_warp(smem_u32(&sh.o_sync));
+        if (!warp_wait(sh, sh.o_sync, nresc & 1, p.status, cl)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          sh.cmd = 1;
+          sh.cmd_arg = static_cast<int>(slot);
+          arrive(sh.corr_go);
+        }
+        __syncwarp();
+        if (!warp_wait(sh, sh.corr_done, nresc & 1, p.status, cl)) {
+          ok = false;
+          break;
+        }
+        ++nresc;
+      }
+      tc_fence_after();
+      for (int pg = 0; ok && pg < 2 && k + pg < s.ke; ++pg) {
+        const int ksteps = (min(kPageTokens, ntok - pg * kPageTokens) + 15) >> 4;
+        const uint32_t a = pkt + pg * kPageTokens * 128;
+#pragma unroll
+        for (int h = 0; h < 2; ++h, ++i) {
+          const uint32_t vs = i % kVSlots;
+          if (!warp_wait(sh, sh.v_full[vs], (i / kVSlots) & 1, p.status, cl)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t vb = smem + kOffV + vs * kVSlot;
+          const uint32_t first = k == s.kb && pg == 0 ? 0u : 1u;
+          if (ksteps == 4) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              mma_bf16_ss_warp(tmem + 256 * h, smem_desc_sw128(a + j * 2048, kPktStride, 1024),
+                               smem_desc_sw128(vb + j * 2048, kVChunk, 1024), idesc, j ? 1u : first);
+          } else {
+            for (int j = 0; j < ksteps; ++j)
+              mma_bf16_ss_warp(tmem + 256 * h, smem_desc_sw128(a + j * 2048, kPktStride, 1024),
+                               smem_desc_sw128(vb + j * 2048, kVChunk, 1024), idesc, j ? 1u : first);
+          }
+          mma_commit_warp(smem_u32(&sh.v_empty[vs]));
+        }
+      }
+      if (!ok) break;
+      mma_commit_warp(smem_u32(&sh.p_free[slot]));
+      if (last) {
+        mma_commit_warp(smem_u32(&sh.o_full));
+        if (lane == 0) {
+          sh.cmd = 2;
+          arrive(sh.corr_go);
+        }
+        __syncwarp();
+      }
+    }
+    ++seg;
+  }
+  if (ok && seg > 0) warp_wait(sh, sh.o_free, (seg - 1) & 1, p.status, cl);   // the last epilogue has taken its command
+  mma_commit_warp(smem_u32(&sh.drain));   // behind everything issued
+  drain_bar(sh.drain, 0);
+  __syncwarp();
   if (lane == 0) {
-    alpha[row] = l == 0.f ? 0.f : p.kv_scale / l;
-    if (g < p.rows) p.lse[static_cast<int64_t>(b) * p.rows + g] =
-        l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+    sh.cmd = 3;
+    arrive(sh.corr_go);
   }
+  __syncwarp();
+}
+
+// A lane of warp 2: gives packet slots back to the S-CTA once the MMAs are done with them.
+__device__ void o_forward(const DecodeParams& p, Shared& sh, int part, uint32_t cl, uint32_t peer) {
+  SegmentWalker w;
+  w.init(p, part);
+  Segment s;
+  uint32_t T = 0;
+  const uint32_t credit = map_to_rank(smem_u32(&sh.credit[0]), peer);
+  while (w.next(s))
+    for (int t = tiles_of(s); t > 0; --t, ++T) {
+      if (!wait_bar(sh, sh.p_free[T & 1], (T >> 1) & 1, p.status, cl)) return;
+      mbar_arrive_remote(credit + (T & 1) * 8);
+    }
+}
+
+// Warps 4..11: rescale O's rows, or normalise and store a finished segment.  Warpgroup wg owns O's columns [256 wg, 256 wg + 256).
+// TMEM lane m is head (m / 64) N/2 + m % 64 of the block, where m % 64 < N/2.
+__device__ void o_epilogue(const DecodeParams& p, Shared& sh, uint32_t smem, int part, uint32_t cl, const Block& blk) {
+  const int t = threadIdx.x - 128, wg = t >> 7, r = t & 127, wq = r >> 5, lane = r & 31;
+  const uint32_t tmem_row = sh.tmem_base + (static_cast<uint32_t>(wq * 32) << 16) + wg * 256;
+  const int h0 = 32 * (wq & 1), n0 = (wq >> 1) * blk.half + h0;                  // the warp's first head
+  const int nrows = max(0, min(min(32, blk.half - h0), blk.valid - n0));         // its heads
+  SegmentWalker w;
+  w.init(p, part);
+  Segment s;
+  uint32_t ncmd = 0, seg = 0;
+  bool have = w.next(s);
+  while (true) {
+    if (!warp_wait(sh, sh.corr_go, ncmd & 1, p.status, cl)) break;
+    ++ncmd;
+    const int cmd = sh.cmd;
+    if (cmd == 3) break;
+    if (cmd == 1) {
+      const uint32_t pkt = smem + sh.cmd_arg * 2 * kPktStride + (r >> 6) * kPktStride;
+      // (a warpgroup that did not rebase sends no factors)
+      const float alpha = __float_as_uint(ld_shared_f32(pkt + kPktFlag)) ? ld_shared_f32(pkt + kPktAlpha + (r & 63) * 4) : 1.f;
+      tc_fence_after();
+      if (__any_sync(0xffffffffu, lane < nrows && alpha != 1.f)) {
+#pragma unroll 1
+        for (int c = 0; c < 256; c += 32) {
+          uint32_t v[32];
+          tmem_ld32(tmem_row + c, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * alpha);
+          tmem_st32(tmem_row + c, v);
+        }
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive(sh.corr_done);
+      continue;
+    }
+    if (!have) break;
+    if (!warp_wait(sh, sh.o_full, seg & 1, p.status, cl)) break;
+    tc_fence_after();
+    const float inv_l = ld_shared_f32(smem + kOffInvL + r * 4);
+    const int ns0 = __ldg(p.num_splits + s.b);
+    const bool final_out = __ldg(p.num_splits + s.b + 1) - ns0 == 1;
+    const bool slot_ok = final_out || split_slot_ok(p, ns0 + s.split);
+    // Through the warp's transpose buffer, so that a store instruction writes 64 bytes of 8 rows.  Buffer row x (64 B) holds
+    // 16-byte unit u at ((u ^ ((x >> 1) & 3)) * 16): the 8 rows that a quarter-warp stores (or the 2 it loads) touch 8
+    // different bank groups.
+    const int64_t head0 = static_cast<int64_t>(s.b) * p.rows + blk.rb * kRowsPerPair + n0;
+    __nv_bfloat16* const obase = p.out + head0 * kDimV + wg * 256;
+    float* const pbase = p.o_part + (static_cast<int64_t>(ns0 + s.split) * p.rows + blk.rb * kRowsPerPair + n0) * kDimV + wg * 256;
+    const uint32_t stg = smem + kOffEpi + ((wg << 2) | wq) * 2048;
+    const int tq = lane & 3;                // transposed: 16-byte quad tq of rows 8 j + (lane >> 2)
+    auto put = [&](int j, uint4 u) { st_shared_v4(stg + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), u); };
+    auto get = [&](int j) {
+      const int x = 8 * j + (lane >> 2);
+      return ld_shared_v4(stg + x * 64 + ((tq ^ ((x >> 1) & 3)) << 4));
+    };
+    auto f = [&](uint32_t v) { return __uint_as_float(v) * inv_l; };
+    auto emit = [&](int c, const uint32_t (&v)[32]) {
+      if (final_out) {   // 32 bf16 columns: 64 B a row
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          put(j, make_uint4(pack_bf16x2(f(v[8 * j]), f(v[8 * j + 1])), pack_bf16x2(f(v[8 * j + 2]), f(v[8 * j + 3])),
+                            pack_bf16x2(f(v[8 * j + 4]), f(v[8 * j + 5])), pack_bf16x2(f(v[8 * j + 6]), f(v[8 * j + 7]))));
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int x = 8 * j + (lane >> 2);
+          const uint4 u = get(j);
+          if (x < nrows) *reinterpret_cast<uint4*>(obase + static_cast<int64_t>(x) * kDimV + c + 8 * tq) = u;
+        }
+        __syncwarp();
+      } else {           // fp32 partials: two passes of 16 columns
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int e = 16 * h + 4 * j;
+            put(j, make_uint4(__float_as_uint(f(v[e])), __float_as_uint(f(v[e + 1])), __float_as_uint(f(v[e + 2])),
+                              __float_as_uint(f(v[e + 3]))));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int x = 8 * j + (lane >> 2);
+            const uint4 u = get(j);
+            if (x < nrows && slot_ok) *reinterpret_cast<uint4*>(pbase + static_cast<int64_t>(x) * kDimV + c + 16 * h + 4 * tq) = u;
+          }
+          __syncwarp();
+        }
+      }
+    };
+    // the TMEM load of the next 32 columns is in flight while the current ones are stored
+    uint32_t va[32], vb[32];
+    tmem_ld32(tmem_row, va);
+#pragma unroll 1
+    for (int c = 0; c < 256; c += 64) {
+      tmem_wait_ld();
+      tmem_ld32(tmem_row + c + 32, vb);
+      emit(c, va);
+      tmem_wait_ld();
+      if (c + 64 < 256) {
+        tmem_ld32(tmem_row + c + 64, va);
+      } else {   // O may be overwritten by the next segment
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive(sh.o_free);
+      }
+      emit(c + 32, vb);
+    }
+    ++seg;
+    have = w.next(s);
+  }
+}
+
+template <bool Sparse>
+__global__ void __launch_bounds__(kThreads, 1) mla_decode_fp4_kernel(const __grid_constant__ DecodeParams p) {
+  extern __shared__ __align__(1024) uint8_t dyn_smem[];
+  const uint32_t smem = smem_u32(dyn_smem);
+  if (smem & 1023u) {   // the swizzled layouts need the base aligned (no static shared memory is declared)
+    if (threadIdx.x == 0) atomicCAS(p.status, 0, MLA_ERR_UNSUPPORTED);
+    return;             // every CTA of the grid takes this branch alike
+  }
+  Shared& sh = *reinterpret_cast<Shared*>(dyn_smem + kOffShared);
+  const int warp = threadIdx.x >> 5;
+  const uint32_t rank = cluster_ctarank();
+  const uint32_t cl = 2u * static_cast<uint32_t>(p.n_rb);
+  const int part = static_cast<int>(blockIdx.x / cl);
+  const Block blk(p, static_cast<int>(rank >> 1));
+  const bool is_s = (rank & 1u) == 0;
+  const uint32_t peer = rank ^ 1u;
+
+  if (threadIdx.x == 0) {
+    sh.abort = 0;
+    sh.cmd = 0;
+    auto init = [](uint64_t& b, uint32_t n) { mbar_init(smem_u32(&b), n); };
+    for (int i = 0; i < 2; ++i) {
+      init(sh.raw_full[i], 1);
+      init(sh.raw_empty[i], 4);      // two warps of each converting warpgroup
+      init(sh.s_full[i], 1);
+      init(sh.s_empty[i], 8);
+      init(sh.p_ready[i], 1);
+      init(sh.st_free[i], 1);
+      init(sh.credit[i], 1);
+      init(sh.p_full[i], 1);
+      init(sh.p_free[i], 1);
+    }
+    for (int i = 0; i < kKSlots; ++i) {
+      init(sh.k_full[i], 8);         // latent: four warps, two each; rope: eight warps
+      init(sh.k_empty[i], 1);
+    }
+    for (int i = 0; i < kVSlots; ++i) {
+      init(sh.v_full[i], 8);
+      init(sh.v_empty[i], 1);
+    }
+    init(sh.q_full, 8);
+    init(sh.o_full, 1);
+    init(sh.o_free, 8);
+    init(sh.o_sync, 1);
+    init(sh.corr_go, 1);
+    init(sh.corr_done, 8);
+    init(sh.drain, 1);
+    fence_mbar_init();
+  }
+  if (threadIdx.x < 128) sh.pos[threadIdx.x] = static_cast<uint16_t>(min(blk.rb * kRowsPerPair + static_cast<int>(threadIdx.x), p.rows - 1) / p.H);
+  __syncwarp();
+  if (warp == 0) tmem_alloc(smem_u32(&sh.tmem_base), 512);
+  tc_fence_before();
   __syncthreads();
-  for (int r = 0; r < kRowsCta && g0 + r < p.rows; ++r)
-    reinterpret_cast<uint32_t*>(p.out + (static_cast<int64_t>(b) * p.rows + g0 + r) * kDimV)[tid] =
-        pack_bf16x2(acc[r][0] * alpha[r], acc[r][1] * alpha[r]);
+  cluster_sync();        // every barrier of the cluster is initialised before any remote use
+  tc_fence_after();
+  griddep_wait();        // the metadata, q and the cache are complete from here on
+
+  if (warp < 4) {
+    regs_down<kRegsMisc>();
+    const bool lane0 = (threadIdx.x & 31) == 0;
+    if (is_s) {
+      if (warp == 0) s_load<Sparse>(p, sh, smem, part, cl);
+      else if (warp == 1) s_mma(p, sh, smem, part, cl, blk);
+      else if (lane0) s_ship(p, sh, smem, part, cl, peer, warp - 2);
+    } else {
+      if (warp == 1) o_mma(p, sh, smem, part, cl);
+      else if (warp == 2 && lane0) o_forward(p, sh, part, cl, peer);
+    }
+  } else if (warp < 12) {
+    regs_up<kRegsSoftmax>();
+    if (is_s) s_softmax<Sparse>(p, sh, smem, part, cl, blk);
+    else o_epilogue(p, sh, smem, part, cl, blk);
+  } else {
+    regs_down<kRegsConvert>();
+    if (is_s) s_convert(p, sh, smem, part, cl, (warp - 12) >> 2);
+    else o_convert<Sparse>(p, sh, smem, part, cl);
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();        // no CTA leaves while a partner may still touch its shared memory
+  __syncwarp();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(sh.tmem_base, 512);
+  }
 }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// One-time set-up of the kernels on the current device.
+bool fp4_ready() {
+  static std::mutex mutex;
+  static bool ready[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  std::lock_guard<std::mutex> lock(mutex);
+  if (ready[dev]) return true;
+  for (auto kernel : {mla_decode_fp4_kernel<false>, mla_decode_fp4_kernel<true>}) {
+    cudaFuncAttributes a;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes)) != cudaSuccess ||
+        cudaFuncGetAttributes(&a, kernel) != cudaSuccess)
+      return false;
+    if (a.numRegs < 96) return false;   // the warpgroups' shares add up to 96 a thread
+  }
+  return ready[dev] = true;
+}
 
 mla_status_t decode_fp4_impl(const void* q, const uint8_t* kv_cache, float kv_scale, int64_t num_blocks,
                              const int32_t* block_table, int max_blocks, const int32_t* seqlens, const int32_t* indices,
@@ -148,18 +1297,33 @@ mla_status_t decode_fp4_impl(const void* q, const uint8_t* kv_cache, float kv_sc
   p.scale_log2 = static_cast<float>(scale_log2);
   p.causal = causal_s_q ? 1 : 0;
   p.kv_scale = kv_scale;
+  p.meta = static_cast<const int32_t*>(metadata);
+  p.num_splits = p.meta + kMetaInts * num_sm_parts;
+  p.num_parts = num_sm_parts;
+  const size_t slots = static_cast<size_t>(B) + static_cast<size_t>(num_sm_parts);   // partial outputs in the workspace
+  p.o_part = static_cast<float*>(workspace);
+  p.lse_part = p.o_part + slots * rows * kDimV;
   p.out = reinterpret_cast<__nv_bfloat16*>(out);
   p.lse = lse;
   p.status = device_status_word();
-  if (!p.status) return MLA_ERR_CUDA;
-  if (cudaFuncSetAttribute(mla_decode_fp4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem)) !=
-      cudaSuccess)
+  if (!p.status || !fp4_ready()) return MLA_ERR_CUDA;
+  p.withhold_first_load = take_withheld_load();
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const unsigned cl = 2u * static_cast<unsigned>(p.n_rb);
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = pdl_config(dim3(static_cast<unsigned>(num_sm_parts) * cl), dim3(kThreads), kSmemBytes, cs, attr);
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cl;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.numAttrs = 2;
+  if ((indices ? cudaLaunchKernelEx(&cfg, mla_decode_fp4_kernel<true>, p)
+               : cudaLaunchKernelEx(&cfg, mla_decode_fp4_kernel<false>, p)) != cudaSuccess)
     return MLA_ERR_CUDA;
-  cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg =
-      pdl_config(dim3(static_cast<unsigned>((rows + kRowsCta - 1) / kRowsCta), static_cast<unsigned>(B)), dim3(256), kSmem,
-                 reinterpret_cast<cudaStream_t>(stream), attr);
-  return cudaLaunchKernelEx(&cfg, mla_decode_fp4_kernel, p) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  return launch_combine(p.o_part, p.lse_part, p.num_splits, B, rows, static_cast<int>(slots), p.out, lse, p.status, cs) ==
+                 cudaSuccess
+             ? MLA_OK
+             : MLA_ERR_CUDA;
 }
 
 }  // namespace
