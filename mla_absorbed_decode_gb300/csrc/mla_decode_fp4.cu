@@ -32,6 +32,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 #include <stdint.h>
 
 #include <climits>
@@ -63,7 +64,7 @@ constexpr uint32_t kPktStride = 17 * 1024;
 constexpr uint32_t kKCol = 256;               // S-CTA's TMEM columns: S^T of two tiles at 0 and 128, the keys from 256
 constexpr float kOffset = 6.f;                // P is taken against 2^-6 of the reference maximum
 constexpr float kTop = kOffset + 8.f;         // an exponent past this rebases its head
-constexpr uint64_t kTimeoutNs = 500ull * 1000 * 1000;
+constexpr uint32_t kTimeoutNs = 500u * 1000 * 1000;
 constexpr float kLn2 = 0.69314718055994530942f;
 // registers a thread: the three kinds of warpgroups share what the launch gets (640 x 96)
 constexpr int kRegsMisc = 64, kRegsSoftmax = 120, kRegsConvert = 88;
@@ -79,12 +80,16 @@ constexpr uint32_t kOffInvL = kOffEpi + 8 * 2048;            // O-CTA: output fa
 constexpr uint32_t kOffShared = kOffRaw + 2 * kPageBytes;
 static_assert(kOffInvL + 512 <= kOffShared, "O-CTA layout");
 
+struct Fp4Params : DecodeParams {
+  int q_box;   // q rows of a TMA box
+};
+
 struct Shared {
   // S-CTA
   uint64_t raw_full[2], raw_empty[2];         // a page of the tile has landed; is in the converters' registers
   uint64_t k_full[kKSlots], k_empty[kKSlots];
   uint64_t s_full[2], s_empty[2];
-  uint64_t q_full;                            // the segment's q is in place (a softmax warp each)
+  uint64_t q_raw, q_full, q_empty;            // the segment's q has landed; is fp16 (a softmax warp each); is done with
   uint64_t p_ready[2], st_free[2];            // a warpgroup's packet is written; has been read by its copy
   uint64_t credit[2];                         // the partner's receive slot is free (remote)
   // O-CTA
@@ -104,41 +109,55 @@ constexpr uint32_t kSmemBytes = kOffShared + sizeof(Shared);
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 
 // ------------------------------------------------------------------ waits --
-__device__ __forceinline__ void raise_abort(Shared& sh, int* status, int code, uint32_t cl) {
-  if (!sh.abort) {
-    atomicCAS(status, 0, code);
-    for (uint32_t r = 0; r < cl; ++r) st_cluster_u32(map_to_rank(smem_u32(const_cast<int*>(&sh.abort)), r), 1u);
-  }
-  sh.abort = 1;
+// Every role waits at several places, and the code of 20 warps has to fit the instruction caches (313 KB of it, mostly inlined
+// ways out of waits, ran 220 us where this takes 70), so a wait that gives up only notes it; the warps report when they leave
+// their roles (leave_role).
+enum : int { kRunning = 0, kTold = 1, kTimedOut = 2 };
+__device__ __forceinline__ uint32_t timer_lo() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
 }
-__device__ __forceinline__ bool wait_slow(Shared& sh, uint32_t bar, uint32_t parity, int* status, uint32_t cl, bool cluster) {
-  const uint64_t t0 = global_timer_ns();
-  while (true) {
-    if (cluster ? mbar_test_cluster(bar, parity) : mbar_test(bar, parity)) return true;
+// Bounded wait; false on abort or timeout.
+template <bool Cluster = false>
+__device__ __forceinline__ bool wait_bar(Shared& sh, uint64_t& b, uint32_t parity) {
+  const uint32_t bar = smem_u32(&b);
+  uint32_t t0 = 0;
+  while (!(Cluster ? mbar_test_cluster(bar, parity) : mbar_test(bar, parity))) {
     if (sh.abort) return false;
-    if (global_timer_ns() - t0 > kTimeoutNs) {
-      raise_abort(sh, status, MLA_ERR_TIMEOUT, cl);
+    const uint32_t t = timer_lo() | 1u;
+    if (t0 == 0) t0 = t;
+    if (t - t0 > kTimeoutNs) {
+      sh.abort = kTimedOut;
       return false;
     }
   }
-}
-// Bounded wait; false on abort or timeout (after raising the abort).
-__device__ __forceinline__ bool wait_bar(Shared& sh, uint64_t& b, uint32_t parity, int* status, uint32_t cl,
-                                         bool cluster = false) {
-  const uint32_t bar = smem_u32(&b);
-  if (cluster ? mbar_test_cluster(bar, parity) : mbar_test(bar, parity)) return true;
-  return wait_slow(sh, bar, parity, status, cl, cluster);
+  return true;
 }
 // The same by all lanes, with one answer.
-__device__ __forceinline__ bool warp_wait(Shared& sh, uint64_t& b, uint32_t parity, int* status, uint32_t cl,
-                                          bool cluster = false) {
-  return __all_sync(0xffffffffu, wait_bar(sh, b, parity, status, cl, cluster));
+template <bool Cluster = false>
+__device__ __forceinline__ bool warp_wait(Shared& sh, uint64_t& b, uint32_t parity) {
+  return __all_sync(0xffffffffu, wait_bar<Cluster>(sh, b, parity));
 }
 // Bounded wait that ignores the abort flag: for what is in flight.
 __device__ __forceinline__ void drain_bar(uint64_t& b, uint32_t parity) {
-  const uint64_t t0 = global_timer_ns();
-  while (!mbar_test(smem_u32(&b), parity))
-    if (global_timer_ns() - t0 > kTimeoutNs) return;
+  uint32_t t0 = 0;
+  while (!mbar_test(smem_u32(&b), parity)) {
+    const uint32_t t = timer_lo() | 1u;
+    if (t0 == 0) t0 = t;
+    if (t - t0 > kTimeoutNs) return;
+  }
+}
+// A warp that has left its role tells the cluster if a wait gave up in this CTA.
+__device__ __forceinline__ void leave_role(Shared& sh, int* status, uint32_t cl) {
+  const int why = sh.abort;
+  if (why == kRunning || (threadIdx.x & 31) != 0) return;
+  if (why == kTimedOut) atomicCAS(status, 0, MLA_ERR_TIMEOUT);
+#pragma unroll 1
+  for (uint32_t r = 0; r < cl; ++r) {
+    const uint32_t at = map_to_rank(smem_u32(const_cast<int*>(&sh.abort)), r);
+    if (r != cluster_ctarank()) st_cluster_u32(at, kTold);
+  }
 }
 __device__ __forceinline__ void arrive(uint64_t& b) { mbar_arrive(smem_u32(&b)); }
 __device__ __forceinline__ void arrive2(uint64_t& b) {
@@ -146,6 +165,8 @@ __device__ __forceinline__ void arrive2(uint64_t& b) {
 }
 
 // ------------------------------------------------------------ instructions --
+// A value that all lanes have, as one that the compiler knows to be uniform (operands of MMAs then need no moves).
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 template <int R>
 __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(R)); }
 template <int R>
@@ -155,14 +176,17 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                :: "r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(&bar)) : "memory");
 }
-// 32 (x4) or 16 (x2) columns of 16 TMEM lanes: lane l of the warp gets, in r[4 n + 2 h + e], row 8 h + l / 4, column
+// 64 (x8) or 16 (x2) columns of 16 TMEM lanes: lane l of the warp gets, in r[4 n + 2 h + e], row 8 h + l / 4, column
 // 8 n + 2 (l % 4) + e.
-__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, float (&r)[16]) {
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, float (&r)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
       : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
-        "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+        "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]),
+        "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]),
+        "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
       : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, float (&r)[8]) {
@@ -225,10 +249,10 @@ struct Segment {
 
 // Walks the segments of one part in order (the same walk in every role).
 struct SegmentWalker {
-  const DecodeParams* p;
+  const Fp4Params* p;
   int b_last, k_end, b, kb, split0;
   bool first, done;
-  __device__ void init(const DecodeParams& prm, int part) {
+  __device__ void init(const Fp4Params& prm, int part) {
     p = &prm;
     const int* m = prm.meta + part * kMetaInts;
     b = m[0];
@@ -268,7 +292,7 @@ struct SegmentWalker {
 
 __device__ __forceinline__ int tiles_of(const Segment& s) { return (s.ke - s.kb + 1) >> 1; }
 // Listed tokens of the tile that starts at page k.
-__device__ __forceinline__ int tile_tokens(const DecodeParams& p, const Segment& s, int k) {
+__device__ __forceinline__ int tile_tokens(const Fp4Params& p, const Segment& s, int k) {
   return min(min(kTile, (s.ke - k) * kPageTokens), __ldg(p.lens + s.b) - k * kPageTokens);
 }
 
@@ -278,29 +302,31 @@ struct PageIter {
   Segment s;
   int k;
   bool valid;
-  __device__ void init(const DecodeParams& p, int part) {
+  __device__ void init(const Fp4Params& p, int part) {
     w.init(p, part);
-    valid = w.next(s);
-    k = valid ? s.kb : 0;
+    valid = true;
+    k = 0;
+    s.ke = 0;
   }
-  __device__ void advance() {
+  __device__ bool next() {   // on to the next page, the first one to begin with
     if (valid && ++k >= s.ke) {
       valid = w.next(s);
-      k = valid ? s.kb : 0;
+      k = s.kb;
     }
+    return valid;
   }
 };
 
 // Whether split slot `slot` lies in the workspace, which holds B + num_parts; one outside (metadata that does not fit the
 // call) is reported and not written.
-__device__ __forceinline__ bool split_slot_ok(const DecodeParams& p, int slot) {
+__device__ __forceinline__ bool split_slot_ok(const Fp4Params& p, int slot) {
   if (slot >= 0 && slot < p.B + p.num_parts) return true;
   atomicCAS(p.status, 0, MLA_ERR_DEVICE_BOUNDS);
   return false;
 }
 
 // Page number of page k of request b; one that is out of range is reported, and page 0 read in its place.
-__device__ __forceinline__ int page_of(const DecodeParams& p, int b, int k) {
+__device__ __forceinline__ int page_of(const Fp4Params& p, int b, int k) {
   int blk = -1;
   if (k < p.max_blocks) blk = __ldg(p.block_table + static_cast<int64_t>(b) * p.max_blocks + k);
   if (blk >= 0 && blk < p.num_blocks) return blk;
@@ -308,19 +334,19 @@ __device__ __forceinline__ int page_of(const DecodeParams& p, int b, int k) {
   return 0;
 }
 // Position of list entry e of request b; -1 where the row of indices ends before it (reported).
-__device__ __forceinline__ int entry_of(const DecodeParams& p, int b, int e) {
+__device__ __forceinline__ int entry_of(const Fp4Params& p, int b, int e) {
   if (e < p.idx_stride) return __ldg(p.indices + static_cast<int64_t>(b) * p.idx_stride + e);
   atomicCAS(p.status, 0, MLA_ERR_DEVICE_BOUNDS);
   return -1;
 }
 // Its page; -1 where the position is none of the request's (reported).
-__device__ __forceinline__ int entry_page(const DecodeParams& p, int b, int t) {
+__device__ __forceinline__ int entry_page(const Fp4Params& p, int b, int t) {
   if (t >= 0 && t < __ldg(p.seqlens + b)) return page_of(p, b, t / kPageTokens);
   atomicCAS(p.status, 0, MLA_ERR_DEVICE_BOUNDS);
   return -1;
 }
 // The cached row of a token; row 0 for a bad one, which is always there.
-__device__ __forceinline__ const uint8_t* row_at(const DecodeParams& p, int t, int blk) {
+__device__ __forceinline__ const uint8_t* row_at(const Fp4Params& p, int t, int blk) {
   const int64_t row = blk < 0 ? 0 : static_cast<int64_t>(blk) * kPageTokens + t % kPageTokens;
   return reinterpret_cast<const uint8_t*>(p.kv) + row * kFp4RowBytes;
 }
@@ -328,7 +354,7 @@ __device__ __forceinline__ const uint8_t* row_at(const DecodeParams& p, int t, i
 // A row block's heads: `valid` of its columns are query rows, the MMA has N (a multiple of 16), a softmax warpgroup N / 2.
 struct Block {
   int rb, valid, N, half;
-  __device__ Block(const DecodeParams& p, int rb_) : rb(rb_) {
+  __device__ Block(const Fp4Params& p, int rb_) : rb(rb_) {
     valid = min(kRowsPerPair, p.rows - rb * kRowsPerPair);
     N = (valid + 15) & ~15;
     half = N >> 1;
@@ -339,7 +365,7 @@ struct Block {
 // Warp 0: the two pages of every tile.  Dense: one copy a page (as far as the request has tokens); lists: a copy a
 // row, whose addresses are looked up while the tile before is being loaded.
 template <bool Sparse>
-__device__ void s_load(const DecodeParams& p, Shared& sh, uint32_t smem, int part, uint32_t cl) {
+__device__ void s_load(const Fp4Params& p, const CUtensorMap* q_map, Shared& sh, uint32_t smem, int part, const Block& blk) {
   const int lane = threadIdx.x & 31;
   SegmentWalker w;
   w.init(p, part);
@@ -348,8 +374,17 @@ __device__ void s_load(const DecodeParams& p, Shared& sh, uint32_t smem, int par
   bool withhold = p.withhold_first_load != 0;   // test hook: the first page never arrives
   bool ok = true, armed[2] = {false, false};
   uint32_t phase[2] = {0, 0};                   // of the last loads into each page
+  uint32_t seg = 0;
   while (ok && w.next(s)) {
     const int L = __ldg(p.lens + s.b);
+    if (!warp_wait(sh, sh.q_empty, (seg & 1) ^ 1)) break;   // (the MMAs of the segment before are done)
+    if (lane == 0) {   // 64 dims of the block's rows a box; rows past the request's are another's, or zeros past q's end
+      mbar_arrive_expect_tx(smem_u32(&sh.q_raw), 9u * static_cast<uint32_t>(p.q_box) * 128u);
+      for (int c = 0; c < 9; ++c)
+        tma_load_3d(smem + c * kQChunk, q_map, smem_u32(&sh.q_raw), 0, s.b * p.rows + blk.rb * kRowsPerPair, c);
+    }
+    __syncwarp();
+    ++seg;
     for (int k = s.kb; ok && k < s.ke; k += 2, ++T) {
       for (int h = 0; h < 2; ++h) {
         const int n = k + h < s.ke ? min(kPageTokens, L - (k + h) * kPageTokens) : 0;   // rows
@@ -365,7 +400,7 @@ __device__ void s_load(const DecodeParams& p, Shared& sh, uint32_t smem, int par
         } else if (n > 0) {
           row[0] = row_at(p, 0, page_of(p, s.b, k + h));
         }
-        if (!warp_wait(sh, sh.raw_empty[h], (T & 1) ^ 1, p.status, cl)) {
+        if (!warp_wait(sh, sh.raw_empty[h], (T & 1) ^ 1)) {
           ok = false;
           break;
         }
@@ -393,13 +428,14 @@ __device__ void s_load(const DecodeParams& p, Shared& sh, uint32_t smem, int par
   if (lane == 0)   // loads still in flight land before the CTA may leave
     for (int h = 0; h < 2; ++h)
       if (armed[h]) drain_bar(sh.raw_full[h], phase[h]);
+  if (lane == 0 && seg > 0) drain_bar(sh.q_raw, (seg - 1) & 1);
   __syncwarp();
 }
 
 // Warps 12..19: a thread a token; warpgroup c takes latent dims [256 c, 256 c + 256) and half of the rope dims.  A tile's codes
 // are read into registers at once, which frees the page buffers for the next tile's loads.  Rows are 352 bytes: lanes 4
 // rows apart would hit the same banks, so rows with bit 2 set read each pair of units the other way round.
-__device__ void s_convert(const DecodeParams& p, Shared& sh, uint32_t smem, int part, uint32_t cl, int c) {
+__device__ void s_convert(const Fp4Params& p, Shared& sh, uint32_t smem, int part, int c) {
   const int quad = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const int h = quad >> 1;                                   // page of the tile
   const int r = (quad & 1) * 32 + lane;                      // row of the page
@@ -418,7 +454,7 @@ __device__ void s_convert(const DecodeParams& p, Shared& sh, uint32_t smem, int 
   uint32_t T = 0;
   while (w.next(s)) {
     for (int t = tiles_of(s); t > 0; --t, ++T) {
-      if (!warp_wait(sh, sh.raw_full[h], T & 1, p.status, cl)) return;
+      if (!warp_wait(sh, sh.raw_full[h], T & 1)) return;
       uint32_t code[4][8], rope[8];
 #pragma unroll
       for (int k = 0; k < 4; ++k) pair(128 * c + 32 * k, code[k]);
@@ -436,7 +472,7 @@ __device__ void s_convert(const DecodeParams& p, Shared& sh, uint32_t smem, int 
         values16(code[k][2], code[k][3], __byte_perm(s01, 0, 0x3232), v + 8);
         values16(code[k][4], code[k][5], __byte_perm(s23, 0, 0x1010), v + 16);
         values16(code[k][6], code[k][7], __byte_perm(s23, 0, 0x3232), v + 24);
-        if (!warp_wait(sh, sh.k_empty[slot], ((i / kKSlots) & 1) ^ 1, p.status, cl)) return;
+        if (!warp_wait(sh, sh.k_empty[slot], ((i / kKSlots) & 1) ^ 1)) return;
         tc_fence_after();
         tmem_st32(tm + slot * 32, v);
         tmem_wait_st();
@@ -448,7 +484,7 @@ __device__ void s_convert(const DecodeParams& p, Shared& sh, uint32_t smem, int 
       uint32_t v[16];
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[2 * j] = e4m3x2_to_f16x2<0>(rope[j]), v[2 * j + 1] = e4m3x2_to_f16x2<1>(rope[j]);
-      if (!warp_wait(sh, sh.k_empty[slot], ((i / kKSlots) & 1) ^ 1, p.status, cl)) return;
+      if (!warp_wait(sh, sh.k_empty[slot], ((i / kKSlots) & 1) ^ 1)) return;
       tc_fence_after();
       tmem_st16(tm + slot * 32 + 16 * c, v);
       tmem_wait_st();
@@ -460,39 +496,41 @@ __device__ void s_convert(const DecodeParams& p, Shared& sh, uint32_t smem, int 
 }
 
 // Warp 1 (all lanes; an elected one issues): S^T = K Q^T, 36 steps of 16 dims a tile.
-__device__ void s_mma(const DecodeParams& p, Shared& sh, uint32_t smem, int part, uint32_t cl, const Block& blk) {
+__device__ void s_mma(const Fp4Params& p, Shared& sh, uint32_t smem, int part, const Block& blk) {
   SegmentWalker w;
   w.init(p, part);
   Segment s;
   uint32_t i = 0, T = 0, seg = 0;
-  const uint32_t tmem = sh.tmem_base;
-  const uint32_t idesc = idesc_f16_f32(kTile, blk.N, 0, 0);
+  const uint32_t tmem = uniform(sh.tmem_base);
+  const uint32_t idesc = uniform(idesc_f16_f32(kTile, blk.N, 0, 0));
   bool ok = true;
   while (ok && w.next(s)) {
-    if (!warp_wait(sh, sh.q_full, seg & 1, p.status, cl)) break;
+    if (!warp_wait(sh, sh.q_full, seg & 1)) break;
     for (int t = tiles_of(s); ok && t > 0; --t, ++T) {
       const uint32_t sb = T & 1;
-      if (!warp_wait(sh, sh.s_empty[sb], ((T >> 1) & 1) ^ 1, p.status, cl)) {
+      if (!warp_wait(sh, sh.s_empty[sb], ((T >> 1) & 1) ^ 1)) {
         ok = false;
         break;
       }
-#pragma unroll
+      const uint32_t d = uniform(tmem + sb * kTile);
+#pragma unroll 1
       for (int it = 0; it < kItems; ++it, ++i) {
         const uint32_t slot = i % kKSlots;
-        if (!warp_wait(sh, sh.k_full[slot], (i / kKSlots) & 1, p.status, cl)) {
+        if (!warp_wait(sh, sh.k_full[slot], (i / kKSlots) & 1)) {
           ok = false;
           break;
         }
         tc_fence_after();
         const int chunk = it < 8 ? (it >> 1) + 4 * (it & 1) : 8;   // the warpgroups' chunks in turn
+        const uint32_t a = uniform(tmem + kKCol + slot * 32), q = uniform(smem + chunk * kQChunk), go_on = uniform(it > 0);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          mma_bf16_ts_warp(tmem + sb * kTile, tmem + kKCol + slot * 32 + j * 8,
-                           smem_desc_sw128(smem + chunk * kQChunk + j * 32, 16, 1024), idesc, it | j ? 1u : 0u);
+          mma_bf16_ts_warp(d, a + j * 8, smem_desc_sw128(q + j * 32, 16, 1024), idesc, j ? 1u : go_on);
         mma_commit_warp(smem_u32(&sh.k_empty[slot]));
       }
       if (ok) mma_commit_warp(smem_u32(&sh.s_full[sb]));
     }
+    if (ok) mma_commit_warp(smem_u32(&sh.q_empty));
     ++seg;
   }
   mma_commit_warp(smem_u32(&sh.drain));   // behind everything issued
@@ -500,53 +538,40 @@ __device__ void s_mma(const DecodeParams& p, Shared& sh, uint32_t smem, int part
   __syncwarp();
 }
 
-// Rows of q of warpgroup w's heads, 4 at a time a warp, into shared memory as fp16, with their scores' factors.
-__device__ void s_load_q(const DecodeParams& p, Shared& sh, uint32_t smem, int b, const Block& blk, int w, int wq, int lane) {
+// Rows of q of warpgroup w's heads, in place: bf16 as loaded to fp16, a warp a row, and their scores' factors.
+__device__ __forceinline__ void s_scale_q(const Fp4Params& p, Shared& sh, uint32_t smem, const Block& blk, int w, int wq, int lane) {
   const float unit = p.scale_log2 * p.kv_scale;
-  for (int j0 = 0; j0 < blk.half; j0 += 16) {
-    uint4 v[4][3];
+#pragma unroll 2
+  for (int j = wq; j < blk.half; j += 4) {
+    const int n = w * blk.half + j;
+    const uint32_t at = smem + (lane >> 3) * kQChunk + n * 128 + (((lane & 7) ^ (n & 7)) << 4);   // 16 bytes of chunk lane / 8
+    uint4 v[3];
+    v[0] = ld_shared_v4(at);
+    v[1] = ld_shared_v4(at + 4 * kQChunk);
+    v[2] = lane < 8 ? ld_shared_v4(at + 8 * kQChunk) : make_uint4(0, 0, 0, 0);
+    float top = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = w * blk.half + j0 + 4 * j + wq;
-      const bool have = j0 + 4 * j < blk.half && n < blk.valid;
-      const uint4* src = reinterpret_cast<const uint4*>(
-          p.q + (static_cast<int64_t>(b) * p.rows + blk.rb * kRowsPerPair + (have ? n : 0)) * kDimQK);
+    for (int u = 0; u < 3; ++u) {
+      const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
 #pragma unroll
-      for (int u = 0; u < 3; ++u)
-        v[j][u] = have && lane + 32 * u < kDimQK / 8 ? __ldg(src + lane + 32 * u) : make_uint4(0, 0, 0, 0);
+      for (int e = 0; e < 4; ++e) top = max_nan(top, max_nan(fabsf(bf16_lo(x[e])), fabsf(bf16_hi(x[e]))));
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = w * blk.half + j0 + 4 * j + wq;
-      float top = 0.f;
+    for (int o = 16; o >= 1; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const bool finite = top <= 3.4e38f;
+    const int e = finite ? max(static_cast<int>(__float_as_uint(top) >> 23), 41) : 141;   // at most a factor 2^100
+    // (a row with an infinity or a NaN becomes NaN; the factor is never 0, so that scores of -inf stay what they are)
+    const float sc = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
+    const float back = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
 #pragma unroll
-      for (int u = 0; u < 3; ++u) {
-        const uint32_t x[4] = {v[j][u].x, v[j][u].y, v[j][u].z, v[j][u].w};
+    for (int u = 0; u < 3; ++u) {
+      const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+      uint32_t y[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) top = max_nan(top, max_nan(fabsf(bf16_lo(x[e])), fabsf(bf16_hi(x[e]))));
-      }
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const bool finite = top <= 3.4e38f;
-      const int e = finite ? max(static_cast<int>(__float_as_uint(top) >> 23), 41) : 141;   // at most a factor 2^100
-      const float sc = finite ? __uint_as_float(static_cast<uint32_t>(268 - e) << 23) : 0.f;
-      // (a row with an infinity or a NaN gets scores of NaN; the factor is never 0, so that masks stay -inf)
-      const float back = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
-      if (j0 + 4 * j >= blk.half) break;
-#pragma unroll
-      for (int u = 0; u < 3; ++u) {
-        const int unit16 = lane + 32 * u;
-        if (unit16 < kDimQK / 8) {
-          const uint32_t x[4] = {v[j][u].x, v[j][u].y, v[j][u].z, v[j][u].w};
-          uint32_t y[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) y[q] = finite ? pack_f16x2(bf16_lo(x[q]) * sc, bf16_hi(x[q]) * sc) : 0u;
-          st_shared_v4(smem + (unit16 >> 3) * kQChunk + n * 128 + (((unit16 & 7) ^ (n & 7)) << 4),
-                       make_uint4(y[0], y[1], y[2], y[3]));
-        }
-      }
-      if (lane == 0) sh.q_scale[n] = finite ? fmaxf(unit * back, 0x1p-126f) : NAN;
+      for (int q = 0; q < 4; ++q) y[q] = finite ? pack_f16x2(bf16_lo(x[q]) * sc, bf16_hi(x[q]) * sc) : 0x7E007E00u;
+      if (u < 2 || lane < 8) st_shared_v4(at + 4 * u * kQChunk, make_uint4(y[0], y[1], y[2], y[3]));
     }
+    if (lane == 0) sh.q_scale[n] = fmaxf(unit * back, 0x1p-126f);
   }
   fence_proxy_async_smem();
   __syncwarp();
@@ -556,7 +581,7 @@ __device__ void s_load_q(const DecodeParams& p, Shared& sh, uint32_t smem, int b
 // Warps 4..11: warpgroup w has heads [w N/2, (w + 1) N/2) of the block.  Thread l of a warp has four of a tile's tokens (rows l / 4
 // + 8 {0..3} of the warp's TMEM quadrant) and up to 16 heads (8 i + 2 (l % 4) + {0, 1}).
 template <bool Sparse>
-__device__ void s_softmax(const DecodeParams& p, Shared& sh, uint32_t smem, int part, uint32_t cl, const Block& blk) {
+__device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int part, const Block& blk) {
   const int t = threadIdx.x - 128, w = t >> 7, wq = (t >> 5) & 3, lane = t & 31, tr = lane >> 2, tc = lane & 3;
   const uint32_t bar = 1 + w;                     // named barrier of the warpgroup
   const int units = blk.half >> 3;                // of 8 heads
@@ -567,12 +592,15 @@ __device__ void s_softmax(const DecodeParams& p, Shared& sh, uint32_t smem, int 
   SegmentWalker walk;
   walk.init(p, part);
   Segment s;
-  uint32_t T = 0;
+  uint32_t T = 0, seg = 0;
   bool ok = true;
   while (ok && walk.next(s)) {
     const int L = __ldg(p.lens + s.b);
     const int L_seq = Sparse ? __ldg(p.seqlens + s.b) : L;
-    s_load_q(p, sh, smem, s.b, blk, w, wq, lane);   // (every MMA of the segment before is complete: its last S was waited for)
+    const bool got = wait_bar(sh, sh.q_raw, seg & 1);
+    if (named_bar_or(bar, 128, !got)) break;
+    ++seg;
+    s_scale_q(p, sh, smem, blk, w, wq, lane);
     named_bar_sync(bar, 128);
     float2 sl[8], nm[8], l[8];                       // score factor, offset - reference maximum (log2), sum of the thread's tokens
     uint32_t fresh = 0;                              // heads that have no reference yet, two bits a unit
@@ -605,75 +633,68 @@ __device__ void s_softmax(const DecodeParams& p, Shared& sh, uint32_t smem, int 
           }
         }
       }
-      bool ok_t = wait_bar(sh, sh.s_full[sb], (T >> 1) & 1, p.status, cl);
-      if (ok_t) ok_t = wait_bar(sh, sh.st_free[w], (T & 1) ^ 1, p.status, cl);   // the last packet has been read
+      bool ok_t = wait_bar(sh, sh.s_full[sb], (T >> 1) & 1);
+      if (ok_t) ok_t = wait_bar(sh, sh.st_free[w], (T & 1) ^ 1);   // the last packet has been read
       __syncwarp();
       tc_fence_after();
-      float2 ls[8];
-      uint32_t top = 0;   // largest P, two fp16
-      auto limit = [&](int col) {
-        return p.causal ? L_seq - p.s_q + sh.pos[w * blk.half + col] + 1 : INT_MAX;
+      // the score of token row j (of the thread's four) and head c, seen or not
+      auto mask = [&](float& x, int j, int c) {
+        const int limit = p.causal ? L_seq - p.s_q + sh.pos[w * blk.half + c] + 1 : INT_MAX;
+        if (key[j] >= limit) x = -INFINITY;
       };
-      auto exponentials = [&] {
+      float2 ls[8];
+      bool rebased = false;
+      while (true) {   // once, or twice where references have to move
+        uint32_t top = 0;   // largest P, two fp16
 #pragma unroll
         for (int i = 0; i < 8; ++i) ls[i] = make_float2(0.f, 0.f);
-        const uint32_t at0 = tm + sb * kTile;
-        float xa[16], xb[16];   // the next 32 columns are on their way while these are worked on
-        auto work = [&](int part4, const float (&x)[16]) {   // part4: token rows 16 (part4 % 2), units from 4 (part4 / 2)
-          const int hf = part4 & 1, i0 = 4 * (part4 >> 1);
+#pragma unroll 1
+        for (int hf = 0; hf < 2; ++hf) {
+          const uint32_t at = tm + sb * kTile + (static_cast<uint32_t>(16 * hf) << 16);
+          const int row = st_row + 16 * hf;
+          float x[32];   // [unit][token row 8 of 16][head 2]
+          tmem_ld_16x256(at, x);
+          tmem_wait_ld();
+          if (masked) {
+            const int k0 = hf ? key[2] : key[0], k1 = hf ? key[3] : key[1];
 #pragma unroll
-          for (int ii = 0; ii < 2; ++ii) {
-            if (i0 + 2 * ii >= units) break;
+            for (int e = 0; e < 16; ++e) {   // heads 8 (e / 2) + 2 tc + e % 2
+              const int c = 8 * (e >> 1) + 2 * tc + (e & 1);
+              const int limit = p.causal ? L_seq - p.s_q + sh.pos[min(w * blk.half + c, 127)] + 1 : INT_MAX;
+              if (k0 >= limit) x[4 * (e >> 1) + (e & 1)] = -INFINITY;
+              if (k1 >= limit) x[4 * (e >> 1) + 2 + (e & 1)] = -INFINITY;
+            }
+          }
+#pragma unroll
+          for (int ii = 0; ii < 4; ++ii) {
+            if (2 * ii >= units) break;
             uint32_t pk[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {   // unit i0 + 2 ii + q / 2, token row q % 2
-              const int i = i0 + 2 * ii + (q >> 1), at = 8 * ii + 2 * q;
-              float2 y = fma2(make_float2(x[at], x[at + 1]), sl[i], nm[i]);
-              if (masked) {
-                const int c = 8 * i + 2 * tc, kk = key[2 * hf + (q & 1)];
-                if (!(kk < limit(c))) y.x = -INFINITY;
-                if (!(kk < limit(c + 1))) y.y = -INFINITY;
-              }
+            for (int q = 0; q < 4; ++q) {   // unit 2 ii + q / 2, token row q % 2
+              const int i = 2 * ii + (q >> 1);
+              float2 y = fma2(make_float2(x[8 * ii + 2 * q], x[8 * ii + 2 * q + 1]), sl[i], nm[i]);
               y.x = fast_exp2(y.x);
               y.y = fast_exp2(y.y);
               ls[i] = add2(ls[i], y);
               pk[q] = pack_f16x2(y.x, y.y);
               top = max_f16x2(top, pk[q]);
             }
-            const int row = st_row + 16 * hf;
-            stmatrix4(pkt + row * 128 + (((i0 + 2 * ii + st_unit) ^ (row & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
+            stmatrix4(pkt + row * 128 + (((2 * ii + st_unit) ^ (row & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
           }
-        };
-        constexpr uint32_t kRow16 = 16u << 16;
-        tmem_ld_16x256(at0, xa);
-        tmem_wait_ld();
-        tmem_ld_16x256(at0 + kRow16, xb);
-        work(0, xa);
-        tmem_wait_ld();
-        if (units > 4) tmem_ld_16x256(at0 + 32, xa);
-        work(1, xb);
-        if (units > 4) {
-          tmem_wait_ld();
-          tmem_ld_16x256(at0 + kRow16 + 32, xb);
-          work(2, xa);
-          tmem_wait_ld();
-          work(3, xb);
         }
-      };
-      exponentials();
-      // a P past 2^14 (0x7400 in fp16), or a head without a reference: the tile again, with new references
-      const bool again = fresh != 0 || (top & 0xFFFFu) > 0x7400u || (top >> 16) > 0x7400u || !ok_t;
-      fence_proxy_async_smem();
-      tc_fence_before();
-      bool rebased = false;
-      if (named_bar_or(bar, 128, again)) {
+        fence_proxy_async_smem();
+        tc_fence_before();
+        if (rebased) break;
+        // a P past 2^14 (0x7400 in fp16), or a head without a reference: the tile again, with new references
+        const bool again = fresh != 0 || (top & 0xFFFFu) > 0x7400u || (top >> 16) > 0x7400u || !ok_t;
+        if (!named_bar_or(bar, 128, again)) break;
         if (named_bar_or(bar, 128, !ok_t)) {
           ok = false;
           break;
         }
-#pragma unroll
-        for (int ii = 0; ii < 4; ++ii) {   // the heads' maxima over the warp's tokens, two units at a time
-          if (2 * ii >= units) break;
+        rebased = true;
+#pragma unroll 1
+        for (int ii = 0; 2 * ii < units; ++ii) {   // the heads' largest scores over the warp's tokens, two units at a time
           float2 cm[2] = {make_float2(-INFINITY, -INFINITY), make_float2(-INFINITY, -INFINITY)};
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
@@ -682,14 +703,11 @@ __device__ void s_softmax(const DecodeParams& p, Shared& sh, uint32_t smem, int 
             tmem_wait_ld();
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const int u = q >> 1, i = 2 * ii + u;
-              float2 y = make_float2(x[2 * q] * sl[i].x, x[2 * q + 1] * sl[i].y);
               if (masked) {
-                const int c = 8 * i + 2 * tc, kk = key[2 * hf + (q & 1)];
-                if (!(kk < limit(c))) y.x = -INFINITY;
-                if (!(kk < limit(c + 1))) y.y = -INFINITY;
+                mask(x[2 * q], 2 * hf + (q & 1), min(16 * ii + 8 * (q >> 1) + 2 * tc, 126 - w * blk.half));
+                mask(x[2 * q + 1], 2 * hf + (q & 1), min(16 * ii + 8 * (q >> 1) + 2 * tc + 1, 127 - w * blk.half));
               }
-              cm[u] = make_float2(fmaxf(cm[u].x, y.x), fmaxf(cm[u].y, y.y));
+              cm[q >> 1] = make_float2(fmaxf(cm[q >> 1].x, x[2 * q]), fmaxf(cm[q >> 1].y, x[2 * q + 1]));
             }
           }
 #pragma unroll
@@ -710,7 +728,8 @@ __device__ void s_softmax(const DecodeParams& p, Shared& sh, uint32_t smem, int 
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int c = 8 * i + 2 * tc + e;
-              const float m = fmaxf(fmaxf(sh.part[w][0][c], sh.part[w][1][c]), fmaxf(sh.part[w][2][c], sh.part[w][3][c]));
+              const float m = fmaxf(fmaxf(sh.part[w][0][c], sh.part[w][1][c]), fmaxf(sh.part[w][2][c], sh.part[w][3][c])) *
+                              (e ? sl[i].y : sl[i].x);
               float& n = e ? nm[i].y : nm[i].x;
               float& sum = e ? l[i].y : l[i].x;
               const uint32_t bit = 1u << (2 * i + e);
@@ -726,11 +745,8 @@ __device__ void s_softmax(const DecodeParams& p, Shared& sh, uint32_t smem, int 
               asm volatile("st.shared.v2.f32 [%0], {%1, %2};" :: "r"(pkt + kPktAlpha + (8 * i + 2 * tc) * 4), "f"(alpha[0]),
                            "f"(alpha[1]) : "memory");
           }
-        exponentials();
-        fence_proxy_async_smem();
-        tc_fence_before();
-        rebased = true;
       }
+      if (!ok) break;
       __syncwarp();
       if (lane == 0) arrive(sh.s_empty[sb]);   // S^T has been read
 #pragma unroll
@@ -780,7 +796,7 @@ __device__ void s_softmax(const DecodeParams& p, Shared& sh, uint32_t smem, int 
 }
 
 // Warps 2 and 3 (a lane each): warpgroup w's packets to the partner.
-__device__ void s_ship(const DecodeParams& p, Shared& sh, uint32_t smem, int part, uint32_t cl, uint32_t peer, int w) {
+__device__ void s_ship(const Fp4Params& p, Shared& sh, uint32_t smem, int part, uint32_t peer, int w) {
   const uint32_t src = smem + kOffSend + w * kPktStride, dst = map_to_rank(smem + w * kPktStride, peer);
   const uint32_t full = map_to_rank(smem_u32(&sh.p_full[0]), peer);
   SegmentWalker walk;
@@ -791,8 +807,8 @@ __device__ void s_ship(const DecodeParams& p, Shared& sh, uint32_t smem, int par
   while (ok && walk.next(s)) {
     for (int t = tiles_of(s); t > 0; --t, ++T) {
       const uint32_t slot = T & 1;
-      if (!wait_bar(sh, sh.p_ready[w], T & 1, p.status, cl) ||
-          !wait_bar(sh, sh.credit[slot], ((T >> 1) & 1) ^ 1, p.status, cl, true)) {
+      if (!wait_bar(sh, sh.p_ready[w], T & 1) ||
+          !wait_bar<true>(sh, sh.credit[slot], ((T >> 1) & 1) ^ 1)) {
         ok = false;
         break;
       }
@@ -811,7 +827,7 @@ __device__ void s_ship(const DecodeParams& p, Shared& sh, uint32_t smem, int par
 // dims in either half.  Four lanes apart two rows and a unit pair: a quarter warp reads 32 bytes of four rows and writes eight different banks.
 // Addresses are looked up two pages ahead, codes loaded one page ahead.
 template <bool Sparse>
-__device__ void o_convert(const DecodeParams& p, Shared& sh, uint32_t smem, int part, uint32_t cl) {
+__device__ void o_convert(const Fp4Params& p, Shared& sh, uint32_t smem, int part) {
   const int v = (threadIdx.x >> 5) - 12, lane = threadIdx.x & 31;
   const int u0 = lane & 1, rr = (lane >> 1) & 3, q = lane >> 3;
   const int r0 = 4 * v + rr;              // rows r0 and r0 + 32
@@ -822,9 +838,9 @@ __device__ void o_convert(const DecodeParams& p, Shared& sh, uint32_t smem, int 
   PageIter it;
   it.init(p, part);
   auto fetch_tokens = [&] {
-    tok.valid = it.valid;
+    tok.valid = it.next();
     tok.n = 0;
-    if (!it.valid) return;
+    if (!tok.valid) return;
     tok.b = it.s.b;
     tok.k = it.k;
     tok.n = min(kPageTokens, __ldg(p.lens + it.s.b) - it.k * kPageTokens);
@@ -835,7 +851,6 @@ __device__ void o_convert(const DecodeParams& p, Shared& sh, uint32_t smem, int 
         tok.t[g] = r0 + 32 * g < tok.n && e < p.idx_stride ? __ldg(p.indices + static_cast<int64_t>(it.s.b) * p.idx_stride + e) : -1;
       }
     }
-    it.advance();
   };
   auto fetch_rows = [&] {   // (what is out of range is reported by the S-CTA's loads and read as row or page 0 here)
     rows.valid = tok.valid;
@@ -878,7 +893,7 @@ __device__ void o_convert(const DecodeParams& p, Shared& sh, uint32_t smem, int 
 #pragma unroll
     for (int h = 0; h < 2; ++h, ++i) {
       const uint32_t slot = i % kVSlots;
-      if (!warp_wait(sh, sh.v_empty[slot], ((i / kVSlots) & 1) ^ 1, p.status, cl)) return false;
+      if (!warp_wait(sh, sh.v_empty[slot], ((i / kVSlots) & 1) ^ 1)) return false;
       const uint32_t base = smem + kOffV + slot * kVSlot + q * kVChunk;
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
@@ -903,33 +918,28 @@ __device__ void o_convert(const DecodeParams& p, Shared& sh, uint32_t smem, int 
     }
     return true;
   };
-  fetch_tokens();
-  fetch_rows();
-  fetch_tokens();
-  fetch_codes(cur);
-  fetch_rows();
-  fetch_tokens();
-  while (cur.valid) {
+  cur.valid = rows.valid = tok.valid = false;
+  do {
     fetch_codes(nxt);
     fetch_rows();
     fetch_tokens();
-    if (!convert(cur)) return;
+    if (cur.valid && !convert(cur)) return;
     cur = nxt;
-  }
+  } while (cur.valid || rows.valid || tok.valid);
 }
 
 // Warp 1 (all lanes; an elected one issues): O += P V, for every page and 256-column half of O a step per 16 tokens.
-__device__ void o_mma(const DecodeParams& p, Shared& sh, uint32_t smem, int part, uint32_t cl) {
+__device__ void o_mma(const Fp4Params& p, Shared& sh, uint32_t smem, int part) {
   const int lane = threadIdx.x & 31;
   SegmentWalker w;
   w.init(p, part);
   Segment s;
   uint32_t T = 0, i = 0, seg = 0, nresc = 0;
-  const uint32_t tmem = sh.tmem_base;
+  const uint32_t tmem = uniform(sh.tmem_base);
   constexpr uint32_t idesc = idesc_f16_f32(128, 256, 1, 1);
   bool ok = true;
   while (ok && w.next(s)) {
-    if (seg > 0 && !warp_wait(sh, sh.o_free, (seg - 1) & 1, p.status, cl)) {
+    if (seg > 0 && !warp_wait(sh, sh.o_free, (seg - 1) & 1)) {
       ok = false;
       break;
     }
@@ -940,7 +950,7 @@ __device__ void o_mma(const DecodeParams& p, Shared& sh, uint32_t smem, int part
       const int ntok = tile_tokens(p, s, k);
       if (lane == 0) mbar_arrive_expect_tx(smem_u32(&sh.p_full[slot]), 2 * kPktBytes);
       __syncwarp();
-      if (!warp_wait(sh, sh.p_full[slot], (T >> 1) & 1, p.status, cl, true)) {
+      if (!warp_wait<true>(sh, sh.p_full[slot], (T >> 1) & 1)) {
         ok = false;
         break;
       }
@@ -950,7 +960,7 @@ __device__ void o_mma(const DecodeParams& p, Shared& sh, uint32_t smem, int part
       __syncwarp();
       if (k != s.kb && __any_sync(0xffffffffu, __float_as_uint(flag) != 0)) {   // scale O before adding this tile
         mma_commit_warp(smem_u32(&sh.o_sync));
-        if (!warp_wait(sh, sh.o_sync, nresc & 1, p.status, cl)) {
+        if (!warp_wait(sh, sh.o_sync, nresc & 1)) {
           ok = false;
           break;
         }
@@ -960,38 +970,31 @@ __device__ void o_mma(const DecodeParams& p, Shared& sh, uint32_t smem, int part
           arrive(sh.corr_go);
         }
         __syncwarp();
-        if (!warp_wait(sh, sh.corr_done, nresc & 1, p.status, cl)) {
+        if (!warp_wait(sh, sh.corr_done, nresc & 1)) {
           ok = false;
           break;
         }
         ++nresc;
       }
       tc_fence_after();
-      for (int pg = 0; ok && pg < 2 && k + pg < s.ke; ++pg) {
+#pragma unroll 1
+      for (int ph = 0; ph < 4 && k + (ph >> 1) < s.ke; ++ph, ++i) {   // half ph % 2 of page ph / 2
+        const int pg = ph >> 1;
         const int ksteps = (min(kPageTokens, ntok - pg * kPageTokens) + 15) >> 4;
-        const uint32_t a = pkt + pg * kPageTokens * 128;
-#pragma unroll
-        for (int h = 0; h < 2; ++h, ++i) {
-          const uint32_t vs = i % kVSlots;
-          if (!warp_wait(sh, sh.v_full[vs], (i / kVSlots) & 1, p.status, cl)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t vb = smem + kOffV + vs * kVSlot;
-          const uint32_t first = k == s.kb && pg == 0 ? 0u : 1u;
-          if (ksteps == 4) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              mma_bf16_ss_warp(tmem + 256 * h, smem_desc_sw128(a + j * 2048, kPktStride, 1024),
-                               smem_desc_sw128(vb + j * 2048, kVChunk, 1024), idesc, j ? 1u : first);
-          } else {
-            for (int j = 0; j < ksteps; ++j)
-              mma_bf16_ss_warp(tmem + 256 * h, smem_desc_sw128(a + j * 2048, kPktStride, 1024),
-                               smem_desc_sw128(vb + j * 2048, kVChunk, 1024), idesc, j ? 1u : first);
-          }
-          mma_commit_warp(smem_u32(&sh.v_empty[vs]));
+        const uint32_t vs = i % kVSlots;
+        if (!warp_wait(sh, sh.v_full[vs], (i / kVSlots) & 1)) {
+          ok = false;
+          break;
         }
+        tc_fence_after();
+        const uint32_t d = uniform(tmem + 256 * (ph & 1)), a = uniform(pkt + pg * kPageTokens * 128);
+        const uint32_t vb = uniform(smem + kOffV + vs * kVSlot), go_on = uniform(k != s.kb || pg > 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j < ksteps)
+            mma_bf16_ss_warp(d, smem_desc_sw128(a + j * 2048, kPktStride, 1024), smem_desc_sw128(vb + j * 2048, kVChunk, 1024),
+                             idesc, j ? 1u : go_on);
+        mma_commit_warp(smem_u32(&sh.v_empty[vs]));
       }
       if (!ok) break;
       mma_commit_warp(smem_u32(&sh.p_free[slot]));
@@ -1006,7 +1009,7 @@ __device__ void o_mma(const DecodeParams& p, Shared& sh, uint32_t smem, int part
     }
     ++seg;
   }
-  if (ok && seg > 0) warp_wait(sh, sh.o_free, (seg - 1) & 1, p.status, cl);   // the last epilogue has taken its command
+  if (ok && seg > 0) warp_wait(sh, sh.o_free, (seg - 1) & 1);   // the last epilogue has taken its command
   mma_commit_warp(smem_u32(&sh.drain));   // behind everything issued
   drain_bar(sh.drain, 0);
   __syncwarp();
@@ -1018,7 +1021,7 @@ __device__ void o_mma(const DecodeParams& p, Shared& sh, uint32_t smem, int part
 }
 
 // A lane of warp 2: gives packet slots back to the S-CTA once the MMAs are done with them.
-__device__ void o_forward(const DecodeParams& p, Shared& sh, int part, uint32_t cl, uint32_t peer) {
+__device__ void o_forward(const Fp4Params& p, Shared& sh, int part, uint32_t peer) {
   SegmentWalker w;
   w.init(p, part);
   Segment s;
@@ -1026,14 +1029,14 @@ __device__ void o_forward(const DecodeParams& p, Shared& sh, int part, uint32_t 
   const uint32_t credit = map_to_rank(smem_u32(&sh.credit[0]), peer);
   while (w.next(s))
     for (int t = tiles_of(s); t > 0; --t, ++T) {
-      if (!wait_bar(sh, sh.p_free[T & 1], (T >> 1) & 1, p.status, cl)) return;
+      if (!wait_bar(sh, sh.p_free[T & 1], (T >> 1) & 1)) return;
       mbar_arrive_remote(credit + (T & 1) * 8);
     }
 }
 
 // Warps 4..11: rescale O's rows, or normalise and store a finished segment.  Warpgroup wg owns O's columns [256 wg, 256 wg + 256).
 // TMEM lane m is head (m / 64) N/2 + m % 64 of the block, where m % 64 < N/2.
-__device__ void o_epilogue(const DecodeParams& p, Shared& sh, uint32_t smem, int part, uint32_t cl, const Block& blk) {
+__device__ void o_epilogue(const Fp4Params& p, Shared& sh, uint32_t smem, int part, const Block& blk) {
   const int t = threadIdx.x - 128, wg = t >> 7, r = t & 127, wq = r >> 5, lane = r & 31;
   const uint32_t tmem_row = sh.tmem_base + (static_cast<uint32_t>(wq * 32) << 16) + wg * 256;
   const int h0 = 32 * (wq & 1), n0 = (wq >> 1) * blk.half + h0;                  // the warp's first head
@@ -1044,7 +1047,7 @@ __device__ void o_epilogue(const DecodeParams& p, Shared& sh, uint32_t smem, int
   uint32_t ncmd = 0, seg = 0;
   bool have = w.next(s);
   while (true) {
-    if (!warp_wait(sh, sh.corr_go, ncmd & 1, p.status, cl)) break;
+    if (!warp_wait(sh, sh.corr_go, ncmd & 1)) break;
     ++ncmd;
     const int cmd = sh.cmd;
     if (cmd == 3) break;
@@ -1071,7 +1074,7 @@ __device__ void o_epilogue(const DecodeParams& p, Shared& sh, uint32_t smem, int
       continue;
     }
     if (!have) break;
-    if (!warp_wait(sh, sh.o_full, seg & 1, p.status, cl)) break;
+    if (!warp_wait(sh, sh.o_full, seg & 1)) break;
     tc_fence_after();
     const float inv_l = ld_shared_f32(smem + kOffInvL + r * 4);
     const int ns0 = __ldg(p.num_splits + s.b);
@@ -1149,7 +1152,8 @@ __device__ void o_epilogue(const DecodeParams& p, Shared& sh, uint32_t smem, int
 }
 
 template <bool Sparse>
-__global__ void __launch_bounds__(kThreads, 1) mla_decode_fp4_kernel(const __grid_constant__ DecodeParams p) {
+__global__ void __launch_bounds__(kThreads, 1) mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap q_map,
+                                                                        const __grid_constant__ Fp4Params p) {
   extern __shared__ __align__(1024) uint8_t dyn_smem[];
   const uint32_t smem = smem_u32(dyn_smem);
   if (smem & 1023u) {   // the swizzled layouts need the base aligned (no static shared memory is declared)
@@ -1166,6 +1170,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_fp4_kernel(const __gri
   const uint32_t peer = rank ^ 1u;
 
   if (threadIdx.x == 0) {
+    if (is_s) prefetch_tensormap(&q_map);
     sh.abort = 0;
     sh.cmd = 0;
     auto init = [](uint64_t& b, uint32_t n) { mbar_init(smem_u32(&b), n); };
@@ -1188,7 +1193,9 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_fp4_kernel(const __gri
       init(sh.v_full[i], 8);
       init(sh.v_empty[i], 1);
     }
+    init(sh.q_raw, 1);
     init(sh.q_full, 8);
+    init(sh.q_empty, 1);
     init(sh.o_full, 1);
     init(sh.o_free, 8);
     init(sh.o_sync, 1);
@@ -1210,23 +1217,24 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_fp4_kernel(const __gri
     regs_down<kRegsMisc>();
     const bool lane0 = (threadIdx.x & 31) == 0;
     if (is_s) {
-      if (warp == 0) s_load<Sparse>(p, sh, smem, part, cl);
-      else if (warp == 1) s_mma(p, sh, smem, part, cl, blk);
-      else if (lane0) s_ship(p, sh, smem, part, cl, peer, warp - 2);
+      if (warp == 0) s_load<Sparse>(p, &q_map, sh, smem, part, blk);
+      else if (warp == 1) s_mma(p, sh, smem, part, blk);
+      else if (lane0) s_ship(p, sh, smem, part, peer, warp - 2);
     } else {
-      if (warp == 1) o_mma(p, sh, smem, part, cl);
-      else if (warp == 2 && lane0) o_forward(p, sh, part, cl, peer);
+      if (warp == 1) o_mma(p, sh, smem, part);
+      else if (warp == 2 && lane0) o_forward(p, sh, part, peer);
     }
   } else if (warp < 12) {
     regs_up<kRegsSoftmax>();
-    if (is_s) s_softmax<Sparse>(p, sh, smem, part, cl, blk);
-    else o_epilogue(p, sh, smem, part, cl, blk);
+    if (is_s) s_softmax<Sparse>(p, sh, smem, part, blk);
+    else o_epilogue(p, sh, smem, part, blk);
   } else {
     regs_down<kRegsConvert>();
-    if (is_s) s_convert(p, sh, smem, part, cl, (warp - 12) >> 2);
-    else o_convert<Sparse>(p, sh, smem, part, cl);
+    if (is_s) s_convert(p, sh, smem, part, (warp - 12) >> 2);
+    else o_convert<Sparse>(p, sh, smem, part);
   }
 
+  leave_role(sh, p.status, cl);
   __syncwarp();
   tc_fence_before();
   __syncthreads();
@@ -1240,6 +1248,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_fp4_kernel(const __gri
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+
 // One-time set-up of the kernels on the current device.
 bool fp4_ready() {
   static std::mutex mutex;
@@ -1248,6 +1258,14 @@ bool fp4_ready() {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
   std::lock_guard<std::mutex> lock(mutex);
   if (ready[dev]) return true;
+  if (!g_encode) {
+    cudaDriverEntryPointQueryResult found;
+    void* fn = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess || fn == nullptr)
+      return false;
+    g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }
   for (auto kernel : {mla_decode_fp4_kernel<false>, mla_decode_fp4_kernel<true>}) {
     cudaFuncAttributes a;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes)) != cudaSuccess ||
@@ -1279,7 +1297,7 @@ mla_status_t decode_fp4_impl(const void* q, const uint8_t* kv_cache, float kv_sc
   const size_t need = mla_decode_workspace_size(B, s_q, H, num_sm_parts);
   if (workspace_bytes < need || !workspace) return MLA_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return MLA_ERR_INVALID_ARG;
-  DecodeParams p = {};
+  Fp4Params p = {};
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.kv = reinterpret_cast<const __nv_bfloat16*>(kv_cache);
   p.num_blocks = num_blocks;
@@ -1308,6 +1326,15 @@ mla_status_t decode_fp4_impl(const void* q, const uint8_t* kv_cache, float kv_sc
   p.status = device_status_word();
   if (!p.status || !fp4_ready()) return MLA_ERR_CUDA;
   p.withhold_first_load = take_withheld_load();
+  // q as [chunk 0..8][row][64 dims], a box 64 dims of a row block (as many rows as its MMA is wide)
+  p.q_box = rows >= kRowsPerPair ? kRowsPerPair : (rows + 15) & ~15;
+  CUtensorMap q_map;
+  const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(B) * rows, kDimQK / 64}, strides[2] = {kDimQK * 2, 128};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(p.q_box), 1}, steps[3] = {1, 1, 1};
+  if (g_encode(&q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, steps,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return MLA_ERR_CUDA;
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   const unsigned cl = 2u * static_cast<unsigned>(p.n_rb);
   cudaLaunchAttribute attr[2];
@@ -1317,8 +1344,8 @@ mla_status_t decode_fp4_impl(const void* q, const uint8_t* kv_cache, float kv_sc
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.numAttrs = 2;
-  if ((indices ? cudaLaunchKernelEx(&cfg, mla_decode_fp4_kernel<true>, p)
-               : cudaLaunchKernelEx(&cfg, mla_decode_fp4_kernel<false>, p)) != cudaSuccess)
+  if ((indices ? cudaLaunchKernelEx(&cfg, mla_decode_fp4_kernel<true>, q_map, p)
+               : cudaLaunchKernelEx(&cfg, mla_decode_fp4_kernel<false>, q_map, p)) != cudaSuccess)
     return MLA_ERR_CUDA;
   return launch_combine(p.o_part, p.lse_part, p.num_splits, B, rows, static_cast<int>(slots), p.out, lse, p.status, cs) ==
                  cudaSuccess
