@@ -53,14 +53,16 @@ constexpr uint32_t kQChunk = 128 * 128;       // 64 dims of the row block's q: u
 constexpr uint32_t kVChunk = 64 * 128;        // 64 dims of a page's values
 constexpr int kVSlots = 4;                    // half pages (64 tokens x 256 dims) of converted values
 constexpr uint32_t kVSlot = 4 * kVChunk;
-constexpr int kKSlots = 8;                    // TMEM slots of converted keys: 128 tokens x 64 dims, 32 columns
-constexpr int kItems = 9;                     // of them a tile
+constexpr int kItems = 9;                     // chunks of converted keys a tile: 128 tokens x 64 dims, 32 TMEM columns, the first
+                                              // 8 (latent) in a slot each, the last (rope) in the first slot once more
 // a packet: what one softmax warpgroup (half of the row block's heads) sends to the O-CTA for a tile
 constexpr uint32_t kPktAlpha = 128 * 128;     // after P^T (128 tokens x 64 heads): float[64], factors of a rebase
 constexpr uint32_t kPktInvL = kPktAlpha + 256;   // float[64], the output's factors (last tile of a segment)
 constexpr uint32_t kPktFlag = kPktInvL + 256;    // whether alpha counts
 constexpr uint32_t kPktBytes = kPktFlag + 16;
 constexpr uint32_t kPktStride = 17 * 1024;
+constexpr uint32_t kRowSlots = 8;             // O-CTA: pages whose rows have been looked up
+constexpr uint32_t kRowBytes = 4 * (kPageTokens + 1);
 constexpr uint32_t kKCol = 256;               // S-CTA's TMEM columns: S^T of two tiles at 0 and 128, the keys from 256
 constexpr float kOffset = 6.f;                // P is taken against 2^-6 of the reference maximum
 constexpr float kTop = kOffset + 8.f;         // an exponent past this rebases its head
@@ -77,8 +79,9 @@ constexpr uint32_t kOffRaw = kOffSend + 2 * kPktStride;      // S-CTA: the two p
 constexpr uint32_t kOffV = 4 * kPktStride;                   // O-CTA: the packets of two tiles first, then values
 constexpr uint32_t kOffEpi = kOffV + kVSlots * kVSlot;       // O-CTA: 2 KiB transpose buffer per epilogue warp
 constexpr uint32_t kOffInvL = kOffEpi + 8 * 2048;            // O-CTA: output factors of the segment [2][64]
+constexpr uint32_t kOffRows = kOffInvL + 512;                // O-CTA: the ring of looked-up rows
 constexpr uint32_t kOffShared = kOffRaw + 2 * kPageBytes;
-static_assert(kOffInvL + 512 <= kOffShared, "O-CTA layout");
+static_assert(kOffRows + kRowSlots * kRowBytes <= kOffShared, "O-CTA layout");
 
 struct Fp4Params : DecodeParams {
   int q_box;   // q rows of a TMA box
@@ -87,24 +90,26 @@ struct Fp4Params : DecodeParams {
 struct Shared {
   // S-CTA
   uint64_t raw_full[2], raw_empty[2];         // a page of the tile has landed; is in the converters' registers
-  uint64_t k_full[kKSlots], k_empty[kKSlots];
+  uint64_t k_full[kItems], k_empty[kItems];   // a chunk of keys is in TMEM; its MMAs are done (each once a tile)
   uint64_t s_full[2], s_empty[2];
   uint64_t q_raw, q_full, q_empty;            // the segment's q has landed; is fp16 (a softmax warp each); is done with
   uint64_t p_ready[2], st_free[2];            // a warpgroup's packet is written; has been read by its copy
   uint64_t credit[2];                         // the partner's receive slot is free (remote)
   // O-CTA
   uint64_t p_full[2], p_free[2];
+  uint64_t rows_full[kRowSlots], rows_empty[kRowSlots];
   uint64_t v_full[kVSlots], v_empty[kVSlots];
   uint64_t o_full, o_free, o_sync, corr_go, corr_done;
   uint64_t drain;                             // both
   uint32_t tmem_base;
   volatile int abort;
   int cmd, cmd_arg;                           // O-CTA: 1 = rescale (by the packets of slot cmd_arg), 2 = epilogue, 3 = leave
-  float q_scale[128];                         // S-CTA: raw score -> log2 units, by column
-  float part[2][4][64];                       // a warpgroup's maxima or sums by warp and head
-  float ref[2][64];
+  alignas(16) float q_scale[128];                         // S-CTA: raw score -> log2 units, by column
+  alignas(16) float part[2][4][64];                       // a warpgroup's maxima or sums by warp and head
+  alignas(16) float ref[2][64];
   uint16_t pos[128];                          // a column's query position
 };
+static_assert(alignof(Shared) == 16 && kOffShared % 16 == 0, "pairs of floats are read and written as 8 bytes");
 constexpr uint32_t kSmemBytes = kOffShared + sizeof(Shared);
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 
@@ -160,9 +165,6 @@ __device__ __forceinline__ void leave_role(Shared& sh, int* status, uint32_t cl)
   }
 }
 __device__ __forceinline__ void arrive(uint64_t& b) { mbar_arrive(smem_u32(&b)); }
-__device__ __forceinline__ void arrive2(uint64_t& b) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], 2;" :: "r"(smem_u32(&b)) : "memory");
-}
 
 // ------------------------------------------------------------ instructions --
 // A value that all lanes have, as one that the compiler knows to be uniform (operands of MMAs then need no moves).
@@ -229,6 +231,38 @@ __device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {
 // kind::f16 with fp16 inputs and fp32 accumulation (the bf16 descriptor without its two type bits).
 __device__ __forceinline__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn, int b_mn) {
   return idesc_bf16_f32(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
+}
+// Four steps of an MMA (all lanes call; an elected one issues), then the arrival on `bar` when they and all before them are
+// done.  One election for all of them: with one a step, the code around the steps took longer than they do.
+// A from TMEM (8 columns a step), B 32 bytes a step.  accumulate: whether the first step adds to what is in D.
+__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred p, t, e;\n\t.reg .b64 b1, b2, b3;\n\t.reg .b32 a1, a2, a3;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
+      "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}"
+      :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(bar) : "memory");
+}
+// Both from shared memory, 16 tokens (2 KiB) of either a step.
+__device__ __forceinline__ void mma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred p, t, e;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "add.s64 a1, %1, 128;\n\tadd.s64 a2, %1, 256;\n\tadd.s64 a3, %1, 384;\n\t"
+      "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}"
+      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(bar) : "memory");
 }
 // 16 latent values (two words of codes) as fp16 pairs; `scale` twice in a word.
 __device__ __forceinline__ void values16(uint32_t w0, uint32_t w1, uint32_t scale, uint32_t* v) {
@@ -305,11 +339,11 @@ struct PageIter {
   __device__ void init(const Fp4Params& p, int part) {
     w.init(p, part);
     valid = true;
-    k = 0;
-    s.ke = 0;
+    s.kb = s.ke = k = 0;
   }
-  __device__ bool next() {   // on to the next page, the first one to begin with
-    if (valid && ++k >= s.ke) {
+  __device__ bool next() {   // on to the next page, the first one to begin with; a segment's last tile has two in any case
+    ++k;
+    if (valid && (k > s.ke || (k == s.ke && ((k - s.kb) & 1) == 0))) {
       valid = w.next(s);
       k = s.kb;
     }
@@ -378,10 +412,10 @@ __device__ void s_load(const Fp4Params& p, const CUtensorMap* q_map, Shared& sh,
   while (ok && w.next(s)) {
     const int L = __ldg(p.lens + s.b);
     if (!warp_wait(sh, sh.q_empty, (seg & 1) ^ 1)) break;   // (the MMAs of the segment before are done)
-    if (lane == 0) {   // 64 dims of the block's rows a box; rows past the request's are another's, or zeros past q's end
+    if (lane == 0) {   // 64 dims of the block's rows a box, in the order in which keys come (a warpgroup's chunks in turn); rows past the request's are another's, or zeros past q's end
       mbar_arrive_expect_tx(smem_u32(&sh.q_raw), 9u * static_cast<uint32_t>(p.q_box) * 128u);
       for (int c = 0; c < 9; ++c)
-        tma_load_3d(smem + c * kQChunk, q_map, smem_u32(&sh.q_raw), 0, s.b * p.rows + blk.rb * kRowsPerPair, c);
+        tma_load_3d(smem + (c < 4 ? 2 * c : c < 8 ? 2 * c - 7 : 8) * kQChunk, q_map, smem_u32(&sh.q_raw), 0, s.b * p.rows + blk.rb * kRowsPerPair, c);
     }
     __syncwarp();
     ++seg;
@@ -462,73 +496,70 @@ __device__ void s_convert(const Fp4Params& p, Shared& sh, uint32_t smem, int par
       pair(kFp4Rope + 32 * c, rope);
       __syncwarp();
       if (lane == 0) arrive(sh.raw_empty[h]);
-      const uint32_t scale[4] = {sc.x, sc.y, sc.z, sc.w};
+      uint32_t scale[4] = {sc.x, sc.y, sc.z, sc.w};
+#pragma unroll 1
+      for (int k2 = 0; k2 < 4; k2 += 2) {   // (two copies of the code instead of four: 18 moves)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t i = kItems * T + 2 * k + c, slot = i % kKSlots;
-        uint32_t v[32];
-        const uint32_t s01 = e4m3x2_to_f16x2<0>(scale[k]), s23 = e4m3x2_to_f16x2<1>(scale[k]);
-        values16(code[k][0], code[k][1], __byte_perm(s01, 0, 0x1010), v);
-        values16(code[k][2], code[k][3], __byte_perm(s01, 0, 0x3232), v + 8);
-        values16(code[k][4], code[k][5], __byte_perm(s23, 0, 0x1010), v + 16);
-        values16(code[k][6], code[k][7], __byte_perm(s23, 0, 0x3232), v + 24);
-        if (!warp_wait(sh, sh.k_empty[slot], ((i / kKSlots) & 1) ^ 1)) return;
-        tc_fence_after();
-        tmem_st32(tm + slot * 32, v);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive2(sh.k_full[slot]);
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t slot = 2 * (k2 + k) + c;
+          uint32_t v[32];
+          const uint32_t s01 = e4m3x2_to_f16x2<0>(scale[k]), s23 = e4m3x2_to_f16x2<1>(scale[k]);
+          values16(code[k][0], code[k][1], __byte_perm(s01, 0, 0x1010), v);
+          values16(code[k][2], code[k][3], __byte_perm(s01, 0, 0x3232), v + 8);
+          values16(code[k][4], code[k][5], __byte_perm(s23, 0, 0x1010), v + 16);
+          values16(code[k][6], code[k][7], __byte_perm(s23, 0, 0x3232), v + 24);
+          if (!warp_wait(sh, sh.k_empty[slot > 0 ? slot : 8], (T & 1) ^ 1)) return;   // (the first slot had the rope chunk last)
+          tc_fence_after();
+          tmem_st32(tm + slot * 32, v);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive(sh.k_full[slot]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) code[0][j] = code[2][j], code[1][j] = code[3][j];
+        scale[0] = scale[2], scale[1] = scale[3];
       }
-      const uint32_t i = kItems * T + 8, slot = i % kKSlots;
       uint32_t v[16];
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[2 * j] = e4m3x2_to_f16x2<0>(rope[j]), v[2 * j + 1] = e4m3x2_to_f16x2<1>(rope[j]);
-      if (!warp_wait(sh, sh.k_empty[slot], ((i / kKSlots) & 1) ^ 1)) return;
+      if (!warp_wait(sh, sh.k_empty[0], T & 1)) return;   // the tile's first chunk is done with
       tc_fence_after();
-      tmem_st16(tm + slot * 32 + 16 * c, v);
+      tmem_st16(tm + 16 * c, v);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive(sh.k_full[slot]);
+      if (lane == 0) arrive(sh.k_full[8]);
     }
   }
 }
 
-// Warp 1 (all lanes; an elected one issues): S^T = K Q^T, 36 steps of 16 dims a tile.
+// Warp 1 (all lanes; an elected one issues): S^T = K Q^T, 36 steps of 16 dims a tile.  Its loop is what the tensor pipe waits for, so
+// it is short: the latent chunks have a slot each, the rope chunk the first slot once more, and q lies in their order.
 __device__ void s_mma(const Fp4Params& p, Shared& sh, uint32_t smem, int part, const Block& blk) {
   SegmentWalker w;
   w.init(p, part);
   Segment s;
-  uint32_t i = 0, T = 0, seg = 0;
+  uint32_t T = 0, seg = 0;
   const uint32_t tmem = uniform(sh.tmem_base);
   const uint32_t idesc = uniform(idesc_f16_f32(kTile, blk.N, 0, 0));
+  const uint64_t q0 = smem_desc_sw128(smem, 16, 1024);
   bool ok = true;
   while (ok && w.next(s)) {
     if (!warp_wait(sh, sh.q_full, seg & 1)) break;
-    for (int t = tiles_of(s); ok && t > 0; --t, ++T) {
+    for (int t = tiles_of(s); t > 0; --t, ++T) {
       const uint32_t sb = T & 1;
-      if (!warp_wait(sh, sh.s_empty[sb], ((T >> 1) & 1) ^ 1)) {
-        ok = false;
-        break;
-      }
+      ok = warp_wait(sh, sh.s_empty[sb], ((T >> 1) & 1) ^ 1);
       const uint32_t d = uniform(tmem + sb * kTile);
 #pragma unroll 1
-      for (int it = 0; it < kItems; ++it, ++i) {
-        const uint32_t slot = i % kKSlots;
-        if (!warp_wait(sh, sh.k_full[slot], (i / kKSlots) & 1)) {
-          ok = false;
-          break;
-        }
+      for (int it = 0; it < kItems; ++it) {
+        ok = ok && warp_wait(sh, sh.k_full[it], T & 1);
+        if (!ok) break;
         tc_fence_after();
-        const int chunk = it < 8 ? (it >> 1) + 4 * (it & 1) : 8;   // the warpgroups' chunks in turn
-        const uint32_t a = uniform(tmem + kKCol + slot * 32), q = uniform(smem + chunk * kQChunk), go_on = uniform(it > 0);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          mma_bf16_ts_warp(d, a + j * 8, smem_desc_sw128(q + j * 32, 16, 1024), idesc, j ? 1u : go_on);
-        mma_commit_warp(smem_u32(&sh.k_empty[slot]));
+        mma4_ts(d, tmem + kKCol + (it & 7) * 32, q0 + it * (kQChunk >> 4), idesc, it > 0, smem_u32(&sh.k_empty[it]));
       }
-      if (ok) mma_commit_warp(smem_u32(&sh.s_full[sb]));
+      if (!ok) break;
+      mma_commit_warp(smem_u32(&sh.s_full[sb]));
     }
     if (ok) mma_commit_warp(smem_u32(&sh.q_empty));
     ++seg;
@@ -822,110 +853,142 @@ __device__ void s_ship(const Fp4Params& p, Shared& sh, uint32_t smem, int part, 
 }
 
 // ------------------------------------------------------------------ O-CTA --
-// Warps 12..19: the latent dims of every page, from global memory through registers into shared memory as fp16 (64 tokens by
-// 64 dims a chunk, 128-byte swizzle).  A thread has two rows of a page, 8 warps a row group of 32, and of each row a unit of 32
-// dims in either half.  Four lanes apart two rows and a unit pair: a quarter warp reads 32 bytes of four rows and writes eight different banks.
-// Addresses are looked up two pages ahead, codes loaded one page ahead.
+__device__ __forceinline__ void st_shared_s32(uint32_t a, int v) { asm volatile("st.shared.b32 [%0], %1;" :: "r"(a), "r"(v) : "memory"); }
+__device__ __forceinline__ int ld_shared_s32(uint32_t a) {
+  int v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// Warp 0: finds the cached rows of every page, kRowSlots pages ahead of the converters at most, puts their numbers into a ring in
+// shared memory (64 of them, and how many count; -1 after the last page) and has them brought into L2.  A lane has two rows; its
+// loads of a list entry, of that token's table entry, and the ring's store are a page apart, so that none waits for the one before.
+// (What is out of range is reported by the S-CTA's loads, and read as row 0 here.)
 template <bool Sparse>
-__device__ void o_convert(const Fp4Params& p, Shared& sh, uint32_t smem, int part) {
+__device__ void o_lookup(const Fp4Params& p, Shared& sh, uint32_t smem, int part) {
+  const int lane = threadIdx.x & 31;
+  struct Tokens { int t[2], n, b, k; bool valid; } tok;
+  struct Blocks { int t[2], blk[2], n; bool valid; } blk;
+  PageIter it;
+  it.init(p, part);
+  tok.valid = blk.valid = false;
+  tok.n = 0;
+  uint32_t i = 0;   // pages
+  while (true) {
+    const bool end = !blk.valid && !tok.valid && !it.valid;
+    if (blk.valid || end) {
+      const uint32_t slot = i % kRowSlots, at = smem + kOffRows + slot * kRowBytes;
+      if (!warp_wait(sh, sh.rows_empty[slot], ((i / kRowSlots) & 1) ^ 1)) return;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int r = lane + 32 * g, t = Sparse ? blk.t[g] : r;
+        const bool good = !end && r < blk.n && blk.blk[g] >= 0 && blk.blk[g] < p.num_blocks;
+        const int row = good ? blk.blk[g] * kPageTokens + t % kPageTokens : Sparse || end ? 0 : r;
+        st_shared_s32(at + r * 4, row);
+        if (Sparse && good) prefetch_l2(reinterpret_cast<const uint8_t*>(p.kv) + static_cast<int64_t>(row) * kFp4RowBytes, kFp4RowBytes);
+        if (!Sparse && good && lane == 0 && g == 0)
+          prefetch_l2(reinterpret_cast<const uint8_t*>(p.kv) + static_cast<int64_t>(row) * kFp4RowBytes, blk.n * kFp4RowBytes);
+      }
+      if (lane == 0) st_shared_s32(at + 256, end ? -1 : blk.n);
+      __syncwarp();
+      if (lane == 0) arrive(sh.rows_full[slot]);
+      if (end) return;
+      ++i;
+    }
+    blk.valid = tok.valid;
+    blk.n = tok.n;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const int t = tok.t[g], k = Sparse ? t / kPageTokens : tok.k;
+      blk.t[g] = t;
+      blk.blk[g] = -1;
+      if (lane + 32 * g < tok.n && k < p.max_blocks && (!Sparse || (t >= 0 && t < __ldg(p.seqlens + tok.b))))
+        blk.blk[g] = __ldg(p.block_table + static_cast<int64_t>(tok.b) * p.max_blocks + k);
+    }
+    tok.valid = it.next();
+    tok.n = 0;
+    if (tok.valid) {
+      tok.b = it.s.b;
+      tok.k = it.k;
+      if (it.k < it.s.ke) tok.n = min(kPageTokens, __ldg(p.lens + it.s.b) - it.k * kPageTokens);
+      if constexpr (Sparse) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const int r = lane + 32 * g, e = it.k * kPageTokens + r;
+          tok.t[g] = r < tok.n && e < p.idx_stride ? __ldg(p.indices + static_cast<int64_t>(it.s.b) * p.idx_stride + e) : -1;
+        }
+      }
+    }
+  }
+}
+
+// Warps 12..19: the latent dims of every page, from global memory through registers into shared memory as fp16 (64 tokens by
+// 64 dims a chunk, 128-byte swizzle).  A thread has two rows of a page, the warps together a row group of 32, and of each row a unit
+// of 32 dims in either half.  Two rows and a unit pair lie four lanes apart: a quarter warp reads 32 bytes of four rows and writes to
+// eight different banks.  The next page's codes are on their way while a page is converted.
+__device__ void o_convert(const Fp4Params& p, Shared& sh, uint32_t smem) {
   const int v = (threadIdx.x >> 5) - 12, lane = threadIdx.x & 31;
   const int u0 = lane & 1, rr = (lane >> 1) & 3, q = lane >> 3;
   const int r0 = 4 * v + rr;              // rows r0 and r0 + 32
   const int unit = 2 * q + u0;            // of the 8 in a half
-  struct Tokens { int t[2]; int b, n, k; bool valid; } tok;            // n: rows of the page that hold tokens
-  struct Rows { const uint8_t* at[2]; int n; bool valid; } rows;
-  struct Codes { uint4 c[2][2]; uint32_t s[2][2]; int n; bool valid; } cur, nxt;   // by row and half
-  PageIter it;
-  it.init(p, part);
-  auto fetch_tokens = [&] {
-    tok.valid = it.next();
-    tok.n = 0;
-    if (!tok.valid) return;
-    tok.b = it.s.b;
-    tok.k = it.k;
-    tok.n = min(kPageTokens, __ldg(p.lens + it.s.b) - it.k * kPageTokens);
-    if constexpr (Sparse) {
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const int e = it.k * kPageTokens + r0 + 32 * g;
-        tok.t[g] = r0 + 32 * g < tok.n && e < p.idx_stride ? __ldg(p.indices + static_cast<int64_t>(it.s.b) * p.idx_stride + e) : -1;
-      }
-    }
-  };
-  auto fetch_rows = [&] {   // (what is out of range is reported by the S-CTA's loads and read as row or page 0 here)
-    rows.valid = tok.valid;
-    rows.n = tok.n;
-    if (!tok.valid) return;
-    if constexpr (Sparse) {
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const int t = tok.t[g];
-        int blk = -1;
-        if (t >= 0 && t < __ldg(p.seqlens + tok.b) && t / kPageTokens < p.max_blocks)
-          blk = __ldg(p.block_table + static_cast<int64_t>(tok.b) * p.max_blocks + t / kPageTokens);
-        rows.at[g] = row_at(p, t < 0 ? 0 : t, blk < p.num_blocks ? blk : -1);
-      }
-    } else {
-      int blk = -1;
-      if (tok.k < p.max_blocks) blk = __ldg(p.block_table + static_cast<int64_t>(tok.b) * p.max_blocks + tok.k);
-      const uint8_t* page = row_at(p, 0, blk < p.num_blocks ? blk : -1);
-      rows.at[0] = page + r0 * kFp4RowBytes;
-      rows.at[1] = page + (r0 + 32) * kFp4RowBytes;
-    }
-  };
-  auto fetch_codes = [&](Codes& d) {
-    d.valid = rows.valid;
-    d.n = rows.n;
-    if (!rows.valid) return;
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      if (r0 + 32 * g < d.n) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          d.c[g][h] = __ldg(reinterpret_cast<const uint4*>(rows.at[g] + 128 * h + 16 * unit));
-          d.s[g][h] = __ldg(reinterpret_cast<const uint16_t*>(rows.at[g] + kFp4Scales + 16 * h + 2 * unit));
-        }
-      }
-    }
-  };
-  uint32_t i = 0;   // half pages
-  auto convert = [&](const Codes& d) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h, ++i) {
-      const uint32_t slot = i % kVSlots;
-      if (!warp_wait(sh, sh.v_empty[slot], ((i / kVSlots) & 1) ^ 1)) return false;
-      const uint32_t base = smem + kOffV + slot * kVSlot + q * kVChunk;
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const int r = r0 + 32 * g;
-        uint32_t x[16];
-        if (r < d.n) {
-          const uint32_t s = e4m3x2_to_f16x2<0>(d.s[g][h]);
-          values16(d.c[g][h].x, d.c[g][h].y, __byte_perm(s, 0, 0x1010), x);
-          values16(d.c[g][h].z, d.c[g][h].w, __byte_perm(s, 0, 0x3232), x + 8);
-        } else {   // P is 0 there, and 0 times what lies in an unused row need not be 0
-#pragma unroll
-          for (int j = 0; j < 16; ++j) x[j] = 0u;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          st_shared_v4(base + r * 128 + (((4 * u0 + j) ^ (r & 7)) << 4),
-                       make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]));
-      }
-      fence_proxy_async_smem();
+  const uint8_t* const kv = reinterpret_cast<const uint8_t*>(p.kv) + 16 * unit;
+  const uint32_t to = smem + kOffV + q * kVChunk + r0 * 128, swizzle = static_cast<uint32_t>(4 * u0) ^ (r0 & 7);
+  struct Codes { uint4 c[2][2]; uint32_t s[2][2]; int n; } cur, nxt;   // by row and half
+  cur.n = -1;
+  uint32_t i = 0;   // pages
+#pragma unroll 1
+  while (true) {
+    {
+      const uint32_t slot = i % kRowSlots, at = smem + kOffRows + slot * kRowBytes;
+      if (!warp_wait(sh, sh.rows_full[slot], (i / kRowSlots) & 1)) return;
+      nxt.n = ld_shared_s32(at + 256);
+      const int row[2] = {ld_shared_s32(at + r0 * 4), ld_shared_s32(at + (r0 + 32) * 4)};
       __syncwarp();
-      if (lane == 0) arrive(sh.v_full[slot]);
+      if (lane == 0) arrive(sh.rows_empty[slot]);
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const uint8_t* src = kv + static_cast<int64_t>(row[g]) * kFp4RowBytes;
+        if (r0 + 32 * g < nxt.n) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            nxt.c[g][h] = __ldg(reinterpret_cast<const uint4*>(src + 128 * h));
+            nxt.s[g][h] = __ldg(reinterpret_cast<const uint16_t*>(src + (kFp4Scales + 16 * h) - 14 * unit));
+          }
+        }
+      }
     }
-    return true;
-  };
-  cur.valid = rows.valid = tok.valid = false;
-  do {
-    fetch_codes(nxt);
-    fetch_rows();
-    fetch_tokens();
-    if (cur.valid && !convert(cur)) return;
+    if (i > 0) {   // page i - 1
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t vs = (2 * (i - 1) + h) % kVSlots;
+        if (!warp_wait(sh, sh.v_empty[vs], (((i - 1) / (kVSlots / 2)) & 1) ^ 1)) return;
+        if (cur.n > 0) {   // (0: a tile's second page that is none)
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            uint32_t x[16];
+            if (r0 + 32 * g < cur.n) {
+              const uint32_t s = e4m3x2_to_f16x2<0>(cur.s[g][h]);
+              values16(cur.c[g][h].x, cur.c[g][h].y, __byte_perm(s, 0, 0x1010), x);
+              values16(cur.c[g][h].z, cur.c[g][h].w, __byte_perm(s, 0, 0x3232), x + 8);
+            } else {   // P is 0 there, and 0 times what lies in an unused row need not be 0
+#pragma unroll
+              for (int j = 0; j < 16; ++j) x[j] = 0u;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)   // (rows 32 apart have the same swizzle)
+              st_shared_v4(to + vs * kVSlot + g * 32 * 128 + ((swizzle ^ j) << 4),
+                           make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]));
+          }
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) arrive(sh.v_full[vs]);
+      }
+    }
+    if (nxt.n < 0) return;
     cur = nxt;
-  } while (cur.valid || rows.valid || tok.valid);
+    ++i;
+  }
 }
 
 // Warp 1 (all lanes; an elected one issues): O += P V, for every page and 256-column half of O a step per 16 tokens.
@@ -934,7 +997,7 @@ __device__ void o_mma(const Fp4Params& p, Shared& sh, uint32_t smem, int part) {
   SegmentWalker w;
   w.init(p, part);
   Segment s;
-  uint32_t T = 0, i = 0, seg = 0, nresc = 0;
+  uint32_t T = 0, seg = 0, nresc = 0;
   const uint32_t tmem = uniform(sh.tmem_base);
   constexpr uint32_t idesc = idesc_f16_f32(128, 256, 1, 1);
   bool ok = true;
@@ -977,24 +1040,23 @@ __device__ void o_mma(const Fp4Params& p, Shared& sh, uint32_t smem, int part) {
         ++nresc;
       }
       tc_fence_after();
+      const uint64_t a = smem_desc_sw128(uniform(pkt), kPktStride, 1024), v0 = smem_desc_sw128(smem + kOffV, kVChunk, 1024);
+      const uint32_t go_on = uniform(k != s.kb);
 #pragma unroll 1
-      for (int ph = 0; ph < 4 && k + (ph >> 1) < s.ke; ++ph, ++i) {   // half ph % 2 of page ph / 2
-        const int pg = ph >> 1;
-        const int ksteps = (min(kPageTokens, ntok - pg * kPageTokens) + 15) >> 4;
-        const uint32_t vs = i % kVSlots;
-        if (!warp_wait(sh, sh.v_full[vs], (i / kVSlots) & 1)) {
-          ok = false;
-          break;
-        }
+      for (int ph = 0; ph < 4; ++ph) {   // half ph % 2 of page ph / 2, in slot ph (a tile of one page leaves two slots empty)
+        const int steps = (ntok - (ph >> 1) * kPageTokens + 15) >> 4;
+        ok = ok && warp_wait(sh, sh.v_full[ph], T & 1);
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t d = uniform(tmem + 256 * (ph & 1)), a = uniform(pkt + pg * kPageTokens * 128);
-        const uint32_t vb = uniform(smem + kOffV + vs * kVSlot), go_on = uniform(k != s.kb || pg > 0);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (j < ksteps)
-            mma_bf16_ss_warp(d, smem_desc_sw128(a + j * 2048, kPktStride, 1024), smem_desc_sw128(vb + j * 2048, kVChunk, 1024),
-                             idesc, j ? 1u : go_on);
-        mma_commit_warp(smem_u32(&sh.v_empty[vs]));
+        const uint64_t pa = a + (ph >> 1) * (kPageTokens * 128 >> 4), vb = v0 + ph * (kVSlot >> 4);
+        if (steps >= 4) {
+          mma4_ss(tmem + 256 * (ph & 1), pa, vb, idesc, ph > 1 ? 1u : go_on, smem_u32(&sh.v_empty[ph]));
+        } else {
+#pragma unroll 1
+          for (int j = 0; j < steps; ++j)
+            mma_bf16_ss_warp(tmem + 256 * (ph & 1), pa + 128 * j, vb + 128 * j, idesc, j || ph > 1 ? 1u : go_on);
+          mma_commit_warp(smem_u32(&sh.v_empty[ph]));
+        }
       }
       if (!ok) break;
       mma_commit_warp(smem_u32(&sh.p_free[slot]));
@@ -1185,9 +1247,13 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_fp4_kernel(const __gri
       init(sh.p_full[i], 1);
       init(sh.p_free[i], 1);
     }
-    for (int i = 0; i < kKSlots; ++i) {
-      init(sh.k_full[i], 8);         // latent: four warps, two each; rope: eight warps
+    for (int i = 0; i < kItems; ++i) {
+      init(sh.k_full[i], i < 8 ? 4 : 8);   // a latent chunk comes from one converting warpgroup, the rope chunk from both
       init(sh.k_empty[i], 1);
+    }
+    for (uint32_t i = 0; i < kRowSlots; ++i) {
+      init(sh.rows_full[i], 1);
+      init(sh.rows_empty[i], 8);
     }
     for (int i = 0; i < kVSlots; ++i) {
       init(sh.v_full[i], 8);
@@ -1221,7 +1287,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_fp4_kernel(const __gri
       else if (warp == 1) s_mma(p, sh, smem, part, blk);
       else if (lane0) s_ship(p, sh, smem, part, peer, warp - 2);
     } else {
-      if (warp == 1) o_mma(p, sh, smem, part);
+      if (warp == 0) o_lookup<Sparse>(p, sh, smem, part);
+      else if (warp == 1) o_mma(p, sh, smem, part);
       else if (warp == 2 && lane0) o_forward(p, sh, part, peer);
     }
   } else if (warp < 12) {
@@ -1231,7 +1298,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_fp4_kernel(const __gri
   } else {
     regs_down<kRegsConvert>();
     if (is_s) s_convert(p, sh, smem, part, (warp - 12) >> 2);
-    else o_convert<Sparse>(p, sh, smem, part);
+    else o_convert(p, sh, smem);
   }
 
   leave_role(sh, p.status, cl);
