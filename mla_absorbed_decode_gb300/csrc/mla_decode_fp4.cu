@@ -48,7 +48,9 @@ namespace {
 
 constexpr int kThreads = 640;   // warps 0..3: loads, MMAs, copies; 4..11: softmax or rescale and epilogue; 12..19: conversion
 constexpr int kTile = 128;      // tokens of a tile: two pages
-constexpr uint32_t kPageBytes = kPageTokens * kFp4RowBytes;
+// a page in the S-CTA's shared memory: 16 bytes between groups of four rows, so that eight rows' units lie in different banks
+constexpr uint32_t kRawGroup = 4 * kFp4RowBytes + 16;
+constexpr uint32_t kRawPage = kPageTokens / 4 * kRawGroup;
 constexpr uint32_t kQChunk = 128 * 128;       // 64 dims of the row block's q: up to 128 rows of 128 bytes, swizzled
 constexpr uint32_t kVChunk = 64 * 128;        // 64 dims of a page's values
 constexpr int kVSlots = 4;                    // half pages (64 tokens x 256 dims) of converted values
@@ -69,7 +71,7 @@ constexpr float kTop = kOffset + 8.f;         // an exponent past this rebases i
 constexpr uint32_t kTimeoutNs = 500u * 1000 * 1000;
 constexpr float kLn2 = 0.69314718055994530942f;
 // registers a thread: the three kinds of warpgroups share what the launch gets (640 x 96)
-constexpr int kRegsMisc = 64, kRegsSoftmax = 120, kRegsConvert = 88;
+constexpr int kRegsMisc = 48, kRegsSoftmax = 128, kRegsConvert = 88;
 static_assert(128 * kRegsMisc + 256 * kRegsSoftmax + 256 * kRegsConvert <= kThreads * 96, "more would wait forever");
 
 
@@ -80,7 +82,7 @@ constexpr uint32_t kOffV = 4 * kPktStride;                   // O-CTA: the packe
 constexpr uint32_t kOffEpi = kOffV + kVSlots * kVSlot;       // O-CTA: 2 KiB transpose buffer per epilogue warp
 constexpr uint32_t kOffInvL = kOffEpi + 8 * 2048;            // O-CTA: output factors of the segment [2][64]
 constexpr uint32_t kOffRows = kOffInvL + 512;                // O-CTA: the ring of looked-up rows
-constexpr uint32_t kOffShared = kOffRaw + 2 * kPageBytes;
+constexpr uint32_t kOffShared = kOffRaw + 2 * kRawPage;
 static_assert(kOffRows + kRowSlots * kRowBytes <= kOffShared, "O-CTA layout");
 
 struct Fp4Params : DecodeParams {
@@ -221,11 +223,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-__device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 // kind::f16 with fp16 inputs and fp32 accumulation (the bf16 descriptor without its two type bits).
@@ -396,7 +393,7 @@ struct Block {
 };
 
 // ------------------------------------------------------------------ S-CTA --
-// Warp 0: the two pages of every tile.  Dense: one copy a page (as far as the request has tokens); lists: a copy a
+// Warp 0: the two pages of every tile.  Dense: a copy for four rows (as far as the request has tokens); lists: a copy a
 // row, whose addresses are looked up while the tile before is being loaded.
 template <bool Sparse>
 __device__ void s_load(const Fp4Params& p, const CUtensorMap* q_map, Shared& sh, uint32_t smem, int part, const Block& blk) {
@@ -422,7 +419,7 @@ __device__ void s_load(const Fp4Params& p, const CUtensorMap* q_map, Shared& sh,
     for (int k = s.kb; ok && k < s.ke; k += 2, ++T) {
       for (int h = 0; h < 2; ++h) {
         const int n = k + h < s.ke ? min(kPageTokens, L - (k + h) * kPageTokens) : 0;   // rows
-        const uint32_t dst = smem + kOffRaw + h * kPageBytes;
+        const uint32_t dst = smem + kOffRaw + h * kRawPage;
         const uint8_t* row[2] = {nullptr, nullptr};
         if constexpr (Sparse) {
           int t[2];
@@ -452,9 +449,10 @@ __device__ void s_load(const Fp4Params& p, const CUtensorMap* q_map, Shared& sh,
         if constexpr (Sparse) {
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            if (row[i]) bulk_load(dst + (lane + 32 * i) * kFp4RowBytes, row[i], kFp4RowBytes, sh.raw_full[h]);
-        } else if (lane == 0 && n > 0) {
-          bulk_load(dst, row[0], static_cast<uint32_t>(n) * kFp4RowBytes, sh.raw_full[h]);
+            if (row[i]) bulk_load(dst + (lane + 32 * i) * kFp4RowBytes + ((lane >> 2) + 8 * i) * 16, row[i], kFp4RowBytes, sh.raw_full[h]);
+        } else if (4 * lane < n) {
+          bulk_load(dst + lane * kRawGroup, row[0] + lane * 4 * kFp4RowBytes,
+                    static_cast<uint32_t>(min(4, n - 4 * lane)) * kFp4RowBytes, sh.raw_full[h]);
         }
       }
     }
@@ -467,20 +465,16 @@ __device__ void s_load(const Fp4Params& p, const CUtensorMap* q_map, Shared& sh,
 }
 
 // Warps 12..19: a thread a token; warpgroup c takes latent dims [256 c, 256 c + 256) and half of the rope dims.  A tile's codes
-// are read into registers at once, which frees the page buffers for the next tile's loads.  Rows are 352 bytes: lanes 4
-// rows apart would hit the same banks, so rows with bit 2 set read each pair of units the other way round.
+// are read into registers at once, which frees the page buffers for the next tile's loads.
 __device__ void s_convert(const Fp4Params& p, Shared& sh, uint32_t smem, int part, int c) {
   const int quad = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const int h = quad >> 1;                                   // page of the tile
   const int r = (quad & 1) * 32 + lane;                      // row of the page
-  const uint32_t raw = smem + kOffRaw + h * kPageBytes + r * kFp4RowBytes;
-  const bool swap = r & 4;
-  const uint32_t first = swap ? 16 : 0;
+  const uint32_t raw = smem + kOffRaw + h * kRawPage + r * kFp4RowBytes + (r >> 2) * 16;
   const uint32_t tm = sh.tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + kKCol;
   auto pair = [&](uint32_t at, uint32_t (&w)[8]) {           // 32 bytes of the row
-    const uint4 a = ld_shared_v4(raw + at + first), b = ld_shared_v4(raw + at + (first ^ 16));
-    w[0] = swap ? b.x : a.x, w[1] = swap ? b.y : a.y, w[2] = swap ? b.z : a.z, w[3] = swap ? b.w : a.w;
-    w[4] = swap ? a.x : b.x, w[5] = swap ? a.y : b.y, w[6] = swap ? a.z : b.z, w[7] = swap ? a.w : b.w;
+    const uint4 a = ld_shared_v4(raw + at), b = ld_shared_v4(raw + at + 16);
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
   };
   SegmentWalker w;
   w.init(p, part);
@@ -676,7 +670,6 @@ __device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int par
       float2 ls[8];
       bool rebased = false;
       while (true) {   // once, or twice where references have to move
-        uint32_t top = 0;   // largest P, two fp16
 #pragma unroll
         for (int i = 0; i < 8; ++i) ls[i] = make_float2(0.f, 0.f);
 #pragma unroll 1
@@ -708,7 +701,6 @@ __device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int par
               y.y = fast_exp2(y.y);
               ls[i] = add2(ls[i], y);
               pk[q] = pack_f16x2(y.x, y.y);
-              top = max_f16x2(top, pk[q]);
             }
             stmatrix4(pkt + row * 128 + (((2 * ii + st_unit) ^ (row & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
           }
@@ -716,8 +708,11 @@ __device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int par
         fence_proxy_async_smem();
         tc_fence_before();
         if (rebased) break;
-        // a P past 2^14 (0x7400 in fp16), or a head without a reference: the tile again, with new references
-        const bool again = fresh != 0 || (top & 0xFFFFu) > 0x7400u || (top >> 16) > 0x7400u || !ok_t;
+        // a P past 2^14 (no sum of four shows less), or a head without a reference: the tile again, with new references
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(ls[i].x, ls[i].y));
+        const bool again = fresh != 0 || top > 0x1p14f || !ok_t;
         if (!named_bar_or(bar, 128, again)) break;
         if (named_bar_or(bar, 128, !ok_t)) {
           ok = false;
@@ -923,71 +918,67 @@ __device__ void o_lookup(const Fp4Params& p, Shared& sh, uint32_t smem, int part
 }
 
 // Warps 12..19: the latent dims of every page, from global memory through registers into shared memory as fp16 (64 tokens by
-// 64 dims a chunk, 128-byte swizzle).  A thread has two rows of a page, the warps together a row group of 32, and of each row a unit
-// of 32 dims in either half.  Two rows and a unit pair lie four lanes apart: a quarter warp reads 32 bytes of four rows and writes to
-// eight different banks.  The next page's codes are on their way while a page is converted.
+// 64 dims a chunk, 128-byte swizzle).  A thread has one row of a page (a quarter warp eight rows: eight different banks) and a chunk of
+// either half; as soon as it has converted one it loads the same one of the next page, which it needs a page later.
 __device__ void o_convert(const Fp4Params& p, Shared& sh, uint32_t smem) {
-  const int v = (threadIdx.x >> 5) - 12, lane = threadIdx.x & 31;
-  const int u0 = lane & 1, rr = (lane >> 1) & 3, q = lane >> 3;
-  const int r0 = 4 * v + rr;              // rows r0 and r0 + 32
-  const int unit = 2 * q + u0;            // of the 8 in a half
-  const uint8_t* const kv = reinterpret_cast<const uint8_t*>(p.kv) + 16 * unit;
-  const uint32_t to = smem + kOffV + q * kVChunk + r0 * 128, swizzle = static_cast<uint32_t>(4 * u0) ^ (r0 & 7);
-  struct Codes { uint4 c[2][2]; uint32_t s[2][2]; int n; } cur, nxt;   // by row and half
-  cur.n = -1;
-  uint32_t i = 0;   // pages
+  const int lane = threadIdx.x & 31, r = 8 * ((threadIdx.x >> 5) - 12) + (lane & 7), chunk = lane >> 3;   // of the 4 in a half
+  const uint8_t* const kv = reinterpret_cast<const uint8_t*>(p.kv);
+  const uint32_t to = smem + kOffV + chunk * kVChunk + r * 128;
+  uint4 code[2][2];
+  uint32_t scale[2];
+  int n = 0, n_next = 0;   // rows that count, of this page and the next (-1: none follows)
+  const uint8_t* src = kv;
+  uint32_t i = 0;          // pages
+  auto load = [&](int h) {
+    if (r < n_next) {
+      code[h][0] = __ldg(reinterpret_cast<const uint4*>(src + 128 * h + 32 * chunk));
+      code[h][1] = __ldg(reinterpret_cast<const uint4*>(src + 128 * h + 32 * chunk + 16));
+      scale[h] = __ldg(reinterpret_cast<const uint32_t*>(src + kFp4Scales + 16 * h + 4 * chunk));
+    }
+  };
 #pragma unroll 1
-  while (true) {
-    {
+  for (bool first = true; n_next >= 0; first = false) {
+    n = n_next;
+    {   // where the next page's row is
       const uint32_t slot = i % kRowSlots, at = smem + kOffRows + slot * kRowBytes;
       if (!warp_wait(sh, sh.rows_full[slot], (i / kRowSlots) & 1)) return;
-      nxt.n = ld_shared_s32(at + 256);
-      const int row[2] = {ld_shared_s32(at + r0 * 4), ld_shared_s32(at + (r0 + 32) * 4)};
+      n_next = ld_shared_s32(at + 256);
+      src = kv + static_cast<int64_t>(ld_shared_s32(at + r * 4)) * kFp4RowBytes;
       __syncwarp();
       if (lane == 0) arrive(sh.rows_empty[slot]);
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const uint8_t* src = kv + static_cast<int64_t>(row[g]) * kFp4RowBytes;
-        if (r0 + 32 * g < nxt.n) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            nxt.c[g][h] = __ldg(reinterpret_cast<const uint4*>(src + 128 * h));
-            nxt.s[g][h] = __ldg(reinterpret_cast<const uint16_t*>(src + (kFp4Scales + 16 * h) - 14 * unit));
-          }
-        }
-      }
     }
-    if (i > 0) {   // page i - 1
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t vs = (2 * (i - 1) + h) % kVSlots;
-        if (!warp_wait(sh, sh.v_empty[vs], (((i - 1) / (kVSlots / 2)) & 1) ^ 1)) return;
-        if (cur.n > 0) {   // (0: a tile's second page that is none)
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            uint32_t x[16];
-            if (r0 + 32 * g < cur.n) {
-              const uint32_t s = e4m3x2_to_f16x2<0>(cur.s[g][h]);
-              values16(cur.c[g][h].x, cur.c[g][h].y, __byte_perm(s, 0, 0x1010), x);
-              values16(cur.c[g][h].z, cur.c[g][h].w, __byte_perm(s, 0, 0x3232), x + 8);
-            } else {   // P is 0 there, and 0 times what lies in an unused row need not be 0
-#pragma unroll
-              for (int j = 0; j < 16; ++j) x[j] = 0u;
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)   // (rows 32 apart have the same swizzle)
-              st_shared_v4(to + vs * kVSlot + g * 32 * 128 + ((swizzle ^ j) << 4),
-                           make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]));
-          }
-          fence_proxy_async_smem();
-        }
-        __syncwarp();
-        if (lane == 0) arrive(sh.v_full[vs]);
-      }
-    }
-    if (nxt.n < 0) return;
-    cur = nxt;
     ++i;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (first) {
+        load(h);
+        continue;
+      }
+      const uint32_t vs = (2 * i + h) % kVSlots;   // page i - 2
+      if (!warp_wait(sh, sh.v_empty[vs], ((i / (kVSlots / 2)) & 1) ^ 0)) return;
+      if (n > 0) {   // (0: a tile's second page that is none)
+        uint32_t x[32];
+        if (r < n) {
+          const uint32_t s01 = e4m3x2_to_f16x2<0>(scale[h]), s23 = e4m3x2_to_f16x2<1>(scale[h]);
+          values16(code[h][0].x, code[h][0].y, __byte_perm(s01, 0, 0x1010), x);
+          values16(code[h][0].z, code[h][0].w, __byte_perm(s01, 0, 0x3232), x + 8);
+          values16(code[h][1].x, code[h][1].y, __byte_perm(s23, 0, 0x1010), x + 16);
+          values16(code[h][1].z, code[h][1].w, __byte_perm(s23, 0, 0x3232), x + 24);
+        } else {   // P is 0 there, and 0 times what lies in an unused row need not be 0
+#pragma unroll
+          for (int j = 0; j < 32; ++j) x[j] = 0u;
+        }
+        load(h);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          st_shared_v4(to + vs * kVSlot + ((j ^ (r & 7)) << 4), make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]));
+        fence_proxy_async_smem();
+      } else {
+        load(h);
+      }
+      __syncwarp();
+      if (lane == 0) arrive(sh.v_full[vs]);
+    }
   }
 }
 
