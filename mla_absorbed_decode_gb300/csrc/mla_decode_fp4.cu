@@ -25,8 +25,8 @@
 // q is bf16 and K fp16, and an MMA takes one type: each row of q is multiplied by a power of two that brings its largest
 // element into [2^14, 2^15) and rounded to fp16, which is exact for elements down to 2^-31 of the largest.
 //
-// Every barrier wait is bounded; on expiry the CTA records MLA_ERR_TIMEOUT, raises an abort flag in every CTA of its cluster,
-// drains what it has in flight and leaves.
+// Every wait is bounded: a pair without progress for 0.5 s records MLA_ERR_TIMEOUT and tells every CTA of its cluster to leave, which
+// they do once what they have in flight has landed.
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -36,6 +36,7 @@
 #include <stdint.h>
 
 #include <climits>
+#include <cstddef>
 #include <cmath>
 #include <mutex>
 
@@ -85,6 +86,8 @@ constexpr uint32_t kOffRows = kOffInvL + 512;                // O-CTA: the ring 
 constexpr uint32_t kOffShared = kOffRaw + 2 * kRawPage;
 static_assert(kOffRows + kRowSlots * kRowBytes <= kOffShared, "O-CTA layout");
 
+constexpr uint32_t kDone = 0xffffffffu;
+
 struct Fp4Params : DecodeParams {
   int q_box;   // q rows of a TMA box
 };
@@ -104,7 +107,8 @@ struct Shared {
   uint64_t o_full, o_free, o_sync, corr_go, corr_done;
   uint64_t drain;                             // both
   uint32_t tmem_base;
-  volatile int abort;
+  uint32_t abort;                             // nonzero: leave
+  uint32_t tiles;                             // O-CTA: tiles whose MMAs are issued, kDone at the end
   int cmd, cmd_arg;                           // O-CTA: 1 = rescale (by the packets of slot cmd_arg), 2 = epilogue, 3 = leave
   alignas(16) float q_scale[128];                         // S-CTA: raw score -> log2 units, by column
   alignas(16) float part[2][4][64];                       // a warpgroup's maxima or sums by warp and head
@@ -116,69 +120,61 @@ constexpr uint32_t kSmemBytes = kOffShared + sizeof(Shared);
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 
 // ------------------------------------------------------------------ waits --
-// Every role waits at several places, and the code of 20 warps has to fit the instruction caches (313 KB of it, mostly inlined
-// ways out of waits, ran 220 us where this takes 70), so a wait that gives up only notes it; the warps report when they leave
-// their roles (leave_role).
-enum : int { kRunning = 0, kTold = 1, kTimedOut = 2 };
+// Address of a member of Shared (an element of an array of barriers: + 8 i).
+#define AT(member) (smem + kOffShared + static_cast<uint32_t>(offsetof(Shared, member)))
+
+// A wait ends when the phase is complete or the CTA has been told to give up, which the watchdog (o_watch) does after 0.5 s without
+// a tile: the code around each of some twenty waits has to be short, since 20 warps of ten kinds share the instruction caches
+// (64 x 4096, 128 heads: 220 us with a way out inlined at every wait, 120 with the same ways made short).  What a role does after
+// a wait that gave up is harmless -- it touches the CTA's own buffers -- and each looks once a tile whether to leave.
+template <bool Cluster = false>
+__device__ __forceinline__ void wait(uint32_t smem, uint32_t bar, uint32_t parity) {
+  if constexpr (Cluster)
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 r;\nAGAIN:\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t@p bra DONE;\n\t"
+        "ld.volatile.shared.b32 r, [%2];\n\tsetp.eq.b32 q, r, 0;\n\t@q bra AGAIN;\nDONE:\n\t}"
+        :: "r"(bar), "r"(parity), "r"(AT(abort)) : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 r;\nAGAIN:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n\t@p bra DONE;\n\t"
+        "ld.volatile.shared.b32 r, [%2];\n\tsetp.eq.b32 q, r, 0;\n\t@q bra AGAIN;\nDONE:\n\t}"
+        :: "r"(bar), "r"(parity), "r"(AT(abort)) : "memory");
+}
+// The same by a warp that goes on together.
+template <bool Cluster = false>
+__device__ __forceinline__ void warp_wait(uint32_t smem, uint32_t bar, uint32_t parity) {
+  wait<Cluster>(smem, bar, parity);
+  __syncwarp();
+}
+__device__ __forceinline__ bool told_to_leave(uint32_t smem) {
+  uint32_t r;
+  asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(r) : "r"(AT(abort)) : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ bool warp_told_to_leave(uint32_t smem) { return __any_sync(0xffffffffu, told_to_leave(smem)); }
 __device__ __forceinline__ uint32_t timer_lo() {
   uint32_t t;
   asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
   return t;
 }
-// Bounded wait; false on abort or timeout.
-template <bool Cluster = false>
-__device__ __forceinline__ bool wait_bar(Shared& sh, uint64_t& b, uint32_t parity) {
-  const uint32_t bar = smem_u32(&b);
-  uint32_t t0 = 0;
-  while (!(Cluster ? mbar_test_cluster(bar, parity) : mbar_test(bar, parity))) {
-    if (sh.abort) return false;
-    const uint32_t t = timer_lo() | 1u;
-    if (t0 == 0) t0 = t;
-    if (t - t0 > kTimeoutNs) {
-      sh.abort = kTimedOut;
-      return false;
-    }
-  }
-  return true;
-}
-// The same by all lanes, with one answer.
-template <bool Cluster = false>
-__device__ __forceinline__ bool warp_wait(Shared& sh, uint64_t& b, uint32_t parity) {
-  return __all_sync(0xffffffffu, wait_bar<Cluster>(sh, b, parity));
-}
 // Bounded wait that ignores the abort flag: for what is in flight.
-__device__ __forceinline__ void drain_bar(uint64_t& b, uint32_t parity) {
-  uint32_t t0 = 0;
-  while (!mbar_test(smem_u32(&b), parity)) {
-    const uint32_t t = timer_lo() | 1u;
-    if (t0 == 0) t0 = t;
-    if (t - t0 > kTimeoutNs) return;
-  }
+__device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity) {
+  const uint32_t t0 = timer_lo();
+  while (!mbar_test(bar, parity))
+    if (timer_lo() - t0 > kTimeoutNs) return;
 }
-// A warp that has left its role tells the cluster if a wait gave up in this CTA.
-__device__ __forceinline__ void leave_role(Shared& sh, int* status, uint32_t cl) {
-  const int why = sh.abort;
-  if (why == kRunning || (threadIdx.x & 31) != 0) return;
-  if (why == kTimedOut) atomicCAS(status, 0, MLA_ERR_TIMEOUT);
-#pragma unroll 1
-  for (uint32_t r = 0; r < cl; ++r) {
-    const uint32_t at = map_to_rank(smem_u32(const_cast<int*>(&sh.abort)), r);
-    if (r != cluster_ctarank()) st_cluster_u32(at, kTold);
-  }
-}
-__device__ __forceinline__ void arrive(uint64_t& b) { mbar_arrive(smem_u32(&b)); }
 
 // ------------------------------------------------------------ instructions --
-// A value that all lanes have, as one that the compiler knows to be uniform (operands of MMAs then need no moves).
-__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 template <int R>
 __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(R)); }
 template <int R>
 __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(R)); }
 // `bytes` (a multiple of 16, both addresses 16-byte aligned) of global memory into shared memory.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t& bar) {
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-               :: "r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(&bar)) : "memory");
+               :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
 // 64 (x8) or 16 (x2) columns of 16 TMEM lanes: lane l of the warp gets, in r[4 n + 2 h + e], row 8 h + l / 4, column
 // 8 n + 2 (l % 4) + e.
@@ -229,37 +225,29 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 __device__ __forceinline__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn, int b_mn) {
   return idesc_bf16_f32(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
 }
-// Four steps of an MMA (all lanes call; an elected one issues), then the arrival on `bar` when they and all before them are
-// done.  One election for all of them: with one a step, the code around the steps took longer than they do.
+// Four steps of an MMA, issued by this thread, then the arrival on `bar` when they and all before them are done.
 // A from TMEM (8 columns a step), B 32 bytes a step.  accumulate: whether the first step adds to what is in D.
 __device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t bar) {
   asm volatile(
-      "{\n\t.reg .pred p, t, e;\n\t.reg .b64 b1, b2, b3;\n\t.reg .b32 a1, a2, a3;\n\t"
+      "{\n\t.reg .pred p, t;\n\t.reg .b64 b1, b2, b3;\n\t.reg .b32 a1, a2, a3;\n\t"
       "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
       "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
       "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t"
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}"
       :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(bar) : "memory");
 }
-// Both from shared memory, 16 tokens (2 KiB) of either a step.
-__device__ __forceinline__ void mma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t bar) {
+// Both from shared memory, 16 tokens (2 KiB) of either a step; `steps` of them.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, t, e;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
-      "add.s64 a1, %1, 128;\n\tadd.s64 a2, %1, 256;\n\tadd.s64 a3, %1, 384;\n\t"
-      "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}"
-      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(bar) : "memory");
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
 }
 // 16 latent values (two words of codes) as fp16 pairs; `scale` twice in a word.
 __device__ __forceinline__ void values16(uint32_t w0, uint32_t w1, uint32_t scale, uint32_t* v) {
@@ -393,180 +381,176 @@ struct Block {
 };
 
 // ------------------------------------------------------------------ S-CTA --
-// Warp 0: the two pages of every tile.  Dense: a copy for four rows (as far as the request has tokens); lists: a copy a
-// row, whose addresses are looked up while the tile before is being loaded.
+// Warp 0: a segment's q, then the two pages of every tile.  Dense: a copy for four rows (as far as the request has tokens); lists: a
+// copy a row, whose addresses are looked up while the tile before is being loaded.
 template <bool Sparse>
-__device__ void s_load(const Fp4Params& p, const CUtensorMap* q_map, Shared& sh, uint32_t smem, int part, const Block& blk) {
+__device__ void s_load(const Fp4Params& p, const CUtensorMap* q_map, uint32_t smem, int part, const Block& blk) {
   const int lane = threadIdx.x & 31;
   SegmentWalker w;
   w.init(p, part);
   Segment s;
-  uint32_t T = 0;
+  uint32_t i = 0, seg = 0;                      // pages (two a tile), segments
   bool withhold = p.withhold_first_load != 0;   // test hook: the first page never arrives
-  bool ok = true, armed[2] = {false, false};
-  uint32_t phase[2] = {0, 0};                   // of the last loads into each page
-  uint32_t seg = 0;
-  while (ok && w.next(s)) {
+  while (w.next(s)) {
     const int L = __ldg(p.lens + s.b);
-    if (!warp_wait(sh, sh.q_empty, (seg & 1) ^ 1)) break;   // (the MMAs of the segment before are done)
-    if (lane == 0) {   // 64 dims of the block's rows a box, in the order in which keys come (a warpgroup's chunks in turn); rows past the request's are another's, or zeros past q's end
-      mbar_arrive_expect_tx(smem_u32(&sh.q_raw), 9u * static_cast<uint32_t>(p.q_box) * 128u);
+    warp_wait(smem, AT(q_empty), (seg & 1) ^ 1);   // (the MMAs of the segment before are done)
+    if (warp_told_to_leave(smem)) break;
+    if (lane == 0) {   // 64 dims of the block's rows a box, in the order in which keys come (a warpgroup's chunks in turn); rows past
+                       // the request's are another's, or zeros past q's end
+      mbar_arrive_expect_tx(AT(q_raw), 9u * static_cast<uint32_t>(p.q_box) * 128u);
+#pragma unroll 1
       for (int c = 0; c < 9; ++c)
-        tma_load_3d(smem + (c < 4 ? 2 * c : c < 8 ? 2 * c - 7 : 8) * kQChunk, q_map, smem_u32(&sh.q_raw), 0, s.b * p.rows + blk.rb * kRowsPerPair, c);
+        tma_load_3d(smem + (c < 4 ? 2 * c : c < 8 ? 2 * c - 7 : 8) * kQChunk, q_map, AT(q_raw), 0, s.b * p.rows + blk.rb * kRowsPerPair, c);
     }
     __syncwarp();
     ++seg;
-    for (int k = s.kb; ok && k < s.ke; k += 2, ++T) {
-      for (int h = 0; h < 2; ++h) {
-        const int n = k + h < s.ke ? min(kPageTokens, L - (k + h) * kPageTokens) : 0;   // rows
-        const uint32_t dst = smem + kOffRaw + h * kRawPage;
-        const uint8_t* row[2] = {nullptr, nullptr};
-        if constexpr (Sparse) {
-          int t[2];
+    const int end = s.kb + 2 * tiles_of(s);
+#pragma unroll 1
+    for (int k = s.kb; k < end; ++k, ++i) {
+      const uint32_t h = i & 1, full = AT(raw_full) + 8 * h, dst = smem + kOffRaw + h * kRawPage;
+      const int n = k < s.ke ? min(kPageTokens, L - k * kPageTokens) : 0;   // rows
+      const uint8_t* row[2] = {nullptr, nullptr};
+      if constexpr (Sparse) {
+        int t[2];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) t[i] = lane + 32 * i < n ? entry_of(p, s.b, (k + h) * kPageTokens + lane + 32 * i) : 0;
+        for (int g = 0; g < 2; ++g) t[g] = lane + 32 * g < n ? entry_of(p, s.b, k * kPageTokens + lane + 32 * g) : 0;
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (lane + 32 * i < n) row[i] = row_at(p, t[i], entry_page(p, s.b, t[i]));
-        } else if (n > 0) {
-          row[0] = row_at(p, 0, page_of(p, s.b, k + h));
-        }
-        if (!warp_wait(sh, sh.raw_empty[h], (T & 1) ^ 1)) {
-          ok = false;
-          break;
-        }
-        if (withhold) {
-          withhold = false;
-          continue;
-        }
-        armed[h] = true;
-        phase[h] = T & 1;
-        if (lane == 0) {
-          if (n > 0) mbar_arrive_expect_tx(smem_u32(&sh.raw_full[h]), static_cast<uint32_t>(n) * kFp4RowBytes);
-          else arrive(sh.raw_full[h]);
-        }
-        __syncwarp();
-        if constexpr (Sparse) {
+        for (int g = 0; g < 2; ++g)
+          if (lane + 32 * g < n) row[g] = row_at(p, t[g], entry_page(p, s.b, t[g]));
+      } else if (n > 0) {
+        row[0] = row_at(p, 0, page_of(p, s.b, k));
+      }
+      warp_wait(smem, AT(raw_empty) + 8 * h, ((i >> 1) & 1) ^ 1);
+      if (warp_told_to_leave(smem)) goto out;
+      if (withhold) {
+        withhold = false;
+        ++i;
+        goto out;
+      }
+      if (lane == 0) {
+        if (n > 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(n) * kFp4RowBytes);
+        else mbar_arrive(full);
+      }
+      __syncwarp();
+      if constexpr (Sparse) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (row[i]) bulk_load(dst + (lane + 32 * i) * kFp4RowBytes + ((lane >> 2) + 8 * i) * 16, row[i], kFp4RowBytes, sh.raw_full[h]);
-        } else if (4 * lane < n) {
-          bulk_load(dst + lane * kRawGroup, row[0] + lane * 4 * kFp4RowBytes,
-                    static_cast<uint32_t>(min(4, n - 4 * lane)) * kFp4RowBytes, sh.raw_full[h]);
-        }
+        for (int g = 0; g < 2; ++g)
+          if (row[g]) bulk_load(dst + (lane + 32 * g) * kFp4RowBytes + ((lane >> 2) + 8 * g) * 16, row[g], kFp4RowBytes, full);
+      } else if (4 * lane < n) {
+        bulk_load(dst + lane * kRawGroup, row[0] + lane * 4 * kFp4RowBytes, static_cast<uint32_t>(min(4, n - 4 * lane)) * kFp4RowBytes, full);
       }
     }
   }
-  if (lane == 0)   // loads still in flight land before the CTA may leave
-    for (int h = 0; h < 2; ++h)
-      if (armed[h]) drain_bar(sh.raw_full[h], phase[h]);
-  if (lane == 0 && seg > 0) drain_bar(sh.q_raw, (seg - 1) & 1);
+out:
+  // Loads still in flight land before the CTA may leave: the last two pages' and the last q's (the phases that their barriers were
+  // armed for last; a withheld page's never comes, which costs the limit).
+  if (lane == 0) {
+    if (seg > 0) drain_bar(AT(q_raw), (seg - 1) & 1);
+    if (i > 0) drain_bar(AT(raw_full) + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1);
+    if (i > 1) drain_bar(AT(raw_full) + 8 * (i & 1), ((i - 2) >> 1) & 1);
+  }
   __syncwarp();
 }
 
 // Warps 12..19: a thread a token; warpgroup c takes latent dims [256 c, 256 c + 256) and half of the rope dims.  A tile's codes
-// are read into registers at once, which frees the page buffers for the next tile's loads.
+// are read into registers at once, which frees the page buffers for the next tile's loads; one copy of the code converts them, and
+// they move up.
 __device__ void s_convert(const Fp4Params& p, Shared& sh, uint32_t smem, int part, int c) {
   const int quad = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
-  const int h = quad >> 1;                                   // page of the tile
+  const uint32_t h = quad >> 1;                              // page of the tile
   const int r = (quad & 1) * 32 + lane;                      // row of the page
   const uint32_t raw = smem + kOffRaw + h * kRawPage + r * kFp4RowBytes + (r >> 2) * 16;
   const uint32_t tm = sh.tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + kKCol;
-  auto pair = [&](uint32_t at, uint32_t (&w)[8]) {           // 32 bytes of the row
-    const uint4 a = ld_shared_v4(raw + at), b = ld_shared_v4(raw + at + 16);
-    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-  };
   SegmentWalker w;
   w.init(p, part);
   Segment s;
   uint32_t T = 0;
   while (w.next(s)) {
-    for (int t = tiles_of(s); t > 0; --t, ++T) {
-      if (!warp_wait(sh, sh.raw_full[h], T & 1)) return;
-      uint32_t code[4][8], rope[8];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) pair(128 * c + 32 * k, code[k]);
-      const uint4 sc = ld_shared_v4(raw + kFp4Scales + 16 * c);
-      pair(kFp4Rope + 32 * c, rope);
-      __syncwarp();
-      if (lane == 0) arrive(sh.raw_empty[h]);
-      uint32_t scale[4] = {sc.x, sc.y, sc.z, sc.w};
 #pragma unroll 1
-      for (int k2 = 0; k2 < 4; k2 += 2) {   // (two copies of the code instead of four: 18 moves)
+    for (int t = tiles_of(s); t > 0; --t, ++T) {
+      warp_wait(smem, AT(raw_full) + 8 * h, T & 1);
+      if (warp_told_to_leave(smem)) return;
+      uint4 code[8];
+      uint4 rope[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t slot = 2 * (k2 + k) + c;
-          uint32_t v[32];
-          const uint32_t s01 = e4m3x2_to_f16x2<0>(scale[k]), s23 = e4m3x2_to_f16x2<1>(scale[k]);
-          values16(code[k][0], code[k][1], __byte_perm(s01, 0, 0x1010), v);
-          values16(code[k][2], code[k][3], __byte_perm(s01, 0, 0x3232), v + 8);
-          values16(code[k][4], code[k][5], __byte_perm(s23, 0, 0x1010), v + 16);
-          values16(code[k][6], code[k][7], __byte_perm(s23, 0, 0x3232), v + 24);
-          if (!warp_wait(sh, sh.k_empty[slot > 0 ? slot : 8], (T & 1) ^ 1)) return;   // (the first slot had the rope chunk last)
-          tc_fence_after();
-          tmem_st32(tm + slot * 32, v);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) arrive(sh.k_full[slot]);
-        }
+      for (int k = 0; k < 8; ++k) code[k] = ld_shared_v4(raw + 128 * c + 16 * k);
+      uint4 sc = ld_shared_v4(raw + kFp4Scales + 16 * c);
+      rope[0] = ld_shared_v4(raw + kFp4Rope + 32 * c);
+      rope[1] = ld_shared_v4(raw + kFp4Rope + 32 * c + 16);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(AT(raw_empty) + 8 * h);
+#pragma unroll 1
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t slot = 2 * k + c;
+        uint32_t v[32];
+        const uint32_t s01 = e4m3x2_to_f16x2<0>(sc.x), s23 = e4m3x2_to_f16x2<1>(sc.x);
+        values16(code[0].x, code[0].y, __byte_perm(s01, 0, 0x1010), v);
+        values16(code[0].z, code[0].w, __byte_perm(s01, 0, 0x3232), v + 8);
+        values16(code[1].x, code[1].y, __byte_perm(s23, 0, 0x1010), v + 16);
+        values16(code[1].z, code[1].w, __byte_perm(s23, 0, 0x3232), v + 24);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) code[0][j] = code[2][j], code[1][j] = code[3][j];
-        scale[0] = scale[2], scale[1] = scale[3];
+        for (int j = 0; j < 6; ++j) code[j] = code[j + 2];
+        sc.x = sc.y, sc.y = sc.z, sc.z = sc.w;
+        warp_wait(smem, AT(k_empty) + 8 * (slot > 0 ? slot : 8), (T & 1) ^ 1);   // (the first slot had the rope chunk last)
+        tc_fence_after();
+        tmem_st32(tm + slot * 32, v);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(AT(k_full) + 8 * slot);
       }
       uint32_t v[16];
+      const uint32_t x[8] = {rope[0].x, rope[0].y, rope[0].z, rope[0].w, rope[1].x, rope[1].y, rope[1].z, rope[1].w};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[2 * j] = e4m3x2_to_f16x2<0>(rope[j]), v[2 * j + 1] = e4m3x2_to_f16x2<1>(rope[j]);
-      if (!warp_wait(sh, sh.k_empty[0], T & 1)) return;   // the tile's first chunk is done with
+      for (int j = 0; j < 8; ++j) v[2 * j] = e4m3x2_to_f16x2<0>(x[j]), v[2 * j + 1] = e4m3x2_to_f16x2<1>(x[j]);
+      warp_wait(smem, AT(k_empty), T & 1);   // the tile's first chunk is done with
       tc_fence_after();
       tmem_st16(tm + 16 * c, v);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive(sh.k_full[8]);
+      if (lane == 0) mbar_arrive(AT(k_full) + 8 * 8);
     }
   }
 }
 
-// Warp 1 (all lanes; an elected one issues): S^T = K Q^T, 36 steps of 16 dims a tile.  Its loop is what the tensor pipe waits for, so
-// it is short: the latent chunks have a slot each, the rope chunk the first slot once more, and q lies in their order.
+// A lane of warp 1: S^T = K Q^T, 36 steps of 16 dims a tile.  Its loop is what the tensor pipe waits for, so it is short: the latent
+// chunks have a slot each, the rope chunk the first slot once more, and q lies in their order.
 __device__ void s_mma(const Fp4Params& p, Shared& sh, uint32_t smem, int part, const Block& blk) {
   SegmentWalker w;
   w.init(p, part);
   Segment s;
   uint32_t T = 0, seg = 0;
-  const uint32_t tmem = uniform(sh.tmem_base);
-  const uint32_t idesc = uniform(idesc_f16_f32(kTile, blk.N, 0, 0));
+  const uint32_t tmem = sh.tmem_base;
+  const uint32_t idesc = idesc_f16_f32(kTile, blk.N, 0, 0);
   const uint64_t q0 = smem_desc_sw128(smem, 16, 1024);
-  bool ok = true;
-  while (ok && w.next(s)) {
-    if (!warp_wait(sh, sh.q_full, seg & 1)) break;
+  while (w.next(s)) {
+    wait(smem, AT(q_full), seg & 1);
+#pragma unroll 1
     for (int t = tiles_of(s); t > 0; --t, ++T) {
       const uint32_t sb = T & 1;
-      ok = warp_wait(sh, sh.s_empty[sb], ((T >> 1) & 1) ^ 1);
-      const uint32_t d = uniform(tmem + sb * kTile);
+      wait(smem, AT(s_empty) + 8 * sb, ((T >> 1) & 1) ^ 1);
+      if (told_to_leave(smem)) goto out;
 #pragma unroll 1
-      for (int it = 0; it < kItems; ++it) {
-        ok = ok && warp_wait(sh, sh.k_full[it], T & 1);
-        if (!ok) break;
+      for (uint32_t it = 0; it < kItems; ++it) {
+        wait(smem, AT(k_full) + 8 * it, T & 1);
         tc_fence_after();
-        mma4_ts(d, tmem + kKCol + (it & 7) * 32, q0 + it * (kQChunk >> 4), idesc, it > 0, smem_u32(&sh.k_empty[it]));
+        mma4_ts(tmem + sb * kTile, tmem + kKCol + (it & 7) * 32, q0 + it * (kQChunk >> 4), idesc, it, AT(k_empty) + 8 * it);
       }
-      if (!ok) break;
-      mma_commit_warp(smem_u32(&sh.s_full[sb]));
+      commit(AT(s_full) + 8 * sb);
     }
-    if (ok) mma_commit_warp(smem_u32(&sh.q_empty));
+    commit(AT(q_empty));
     ++seg;
   }
-  mma_commit_warp(smem_u32(&sh.drain));   // behind everything issued
-  drain_bar(sh.drain, 0);
-  __syncwarp();
+out:
+  commit(AT(drain));   // behind everything issued
+  drain_bar(AT(drain), 0);
 }
 
 // Rows of q of warpgroup w's heads, in place: bf16 as loaded to fp16, a warp a row, and their scores' factors.
 __device__ __forceinline__ void s_scale_q(const Fp4Params& p, Shared& sh, uint32_t smem, const Block& blk, int w, int wq, int lane) {
   const float unit = p.scale_log2 * p.kv_scale;
-#pragma unroll 2
+#pragma unroll 1
   for (int j = wq; j < blk.half; j += 4) {
     const int n = w * blk.half + j;
     const uint32_t at = smem + (lane >> 3) * kQChunk + n * 128 + (((lane & 7) ^ (n & 7)) << 4);   // 16 bytes of chunk lane / 8
@@ -600,49 +584,49 @@ __device__ __forceinline__ void s_scale_q(const Fp4Params& p, Shared& sh, uint32
   }
   fence_proxy_async_smem();
   __syncwarp();
-  if (lane == 0) arrive(sh.q_full);
+  if (lane == 0) mbar_arrive(AT(q_full));
 }
 
 // Warps 4..11: warpgroup w has heads [w N/2, (w + 1) N/2) of the block.  Thread l of a warp has four of a tile's tokens (rows l / 4
 // + 8 {0..3} of the warp's TMEM quadrant) and up to 16 heads (8 i + 2 (l % 4) + {0, 1}).
 template <bool Sparse>
 __device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int part, const Block& blk) {
-  const int t = threadIdx.x - 128, w = t >> 7, wq = (t >> 5) & 3, lane = t & 31, tr = lane >> 2, tc = lane & 3;
+  const int t = threadIdx.x & 127, w = (threadIdx.x - 128) >> 7, wq = t >> 5, lane = t & 31, tr = lane >> 2, tc = lane & 3;
   const uint32_t bar = 1 + w;                     // named barrier of the warpgroup
   const int units = blk.half >> 3;                // of 8 heads
   const uint32_t tm = sh.tmem_base + (static_cast<uint32_t>(wq * 32) << 16) + w * blk.half;
   const uint32_t pkt = smem + kOffSend + w * kPktStride;
   // stmatrix: lane 8 m + r has row r of matrix m: unit m / 2 of a pair, rows 8 (m % 2) + r of 16
-  const int st_row = 32 * wq + 8 * ((lane >> 3) & 1) + (lane & 7), st_unit = lane >> 4;
+  const uint32_t st = pkt + (32 * wq + 8 * ((lane >> 3) & 1) + (lane & 7)) * 128, st_unit = (lane >> 4) ^ (lane & 7);
   SegmentWalker walk;
   walk.init(p, part);
   Segment s;
   uint32_t T = 0, seg = 0;
-  bool ok = true;
-  while (ok && walk.next(s)) {
+  while (walk.next(s)) {
     const int L = __ldg(p.lens + s.b);
     const int L_seq = Sparse ? __ldg(p.seqlens + s.b) : L;
-    const bool got = wait_bar(sh, sh.q_raw, seg & 1);
-    if (named_bar_or(bar, 128, !got)) break;
+    wait(smem, AT(q_raw), seg & 1);
+    if (named_bar_or(bar, 128, told_to_leave(smem))) break;
     ++seg;
     s_scale_q(p, sh, smem, blk, w, wq, lane);
+    if (t < 64) sh.ref[w][t] = -INFINITY;
     named_bar_sync(bar, 128);
-    float2 sl[8], nm[8], l[8];                       // score factor, offset - reference maximum (log2), sum of the thread's tokens
-    uint32_t fresh = 0;                              // heads that have no reference yet, two bits a unit
+    // score factor, offset - reference maximum (log2; -inf: none yet, exponentials are 0), sum over the thread's tokens
+    float2 sl[8], nm[8], l[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      // (units are taken in pairs: one past the heads gives exponents of -inf)
       sl[i] = i < units ? *reinterpret_cast<const float2*>(&sh.q_scale[w * blk.half + 8 * i + 2 * tc]) : make_float2(0.f, 0.f);
-      nm[i] = i < units ? make_float2(0.f, 0.f) : make_float2(-INFINITY, -INFINITY);
+      nm[i] = make_float2(-INFINITY, -INFINITY);
       l[i] = make_float2(0.f, 0.f);
-      if (i < units) fresh |= 3u << (2 * i);
     }
+    bool unset = true;   // some head has no reference yet
+#pragma unroll 1
     for (int k = s.kb; k < s.ke; k += 2, ++T) {
       const uint32_t sb = T & 1;
       const int ntok = min(min(kTile, (s.ke - k) * kPageTokens), L - k * kPageTokens);
-      const bool last = k + 2 >= s.ke;
-      // a token is seen by a head whose limit lies above its key (its position; none past the tile's tokens)
+      // a token is seen by a head whose limit lies above its key: its position; none past the tile's tokens
       const bool masked = ntok < kTile || (p.causal && (Sparse || k * kPageTokens + kTile > L_seq - p.s_q + 1));
+      const int limit = p.causal ? L_seq - p.s_q + 1 : INT_MAX, of_pos = p.causal ? 0xffff : 0;
       int key[4];
       if (masked) {
 #pragma unroll
@@ -658,35 +642,30 @@ __device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int par
           }
         }
       }
-      bool ok_t = wait_bar(sh, sh.s_full[sb], (T >> 1) & 1);
-      if (ok_t) ok_t = wait_bar(sh, sh.st_free[w], (T & 1) ^ 1);   // the last packet has been read
+      wait(smem, AT(s_full) + 8 * sb, (T >> 1) & 1);
+      wait(smem, AT(st_free) + 8 * w, (T & 1) ^ 1);   // the last packet has been read
       __syncwarp();
       tc_fence_after();
-      // the score of token row j (of the thread's four) and head c, seen or not
-      auto mask = [&](float& x, int j, int c) {
-        const int limit = p.causal ? L_seq - p.s_q + sh.pos[w * blk.half + c] + 1 : INT_MAX;
-        if (key[j] >= limit) x = -INFINITY;
-      };
       float2 ls[8];
       bool rebased = false;
       while (true) {   // once, or twice where references have to move
 #pragma unroll
         for (int i = 0; i < 8; ++i) ls[i] = make_float2(0.f, 0.f);
 #pragma unroll 1
-        for (int hf = 0; hf < 2; ++hf) {
-          const uint32_t at = tm + sb * kTile + (static_cast<uint32_t>(16 * hf) << 16);
-          const int row = st_row + 16 * hf;
+        for (uint32_t hf = 0; hf < 2; ++hf) {
           float x[32];   // [unit][token row 8 of 16][head 2]
-          tmem_ld_16x256(at, x);
+          tmem_ld_16x256(tm + sb * kTile + (hf << 20), x);
           tmem_wait_ld();
           if (masked) {
             const int k0 = hf ? key[2] : key[0], k1 = hf ? key[3] : key[1];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {   // heads 8 (e / 2) + 2 tc + e % 2
-              const int c = 8 * (e >> 1) + 2 * tc + (e & 1);
-              const int limit = p.causal ? L_seq - p.s_q + sh.pos[min(w * blk.half + c, 127)] + 1 : INT_MAX;
-              if (k0 >= limit) x[4 * (e >> 1) + (e & 1)] = -INFINITY;
-              if (k1 >= limit) x[4 * (e >> 1) + 2 + (e & 1)] = -INFINITY;
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t pos = *reinterpret_cast<const uint32_t*>(&sh.pos[w * blk.half + 8 * i + 2 * tc]);   // (two heads')
+              const int l0 = limit + static_cast<int>(pos & of_pos), l1 = limit + static_cast<int>((pos >> 16) & of_pos);
+              if (k0 >= l0) x[4 * i] = -INFINITY;
+              if (k0 >= l1) x[4 * i + 1] = -INFINITY;
+              if (k1 >= l0) x[4 * i + 2] = -INFINITY;
+              if (k1 >= l1) x[4 * i + 3] = -INFINITY;
             }
           }
 #pragma unroll
@@ -702,7 +681,7 @@ __device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int par
               ls[i] = add2(ls[i], y);
               pk[q] = pack_f16x2(y.x, y.y);
             }
-            stmatrix4(pkt + row * 128 + (((2 * ii + st_unit) ^ (row & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
+            stmatrix4(st + hf * (16 * 128) + (((2 * ii) ^ st_unit) << 4), pk[0], pk[1], pk[2], pk[3]);
           }
         }
         fence_proxy_async_smem();
@@ -712,33 +691,31 @@ __device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int par
         float top = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(ls[i].x, ls[i].y));
-        const bool again = fresh != 0 || top > 0x1p14f || !ok_t;
-        if (!named_bar_or(bar, 128, again)) break;
-        if (named_bar_or(bar, 128, !ok_t)) {
-          ok = false;
-          break;
-        }
+        if (!named_bar_or(bar, 128, unset || top > 0x1p14f || told_to_leave(smem))) break;
+        if (named_bar_or(bar, 128, told_to_leave(smem))) return;
         rebased = true;
 #pragma unroll 1
         for (int ii = 0; 2 * ii < units; ++ii) {   // the heads' largest scores over the warp's tokens, two units at a time
           float2 cm[2] = {make_float2(-INFINITY, -INFINITY), make_float2(-INFINITY, -INFINITY)};
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll 1
+          for (uint32_t hf = 0; hf < 2; ++hf) {
             float x[8];
-            tmem_ld_16x256(tm + sb * kTile + 16 * ii + (static_cast<uint32_t>(16 * hf) << 16), x);
+            tmem_ld_16x256(tm + sb * kTile + 16 * ii + (hf << 20), x);
             tmem_wait_ld();
+            const int k0 = !masked ? 0 : hf ? key[2] : key[0], k1 = !masked ? 0 : hf ? key[3] : key[1];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if (masked) {
-                mask(x[2 * q], 2 * hf + (q & 1), min(16 * ii + 8 * (q >> 1) + 2 * tc, 126 - w * blk.half));
-                mask(x[2 * q + 1], 2 * hf + (q & 1), min(16 * ii + 8 * (q >> 1) + 2 * tc + 1, 127 - w * blk.half));
-              }
-              cm[q >> 1] = make_float2(fmaxf(cm[q >> 1].x, x[2 * q]), fmaxf(cm[q >> 1].y, x[2 * q + 1]));
+            for (int u = 0; u < 2; ++u) {
+              const uint32_t pos = *reinterpret_cast<const uint32_t*>(&sh.pos[w * blk.half + 16 * ii + 8 * u + 2 * tc]);
+              const int l0 = limit + static_cast<int>(pos & of_pos), l1 = limit + static_cast<int>((pos >> 16) & of_pos);
+              if (!masked || k0 < l0) cm[u].x = fmaxf(cm[u].x, x[4 * u]);
+              if (!masked || k0 < l1) cm[u].y = fmaxf(cm[u].y, x[4 * u + 1]);
+              if (!masked || k1 < l0) cm[u].x = fmaxf(cm[u].x, x[4 * u + 2]);
+              if (!masked || k1 < l1) cm[u].y = fmaxf(cm[u].y, x[4 * u + 3]);
             }
           }
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-#pragma unroll
+#pragma unroll 1
             for (int o = 4; o <= 16; o <<= 1) {
               cm[u].x = fmaxf(cm[u].x, __shfl_xor_sync(0xffffffffu, cm[u].x, o));
               cm[u].y = fmaxf(cm[u].y, __shfl_xor_sync(0xffffffffu, cm[u].y, o));
@@ -747,103 +724,93 @@ __device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int par
           }
         }
         named_bar_sync(bar, 128);
+        if (t < blk.half) {   // a thread a head: its new reference, and what it makes of the sums so far
+          const float m = fmaxf(fmaxf(sh.part[w][0][t], sh.part[w][1][t]), fmaxf(sh.part[w][2][t], sh.part[w][3][t])) *
+                          sh.q_scale[w * blk.half + t];
+          const float old = sh.ref[w][t];
+          float alpha = 1.f;
+          if (old == -INFINITY ? m > -INFINITY : m + old > kTop) {
+            if (old != -INFINITY) alpha = fast_exp2(kOffset - old - m);
+            sh.ref[w][t] = kOffset - m;
+          }
+          asm volatile("st.shared.f32 [%0], %1;" :: "r"(pkt + kPktAlpha + t * 4), "f"(alpha) : "memory");
+        }
+        named_bar_sync(bar, 128);
+        unset = false;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if (i < units) {
-            float alpha[2] = {1.f, 1.f};
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int c = 8 * i + 2 * tc + e;
-              const float m = fmaxf(fmaxf(sh.part[w][0][c], sh.part[w][1][c]), fmaxf(sh.part[w][2][c], sh.part[w][3][c])) *
-                              (e ? sl[i].y : sl[i].x);
-              float& n = e ? nm[i].y : nm[i].x;
-              float& sum = e ? l[i].y : l[i].x;
-              const uint32_t bit = 1u << (2 * i + e);
-              if (fresh & bit) {
-                if (m > -INFINITY) n = kOffset - m, fresh &= ~bit;
-              } else if (m + n > kTop) {
-                alpha[e] = fast_exp2(kOffset - n - m);
-                n = kOffset - m;
-                sum *= alpha[e];
-              }
-            }
-            if (wq == 0 && tr == 0)
-              asm volatile("st.shared.v2.f32 [%0], {%1, %2};" :: "r"(pkt + kPktAlpha + (8 * i + 2 * tc) * 4), "f"(alpha[0]),
-                           "f"(alpha[1]) : "memory");
+            nm[i] = *reinterpret_cast<const float2*>(&sh.ref[w][8 * i + 2 * tc]);
+            l[i].x *= ld_shared_f32(pkt + kPktAlpha + (8 * i + 2 * tc) * 4);
+            l[i].y *= ld_shared_f32(pkt + kPktAlpha + (8 * i + 2 * tc) * 4 + 4);
+            unset = unset || nm[i].x == -INFINITY || nm[i].y == -INFINITY;
           }
       }
-      if (!ok) break;
       __syncwarp();
-      if (lane == 0) arrive(sh.s_empty[sb]);   // S^T has been read
+      if (lane == 0) mbar_arrive(AT(s_empty) + 8 * sb);   // S^T has been read
 #pragma unroll
       for (int i = 0; i < 8; ++i) l[i] = add2(l[i], ls[i]);
-      if (last) {   // the heads' sums over the warpgroup's threads
+      const bool last = k + 2 >= s.ke;
+      if (t == 0) asm volatile("st.shared.u32 [%0], %1;" :: "r"(pkt + kPktFlag), "r"(rebased ? 1 : 0) : "memory");
+      if (rebased || last) {
+        if (last) {   // the heads' sums over the warpgroup's threads
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i < units) {
-            float2 v = l[i];
+          for (int i = 0; i < 8; ++i) {
 #pragma unroll
             for (int o = 4; o <= 16; o <<= 1) {
-              v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-              v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+              l[i].x += __shfl_xor_sync(0xffffffffu, l[i].x, o);
+              l[i].y += __shfl_xor_sync(0xffffffffu, l[i].y, o);
             }
-            if (rebased && i == 0) named_bar_sync(bar, 128);   // (part still holds the maxima)
-            if (tr == 0) {
-              *reinterpret_cast<float2*>(&sh.part[w][wq][8 * i + 2 * tc]) = v;
-              if (wq == 0) *reinterpret_cast<float2*>(&sh.ref[w][8 * i + 2 * tc]) = nm[i];
-            }
+            if (tr == 0) *reinterpret_cast<float2*>(&sh.part[w][wq][8 * i + 2 * tc]) = l[i];
           }
-        named_bar_sync(bar, 128);
-        const int c = t & 127;
-        if (c < blk.half) {
-          const float sum = (sh.part[w][0][c] + sh.part[w][1][c]) + (sh.part[w][2][c] + sh.part[w][3][c]);
-          asm volatile("st.shared.f32 [%0], %1;" :: "r"(pkt + kPktInvL + c * 4), "f"(sum == 0.f ? 0.f : p.kv_scale / sum)
-                       : "memory");
-          const int n = w * blk.half + c, g = blk.rb * kRowsPerPair + n;
-          if (n < blk.valid) {
-            const float lse = sum == 0.f ? -INFINITY : (log2f(sum) - sh.ref[w][c]) * kLn2;
-            const int ns0 = __ldg(p.num_splits + s.b), nsplit = __ldg(p.num_splits + s.b + 1) - ns0;
-            if (nsplit == 1) p.lse[static_cast<int64_t>(s.b) * p.rows + g] = lse;
-            else if (split_slot_ok(p, ns0 + s.split))   // (NaN travels as +inf, whose weight the merge makes NaN)
-              p.lse_part[static_cast<int64_t>(ns0 + s.split) * p.rows + g] = isnan(lse) ? INFINITY : lse;
+          named_bar_sync(bar, 128);
+          if (t < blk.half) {
+            const float sum = (sh.part[w][0][t] + sh.part[w][1][t]) + (sh.part[w][2][t] + sh.part[w][3][t]);
+            asm volatile("st.shared.f32 [%0], %1;" :: "r"(pkt + kPktInvL + t * 4),
+                         "f"(sum == 0.f ? 0.f : __fdividef(p.kv_scale, sum)) : "memory");
+            const int n = w * blk.half + t, g = blk.rb * kRowsPerPair + n;
+            if (n < blk.valid) {
+              const float lse = sum == 0.f ? -INFINITY : (log2f(sum) - sh.ref[w][t]) * kLn2;
+              const int ns0 = __ldg(p.num_splits + s.b), nsplit = __ldg(p.num_splits + s.b + 1) - ns0;
+              if (nsplit == 1) p.lse[static_cast<int64_t>(s.b) * p.rows + g] = lse;
+              else if (split_slot_ok(p, ns0 + s.split))   // (NaN travels as +inf, whose weight the merge makes NaN)
+                p.lse_part[static_cast<int64_t>(ns0 + s.split) * p.rows + g] = isnan(lse) ? INFINITY : lse;
+            }
           }
         }
-      }
-      if (t - 128 * w == 0) asm volatile("st.shared.u32 [%0], %1;" :: "r"(pkt + kPktFlag), "r"(rebased ? 1 : 0) : "memory");
-      if (rebased || last) {
         fence_proxy_async_smem();
         named_bar_sync(bar, 128);
-      } else if (t - 128 * w == 0) {
-        fence_proxy_async_smem();
       }
-      if (t - 128 * w == 0) arrive(sh.p_ready[w]);
+      if (t == 0) {
+        fence_proxy_async_smem();
+        mbar_arrive(AT(p_ready) + 8 * w);
+      }
     }
   }
 }
 
 // Warps 2 and 3 (a lane each): warpgroup w's packets to the partner.
-__device__ void s_ship(const Fp4Params& p, Shared& sh, uint32_t smem, int part, uint32_t peer, int w) {
+__device__ void s_ship(const Fp4Params& p, uint32_t smem, int part, uint32_t peer, int w) {
   const uint32_t src = smem + kOffSend + w * kPktStride, dst = map_to_rank(smem + w * kPktStride, peer);
-  const uint32_t full = map_to_rank(smem_u32(&sh.p_full[0]), peer);
+  const uint32_t full = map_to_rank(AT(p_full), peer);
   SegmentWalker walk;
   walk.init(p, part);
   Segment s;
   uint32_t T = 0;
-  bool ok = true;
-  while (ok && walk.next(s)) {
+  while (walk.next(s)) {
+#pragma unroll 1
     for (int t = tiles_of(s); t > 0; --t, ++T) {
       const uint32_t slot = T & 1;
-      if (!wait_bar(sh, sh.p_ready[w], T & 1) ||
-          !wait_bar<true>(sh, sh.credit[slot], ((T >> 1) & 1) ^ 1)) {
-        ok = false;
-        break;
-      }
+      wait(smem, AT(p_ready) + 8 * w, T & 1);
+      wait<true>(smem, AT(credit) + 8 * slot, ((T >> 1) & 1) ^ 1);
+      if (told_to_leave(smem)) goto out;
       bulk_copy_to_cluster(dst + slot * 2 * kPktStride, src, kPktBytes, full + slot * 8);
       bulk_commit_group();
       bulk_wait_group_read<0>();
-      arrive(sh.st_free[w]);
+      mbar_arrive(AT(st_free) + 8 * w);
     }
   }
+out:
   bulk_wait_group<0>();   // copies land before the CTA may leave
 }
 
@@ -860,7 +827,7 @@ __device__ __forceinline__ int ld_shared_s32(uint32_t a) {
 // loads of a list entry, of that token's table entry, and the ring's store are a page apart, so that none waits for the one before.
 // (What is out of range is reported by the S-CTA's loads, and read as row 0 here.)
 template <bool Sparse>
-__device__ void o_lookup(const Fp4Params& p, Shared& sh, uint32_t smem, int part) {
+__device__ void o_lookup(const Fp4Params& p, uint32_t smem, int part) {
   const int lane = threadIdx.x & 31;
   struct Tokens { int t[2], n, b, k; bool valid; } tok;
   struct Blocks { int t[2], blk[2], n; bool valid; } blk;
@@ -873,7 +840,8 @@ __device__ void o_lookup(const Fp4Params& p, Shared& sh, uint32_t smem, int part
     const bool end = !blk.valid && !tok.valid && !it.valid;
     if (blk.valid || end) {
       const uint32_t slot = i % kRowSlots, at = smem + kOffRows + slot * kRowBytes;
-      if (!warp_wait(sh, sh.rows_empty[slot], ((i / kRowSlots) & 1) ^ 1)) return;
+      warp_wait(smem, AT(rows_empty) + 8 * slot, ((i / kRowSlots) & 1) ^ 1);
+      if (warp_told_to_leave(smem)) return;
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         const int r = lane + 32 * g, t = Sparse ? blk.t[g] : r;
@@ -886,7 +854,7 @@ __device__ void o_lookup(const Fp4Params& p, Shared& sh, uint32_t smem, int part
       }
       if (lane == 0) st_shared_s32(at + 256, end ? -1 : blk.n);
       __syncwarp();
-      if (lane == 0) arrive(sh.rows_full[slot]);
+      if (lane == 0) mbar_arrive(AT(rows_full) + 8 * slot);
       if (end) return;
       ++i;
     }
@@ -920,7 +888,7 @@ __device__ void o_lookup(const Fp4Params& p, Shared& sh, uint32_t smem, int part
 // Warps 12..19: the latent dims of every page, from global memory through registers into shared memory as fp16 (64 tokens by
 // 64 dims a chunk, 128-byte swizzle).  A thread has one row of a page (a quarter warp eight rows: eight different banks) and a chunk of
 // either half; as soon as it has converted one it loads the same one of the next page, which it needs a page later.
-__device__ void o_convert(const Fp4Params& p, Shared& sh, uint32_t smem) {
+__device__ void o_convert(const Fp4Params& p, uint32_t smem) {
   const int lane = threadIdx.x & 31, r = 8 * ((threadIdx.x >> 5) - 12) + (lane & 7), chunk = lane >> 3;   // of the 4 in a half
   const uint8_t* const kv = reinterpret_cast<const uint8_t*>(p.kv);
   const uint32_t to = smem + kOffV + chunk * kVChunk + r * 128;
@@ -941,11 +909,12 @@ __device__ void o_convert(const Fp4Params& p, Shared& sh, uint32_t smem) {
     n = n_next;
     {   // where the next page's row is
       const uint32_t slot = i % kRowSlots, at = smem + kOffRows + slot * kRowBytes;
-      if (!warp_wait(sh, sh.rows_full[slot], (i / kRowSlots) & 1)) return;
+      warp_wait(smem, AT(rows_full) + 8 * slot, (i / kRowSlots) & 1);
+      if (warp_told_to_leave(smem)) return;
       n_next = ld_shared_s32(at + 256);
       src = kv + static_cast<int64_t>(ld_shared_s32(at + r * 4)) * kFp4RowBytes;
       __syncwarp();
-      if (lane == 0) arrive(sh.rows_empty[slot]);
+      if (lane == 0) mbar_arrive(AT(rows_empty) + 8 * slot);
     }
     ++i;
 #pragma unroll
@@ -955,7 +924,7 @@ __device__ void o_convert(const Fp4Params& p, Shared& sh, uint32_t smem) {
         continue;
       }
       const uint32_t vs = (2 * i + h) % kVSlots;   // page i - 2
-      if (!warp_wait(sh, sh.v_empty[vs], ((i / (kVSlots / 2)) & 1) ^ 0)) return;
+      warp_wait(smem, AT(v_empty) + 8 * vs, (i / (kVSlots / 2)) & 1);
       if (n > 0) {   // (0: a tile's second page that is none)
         uint32_t x[32];
         if (r < n) {
@@ -977,114 +946,108 @@ __device__ void o_convert(const Fp4Params& p, Shared& sh, uint32_t smem) {
         load(h);
       }
       __syncwarp();
-      if (lane == 0) arrive(sh.v_full[vs]);
+      if (lane == 0) mbar_arrive(AT(v_full) + 8 * vs);
     }
   }
 }
 
-// Warp 1 (all lanes; an elected one issues): O += P V, for every page and 256-column half of O a step per 16 tokens.
+// A lane of warp 1: O += P V, for every page and 256-column half of O a step per 16 tokens.
 __device__ void o_mma(const Fp4Params& p, Shared& sh, uint32_t smem, int part) {
-  const int lane = threadIdx.x & 31;
   SegmentWalker w;
   w.init(p, part);
   Segment s;
   uint32_t T = 0, seg = 0, nresc = 0;
-  const uint32_t tmem = uniform(sh.tmem_base);
+  const uint32_t tmem = sh.tmem_base;
   constexpr uint32_t idesc = idesc_f16_f32(128, 256, 1, 1);
-  bool ok = true;
-  while (ok && w.next(s)) {
-    if (seg > 0 && !warp_wait(sh, sh.o_free, (seg - 1) & 1)) {
-      ok = false;
-      break;
-    }
-    for (int k = s.kb; ok && k < s.ke; k += 2, ++T) {
-      const uint32_t slot = T & 1;
-      const uint32_t pkt = smem + slot * 2 * kPktStride;
+  const uint64_t v0 = smem_desc_sw128(smem + kOffV, kVChunk, 1024);
+  while (w.next(s)) {
+    if (seg > 0) wait(smem, AT(o_free), (seg - 1) & 1);
+#pragma unroll 1
+    for (int k = s.kb; k < s.ke; k += 2, ++T) {
+      const uint32_t slot = T & 1, pkt = smem + slot * 2 * kPktStride, full = AT(p_full) + 8 * slot;
       const bool last = k + 2 >= s.ke;
       const int ntok = tile_tokens(p, s, k);
-      if (lane == 0) mbar_arrive_expect_tx(smem_u32(&sh.p_full[slot]), 2 * kPktBytes);
-      __syncwarp();
-      if (!warp_wait<true>(sh, sh.p_full[slot], (T >> 1) & 1)) {
-        ok = false;
-        break;
-      }
-      if (last)   // before the slot can be reused
-        st_shared_v4(smem + kOffInvL + lane * 16, ld_shared_v4(pkt + (lane >> 4) * kPktStride + kPktInvL + (lane & 15) * 16));
-      const float flag = ld_shared_f32(pkt + (lane & 1) * kPktStride + kPktFlag);
-      __syncwarp();
-      if (k != s.kb && __any_sync(0xffffffffu, __float_as_uint(flag) != 0)) {   // scale O before adding this tile
-        mma_commit_warp(smem_u32(&sh.o_sync));
-        if (!warp_wait(sh, sh.o_sync, nresc & 1)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) {
-          sh.cmd = 1;
-          sh.cmd_arg = static_cast<int>(slot);
-          arrive(sh.corr_go);
-        }
-        __syncwarp();
-        if (!warp_wait(sh, sh.corr_done, nresc & 1)) {
-          ok = false;
-          break;
-        }
+      mbar_arrive_expect_tx(full, 2 * kPktBytes);
+      wait<true>(smem, full, (T >> 1) & 1);
+      if (told_to_leave(smem)) goto out;
+      if (k != s.kb && (ld_shared_s32(pkt + kPktFlag) | ld_shared_s32(pkt + kPktStride + kPktFlag))) {   // scale O before adding
+        commit(AT(o_sync));
+        wait(smem, AT(o_sync), nresc & 1);
+        sh.cmd = 1;
+        sh.cmd_arg = static_cast<int>(slot);
+        mbar_arrive(AT(corr_go));
+        wait(smem, AT(corr_done), nresc & 1);
         ++nresc;
       }
       tc_fence_after();
-      const uint64_t a = smem_desc_sw128(uniform(pkt), kPktStride, 1024), v0 = smem_desc_sw128(smem + kOffV, kVChunk, 1024);
-      const uint32_t go_on = uniform(k != s.kb);
+      const uint64_t a = smem_desc_sw128(pkt, kPktStride, 1024);
 #pragma unroll 1
-      for (int ph = 0; ph < 4; ++ph) {   // half ph % 2 of page ph / 2, in slot ph (a tile of one page leaves two slots empty)
-        const int steps = (ntok - (ph >> 1) * kPageTokens + 15) >> 4;
-        ok = ok && warp_wait(sh, sh.v_full[ph], T & 1);
-        if (!ok) break;
-        tc_fence_after();
+      for (uint32_t ph = 0; ph < 4; ++ph) {   // half ph % 2 of page ph / 2, in slot ph (a tile of one page leaves two slots empty)
+        const int steps = min(4, (ntok - static_cast<int>(ph >> 1) * kPageTokens + 15) >> 4);
         const uint64_t pa = a + (ph >> 1) * (kPageTokens * 128 >> 4), vb = v0 + ph * (kVSlot >> 4);
-        if (steps >= 4) {
-          mma4_ss(tmem + 256 * (ph & 1), pa, vb, idesc, ph > 1 ? 1u : go_on, smem_u32(&sh.v_empty[ph]));
-        } else {
+        wait(smem, AT(v_full) + 8 * ph, T & 1);
+        tc_fence_after();
 #pragma unroll 1
-          for (int j = 0; j < steps; ++j)
-            mma_bf16_ss_warp(tmem + 256 * (ph & 1), pa + 128 * j, vb + 128 * j, idesc, j || ph > 1 ? 1u : go_on);
-          mma_commit_warp(smem_u32(&sh.v_empty[ph]));
-        }
+        for (int j = 0; j < steps; ++j) mma_ss(tmem + 256 * (ph & 1), pa + 128 * j, vb + 128 * j, idesc, k != s.kb || ph > 1 || j > 0);
+        commit(AT(v_empty) + 8 * ph);
       }
-      if (!ok) break;
-      mma_commit_warp(smem_u32(&sh.p_free[slot]));
-      if (last) {
-        mma_commit_warp(smem_u32(&sh.o_full));
-        if (lane == 0) {
-          sh.cmd = 2;
-          arrive(sh.corr_go);
-        }
-        __syncwarp();
+      if (last) {   // the output's factors, before the packet's slot can be reused
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+          st_shared_v4(smem + kOffInvL + i * 16, ld_shared_v4(pkt + (i >> 4) * kPktStride + kPktInvL + (i & 15) * 16));
+        commit(AT(o_full));
+        sh.cmd = 2;
+        mbar_arrive(AT(corr_go));
       }
+      commit(AT(p_free) + 8 * slot);
+      asm volatile("st.volatile.shared.b32 [%0], %1;" :: "r"(AT(tiles)), "r"(T + 1) : "memory");
     }
     ++seg;
   }
-  if (ok && seg > 0) warp_wait(sh, sh.o_free, (seg - 1) & 1);   // the last epilogue has taken its command
-  mma_commit_warp(smem_u32(&sh.drain));   // behind everything issued
-  drain_bar(sh.drain, 0);
-  __syncwarp();
-  if (lane == 0) {
-    sh.cmd = 3;
-    arrive(sh.corr_go);
-  }
-  __syncwarp();
+  if (seg > 0) wait(smem, AT(o_free), (seg - 1) & 1);   // the last epilogue has taken its command
+out:
+  commit(AT(drain));   // behind everything issued
+  drain_bar(AT(drain), 0);
+  sh.cmd = 3;
+  mbar_arrive(AT(corr_go));
+  asm volatile("st.volatile.shared.b32 [%0], %1;" :: "r"(AT(tiles)), "r"(kDone) : "memory");
 }
 
 // A lane of warp 2: gives packet slots back to the S-CTA once the MMAs are done with them.
-__device__ void o_forward(const Fp4Params& p, Shared& sh, int part, uint32_t peer) {
+__device__ void o_forward(const Fp4Params& p, uint32_t smem, int part, uint32_t peer) {
   SegmentWalker w;
   w.init(p, part);
   Segment s;
   uint32_t T = 0;
-  const uint32_t credit = map_to_rank(smem_u32(&sh.credit[0]), peer);
+  const uint32_t credit = map_to_rank(AT(credit), peer);
   while (w.next(s))
+#pragma unroll 1
     for (int t = tiles_of(s); t > 0; --t, ++T) {
-      if (!wait_bar(sh, sh.p_free[T & 1], (T >> 1) & 1)) return;
+      wait(smem, AT(p_free) + 8 * (T & 1), (T >> 1) & 1);
+      if (told_to_leave(smem)) return;
       mbar_arrive_remote(credit + (T & 1) * 8);
     }
+}
+
+// A lane of warp 3: the pair's limit on waiting.  No tile's MMAs for kTimeoutNs (every role's progress is needed for one): the status
+// word gets MLA_ERR_TIMEOUT, and all CTAs of the cluster are told to leave.
+__device__ void o_watch(const Fp4Params& p, uint32_t smem, uint32_t cl) {
+  uint32_t seen = 0, since = timer_lo();
+  while (true) {
+    uint32_t tiles;
+    asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(tiles) : "r"(AT(tiles)) : "memory");
+    if (tiles == kDone || told_to_leave(smem)) return;
+    const uint32_t now = timer_lo();
+    if (tiles != seen) {
+      seen = tiles;
+      since = now;
+    } else if (now - since > kTimeoutNs) {
+      atomicCAS(p.status, 0, MLA_ERR_TIMEOUT);
+      for (uint32_t r = 0; r < cl; ++r) st_cluster_u32(map_to_rank(AT(abort), r), 1u);
+      return;
+    }
+    __nanosleep(500);
+  }
 }
 
 // Warps 4..11: rescale O's rows, or normalise and store a finished segment.  Warpgroup wg owns O's columns [256 wg, 256 wg + 256).
@@ -1100,7 +1063,8 @@ __device__ void o_epilogue(const Fp4Params& p, Shared& sh, uint32_t smem, int pa
   uint32_t ncmd = 0, seg = 0;
   bool have = w.next(s);
   while (true) {
-    if (!warp_wait(sh, sh.corr_go, ncmd & 1)) break;
+    warp_wait(smem, AT(corr_go), ncmd & 1);
+    if (warp_told_to_leave(smem)) break;
     ++ncmd;
     const int cmd = sh.cmd;
     if (cmd == 3) break;
@@ -1123,11 +1087,11 @@ __device__ void o_epilogue(const Fp4Params& p, Shared& sh, uint32_t smem, int pa
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive(sh.corr_done);
+      if (lane == 0) mbar_arrive(AT(corr_done));
       continue;
     }
     if (!have) break;
-    if (!warp_wait(sh, sh.o_full, seg & 1)) break;
+    warp_wait(smem, AT(o_full), seg & 1);
     tc_fence_after();
     const float inv_l = ld_shared_f32(smem + kOffInvL + r * 4);
     const int ns0 = __ldg(p.num_splits + s.b);
@@ -1195,7 +1159,7 @@ __device__ void o_epilogue(const Fp4Params& p, Shared& sh, uint32_t smem, int pa
       } else {   // O may be overwritten by the next segment
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive(sh.o_free);
+        if (lane == 0) mbar_arrive(AT(o_free));
       }
       emit(c + 32, vb);
     }
@@ -1225,6 +1189,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_fp4_kernel(const __gri
   if (threadIdx.x == 0) {
     if (is_s) prefetch_tensormap(&q_map);
     sh.abort = 0;
+    sh.tiles = 0;
     sh.cmd = 0;
     auto init = [](uint64_t& b, uint32_t n) { mbar_init(smem_u32(&b), n); };
     for (int i = 0; i < 2; ++i) {
@@ -1274,13 +1239,14 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_fp4_kernel(const __gri
     regs_down<kRegsMisc>();
     const bool lane0 = (threadIdx.x & 31) == 0;
     if (is_s) {
-      if (warp == 0) s_load<Sparse>(p, &q_map, sh, smem, part, blk);
-      else if (warp == 1) s_mma(p, sh, smem, part, blk);
-      else if (lane0) s_ship(p, sh, smem, part, peer, warp - 2);
+      if (warp == 0) s_load<Sparse>(p, &q_map, smem, part, blk);
+      else if (lane0 && warp == 1) s_mma(p, sh, smem, part, blk);
+      else if (lane0) s_ship(p, smem, part, peer, warp - 2);
     } else {
-      if (warp == 0) o_lookup<Sparse>(p, sh, smem, part);
-      else if (warp == 1) o_mma(p, sh, smem, part);
-      else if (warp == 2 && lane0) o_forward(p, sh, part, peer);
+      if (warp == 0) o_lookup<Sparse>(p, smem, part);
+      else if (lane0 && warp == 1) o_mma(p, sh, smem, part);
+      else if (lane0 && warp == 2) o_forward(p, smem, part, peer);
+      else if (lane0) o_watch(p, smem, cl);
     }
   } else if (warp < 12) {
     regs_up<kRegsSoftmax>();
@@ -1289,10 +1255,9 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_fp4_kernel(const __gri
   } else {
     regs_down<kRegsConvert>();
     if (is_s) s_convert(p, sh, smem, part, (warp - 12) >> 2);
-    else o_convert(p, sh, smem);
+    else o_convert(p, smem);
   }
 
-  leave_role(sh, p.status, cl);
   __syncwarp();
   tc_fence_before();
   __syncthreads();

@@ -1,0 +1,1406 @@
+// Absorbed MLA decode over the 4-bit latent cache (mla_fp4.cuh): dense, and over lists of tokens.
+// C entries at the end (declared in mla.h).
+//
+//   s_t = scale * <q, kv_t>,  p_t = exp(s_t - max),  out = sum_t p_t kv_t[0:512] / sum_t p_t,  lse = ln sum_t exp(s_t)
+//
+// for every query row (head and query position) of a request, whose rows share the cached tokens.  A token is 352 bytes, and
+// 2176 FLOP per row: at 128 rows 791 FLOP/B, so the tensor pipes bound it, not HBM.  The codes become fp16 on the
+// way to them (code * scale is exact there; kv_scale goes into the scores and the output), and the work of a 128-row block is
+// split over a CTA pair, because an output accumulator of 128 x 512 takes all of one SM's TMEM:
+//   * the S-CTA (even cluster rank) computes S^T = K Q^T in tiles of 128 tokens (two pages): tokens on the TMEM lanes, so that
+//     the converted keys go from the converting threads' registers straight into TMEM as the MMA's A operand (a thread
+//     a token) and never through shared memory, whose bandwidth the operands need; Q is the B operand, in
+//     shared memory for a whole segment.  An MMA is as wide as there are heads (rounded up to 16), so few heads cost little.
+//     S^T is read with four tokens and 16 heads in a thread, which keeps the heads' running maxima and sums in registers;
+//     P^T goes to the partner with one shared-to-shared bulk copy a tile and warpgroup;
+//   * the O-CTA (odd rank) converts the latent part of the pages into shared memory (they hit L2 behind the S-CTA's loads) and
+//     accumulates O += P V, P^T and V both read by the MMA as they lie (tokens by rows: transposed operands).
+// Rows past 128 go to further pairs of the cluster, which walk the same pages.  A cluster is one part of the split schedule.
+//
+// The softmax is online, with the reference maximum of a head raised only where a score passes it by 2^8: the threads take the
+// exponentials against the old reference, and a vote (the barrier that ends a tile anyhow) tells whether one overflowed its room;
+// only then the tile is done again with new references, and O rescaled.  P is fp16 with an offset of 2^6, so that everything down to
+// 2^-20 of the reference keeps 11 bits.
+//
+// q is bf16 and K fp16, and an MMA takes one type: each row of q is multiplied by a power of two that brings its largest
+// element into [2^14, 2^15) and rounded to fp16, which is exact for elements down to 2^-31 of the largest.
+//
+// Every wait is bounded: a pair without progress for 0.5 s records MLA_ERR_TIMEOUT and tells every CTA of its cluster to leave, which
+// they do once what they have in flight has landed.
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+#include <stdint.h>
+
+#include <climits>
+#include <cstddef>
+#include <cmath>
+#include <mutex>
+
+#include "mla_fp4.cuh"
+#include "mla_kernels.h"
+#include "mla_ptx.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kThreads = 640;   // warps 0..3: loads, MMAs, copies; 4..11: softmax or rescale and epilogue; 12..19: conversion
+constexpr int kTile = 128;      // tokens of a tile: two pages
+// a page in the S-CTA's shared memory: 16 bytes between groups of four rows, so that eight rows' units lie in different banks
+constexpr uint32_t kRawGroup = 4 * kFp4RowBytes + 16;
+constexpr uint32_t kRawPage = kPageTokens / 4 * kRawGroup;
+constexpr uint32_t kQChunk = 128 * 128;       // 64 dims of the row block's q: up to 128 rows of 128 bytes, swizzled
+constexpr uint32_t kVChunk = 64 * 128;        // 64 dims of a page's values
+constexpr int kVSlots = 4;                    // half pages (64 tokens x 256 dims) of converted values
+constexpr uint32_t kVSlot = 4 * kVChunk;
+constexpr int kItems = 9;                     // chunks of converted keys a tile: 128 tokens x 64 dims, 32 TMEM columns, the first
+                                              // 8 (latent) in a slot each, the last (rope) in the first slot once more
+// a packet: what one softmax warpgroup (half of the row block's heads) sends to the O-CTA for a tile
+constexpr uint32_t kPktAlpha = 128 * 128;     // after P^T (128 tokens x 64 heads): float[64], factors of a rebase
+constexpr uint32_t kPktInvL = kPktAlpha + 256;   // float[64], the output's factors (last tile of a segment)
+constexpr uint32_t kPktFlag = kPktInvL + 256;    // whether alpha counts
+constexpr uint32_t kPktBytes = kPktFlag + 16;
+constexpr uint32_t kPktStride = 17 * 1024;
+constexpr uint32_t kRowSlots = 8;             // O-CTA: pages whose rows have been looked up
+constexpr uint32_t kRowBytes = 4 * (kPageTokens + 1);
+constexpr uint32_t kKCol = 256;               // S-CTA's TMEM columns: S^T of two tiles at 0 and 128, the keys from 256
+constexpr float kOffset = 6.f;                // P is taken against 2^-6 of the reference maximum
+constexpr float kTop = kOffset + 8.f;         // an exponent past this rebases its head
+constexpr uint32_t kTimeoutNs = 500u * 1000 * 1000;
+constexpr float kLn2 = 0.69314718055994530942f;
+// registers a thread: the three kinds of warpgroups share what the launch gets (640 x 96)
+constexpr int kRegsMisc = 48, kRegsSoftmax = 128, kRegsConvert = 88;
+static_assert(128 * kRegsMisc + 256 * kRegsSoftmax + 256 * kRegsConvert <= kThreads * 96, "more would wait forever");
+
+
+// shared memory (offsets from a 1024-byte aligned base)
+constexpr uint32_t kOffSend = 9 * kQChunk;                   // S-CTA: q first, then a packet of each warpgroup
+constexpr uint32_t kOffRaw = kOffSend + 2 * kPktStride;      // S-CTA: the two pages of a tile as cached
+constexpr uint32_t kOffV = 4 * kPktStride;                   // O-CTA: the packets of two tiles first, then values
+constexpr uint32_t kOffEpi = kOffV + kVSlots * kVSlot;       // O-CTA: 2 KiB transpose buffer per epilogue warp
+constexpr uint32_t kOffInvL = kOffEpi + 8 * 2048;            // O-CTA: output factors of the segment [2][64]
+constexpr uint32_t kOffRows = kOffInvL + 512;                // O-CTA: the ring of looked-up rows
+constexpr uint32_t kOffShared = kOffRaw + 2 * kRawPage;
+static_assert(kOffRows + kRowSlots * kRowBytes <= kOffShared, "O-CTA layout");
+
+constexpr uint32_t kDone = 0xffffffffu;
+
+struct Fp4Params : DecodeParams {
+  int q_box;   // q rows of a TMA box
+};
+
+struct Shared {
+  // S-CTA
+  uint64_t raw_full[2], raw_empty[2];         // a page of the tile has landed; is in the converters' registers
+  uint64_t k_full[kItems], k_empty[kItems];   // a chunk of keys is in TMEM; its MMAs are done (each once a tile)
+  uint64_t s_full[2], s_empty[2];
+  uint64_t q_raw, q_full, q_empty;            // the segment's q has landed; is fp16 (a softmax warp each); is done with
+  uint64_t p_ready[2], st_free[2];            // a warpgroup's packet is written; has been read by its copy
+  uint64_t credit[2];                         // the partner's receive slot is free (remote)
+  // O-CTA
+  uint64_t p_full[2], p_free[2];
+  uint64_t rows_full[kRowSlots], rows_empty[kRowSlots];
+  uint64_t v_full[kVSlots], v_empty[kVSlots];
+  uint64_t o_full, o_free, o_sync, corr_go, corr_done;
+  uint64_t drain;                             // both
+  uint32_t tmem_base;
+  uint32_t abort;                             // nonzero: leave
+  uint32_t tiles;                             // O-CTA: tiles whose MMAs are issued, kDone at the end
+  int cmd, cmd_arg;                           // O-CTA: 1 = rescale (by the packets of slot cmd_arg), 2 = epilogue, 3 = leave
+  alignas(16) float q_scale[128];                         // S-CTA: raw score -> log2 units, by column
+  alignas(16) float part[2][4][64];                       // a warpgroup's maxima or sums by warp and head
+  alignas(16) float ref[2][64];
+  uint16_t pos[128];                          // a column's query position
+};
+static_assert(alignof(Shared) == 16 && kOffShared % 16 == 0, "pairs of floats are read and written as 8 bytes");
+constexpr uint32_t kSmemBytes = kOffShared + sizeof(Shared);
+static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+
+// ------------------------------------------------------------------ waits --
+// Address of a member of Shared (an element of an array of barriers: + 8 i).
+#define AT(member) (smem + kOffShared + static_cast<uint32_t>(offsetof(Shared, member)))
+
+// A wait ends when the phase is complete or the CTA has been told to give up, which the watchdog (o_watch) does after 0.5 s without
+// a tile: the code around each of some twenty waits has to be short, since 20 warps of ten kinds share the instruction caches
+// (64 x 4096, 128 heads: 220 us with a way out inlined at every wait, 120 with the same ways made short).  What a role does after
+// a wait that gave up is harmless -- it touches the CTA's own buffers -- and each looks once a tile whether to leave.
+template <bool Cluster = false>
+__device__ __forceinline__ void wait(uint32_t smem, uint32_t bar, uint32_t parity) {
+  if constexpr (Cluster)
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 r;\nAGAIN:\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t@p bra DONE;\n\t"
+        "ld.volatile.shared.b32 r, [%2];\n\tsetp.eq.b32 q, r, 0;\n\t@q bra AGAIN;\nDONE:\n\t}"
+        :: "r"(bar), "r"(parity), "r"(AT(abort)) : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 r;\nAGAIN:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n\t@p bra DONE;\n\t"
+        "ld.volatile.shared.b32 r, [%2];\n\tsetp.eq.b32 q, r, 0;\n\t@q bra AGAIN;\nDONE:\n\t}"
+        :: "r"(bar), "r"(parity), "r"(AT(abort)) : "memory");
+}
+// The same by a warp that goes on together.
+template <bool Cluster = false>
+__device__ __forceinline__ void warp_wait(uint32_t smem, uint32_t bar, uint32_t parity) {
+  wait<Cluster>(smem, bar, parity);
+  __syncwarp();
+}
+__device__ __forceinline__ bool told_to_leave(uint32_t smem) {
+  uint32_t r;
+  asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(r) : "r"(AT(abort)) : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ bool warp_told_to_leave(uint32_t smem) { return __any_sync(0xffffffffu, told_to_leave(smem)); }
+__device__ __forceinline__ uint32_t timer_lo() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
+// Bounded wait that ignores the abort flag: for what is in flight.
+__device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity) {
+  const uint32_t t0 = timer_lo();
+  while (!mbar_test(bar, parity))
+    if (timer_lo() - t0 > kTimeoutNs) return;
+}
+
+// ------------------------------------------------------------ instructions --
+template <int R>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(R)); }
+template <int R>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(R)); }
+// `bytes` (a multiple of 16, both addresses 16-byte aligned) of global memory into shared memory.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+// 64 (x8) or 16 (x2) columns of 16 TMEM lanes: lane l of the warp gets, in r[4 n + 2 h + e], row 8 h + l / 4, column
+// 8 n + 2 (l % 4) + e.
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, float (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+        "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]),
+        "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]),
+        "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, float (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+      : "r"(taddr));
+}
+// Four 8 x 8 matrices of 16-bit elements: register m of lane l has row l / 4, columns 2 (l % 4) and the next, of matrix m, whose
+// row r goes to the 16 bytes at lane 8 m + r's address.
+__device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};"
+               :: "r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+// Two floats an instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+// kind::f16 with fp16 inputs and fp32 accumulation (the bf16 descriptor without its two type bits).
+__device__ __forceinline__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn, int b_mn) {
+  return idesc_bf16_f32(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
+}
+// Four steps of an MMA, issued by this thread, then the arrival on `bar` when they and all before them are done.
+// A from TMEM (8 columns a step), B 32 bytes a step.  accumulate: whether the first step adds to what is in D.
+__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred p, t;\n\t.reg .b64 b1, b2, b3;\n\t.reg .b32 a1, a2, a3;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
+      "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t"
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}"
+      :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(bar) : "memory");
+}
+// Both from shared memory, 16 tokens (2 KiB) of either a step; `steps` of them.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
+}
+// 16 latent values (two words of codes) as fp16 pairs; `scale` twice in a word.
+__device__ __forceinline__ void values16(uint32_t w0, uint32_t w1, uint32_t scale, uint32_t* v) {
+  v[0] = mul_f16x2(e2m1x2_to_f16x2<0>(w0), scale);
+  v[1] = mul_f16x2(e2m1x2_to_f16x2<1>(w0), scale);
+  v[2] = mul_f16x2(e2m1x2_to_f16x2<2>(w0), scale);
+  v[3] = mul_f16x2(e2m1x2_to_f16x2<3>(w0), scale);
+  v[4] = mul_f16x2(e2m1x2_to_f16x2<0>(w1), scale);
+  v[5] = mul_f16x2(e2m1x2_to_f16x2<1>(w1), scale);
+  v[6] = mul_f16x2(e2m1x2_to_f16x2<2>(w1), scale);
+  v[7] = mul_f16x2(e2m1x2_to_f16x2<3>(w1), scale);
+}
+
+// ------------------------------------------------------------------- walk --
+struct Segment {
+  int b, kb, ke, split;   // request, page range, split index within the request
+};
+
+// Walks the segments of one part in order (the same walk in every role).
+struct SegmentWalker {
+  const Fp4Params* p;
+  int b_last, k_end, b, kb, split0;
+  bool first, done;
+  __device__ void init(const Fp4Params& prm, int part) {
+    p = &prm;
+    const int* m = prm.meta + part * kMetaInts;
+    b = m[0];
+    kb = m[1];
+    b_last = m[2];
+    k_end = m[3];
+    split0 = m[4];
+    first = true;
+    done = b < 0;
+    // a record that does not fit this call would send the walk past the caller's buffers: reported, and nothing walked
+    if (!done && (b >= prm.B || b_last < b || b_last >= prm.B || kb < 0 || k_end < 0 || split0 < 0)) {
+      atomicCAS(prm.status, 0, MLA_ERR_DEVICE_BOUNDS);
+      done = true;
+    }
+  }
+  __device__ bool next(Segment& s) {
+    while (!done) {
+      if (b > b_last) {
+        done = true;
+        break;
+      }
+      const int L = __ldg(p->lens + b);
+      const int nb = L > 0 ? (L - 1) / kPageTokens + 1 : 0;
+      const int k0 = first ? kb : 0;
+      const int k1 = b == b_last ? min(k_end, nb) : nb;
+      const int sp = first ? split0 : 0;
+      first = false;
+      const int cur = b++;
+      if (k1 > k0) {
+        s.b = cur, s.kb = k0, s.ke = k1, s.split = sp;
+        return true;
+      }
+    }
+    return false;
+  }
+};
+
+__device__ __forceinline__ int tiles_of(const Segment& s) { return (s.ke - s.kb + 1) >> 1; }
+// Listed tokens of the tile that starts at page k.
+__device__ __forceinline__ int tile_tokens(const Fp4Params& p, const Segment& s, int k) {
+  return min(min(kTile, (s.ke - k) * kPageTokens), __ldg(p.lens + s.b) - k * kPageTokens);
+}
+
+// Walks the pages of one part.
+struct PageIter {
+  SegmentWalker w;
+  Segment s;
+  int k;
+  bool valid;
+  __device__ void init(const Fp4Params& p, int part) {
+    w.init(p, part);
+    valid = true;
+    s.kb = s.ke = k = 0;
+  }
+  __device__ bool next() {   // on to the next page, the first one to begin with; a segment's last tile has two in any case
+    ++k;
+    if (valid && (k > s.ke || (k == s.ke && ((k - s.kb) & 1) == 0))) {
+      valid = w.next(s);
+      k = s.kb;
+    }
+    return valid;
+  }
+};
+
+// Whether split slot `slot` lies in the workspace, which holds B + num_parts; one outside (metadata that does not fit the
+// call) is reported and not written.
+__device__ __forceinline__ bool split_slot_ok(const Fp4Params& p, int slot) {
+  if (slot >= 0 && slot < p.B + p.num_parts) return true;
+  atomicCAS(p.status, 0, MLA_ERR_DEVICE_BOUNDS);
+  return false;
+}
+
+// Page number of page k of request b; one that is out of range is reported, and page 0 read in its place.
+__device__ __forceinline__ int page_of(const Fp4Params& p, int b, int k) {
+  int blk = -1;
+  if (k < p.max_blocks) blk = __ldg(p.block_table + static_cast<int64_t>(b) * p.max_blocks + k);
+  if (blk >= 0 && blk < p.num_blocks) return blk;
+  atomicCAS(p.status, 0, MLA_ERR_DEVICE_BOUNDS);
+  return 0;
+}
+// Position of list entry e of request b; -1 where the row of indices ends before it (reported).
+__device__ __forceinline__ int entry_of(const Fp4Params& p, int b, int e) {
+  if (e < p.idx_stride) return __ldg(p.indices + static_cast<int64_t>(b) * p.idx_stride + e);
+  atomicCAS(p.status, 0, MLA_ERR_DEVICE_BOUNDS);
+  return -1;
+}
+// Its page; -1 where the position is none of the request's (reported).
+__device__ __forceinline__ int entry_page(const Fp4Params& p, int b, int t) {
+  if (t >= 0 && t < __ldg(p.seqlens + b)) return page_of(p, b, t / kPageTokens);
+  atomicCAS(p.status, 0, MLA_ERR_DEVICE_BOUNDS);
+  return -1;
+}
+// The cached row of a token; row 0 for a bad one, which is always there.
+__device__ __forceinline__ const uint8_t* row_at(const Fp4Params& p, int t, int blk) {
+  const int64_t row = blk < 0 ? 0 : static_cast<int64_t>(blk) * kPageTokens + t % kPageTokens;
+  return reinterpret_cast<const uint8_t*>(p.kv) + row * kFp4RowBytes;
+}
+
+// A row block's heads: `valid` of its columns are query rows, the MMA has N (a multiple of 16), a softmax warpgroup N / 2.
+struct Block {
+  int rb, valid, N, half;
+  __device__ Block(const Fp4Params& p, int rb_) : rb(rb_) {
+    valid = min(kRowsPerPair, p.rows - rb * kRowsPerPair);
+    N = (valid + 15) & ~15;
+    half = N >> 1;
+  }
+};
+
+// ------------------------------------------------------------------ S-CTA --
+// Warp 0: a segment's q, then the two pages of every tile.  Dense: a copy for four rows (as far as the request has tokens); lists: a
+// copy a row, whose addresses are looked up while the tile before is being loaded.
+template <bool Sparse>
+__device__ void s_load(const Fp4Params& p, const CUtensorMap* q_map, uint32_t smem, int part, const Block& blk) {
+  const int lane = threadIdx.x & 31;
+  SegmentWalker w;
+  w.init(p, part);
+  Segment s;
+  uint32_t i = 0, seg = 0;                      // pages (two a tile), segments
+  bool withhold = p.withhold_first_load != 0;   // test hook: the first page never arrives
+  while (w.next(s)) {
+    const int L = __ldg(p.lens + s.b);
+    warp_wait(smem, AT(q_empty), (seg & 1) ^ 1);   // (the MMAs of the segment before are done)
+    if (warp_told_to_leave(smem)) break;
+    if (lane == 0) {   // 64 dims of the block's rows a box, in the order in which keys come (a warpgroup's chunks in turn); rows past
+                       // the request's are another's, or zeros past q's end
+      mbar_arrive_expect_tx(AT(q_raw), 9u * static_cast<uint32_t>(p.q_box) * 128u);
+#pragma unroll 1
+      for (int c = 0; c < 9; ++c)
+        tma_load_3d(smem + (c < 4 ? 2 * c : c < 8 ? 2 * c - 7 : 8) * kQChunk, q_map, AT(q_raw), 0, s.b * p.rows + blk.rb * kRowsPerPair, c);
+    }
+    __syncwarp();
+    ++seg;
+    const int end = s.kb + 2 * tiles_of(s);
+#pragma unroll 1
+    for (int k = s.kb; k < end; ++k, ++i) {
+      const uint32_t h = i & 1, full = AT(raw_full) + 8 * h, dst = smem + kOffRaw + h * kRawPage;
+      const int n = k < s.ke ? min(kPageTokens, L - k * kPageTokens) : 0;   // rows
+      const uint8_t* row[2] = {nullptr, nullptr};
+      if constexpr (Sparse) {
+        int t[2];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) t[g] = lane + 32 * g < n ? entry_of(p, s.b, k * kPageTokens + lane + 32 * g) : 0;
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+          if (lane + 32 * g < n) row[g] = row_at(p, t[g], entry_page(p, s.b, t[g]));
+      } else if (n > 0) {
+        row[0] = row_at(p, 0, page_of(p, s.b, k));
+      }
+      warp_wait(smem, AT(raw_empty) + 8 * h, ((i >> 1) & 1) ^ 1);
+      if (warp_told_to_leave(smem)) goto out;
+      if (withhold) {
+        withhold = false;
+        ++i;
+        goto out;
+      }
+      if (lane == 0) {
+        if (n > 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(n) * kFp4RowBytes);
+        else mbar_arrive(full);
+      }
+      __syncwarp();
+      if constexpr (Sparse) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+          if (row[g]) bulk_load(dst + (lane + 32 * g) * kFp4RowBytes + ((lane >> 2) + 8 * g) * 16, row[g], kFp4RowBytes, full);
+      } else if (4 * lane < n) {
+        bulk_load(dst + lane * kRawGroup, row[0] + lane * 4 * kFp4RowBytes, static_cast<uint32_t>(min(4, n - 4 * lane)) * kFp4RowBytes, full);
+      }
+    }
+  }
+out:
+  // Loads still in flight land before the CTA may leave: the last two pages' and the last q's (the phases that their barriers were
+  // armed for last; a withheld page's never comes, which costs the limit).
+  if (lane == 0) {
+    if (seg > 0) drain_bar(AT(q_raw), (seg - 1) & 1);
+    if (i > 0) drain_bar(AT(raw_full) + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1);
+    if (i > 1) drain_bar(AT(raw_full) + 8 * (i & 1), ((i - 2) >> 1) & 1);
+  }
+  __syncwarp();
+}
+
+// Warps 12..19: a thread a token; warpgroup c takes latent dims [256 c, 256 c + 256) and half of the rope dims.  A tile's codes
+// are read into registers at once, which frees the page buffers for the next tile's loads; one copy of the code converts them, and
+// they move up.
+__device__ void s_convert(const Fp4Params& p, Shared& sh, uint32_t smem, int part, int c) {
+  const int quad = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  const uint32_t h = quad >> 1;                              // page of the tile
+  const int r = (quad & 1) * 32 + lane;                      // row of the page
+  const uint32_t raw = smem + kOffRaw + h * kRawPage + r * kFp4RowBytes + (r >> 2) * 16;
+  const uint32_t tm = sh.tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + kKCol;
+  SegmentWalker w;
+  w.init(p, part);
+  Segment s;
+  uint32_t T = 0;
+  while (w.next(s)) {
+#pragma unroll 1
+    for (int t = tiles_of(s); t > 0; --t, ++T) {
+      warp_wait(smem, AT(raw_full) + 8 * h, T & 1);
+      if (warp_told_to_leave(smem)) return;
+      uint4 code[8];
+      uint4 rope[2];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) code[k] = ld_shared_v4(raw + 128 * c + 16 * k);
+      uint4 sc = ld_shared_v4(raw + kFp4Scales + 16 * c);
+      rope[0] = ld_shared_v4(raw + kFp4Rope + 32 * c);
+      rope[1] = ld_shared_v4(raw + kFp4Rope + 32 * c + 16);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(AT(raw_empty) + 8 * h);
+#pragma unroll 1
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t slot = 2 * k + c;
+        uint32_t v[32];
+        const uint32_t s01 = e4m3x2_to_f16x2<0>(sc.x), s23 = e4m3x2_to_f16x2<1>(sc.x);
+        values16(code[0].x, code[0].y, __byte_perm(s01, 0, 0x1010), v);
+        values16(code[0].z, code[0].w, __byte_perm(s01, 0, 0x3232), v + 8);
+        values16(code[1].x, code[1].y, __byte_perm(s23, 0, 0x1010), v + 16);
+        values16(code[1].z, code[1].w, __byte_perm(s23, 0, 0x3232), v + 24);
+#pragma unroll
+        for (int j = 0; j < 6; ++j) code[j] = code[j + 2];
+        sc.x = sc.y, sc.y = sc.z, sc.z = sc.w;
+        warp_wait(smem, AT(k_empty) + 8 * (slot > 0 ? slot : 8), (T & 1) ^ 1);   // (the first slot had the rope chunk last)
+        tc_fence_after();
+        tmem_st32(tm + slot * 32, v);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(AT(k_full) + 8 * slot);
+      }
+      uint32_t v[16];
+      const uint32_t x[8] = {rope[0].x, rope[0].y, rope[0].z, rope[0].w, rope[1].x, rope[1].y, rope[1].z, rope[1].w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[2 * j] = e4m3x2_to_f16x2<0>(x[j]), v[2 * j + 1] = e4m3x2_to_f16x2<1>(x[j]);
+      warp_wait(smem, AT(k_empty), T & 1);   // the tile's first chunk is done with
+      tc_fence_after();
+      tmem_st16(tm + 16 * c, v);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(AT(k_full) + 8 * 8);
+    }
+  }
+}
+
+// A lane of warp 1: S^T = K Q^T, 36 steps of 16 dims a tile.  Its loop is what the tensor pipe waits for, so it is short: the latent
+// chunks have a slot each, the rope chunk the first slot once more, and q lies in their order.
+__device__ void s_mma(const Fp4Params& p, Shared& sh, uint32_t smem, int part, const Block& blk) {
+  SegmentWalker w;
+  w.init(p, part);
+  Segment s;
+  uint32_t T = 0, seg = 0;
+  const uint32_t tmem = sh.tmem_base;
+  const uint32_t idesc = idesc_f16_f32(kTile, blk.N, 0, 0);
+  const uint64_t q0 = smem_desc_sw128(smem, 16, 1024);
+  while (w.next(s)) {
+    wait(smem, AT(q_full), seg & 1);
+#pragma unroll 1
+    for (int t = tiles_of(s); t > 0; --t, ++T) {
+      const uint32_t sb = T & 1;
+      wait(smem, AT(s_empty) + 8 * sb, ((T >> 1) & 1) ^ 1);
+      if (told_to_leave(smem)) goto out;
+#pragma unroll 1
+      for (uint32_t it = 0; it < kItems; ++it) {
+        wait(smem, AT(k_full) + 8 * it, T & 1);
+        tc_fence_after();
+        mma4_ts(tmem + sb * kTile, tmem + kKCol + (it & 7) * 32, q0 + it * (kQChunk >> 4), idesc, it, AT(k_empty) + 8 * it);
+      }
+      commit(AT(s_full) + 8 * sb);
+    }
+    commit(AT(q_empty));
+    ++seg;
+  }
+out:
+  commit(AT(drain));   // behind everything issued
+  drain_bar(AT(drain), 0);
+}
+
+// Rows of q of warpgroup w's heads, in place: bf16 as loaded to fp16, a warp a row, and their scores' factors.
+__device__ __forceinline__ void s_scale_q(const Fp4Params& p, Shared& sh, uint32_t smem, const Block& blk, int w, int wq, int lane) {
+  const float unit = p.scale_log2 * p.kv_scale;
+#pragma unroll 1
+  for (int j = wq; j < blk.half; j += 4) {
+    const int n = w * blk.half + j;
+    const uint32_t at = smem + (lane >> 3) * kQChunk + n * 128 + (((lane & 7) ^ (n & 7)) << 4);   // 16 bytes of chunk lane / 8
+    uint4 v[3];
+    v[0] = ld_shared_v4(at);
+    v[1] = ld_shared_v4(at + 4 * kQChunk);
+    v[2] = lane < 8 ? ld_shared_v4(at + 8 * kQChunk) : make_uint4(0, 0, 0, 0);
+    float top = 0.f;
+#pragma unroll
+    for (int u = 0; u < 3; ++u) {
+      const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = max_nan(top, max_nan(fabsf(bf16_lo(x[e])), fabsf(bf16_hi(x[e]))));
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const bool finite = top <= 3.4e38f;
+    const int e = finite ? max(static_cast<int>(__float_as_uint(top) >> 23), 41) : 141;   // at most a factor 2^100
+    // (a row with an infinity or a NaN becomes NaN; the factor is never 0, so that scores of -inf stay what they are)
+    const float sc = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
+    const float back = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+#pragma unroll
+    for (int u = 0; u < 3; ++u) {
+      const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+      uint32_t y[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) y[q] = finite ? pack_f16x2(bf16_lo(x[q]) * sc, bf16_hi(x[q]) * sc) : 0x7E007E00u;
+      if (u < 2 || lane < 8) st_shared_v4(at + 4 * u * kQChunk, make_uint4(y[0], y[1], y[2], y[3]));
+    }
+    if (lane == 0) sh.q_scale[n] = fmaxf(unit * back, 0x1p-126f);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(AT(q_full));
+}
+
+// Warps 4..11: warpgroup w has heads [w N/2, (w + 1) N/2) of the block.  Thread l of a warp has four of a tile's tokens (rows l / 4
+// + 8 {0..3} of the warp's TMEM quadrant) and up to 16 heads (8 i + 2 (l % 4) + {0, 1}).
+template <bool Sparse>
+__device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int part, const Block& blk) {
+  const int t = threadIdx.x & 127, w = (threadIdx.x - 128) >> 7, wq = t >> 5, lane = t & 31, tr = lane >> 2, tc = lane & 3;
+  const uint32_t bar = 1 + w;                     // named barrier of the warpgroup
+  const int units = blk.half >> 3;                // of 8 heads
+  const uint32_t tm = sh.tmem_base + (static_cast<uint32_t>(wq * 32) << 16) + w * blk.half;
+  const uint32_t pkt = smem + kOffSend + w * kPktStride;
+  // stmatrix: lane 8 m + r has row r of matrix m: unit m / 2 of a pair, rows 8 (m % 2) + r of 16
+  const uint32_t st = pkt + (32 * wq + 8 * ((lane >> 3) & 1) + (lane & 7)) * 128, st_unit = (lane >> 4) ^ (lane & 7);
+  SegmentWalker walk;
+  walk.init(p, part);
+  Segment s;
+  uint32_t T = 0, seg = 0;
+  while (walk.next(s)) {
+    const int L = __ldg(p.lens + s.b);
+    const int L_seq = Sparse ? __ldg(p.seqlens + s.b) : L;
+    wait(smem, AT(q_raw), seg & 1);
+    if (named_bar_or(bar, 128, told_to_leave(smem))) break;
+    ++seg;
+    s_scale_q(p, sh, smem, blk, w, wq, lane);
+    if (t < 64) sh.ref[w][t] = -INFINITY;
+    named_bar_sync(bar, 128);
+    // score factor, offset - reference maximum (log2; -inf: none yet, exponentials are 0), sum over the thread's tokens
+    float2 sl[8], nm[8], l[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      sl[i] = i < units ? *reinterpret_cast<const float2*>(&sh.q_scale[w * blk.half + 8 * i + 2 * tc]) : make_float2(0.f, 0.f);
+      nm[i] = make_float2(-INFINITY, -INFINITY);
+      l[i] = make_float2(0.f, 0.f);
+    }
+    bool unset = true;   // some head has no reference yet
+#pragma unroll 1
+    for (int k = s.kb; k < s.ke; k += 2, ++T) {
+      const uint32_t sb = T & 1;
+      const int ntok = min(min(kTile, (s.ke - k) * kPageTokens), L - k * kPageTokens);
+      // a token is seen by a head whose limit lies above its key: its position; none past the tile's tokens
+      const bool masked = ntok < kTile || (p.causal && (Sparse || k * kPageTokens + kTile > L_seq - p.s_q + 1));
+      const int limit = p.causal ? L_seq - p.s_q + 1 : INT_MAX, of_pos = p.causal ? 0xffff : 0;
+      int key[4];
+      if (masked) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int tok = 32 * wq + 8 * j + tr, e = k * kPageTokens + tok;
+          key[j] = INT_MAX;
+          if (tok < ntok) {
+            key[j] = e;
+            if (Sparse) {   // (a bad entry is reported by the loads, and seen by nobody)
+              const int at = e < p.idx_stride ? __ldg(p.indices + static_cast<int64_t>(s.b) * p.idx_stride + e) : -1;
+              key[j] = at >= 0 && at < L_seq ? at : INT_MAX;
+            }
+          }
+        }
+      }
+      wait(smem, AT(s_full) + 8 * sb, (T >> 1) & 1);
+      wait(smem, AT(st_free) + 8 * w, (T & 1) ^ 1);   // the last packet has been read
+      __syncwarp();
+      tc_fence_after();
+      float2 ls[8];
+      bool rebased = false;
+      while (true) {   // once, or twice where references have to move
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ls[i] = make_float2(0.f, 0.f);
+#pragma unroll 1
+        for (uint32_t hf = 0; hf < 2; ++hf) {
+          float x[32];   // [unit][token row 8 of 16][head 2]
+          tmem_ld_16x256(tm + sb * kTile + (hf << 20), x);
+          tmem_wait_ld();
+          if (false) {
+            const int k0 = hf ? key[2] : key[0], k1 = hf ? key[3] : key[1];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t pos = *reinterpret_cast<const uint32_t*>(&sh.pos[w * blk.half + 8 * i + 2 * tc]);   // (two heads')
+              const int l0 = limit + static_cast<int>(pos & of_pos), l1 = limit + static_cast<int>((pos >> 16) & of_pos);
+              if (k0 >= l0) x[4 * i] = -INFINITY;
+              if (k0 >= l1) x[4 * i + 1] = -INFINITY;
+              if (k1 >= l0) x[4 * i + 2] = -INFINITY;
+              if (k1 >= l1) x[4 * i + 3] = -INFINITY;
+            }
+          }
+#pragma unroll
+          for (int ii = 0; ii < 4; ++ii) {
+            if (2 * ii >= units) break;
+            uint32_t pk[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {   // unit 2 ii + q / 2, token row q % 2
+              const int i = 2 * ii + (q >> 1);
+              float2 y = fma2(make_float2(x[8 * ii + 2 * q], x[8 * ii + 2 * q + 1]), sl[i], nm[i]);
+              y.x = fast_exp2(y.x);
+              y.y = fast_exp2(y.y);
+              ls[i] = add2(ls[i], y);
+              pk[q] = pack_f16x2(y.x, y.y);
+            }
+            stmatrix4(st + hf * (16 * 128) + (((2 * ii) ^ st_unit) << 4), pk[0], pk[1], pk[2], pk[3]);
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        if (rebased) break;
+        // a P past 2^14 (no sum of four shows less), or a head without a reference: the tile again, with new references
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(ls[i].x, ls[i].y));
+        if (!named_bar_or(bar, 128, unset || top > 0x1p14f || told_to_leave(smem))) break;
+        if (named_bar_or(bar, 128, told_to_leave(smem))) return;
+        rebased = true;
+#pragma unroll 1
+        for (int ii = 0; 2 * ii < units; ++ii) {   // the heads' largest scores over the warp's tokens, two units at a time
+          float2 cm[2] = {make_float2(-INFINITY, -INFINITY), make_float2(-INFINITY, -INFINITY)};
+#pragma unroll 1
+          for (uint32_t hf = 0; hf < 2; ++hf) {
+            float x[8];
+            tmem_ld_16x256(tm + sb * kTile + 16 * ii + (hf << 20), x);
+            tmem_wait_ld();
+            const int k0 = !masked ? 0 : hf ? key[2] : key[0], k1 = !masked ? 0 : hf ? key[3] : key[1];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const uint32_t pos = *reinterpret_cast<const uint32_t*>(&sh.pos[w * blk.half + 16 * ii + 8 * u + 2 * tc]);
+              const int l0 = limit + static_cast<int>(pos & of_pos), l1 = limit + static_cast<int>((pos >> 16) & of_pos);
+              if (!masked || k0 < l0) cm[u].x = fmaxf(cm[u].x, x[4 * u]);
+              if (!masked || k0 < l1) cm[u].y = fmaxf(cm[u].y, x[4 * u + 1]);
+              if (!masked || k1 < l0) cm[u].x = fmaxf(cm[u].x, x[4 * u + 2]);
+              if (!masked || k1 < l1) cm[u].y = fmaxf(cm[u].y, x[4 * u + 3]);
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+#pragma unroll 1
+            for (int o = 4; o <= 16; o <<= 1) {
+              cm[u].x = fmaxf(cm[u].x, __shfl_xor_sync(0xffffffffu, cm[u].x, o));
+              cm[u].y = fmaxf(cm[u].y, __shfl_xor_sync(0xffffffffu, cm[u].y, o));
+            }
+            if (tr == 0) *reinterpret_cast<float2*>(&sh.part[w][wq][16 * ii + 8 * u + 2 * tc]) = cm[u];
+          }
+        }
+        named_bar_sync(bar, 128);
+        if (t < blk.half) {   // a thread a head: its new reference, and what it makes of the sums so far
+          const float m = fmaxf(fmaxf(sh.part[w][0][t], sh.part[w][1][t]), fmaxf(sh.part[w][2][t], sh.part[w][3][t])) *
+                          sh.q_scale[w * blk.half + t];
+          const float old = sh.ref[w][t];
+          float alpha = 1.f;
+          if (old == -INFINITY ? m > -INFINITY : m + old > kTop) {
+            if (old != -INFINITY) alpha = fast_exp2(kOffset - old - m);
+            sh.ref[w][t] = kOffset - m;
+          }
+          asm volatile("st.shared.f32 [%0], %1;" :: "r"(pkt + kPktAlpha + t * 4), "f"(alpha) : "memory");
+        }
+        named_bar_sync(bar, 128);
+        unset = false;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i < units) {
+            nm[i] = *reinterpret_cast<const float2*>(&sh.ref[w][8 * i + 2 * tc]);
+            l[i].x *= ld_shared_f32(pkt + kPktAlpha + (8 * i + 2 * tc) * 4);
+            l[i].y *= ld_shared_f32(pkt + kPktAlpha + (8 * i + 2 * tc) * 4 + 4);
+            unset = unset || nm[i].x == -INFINITY || nm[i].y == -INFINITY;
+          }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(AT(s_empty) + 8 * sb);   // S^T has been read
+#pragma unroll
+      for (int i = 0; i < 8; ++i) l[i] = add2(l[i], ls[i]);
+      const bool last = k + 2 >= s.ke;
+      if (t == 0) asm volatile("st.shared.u32 [%0], %1;" :: "r"(pkt + kPktFlag), "r"(rebased ? 1 : 0) : "memory");
+      if (rebased || last) {
+        if (last) {   // the heads' sums over the warpgroup's threads
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+#pragma unroll
+            for (int o = 4; o <= 16; o <<= 1) {
+              l[i].x += __shfl_xor_sync(0xffffffffu, l[i].x, o);
+              l[i].y += __shfl_xor_sync(0xffffffffu, l[i].y, o);
+            }
+            if (tr == 0) *reinterpret_cast<float2*>(&sh.part[w][wq][8 * i + 2 * tc]) = l[i];
+          }
+          named_bar_sync(bar, 128);
+          if (t < blk.half) {
+            const float sum = (sh.part[w][0][t] + sh.part[w][1][t]) + (sh.part[w][2][t] + sh.part[w][3][t]);
+            asm volatile("st.shared.f32 [%0], %1;" :: "r"(pkt + kPktInvL + t * 4),
+                         "f"(sum == 0.f ? 0.f : __fdividef(p.kv_scale, sum)) : "memory");
+            const int n = w * blk.half + t, g = blk.rb * kRowsPerPair + n;
+            if (n < blk.valid) {
+              const float lse = sum == 0.f ? -INFINITY : (log2f(sum) - sh.ref[w][t]) * kLn2;
+              const int ns0 = __ldg(p.num_splits + s.b), nsplit = __ldg(p.num_splits + s.b + 1) - ns0;
+              if (nsplit == 1) p.lse[static_cast<int64_t>(s.b) * p.rows + g] = lse;
+              else if (split_slot_ok(p, ns0 + s.split))   // (NaN travels as +inf, whose weight the merge makes NaN)
+                p.lse_part[static_cast<int64_t>(ns0 + s.split) * p.rows + g] = isnan(lse) ? INFINITY : lse;
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        named_bar_sync(bar, 128);
+      }
+      if (t == 0) {
+        fence_proxy_async_smem();
+        mbar_arrive(AT(p_ready) + 8 * w);
+      }
+    }
+  }
+}
+
+// Warps 2 and 3 (a lane each): warpgroup w's packets to the partner.
+__device__ void s_ship(const Fp4Params& p, uint32_t smem, int part, uint32_t peer, int w) {
+  const uint32_t src = smem + kOffSend + w * kPktStride, dst = map_to_rank(smem + w * kPktStride, peer);
+  const uint32_t full = map_to_rank(AT(p_full), peer);
+  SegmentWalker walk;
+  walk.init(p, part);
+  Segment s;
+  uint32_t T = 0;
+  while (walk.next(s)) {
+#pragma unroll 1
+    for (int t = tiles_of(s); t > 0; --t, ++T) {
+      const uint32_t slot = T & 1;
+      wait(smem, AT(p_ready) + 8 * w, T & 1);
+      wait<true>(smem, AT(credit) + 8 * slot, ((T >> 1) & 1) ^ 1);
+      if (told_to_leave(smem)) goto out;
+      bulk_copy_to_cluster(dst + slot * 2 * kPktStride, src, kPktBytes, full + slot * 8);
+      bulk_commit_group();
+      bulk_wait_group_read<0>();
+      mbar_arrive(AT(st_free) + 8 * w);
+    }
+  }
+out:
+  bulk_wait_group<0>();   // copies land before the CTA may leave
+}
+
+// ------------------------------------------------------------------ O-CTA --
+__device__ __forceinline__ void st_shared_s32(uint32_t a, int v) { asm volatile("st.shared.b32 [%0], %1;" :: "r"(a), "r"(v) : "memory"); }
+__device__ __forceinline__ int ld_shared_s32(uint32_t a) {
+  int v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// Warp 0: finds the cached rows of every page, kRowSlots pages ahead of the converters at most, puts their numbers into a ring in
+// shared memory (64 of them, and how many count; -1 after the last page) and has them brought into L2.  A lane has two rows; its
+// loads of a list entry, of that token's table entry, and the ring's store are a page apart, so that none waits for the one before.
+// (What is out of range is reported by the S-CTA's loads, and read as row 0 here.)
+template <bool Sparse>
+__device__ void o_lookup(const Fp4Params& p, uint32_t smem, int part) {
+  const int lane = threadIdx.x & 31;
+  struct Tokens { int t[2], n, b, k; bool valid; } tok;
+  struct Blocks { int t[2], blk[2], n; bool valid; } blk;
+  PageIter it;
+  it.init(p, part);
+  tok.valid = blk.valid = false;
+  tok.n = 0;
+  uint32_t i = 0;   // pages
+  while (true) {
+    const bool end = !blk.valid && !tok.valid && !it.valid;
+    if (blk.valid || end) {
+      const uint32_t slot = i % kRowSlots, at = smem + kOffRows + slot * kRowBytes;
+      warp_wait(smem, AT(rows_empty) + 8 * slot, ((i / kRowSlots) & 1) ^ 1);
+      if (warp_told_to_leave(smem)) return;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int r = lane + 32 * g, t = Sparse ? blk.t[g] : r;
+        const bool good = !end && r < blk.n && blk.blk[g] >= 0 && blk.blk[g] < p.num_blocks;
+        const int row = good ? blk.blk[g] * kPageTokens + t % kPageTokens : Sparse || end ? 0 : r;
+        st_shared_s32(at + r * 4, row);
+        if (Sparse && good) prefetch_l2(reinterpret_cast<const uint8_t*>(p.kv) + static_cast<int64_t>(row) * kFp4RowBytes, kFp4RowBytes);
+        if (!Sparse && good && lane == 0 && g == 0)
+          prefetch_l2(reinterpret_cast<const uint8_t*>(p.kv) + static_cast<int64_t>(row) * kFp4RowBytes, blk.n * kFp4RowBytes);
+      }
+      if (lane == 0) st_shared_s32(at + 256, end ? -1 : blk.n);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(AT(rows_full) + 8 * slot);
+      if (end) return;
+      ++i;
+    }
+    blk.valid = tok.valid;
+    blk.n = tok.n;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const int t = tok.t[g], k = Sparse ? t / kPageTokens : tok.k;
+      blk.t[g] = t;
+      blk.blk[g] = -1;
+      if (lane + 32 * g < tok.n && k < p.max_blocks && (!Sparse || (t >= 0 && t < __ldg(p.seqlens + tok.b))))
+        blk.blk[g] = __ldg(p.block_table + static_cast<int64_t>(tok.b) * p.max_blocks + k);
+    }
+    tok.valid = it.next();
+    tok.n = 0;
+    if (tok.valid) {
+      tok.b = it.s.b;
+      tok.k = it.k;
+      if (it.k < it.s.ke) tok.n = min(kPageTokens, __ldg(p.lens + it.s.b) - it.k * kPageTokens);
+      if constexpr (Sparse) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const int r = lane + 32 * g, e = it.k * kPageTokens + r;
+          tok.t[g] = r < tok.n && e < p.idx_stride ? __ldg(p.indices + static_cast<int64_t>(it.s.b) * p.idx_stride + e) : -1;
+        }
+      }
+    }
+  }
+}
+
+// Warps 12..19: the latent dims of every page, from global memory through registers into shared memory as fp16 (64 tokens by
+// 64 dims a chunk, 128-byte swizzle).  A thread has one row of a page (a quarter warp eight rows: eight different banks) and a chunk of
+// either half; as soon as it has converted one it loads the same one of the next page, which it needs a page later.
+__device__ void o_convert(const Fp4Params& p, uint32_t smem) {
+  const int lane = threadIdx.x & 31, r = 8 * ((threadIdx.x >> 5) - 12) + (lane & 7), chunk = lane >> 3;   // of the 4 in a half
+  const uint8_t* const kv = reinterpret_cast<const uint8_t*>(p.kv);
+  const uint32_t to = smem + kOffV + chunk * kVChunk + r * 128;
+  uint4 code[2][2];
+  uint32_t scale[2];
+  int n = 0, n_next = 0;   // rows that count, of this page and the next (-1: none follows)
+  const uint8_t* src = kv;
+  uint32_t i = 0;          // pages
+  auto load = [&](int h) {
+    if (r < n_next) {
+      code[h][0] = __ldg(reinterpret_cast<const uint4*>(src + 128 * h + 32 * chunk));
+      code[h][1] = __ldg(reinterpret_cast<const uint4*>(src + 128 * h + 32 * chunk + 16));
+      scale[h] = __ldg(reinterpret_cast<const uint32_t*>(src + kFp4Scales + 16 * h + 4 * chunk));
+    }
+  };
+#pragma unroll 1
+  for (bool first = true; n_next >= 0; first = false) {
+    n = n_next;
+    {   // where the next page's row is
+      const uint32_t slot = i % kRowSlots, at = smem + kOffRows + slot * kRowBytes;
+      warp_wait(smem, AT(rows_full) + 8 * slot, (i / kRowSlots) & 1);
+      if (warp_told_to_leave(smem)) return;
+      n_next = ld_shared_s32(at + 256);
+      src = kv + static_cast<int64_t>(ld_shared_s32(at + r * 4)) * kFp4RowBytes;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(AT(rows_empty) + 8 * slot);
+    }
+    ++i;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (first) {
+        load(h);
+        continue;
+      }
+      const uint32_t vs = (2 * i + h) % kVSlots;   // page i - 2
+      warp_wait(smem, AT(v_empty) + 8 * vs, (i / (kVSlots / 2)) & 1);
+      if (n > 0) {   // (0: a tile's second page that is none)
+        uint32_t x[32];
+        if (r < n) {
+          const uint32_t s01 = e4m3x2_to_f16x2<0>(scale[h]), s23 = e4m3x2_to_f16x2<1>(scale[h]);
+          values16(code[h][0].x, code[h][0].y, __byte_perm(s01, 0, 0x1010), x);
+          values16(code[h][0].z, code[h][0].w, __byte_perm(s01, 0, 0x3232), x + 8);
+          values16(code[h][1].x, code[h][1].y, __byte_perm(s23, 0, 0x1010), x + 16);
+          values16(code[h][1].z, code[h][1].w, __byte_perm(s23, 0, 0x3232), x + 24);
+        } else {   // P is 0 there, and 0 times what lies in an unused row need not be 0
+#pragma unroll
+          for (int j = 0; j < 32; ++j) x[j] = 0u;
+        }
+        load(h);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          st_shared_v4(to + vs * kVSlot + ((j ^ (r & 7)) << 4), make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]));
+        fence_proxy_async_smem();
+      } else {
+        load(h);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(AT(v_full) + 8 * vs);
+    }
+  }
+}
+
+// A lane of warp 1: O += P V, for every page and 256-column half of O a step per 16 tokens.
+__device__ void o_mma(const Fp4Params& p, Shared& sh, uint32_t smem, int part) {
+  SegmentWalker w;
+  w.init(p, part);
+  Segment s;
+  uint32_t T = 0, seg = 0, nresc = 0;
+  const uint32_t tmem = sh.tmem_base;
+  constexpr uint32_t idesc = idesc_f16_f32(128, 256, 1, 1);
+  const uint64_t v0 = smem_desc_sw128(smem + kOffV, kVChunk, 1024);
+  while (w.next(s)) {
+    if (seg > 0) wait(smem, AT(o_free), (seg - 1) & 1);
+#pragma unroll 1
+    for (int k = s.kb; k < s.ke; k += 2, ++T) {
+      const uint32_t slot = T & 1, pkt = smem + slot * 2 * kPktStride, full = AT(p_full) + 8 * slot;
+      const bool last = k + 2 >= s.ke;
+      const int ntok = tile_tokens(p, s, k);
+      mbar_arrive_expect_tx(full, 2 * kPktBytes);
+      wait<true>(smem, full, (T >> 1) & 1);
+      if (told_to_leave(smem)) goto out;
+      if (k != s.kb && (ld_shared_s32(pkt + kPktFlag) | ld_shared_s32(pkt + kPktStride + kPktFlag))) {   // scale O before adding
+        commit(AT(o_sync));
+        wait(smem, AT(o_sync), nresc & 1);
+        sh.cmd = 1;
+        sh.cmd_arg = static_cast<int>(slot);
+        mbar_arrive(AT(corr_go));
+        wait(smem, AT(corr_done), nresc & 1);
+        ++nresc;
+      }
+      tc_fence_after();
+      const uint64_t a = smem_desc_sw128(pkt, kPktStride, 1024);
+#pragma unroll 1
+      for (uint32_t ph = 0; ph < 4; ++ph) {   // half ph % 2 of page ph / 2, in slot ph (a tile of one page leaves two slots empty)
+        const int steps = min(4, (ntok - static_cast<int>(ph >> 1) * kPageTokens + 15) >> 4);
+        const uint64_t pa = a + (ph >> 1) * (kPageTokens * 128 >> 4), vb = v0 + ph * (kVSlot >> 4);
+        wait(smem, AT(v_full) + 8 * ph, T & 1);
+        tc_fence_after();
+#pragma unroll 1
+        for (int j = 0; j < steps; ++j) mma_ss(tmem + 256 * (ph & 1), pa + 128 * j, vb + 128 * j, idesc, k != s.kb || ph > 1 || j > 0);
+        commit(AT(v_empty) + 8 * ph);
+      }
+      if (last) {   // the output's factors, before the packet's slot can be reused
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+          st_shared_v4(smem + kOffInvL + i * 16, ld_shared_v4(pkt + (i >> 4) * kPktStride + kPktInvL + (i & 15) * 16));
+        commit(AT(o_full));
+        sh.cmd = 2;
+        mbar_arrive(AT(corr_go));
+      }
+      commit(AT(p_free) + 8 * slot);
+      asm volatile("st.volatile.shared.b32 [%0], %1;" :: "r"(AT(tiles)), "r"(T + 1) : "memory");
+    }
+    ++seg;
+  }
+  if (seg > 0) wait(smem, AT(o_free), (seg - 1) & 1);   // the last epilogue has taken its command
+out:
+  commit(AT(drain));   // behind everything issued
+  drain_bar(AT(drain), 0);
+  sh.cmd = 3;
+  mbar_arrive(AT(corr_go));
+  asm volatile("st.volatile.shared.b32 [%0], %1;" :: "r"(AT(tiles)), "r"(kDone) : "memory");
+}
+
+// A lane of warp 2: gives packet slots back to the S-CTA once the MMAs are done with them.
+__device__ void o_forward(const Fp4Params& p, uint32_t smem, int part, uint32_t peer) {
+  SegmentWalker w;
+  w.init(p, part);
+  Segment s;
+  uint32_t T = 0;
+  const uint32_t credit = map_to_rank(AT(credit), peer);
+  while (w.next(s))
+#pragma unroll 1
+    for (int t = tiles_of(s); t > 0; --t, ++T) {
+      wait(smem, AT(p_free) + 8 * (T & 1), (T >> 1) & 1);
+      if (told_to_leave(smem)) return;
+      mbar_arrive_remote(credit + (T & 1) * 8);
+    }
+}
+
+// A lane of warp 3: the pair's limit on waiting.  No tile's MMAs for kTimeoutNs (every role's progress is needed for one): the status
+// word gets MLA_ERR_TIMEOUT, and all CTAs of the cluster are told to leave.
+__device__ void o_watch(const Fp4Params& p, uint32_t smem, uint32_t cl) {
+  uint32_t seen = 0, since = timer_lo();
+  while (true) {
+    uint32_t tiles;
+    asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(tiles) : "r"(AT(tiles)) : "memory");
+    if (tiles == kDone || told_to_leave(smem)) return;
+    const uint32_t now = timer_lo();
+    if (tiles != seen) {
+      seen = tiles;
+      since = now;
+    } else if (now - since > kTimeoutNs) {
+      atomicCAS(p.status, 0, MLA_ERR_TIMEOUT);
+      for (uint32_t r = 0; r < cl; ++r) st_cluster_u32(map_to_rank(AT(abort), r), 1u);
+      return;
+    }
+    __nanosleep(500);
+  }
+}
+
+// Warps 4..11: rescale O's rows, or normalise and store a finished segment.  Warpgroup wg owns O's columns [256 wg, 256 wg + 256).
+// TMEM lane m is head (m / 64) N/2 + m % 64 of the block, where m % 64 < N/2.
+__device__ void o_epilogue(const Fp4Params& p, Shared& sh, uint32_t smem, int part, const Block& blk) {
+  const int t = threadIdx.x - 128, wg = t >> 7, r = t & 127, wq = r >> 5, lane = r & 31;
+  const uint32_t tmem_row = sh.tmem_base + (static_cast<uint32_t>(wq * 32) << 16) + wg * 256;
+  const int h0 = 32 * (wq & 1), n0 = (wq >> 1) * blk.half + h0;                  // the warp's first head
+  const int nrows = max(0, min(min(32, blk.half - h0), blk.valid - n0));         // its heads
+  SegmentWalker w;
+  w.init(p, part);
+  Segment s;
+  uint32_t ncmd = 0, seg = 0;
+  bool have = w.next(s);
+  while (true) {
+    warp_wait(smem, AT(corr_go), ncmd & 1);
+    if (warp_told_to_leave(smem)) break;
+    ++ncmd;
+    const int cmd = sh.cmd;
+    if (cmd == 3) break;
+    if (cmd == 1) {
+      const uint32_t pkt = smem + sh.cmd_arg * 2 * kPktStride + (r >> 6) * kPktStride;
+      // (a warpgroup that did not rebase sends no factors)
+      const float alpha = __float_as_uint(ld_shared_f32(pkt + kPktFlag)) ? ld_shared_f32(pkt + kPktAlpha + (r & 63) * 4) : 1.f;
+      tc_fence_after();
+      if (__any_sync(0xffffffffu, lane < nrows && alpha != 1.f)) {
+#pragma unroll 1
+        for (int c = 0; c < 256; c += 32) {
+          uint32_t v[32];
+          tmem_ld32(tmem_row + c, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * alpha);
+          tmem_st32(tmem_row + c, v);
+        }
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(AT(corr_done));
+      continue;
+    }
+    if (!have) break;
+    warp_wait(smem, AT(o_full), seg & 1);
+    tc_fence_after();
+    const float inv_l = ld_shared_f32(smem + kOffInvL + r * 4);
+    const int ns0 = __ldg(p.num_splits + s.b);
+    const bool final_out = __ldg(p.num_splits + s.b + 1) - ns0 == 1;
+    const bool slot_ok = final_out || split_slot_ok(p, ns0 + s.split);
+    // Through the warp's transpose buffer, so that a store instruction writes 64 bytes of 8 rows.  Buffer row x (64 B) holds
+    // 16-byte unit u at ((u ^ ((x >> 1) & 3)) * 16): the 8 rows that a quarter-warp stores (or the 2 it loads) touch 8
+    // different bank groups.
+    const int64_t head0 = static_cast<int64_t>(s.b) * p.rows + blk.rb * kRowsPerPair + n0;
+    __nv_bfloat16* const obase = p.out + head0 * kDimV + wg * 256;
+    float* const pbase = p.o_part + (static_cast<int64_t>(ns0 + s.split) * p.rows + blk.rb * kRowsPerPair + n0) * kDimV + wg * 256;
+    const uint32_t stg = smem + kOffEpi + ((wg << 2) | wq) * 2048;
+    const int tq = lane & 3;                // transposed: 16-byte quad tq of rows 8 j + (lane >> 2)
+    auto put = [&](int j, uint4 u) { st_shared_v4(stg + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), u); };
+    auto get = [&](int j) {
+      const int x = 8 * j + (lane >> 2);
+      return ld_shared_v4(stg + x * 64 + ((tq ^ ((x >> 1) & 3)) << 4));
+    };
+    auto f = [&](uint32_t v) { return __uint_as_float(v) * inv_l; };
+    auto emit = [&](int c, const uint32_t (&v)[32]) {
+      if (final_out) {   // 32 bf16 columns: 64 B a row
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          put(j, make_uint4(pack_bf16x2(f(v[8 * j]), f(v[8 * j + 1])), pack_bf16x2(f(v[8 * j + 2]), f(v[8 * j + 3])),
+                            pack_bf16x2(f(v[8 * j + 4]), f(v[8 * j + 5])), pack_bf16x2(f(v[8 * j + 6]), f(v[8 * j + 7]))));
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int x = 8 * j + (lane >> 2);
+          const uint4 u = get(j);
+          if (x < nrows) *reinterpret_cast<uint4*>(obase + static_cast<int64_t>(x) * kDimV + c + 8 * tq) = u;
+        }
+        __syncwarp();
+      } else {           // fp32 partials: two passes of 16 columns
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int e = 16 * h + 4 * j;
+            put(j, make_uint4(__float_as_uint(f(v[e])), __float_as_uint(f(v[e + 1])), __float_as_uint(f(v[e + 2])),
+                              __float_as_uint(f(v[e + 3]))));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int x = 8 * j + (lane >> 2);
+            const uint4 u = get(j);
+            if (x < nrows && slot_ok) *reinterpret_cast<uint4*>(pbase + static_cast<int64_t>(x) * kDimV + c + 16 * h + 4 * tq) = u;
+          }
+          __syncwarp();
+        }
+      }
+    };
+    // the TMEM load of the next 32 columns is in flight while the current ones are stored
+    uint32_t va[32], vb[32];
+    tmem_ld32(tmem_row, va);
+#pragma unroll 1
+    for (int c = 0; c < 256; c += 64) {
+      tmem_wait_ld();
+      tmem_ld32(tmem_row + c + 32, vb);
+      emit(c, va);
+      tmem_wait_ld();
+      if (c + 64 < 256) {
+        tmem_ld32(tmem_row + c + 64, va);
+      } else {   // O may be overwritten by the next segment
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(AT(o_free));
+      }
+      emit(c + 32, vb);
+    }
+    ++seg;
+    have = w.next(s);
+  }
+}
+
+template <bool Sparse>
+__global__ void __launch_bounds__(kThreads, 1) mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap q_map,
+                                                                        const __grid_constant__ Fp4Params p) {
+  extern __shared__ __align__(1024) uint8_t dyn_smem[];
+  const uint32_t smem = smem_u32(dyn_smem);
+  if (smem & 1023u) {   // the swizzled layouts need the base aligned (no static shared memory is declared)
+    if (threadIdx.x == 0) atomicCAS(p.status, 0, MLA_ERR_UNSUPPORTED);
+    return;             // every CTA of the grid takes this branch alike
+  }
+  Shared& sh = *reinterpret_cast<Shared*>(dyn_smem + kOffShared);
+  const int warp = threadIdx.x >> 5;
+  const uint32_t rank = cluster_ctarank();
+  const uint32_t cl = 2u * static_cast<uint32_t>(p.n_rb);
+  const int part = static_cast<int>(blockIdx.x / cl);
+  const Block blk(p, static_cast<int>(rank >> 1));
+  const bool is_s = (rank & 1u) == 0;
+  const uint32_t peer = rank ^ 1u;
+
+  if (threadIdx.x == 0) {
+    if (is_s) prefetch_tensormap(&q_map);
+    sh.abort = 0;
+    sh.tiles = 0;
+    sh.cmd = 0;
+    auto init = [](uint64_t& b, uint32_t n) { mbar_init(smem_u32(&b), n); };
+    for (int i = 0; i < 2; ++i) {
+      init(sh.raw_full[i], 1);
+      init(sh.raw_empty[i], 4);      // two warps of each converting warpgroup
+      init(sh.s_full[i], 1);
+      init(sh.s_empty[i], 8);
+      init(sh.p_ready[i], 1);
+      init(sh.st_free[i], 1);
+      init(sh.credit[i], 1);
+      init(sh.p_full[i], 1);
+      init(sh.p_free[i], 1);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      init(sh.k_full[i], i < 8 ? 4 : 8);   // a latent chunk comes from one converting warpgroup, the rope chunk from both
+      init(sh.k_empty[i], 1);
+    }
+    for (uint32_t i = 0; i < kRowSlots; ++i) {
+      init(sh.rows_full[i], 1);
+      init(sh.rows_empty[i], 8);
+    }
+    for (int i = 0; i < kVSlots; ++i) {
+      init(sh.v_full[i], 8);
+      init(sh.v_empty[i], 1);
+    }
+    init(sh.q_raw, 1);
+    init(sh.q_full, 8);
+    init(sh.q_empty, 1);
+    init(sh.o_full, 1);
+    init(sh.o_free, 8);
+    init(sh.o_sync, 1);
+    init(sh.corr_go, 1);
+    init(sh.corr_done, 8);
+    init(sh.drain, 1);
+    fence_mbar_init();
+  }
+  if (threadIdx.x < 128) sh.pos[threadIdx.x] = static_cast<uint16_t>(min(blk.rb * kRowsPerPair + static_cast<int>(threadIdx.x), p.rows - 1) / p.H);
+  __syncwarp();
+  if (warp == 0) tmem_alloc(smem_u32(&sh.tmem_base), 512);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();        // every barrier of the cluster is initialised before any remote use
+  tc_fence_after();
+  griddep_wait();        // the metadata, q and the cache are complete from here on
+
+  if (warp < 4) {
+    regs_down<kRegsMisc>();
+    const bool lane0 = (threadIdx.x & 31) == 0;
+    if (is_s) {
+      if (warp == 0) s_load<Sparse>(p, &q_map, smem, part, blk);
+      else if (lane0 && warp == 1) s_mma(p, sh, smem, part, blk);
+      else if (lane0) s_ship(p, smem, part, peer, warp - 2);
+    } else {
+      if (warp == 0) o_lookup<Sparse>(p, smem, part);
+      else if (lane0 && warp == 1) o_mma(p, sh, smem, part);
+      else if (lane0 && warp == 2) o_forward(p, smem, part, peer);
+      else if (lane0) o_watch(p, smem, cl);
+    }
+  } else if (warp < 12) {
+    regs_up<kRegsSoftmax>();
+    if (is_s) s_softmax<Sparse>(p, sh, smem, part, blk);
+    else o_epilogue(p, sh, smem, part, blk);
+  } else {
+    regs_down<kRegsConvert>();
+    if (is_s) s_convert(p, sh, smem, part, (warp - 12) >> 2);
+    else o_convert(p, smem);
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();        // no CTA leaves while a partner may still touch its shared memory
+  __syncwarp();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(sh.tmem_base, 512);
+  }
+}
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+
+// One-time set-up of the kernels on the current device.
+bool fp4_ready() {
+  static std::mutex mutex;
+  static bool ready[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  std::lock_guard<std::mutex> lock(mutex);
+  if (ready[dev]) return true;
+  if (!g_encode) {
+    cudaDriverEntryPointQueryResult found;
+    void* fn = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess || fn == nullptr)
+      return false;
+    g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }
+  for (auto kernel : {mla_decode_fp4_kernel<false>, mla_decode_fp4_kernel<true>}) {
+    cudaFuncAttributes a;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes)) != cudaSuccess ||
+        cudaFuncGetAttributes(&a, kernel) != cudaSuccess)
+      return false;
+    if (a.numRegs < 96) return false;   // the warpgroups' shares add up to 96 a thread
+  }
+  return ready[dev] = true;
+}
+
+mla_status_t decode_fp4_impl(const void* q, const uint8_t* kv_cache, float kv_scale, int64_t num_blocks,
+                             const int32_t* block_table, int max_blocks, const int32_t* seqlens, const int32_t* indices,
+                             int64_t index_stride, const int32_t* topk_lens, int B, int s_q, int H, float softmax_scale,
+                             int causal_s_q, const void* metadata, int num_sm_parts, void* workspace,
+                             size_t workspace_bytes, mla_bf16_t* out, float* lse, mla_stream_t stream) {
+  if (!q || !kv_cache || !block_table || !seqlens || !metadata || !out || !lse) return MLA_ERR_INVALID_ARG;
+  if (B < 1 || s_q < 1 || H < 1 || num_blocks < 1 || max_blocks < 1 || num_sm_parts < 1) return MLA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(kv_cache, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(block_table, 4) ||
+      !aligned(seqlens, 4) || !aligned(metadata, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (indices && (!topk_lens || index_stride < 1 || !aligned(indices, 4) || !aligned(topk_lens, 4))) return MLA_ERR_INVALID_ARG;
+  if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.f)) return MLA_ERR_INVALID_ARG;
+  if (!std::isfinite(kv_scale) || !(kv_scale > 0.f) || !fp4_scale_ok(kv_scale)) return MLA_ERR_INVALID_ARG;
+  const double scale_log2 = static_cast<double>(softmax_scale) * 1.4426950408889634074;
+  if (!std::isnormal(static_cast<float>(scale_log2 * kv_scale))) return MLA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(s_q) * H > kMaxPairsPerCluster * kRowsPerPair || B > kScheduleMaxB) return MLA_ERR_UNSUPPORTED;
+  if (num_blocks > ((int64_t(1) << 31) - kPageTokens) / kPageTokens) return MLA_ERR_UNSUPPORTED;
+  const int rows = s_q * H;
+  const size_t need = mla_decode_workspace_size(B, s_q, H, num_sm_parts);
+  if (workspace_bytes < need || !workspace) return MLA_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return MLA_ERR_INVALID_ARG;
+  Fp4Params p = {};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.kv = reinterpret_cast<const __nv_bfloat16*>(kv_cache);
+  p.num_blocks = num_blocks;
+  p.block_table = block_table;
+  p.max_blocks = max_blocks;
+  p.seqlens = seqlens;
+  p.lens = indices ? topk_lens : seqlens;
+  p.indices = indices;
+  p.idx_stride = indices ? index_stride : 0;
+  p.B = B;
+  p.s_q = s_q;
+  p.H = H;
+  p.rows = rows;
+  p.n_rb = (rows + kRowsPerPair - 1) / kRowsPerPair;
+  p.scale_log2 = static_cast<float>(scale_log2);
+  p.causal = causal_s_q ? 1 : 0;
+  p.kv_scale = kv_scale;
+  p.meta = static_cast<const int32_t*>(metadata);
+  p.num_splits = p.meta + kMetaInts * num_sm_parts;
+  p.num_parts = num_sm_parts;
+  const size_t slots = static_cast<size_t>(B) + static_cast<size_t>(num_sm_parts);   // partial outputs in the workspace
+  p.o_part = static_cast<float*>(workspace);
+  p.lse_part = p.o_part + slots * rows * kDimV;
+  p.out = reinterpret_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.status = device_status_word();
+  if (!p.status || !fp4_ready()) return MLA_ERR_CUDA;
+  p.withhold_first_load = take_withheld_load();
+  // q as [chunk 0..8][row][64 dims], a box 64 dims of a row block (as many rows as its MMA is wide)
+  p.q_box = rows >= kRowsPerPair ? kRowsPerPair : (rows + 15) & ~15;
+  CUtensorMap q_map;
+  const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(B) * rows, kDimQK / 64}, strides[2] = {kDimQK * 2, 128};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(p.q_box), 1}, steps[3] = {1, 1, 1};
+  if (g_encode(&q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, steps,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return MLA_ERR_CUDA;
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const unsigned cl = 2u * static_cast<unsigned>(p.n_rb);
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = pdl_config(dim3(static_cast<unsigned>(num_sm_parts) * cl), dim3(kThreads), kSmemBytes, cs, attr);
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cl;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.numAttrs = 2;
+  if ((indices ? cudaLaunchKernelEx(&cfg, mla_decode_fp4_kernel<true>, q_map, p)
+               : cudaLaunchKernelEx(&cfg, mla_decode_fp4_kernel<false>, q_map, p)) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  return launch_combine(p.o_part, p.lse_part, p.num_splits, B, rows, static_cast<int>(slots), p.out, lse, p.status, cs) ==
+                 cudaSuccess
+             ? MLA_OK
+             : MLA_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace mla
+
+using namespace mla;
+
+extern "C" {
+
+mla_status_t mla_decode_fp4(const mla_bf16_t* q, const uint8_t* kv_cache, float kv_scale, int64_t num_blocks,
+                            const int32_t* block_table, int max_blocks, const int32_t* seqlens, int B, int s_q, int H,
+                            float softmax_scale, int causal_s_q, const void* metadata, int num_sm_parts,
+                            void* workspace, size_t workspace_bytes, mla_bf16_t* out, float* lse, mla_stream_t stream) {
+  return decode_fp4_impl(q, kv_cache, kv_scale, num_blocks, block_table, max_blocks, seqlens, nullptr, 0, nullptr, B, s_q, H,
+                         softmax_scale, causal_s_q, metadata, num_sm_parts, workspace, workspace_bytes, out, lse, stream);
+}
+
+mla_status_t mla_decode_sparse_fp4(const mla_bf16_t* q, const uint8_t* kv_cache, float kv_scale, int64_t num_blocks,
+                                   const int32_t* block_table, int max_blocks, const int32_t* seqlens,
+                                   const int32_t* indices, int64_t index_stride, const int32_t* topk_lens, int B, int s_q,
+                                   int H, float softmax_scale, int causal_s_q, const void* metadata, int num_sm_parts,
+                                   void* workspace, size_t workspace_bytes, mla_bf16_t* out, float* lse,
+                                   mla_stream_t stream) {
+  if (!indices) return MLA_ERR_INVALID_ARG;
+  return decode_fp4_impl(q, kv_cache, kv_scale, num_blocks, block_table, max_blocks, seqlens, indices, index_stride,
+                         topk_lens, B, s_q, H, softmax_scale, causal_s_q, metadata, num_sm_parts, workspace,
+                         workspace_bytes, out, lse, stream);
+}
+
+}  // extern "C"
