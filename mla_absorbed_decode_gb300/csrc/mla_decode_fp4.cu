@@ -225,29 +225,40 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 __device__ __forceinline__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn, int b_mn) {
   return idesc_bf16_f32(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
 }
-// Four steps of an MMA, issued by this thread, then the arrival on `bar` when they and all before them are done.
+// A value that all lanes have, as one that the compiler knows to be uniform.  An MMA takes its operands from uniform registers: issued
+// by a whole warp that elects a lane, with operands known to be uniform, a step takes 50 clk; from one lane's own
+// registers 70 to 140 (the pipe takes 64 for 128 x 128 x 16).
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+// Four steps of an MMA (all lanes call), then the arrival on `bar` when they and all before them are done.
 // A from TMEM (8 columns a step), B 32 bytes a step.  accumulate: whether the first step adds to what is in D.
 __device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t bar) {
   asm volatile(
-      "{\n\t.reg .pred p, t;\n\t.reg .b64 b1, b2, b3;\n\t.reg .b32 a1, a2, a3;\n\t"
+      "{\n\t.reg .pred p, t, e;\n\t.reg .b64 b1, b2, b3;\n\t.reg .b32 a1, a2, a3;\n\t"
       "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
       "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
       "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t"
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}"
       :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(bar) : "memory");
 }
-// Both from shared memory, 16 tokens (2 KiB) of either a step; `steps` of them.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// Both from shared memory, 16 tokens (2 KiB) of either a step.
+__device__ __forceinline__ void mma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t bar) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
-}
-__device__ __forceinline__ void commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
+      "{\n\t.reg .pred p, t, e;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "add.s64 a1, %1, 128;\n\tadd.s64 a2, %1, 256;\n\tadd.s64 a3, %1, 384;\n\t"
+      "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}"
+      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(bar) : "memory");
 }
 // 16 latent values (two words of codes) as fp16 pairs; `scale` twice in a word.
 __device__ __forceinline__ void values16(uint32_t w0, uint32_t w1, uint32_t scale, uint32_t* v) {
@@ -514,37 +525,39 @@ __device__ void s_convert(const Fp4Params& p, Shared& sh, uint32_t smem, int par
   }
 }
 
-// A lane of warp 1: S^T = K Q^T, 36 steps of 16 dims a tile.  Its loop is what the tensor pipe waits for, so it is short: the latent
-// chunks have a slot each, the rope chunk the first slot once more, and q lies in their order.
+// Warp 1: S^T = K Q^T, 36 steps of 16 dims a tile.  Its loop is what the tensor pipe waits for, so it is short: the latent chunks have
+// a slot each, the rope chunk the first slot once more, and q lies in their order.
 __device__ void s_mma(const Fp4Params& p, Shared& sh, uint32_t smem, int part, const Block& blk) {
   SegmentWalker w;
   w.init(p, part);
   Segment s;
   uint32_t T = 0, seg = 0;
-  const uint32_t tmem = sh.tmem_base;
-  const uint32_t idesc = idesc_f16_f32(kTile, blk.N, 0, 0);
+  const uint32_t tmem = uniform(sh.tmem_base);
+  const uint32_t idesc = uniform(idesc_f16_f32(kTile, blk.N, 0, 0));
   const uint64_t q0 = smem_desc_sw128(smem, 16, 1024);
   while (w.next(s)) {
-    wait(smem, AT(q_full), seg & 1);
+    warp_wait(smem, AT(q_full), seg & 1);
 #pragma unroll 1
     for (int t = tiles_of(s); t > 0; --t, ++T) {
       const uint32_t sb = T & 1;
-      wait(smem, AT(s_empty) + 8 * sb, ((T >> 1) & 1) ^ 1);
-      if (told_to_leave(smem)) goto out;
+      warp_wait(smem, AT(s_empty) + 8 * sb, ((T >> 1) & 1) ^ 1);
+      if (warp_told_to_leave(smem)) goto out;
+      const uint32_t d = uniform(tmem + sb * kTile);
 #pragma unroll 1
       for (uint32_t it = 0; it < kItems; ++it) {
-        wait(smem, AT(k_full) + 8 * it, T & 1);
+        warp_wait(smem, AT(k_full) + 8 * it, T & 1);
         tc_fence_after();
-        mma4_ts(tmem + sb * kTile, tmem + kKCol + (it & 7) * 32, q0 + it * (kQChunk >> 4), idesc, it, AT(k_empty) + 8 * it);
+        mma4_ts(d, tmem + kKCol + (it & 7) * 32, q0 + it * (kQChunk >> 4), idesc, it, AT(k_empty) + 8 * it);
       }
-      commit(AT(s_full) + 8 * sb);
+      mma_commit_warp(AT(s_full) + 8 * sb);
     }
-    commit(AT(q_empty));
+    mma_commit_warp(AT(q_empty));
     ++seg;
   }
 out:
-  commit(AT(drain));   // behind everything issued
+  mma_commit_warp(AT(drain));   // behind everything issued
   drain_bar(AT(drain), 0);
+  __syncwarp();
 }
 
 // Rows of q of warpgroup w's heads, in place: bf16 as loaded to fp16, a warp a row, and their scores' factors.
@@ -951,66 +964,82 @@ __device__ void o_convert(const Fp4Params& p, uint32_t smem) {
   }
 }
 
-// A lane of warp 1: O += P V, for every page and 256-column half of O a step per 16 tokens.
+// Warp 1: O += P V, for every page and 256-column half of O a step per 16 tokens.
 __device__ void o_mma(const Fp4Params& p, Shared& sh, uint32_t smem, int part) {
+  const int lane = threadIdx.x & 31;
   SegmentWalker w;
   w.init(p, part);
   Segment s;
   uint32_t T = 0, seg = 0, nresc = 0;
-  const uint32_t tmem = sh.tmem_base;
+  const uint32_t tmem = uniform(sh.tmem_base);
   constexpr uint32_t idesc = idesc_f16_f32(128, 256, 1, 1);
   const uint64_t v0 = smem_desc_sw128(smem + kOffV, kVChunk, 1024);
   while (w.next(s)) {
-    if (seg > 0) wait(smem, AT(o_free), (seg - 1) & 1);
+    if (seg > 0) warp_wait(smem, AT(o_free), (seg - 1) & 1);
 #pragma unroll 1
     for (int k = s.kb; k < s.ke; k += 2, ++T) {
       const uint32_t slot = T & 1, pkt = smem + slot * 2 * kPktStride, full = AT(p_full) + 8 * slot;
       const bool last = k + 2 >= s.ke;
       const int ntok = tile_tokens(p, s, k);
-      mbar_arrive_expect_tx(full, 2 * kPktBytes);
-      wait<true>(smem, full, (T >> 1) & 1);
-      if (told_to_leave(smem)) goto out;
+      if (lane == 0) mbar_arrive_expect_tx(full, 2 * kPktBytes);
+      __syncwarp();
+      warp_wait<true>(smem, full, (T >> 1) & 1);
+      if (warp_told_to_leave(smem)) goto out;
+      if (last)   // the output's factors, before the packet's slot can be reused
+        st_shared_v4(smem + kOffInvL + lane * 16, ld_shared_v4(pkt + (lane >> 4) * kPktStride + kPktInvL + (lane & 15) * 16));
       if (k != s.kb && (ld_shared_s32(pkt + kPktFlag) | ld_shared_s32(pkt + kPktStride + kPktFlag))) {   // scale O before adding
-        commit(AT(o_sync));
-        wait(smem, AT(o_sync), nresc & 1);
-        sh.cmd = 1;
-        sh.cmd_arg = static_cast<int>(slot);
-        mbar_arrive(AT(corr_go));
-        wait(smem, AT(corr_done), nresc & 1);
+        mma_commit_warp(AT(o_sync));
+        warp_wait(smem, AT(o_sync), nresc & 1);
+        if (lane == 0) {
+          sh.cmd = 1;
+          sh.cmd_arg = static_cast<int>(slot);
+          mbar_arrive(AT(corr_go));
+        }
+        __syncwarp();
+        warp_wait(smem, AT(corr_done), nresc & 1);
         ++nresc;
       }
       tc_fence_after();
-      const uint64_t a = smem_desc_sw128(pkt, kPktStride, 1024);
+      const uint64_t a = smem_desc_sw128(uniform(pkt), kPktStride, 1024);
+      const uint32_t go_on = uniform(k != s.kb);
 #pragma unroll 1
       for (uint32_t ph = 0; ph < 4; ++ph) {   // half ph % 2 of page ph / 2, in slot ph (a tile of one page leaves two slots empty)
-        const int steps = min(4, (ntok - static_cast<int>(ph >> 1) * kPageTokens + 15) >> 4);
+        const int steps = (ntok - static_cast<int>(ph >> 1) * kPageTokens + 15) >> 4;
         const uint64_t pa = a + (ph >> 1) * (kPageTokens * 128 >> 4), vb = v0 + ph * (kVSlot >> 4);
-        wait(smem, AT(v_full) + 8 * ph, T & 1);
+        warp_wait(smem, AT(v_full) + 8 * ph, T & 1);
         tc_fence_after();
+        if (steps >= 4) {
+          mma4_ss(tmem + 256 * (ph & 1), pa, vb, idesc, ph > 1 ? 1u : go_on, AT(v_empty) + 8 * ph);
+        } else {
 #pragma unroll 1
-        for (int j = 0; j < steps; ++j) mma_ss(tmem + 256 * (ph & 1), pa + 128 * j, vb + 128 * j, idesc, k != s.kb || ph > 1 || j > 0);
-        commit(AT(v_empty) + 8 * ph);
+          for (int j = 0; j < steps; ++j)
+            mma_bf16_ss_warp(tmem + 256 * (ph & 1), pa + 128 * j, vb + 128 * j, idesc, j || ph > 1 ? 1u : go_on);
+          mma_commit_warp(AT(v_empty) + 8 * ph);
+        }
       }
-      if (last) {   // the output's factors, before the packet's slot can be reused
-#pragma unroll 1
-        for (int i = 0; i < 32; ++i)
-          st_shared_v4(smem + kOffInvL + i * 16, ld_shared_v4(pkt + (i >> 4) * kPktStride + kPktInvL + (i & 15) * 16));
-        commit(AT(o_full));
-        sh.cmd = 2;
-        mbar_arrive(AT(corr_go));
+      mma_commit_warp(AT(p_free) + 8 * slot);
+      if (last) mma_commit_warp(AT(o_full));
+      if (lane == 0) {
+        if (last) {
+          sh.cmd = 2;
+          mbar_arrive(AT(corr_go));
+        }
+        asm volatile("st.volatile.shared.b32 [%0], %1;" :: "r"(AT(tiles)), "r"(T + 1) : "memory");
       }
-      commit(AT(p_free) + 8 * slot);
-      asm volatile("st.volatile.shared.b32 [%0], %1;" :: "r"(AT(tiles)), "r"(T + 1) : "memory");
+      __syncwarp();
     }
     ++seg;
   }
-  if (seg > 0) wait(smem, AT(o_free), (seg - 1) & 1);   // the last epilogue has taken its command
+  if (seg > 0) warp_wait(smem, AT(o_free), (seg - 1) & 1);   // the last epilogue has taken its command
 out:
-  commit(AT(drain));   // behind everything issued
+  mma_commit_warp(AT(drain));   // behind everything issued
   drain_bar(AT(drain), 0);
-  sh.cmd = 3;
-  mbar_arrive(AT(corr_go));
-  asm volatile("st.volatile.shared.b32 [%0], %1;" :: "r"(AT(tiles)), "r"(kDone) : "memory");
+  __syncwarp();
+  if (lane == 0) {
+    sh.cmd = 3;
+    mbar_arrive(AT(corr_go));
+    asm volatile("st.volatile.shared.b32 [%0], %1;" :: "r"(AT(tiles)), "r"(kDone) : "memory");
+  }
 }
 
 // A lane of warp 2: gives packet slots back to the S-CTA once the MMAs are done with them.
@@ -1240,11 +1269,11 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_fp4_kernel(const __gri
     const bool lane0 = (threadIdx.x & 31) == 0;
     if (is_s) {
       if (warp == 0) s_load<Sparse>(p, &q_map, smem, part, blk);
-      else if (lane0 && warp == 1) s_mma(p, sh, smem, part, blk);
+      else if (warp == 1) s_mma(p, sh, smem, part, blk);
       else if (lane0) s_ship(p, smem, part, peer, warp - 2);
     } else {
       if (warp == 0) o_lookup<Sparse>(p, smem, part);
-      else if (lane0 && warp == 1) o_mma(p, sh, smem, part);
+      else if (warp == 1) o_mma(p, sh, smem, part);
       else if (lane0 && warp == 2) o_forward(p, smem, part, peer);
       else if (lane0) o_watch(p, smem, cl);
     }
