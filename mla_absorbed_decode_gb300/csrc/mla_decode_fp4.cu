@@ -56,8 +56,10 @@ constexpr uint32_t kQChunk = 128 * 128;       // 64 dims of the row block's q: u
 constexpr uint32_t kVChunk = 64 * 128;        // 64 dims of a page's values
 constexpr int kVSlots = 4;                    // half pages (64 tokens x 256 dims) of converted values
 constexpr uint32_t kVSlot = 4 * kVChunk;
-constexpr int kItems = 9;                     // chunks of converted keys a tile: 128 tokens x 64 dims, 32 TMEM columns, the first
-                                              // 8 (latent) in a slot each, the last (rope) in the first slot once more
+// converted keys of a tile, in the order of their MMAs: latent chunks (128 tokens x 64 dims, 32 TMEM columns) in pairs, one from
+// each converting warpgroup, and the rope chunk in the middle.  The pairs have slots of their own; the rope chunk goes where the
+// first pair's first chunk was, which is done with by then, as the rope chunk is when the next tile's first pair comes.
+constexpr int kItems = 5, kRopeItem = 2;
 // a packet: what one softmax warpgroup (half of the row block's heads) sends to the O-CTA for a tile
 constexpr uint32_t kPktAlpha = 128 * 128;     // after P^T (128 tokens x 64 heads): float[64], factors of a rebase
 constexpr uint32_t kPktInvL = kPktAlpha + 256;   // float[64], the output's factors (last tile of a segment)
@@ -95,7 +97,7 @@ struct Fp4Params : DecodeParams {
 struct Shared {
   // S-CTA
   uint64_t raw_full[2], raw_empty[2];         // a page of the tile has landed; is in the converters' registers
-  uint64_t k_full[kItems], k_empty[kItems];   // a chunk of keys is in TMEM; its MMAs are done (each once a tile)
+  uint64_t k_full[kItems], k_empty[kItems];   // an item of keys is in TMEM (eight warps); its MMAs are done
   uint64_t s_full[2], s_empty[2];
   uint64_t q_raw, q_full, q_empty;            // the segment's q has landed; is fp16 (a softmax warp each); is done with
   uint64_t p_ready[2], st_free[2];            // a warpgroup's packet is written; has been read by its copy
@@ -245,6 +247,27 @@ __device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}"
       :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(bar) : "memory");
 }
+// Eight steps: of the second four, B's chunk follows the first's.
+__device__ __forceinline__ void mma8_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred p, t, e;\n\t.reg .b64 b1, b2, b3, b4, b5, b6, b7;\n\t.reg .b32 a1, a2, a3, a4, a5, a6, a7;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
+      "add.s64 b4, %2, %6;\n\tadd.s64 b5, %2, %6 + 2;\n\tadd.s64 b6, %2, %6 + 4;\n\tadd.s64 b7, %2, %6 + 6;\n\t"
+      "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\tadd.s32 a4, %1, 32;\n\tadd.s32 a5, %1, 40;\n\t"
+      "add.s32 a6, %1, 48;\n\tadd.s32 a7, %1, 56;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a4], b4, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a5], b5, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a6], b6, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a7], b7, %3, t;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}"
+      :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(bar), "n"(kQChunk >> 4) : "memory");
+}
 // Both from shared memory, 16 tokens (2 KiB) of either a step.
 __device__ __forceinline__ void mma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t bar) {
   asm volatile(
@@ -392,6 +415,12 @@ struct Block {
 };
 
 // ------------------------------------------------------------------ S-CTA --
+// Where q's 64 dims `c` lie: the warpgroups' chunks (c < 4, and from 4 on) in turn, the rope dims between the second pair and the third.
+__device__ __forceinline__ int q_place(int c) {
+  const int k = c & 3, at = 2 * k + (c >> 2);
+  return c == 8 ? 4 : at < 4 ? at : at + 1;
+}
+
 // Warp 0: a segment's q, then the two pages of every tile.  Dense: a copy for four rows (as far as the request has tokens); lists: a
 // copy a row, whose addresses are looked up while the tile before is being loaded.
 template <bool Sparse>
@@ -411,7 +440,7 @@ __device__ void s_load(const Fp4Params& p, const CUtensorMap* q_map, uint32_t sm
       mbar_arrive_expect_tx(AT(q_raw), 9u * static_cast<uint32_t>(p.q_box) * 128u);
 #pragma unroll 1
       for (int c = 0; c < 9; ++c)
-        tma_load_3d(smem + (c < 4 ? 2 * c : c < 8 ? 2 * c - 7 : 8) * kQChunk, q_map, AT(q_raw), 0, s.b * p.rows + blk.rb * kRowsPerPair, c);
+        tma_load_3d(smem + q_place(c) * kQChunk, q_map, AT(q_raw), 0, s.b * p.rows + blk.rb * kRowsPerPair, c);
     }
     __syncwarp();
     ++seg;
@@ -464,8 +493,7 @@ out:
 }
 
 // Warps 12..19: a thread a token; warpgroup c takes latent dims [256 c, 256 c + 256) and half of the rope dims.  A tile's codes
-// are read into registers at once, which frees the page buffers for the next tile's loads; one copy of the code converts them, and
-// they move up.
+// are read into registers at once, which frees the page buffers for the next tile's loads.
 __device__ void s_convert(const Fp4Params& p, Shared& sh, uint32_t smem, int part, int c) {
   const int quad = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const uint32_t h = quad >> 1;                              // page of the tile
@@ -490,9 +518,9 @@ __device__ void s_convert(const Fp4Params& p, Shared& sh, uint32_t smem, int par
       rope[1] = ld_shared_v4(raw + kFp4Rope + 32 * c + 16);
       __syncwarp();
       if (lane == 0) mbar_arrive(AT(raw_empty) + 8 * h);
-#pragma unroll 1
+#pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint32_t slot = 2 * k + c;
+        const uint32_t item = k < 2 ? k : k + 1;
         uint32_t v[32];
         const uint32_t s01 = e4m3x2_to_f16x2<0>(sc.x), s23 = e4m3x2_to_f16x2<1>(sc.x);
         values16(code[0].x, code[0].y, __byte_perm(s01, 0, 0x1010), v);
@@ -502,31 +530,31 @@ __device__ void s_convert(const Fp4Params& p, Shared& sh, uint32_t smem, int par
 #pragma unroll
         for (int j = 0; j < 6; ++j) code[j] = code[j + 2];
         sc.x = sc.y, sc.y = sc.z, sc.z = sc.w;
-        warp_wait(smem, AT(k_empty) + 8 * (slot > 0 ? slot : 8), (T & 1) ^ 1);   // (the first slot had the rope chunk last)
+        warp_wait(smem, AT(k_empty) + 8 * (k > 0 ? item : kRopeItem), (T & 1) ^ 1);   // (the first pair's slots had the rope chunk last)
         tc_fence_after();
-        tmem_st32(tm + slot * 32, v);
+        tmem_st32(tm + (2 * k + c) * 32, v);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(AT(k_full) + 8 * slot);
-      }
-      uint32_t v[16];
-      const uint32_t x[8] = {rope[0].x, rope[0].y, rope[0].z, rope[0].w, rope[1].x, rope[1].y, rope[1].z, rope[1].w};
+        if (lane == 0) mbar_arrive(AT(k_full) + 8 * item);
+        if (k == 1) {
+          const uint32_t x[8] = {rope[0].x, rope[0].y, rope[0].z, rope[0].w, rope[1].x, rope[1].y, rope[1].z, rope[1].w};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[2 * j] = e4m3x2_to_f16x2<0>(x[j]), v[2 * j + 1] = e4m3x2_to_f16x2<1>(x[j]);
-      warp_wait(smem, AT(k_empty), T & 1);   // the tile's first chunk is done with
-      tc_fence_after();
-      tmem_st16(tm + 16 * c, v);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(AT(k_full) + 8 * 8);
+          for (int j = 0; j < 8; ++j) v[2 * j] = e4m3x2_to_f16x2<0>(x[j]), v[2 * j + 1] = e4m3x2_to_f16x2<1>(x[j]);
+          warp_wait(smem, AT(k_empty), T & 1);   // the tile's first pair is done with
+          tc_fence_after();
+          tmem_st16(tm + 16 * c, v);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(AT(k_full) + 8 * kRopeItem);
+        }
+      }
     }
   }
 }
 
-// Warp 1: S^T = K Q^T, 36 steps of 16 dims a tile.  Its loop is what the tensor pipe waits for, so it is short: the latent chunks have
-// a slot each, the rope chunk the first slot once more, and q lies in their order.
+// Warp 1: S^T = K Q^T, 36 steps of 16 dims a tile.  Its loop is what the tensor pipe waits for: few waits, and q lies in the keys' order.
 __device__ void s_mma(const Fp4Params& p, Shared& sh, uint32_t smem, int part, const Block& blk) {
   SegmentWalker w;
   w.init(p, part);
@@ -547,7 +575,13 @@ __device__ void s_mma(const Fp4Params& p, Shared& sh, uint32_t smem, int part, c
       for (uint32_t it = 0; it < kItems; ++it) {
         warp_wait(smem, AT(k_full) + 8 * it, T & 1);
         tc_fence_after();
-        mma4_ts(d, tmem + kKCol + (it & 7) * 32, q0 + it * (kQChunk >> 4), idesc, it, AT(k_empty) + 8 * it);
+        const uint32_t bar = AT(k_empty) + 8 * it;
+        if (it == kRopeItem) {
+          mma4_ts(d, tmem + kKCol, q0 + 4 * (kQChunk >> 4), idesc, 1u, bar);
+        } else {
+          const uint32_t pair = it > kRopeItem ? it - 1 : it, at = it > kRopeItem ? 2 * it - 1 : 2 * it;
+          mma8_ts(d, tmem + kKCol + pair * 64, q0 + at * (kQChunk >> 4), idesc, it, bar);
+        }
       }
       mma_commit_warp(AT(s_full) + 8 * sb);
     }
@@ -1233,7 +1267,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_fp4_kernel(const __gri
       init(sh.p_free[i], 1);
     }
     for (int i = 0; i < kItems; ++i) {
-      init(sh.k_full[i], i < 8 ? 4 : 8);   // a latent chunk comes from one converting warpgroup, the rope chunk from both
+      init(sh.k_full[i], 8);
       init(sh.k_empty[i], 1);
     }
     for (uint32_t i = 0; i < kRowSlots; ++i) {
