@@ -49,9 +49,7 @@ namespace {
 
 constexpr int kThreads = 640;   // warps 0..3: loads, MMAs, copies; 4..11: softmax or rescale and epilogue; 12..19: conversion
 constexpr int kTile = 128;      // tokens of a tile: two pages
-// a page in the S-CTA's shared memory: 16 bytes between groups of four rows, so that eight rows' units lie in different banks
-constexpr uint32_t kRawGroup = 4 * kFp4RowBytes + 16;
-constexpr uint32_t kRawPage = kPageTokens / 4 * kRawGroup;
+constexpr uint32_t kRawPage = kPageTokens * kFp4RowBytes;
 constexpr uint32_t kQChunk = 128 * 128;       // 64 dims of the row block's q: up to 128 rows of 128 bytes, swizzled
 constexpr uint32_t kVChunk = 64 * 128;        // 64 dims of a page's values
 constexpr int kVSlots = 4;                    // half pages (64 tokens x 256 dims) of converted values
@@ -421,8 +419,9 @@ __device__ __forceinline__ int q_place(int c) {
   return c == 8 ? 4 : at < 4 ? at : at + 1;
 }
 
-// Warp 0: a segment's q, then the two pages of every tile.  Dense: a copy for four rows (as far as the request has tokens); lists: a
-// copy a row, whose addresses are looked up while the tile before is being loaded.
+// Warp 0: a segment's q, then the two pages of every tile.  Dense: a copy a page (as far as the request has tokens; in 16 copies, with
+// gaps that would spare the converters bank conflicts, a page took a microsecond longer); lists: a copy a row, whose addresses are
+// looked up while the page before is being loaded.
 template <bool Sparse>
 __device__ void s_load(const Fp4Params& p, const CUtensorMap* q_map, uint32_t smem, int part, const Block& blk) {
   const int lane = threadIdx.x & 31;
@@ -475,9 +474,9 @@ __device__ void s_load(const Fp4Params& p, const CUtensorMap* q_map, uint32_t sm
       if constexpr (Sparse) {
 #pragma unroll
         for (int g = 0; g < 2; ++g)
-          if (row[g]) bulk_load(dst + (lane + 32 * g) * kFp4RowBytes + ((lane >> 2) + 8 * g) * 16, row[g], kFp4RowBytes, full);
-      } else if (4 * lane < n) {
-        bulk_load(dst + lane * kRawGroup, row[0] + lane * 4 * kFp4RowBytes, static_cast<uint32_t>(min(4, n - 4 * lane)) * kFp4RowBytes, full);
+          if (row[g]) bulk_load(dst + (lane + 32 * g) * kFp4RowBytes, row[g], kFp4RowBytes, full);
+      } else if (lane == 0 && n > 0) {
+        bulk_load(dst, row[0], static_cast<uint32_t>(n) * kFp4RowBytes, full);
       }
     }
   }
@@ -498,7 +497,7 @@ __device__ void s_convert(const Fp4Params& p, Shared& sh, uint32_t smem, int par
   const int quad = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const uint32_t h = quad >> 1;                              // page of the tile
   const int r = (quad & 1) * 32 + lane;                      // row of the page
-  const uint32_t raw = smem + kOffRaw + h * kRawPage + r * kFp4RowBytes + (r >> 2) * 16;
+  const uint32_t raw = smem + kOffRaw + h * kRawPage + r * kFp4RowBytes;
   const uint32_t tm = sh.tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + kKCol;
   SegmentWalker w;
   w.init(p, part);
