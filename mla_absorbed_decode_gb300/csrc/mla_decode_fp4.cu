@@ -60,10 +60,12 @@ constexpr uint32_t kVSlot = 4 * kVChunk;
 constexpr int kItems = 5, kRopeItem = 2;
 // a packet: what one softmax warpgroup (half of the row block's heads) sends to the O-CTA for a tile
 constexpr uint32_t kPktAlpha = 128 * 128;     // after P^T (128 tokens x 64 heads): float[64], factors of a rebase
-constexpr uint32_t kPktInvL = kPktAlpha + 256;   // float[64], the output's factors (last tile of a segment)
-constexpr uint32_t kPktFlag = kPktInvL + 256;    // whether alpha counts
+constexpr uint32_t kPktFlag = kPktAlpha + 256;   // whether alpha counts
 constexpr uint32_t kPktBytes = kPktFlag + 16;
 constexpr uint32_t kPktStride = 17 * 1024;
+// O-CTA: segments whose output factors may be there.  The S-CTA is at most three tiles ahead of the MMAs, which wait for the epilogue
+// of the segment before.
+constexpr uint32_t kInvSlots = 4;
 constexpr uint32_t kRowSlots = 8;             // O-CTA: pages whose rows have been looked up
 constexpr uint32_t kRowBytes = 4 * (kPageTokens + 1);
 constexpr uint32_t kKCol = 256;               // S-CTA's TMEM columns: S^T of two tiles at 0 and 128, the keys from 256
@@ -72,7 +74,7 @@ constexpr float kTop = kOffset + 8.f;         // an exponent past this rebases i
 constexpr uint32_t kTimeoutNs = 500u * 1000 * 1000;
 constexpr float kLn2 = 0.69314718055994530942f;
 // registers a thread: the three kinds of warpgroups share what the launch gets (640 x 96)
-constexpr int kRegsMisc = 48, kRegsSoftmax = 128, kRegsConvert = 88;
+constexpr int kRegsMisc = 48, kRegsSoftmax = 136, kRegsConvert = 80;
 static_assert(128 * kRegsMisc + 256 * kRegsSoftmax + 256 * kRegsConvert <= kThreads * 96, "more would wait forever");
 
 
@@ -81,8 +83,8 @@ constexpr uint32_t kOffSend = 9 * kQChunk;                   // S-CTA: q first, 
 constexpr uint32_t kOffRaw = kOffSend + 2 * kPktStride;      // S-CTA: the two pages of a tile as cached
 constexpr uint32_t kOffV = 4 * kPktStride;                   // O-CTA: the packets of two tiles first, then values
 constexpr uint32_t kOffEpi = kOffV + kVSlots * kVSlot;       // O-CTA: 2 KiB transpose buffer per epilogue warp
-constexpr uint32_t kOffInvL = kOffEpi + 8 * 2048;            // O-CTA: output factors of the segment [2][64]
-constexpr uint32_t kOffRows = kOffInvL + 512;                // O-CTA: the ring of looked-up rows
+constexpr uint32_t kOffInvL = kOffEpi + 8 * 2048;            // O-CTA: output factors of segments [kInvSlots][2][64]
+constexpr uint32_t kOffRows = kOffInvL + kInvSlots * 512;    // O-CTA: the ring of looked-up rows
 constexpr uint32_t kOffShared = kOffRaw + 2 * kRawPage;
 static_assert(kOffRows + kRowSlots * kRowBytes <= kOffShared, "O-CTA layout");
 
@@ -105,6 +107,7 @@ struct Shared {
   uint64_t rows_full[kRowSlots], rows_empty[kRowSlots];
   uint64_t v_full[kVSlots], v_empty[kVSlots];
   uint64_t o_full, o_free, o_sync, corr_go, corr_done;
+  uint64_t inv_full[kInvSlots];               // a segment's output factors have come (64 threads of either softmax warpgroup)
   uint64_t drain;                             // both
   uint32_t tmem_base;
   uint32_t abort;                             // nonzero: leave
@@ -176,8 +179,16 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
-// 64 (x8) or 16 (x2) columns of 16 TMEM lanes: lane l of the warp gets, in r[4 n + 2 h + e], row 8 h + l / 4, column
+// 32 (x4) or 16 (x2) columns of 16 TMEM lanes: lane l of the warp gets, in r[4 n + 2 h + e], row 8 h + l / 4, column
 // 8 n + 2 (l % 4) + e.
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, float (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+        "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+      : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, float (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
@@ -189,11 +200,9 @@ __device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, float (&r)[32]) {
         "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, float (&r)[8]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
-      : "r"(taddr));
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]) : "r"(taddr));
 }
 // Four 8 x 8 matrices of 16-bit elements: register m of lane l has row l / 4, columns 2 (l % 4) and the next, of matrix m, whose
 // row r goes to the 16 bytes at lane 8 m + r's address.
@@ -593,40 +602,56 @@ out:
   __syncwarp();
 }
 
-// Rows of q of warpgroup w's heads, in place: bf16 as loaded to fp16, a warp a row, and their scores' factors.
+// Rows of q of warpgroup w's heads, in place: bf16 as loaded to fp16, a warp a row (four at a time, or a segment's first MMA waits 9000
+// cycles for 128 of them), and their scores' factors.
 __device__ __forceinline__ void s_scale_q(const Fp4Params& p, Shared& sh, uint32_t smem, const Block& blk, int w, int wq, int lane) {
   const float unit = p.scale_log2 * p.kv_scale;
 #pragma unroll 1
-  for (int j = wq; j < blk.half; j += 4) {
-    const int n = w * blk.half + j;
-    const uint32_t at = smem + (lane >> 3) * kQChunk + n * 128 + (((lane & 7) ^ (n & 7)) << 4);   // 16 bytes of chunk lane / 8
-    uint4 v[3];
-    v[0] = ld_shared_v4(at);
-    v[1] = ld_shared_v4(at + 4 * kQChunk);
-    v[2] = lane < 8 ? ld_shared_v4(at + 8 * kQChunk) : make_uint4(0, 0, 0, 0);
-    float top = 0.f;
+  for (int j = wq; j < blk.half; j += 16) {
+    uint4 v[4][3];
+    float top[4];
+    auto at = [&](int g) {   // 16 bytes of chunk lane / 8
+      const int n = w * blk.half + min(j + 4 * g, blk.half - 1);
+      return smem + (lane >> 3) * kQChunk + n * 128 + (((lane & 7) ^ (n & 7)) << 4);
+    };
 #pragma unroll
-    for (int u = 0; u < 3; ++u) {
-      const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) top = max_nan(top, max_nan(fabsf(bf16_lo(x[e])), fabsf(bf16_hi(x[e]))));
+    for (int g = 0; g < 4; ++g) {
+      v[g][0] = ld_shared_v4(at(g));
+      v[g][1] = ld_shared_v4(at(g) + 4 * kQChunk);
+      v[g][2] = lane < 8 ? ld_shared_v4(at(g) + 8 * kQChunk) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const bool finite = top <= 3.4e38f;
-    const int e = finite ? max(static_cast<int>(__float_as_uint(top) >> 23), 41) : 141;   // at most a factor 2^100
-    // (a row with an infinity or a NaN becomes NaN; the factor is never 0, so that scores of -inf stay what they are)
-    const float sc = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
-    const float back = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+    for (int g = 0; g < 4; ++g) {
+      top[g] = 0.f;
 #pragma unroll
-    for (int u = 0; u < 3; ++u) {
-      const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-      uint32_t y[4];
+      for (int u = 0; u < 3; ++u) {
+        const uint32_t x[4] = {v[g][u].x, v[g][u].y, v[g][u].z, v[g][u].w};
 #pragma unroll
-      for (int q = 0; q < 4; ++q) y[q] = finite ? pack_f16x2(bf16_lo(x[q]) * sc, bf16_hi(x[q]) * sc) : 0x7E007E00u;
-      if (u < 2 || lane < 8) st_shared_v4(at + 4 * u * kQChunk, make_uint4(y[0], y[1], y[2], y[3]));
+        for (int e = 0; e < 4; ++e) top[g] = max_nan(top[g], max_nan(fabsf(bf16_lo(x[e])), fabsf(bf16_hi(x[e]))));
+      }
     }
-    if (lane == 0) sh.q_scale[n] = fmaxf(unit * back, 0x1p-126f);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) top[g] = max_nan(top[g], __shfl_xor_sync(0xffffffffu, top[g], o));
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      if (j + 4 * g >= blk.half) break;
+      const bool finite = top[g] <= 3.4e38f;
+      const int e = finite ? max(static_cast<int>(__float_as_uint(top[g]) >> 23), 41) : 141;   // at most a factor 2^100
+      // (a row with an infinity or a NaN becomes NaN; the factor is never 0, so that scores of -inf stay what they are)
+      const float sc = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
+      const float back = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+#pragma unroll
+      for (int u = 0; u < 3; ++u) {
+        const uint32_t x[4] = {v[g][u].x, v[g][u].y, v[g][u].z, v[g][u].w};
+        uint32_t y[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) y[q] = finite ? pack_f16x2(bf16_lo(x[q]) * sc, bf16_hi(x[q]) * sc) : 0x7E007E00u;
+        if (u < 2 || lane < 8) st_shared_v4(at(g) + 4 * u * kQChunk, make_uint4(y[0], y[1], y[2], y[3]));
+      }
+      if (lane == 0) sh.q_scale[w * blk.half + j + 4 * g] = fmaxf(unit * back, 0x1p-126f);
+    }
   }
   fence_proxy_async_smem();
   __syncwarp();
@@ -636,7 +661,7 @@ __device__ __forceinline__ void s_scale_q(const Fp4Params& p, Shared& sh, uint32
 // Warps 4..11: warpgroup w has heads [w N/2, (w + 1) N/2) of the block.  Thread l of a warp has four of a tile's tokens (rows l / 4
 // + 8 {0..3} of the warp's TMEM quadrant) and up to 16 heads (8 i + 2 (l % 4) + {0, 1}).
 template <bool Sparse>
-__device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int part, const Block& blk) {
+__device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int part, const Block& blk, uint32_t peer) {
   const int t = threadIdx.x & 127, w = (threadIdx.x - 128) >> 7, wq = t >> 5, lane = t & 31, tr = lane >> 2, tc = lane & 3;
   const uint32_t bar = 1 + w;                     // named barrier of the warpgroup
   const int units = blk.half >> 3;                // of 8 heads
@@ -665,109 +690,95 @@ __device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int par
       nm[i] = make_float2(-INFINITY, -INFINITY);
       l[i] = make_float2(0.f, 0.f);
     }
-    bool unset = true;   // some head has no reference yet
+    bool unset = true;   // some head of the warpgroup has no reference yet
 #pragma unroll 1
     for (int k = s.kb; k < s.ke; k += 2, ++T) {
       const uint32_t sb = T & 1;
       const int ntok = min(min(kTile, (s.ke - k) * kPageTokens), L - k * kPageTokens);
-      // a token is seen by a head whose limit lies above its key: its position; none past the tile's tokens
-      const bool masked = ntok < kTile || (p.causal && (Sparse || k * kPageTokens + kTile > L_seq - p.s_q + 1));
-      const int limit = p.causal ? L_seq - p.s_q + 1 : INT_MAX, of_pos = p.causal ? 0xffff : 0;
-      int key[4];
-      if (masked) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int tok = 32 * wq + 8 * j + tr, e = k * kPageTokens + tok;
-          key[j] = INT_MAX;
-          if (tok < ntok) {
-            key[j] = e;
-            if (Sparse) {   // (a bad entry is reported by the loads, and seen by nobody)
-              const int at = e < p.idx_stride ? __ldg(p.indices + static_cast<int64_t>(s.b) * p.idx_stride + e) : -1;
-              key[j] = at >= 0 && at < L_seq ? at : INT_MAX;
-            }
-          }
-        }
-      }
       wait(smem, AT(s_full) + 8 * sb, (T >> 1) & 1);
-      wait(smem, AT(st_free) + 8 * w, (T & 1) ^ 1);   // the last packet has been read
       __syncwarp();
       tc_fence_after();
+      // Scores that are not seen become -inf where they lie, so that the loop below need not know: lane by token, a few tiles only.
+      if (ntok < kTile || (p.causal && (Sparse || k * kPageTokens + kTile > L_seq - p.s_q + 1))) {
+        const int tok = 32 * wq + lane, e = k * kPageTokens + tok;
+        int key = tok < ntok ? e : INT_MAX;   // the token's position; a head sees those below its limit
+        if (Sparse && tok < ntok) {           // (a bad entry is reported by the loads, and seen by nobody)
+          const int at = e < p.idx_stride ? __ldg(p.indices + static_cast<int64_t>(s.b) * p.idx_stride + e) : -1;
+          key = at >= 0 && at < L_seq ? at : INT_MAX;
+        }
+#pragma unroll 1
+        for (int c = 0; c < blk.half; c += 8) {
+          uint32_t x[8];
+          tmem_ld8(tm + sb * kTile + c, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (key >= (p.causal ? L_seq - p.s_q + 1 + sh.pos[w * blk.half + c + j] : INT_MAX)) x[j] = 0xff800000u;
+          tmem_st8(tm + sb * kTile + c, x);
+        }
+        tmem_wait_st();
+      }
+      wait(smem, AT(st_free) + 8 * w, (T & 1) ^ 1);   // the last packet has been read
+      __syncwarp();
       float2 ls[8];
       bool rebased = false;
       while (true) {   // once, or twice where references have to move
+        if (!unset || rebased) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ls[i] = make_float2(0.f, 0.f);
+          for (int i = 0; i < 8; ++i) ls[i] = make_float2(0.f, 0.f);
 #pragma unroll 1
-        for (uint32_t hf = 0; hf < 2; ++hf) {
-          float x[32];   // [unit][token row 8 of 16][head 2]
-          tmem_ld_16x256(tm + sb * kTile + (hf << 20), x);
-          tmem_wait_ld();
-          if (masked) {
-            const int k0 = hf ? key[2] : key[0], k1 = hf ? key[3] : key[1];
+          for (uint32_t hf = 0; hf < 2; ++hf) {
+            float x[32];   // [unit][token row 8 of 16][head 2]
+            tmem_ld_16x256(tm + sb * kTile + (hf << 20), x);
+            tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint32_t pos = *reinterpret_cast<const uint32_t*>(&sh.pos[w * blk.half + 8 * i + 2 * tc]);   // (two heads')
-              const int l0 = limit + static_cast<int>(pos & of_pos), l1 = limit + static_cast<int>((pos >> 16) & of_pos);
-              if (k0 >= l0) x[4 * i] = -INFINITY;
-              if (k0 >= l1) x[4 * i + 1] = -INFINITY;
-              if (k1 >= l0) x[4 * i + 2] = -INFINITY;
-              if (k1 >= l1) x[4 * i + 3] = -INFINITY;
+            for (int ii = 0; ii < 4; ++ii) {
+              if (2 * ii >= units) break;
+              uint32_t pk[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {   // unit 2 ii + q / 2, token row q % 2
+                const int i = 2 * ii + (q >> 1);
+                float2 y = fma2(make_float2(x[8 * ii + 2 * q], x[8 * ii + 2 * q + 1]), sl[i], nm[i]);
+                y.x = fast_exp2(y.x);
+                y.y = fast_exp2(y.y);
+                ls[i] = add2(ls[i], y);
+                pk[q] = pack_f16x2(y.x, y.y);
+              }
+              stmatrix4(st + hf * (16 * 128) + (((2 * ii) ^ st_unit) << 4), pk[0], pk[1], pk[2], pk[3]);
             }
           }
+          if (t == 0) asm volatile("st.shared.u32 [%0], %1;" :: "r"(pkt + kPktFlag), "r"(rebased ? 1 : 0) : "memory");
+          fence_proxy_async_smem();
+          tc_fence_before();
+          // a P past 2^14 (no sum of four shows less): the tile again, with new references
+          float top = 0.f;
 #pragma unroll
-          for (int ii = 0; ii < 4; ++ii) {
-            if (2 * ii >= units) break;
-            uint32_t pk[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {   // unit 2 ii + q / 2, token row q % 2
-              const int i = 2 * ii + (q >> 1);
-              float2 y = fma2(make_float2(x[8 * ii + 2 * q], x[8 * ii + 2 * q + 1]), sl[i], nm[i]);
-              y.x = fast_exp2(y.x);
-              y.y = fast_exp2(y.y);
-              ls[i] = add2(ls[i], y);
-              pk[q] = pack_f16x2(y.x, y.y);
-            }
-            stmatrix4(st + hf * (16 * 128) + (((2 * ii) ^ st_unit) << 4), pk[0], pk[1], pk[2], pk[3]);
-          }
+          for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(ls[i].x, ls[i].y));
+          if (!named_bar_or(bar, 128, (!rebased && top > 0x1p14f) || told_to_leave(smem))) break;
         }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        if (rebased) break;
-        // a P past 2^14 (no sum of four shows less), or a head without a reference: the tile again, with new references
-        float top = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(ls[i].x, ls[i].y));
-        if (!named_bar_or(bar, 128, unset || top > 0x1p14f || told_to_leave(smem))) break;
         if (named_bar_or(bar, 128, told_to_leave(smem))) return;
         rebased = true;
 #pragma unroll 1
-        for (int ii = 0; 2 * ii < units; ++ii) {   // the heads' largest scores over the warp's tokens, two units at a time
-          float2 cm[2] = {make_float2(-INFINITY, -INFINITY), make_float2(-INFINITY, -INFINITY)};
-#pragma unroll 1
-          for (uint32_t hf = 0; hf < 2; ++hf) {
-            float x[8];
-            tmem_ld_16x256(tm + sb * kTile + 16 * ii + (hf << 20), x);
-            tmem_wait_ld();
-            const int k0 = !masked ? 0 : hf ? key[2] : key[0], k1 = !masked ? 0 : hf ? key[3] : key[1];
+        for (int i0 = 0; i0 < units; i0 += 4) {   // the heads' largest scores over the warp's tokens, four units at a time
+          float x[2][16];
+          float2 cm[4];
+          tmem_ld_16x256(tm + sb * kTile + 8 * i0, x[0]);
+          tmem_ld_16x256(tm + sb * kTile + 8 * i0 + (1u << 20), x[1]);
+          tmem_wait_ld();
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const uint32_t pos = *reinterpret_cast<const uint32_t*>(&sh.pos[w * blk.half + 16 * ii + 8 * u + 2 * tc]);
-              const int l0 = limit + static_cast<int>(pos & of_pos), l1 = limit + static_cast<int>((pos >> 16) & of_pos);
-              if (!masked || k0 < l0) cm[u].x = fmaxf(cm[u].x, x[4 * u]);
-              if (!masked || k0 < l1) cm[u].y = fmaxf(cm[u].y, x[4 * u + 1]);
-              if (!masked || k1 < l0) cm[u].x = fmaxf(cm[u].x, x[4 * u + 2]);
-              if (!masked || k1 < l1) cm[u].y = fmaxf(cm[u].y, x[4 * u + 3]);
-            }
-          }
+          for (int u = 0; u < 4; ++u)
+            cm[u] = make_float2(fmaxf(fmaxf(x[0][4 * u], x[0][4 * u + 2]), fmaxf(x[1][4 * u], x[1][4 * u + 2])),
+                                fmaxf(fmaxf(x[0][4 * u + 1], x[0][4 * u + 3]), fmaxf(x[1][4 * u + 1], x[1][4 * u + 3])));
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-#pragma unroll 1
-            for (int o = 4; o <= 16; o <<= 1) {
+          for (int o = 4; o <= 16; o <<= 1)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
               cm[u].x = fmaxf(cm[u].x, __shfl_xor_sync(0xffffffffu, cm[u].x, o));
               cm[u].y = fmaxf(cm[u].y, __shfl_xor_sync(0xffffffffu, cm[u].y, o));
             }
-            if (tr == 0) *reinterpret_cast<float2*>(&sh.part[w][wq][16 * ii + 8 * u + 2 * tc]) = cm[u];
-          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (tr == 0) *reinterpret_cast<float2*>(&sh.part[w][wq][8 * (i0 + u) + 2 * tc]) = cm[u];
         }
         named_bar_sync(bar, 128);
         if (t < blk.half) {   // a thread a head: its new reference, and what it makes of the sums so far
@@ -791,45 +802,36 @@ __device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int par
             l[i].y *= ld_shared_f32(pkt + kPktAlpha + (8 * i + 2 * tc) * 4 + 4);
             unset = unset || nm[i].x == -INFINITY || nm[i].y == -INFINITY;
           }
+        unset = named_bar_or(bar, 128, unset);   // (alike for the warpgroup)
       }
-      __syncwarp();
+      if (t == 0) mbar_arrive(AT(p_ready) + 8 * w);
       if (lane == 0) mbar_arrive(AT(s_empty) + 8 * sb);   // S^T has been read
 #pragma unroll
       for (int i = 0; i < 8; ++i) l[i] = add2(l[i], ls[i]);
-      const bool last = k + 2 >= s.ke;
-      if (t == 0) asm volatile("st.shared.u32 [%0], %1;" :: "r"(pkt + kPktFlag), "r"(rebased ? 1 : 0) : "memory");
-      if (rebased || last) {
-        if (last) {   // the heads' sums over the warpgroup's threads
+    }
+    // the heads' sums over the warpgroup's threads, and a thread a head: the output's factor to the partner, and the lse
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 8; ++i) {
 #pragma unroll
-            for (int o = 4; o <= 16; o <<= 1) {
-              l[i].x += __shfl_xor_sync(0xffffffffu, l[i].x, o);
-              l[i].y += __shfl_xor_sync(0xffffffffu, l[i].y, o);
-            }
-            if (tr == 0) *reinterpret_cast<float2*>(&sh.part[w][wq][8 * i + 2 * tc]) = l[i];
-          }
-          named_bar_sync(bar, 128);
-          if (t < blk.half) {
-            const float sum = (sh.part[w][0][t] + sh.part[w][1][t]) + (sh.part[w][2][t] + sh.part[w][3][t]);
-            asm volatile("st.shared.f32 [%0], %1;" :: "r"(pkt + kPktInvL + t * 4),
-                         "f"(sum == 0.f ? 0.f : __fdividef(p.kv_scale, sum)) : "memory");
-            const int n = w * blk.half + t, g = blk.rb * kRowsPerPair + n;
-            if (n < blk.valid) {
-              const float lse = sum == 0.f ? -INFINITY : (log2f(sum) - sh.ref[w][t]) * kLn2;
-              const int ns0 = __ldg(p.num_splits + s.b), nsplit = __ldg(p.num_splits + s.b + 1) - ns0;
-              if (nsplit == 1) p.lse[static_cast<int64_t>(s.b) * p.rows + g] = lse;
-              else if (split_slot_ok(p, ns0 + s.split))   // (NaN travels as +inf, whose weight the merge makes NaN)
-                p.lse_part[static_cast<int64_t>(ns0 + s.split) * p.rows + g] = isnan(lse) ? INFINITY : lse;
-            }
-          }
-        }
-        fence_proxy_async_smem();
-        named_bar_sync(bar, 128);
+      for (int o = 4; o <= 16; o <<= 1) {
+        l[i].x += __shfl_xor_sync(0xffffffffu, l[i].x, o);
+        l[i].y += __shfl_xor_sync(0xffffffffu, l[i].y, o);
       }
-      if (t == 0) {
-        fence_proxy_async_smem();
-        mbar_arrive(AT(p_ready) + 8 * w);
+      if (tr == 0) *reinterpret_cast<float2*>(&sh.part[w][wq][8 * i + 2 * tc]) = l[i];
+    }
+    named_bar_sync(bar, 128);
+    if (t < 64) {
+      const float sum = (sh.part[w][0][t] + sh.part[w][1][t]) + (sh.part[w][2][t] + sh.part[w][3][t]);
+      const uint32_t inv = map_to_rank(smem + kOffInvL + ((seg - 1) % kInvSlots) * 512 + w * 256 + t * 4, peer);
+      st_cluster_u32(inv, __float_as_uint(sum == 0.f ? 0.f : __fdividef(p.kv_scale, sum)));
+      mbar_arrive_remote(map_to_rank(AT(inv_full) + 8 * ((seg - 1) % kInvSlots), peer));
+      const int n = w * blk.half + t, g = blk.rb * kRowsPerPair + n;
+      if (t < blk.half && n < blk.valid) {
+        const float lse = sum == 0.f ? -INFINITY : (log2f(sum) - sh.ref[w][t]) * kLn2;
+        const int ns0 = __ldg(p.num_splits + s.b), nsplit = __ldg(p.num_splits + s.b + 1) - ns0;
+        if (nsplit == 1) p.lse[static_cast<int64_t>(s.b) * p.rows + g] = lse;
+        else if (split_slot_ok(p, ns0 + s.split))   // (NaN travels as +inf, whose weight the merge makes NaN)
+          p.lse_part[static_cast<int64_t>(ns0 + s.split) * p.rows + g] = isnan(lse) ? INFINITY : lse;
       }
     }
   }
@@ -847,8 +849,8 @@ __device__ void s_ship(const Fp4Params& p, uint32_t smem, int part, uint32_t pee
 #pragma unroll 1
     for (int t = tiles_of(s); t > 0; --t, ++T) {
       const uint32_t slot = T & 1;
-      wait(smem, AT(p_ready) + 8 * w, T & 1);
       wait<true>(smem, AT(credit) + 8 * slot, ((T >> 1) & 1) ^ 1);
+      wait(smem, AT(p_ready) + 8 * w, T & 1);
       if (told_to_leave(smem)) goto out;
       bulk_copy_to_cluster(dst + slot * 2 * kPktStride, src, kPktBytes, full + slot * 8);
       bulk_commit_group();
@@ -932,68 +934,74 @@ __device__ void o_lookup(const Fp4Params& p, uint32_t smem, int part) {
 }
 
 // Warps 12..19: the latent dims of every page, from global memory through registers into shared memory as fp16 (64 tokens by
-// 64 dims a chunk, 128-byte swizzle).  A thread has one row of a page (a quarter warp eight rows: eight different banks) and a chunk of
-// either half; as soon as it has converted one it loads the same one of the next page, which it needs a page later.
+// 64 dims a chunk, 128-byte swizzle).  A warpgroup has a half of the dims, a thread a row of the page (a quarter warp eight rows:
+// eight different banks) and two of the half's four chunks; as soon as it has converted one it loads the same one of the next page,
+// which it needs a page later.
 __device__ void o_convert(const Fp4Params& p, uint32_t smem) {
-  const int lane = threadIdx.x & 31, r = 8 * ((threadIdx.x >> 5) - 12) + (lane & 7), chunk = lane >> 3;   // of the 4 in a half
+  const int lane = threadIdx.x & 31, r = 16 * ((threadIdx.x >> 5) & 3) + (lane & 15), half = (threadIdx.x >> 7) - 3;
+  const uint32_t chunk = lane >> 4, dims = 128 * half + 32 * chunk, scales = kFp4Scales + 16 * half + 4 * chunk;   // and the chunk two on
   const uint8_t* const kv = reinterpret_cast<const uint8_t*>(p.kv);
-  const uint32_t to = smem + kOffV + chunk * kVChunk + r * 128;
+  const uint32_t to = smem + kOffV + half * kVSlot + chunk * kVChunk + r * 128;
   uint4 code[2][2];
   uint32_t scale[2];
-  int n = 0, n_next = 0;   // rows that count, of this page and the next (-1: none follows)
   const uint8_t* src = kv;
-  uint32_t i = 0;          // pages
-  auto load = [&](int h) {
+  int n = 0, n_next = 0;   // rows that count, of this page and the next (-1: none follows)
+  uint32_t i = 0;          // pages looked up
+  auto look_up = [&]() {   // where the next page's row is
+    const uint32_t slot = i % kRowSlots, at = smem + kOffRows + slot * kRowBytes;
+    warp_wait(smem, AT(rows_full) + 8 * slot, (i / kRowSlots) & 1);
+    n_next = ld_shared_s32(at + 256);
+    src = kv + static_cast<int64_t>(ld_shared_s32(at + r * 4)) * kFp4RowBytes;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(AT(rows_empty) + 8 * slot);
+    ++i;
+  };
+  auto load = [&](int c) {
     if (r < n_next) {
-      code[h][0] = __ldg(reinterpret_cast<const uint4*>(src + 128 * h + 32 * chunk));
-      code[h][1] = __ldg(reinterpret_cast<const uint4*>(src + 128 * h + 32 * chunk + 16));
-      scale[h] = __ldg(reinterpret_cast<const uint32_t*>(src + kFp4Scales + 16 * h + 4 * chunk));
+      code[c][0] = __ldg(reinterpret_cast<const uint4*>(src + dims + 64 * c));
+      code[c][1] = __ldg(reinterpret_cast<const uint4*>(src + dims + 64 * c + 16));
+      scale[c] = __ldg(reinterpret_cast<const uint32_t*>(src + scales + 8 * c));
     }
   };
+  look_up();
+  if (warp_told_to_leave(smem)) return;
+  load(0);
+  load(1);
+  n = n_next;
 #pragma unroll 1
-  for (bool first = true; n_next >= 0; first = false) {
-    n = n_next;
-    {   // where the next page's row is
-      const uint32_t slot = i % kRowSlots, at = smem + kOffRows + slot * kRowBytes;
-      warp_wait(smem, AT(rows_full) + 8 * slot, (i / kRowSlots) & 1);
-      if (warp_told_to_leave(smem)) return;
-      n_next = ld_shared_s32(at + 256);
-      src = kv + static_cast<int64_t>(ld_shared_s32(at + r * 4)) * kFp4RowBytes;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(AT(rows_empty) + 8 * slot);
-    }
-    ++i;
+  for (uint32_t page = 0; n >= 0; ++page) {
+    look_up();
+    if (warp_told_to_leave(smem)) return;
+    const uint32_t vs = 2 * (page & 1) + half;
+    warp_wait(smem, AT(v_empty) + 8 * vs, ((page >> 1) & 1) ^ 1);
+    if (n > 0) {   // (0: a tile's second page that is none)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (first) {
-        load(h);
-        continue;
-      }
-      const uint32_t vs = (2 * i + h) % kVSlots;   // page i - 2
-      warp_wait(smem, AT(v_empty) + 8 * vs, (i / (kVSlots / 2)) & 1);
-      if (n > 0) {   // (0: a tile's second page that is none)
+      for (int c = 0; c < 2; ++c) {
         uint32_t x[32];
         if (r < n) {
-          const uint32_t s01 = e4m3x2_to_f16x2<0>(scale[h]), s23 = e4m3x2_to_f16x2<1>(scale[h]);
-          values16(code[h][0].x, code[h][0].y, __byte_perm(s01, 0, 0x1010), x);
-          values16(code[h][0].z, code[h][0].w, __byte_perm(s01, 0, 0x3232), x + 8);
-          values16(code[h][1].x, code[h][1].y, __byte_perm(s23, 0, 0x1010), x + 16);
-          values16(code[h][1].z, code[h][1].w, __byte_perm(s23, 0, 0x3232), x + 24);
+          const uint32_t s01 = e4m3x2_to_f16x2<0>(scale[c]), s23 = e4m3x2_to_f16x2<1>(scale[c]);
+          values16(code[c][0].x, code[c][0].y, __byte_perm(s01, 0, 0x1010), x);
+          values16(code[c][0].z, code[c][0].w, __byte_perm(s01, 0, 0x3232), x + 8);
+          values16(code[c][1].x, code[c][1].y, __byte_perm(s23, 0, 0x1010), x + 16);
+          values16(code[c][1].z, code[c][1].w, __byte_perm(s23, 0, 0x3232), x + 24);
         } else {   // P is 0 there, and 0 times what lies in an unused row need not be 0
 #pragma unroll
           for (int j = 0; j < 32; ++j) x[j] = 0u;
         }
-        load(h);
+        load(c);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          st_shared_v4(to + vs * kVSlot + ((j ^ (r & 7)) << 4), make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]));
-        fence_proxy_async_smem();
-      } else {
-        load(h);
+          st_shared_v4(to + (page & 1) * (2 * kVSlot) + c * (2 * kVChunk) + ((j ^ (r & 7)) << 4),
+                       make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]));
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(AT(v_full) + 8 * vs);
+      fence_proxy_async_smem();
+    } else {
+      load(0);
+      load(1);
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(AT(v_full) + 8 * vs);
+    n = n_next;
   }
 }
 
@@ -1018,8 +1026,6 @@ __device__ void o_mma(const Fp4Params& p, Shared& sh, uint32_t smem, int part) {
       __syncwarp();
       warp_wait<true>(smem, full, (T >> 1) & 1);
       if (warp_told_to_leave(smem)) goto out;
-      if (last)   // the output's factors, before the packet's slot can be reused
-        st_shared_v4(smem + kOffInvL + lane * 16, ld_shared_v4(pkt + (lane >> 4) * kPktStride + kPktInvL + (lane & 15) * 16));
       if (k != s.kb && (ld_shared_s32(pkt + kPktFlag) | ld_shared_s32(pkt + kPktStride + kPktFlag))) {   // scale O before adding
         mma_commit_warp(AT(o_sync));
         warp_wait(smem, AT(o_sync), nresc & 1);
@@ -1155,7 +1161,8 @@ __device__ void o_epilogue(const Fp4Params& p, Shared& sh, uint32_t smem, int pa
     if (!have) break;
     warp_wait(smem, AT(o_full), seg & 1);
     tc_fence_after();
-    const float inv_l = ld_shared_f32(smem + kOffInvL + r * 4);
+    warp_wait<true>(smem, AT(inv_full) + 8 * (seg % kInvSlots), (seg / kInvSlots) & 1);
+    const float inv_l = ld_shared_f32(smem + kOffInvL + (seg % kInvSlots) * 512 + r * 4);
     const int ns0 = __ldg(p.num_splits + s.b);
     const bool final_out = __ldg(p.num_splits + s.b + 1) - ns0 == 1;
     const bool slot_ok = final_out || split_slot_ok(p, ns0 + s.split);
@@ -1274,7 +1281,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_fp4_kernel(const __gri
       init(sh.rows_empty[i], 8);
     }
     for (int i = 0; i < kVSlots; ++i) {
-      init(sh.v_full[i], 8);
+      init(sh.v_full[i], 4);
       init(sh.v_empty[i], 1);
     }
     init(sh.q_raw, 1);
@@ -1285,6 +1292,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_fp4_kernel(const __gri
     init(sh.o_sync, 1);
     init(sh.corr_go, 1);
     init(sh.corr_done, 8);
+    for (uint32_t i = 0; i < kInvSlots; ++i) init(sh.inv_full[i], 128);
     init(sh.drain, 1);
     fence_mbar_init();
   }
@@ -1312,7 +1320,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_fp4_kernel(const __gri
     }
   } else if (warp < 12) {
     regs_up<kRegsSoftmax>();
-    if (is_s) s_softmax<Sparse>(p, sh, smem, part, blk);
+    if (is_s) s_softmax<Sparse>(p, sh, smem, part, blk, peer);
     else o_epilogue(p, sh, smem, part, blk);
   } else {
     regs_down<kRegsConvert>();
