@@ -175,6 +175,7 @@ __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.al
 template <int R>
 __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(R)); }
 // `bytes` (a multiple of 16, both addresses 16-byte aligned) of global memory into shared memory.
+__device__ __forceinline__ void prefetch_line(const void* at) { asm volatile("prefetch.global.L2 [%0];" :: "l"(at) : "memory"); }
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
@@ -209,6 +210,12 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
 __device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};"
                :: "r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void st_shared_s32(uint32_t a, int v) { asm volatile("st.shared.b32 [%0], %1;" :: "r"(a), "r"(v) : "memory"); }
+__device__ __forceinline__ int ld_shared_s32(uint32_t a) {
+  int v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
 }
 // Two floats an instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -360,18 +367,22 @@ __device__ __forceinline__ int tile_tokens(const Fp4Params& p, const Segment& s,
 struct PageIter {
   SegmentWalker w;
   Segment s;
-  int k;
+  int k, L, L_seq;   // listed tokens and length of the segment's request
   bool valid;
   __device__ void init(const Fp4Params& p, int part) {
     w.init(p, part);
     valid = true;
     s.kb = s.ke = k = 0;
   }
-  __device__ bool next() {   // on to the next page, the first one to begin with; a segment's last tile has two in any case
+  __device__ bool next(const Fp4Params& p) {   // on to the next page, the first one to begin with; a segment's last tile has two in any case
     ++k;
     if (valid && (k > s.ke || (k == s.ke && ((k - s.kb) & 1) == 0))) {
       valid = w.next(s);
       k = s.kb;
+      if (valid) {
+        L = __ldg(p.lens + s.b);
+        L_seq = __ldg(p.seqlens + s.b);
+      }
     }
     return valid;
   }
@@ -393,23 +404,66 @@ __device__ __forceinline__ int page_of(const Fp4Params& p, int b, int k) {
   atomicCAS(p.status, 0, MLA_ERR_DEVICE_BOUNDS);
   return 0;
 }
-// Position of list entry e of request b; -1 where the row of indices ends before it (reported).
-__device__ __forceinline__ int entry_of(const Fp4Params& p, int b, int e) {
-  if (e < p.idx_stride) return __ldg(p.indices + static_cast<int64_t>(b) * p.idx_stride + e);
-  atomicCAS(p.status, 0, MLA_ERR_DEVICE_BOUNDS);
-  return -1;
-}
-// Its page; -1 where the position is none of the request's (reported).
-__device__ __forceinline__ int entry_page(const Fp4Params& p, int b, int t) {
-  if (t >= 0 && t < __ldg(p.seqlens + b)) return page_of(p, b, t / kPageTokens);
-  atomicCAS(p.status, 0, MLA_ERR_DEVICE_BOUNDS);
-  return -1;
-}
-// The cached row of a token; row 0 for a bad one, which is always there.
-__device__ __forceinline__ const uint8_t* row_at(const Fp4Params& p, int t, int blk) {
-  const int64_t row = blk < 0 ? 0 : static_cast<int64_t>(blk) * kPageTokens + t % kPageTokens;
-  return reinterpret_cast<const uint8_t*>(p.kv) + row * kFp4RowBytes;
-}
+
+// Finds the cached rows of every page of a part, a warp's work: a lane has rows `lane` and `lane + 32` of the page.  Its loads of a list
+// entry, of that token's table entry, and the use of the row are a page apart, so that none waits for the one before.
+constexpr int kListAhead = 4 * kPageTokens;   // list entries that are brought into L2 ahead of their loads
+template <bool Sparse>
+struct RowFinder {
+  int row[2], n;   // of the page at hand: cached rows (-1: the page ends before; -2: a list or table entry is out of range), their number
+  PageIter it;
+  struct { int t[2], n, b, k, L_seq; bool valid; } tok;     // the page whose list entries are being loaded
+  struct { int t[2], blk[2], n; bool valid; } tab;   // the one before it, whose table entries are
+  int lane;
+  __device__ void init(const Fp4Params& p, int part) {
+    lane = threadIdx.x & 31;
+    it.init(p, part);
+    tok.valid = tab.valid = false;
+    tok.n = tab.n = 0;
+  }
+  // On to the next page; false after the last.
+  __device__ bool next(const Fp4Params& p) {
+    bool have;
+    do {
+      have = tab.valid;
+      if (!have && !tok.valid && !it.valid) return false;
+      n = tab.n;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int r = lane + 32 * g;
+        row[g] = r >= n ? -1 : tab.blk[g] < 0 || tab.blk[g] >= p.num_blocks ? -2 : tab.blk[g] * kPageTokens + (Sparse ? tab.t[g] % kPageTokens : r);
+      }
+      tab.valid = tok.valid;
+      tab.n = tok.n;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int t = tok.t[g], k = Sparse ? t / kPageTokens : tok.k;
+        tab.t[g] = t;
+        tab.blk[g] = -1;
+        if (lane + 32 * g < tok.n && k < p.max_blocks && (!Sparse || (t >= 0 && t < tok.L_seq)))
+          tab.blk[g] = __ldg(p.block_table + static_cast<int64_t>(tok.b) * p.max_blocks + k);
+      }
+      tok.valid = it.next(p);
+      tok.n = 0;
+      if (tok.valid) {
+        tok.b = it.s.b;
+        tok.k = it.k;
+        tok.L_seq = it.L_seq;
+        if (it.k < it.s.ke) tok.n = min(kPageTokens, it.L - it.k * kPageTokens);
+        if constexpr (Sparse) {
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const int r = lane + 32 * g, e = it.k * kPageTokens + r;
+            const int32_t* const at = p.indices + static_cast<int64_t>(it.s.b) * p.idx_stride + e;
+            tok.t[g] = r < tok.n && e < p.idx_stride ? __ldg(at) : -1;
+            if (lane == 0 && e + kListAhead < min(static_cast<int64_t>(it.L), p.idx_stride)) prefetch_line(at + kListAhead);
+          }
+        }
+      }
+    } while (!have);
+    return true;
+  }
+};
 
 // A row block's heads: `valid` of its columns are query rows, the MMA has N (a multiple of 16), a softmax warpgroup N / 2.
 struct Block {
@@ -428,46 +482,23 @@ __device__ __forceinline__ int q_place(int c) {
   return c == 8 ? 4 : at < 4 ? at : at + 1;
 }
 
-// Warp 0: a segment's q, then the two pages of every tile.  Dense: a copy a page (as far as the request has tokens; in 16 copies, with
-// gaps that would spare the converters bank conflicts, a page took a microsecond longer); lists: a copy a row, whose addresses are
-// looked up while the page before is being loaded.
-template <bool Sparse>
-__device__ void s_load(const Fp4Params& p, const CUtensorMap* q_map, uint32_t smem, int part, const Block& blk) {
+// Warp 0, dense: the two pages of every tile, a copy a page as far as the request has tokens (in 16 copies, with
+// gaps that would spare the converters bank conflicts, a page took a microsecond longer).
+__device__ void s_load(const Fp4Params& p, uint32_t smem, int part) {
   const int lane = threadIdx.x & 31;
   SegmentWalker w;
   w.init(p, part);
   Segment s;
-  uint32_t i = 0, seg = 0;                      // pages (two a tile), segments
+  uint32_t i = 0;                               // pages (two a tile)
   bool withhold = p.withhold_first_load != 0;   // test hook: the first page never arrives
   while (w.next(s)) {
     const int L = __ldg(p.lens + s.b);
-    warp_wait(smem, AT(q_empty), (seg & 1) ^ 1);   // (the MMAs of the segment before are done)
-    if (warp_told_to_leave(smem)) break;
-    if (lane == 0) {   // 64 dims of the block's rows a box, in the order in which keys come (a warpgroup's chunks in turn); rows past
-                       // the request's are another's, or zeros past q's end
-      mbar_arrive_expect_tx(AT(q_raw), 9u * static_cast<uint32_t>(p.q_box) * 128u);
-#pragma unroll 1
-      for (int c = 0; c < 9; ++c)
-        tma_load_3d(smem + q_place(c) * kQChunk, q_map, AT(q_raw), 0, s.b * p.rows + blk.rb * kRowsPerPair, c);
-    }
-    __syncwarp();
-    ++seg;
     const int end = s.kb + 2 * tiles_of(s);
 #pragma unroll 1
     for (int k = s.kb; k < end; ++k, ++i) {
-      const uint32_t h = i & 1, full = AT(raw_full) + 8 * h, dst = smem + kOffRaw + h * kRawPage;
+      const uint32_t h = i & 1, full = AT(raw_full) + 8 * h;
       const int n = k < s.ke ? min(kPageTokens, L - k * kPageTokens) : 0;   // rows
-      const uint8_t* row[2] = {nullptr, nullptr};
-      if constexpr (Sparse) {
-        int t[2];
-#pragma unroll
-        for (int g = 0; g < 2; ++g) t[g] = lane + 32 * g < n ? entry_of(p, s.b, k * kPageTokens + lane + 32 * g) : 0;
-#pragma unroll
-        for (int g = 0; g < 2; ++g)
-          if (lane + 32 * g < n) row[g] = row_at(p, t[g], entry_page(p, s.b, t[g]));
-      } else if (n > 0) {
-        row[0] = row_at(p, 0, page_of(p, s.b, k));
-      }
+      const int64_t row = n > 0 ? static_cast<int64_t>(page_of(p, s.b, k)) * kPageTokens : 0;
       warp_wait(smem, AT(raw_empty) + 8 * h, ((i >> 1) & 1) ^ 1);
       if (warp_told_to_leave(smem)) goto out;
       if (withhold) {
@@ -476,94 +507,188 @@ __device__ void s_load(const Fp4Params& p, const CUtensorMap* q_map, uint32_t sm
         goto out;
       }
       if (lane == 0) {
-        if (n > 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(n) * kFp4RowBytes);
-        else mbar_arrive(full);
+        const uint32_t bytes = static_cast<uint32_t>(n) * kFp4RowBytes;
+        if (n > 0) {
+          mbar_arrive_expect_tx(full, bytes);
+          bulk_load(smem + kOffRaw + h * kRawPage, reinterpret_cast<const uint8_t*>(p.kv) + row * kFp4RowBytes, bytes, full);
+        } else {
+          mbar_arrive(full);
+        }
       }
       __syncwarp();
-      if constexpr (Sparse) {
-#pragma unroll
-        for (int g = 0; g < 2; ++g)
-          if (row[g]) bulk_load(dst + (lane + 32 * g) * kFp4RowBytes, row[g], kFp4RowBytes, full);
-      } else if (lane == 0 && n > 0) {
-        bulk_load(dst, row[0], static_cast<uint32_t>(n) * kFp4RowBytes, full);
-      }
     }
   }
 out:
-  // Loads still in flight land before the CTA may leave: the last two pages' and the last q's (the phases that their barriers were
-  // armed for last; a withheld page's never comes, which costs the limit).
+  // Loads still in flight land before the CTA may leave: the last two pages' (the phases that their barriers were armed for last; a
+  // withheld page's never comes, which costs the limit).
   if (lane == 0) {
-    if (seg > 0) drain_bar(AT(q_raw), (seg - 1) & 1);
     if (i > 0) drain_bar(AT(raw_full) + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1);
     if (i > 1) drain_bar(AT(raw_full) + 8 * (i & 1), ((i - 2) >> 1) & 1);
   }
   __syncwarp();
 }
 
-// Warps 12..19: a thread a token; warpgroup c takes latent dims [256 c, 256 c + 256) and half of the rope dims.  A tile's codes
-// are read into registers at once, which frees the page buffers for the next tile's loads.
+// Finds the cached rows of every page, kRowSlots pages ahead of the converters at most, and puts their numbers into a ring in shared
+// memory (64 of them, and how many count; -1 on either page of a tile after the last).  The O-CTA's warp 0 also has them brought into
+// L2; the S-CTA's, for lists, reports what is out of range (row 0 is read in its place, which is always there).
+template <bool Sparse, bool IsS>
+__device__ void find_rows(const Fp4Params& p, uint32_t smem, int part) {
+  const int lane = threadIdx.x & 31;
+  RowFinder<Sparse> rows;
+  rows.init(p, part);
+  int end = 0;
+#pragma unroll 1
+  for (uint32_t i = 0; end < 2; ++i) {
+    if (end > 0 || !rows.next(p)) ++end;
+    if (IsS && p.withhold_first_load != 0) break;   // test hook: the first page never arrives
+    const uint32_t slot = i % kRowSlots, at = smem + (IsS ? kOffRaw : kOffRows) + slot * kRowBytes;
+    warp_wait(smem, AT(rows_empty) + 8 * slot, ((i / kRowSlots) & 1) ^ 1);
+    if (warp_told_to_leave(smem)) break;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const int row = end > 0 ? -1 : rows.row[g];
+      if (IsS && row == -2) atomicCAS(p.status, 0, MLA_ERR_DEVICE_BOUNDS);
+      st_shared_s32(at + (lane + 32 * g) * 4, row >= 0 ? row : Sparse ? 0 : lane + 32 * g);
+      if (!IsS && row >= 0) {
+        const uint8_t* const src = reinterpret_cast<const uint8_t*>(p.kv) + static_cast<int64_t>(row) * kFp4RowBytes;
+        if constexpr (Sparse) {   // (a bulk prefetch a row took longer: 104 against 90 us for 64 x 2048 listed tokens)
+#pragma unroll
+          for (int c = 0; c < kFp4RowBytes + 127; c += 128) prefetch_line(src + min(c, kFp4RowBytes - 1));
+        } else if (lane == 0 && g == 0) {
+          prefetch_l2(src, rows.n * kFp4RowBytes);
+        }
+      }
+    }
+    if (lane == 0) st_shared_s32(at + 256, end > 0 ? -1 : rows.n);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(AT(rows_full) + 8 * slot);
+  }
+}
+
+// Warps 12..19: a thread a token; warpgroup c takes latent dims [256 c, 256 c + 256) and half of the rope dims.  Dense: a tile's
+// codes are read into registers at once, which frees the page buffers for the next tile's loads.  Lists: a thread loads its row from
+// global memory, every part as soon as the same part of the tile before has been converted (by copies of a row each into the page
+// buffers 64 x 2048 listed tokens took 122 us).
+template <bool Sparse>
 __device__ void s_convert(const Fp4Params& p, Shared& sh, uint32_t smem, int part, int c) {
   const int quad = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const uint32_t h = quad >> 1;                              // page of the tile
   const int r = (quad & 1) * 32 + lane;                      // row of the page
   const uint32_t raw = smem + kOffRaw + h * kRawPage + r * kFp4RowBytes;
   const uint32_t tm = sh.tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + kKCol;
+  constexpr int kRow = Sparse ? 16 : 32;
+  uint4 code[8], rope[2], sc;
+  // lists: the next tile's row, and loads of its parts
+  const uint8_t* src = nullptr;
+  int n = 0, n_next = 0;   // rows that count of the thread's page, and of the next tile's (-1: none follows)
+  uint32_t i = h;
+  auto look_up = [&]() {
+    const uint32_t slot = i % kRowSlots, at = smem + kOffRaw + slot * kRowBytes;
+    warp_wait(smem, AT(rows_full) + 8 * slot, (i / kRowSlots) & 1);
+    n_next = ld_shared_s32(at + 256);
+    src = reinterpret_cast<const uint8_t*>(p.kv) + static_cast<int64_t>(ld_shared_s32(at + r * 4)) * kFp4RowBytes;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(AT(rows_empty) + 8 * slot);
+    i += 2;
+  };
+  auto load = [&](uint4* to, uint32_t offset) { if (r < n_next) *to = __ldg(reinterpret_cast<const uint4*>(src + offset)); };
   SegmentWalker w;
-  w.init(p, part);
   Segment s;
-  uint32_t T = 0;
-  while (w.next(s)) {
+  int t = 0;               // dense: tiles of the segment to come
+  if constexpr (Sparse) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) code[k] = make_uint4(0, 0, 0, 0);
+    rope[0] = rope[1] = sc = make_uint4(0, 0, 0, 0);
+    look_up();
+    if (warp_told_to_leave(smem)) return;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) load(&code[k], 128 * c + 16 * k);
+    load(&sc, kFp4Scales + 16 * c);
+    load(&rope[0], kFp4Rope + 32 * c);
+    load(&rope[1], kFp4Rope + 32 * c + 16);
+    n = n_next;
+  } else {
+    w.init(p, part);
+  }
 #pragma unroll 1
-    for (int t = tiles_of(s); t > 0; --t, ++T) {
+  for (uint32_t T = 0; Sparse ? n >= 0 : true; ++T) {
+    if constexpr (Sparse) {
+      look_up();
+    } else {
+      if (t == 0) {
+        if (!w.next(s)) break;
+        t = tiles_of(s);
+      }
+      --t;
       warp_wait(smem, AT(raw_full) + 8 * h, T & 1);
-      if (warp_told_to_leave(smem)) return;
-      uint4 code[8];
-      uint4 rope[2];
+    }
+    if (warp_told_to_leave(smem)) return;
+    if constexpr (!Sparse) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) code[k] = ld_shared_v4(raw + 128 * c + 16 * k);
-      uint4 sc = ld_shared_v4(raw + kFp4Scales + 16 * c);
+      sc = ld_shared_v4(raw + kFp4Scales + 16 * c);
       rope[0] = ld_shared_v4(raw + kFp4Rope + 32 * c);
       rope[1] = ld_shared_v4(raw + kFp4Rope + 32 * c + 16);
       __syncwarp();
       if (lane == 0) mbar_arrive(AT(raw_empty) + 8 * h);
+    }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t item = k < 2 ? k : k + 1;
-        uint32_t v[32];
-        const uint32_t s01 = e4m3x2_to_f16x2<0>(sc.x), s23 = e4m3x2_to_f16x2<1>(sc.x);
-        values16(code[0].x, code[0].y, __byte_perm(s01, 0, 0x1010), v);
-        values16(code[0].z, code[0].w, __byte_perm(s01, 0, 0x3232), v + 8);
-        values16(code[1].x, code[1].y, __byte_perm(s23, 0, 0x1010), v + 16);
-        values16(code[1].z, code[1].w, __byte_perm(s23, 0, 0x3232), v + 24);
-#pragma unroll
-        for (int j = 0; j < 6; ++j) code[j] = code[j + 2];
-        sc.x = sc.y, sc.y = sc.z, sc.z = sc.w;
-        warp_wait(smem, AT(k_empty) + 8 * (k > 0 ? item : kRopeItem), (T & 1) ^ 1);   // (the first pair's slots had the rope chunk last)
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t item = k < 2 ? k : k + 1;
+      const uint32_t empty = AT(k_empty) + 8 * (k > 0 ? item : kRopeItem);   // (the first pair's slots had the rope chunk last)
+      const uint32_t sk = k == 0 ? sc.x : k == 1 ? sc.y : k == 2 ? sc.z : sc.w;
+      const uint32_t s01 = e4m3x2_to_f16x2<0>(sk), s23 = e4m3x2_to_f16x2<1>(sk);
+      uint32_t v[kRow];
+      if constexpr (Sparse) {   // (in two halves, or registers run out)
+        warp_wait(smem, empty, (T & 1) ^ 1);
+        tc_fence_after();
+        values16(code[2 * k].x, code[2 * k].y, __byte_perm(s01, 0, 0x1010), v);
+        values16(code[2 * k].z, code[2 * k].w, __byte_perm(s01, 0, 0x3232), v + 8);
+        load(&code[2 * k], 128 * c + 32 * k);
+        tmem_st16(tm + (2 * k + c) * 32, v);
+        values16(code[2 * k + 1].x, code[2 * k + 1].y, __byte_perm(s23, 0, 0x1010), v);
+        values16(code[2 * k + 1].z, code[2 * k + 1].w, __byte_perm(s23, 0, 0x3232), v + 8);
+        load(&code[2 * k + 1], 128 * c + 32 * k + 16);
+        if (k == 3) load(&sc, kFp4Scales + 16 * c);
+        tmem_st16(tm + (2 * k + c) * 32 + 16, v);
+      } else {
+        values16(code[2 * k].x, code[2 * k].y, __byte_perm(s01, 0, 0x1010), v);
+        values16(code[2 * k].z, code[2 * k].w, __byte_perm(s01, 0, 0x3232), v + 8);
+        values16(code[2 * k + 1].x, code[2 * k + 1].y, __byte_perm(s23, 0, 0x1010), v + 16);
+        values16(code[2 * k + 1].z, code[2 * k + 1].w, __byte_perm(s23, 0, 0x3232), v + 24);
+        warp_wait(smem, empty, (T & 1) ^ 1);
         tc_fence_after();
         tmem_st32(tm + (2 * k + c) * 32, v);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(AT(k_full) + 8 * item);
+      if (k == 1) {
+        const uint32_t x[8] = {rope[0].x, rope[0].y, rope[0].z, rope[0].w, rope[1].x, rope[1].y, rope[1].z, rope[1].w};
+        uint32_t u[16];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[2 * j] = e4m3x2_to_f16x2<0>(x[j]), u[2 * j + 1] = e4m3x2_to_f16x2<1>(x[j]);
+        if constexpr (Sparse) {
+          load(&rope[0], kFp4Rope + 32 * c);
+          load(&rope[1], kFp4Rope + 32 * c + 16);
+        }
+        warp_wait(smem, AT(k_empty), T & 1);   // the tile's first pair is done with
+        tc_fence_after();
+        tmem_st16(tm + 16 * c, u);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(AT(k_full) + 8 * item);
-        if (k == 1) {
-          const uint32_t x[8] = {rope[0].x, rope[0].y, rope[0].z, rope[0].w, rope[1].x, rope[1].y, rope[1].z, rope[1].w};
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[2 * j] = e4m3x2_to_f16x2<0>(x[j]), v[2 * j + 1] = e4m3x2_to_f16x2<1>(x[j]);
-          warp_wait(smem, AT(k_empty), T & 1);   // the tile's first pair is done with
-          tc_fence_after();
-          tmem_st16(tm + 16 * c, v);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(AT(k_full) + 8 * kRopeItem);
-        }
+        if (lane == 0) mbar_arrive(AT(k_full) + 8 * kRopeItem);
       }
     }
+    n = n_next;
   }
 }
 
-// Warp 1: S^T = K Q^T, 36 steps of 16 dims a tile.  Its loop is what the tensor pipe waits for: few waits, and q lies in the keys' order.
-__device__ void s_mma(const Fp4Params& p, Shared& sh, uint32_t smem, int part, const Block& blk) {
+// Warp 1: a segment's q; then S^T = K Q^T, 36 steps of 16 dims a tile.  Its loop is what the tensor pipe waits for: few waits, and q
+// lies in the keys' order.
+__device__ void s_mma(const Fp4Params& p, const CUtensorMap* q_map, Shared& sh, uint32_t smem, int part, const Block& blk) {
   SegmentWalker w;
   w.init(p, part);
   Segment s;
@@ -572,7 +697,16 @@ __device__ void s_mma(const Fp4Params& p, Shared& sh, uint32_t smem, int part, c
   const uint32_t idesc = uniform(idesc_f16_f32(kTile, blk.N, 0, 0));
   const uint64_t q0 = smem_desc_sw128(smem, 16, 1024);
   while (w.next(s)) {
-    warp_wait(smem, AT(q_full), seg & 1);
+    warp_wait(smem, AT(q_empty), (seg & 1) ^ 1);   // (the MMAs of the segment before are done)
+    if (warp_told_to_leave(smem)) goto out;
+    if ((threadIdx.x & 31) == 0) {   // 64 dims of the block's rows a box; rows past the request's are another's, or zeros past q's end
+      mbar_arrive_expect_tx(AT(q_raw), 9u * static_cast<uint32_t>(p.q_box) * 128u);
+#pragma unroll 1
+      for (int c = 0; c < 9; ++c) tma_load_3d(smem + q_place(c) * kQChunk, q_map, AT(q_raw), 0, s.b * p.rows + blk.rb * kRowsPerPair, c);
+    }
+    __syncwarp();
+    ++seg;
+    warp_wait(smem, AT(q_full), (seg - 1) & 1);
 #pragma unroll 1
     for (int t = tiles_of(s); t > 0; --t, ++T) {
       const uint32_t sb = T & 1;
@@ -594,11 +728,11 @@ __device__ void s_mma(const Fp4Params& p, Shared& sh, uint32_t smem, int part, c
       mma_commit_warp(AT(s_full) + 8 * sb);
     }
     mma_commit_warp(AT(q_empty));
-    ++seg;
   }
 out:
   mma_commit_warp(AT(drain));   // behind everything issued
   drain_bar(AT(drain), 0);
+  if (seg > 0) drain_bar(AT(q_raw), (seg - 1) & 1);   // and the last q lands before the CTA may leave
   __syncwarp();
 }
 
@@ -695,17 +829,19 @@ __device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int par
     for (int k = s.kb; k < s.ke; k += 2, ++T) {
       const uint32_t sb = T & 1;
       const int ntok = min(min(kTile, (s.ke - k) * kPageTokens), L - k * kPageTokens);
+      // Scores that are not seen become -inf where they lie, so that the loop below need not know: lane by token, a few tiles only
+      // (with lists and several query positions, all).
+      const bool masked = ntok < kTile || (p.causal && (Sparse || k * kPageTokens + kTile > L_seq - p.s_q + 1));
+      int key = INT_MAX;   // the token's position; a head sees those below its limit
+      if (masked) {
+        const int tok = 32 * wq + lane, e = k * kPageTokens + tok;
+        if (tok < ntok) key = !Sparse ? e : e < p.idx_stride ? __ldg(p.indices + static_cast<int64_t>(s.b) * p.idx_stride + e) : -1;
+      }
       wait(smem, AT(s_full) + 8 * sb, (T >> 1) & 1);
       __syncwarp();
       tc_fence_after();
-      // Scores that are not seen become -inf where they lie, so that the loop below need not know: lane by token, a few tiles only.
-      if (ntok < kTile || (p.causal && (Sparse || k * kPageTokens + kTile > L_seq - p.s_q + 1))) {
-        const int tok = 32 * wq + lane, e = k * kPageTokens + tok;
-        int key = tok < ntok ? e : INT_MAX;   // the token's position; a head sees those below its limit
-        if (Sparse && tok < ntok) {           // (a bad entry is reported by the loads, and seen by nobody)
-          const int at = e < p.idx_stride ? __ldg(p.indices + static_cast<int64_t>(s.b) * p.idx_stride + e) : -1;
-          key = at >= 0 && at < L_seq ? at : INT_MAX;
-        }
+      if (masked) {
+        if (Sparse && (key < 0 || key >= L_seq)) key = INT_MAX;   // (a bad entry is reported by the loads, and seen by nobody)
 #pragma unroll 1
         for (int c = 0; c < blk.half; c += 8) {
           uint32_t x[8];
@@ -863,76 +999,6 @@ out:
 }
 
 // ------------------------------------------------------------------ O-CTA --
-__device__ __forceinline__ void st_shared_s32(uint32_t a, int v) { asm volatile("st.shared.b32 [%0], %1;" :: "r"(a), "r"(v) : "memory"); }
-__device__ __forceinline__ int ld_shared_s32(uint32_t a) {
-  int v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
-
-// Warp 0: finds the cached rows of every page, kRowSlots pages ahead of the converters at most, puts their numbers into a ring in
-// shared memory (64 of them, and how many count; -1 after the last page) and has them brought into L2.  A lane has two rows; its
-// loads of a list entry, of that token's table entry, and the ring's store are a page apart, so that none waits for the one before.
-// (What is out of range is reported by the S-CTA's loads, and read as row 0 here.)
-template <bool Sparse>
-__device__ void o_lookup(const Fp4Params& p, uint32_t smem, int part) {
-  const int lane = threadIdx.x & 31;
-  struct Tokens { int t[2], n, b, k; bool valid; } tok;
-  struct Blocks { int t[2], blk[2], n; bool valid; } blk;
-  PageIter it;
-  it.init(p, part);
-  tok.valid = blk.valid = false;
-  tok.n = 0;
-  uint32_t i = 0;   // pages
-  while (true) {
-    const bool end = !blk.valid && !tok.valid && !it.valid;
-    if (blk.valid || end) {
-      const uint32_t slot = i % kRowSlots, at = smem + kOffRows + slot * kRowBytes;
-      warp_wait(smem, AT(rows_empty) + 8 * slot, ((i / kRowSlots) & 1) ^ 1);
-      if (warp_told_to_leave(smem)) return;
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const int r = lane + 32 * g, t = Sparse ? blk.t[g] : r;
-        const bool good = !end && r < blk.n && blk.blk[g] >= 0 && blk.blk[g] < p.num_blocks;
-        const int row = good ? blk.blk[g] * kPageTokens + t % kPageTokens : Sparse || end ? 0 : r;
-        st_shared_s32(at + r * 4, row);
-        if (Sparse && good) prefetch_l2(reinterpret_cast<const uint8_t*>(p.kv) + static_cast<int64_t>(row) * kFp4RowBytes, kFp4RowBytes);
-        if (!Sparse && good && lane == 0 && g == 0)
-          prefetch_l2(reinterpret_cast<const uint8_t*>(p.kv) + static_cast<int64_t>(row) * kFp4RowBytes, blk.n * kFp4RowBytes);
-      }
-      if (lane == 0) st_shared_s32(at + 256, end ? -1 : blk.n);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(AT(rows_full) + 8 * slot);
-      if (end) return;
-      ++i;
-    }
-    blk.valid = tok.valid;
-    blk.n = tok.n;
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const int t = tok.t[g], k = Sparse ? t / kPageTokens : tok.k;
-      blk.t[g] = t;
-      blk.blk[g] = -1;
-      if (lane + 32 * g < tok.n && k < p.max_blocks && (!Sparse || (t >= 0 && t < __ldg(p.seqlens + tok.b))))
-        blk.blk[g] = __ldg(p.block_table + static_cast<int64_t>(tok.b) * p.max_blocks + k);
-    }
-    tok.valid = it.next();
-    tok.n = 0;
-    if (tok.valid) {
-      tok.b = it.s.b;
-      tok.k = it.k;
-      if (it.k < it.s.ke) tok.n = min(kPageTokens, __ldg(p.lens + it.s.b) - it.k * kPageTokens);
-      if constexpr (Sparse) {
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const int r = lane + 32 * g, e = it.k * kPageTokens + r;
-          tok.t[g] = r < tok.n && e < p.idx_stride ? __ldg(p.indices + static_cast<int64_t>(it.s.b) * p.idx_stride + e) : -1;
-        }
-      }
-    }
-  }
-}
-
 // Warps 12..19: the latent dims of every page, from global memory through registers into shared memory as fp16 (64 tokens by
 // 64 dims a chunk, 128-byte swizzle).  A warpgroup has a half of the dims, a thread a row of the page (a quarter warp eight rows:
 // eight different banks) and two of the half's four chunks; as soon as it has converted one it loads the same one of the next page,
@@ -1278,7 +1344,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_fp4_kernel(const __gri
     }
     for (uint32_t i = 0; i < kRowSlots; ++i) {
       init(sh.rows_full[i], 1);
-      init(sh.rows_empty[i], 8);
+      init(sh.rows_empty[i], is_s ? 4 : 8);   // (the S-CTA's pages go to half of the converters)
     }
     for (int i = 0; i < kVSlots; ++i) {
       init(sh.v_full[i], 4);
@@ -1309,11 +1375,13 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_fp4_kernel(const __gri
     regs_down<kRegsMisc>();
     const bool lane0 = (threadIdx.x & 31) == 0;
     if (is_s) {
-      if (warp == 0) s_load<Sparse>(p, &q_map, smem, part, blk);
-      else if (warp == 1) s_mma(p, sh, smem, part, blk);
+      if (warp == 0) {
+        if constexpr (Sparse) find_rows<true, true>(p, smem, part);
+        else s_load(p, smem, part);
+      } else if (warp == 1) s_mma(p, &q_map, sh, smem, part, blk);
       else if (lane0) s_ship(p, smem, part, peer, warp - 2);
     } else {
-      if (warp == 0) o_lookup<Sparse>(p, smem, part);
+      if (warp == 0) find_rows<Sparse, false>(p, smem, part);
       else if (warp == 1) o_mma(p, sh, smem, part);
       else if (lane0 && warp == 2) o_forward(p, smem, part, peer);
       else if (lane0) o_watch(p, smem, cl);
@@ -1324,7 +1392,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_fp4_kernel(const __gri
     else o_epilogue(p, sh, smem, part, blk);
   } else {
     regs_down<kRegsConvert>();
-    if (is_s) s_convert(p, sh, smem, part, (warp - 12) >> 2);
+    if (is_s) s_convert<Sparse>(p, sh, smem, part, (warp - 12) >> 2);
     else o_convert(p, smem);
   }
 
@@ -1406,7 +1474,7 @@ mla_status_t decode_fp4_impl(const void* q, const uint8_t* kv_cache, float kv_sc
   p.rows = rows;
   p.n_rb = (rows + kRowsPerPair - 1) / kRowsPerPair;
   p.scale_log2 = static_cast<float>(scale_log2);
-  p.causal = causal_s_q ? 1 : 0;
+  p.causal = causal_s_q && s_q > 1 ? 1 : 0;   // (a single query position sees every token)
   p.kv_scale = kv_scale;
   p.meta = static_cast<const int32_t*>(metadata);
   p.num_splits = p.meta + kMetaInts * num_sm_parts;
