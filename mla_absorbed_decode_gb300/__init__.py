@@ -705,14 +705,17 @@ class DecodeStep:
 
     Buffers (q, out, lse, o, metadata, workspace) are allocated once here, with
     torch, and reused; `run` launches only library kernels.  With kv_scale given, the
-    cache passed to `run` / `capture` is an FP8 (E4M3) cache with that per-tensor scale.
+    cache passed to `run` / `capture` is an FP8 (E4M3) cache with that per-tensor scale,
+    or, with kv_bits=4 too, a 4-bit one (cache_append_fp4).
     """
 
     def __init__(self, B: int, s_q: int, H: int, seqlens: torch.Tensor, causal: bool, softmax_scale: float,
-                 parts: int | None = None, device="cuda", kv_scale: float | None = None):
+                 parts: int | None = None, device="cuda", kv_scale: float | None = None, kv_bits: int | None = None):
+        if kv_bits not in (None, 4, 8) or (kv_bits is not None and kv_scale is None):
+            raise ValueError("kv_bits (4 or 8) goes with a kv_scale")
         self.B, self.s_q, self.H = B, s_q, H
         self.causal, self.scale = causal, softmax_scale
-        self.kv_scale = kv_scale
+        self.kv_scale, self.kv_bits = kv_scale, 16 if kv_scale is None else kv_bits or 8
         self.parts = parts if parts is not None else num_sm_parts(s_q, H)
         dev = torch.device(device)
         self.q = torch.empty((B, s_q, H, 576), dtype=torch.bfloat16, device=dev)
@@ -779,22 +782,35 @@ class DecodeStep:
             decode(self.q, kv_cache, block_table, self.seqlens, self.scale, self.causal, self.metadata, self.parts,
                    workspace=self.workspace, out=self.out, lse=self.lse, stream=stream)
         else:
-            decode_fp8(self.q, kv_cache, self.kv_scale, block_table, self.seqlens, self.scale, self.causal,
-                       self.metadata, self.parts, workspace=self.workspace, out=self.out, lse=self.lse, stream=stream)
+            call = decode_fp4 if self.kv_bits == 4 else decode_fp8
+            call(self.q, kv_cache, self.kv_scale, block_table, self.seqlens, self.scale, self.causal,
+                 self.metadata, self.parts, workspace=self.workspace, out=self.out, lse=self.lse, stream=stream)
+
+    def _not_4_bit(self, what):
+        if self.kv_bits == 4:
+            raise ValueError(f"{what} does not read a 4-bit cache")
 
     def append(self, c, k_pe, kv_cache, block_table, positions=None, rope_theta: float = 10000.0, sections=(32,),
-               interleaved: bool = False, stream=None):
+               interleaved: bool = False, stream=None, norm_weight=None, norm_eps: float = 1e-6):
         """The step's new rows (c [B*s_q,512], k_pe [B*s_q,64]) into the cache as each request's last s_q
-        tokens (seqlens counts them), before `run`; k_pe rotated by positions where they are given.  In a batch
+        tokens (seqlens counts them), before `run`; k_pe rotated by positions where they are given, and c, for a
+        4-bit cache, RMS-normalised where norm_weight [512] is.  In a batch
         padded with empty requests cache_append, whose new_offsets give those no row, is the call to make."""
         rot = dict(positions=positions, sections=sections, rope_theta=rope_theta, interleaved=interleaved, stream=stream)
-        if self.kv_scale is None:
+        if norm_weight is not None and self.kv_bits != 4:
+            raise ValueError("the norm is part of the append to a 4-bit cache alone")
+        if self.kv_bits == 4:
+            cache_append_fp4(c, k_pe, kv_cache, self.kv_scale, block_table, self.seqlens, norm_weight=norm_weight,
+                             norm_eps=norm_eps, **rot)
+        elif self.kv_scale is None:
             cache_append(c, k_pe, kv_cache, block_table, self.seqlens, **rot)
         else:
             cache_append_fp8(c, k_pe, kv_cache, self.kv_scale, block_table, self.seqlens, **rot)
 
     def accumulate_weights(self, kv_cache, block_table, weights, stream=None):
-        """Adds the attention weight of the step that `run` / `replay` has just done to weights [B, slots]."""
+        """Adds the attention weight of the step that `run` / `replay` has just done to weights [B, slots]
+        (of a bf16 or FP8 cache)."""
+        self._not_4_bit("accumulate_weights")
         if self.kv_scale is None:
             attn_weights(self.q, self.lse, kv_cache, block_table, self.seqlens, self.scale, self.causal, weights,
                          stream=stream)
@@ -805,7 +821,8 @@ class DecodeStep:
     def evict(self, kv_cache, block_table, weights, budget: int, sink: int = 0, recent: int = 0, arrival=None,
               width: int | None = None, kept=None, weights_out=None, arrival_out=None, stream=None):
         """Evicts down to `budget` tokens a request (see evict()); seqlens is changed in place and the schedule
-        recomputed.  Returns (kept, weights_out, arrival_out)."""
+        recomputed.  Returns (kept, weights_out, arrival_out).  (Of a bf16 or FP8 cache.)"""
+        self._not_4_bit("evict")
         call = evict if self.kv_scale is None else evict_fp8
         outs = call(kv_cache, block_table, self.seqlens, weights, budget, sink=sink, recent=recent, arrival=arrival,
                     width=width, new_seqlens=self.seqlens, kept=kept, weights_out=weights_out, arrival_out=arrival_out,

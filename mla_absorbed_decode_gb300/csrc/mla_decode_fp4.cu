@@ -108,6 +108,7 @@ struct Shared {
   uint64_t v_full[kVSlots], v_empty[kVSlots];
   uint64_t o_full, o_free, o_sync, corr_go, corr_done;
   uint64_t inv_full[kInvSlots];               // a segment's output factors have come (64 threads of either softmax warpgroup)
+  uint64_t gone;                              // the S-CTA's converters have ended (a warp each, remote)
   uint64_t drain;                             // both
   uint32_t tmem_base;
   uint32_t abort;                             // nonzero: leave
@@ -540,7 +541,7 @@ __device__ void find_rows(const Fp4Params& p, uint32_t smem, int part) {
 #pragma unroll 1
   for (uint32_t i = 0; end < 2; ++i) {
     if (end > 0 || !rows.next(p)) ++end;
-    if (IsS && p.withhold_first_load != 0) break;   // test hook: the first page never arrives
+    if (IsS && end == 0 && p.withhold_first_load != 0) break;   // test hook: the first page never arrives
     const uint32_t slot = i % kRowSlots, at = smem + (IsS ? kOffRaw : kOffRows) + slot * kRowBytes;
     warp_wait(smem, AT(rows_empty) + 8 * slot, ((i / kRowSlots) & 1) ^ 1);
     if (warp_told_to_leave(smem)) break;
@@ -1163,14 +1164,15 @@ __device__ void o_forward(const Fp4Params& p, uint32_t smem, int part, uint32_t 
     }
 }
 
-// A lane of warp 3: the pair's limit on waiting.  No tile's MMAs for kTimeoutNs (every role's progress is needed for one): the status
-// word gets MLA_ERR_TIMEOUT, and all CTAs of the cluster are told to leave.
+// A lane of warp 3: the pair's limit on waiting.  No tile's MMAs for kTimeoutNs (every role's progress is needed for one), or the S-CTA's
+// converters, which alone may wait once all tiles are done, still there so long after the last: the status word gets
+// MLA_ERR_TIMEOUT, and all CTAs of the cluster are told to leave.
 __device__ void o_watch(const Fp4Params& p, uint32_t smem, uint32_t cl) {
   uint32_t seen = 0, since = timer_lo();
   while (true) {
     uint32_t tiles;
     asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(tiles) : "r"(AT(tiles)) : "memory");
-    if (tiles == kDone || told_to_leave(smem)) return;
+    if ((tiles == kDone && mbar_test(AT(gone), 0)) || told_to_leave(smem)) return;
     const uint32_t now = timer_lo();
     if (tiles != seen) {
       seen = tiles;
@@ -1359,6 +1361,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_fp4_kernel(const __gri
     init(sh.corr_go, 1);
     init(sh.corr_done, 8);
     for (uint32_t i = 0; i < kInvSlots; ++i) init(sh.inv_full[i], 128);
+    init(sh.gone, 8);
     init(sh.drain, 1);
     fence_mbar_init();
   }
@@ -1392,8 +1395,13 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_fp4_kernel(const __gri
     else o_epilogue(p, sh, smem, part, blk);
   } else {
     regs_down<kRegsConvert>();
-    if (is_s) s_convert<Sparse>(p, sh, smem, part, (warp - 12) >> 2);
-    else o_convert(p, smem);
+    if (is_s) {
+      s_convert<Sparse>(p, sh, smem, part, (warp - 12) >> 2);
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive_remote(map_to_rank(AT(gone), peer));
+    } else {
+      o_convert(p, smem);
+    }
   }
 
   __syncwarp();
