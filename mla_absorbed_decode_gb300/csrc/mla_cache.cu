@@ -42,6 +42,57 @@ __device__ __forceinline__ float2 rope_turn(const RopeTable& t, float hi, float 
   return make_float2(cs, sn);
 }
 
+// A value as the sum of two floats.
+struct Float2Sum {
+  float hi, lo;
+};
+// v / d, d > 0, to 24 bits with the last bit set where bits are lost (toward zero): a later rounding to fewer bits then falls as that
+// of the quotient itself would.
+__device__ __forceinline__ float quotient_for_rounding(Float2Sum v, float d) {
+  const float q = __fdiv_rn(v.hi, d), rest = fmaf(-q, d, v.hi) + v.lo;
+  if (!(rest != 0.f) || q == 0.f || !(fabsf(q) <= 3.4e38f)) return q;
+  return __uint_as_float((__float_as_uint(q) - ((rest < 0.f) == (q > 0.f) ? 1u : 0u)) | 1u);
+}
+// x0 a + x1 b, the factors sums of two floats.
+__device__ __forceinline__ Float2Sum dot2(float x0, Float2Sum a, float x1, Float2Sum b) {
+  const float p = __fmul_rn(x0, a.hi), q = __fmul_rn(x1, b.hi), s = __fadd_rn(p, q), t = __fsub_rn(s, p);
+  const float lost = __fadd_rn(__fsub_rn(p, __fsub_rn(s, t)), __fsub_rn(q, t));   // of the sum
+  const float lo = lost + (fmaf(x0, a.hi, -p) + fmaf(x0, a.lo, fmaf(x1, b.hi, -q) + x1 * b.lo));
+  const float hi = __fadd_rn(s, lo);
+  return {hi, __fsub_rn(lo, __fsub_rn(hi, s))};
+}
+// The pair (x0, x1) turned by the angle pos * (hi + lo), for codes: a value is off by about 2^-26 of the pair's norm (positions
+// below 2^17; 2^-19 up to 2^24), where rope_turn's hardware sine, off by 2^-21, would move many times as many codes that lie
+// halfway.  The angle less k quarter turns (pi / 2 in three floats, products with their rounding errors) is a pair of floats in
+// [-pi / 4, pi / 4], its sine and cosine are Taylor polynomials whose leading terms are added up exactly.
+__device__ __forceinline__ void rope_turned(float hi, float lo, int pos, float x0, float x1, Float2Sum (&y)[2]) {
+  constexpr float kQuarter1 = 0x1.921fb6p+0f, kQuarter2 = -0x1.777a5cp-25f, kQuarter3 = -0x1.ee59dap-50f;
+  const float fp = static_cast<float>(pos);
+  const float a = __fmul_rn(fp, hi), b = fmaf(fp, lo, fmaf(fp, hi, -a));
+  const float k = rintf(__fmul_rn(a, 0.636619772f));
+  const float p1 = __fmul_rn(k, kQuarter1), p2 = __fmul_rn(k, kQuarter2);
+  const float t = __fsub_rn(a, p1), u = __fsub_rn(t, p2), v = __fsub_rn(u, t);
+  const float e = __fadd_rn(__fsub_rn(t, __fsub_rn(u, v)), __fsub_rn(-p2, v));   // (t - p2) - u
+  const float l = e + ((b - fmaf(k, kQuarter1, -p1)) - fmaf(k, kQuarter3, fmaf(k, kQuarter2, -p2)));
+  const float r = __fadd_rn(u, l), rl = __fsub_rn(l, __fsub_rn(r, u));
+  const float z = __fmul_rn(r, r), zl = fmaf(r, r, -z) + 2.f * r * rl;
+  const float s1 = r * z * fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, 1.f / 6227020800.f, -1.f / 39916800.f), 1.f / 362880.f), -1.f / 5040.f),
+                                        1.f / 120.f), -1.f / 6.f);
+  const float sh = __fadd_rn(r, s1), sl = __fadd_rn(__fsub_rn(r, sh), s1) + fmaf(-0.5f * z, rl, rl);
+  const float h = 0.5f * z, c0 = __fsub_rn(1.f, h);
+  const float c1 = fmaf(z * z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, 1.f / 479001600.f, -1.f / 3628800.f), 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f),
+                        -0.5f * zl);
+  const float ch = __fadd_rn(c0, c1);
+  const float cl = __fadd_rn(__fsub_rn(c0, ch), c1) + __fsub_rn(__fsub_rn(1.f, c0), h);
+  const int quarter = static_cast<int>(k);
+  const bool odd = quarter & 1;
+  Float2Sum sn = odd ? Float2Sum{ch, cl} : Float2Sum{sh, sl}, cs = odd ? Float2Sum{sh, sl} : Float2Sum{ch, cl};
+  if (quarter & 2) sn = {-sn.hi, -sn.lo};
+  if ((quarter + 1) & 2) cs = {-cs.hi, -cs.lo};
+  y[0] = dot2(x0, cs, -x1, sn);
+  y[1] = dot2(x0, sn, x1, cs);
+}
+
 // ------------------------------------------------------------------- rope --
 struct RopeParams {
   const __nv_bfloat16* x;
@@ -246,12 +297,8 @@ __global__ void __launch_bounds__(128) mla_append_fp4_kernel(const __grid_consta
   }
   const int64_t row = append_target(p, r, lane);
   if (row < 0) return;
-  float x0 = bf16_lo(pe), x1 = bf16_hi(pe);
-  if (p.positions != nullptr) {
-    const float2 turn = rope_turn(p.table, s_hi[lane], s_lo[lane], pos);
-    const float y0 = fmaf(x0, turn.x, -x1 * turn.y), y1 = fmaf(x0, turn.y, x1 * turn.x);
-    x0 = y0, x1 = y1;
-  }
+  Float2Sum rope[2] = {{bf16_lo(pe), 0.f}, {bf16_hi(pe), 0.f}};
+  if (p.positions != nullptr) rope_turned(s_hi[lane], s_lo[lane], pos, rope[0].hi, rope[1].hi, rope);
   const uint32_t cw[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
   float y[16];
 #pragma unroll
@@ -282,7 +329,7 @@ __global__ void __launch_bounds__(128) mla_append_fp4_kernel(const __grid_consta
   *reinterpret_cast<uint2*>(dst + 8 * lane) = make_uint2(code[0], code[1]);
   dst[kFp4Scales + lane] = static_cast<uint8_t>(scale);
   *reinterpret_cast<uint16_t*>(dst + kFp4Rope + 2 * lane) =
-      static_cast<uint16_t>(cvt_e4m3x2(__fdiv_rn(x0, p.kv_scale), __fdiv_rn(x1, p.kv_scale)));
+      static_cast<uint16_t>(cvt_e4m3x2(quotient_for_rounding(rope[0], p.kv_scale), quotient_for_rounding(rope[1], p.kv_scale)));
 }
 
 // ------------------------------------------------------------------ evict --

@@ -315,7 +315,7 @@ def test_decode_tensors_that_are_refused(sparse):
     _refused(sparse, "out", out=torch.zeros((2, 1, 16, 512)))
     _refused(sparse, "lse", lse=torch.zeros((2, 1, 17)))
     _refused(sparse, "lse", lse=torch.zeros((2, 1, 16), dtype=BF))
-    _refused(sparse, "", workspace=torch.zeros(1024, dtype=torch.uint8))
+    _refused(sparse, "mla_decode", workspace=torch.zeros(1024, dtype=torch.uint8))
 
 
 def test_decode_lists_that_are_refused():
