@@ -268,8 +268,9 @@ __global__ void __launch_bounds__(128) mla_append_kernel(const __grid_constant__
 // A row of the 4-bit cache (mla_fp4.cuh) from one new row, one warp a row: a lane has one group of 16 latent values, which
 // it normalises, scales and rounds, and one pair of k_pe.
 //   y = c, or c * rsqrt(mean(c^2) + eps) * w;  scale = E4M3(max|y| / (6 kv_scale));  code = E2M1(y / (scale kv_scale))
-// The quotients are IEEE divisions in fp32 (a reciprocal's last bit would move codes that lie halfway); values of a
-// group whose scale rounds to 0 are stored as 0.
+// The quotients are IEEE divisions in fp32 (a reciprocal's last bit would move codes that lie halfway); for the codes they are
+// taken only where products with a little less and a little more than the reciprocal (off by 2^-22 at most with their rounding, the
+// margin is 2^-21) round to different ones.  Values of a group whose scale rounds to 0 are stored as 0.
 template <bool Norm>
 __global__ void __launch_bounds__(128) mla_append_fp4_kernel(const __grid_constant__ AppendParams p) {
   __shared__ float s_hi[kPairs], s_lo[kPairs];
@@ -321,9 +322,19 @@ __global__ void __launch_bounds__(128) mla_append_fp4_kernel(const __grid_consta
   const float step = e4m3x2_to_float2(scale).x * p.kv_scale;
   uint32_t code[2] = {0u, 0u};
   if (step > 0.f) {   // (no group whose scale is 0 or NaN)
+    const float inv = __frcp_rn(step), less = inv * (1.f - 0x1p-21f), more = inv * (1.f + 0x1p-21f);
+    uint32_t other[2] = {0u, 0u};
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      code[i >> 2] |= cvt_e2m1x2(__fdiv_rn(y[2 * i], step), __fdiv_rn(y[2 * i + 1], step)) << (8 * (i & 3));
+    for (int i = 0; i < 8; ++i) {
+      code[i >> 2] |= cvt_e2m1x2(y[2 * i] * less, y[2 * i + 1] * less) << (8 * (i & 3));
+      other[i >> 2] |= cvt_e2m1x2(y[2 * i] * more, y[2 * i + 1] * more) << (8 * (i & 3));
+    }
+    if (code[0] != other[0] || code[1] != other[1]) {
+      code[0] = code[1] = 0u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        code[i >> 2] |= cvt_e2m1x2(__fdiv_rn(y[2 * i], step), __fdiv_rn(y[2 * i + 1], step)) << (8 * (i & 3));
+    }
   }
   uint8_t* dst = static_cast<uint8_t*>(p.kv) + row * kFp4RowBytes;
   *reinterpret_cast<uint2*>(dst + 8 * lane) = make_uint2(code[0], code[1]);
