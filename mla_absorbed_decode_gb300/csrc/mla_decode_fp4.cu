@@ -100,7 +100,6 @@ struct Shared {
   uint64_t k_full[kItems], k_empty[kItems];   // an item of keys is in TMEM (eight warps); its MMAs are done
   uint64_t s_full[2], s_empty[2];
   uint64_t q_raw, q_full, q_empty;            // the segment's q has landed; is fp16 (a softmax warp each); is done with
-  uint64_t p_ready[2], st_free[2];            // a warpgroup's packet is written; has been read by its copy
   uint64_t credit[2];                         // the partner's receive slot is free (remote)
   // O-CTA
   uint64_t p_full[2], p_free[2];
@@ -801,7 +800,8 @@ __device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int par
   const uint32_t bar = 1 + w;                     // named barrier of the warpgroup
   const int units = blk.half >> 3;                // of 8 heads
   const uint32_t tm = sh.tmem_base + (static_cast<uint32_t>(wq * 32) << 16) + w * blk.half;
-  const uint32_t pkt = smem + kOffSend + w * kPktStride;
+  const uint32_t pkt = smem + kOffSend + w * kPktStride, dst = map_to_rank(smem + w * kPktStride, peer);
+  const uint32_t full = map_to_rank(AT(p_full), peer);
   // stmatrix: lane 8 m + r has row r of matrix m: unit m / 2 of a pair, rows 8 (m % 2) + r of 16
   const uint32_t st = pkt + (32 * wq + 8 * ((lane >> 3) & 1) + (lane & 7)) * 128, st_unit = (lane >> 4) ^ (lane & 7);
   SegmentWalker walk;
@@ -855,7 +855,7 @@ __device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int par
         }
         tmem_wait_st();
       }
-      wait(smem, AT(st_free) + 8 * w, (T & 1) ^ 1);   // the last packet has been read
+      if (lane == 0) bulk_wait_group_read<0>();   // the warp's part of the last packet has been read
       __syncwarp();
       float2 ls[8];
       bool rebased = false;
@@ -891,9 +891,10 @@ __device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int par
           float top = 0.f;
 #pragma unroll
           for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(ls[i].x, ls[i].y));
+          wait<true>(smem, AT(credit) + 8 * sb, ((T >> 1) & 1) ^ 1);   // (most often there long since)
           if (!named_bar_or(bar, 128, (!rebased && top > 0x1p14f) || told_to_leave(smem))) break;
         }
-        if (named_bar_or(bar, 128, told_to_leave(smem))) return;
+        if (named_bar_or(bar, 128, told_to_leave(smem))) goto out;
         rebased = true;
 #pragma unroll 1
         for (int i0 = 0; i0 < units; i0 += 4) {   // the heads' largest scores over the warp's tokens, four units at a time
@@ -941,8 +942,12 @@ __device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int par
           }
         unset = named_bar_or(bar, 128, unset);   // (alike for the warpgroup)
       }
-      if (t == 0) mbar_arrive(AT(p_ready) + 8 * w);
-      if (lane == 0) mbar_arrive(AT(s_empty) + 8 * sb);   // S^T has been read
+      if (lane == 0) {   // the warp's 32 tokens to the partner, and from the first warp the factors
+        bulk_copy_to_cluster(dst + sb * 2 * kPktStride + wq * 4096, pkt + wq * 4096, 4096, full + 8 * sb);
+        if (wq == 0) bulk_copy_to_cluster(dst + sb * 2 * kPktStride + kPktAlpha, pkt + kPktAlpha, kPktBytes - kPktAlpha, full + 8 * sb);
+        bulk_commit_group();
+        mbar_arrive(AT(s_empty) + 8 * sb);   // S^T has been read
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) l[i] = add2(l[i], ls[i]);
     }
@@ -972,31 +977,9 @@ __device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int par
       }
     }
   }
-}
-
-// Warps 2 and 3 (a lane each): warpgroup w's packets to the partner.
-__device__ void s_ship(const Fp4Params& p, uint32_t smem, int part, uint32_t peer, int w) {
-  const uint32_t src = smem + kOffSend + w * kPktStride, dst = map_to_rank(smem + w * kPktStride, peer);
-  const uint32_t full = map_to_rank(AT(p_full), peer);
-  SegmentWalker walk;
-  walk.init(p, part);
-  Segment s;
-  uint32_t T = 0;
-  while (walk.next(s)) {
-#pragma unroll 1
-    for (int t = tiles_of(s); t > 0; --t, ++T) {
-      const uint32_t slot = T & 1;
-      wait<true>(smem, AT(credit) + 8 * slot, ((T >> 1) & 1) ^ 1);
-      wait(smem, AT(p_ready) + 8 * w, T & 1);
-      if (told_to_leave(smem)) goto out;
-      bulk_copy_to_cluster(dst + slot * 2 * kPktStride, src, kPktBytes, full + slot * 8);
-      bulk_commit_group();
-      bulk_wait_group_read<0>();
-      mbar_arrive(AT(st_free) + 8 * w);
-    }
-  }
 out:
-  bulk_wait_group<0>();   // copies land before the CTA may leave
+  if (lane == 0) bulk_wait_group<0>();   // copies land before the CTA may leave
+  __syncwarp();
 }
 
 // ------------------------------------------------------------------ O-CTA --
@@ -1334,8 +1317,6 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_fp4_kernel(const __gri
       init(sh.raw_empty[i], 4);      // two warps of each converting warpgroup
       init(sh.s_full[i], 1);
       init(sh.s_empty[i], 8);
-      init(sh.p_ready[i], 1);
-      init(sh.st_free[i], 1);
       init(sh.credit[i], 1);
       init(sh.p_full[i], 1);
       init(sh.p_free[i], 1);
@@ -1382,7 +1363,6 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_fp4_kernel(const __gri
         if constexpr (Sparse) find_rows<true, true>(p, smem, part);
         else s_load(p, smem, part);
       } else if (warp == 1) s_mma(p, &q_map, sh, smem, part, blk);
-      else if (lane0) s_ship(p, smem, part, peer, warp - 2);
     } else {
       if (warp == 0) find_rows<Sparse, false>(p, smem, part);
       else if (warp == 1) o_mma(p, sh, smem, part);
