@@ -175,7 +175,7 @@ mla_status_t mla_decode_sparse_fp8(const mla_bf16_t* q, const uint8_t* kv_cache,
  *   [256, 288)  32 E4M3 scales, one for 16 latent dims
  *   [288, 352)  64 E4M3 codes of the RoPE key
  *   kv_t[d] = code[d] * scale[d / 16] * kv_scale (d < 512),  kv_t[512 + j] = code[j] * kv_scale
- *  kv_cache  [num_blocks, 64, 352] bytes, 16-byte aligned
+ *  kv_cache  [num_blocks, 64, 352] bytes, 32-byte aligned
  *  kv_scale  one scale for the whole cache, in [2^-116, 2^115], and softmax_scale * kv_scale * log2(e) a normal
  *            float32 (else MLA_ERR_INVALID_ARG)
  * The attention is that of mla_decode over these values; q stays bf16.  Other arguments, results and

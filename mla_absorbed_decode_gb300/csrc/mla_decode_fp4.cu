@@ -175,6 +175,11 @@ __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.al
 template <int R>
 __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(R)); }
 // `bytes` (a multiple of 16, both addresses 16-byte aligned) of global memory into shared memory.
+// 32 aligned bytes.
+__device__ __forceinline__ void load32(const void* at, uint4& a, uint4& b) {
+  asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+      : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w) : "l"(at));
+}
 __device__ __forceinline__ void prefetch_line(const void* at) { asm volatile("prefetch.global.L2 [%0];" :: "l"(at) : "memory"); }
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
@@ -591,7 +596,8 @@ __device__ void s_convert(const Fp4Params& p, Shared& sh, uint32_t smem, int par
     if (lane == 0) mbar_arrive(AT(rows_empty) + 8 * slot);
     i += 2;
   };
-  auto load = [&](uint4* to, uint32_t offset) { if (r < n_next) *to = __ldg(reinterpret_cast<const uint4*>(src + offset)); };
+  auto load = [&](uint4* to, uint32_t offset) { if (r < n_next) load32(src + offset, to[0], to[1]); };
+  auto load_scales = [&]() { if (r < n_next) sc = __ldg(reinterpret_cast<const uint4*>(src + kFp4Scales + 16 * c)); };
   SegmentWalker w;
   Segment s;
   int t = 0;               // dense: tiles of the segment to come
@@ -602,10 +608,9 @@ __device__ void s_convert(const Fp4Params& p, Shared& sh, uint32_t smem, int par
     look_up();
     if (warp_told_to_leave(smem)) return;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) load(&code[k], 128 * c + 16 * k);
-    load(&sc, kFp4Scales + 16 * c);
-    load(&rope[0], kFp4Rope + 32 * c);
-    load(&rope[1], kFp4Rope + 32 * c + 16);
+    for (int k = 0; k < 4; ++k) load(&code[2 * k], 128 * c + 32 * k);
+    load_scales();
+    load(rope, kFp4Rope + 32 * c);
     n = n_next;
   } else {
     w.init(p, part);
@@ -644,12 +649,11 @@ __device__ void s_convert(const Fp4Params& p, Shared& sh, uint32_t smem, int par
         tc_fence_after();
         values16(code[2 * k].x, code[2 * k].y, __byte_perm(s01, 0, 0x1010), v);
         values16(code[2 * k].z, code[2 * k].w, __byte_perm(s01, 0, 0x3232), v + 8);
-        load(&code[2 * k], 128 * c + 32 * k);
         tmem_st16(tm + (2 * k + c) * 32, v);
         values16(code[2 * k + 1].x, code[2 * k + 1].y, __byte_perm(s23, 0, 0x1010), v);
         values16(code[2 * k + 1].z, code[2 * k + 1].w, __byte_perm(s23, 0, 0x3232), v + 8);
-        load(&code[2 * k + 1], 128 * c + 32 * k + 16);
-        if (k == 3) load(&sc, kFp4Scales + 16 * c);
+        load(&code[2 * k], 128 * c + 32 * k);
+        if (k == 3) load_scales();
         tmem_st16(tm + (2 * k + c) * 32 + 16, v);
       } else {
         values16(code[2 * k].x, code[2 * k].y, __byte_perm(s01, 0, 0x1010), v);
@@ -670,8 +674,7 @@ __device__ void s_convert(const Fp4Params& p, Shared& sh, uint32_t smem, int par
 #pragma unroll
         for (int j = 0; j < 8; ++j) u[2 * j] = e4m3x2_to_f16x2<0>(x[j]), u[2 * j + 1] = e4m3x2_to_f16x2<1>(x[j]);
         if constexpr (Sparse) {
-          load(&rope[0], kFp4Rope + 32 * c);
-          load(&rope[1], kFp4Rope + 32 * c + 16);
+          load(rope, kFp4Rope + 32 * c);
         }
         warp_wait(smem, AT(k_empty), T & 1);   // the tile's first pair is done with
         tc_fence_after();
@@ -1008,8 +1011,7 @@ __device__ void o_convert(const Fp4Params& p, uint32_t smem) {
   };
   auto load = [&](int c) {
     if (r < n_next) {
-      code[c][0] = __ldg(reinterpret_cast<const uint4*>(src + dims + 64 * c));
-      code[c][1] = __ldg(reinterpret_cast<const uint4*>(src + dims + 64 * c + 16));
+      load32(src + dims + 64 * c, code[c][0], code[c][1]);
       scale[c] = __ldg(reinterpret_cast<const uint32_t*>(src + scales + 8 * c));
     }
   };
@@ -1432,7 +1434,7 @@ mla_status_t decode_fp4_impl(const void* q, const uint8_t* kv_cache, float kv_sc
                              size_t workspace_bytes, mla_bf16_t* out, float* lse, mla_stream_t stream) {
   if (!q || !kv_cache || !block_table || !seqlens || !metadata || !out || !lse) return MLA_ERR_INVALID_ARG;
   if (B < 1 || s_q < 1 || H < 1 || num_blocks < 1 || max_blocks < 1 || num_sm_parts < 1) return MLA_ERR_INVALID_ARG;
-  if (!aligned(q, 16) || !aligned(kv_cache, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(block_table, 4) ||
+  if (!aligned(q, 16) || !aligned(kv_cache, 32) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(block_table, 4) ||
       !aligned(seqlens, 4) || !aligned(metadata, 4))
     return MLA_ERR_INVALID_ARG;
   if (indices && (!topk_lens || index_stride < 1 || !aligned(indices, 4) || !aligned(topk_lens, 4))) return MLA_ERR_INVALID_ARG;

@@ -51,7 +51,7 @@ def _append(mla, **more):
 
 @pytest.mark.parametrize("sparse", [False, True])
 def test_decode_valid_calls_pass_every_check(mla, sparse):
-    for more in ({}, dict(kv=FAR + 16), dict(B=16384, s_q=1, H=1, parts=1), dict(s_q=1, H=512), dict(s_q=4, H=128),
+    for more in ({}, dict(kv=FAR + 32), dict(B=16384, s_q=1, H=1, parts=1), dict(s_q=1, H=512), dict(s_q=4, H=128),
                  dict(kv_scale=2.0 ** 115), dict(kv_scale=2.0 ** -116, softmax_scale=1.0), dict(num_blocks=2 ** 25 - 1),
                  dict(index_stride=2 ** 40), dict(max_blocks=2 ** 31 - 1), dict(softmax_scale=3e38)):
         assert _decode(mla, sparse, **more) == PASSED, more
@@ -59,7 +59,7 @@ def test_decode_valid_calls_pass_every_check(mla, sparse):
 
 @pytest.mark.parametrize("sparse", [False, True])
 @pytest.mark.parametrize("name,values,error", [
-    ("q", (None, FAR + 8), 1), ("kv", (None, 2 * FAR + 8), 1), ("kv_scale", (0.0, -1.0, NAN, INF, HUGE, TINY), 1),
+    ("q", (None, FAR + 8), 1), ("kv", (None, 2 * FAR + 8, 2 * FAR + 16), 1), ("kv_scale", (0.0, -1.0, NAN, INF, HUGE, TINY), 1),
     ("num_blocks", (0, -1), 1), ("num_blocks", (2 ** 25, 2 ** 40, 2 ** 62), 2), ("table", (None, 3 * FAR + 2), 1),
     ("max_blocks", (0, -1), 1), ("seqlens", (None, 4 * FAR + 2), 1), ("B", (0, -1), 1), ("B", (16385,), 2), ("s_q", (0, -1), 1),
     ("s_q", (65,), 2), ("H", (0, -1), 1), ("H", (257, 513), 2), ("softmax_scale", (0.0, -0.1, NAN, INF, 1e-44), 1),
