@@ -11,14 +11,21 @@
 //     the converted keys go from the converting threads' registers straight into TMEM as the MMA's A operand (a thread
 //     a token) and never through shared memory, whose bandwidth the operands need; Q is the B operand, in
 //     shared memory for a whole segment.  An MMA is as wide as there are heads (rounded up to 16), so few heads cost little.
-//     S^T is read with four tokens and 16 heads in a thread, which keeps the heads' running maxima and sums in registers;
-//     P^T goes to the partner with one shared-to-shared bulk copy a tile and warpgroup;
-//   * the O-CTA (odd rank) converts the latent part of the pages into shared memory (they hit L2 behind the S-CTA's loads) and
-//     accumulates O += P V, P^T and V both read by the MMA as they lie (tokens by rows: transposed operands).
+//     S^T is read with four tokens and 16 heads in a thread, which keeps the heads' references and sums in registers;
+//     each softmax warp sends its 32 tokens of P^T to the partner with one shared-to-shared bulk copy a tile;
+//   * the O-CTA (odd rank) converts the latent part of the pages into shared memory (from L2, where its row finder has them brought)
+//     and accumulates O += P V, P^T and V both read by the MMA as they lie (tokens by rows: transposed operands).
 // Rows past 128 go to further pairs of the cluster, which walk the same pages.  A cluster is one part of the split schedule.
 //
+// Measured (GB300, 1.9 GHz; call with its merge, q and cache from HBM): 64 x 4096 tokens, 128 heads 88 us (832 TFLOP/s, 0.43 of a
+// library's bf16 product), 16 heads 74 us; 64 x 2 x 8192: 281 us (1040 TFLOP/s); 4 x 131072: 205 us; 64 lists of 2048 tokens: 82 us;
+// 2 x 300 tokens, 16 heads: 16 us.  A tile takes a pair 4000 to 4300 cycles, of which S's MMAs are 2304 and O's 2048: what is between
+// are the waits of chains (keys converted -> MMA -> exponentials -> vote -> copy -> MMA) whose links take 100 to 300 cycles each however
+// little they do, with 20 warps on an SM that issue 0.57 of the time, and the O-CTA's shared memory (V written once and read by the MMAs
+// with P: 2800 of the 4000 cycles at 128 bytes each).
+//
 // The softmax is online, with the reference maximum of a head raised only where a score passes it by 2^8: the threads take the
-// exponentials against the old reference, and a vote (the barrier that ends a tile anyhow) tells whether one overflowed its room;
+// exponentials against the old reference, and a vote (the barrier that ends a tile) tells whether one overflowed its room;
 // only then the tile is done again with new references, and O rescaled.  P is fp16 with an offset of 2^6, so that everything down to
 // 2^-20 of the reference keeps 11 bits.
 //
@@ -63,10 +70,10 @@ constexpr uint32_t kPktAlpha = 128 * 128;     // after P^T (128 tokens x 64 head
 constexpr uint32_t kPktFlag = kPktAlpha + 256;   // whether alpha counts
 constexpr uint32_t kPktBytes = kPktFlag + 16;
 constexpr uint32_t kPktStride = 17 * 1024;
-// O-CTA: segments whose output factors may be there.  The S-CTA is at most three tiles ahead of the MMAs, which wait for the epilogue
-// of the segment before.
+// O-CTA: segments whose output factors may be there.  The S-CTA has sent at most two tiles that the MMAs are not done with, and these
+// wait for the epilogue of the segment before.
 constexpr uint32_t kInvSlots = 4;
-constexpr uint32_t kRowSlots = 8;             // O-CTA: pages whose rows have been looked up
+constexpr uint32_t kRowSlots = 8;             // pages whose rows have been found (16: the same speed)
 constexpr uint32_t kRowBytes = 4 * (kPageTokens + 1);
 constexpr uint32_t kKCol = 256;               // S-CTA's TMEM columns: S^T of two tiles at 0 and 128, the keys from 256
 constexpr float kOffset = 6.f;                // P is taken against 2^-6 of the reference maximum
@@ -77,14 +84,13 @@ constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kRegsMisc = 48, kRegsSoftmax = 136, kRegsConvert = 80;
 static_assert(128 * kRegsMisc + 256 * kRegsSoftmax + 256 * kRegsConvert <= kThreads * 96, "more would wait forever");
 
-
 // shared memory (offsets from a 1024-byte aligned base)
 constexpr uint32_t kOffSend = 9 * kQChunk;                   // S-CTA: q first, then a packet of each warpgroup
-constexpr uint32_t kOffRaw = kOffSend + 2 * kPktStride;      // S-CTA: the two pages of a tile as cached
+constexpr uint32_t kOffRaw = kOffSend + 2 * kPktStride;      // S-CTA: the two pages of a tile as cached (lists: the ring of found rows)
 constexpr uint32_t kOffV = 4 * kPktStride;                   // O-CTA: the packets of two tiles first, then values
 constexpr uint32_t kOffEpi = kOffV + kVSlots * kVSlot;       // O-CTA: 2 KiB transpose buffer per epilogue warp
 constexpr uint32_t kOffInvL = kOffEpi + 8 * 2048;            // O-CTA: output factors of segments [kInvSlots][2][64]
-constexpr uint32_t kOffRows = kOffInvL + kInvSlots * 512;    // O-CTA: the ring of looked-up rows
+constexpr uint32_t kOffRows = kOffInvL + kInvSlots * 512;    // O-CTA: the ring of found rows
 constexpr uint32_t kOffShared = kOffRaw + 2 * kRawPage;
 static_assert(kOffRows + kRowSlots * kRowBytes <= kOffShared, "O-CTA layout");
 
@@ -103,7 +109,7 @@ struct Shared {
   uint64_t credit[2];                         // the partner's receive slot is free (remote)
   // O-CTA
   uint64_t p_full[2], p_free[2];
-  uint64_t rows_full[kRowSlots], rows_empty[kRowSlots];
+  uint64_t rows_full[kRowSlots], rows_empty[kRowSlots];   // (lists: the S-CTA's too)
   uint64_t v_full[kVSlots], v_empty[kVSlots];
   uint64_t o_full, o_free, o_sync, corr_go, corr_done;
   uint64_t inv_full[kInvSlots];               // a segment's output factors have come (64 threads of either softmax warpgroup)
@@ -128,7 +134,7 @@ static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 
 // A wait ends when the phase is complete or the CTA has been told to give up, which the watchdog (o_watch) does after 0.5 s without
 // a tile: the code around each of some twenty waits has to be short, since 20 warps of ten kinds share the instruction caches
-// (64 x 4096, 128 heads: 220 us with a way out inlined at every wait, 120 with the same ways made short).  What a role does after
+// (64 x 4096, 128 heads: an early form took 220 us with a way out inlined at every wait, 120 with the same ways made short).  What a role does after
 // a wait that gave up is harmless -- it touches the CTA's own buffers -- and each looks once a tile whether to leave.
 template <bool Cluster = false>
 __device__ __forceinline__ void wait(uint32_t smem, uint32_t bar, uint32_t parity) {
@@ -573,7 +579,7 @@ __device__ void find_rows(const Fp4Params& p, uint32_t smem, int part) {
 // Warps 12..19: a thread a token; warpgroup c takes latent dims [256 c, 256 c + 256) and half of the rope dims.  Dense: a tile's
 // codes are read into registers at once, which frees the page buffers for the next tile's loads.  Lists: a thread loads its row from
 // global memory, every part as soon as the same part of the tile before has been converted (by copies of a row each into the page
-// buffers 64 x 2048 listed tokens took 122 us).
+// buffers 64 x 2048 listed tokens took 122 us; now 82, 90 with loads of 16 bytes).
 template <bool Sparse>
 __device__ void s_convert(const Fp4Params& p, Shared& sh, uint32_t smem, int part, int c) {
   const int quad = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
