@@ -17,8 +17,8 @@
 //     and accumulates O += P V, P^T and V both read by the MMA as they lie (tokens by rows: transposed operands).
 // Rows past 128 go to further pairs of the cluster, which walk the same pages.  A cluster is one part of the split schedule.
 //
-// Measured (GB300, 1.9 GHz; call with its merge, q and cache from HBM): 64 x 4096 tokens, 128 heads 88 us (832 TFLOP/s, 0.43 of a
-// library's bf16 product), 16 heads 74 us; 64 x 2 x 8192: 281 us (1040 TFLOP/s); 4 x 131072: 205 us; 64 lists of 2048 tokens: 82 us;
+// Measured (GB300, 1.9 GHz; call with its merge, q and cache from HBM): 64 x 4096 tokens, 128 heads 86 us (847 TFLOP/s, 0.44 of a
+// library's bf16 product), 16 heads 73 us; 64 x 2 x 8192: 277 us (1054 TFLOP/s); 4 x 131072: 205 us; 64 lists of 2048 tokens: 82 us;
 // 2 x 300 tokens, 16 heads: 16 us.  A tile takes a pair 4000 to 4300 cycles, of which S's MMAs are 2304 and O's 2048: what is between
 // are the waits of chains (keys converted -> MMA -> exponentials -> vote -> copy -> MMA) whose links take 100 to 300 cycles each however
 // little they do, with 20 warps on an SM that issue 0.57 of the time, and the O-CTA's shared memory (V written once and read by the MMAs
@@ -150,6 +150,16 @@ __device__ __forceinline__ void wait(uint32_t smem, uint32_t bar, uint32_t parit
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n\t@p bra DONE;\n\t"
         "ld.volatile.shared.b32 r, [%2];\n\tsetp.eq.b32 q, r, 0;\n\t@q bra AGAIN;\nDONE:\n\t}"
         :: "r"(bar), "r"(parity), "r"(AT(abort)) : "memory");
+}
+// The same, and whether the phase is complete.
+__device__ __forceinline__ bool wait_done(uint32_t smem, uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b32 r;\nAGAIN:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+      "ld.volatile.shared.b32 r, [%3];\n\tsetp.eq.b32 q, r, 0;\n\t@q bra AGAIN;\nDONE:\n\tselp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(done) : "r"(bar), "r"(parity), "r"(AT(abort)) : "memory");
+  return done != 0;
 }
 // The same by a warp that goes on together.
 template <bool Cluster = false>
@@ -847,7 +857,8 @@ __device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int par
         const int tok = 32 * wq + lane, e = k * kPageTokens + tok;
         if (tok < ntok) key = !Sparse ? e : e < p.idx_stride ? __ldg(p.indices + static_cast<int64_t>(s.b) * p.idx_stride + e) : -1;
       }
-      wait(smem, AT(s_full) + 8 * sb, (T >> 1) & 1);
+      if (lane == 0) bulk_wait_group_read<0>();   // the warp's part of the last packet has been read
+      bool leave = !wait_done(smem, AT(s_full) + 8 * sb, (T >> 1) & 1);
       __syncwarp();
       tc_fence_after();
       if (masked) {
@@ -864,8 +875,6 @@ __device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int par
         }
         tmem_wait_st();
       }
-      if (lane == 0) bulk_wait_group_read<0>();   // the warp's part of the last packet has been read
-      __syncwarp();
       float2 ls[8];
       bool rebased = false;
       while (true) {   // once, or twice where references have to move
@@ -893,17 +902,17 @@ __device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int par
               stmatrix4(st + hf * (16 * 128) + (((2 * ii) ^ st_unit) << 4), pk[0], pk[1], pk[2], pk[3]);
             }
           }
-          if (t == 0) asm volatile("st.shared.u32 [%0], %1;" :: "r"(pkt + kPktFlag), "r"(rebased ? 1 : 0) : "memory");
+          if (t == 96) asm volatile("st.shared.u32 [%0], %1;" :: "r"(pkt + kPktFlag), "r"(rebased ? 1 : 0) : "memory");
           fence_proxy_async_smem();
           tc_fence_before();
           // a P past 2^14 (no sum of four shows less): the tile again, with new references
           float top = 0.f;
 #pragma unroll
           for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(ls[i].x, ls[i].y));
-          wait<true>(smem, AT(credit) + 8 * sb, ((T >> 1) & 1) ^ 1);   // (most often there long since)
-          if (!named_bar_or(bar, 128, (!rebased && top > 0x1p14f) || told_to_leave(smem))) break;
+          leave |= !wait_done(smem, AT(credit) + 8 * sb, ((T >> 1) & 1) ^ 1);   // (most often there long since)
+          if (!named_bar_or(bar, 128, (!rebased && top > 0x1p14f) || leave)) break;
         }
-        if (named_bar_or(bar, 128, told_to_leave(smem))) goto out;
+        if (named_bar_or(bar, 128, leave)) goto out;
         rebased = true;
 #pragma unroll 1
         for (int i0 = 0; i0 < units; i0 += 4) {   // the heads' largest scores over the warp's tokens, four units at a time
@@ -951,11 +960,11 @@ __device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int par
           }
         unset = named_bar_or(bar, 128, unset);   // (alike for the warpgroup)
       }
-      if (lane == 0) {   // the warp's 32 tokens to the partner, and from the first warp the factors
-        bulk_copy_to_cluster(dst + sb * 2 * kPktStride + wq * 4096, pkt + wq * 4096, 4096, full + 8 * sb);
-        if (wq == 0) bulk_copy_to_cluster(dst + sb * 2 * kPktStride + kPktAlpha, pkt + kPktAlpha, kPktBytes - kPktAlpha, full + 8 * sb);
-        bulk_commit_group();
+      if (lane == 0) {
         mbar_arrive(AT(s_empty) + 8 * sb);   // S^T has been read
+        // the warp's 32 tokens to the partner, the last warp's with the factors behind them
+        bulk_copy_to_cluster(dst + sb * 2 * kPktStride + wq * 4096, pkt + wq * 4096, wq == 3 ? kPktBytes - 3 * 4096 : 4096, full + 8 * sb);
+        bulk_commit_group();
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) l[i] = add2(l[i], ls[i]);
@@ -1082,7 +1091,7 @@ __device__ void o_mma(const Fp4Params& p, Shared& sh, uint32_t smem, int part) {
       const int ntok = tile_tokens(p, s, k);
       if (lane == 0) mbar_arrive_expect_tx(full, 2 * kPktBytes);
       __syncwarp();
-      warp_wait<true>(smem, full, (T >> 1) & 1);
+      warp_wait(smem, full, (T >> 1) & 1);
       if (warp_told_to_leave(smem)) goto out;
       if (k != s.kb && (ld_shared_s32(pkt + kPktFlag) | ld_shared_s32(pkt + kPktStride + kPktFlag))) {   // scale O before adding
         mma_commit_warp(AT(o_sync));
