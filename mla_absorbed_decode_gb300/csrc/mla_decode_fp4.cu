@@ -17,8 +17,8 @@
 //     and accumulates O += P V, P^T and V both read by the MMA as they lie (tokens by rows: transposed operands).
 // Rows past 128 go to further pairs of the cluster, which walk the same pages.  A cluster is one part of the split schedule.
 //
-// Measured (GB300, 1.9 GHz; call with its merge, q and cache from HBM): 64 x 4096 tokens, 128 heads 86 us (847 TFLOP/s, 0.44 of a
-// library's bf16 product), 16 heads 73 us; 64 x 2 x 8192: 277 us (1054 TFLOP/s); 4 x 131072: 197 us; 64 lists of 2048 tokens: 82 us;
+// Measured (GB300, 1.9 GHz; call with its merge, q and cache from HBM): 64 x 4096 tokens, 128 heads 85 us (858 TFLOP/s, 0.44 of a
+// library's bf16 product), 16 heads 73 us; 64 x 2 x 8192: 274 us (1066 TFLOP/s); 4 x 131072: 197 us; 64 lists of 2048 tokens: 82 us;
 // 2 x 300 tokens, 16 heads: 16 us.  A tile takes a pair 4000 to 4300 cycles, of which S's MMAs are 2304 and O's 2048: what is between
 // are the waits of chains (keys converted -> MMA -> exponentials -> vote -> copy -> MMA) whose links take 100 to 300 cycles each however
 // little they do, with 20 warps on an SM that issue 0.57 of the time, and the O-CTA's shared memory (V written once and read by the MMAs
@@ -1372,33 +1372,37 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_fp4_kernel(const __gri
   tc_fence_after();
   griddep_wait();        // the metadata, q and the cache are complete from here on
 
-  if (warp < 4) {
-    regs_down<kRegsMisc>();
-    const bool lane0 = (threadIdx.x & 31) == 0;
-    if (is_s) {
-      if (warp == 0) {
-        if constexpr (Sparse) find_rows<true, true>(p, smem, part);
-        else s_load(p, smem, part);
-      } else if (warp == 1) s_mma(p, &q_map, sh, smem, part, blk);
-    } else {
-      if (warp == 0) find_rows<Sparse, false>(p, smem, part);
-      else if (warp == 1) o_mma(p, sh, smem, part);
-      else if (lane0 && warp == 2) o_forward(p, smem, part, peer);
-      else if (lane0) o_watch(p, smem, cl);
-    }
-  } else if (warp < 12) {
-    regs_up<kRegsSoftmax>();
-    if (is_s) s_softmax<Sparse>(p, sh, smem, part, blk, peer);
-    else o_epilogue(p, sh, smem, part, blk);
-  } else {
+  // Each CTA's hot loops lie together: of 30 orders of these branches, 64 x 2 x 8192 took from 273 to 340 us, best with the S-CTA's three
+  // roles side by side and the O-CTA's conversion next to its MMAs (the roles of an SM share its instruction caches).
+  const bool lane0 = (threadIdx.x & 31) == 0;
+  if (is_s && warp >= 12) {
     regs_down<kRegsConvert>();
-    if (is_s) {
-      s_convert<Sparse>(p, sh, smem, part, (warp - 12) >> 2);
-      __syncwarp();
-      if ((threadIdx.x & 31) == 0) mbar_arrive_remote(map_to_rank(AT(gone), peer));
-    } else {
-      o_convert(p, smem);
+    s_convert<Sparse>(p, sh, smem, part, (warp - 12) >> 2);
+    __syncwarp();
+    if (lane0) mbar_arrive_remote(map_to_rank(AT(gone), peer));
+  } else if (is_s && warp >= 4 && warp < 12) {
+    regs_up<kRegsSoftmax>();
+    s_softmax<Sparse>(p, sh, smem, part, blk, peer);
+  } else if (is_s && warp < 4) {
+    regs_down<kRegsMisc>();
+    if (warp == 0) {
+      if constexpr (Sparse) find_rows<true, true>(p, smem, part);
+      else s_load(p, smem, part);
+    } else if (warp == 1) {
+      s_mma(p, &q_map, sh, smem, part, blk);
     }
+  } else if (!is_s && warp >= 4 && warp < 12) {
+    regs_up<kRegsSoftmax>();
+    o_epilogue(p, sh, smem, part, blk);
+  } else if (!is_s && warp >= 12) {
+    regs_down<kRegsConvert>();
+    o_convert(p, smem);
+  } else {
+    regs_down<kRegsMisc>();
+    if (warp == 0) find_rows<Sparse, false>(p, smem, part);
+    else if (warp == 1) o_mma(p, sh, smem, part);
+    else if (lane0 && warp == 2) o_forward(p, smem, part, peer);
+    else if (lane0) o_watch(p, smem, cl);
   }
 
   __syncwarp();
