@@ -755,56 +755,54 @@ out:
   __syncwarp();
 }
 
-// Rows of q of warpgroup w's heads, in place: bf16 as loaded to fp16, a warp a row (four at a time, or a segment's first MMA waits 9000
-// cycles for 128 of them), and their scores' factors.
+// Rows of q of warpgroup w's heads, in place: bf16 as loaded to fp16, and their scores' factors.  A warp takes four rows at a time (a
+// segment's first MMA waits for it: 9000 cycles for 128 rows one by one): of each 32 bytes a lane for the latent dims, of the four
+// RoPE parts 16 bytes a lane.  The largest element is found in the bits, whose order is that of the absolute values (a NaN's the highest).
 __device__ __forceinline__ void s_scale_q(const Fp4Params& p, Shared& sh, uint32_t smem, const Block& blk, int w, int wq, int lane) {
   const float unit = p.scale_log2 * p.kv_scale;
 #pragma unroll 1
   for (int j = wq; j < blk.half; j += 16) {
-    uint4 v[4][3];
-    float top[4];
-    auto at = [&](int g) {   // 16 bytes of chunk lane / 8
+    auto place = [&](int g, int chunk) {   // 16 bytes, lane % 8, of a chunk of row g
       const int n = w * blk.half + min(j + 4 * g, blk.half - 1);
-      return smem + (lane >> 3) * kQChunk + n * 128 + (((lane & 7) ^ (n & 7)) << 4);
+      return smem + chunk * kQChunk + n * 128 + (((lane & 7) ^ (n & 7)) << 4);
     };
+    auto largest = [](uint32_t top, const uint4& v) {
+      return __vmaxu2(__vmaxu2(top, __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu)), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+    };
+    auto scaled = [](const uint4& v, uint32_t e) {   // (a row with an infinity or a NaN, e = 255, becomes NaN)
+      const float sc = __uint_as_float((268u - e) << 23);
+      const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+      uint32_t y[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) y[q] = e < 255 ? pack_f16x2(bf16_lo(x[q]) * sc, bf16_hi(x[q]) * sc) : 0x7E007E00u;
+      return make_uint4(y[0], y[1], y[2], y[3]);
+    };
+    const int mine = lane >> 3;   // the row whose RoPE part the lane has
+    uint4 v[4][2];
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) v[g][u] = ld_shared_v4(place(g, (lane >> 3) + 4 * u));
+    const uint4 rope = ld_shared_v4(place(mine, 8));
+    const uint32_t rope_top = largest(0u, rope);
+    uint32_t e[4], rope_e = 0;
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      v[g][0] = ld_shared_v4(at(g));
-      v[g][1] = ld_shared_v4(at(g) + 4 * kQChunk);
-      v[g][2] = lane < 8 ? ld_shared_v4(at(g) + 8 * kQChunk) : make_uint4(0, 0, 0, 0);
+      uint32_t top = largest(largest(mine == g ? rope_top : 0u, v[g][0]), v[g][1]);
+      top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
+      e[g] = max(top >> 7, 41u);   // the exponent: a factor of 2^100 at most
+      if (mine == g) rope_e = e[g];
     }
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      top[g] = 0.f;
-#pragma unroll
-      for (int u = 0; u < 3; ++u) {
-        const uint32_t x[4] = {v[g][u].x, v[g][u].y, v[g][u].z, v[g][u].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) top[g] = max_nan(top[g], max_nan(fabsf(bf16_lo(x[e])), fabsf(bf16_hi(x[e]))));
-      }
-    }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) top[g] = max_nan(top[g], __shfl_xor_sync(0xffffffffu, top[g], o));
+    __syncwarp();
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       if (j + 4 * g >= blk.half) break;
-      const bool finite = top[g] <= 3.4e38f;
-      const int e = finite ? max(static_cast<int>(__float_as_uint(top[g]) >> 23), 41) : 141;   // at most a factor 2^100
-      // (a row with an infinity or a NaN becomes NaN; the factor is never 0, so that scores of -inf stay what they are)
-      const float sc = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
-      const float back = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
 #pragma unroll
-      for (int u = 0; u < 3; ++u) {
-        const uint32_t x[4] = {v[g][u].x, v[g][u].y, v[g][u].z, v[g][u].w};
-        uint32_t y[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) y[q] = finite ? pack_f16x2(bf16_lo(x[q]) * sc, bf16_hi(x[q]) * sc) : 0x7E007E00u;
-        if (u < 2 || lane < 8) st_shared_v4(at(g) + 4 * u * kQChunk, make_uint4(y[0], y[1], y[2], y[3]));
-      }
-      if (lane == 0) sh.q_scale[w * blk.half + j + 4 * g] = fmaxf(unit * back, 0x1p-126f);
+      for (int u = 0; u < 2; ++u) st_shared_v4(place(g, (lane >> 3) + 4 * u), scaled(v[g][u], e[g]));
+      // (the factor is never 0, so that scores of -inf stay what they are)
+      if (lane == 0) sh.q_scale[w * blk.half + j + 4 * g] = fmaxf(unit * __uint_as_float((min(e[g], 141u) - 14u) << 23), 0x1p-126f);
     }
+    if (j + 4 * mine < blk.half) st_shared_v4(place(mine, 8), scaled(rope, rope_e));
   }
   fence_proxy_async_smem();
   __syncwarp();
