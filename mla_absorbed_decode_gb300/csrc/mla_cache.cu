@@ -46,20 +46,26 @@ __device__ __forceinline__ float2 rope_turn(const RopeTable& t, float hi, float 
 struct Float2Sum {
   float hi, lo;
 };
+__device__ __forceinline__ Float2Sum add_exactly(Float2Sum a, Float2Sum b) {   // (up to the sum of the low parts)
+  const float s = __fadd_rn(a.hi, b.hi), t = __fsub_rn(s, a.hi);
+  return {s, __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, t)), __fsub_rn(b.hi, t)) + (a.lo + b.lo)};
+}
+__device__ __forceinline__ Float2Sum times(float a, Float2Sum b) {
+  const float p = __fmul_rn(a, b.hi);
+  return {p, fmaf(a, b.hi, -p) + a * b.lo};
+}
 // v / d, d > 0, to 24 bits with the last bit set where bits are lost (toward zero): a later rounding to fewer bits then falls as that
 // of the quotient itself would.
-__device__ __forceinline__ float quotient_for_rounding(Float2Sum v, float d) {
-  const float q = __fdiv_rn(v.hi, d), rest = fmaf(-q, d, v.hi) + v.lo;
+__device__ __forceinline__ float quotient_for_rounding(Float2Sum v, Float2Sum d) {
+  const float q = __fdiv_rn(v.hi, d.hi), rest = fmaf(-q, d.hi, v.hi) + fmaf(-q, d.lo, v.lo);
   if (!(rest != 0.f) || q == 0.f || !(fabsf(q) <= 3.4e38f)) return q;
   return __uint_as_float((__float_as_uint(q) - ((rest < 0.f) == (q > 0.f) ? 1u : 0u)) | 1u);
 }
 // x0 a + x1 b, the factors sums of two floats.
 __device__ __forceinline__ Float2Sum dot2(float x0, Float2Sum a, float x1, Float2Sum b) {
-  const float p = __fmul_rn(x0, a.hi), q = __fmul_rn(x1, b.hi), s = __fadd_rn(p, q), t = __fsub_rn(s, p);
-  const float lost = __fadd_rn(__fsub_rn(p, __fsub_rn(s, t)), __fsub_rn(q, t));   // of the sum
-  const float lo = lost + (fmaf(x0, a.hi, -p) + fmaf(x0, a.lo, fmaf(x1, b.hi, -q) + x1 * b.lo));
-  const float hi = __fadd_rn(s, lo);
-  return {hi, __fsub_rn(lo, __fsub_rn(hi, s))};
+  const Float2Sum s = add_exactly(times(x0, a), times(x1, b));
+  const float hi = __fadd_rn(s.hi, s.lo);
+  return {hi, __fsub_rn(s.lo, __fsub_rn(hi, s.hi))};
 }
 // The pair (x0, x1) turned by the angle pos * (hi + lo), for codes: a value is off by about 2^-26 of the pair's norm (positions
 // below 2^17; 2^-19 up to 2^24), where rope_turn's hardware sine, off by 2^-21, would move many times as many codes that lie
@@ -268,9 +274,11 @@ __global__ void __launch_bounds__(128) mla_append_kernel(const __grid_constant__
 // A row of the 4-bit cache (mla_fp4.cuh) from one new row, one warp a row: a lane has one group of 16 latent values, which
 // it normalises, scales and rounds, and one pair of k_pe.
 //   y = c, or c * rsqrt(mean(c^2) + eps) * w;  scale = E4M3(max|y| / (6 kv_scale));  code = E2M1(y / (scale kv_scale))
-// The quotients are IEEE divisions in fp32 (a reciprocal's last bit would move codes that lie halfway); for the codes they are
-// taken only where products with a little less and a little more than the reciprocal (off by 2^-22 at most with their rounding, the
-// margin is 2^-21) round to different ones.  Values of a group whose scale rounds to 0 are stored as 0.
+// Codes that lie halfway are few but a flipped scale moves its whole group, so what is rounded is known to more than fp32's 24 bits:
+// values, scales and quotients are sums of two floats, and codes come out as from 64 bits.  The codes' quotients are formed only
+// where products with a little less and a little more than the factor (off by 2^-21 at most with all roundings, the margin is 2^-20)
+// round to different ones.  Values of a group whose scale rounds to 0 are stored as 0.
+// 32768 rows without a norm 26 us from a graph, 49 MB: the instructions bound it, some 450 a row, not the bytes (7 us).
 template <bool Norm>
 __global__ void __launch_bounds__(128) mla_append_fp4_kernel(const __grid_constant__ AppendParams p) {
   __shared__ float s_hi[kPairs], s_lo[kPairs];
@@ -301,28 +309,39 @@ __global__ void __launch_bounds__(128) mla_append_fp4_kernel(const __grid_consta
   Float2Sum rope[2] = {{bf16_lo(pe), 0.f}, {bf16_hi(pe), 0.f}};
   if (p.positions != nullptr) rope_turned(s_hi[lane], s_lo[lane], pos, rope[0].hi, rope[1].hi, rope);
   const uint32_t cw[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-  float y[16];
+  float y[16];                     // the values are y * inv
+  Float2Sum inv = {1.f, 0.f};
 #pragma unroll
   for (int i = 0; i < 8; ++i) y[2 * i] = bf16_lo(cw[i]), y[2 * i + 1] = bf16_hi(cw[i]);
   if constexpr (Norm) {
-    float ss = 0.f;
+    Float2Sum ss = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 16; ++i) ss = fmaf(y[i], y[i], ss);
+    for (int i = 0; i < 16; ++i) ss = add_exactly(ss, {__fmul_rn(y[i], y[i]), 0.f});   // (squares of bf16 are exact)
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float inv = rsqrtf(ss * (1.f / kDimV) + p.norm_eps);
+    for (int o = 16; o >= 1; o >>= 1) ss = add_exactly(ss, {__shfl_xor_sync(0xffffffffu, ss.hi, o), __shfl_xor_sync(0xffffffffu, ss.lo, o)});
+    ss = add_exactly({ss.hi * (1.f / kDimV), ss.lo * (1.f / kDimV)}, {p.norm_eps, 0.f});
+    // its inverse root: an approximation and one step of Newton's method for the rest, then a power of two times a number in [1, 2)
+    const float r = rsqrtf(ss.hi);
+    const Float2Sum rr = times(r, {r, 0.f}), one = times(ss.hi, rr);
+    const float rest = 0.5f * r * (((1.f - one.hi) - one.lo) - ss.lo * rr.hi);
+    const uint32_t bits = __float_as_uint(r), e = bits >> 23;
+    float p2 = r;
+    if (e > 0 && e < 254 && fabsf(rest) < r) {   // (not for rows of zeros or with infinities)
+      p2 = __uint_as_float(e << 23);
+      inv = {__uint_as_float((bits & 0x007FFFFFu) | 0x3F800000u), rest * __uint_as_float((254u - e) << 23)};
+    }
     const uint32_t ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[2 * i] = y[2 * i] * inv * bf16_lo(ww[i]), y[2 * i + 1] = y[2 * i + 1] * inv * bf16_hi(ww[i]);
+    for (int i = 0; i < 8; ++i) y[2 * i] = y[2 * i] * p2 * bf16_lo(ww[i]), y[2 * i + 1] = y[2 * i + 1] * p2 * bf16_hi(ww[i]);
   }
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) amax = max_nan(amax, fabsf(y[i]));
-  const uint32_t scale = cvt_e4m3x2(__fdiv_rn(amax, 6.f * p.kv_scale), 0.f) & 0xFFu;
-  const float step = e4m3x2_to_float2(scale).x * p.kv_scale;
+  const uint32_t scale = cvt_e4m3x2(quotient_for_rounding(times(amax, inv), times(6.f, {p.kv_scale, 0.f})), 0.f) & 0xFFu;
+  const Float2Sum step = times(e4m3x2_to_float2(scale).x, {p.kv_scale, 0.f});
   uint32_t code[2] = {0u, 0u};
-  if (step > 0.f) {   // (no group whose scale is 0 or NaN)
-    const float inv = __frcp_rn(step), less = inv * (1.f - 0x1p-21f), more = inv * (1.f + 0x1p-21f);
+  if (step.hi > 0.f) {   // (no group whose scale is 0 or NaN)
+    const float f = __frcp_rn(step.hi) * inv.hi, less = f * (1.f - 0x1p-20f), more = f * (1.f + 0x1p-20f);
     uint32_t other[2] = {0u, 0u};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -333,14 +352,15 @@ __global__ void __launch_bounds__(128) mla_append_fp4_kernel(const __grid_consta
       code[0] = code[1] = 0u;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        code[i >> 2] |= cvt_e2m1x2(__fdiv_rn(y[2 * i], step), __fdiv_rn(y[2 * i + 1], step)) << (8 * (i & 3));
+        code[i >> 2] |= cvt_e2m1x2(quotient_for_rounding(times(y[2 * i], inv), step), quotient_for_rounding(times(y[2 * i + 1], inv), step))
+                        << (8 * (i & 3));
     }
   }
   uint8_t* dst = static_cast<uint8_t*>(p.kv) + row * kFp4RowBytes;
   *reinterpret_cast<uint2*>(dst + 8 * lane) = make_uint2(code[0], code[1]);
   dst[kFp4Scales + lane] = static_cast<uint8_t>(scale);
   *reinterpret_cast<uint16_t*>(dst + kFp4Rope + 2 * lane) =
-      static_cast<uint16_t>(cvt_e4m3x2(quotient_for_rounding(rope[0], p.kv_scale), quotient_for_rounding(rope[1], p.kv_scale)));
+      static_cast<uint16_t>(cvt_e4m3x2(quotient_for_rounding(rope[0], {p.kv_scale, 0.f}), quotient_for_rounding(rope[1], {p.kv_scale, 0.f})));
 }
 
 // ------------------------------------------------------------------ evict --

@@ -17,8 +17,8 @@
 //     and accumulates O += P V, P^T and V both read by the MMA as they lie (tokens by rows: transposed operands).
 // Rows past 128 go to further pairs of the cluster, which walk the same pages.  A cluster is one part of the split schedule.
 //
-// Measured (GB300, 1.9 GHz; call with its merge, q and cache from HBM): 64 x 4096 tokens, 128 heads 85 us (858 TFLOP/s, 0.44 of a
-// library's bf16 product), 16 heads 73 us; 64 x 2 x 8192: 274 us (1066 TFLOP/s); 4 x 131072: 197 us; 64 lists of 2048 tokens: 82 us;
+// Measured (GB300, 1.9 GHz; call with its merge, q and cache from HBM): 64 x 4096 tokens, 128 heads 84 us (867 TFLOP/s, 0.45 of a
+// library's bf16 product), 16 heads 74 us; 64 x 2 x 8192: 271 us (1078 TFLOP/s); 4 x 131072: 198 us; 64 lists of 2048 tokens: 82 us;
 // 2 x 300 tokens, 16 heads: 16 us.  A tile takes a pair 4000 to 4300 cycles, of which S's MMAs are 2304 and O's 2048: what is between
 // are the waits of chains (keys converted -> MMA -> exponentials -> vote -> copy -> MMA) whose links take 100 to 300 cycles each however
 // little they do, with 20 warps on an SM that issue 0.57 of the time, and the O-CTA's shared memory (V written once and read by the MMAs
