@@ -612,8 +612,9 @@ __device__ void s_convert(const Fp4Params& p, Shared& sh, uint32_t smem, int par
     if (lane == 0) mbar_arrive(AT(rows_empty) + 8 * slot);
     i += 2;
   };
-  auto load = [&](uint4* to, uint32_t offset) { if (r < n_next) load32(src + offset, to[0], to[1]); };
-  auto load_scales = [&]() { if (r < n_next) sc = __ldg(reinterpret_cast<const uint4*>(src + kFp4Scales + 16 * c)); };
+  // (a row past the page's end is row 0, read and not seen: under a condition a load would be waited for at once)
+  auto load = [&](uint4* to, uint32_t offset) { load32(src + offset, to[0], to[1]); };
+  auto load_scales = [&]() { sc = __ldg(reinterpret_cast<const uint4*>(src + kFp4Scales + 16 * c)); };
   SegmentWalker w;
   Segment s;
   int t = 0;               // dense: tiles of the segment to come
