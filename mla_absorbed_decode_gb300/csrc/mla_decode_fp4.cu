@@ -81,7 +81,7 @@ constexpr float kTop = kOffset + 8.f;         // an exponent past this rebases i
 constexpr uint32_t kTimeoutNs = 500u * 1000 * 1000;
 constexpr float kLn2 = 0.69314718055994530942f;
 // registers a thread: the three kinds of warpgroups share what the launch gets (640 x 96)
-constexpr int kRegsMisc = 48, kRegsSoftmax = 136, kRegsConvert = 80;
+constexpr int kRegsMisc = 64, kRegsSoftmax = 120, kRegsConvert = 88;
 static_assert(128 * kRegsMisc + 256 * kRegsSoftmax + 256 * kRegsConvert <= kThreads * 96, "more would wait forever");
 
 // shared memory (offsets from a 1024-byte aligned base)
