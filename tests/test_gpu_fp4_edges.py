@@ -346,3 +346,25 @@ def test_append_tensors_that_are_refused():
     for norm in (torch.ones(512), torch.ones(256, dtype=BF), torch.ones(1024, dtype=BF)[::2]):
         refused("norm_weight", norm_weight=norm.cuda() if norm.is_contiguous() else torch.ones(1024, dtype=BF, device="cuda")[::2])
     refused("norm_weight", norm_weight=torch.ones(512, dtype=BF))      # not on the GPU
+
+
+# ------------------------------------------------------------------------------------ rounding --
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("kv_scale", [2.0 ** -6, 0.013])
+def test_append_codes_are_those_of_64_bits(norm, kv_scale):
+    """Latent codes and scales from values that are known to 2^-40 of themselves (sums of two floats): none of the 2.1 million
+    differs from the oracle's, whose 64 bits would have to lie within that of a halfway point (expected: 4e-6 of them)."""
+    import mla_absorbed_decode_gb300 as mla
+    g = torch.Generator().manual_seed(9)
+    N, blocks = 4096, 64
+    rows = torch.randn((N, 576), generator=g).to(BF)
+    w = (1 + 0.3 * torch.randn(512, generator=g)).to(BF)
+    kv = torch.zeros((blocks, 64, 352), dtype=torch.uint8, device="cuda")
+    table = torch.arange(blocks, dtype=torch.int32, device="cuda").view(1, blocks)
+    mla.cache_append_fp4(rows[:, :512].cuda(), rows[:, 512:].cuda(), kv, kv_scale, table,
+                         torch.tensor([N], dtype=torch.int32, device="cuda"), norm_weight=w.cuda() if norm else None)
+    assert mla.get_device_status() == 0
+    x = to_np(rows)
+    if norm:
+        x = np.concatenate((oracle.normed_latent(x[:, :512], to_np(w), float(np.float32(1e-6))), x[:, 512:]), axis=1)
+    assert np.array_equal(kv.view(N, 352).cpu().numpy(), oracle.pack_fp4(x, kv_scale))
