@@ -17,8 +17,8 @@
 //     and accumulates O += P V, P^T and V both read by the MMA as they lie (tokens by rows: transposed operands).
 // Rows past 128 go to further pairs of the cluster, which walk the same pages.  A cluster is one part of the split schedule.
 //
-// Measured (GB300, 1.9 GHz; call with its merge, q and cache from HBM): 64 x 4096 tokens, 128 heads 84 us (867 TFLOP/s, 0.45 of a
-// library's bf16 product), 16 heads 74 us; 64 x 2 x 8192: 271 us (1078 TFLOP/s); 4 x 131072: 198 us; 64 lists of 2048 tokens: 82 us;
+// Measured (GB300, 1.9 GHz; call with its merge, q and cache from HBM): 64 x 4096 tokens, 128 heads 83.7 us (872 TFLOP/s, 0.45 of a
+// library's bf16 product), 16 heads 70 us; 64 x 2 x 8192: 268 us (1090 TFLOP/s); 4 x 131072: 196 us; 64 lists of 2048 tokens: 66 us;
 // 2 x 300 tokens, 16 heads: 16 us.  A tile takes a pair 4000 to 4300 cycles, of which S's MMAs are 2304 and O's 2048: what is between
 // are the waits of chains (keys converted -> MMA -> exponentials -> vote -> copy -> MMA) whose links take 100 to 300 cycles each however
 // little they do, with 20 warps on an SM that issue 0.57 of the time, and the O-CTA's shared memory (V written once and read by the MMAs
@@ -80,7 +80,8 @@ constexpr float kOffset = 6.f;                // P is taken against 2^-6 of the 
 constexpr float kTop = kOffset + 8.f;         // an exponent past this rebases its head
 constexpr uint32_t kTimeoutNs = 500u * 1000 * 1000;
 constexpr float kLn2 = 0.69314718055994530942f;
-// registers a thread: the three kinds of warpgroups share what the launch gets (640 x 96)
+// Registers a thread: the three kinds of warpgroups share what the launch gets (640 x 96).  No loop may spill: with 48 / 136 / 80, where a
+// converter spilled 4 to 30 bytes a thread, its loop was up to 25% slower (its fences to the other proxy seem to wait for these too).
 constexpr int kRegsMisc = 64, kRegsSoftmax = 120, kRegsConvert = 88;
 static_assert(128 * kRegsMisc + 256 * kRegsSoftmax + 256 * kRegsConvert <= kThreads * 96, "more would wait forever");
 
@@ -572,7 +573,7 @@ __device__ void find_rows(const Fp4Params& p, uint32_t smem, int part) {
       st_shared_s32(at + (lane + 32 * g) * 4, row >= 0 ? row : Sparse ? 0 : lane + 32 * g);
       if (!IsS && row >= 0) {
         const uint8_t* const src = reinterpret_cast<const uint8_t*>(p.kv) + static_cast<int64_t>(row) * kFp4RowBytes;
-        if constexpr (Sparse) {   // (a bulk prefetch a row took longer: 104 against 90 us for 64 x 2048 listed tokens)
+        if constexpr (Sparse) {   // (a bulk prefetch a row took longer: 104 against 90 us for 64 x 2048 listed tokens at that time)
 #pragma unroll
           for (int c = 0; c < kFp4RowBytes + 127; c += 128) prefetch_line(src + min(c, kFp4RowBytes - 1));
         } else if (lane == 0 && g == 0) {
@@ -589,7 +590,7 @@ __device__ void find_rows(const Fp4Params& p, uint32_t smem, int part) {
 // Warps 12..19: a thread a token; warpgroup c takes latent dims [256 c, 256 c + 256) and half of the rope dims.  Dense: a tile's
 // codes are read into registers at once, which frees the page buffers for the next tile's loads.  Lists: a thread loads its row from
 // global memory, every part as soon as the same part of the tile before has been converted (by copies of a row each into the page
-// buffers 64 x 2048 listed tokens took 122 us; now 82, 90 with loads of 16 bytes).
+// buffers 64 x 2048 listed tokens took 122 us; now 66).
 template <bool Sparse>
 __device__ void s_convert(const Fp4Params& p, Shared& sh, uint32_t smem, int part, int c) {
   const int quad = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
@@ -1371,8 +1372,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_fp4_kernel(const __gri
   tc_fence_after();
   griddep_wait();        // the metadata, q and the cache are complete from here on
 
-  // Each CTA's hot loops lie together: of 30 orders of these branches, 64 x 2 x 8192 took from 273 to 340 us, best with the S-CTA's three
-  // roles side by side and the O-CTA's conversion next to its MMAs (the roles of an SM share its instruction caches).
+  // Each CTA's hot loops lie together (the roles of an SM share its instruction caches): of eight orders of these branches, 64 x 2 x 8192
+  // took from 267 to 276 us, 16 heads of 64 x 4096 70 to 75.
   const bool lane0 = (threadIdx.x & 31) == 0;
   if (is_s && warp >= 12) {
     regs_down<kRegsConvert>();
