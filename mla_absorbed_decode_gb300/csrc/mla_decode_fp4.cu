@@ -62,9 +62,10 @@ constexpr uint32_t kVChunk = 64 * 128;        // 64 dims of a page's values
 constexpr int kVSlots = 4;                    // half pages (64 tokens x 256 dims) of converted values
 constexpr uint32_t kVSlot = 4 * kVChunk;
 // converted keys of a tile, in the order of their MMAs: latent chunks (128 tokens x 64 dims, 32 TMEM columns) in pairs, one from
-// each converting warpgroup, and the rope chunk in the middle.  The pairs have slots of their own; the rope chunk goes where the
-// first pair's first chunk was, which is done with by then, as the rope chunk is when the next tile's first pair comes.
-constexpr int kItems = 5, kRopeItem = 2;
+// each converting warpgroup, and the rope chunk before the last pair.  The pairs have slots of their own; the rope chunk goes where the
+// first pair's first chunk was, which is done with by the time that it is converted, as the rope chunk is when the next tile's first
+// pair comes (a pair earlier the converters waited for the one, 83.7 us instead of 81.4; at the end for the other with 16 heads).
+constexpr int kItems = 5, kRopeItem = 3;
 // a packet: what one softmax warpgroup (half of the row block's heads) sends to the O-CTA for a tile
 constexpr uint32_t kPktAlpha = 128 * 128;     // after P^T (128 tokens x 64 heads): float[64], factors of a rebase
 constexpr uint32_t kPktFlag = kPktAlpha + 256;   // whether alpha counts
@@ -498,10 +499,10 @@ struct Block {
 };
 
 // ------------------------------------------------------------------ S-CTA --
-// Where q's 64 dims `c` lie: the warpgroups' chunks (c < 4, and from 4 on) in turn, the rope dims between the second pair and the third.
+// Where q's 64 dims `c` lie: the warpgroups' chunks (c < 4, and from 4 on) in turn, the rope dims before the last pair.
 __device__ __forceinline__ int q_place(int c) {
   const int k = c & 3, at = 2 * k + (c >> 2);
-  return c == 8 ? 4 : at < 4 ? at : at + 1;
+  return c == 8 ? 2 * kRopeItem : at < 2 * kRopeItem ? at : at + 1;
 }
 
 // Warp 0, dense: the two pages of every tile, a copy a page as far as the request has tokens (in 16 copies, with
@@ -657,7 +658,7 @@ __device__ void s_convert(const Fp4Params& p, Shared& sh, uint32_t smem, int par
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const uint32_t item = k < 2 ? k : k + 1;
+      const uint32_t item = k < kRopeItem ? k : k + 1;
       const uint32_t empty = AT(k_empty) + 8 * (k > 0 ? item : kRopeItem);   // (the first pair's slots had the rope chunk last)
       const uint32_t sk = k == 0 ? sc.x : k == 1 ? sc.y : k == 2 ? sc.z : sc.w;
       const uint32_t s01 = e4m3x2_to_f16x2<0>(sk), s23 = e4m3x2_to_f16x2<1>(sk);
@@ -686,7 +687,7 @@ __device__ void s_convert(const Fp4Params& p, Shared& sh, uint32_t smem, int par
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(AT(k_full) + 8 * item);
-      if (k == 1) {
+      if (k == kRopeItem - 1) {
         const uint32_t x[8] = {rope[0].x, rope[0].y, rope[0].z, rope[0].w, rope[1].x, rope[1].y, rope[1].z, rope[1].w};
         uint32_t u[16];
 #pragma unroll
@@ -740,7 +741,7 @@ __device__ void s_mma(const Fp4Params& p, const CUtensorMap* q_map, Shared& sh, 
         tc_fence_after();
         const uint32_t bar = AT(k_empty) + 8 * it;
         if (it == kRopeItem) {
-          mma4_ts(d, tmem + kKCol, q0 + 4 * (kQChunk >> 4), idesc, 1u, bar);
+          mma4_ts(d, tmem + kKCol, q0 + 2 * kRopeItem * (kQChunk >> 4), idesc, 1u, bar);
         } else {
           const uint32_t pair = it > kRopeItem ? it - 1 : it, at = it > kRopeItem ? 2 * it - 1 : 2 * it;
           mma8_ts(d, tmem + kKCol + pair * 64, q0 + at * (kQChunk >> 4), idesc, it, bar);
