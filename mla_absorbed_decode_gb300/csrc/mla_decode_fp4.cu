@@ -17,12 +17,12 @@
 //     and accumulates O += P V, P^T and V both read by the MMA as they lie (tokens by rows: transposed operands).
 // Rows past 128 go to further pairs of the cluster, which walk the same pages.  A cluster is one part of the split schedule.
 //
-// Measured (GB300, 1.9 GHz; call with its merge, q and cache from HBM): 64 x 4096 tokens, 128 heads 83.7 us (872 TFLOP/s, 0.45 of a
-// library's bf16 product), 16 heads 70 us; 64 x 2 x 8192: 268 us (1090 TFLOP/s); 4 x 131072: 196 us; 64 lists of 2048 tokens: 66 us;
-// 2 x 300 tokens, 16 heads: 16 us.  A tile takes a pair 4000 to 4300 cycles, of which S's MMAs are 2304 and O's 2048: what is between
-// are the waits of chains (keys converted -> MMA -> exponentials -> vote -> copy -> MMA) whose links take 100 to 300 cycles each however
-// little they do, with 20 warps on an SM that issue 0.57 of the time, and the O-CTA's shared memory (V written once and read by the MMAs
-// with P: 2800 of the 4000 cycles at 128 bytes each).
+// Measured (GB300, 1.9 GHz; call with its merge, q and cache from HBM): 64 x 4096 tokens, 128 heads 81.6 us (895 TFLOP/s, 0.46 of a
+// library's bf16 product), 16 heads 70 us; 64 x 2 x 8192: 263 us (1110 TFLOP/s); 4 x 131072: 194 us; 64 lists of 2048 tokens: 65 us;
+// 2 x 300 tokens, 16 heads: 16 us.  A tile takes a pair 3800 cycles, of which S's MMAs are 2304 and O's 2048: what is between are the
+// waits of chains (keys converted -> MMA -> exponentials -> vote -> copy -> MMA) whose links take 100 to 300 cycles each however little
+// they do, with 20 warps on an SM that issue 0.57 of the time; TMEM, where MMAs without gaps hold up the others' loads and stores; and the
+// O-CTA's shared memory (V written once and read by the MMAs with P: 2800 cycles at 128 bytes each).
 //
 // The softmax is online, with the reference maximum of a head raised only where a score passes it by 2^8: the threads take the
 // exponentials against the old reference, and a vote (the barrier that ends a tile) tells whether one overflowed its room;
