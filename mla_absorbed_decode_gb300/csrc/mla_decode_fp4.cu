@@ -12,7 +12,8 @@
 //     a token) and never through shared memory, whose bandwidth the operands need; Q is the B operand, in
 //     shared memory for a whole segment.  An MMA is as wide as there are heads (rounded up to 16), so few heads cost little.
 //     S^T is read with four tokens and 16 heads in a thread, which keeps the heads' references and sums in registers;
-//     each softmax warp sends its 32 tokens of P^T to the partner with one shared-to-shared bulk copy a tile;
+//     each softmax warp sends its 32 tokens of P^T to the partner with one shared-to-shared bulk copy a tile, and overwrites them
+//     once the partner has told its warpgroup that they have landed;
 //   * the O-CTA (odd rank) converts the latent part of the pages into shared memory (from L2, where its row finder has them brought)
 //     and accumulates O += P V, P^T and V both read by the MMA as they lie (tokens by rows: transposed operands).
 // Rows past 128 go to further pairs of the cluster, which walk the same pages.  A cluster is one part of the split schedule.
@@ -109,8 +110,10 @@ struct Shared {
   uint64_t s_full[2], s_empty[2];
   uint64_t q_raw, q_full, q_empty;            // the segment's q has landed; is fp16 (a softmax warp each); is done with
   uint64_t credit[2];                         // the partner's receive slot is free (remote)
+  uint64_t sent[2];                           // a warpgroup's last packet has landed, and may be overwritten here (remote)
   // O-CTA
-  uint64_t p_full[2], p_free[2];
+  uint64_t p_full[2][2];                      // a slot's packet of a warpgroup has landed
+  uint64_t p_free[2];
   uint64_t rows_full[kRowSlots], rows_empty[kRowSlots];   // (lists: the S-CTA's too)
   uint64_t v_full[kVSlots], v_empty[kVSlots];
   uint64_t o_full, o_free, o_sync, corr_go, corr_done;
@@ -821,7 +824,7 @@ __device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int par
   const int units = blk.half >> 3;                // of 8 heads
   const uint32_t tm = sh.tmem_base + (static_cast<uint32_t>(wq * 32) << 16) + w * blk.half;
   const uint32_t pkt = smem + kOffSend + w * kPktStride, dst = map_to_rank(smem + w * kPktStride, peer);
-  const uint32_t full = map_to_rank(AT(p_full), peer);
+  const uint32_t full = map_to_rank(AT(p_full) + 8 * w, peer);
   // stmatrix: lane 8 m + r has row r of matrix m: unit m / 2 of a pair, rows 8 (m % 2) + r of 16
   const uint32_t st = pkt + (32 * wq + 8 * ((lane >> 3) & 1) + (lane & 7)) * 128, st_unit = (lane >> 4) ^ (lane & 7);
   SegmentWalker walk;
@@ -858,7 +861,6 @@ __device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int par
         const int tok = 32 * wq + lane, e = k * kPageTokens + tok;
         if (tok < ntok) key = !Sparse ? e : e < p.idx_stride ? __ldg(p.indices + static_cast<int64_t>(s.b) * p.idx_stride + e) : -1;
       }
-      if (lane == 0) bulk_wait_group_read<0>();   // the warp's part of the last packet has been read
       bool leave = !wait_done(smem, AT(s_full) + 8 * sb, (T >> 1) & 1);
       __syncwarp();
       tc_fence_after();
@@ -900,6 +902,10 @@ __device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int par
                 ls[i] = add2(ls[i], y);
                 pk[q] = pack_f16x2(y.x, y.y);
               }
+              if (hf == 0 && ii == 0) {   // the warpgroup's last packet has landed (waited for behind more exponentials: no gain)
+                leave |= !wait_done(smem, AT(sent) + 8 * w, (T & 1) ^ 1);
+                __syncwarp();
+              }
               stmatrix4(st + hf * (16 * 128) + (((2 * ii) ^ st_unit) << 4), pk[0], pk[1], pk[2], pk[3]);
             }
           }
@@ -938,6 +944,7 @@ __device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int par
             if (tr == 0) *reinterpret_cast<float2*>(&sh.part[w][wq][8 * (i0 + u) + 2 * tc]) = cm[u];
         }
         named_bar_sync(bar, 128);
+        leave |= !wait_done(smem, AT(sent) + 8 * w, (T & 1) ^ 1);   // (the factors below go into the packet too)
         if (t < blk.half) {   // a thread a head: its new reference, and what it makes of the sums so far
           const float m = fmaxf(fmaxf(sh.part[w][0][t], sh.part[w][1][t]), fmaxf(sh.part[w][2][t], sh.part[w][3][t])) *
                           sh.q_scale[w * blk.half + t];
@@ -964,8 +971,7 @@ __device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int par
       if (lane == 0) {
         mbar_arrive(AT(s_empty) + 8 * sb);   // S^T has been read
         // the warp's 32 tokens to the partner, the last warp's with the factors behind them
-        bulk_copy_to_cluster(dst + sb * 2 * kPktStride + wq * 4096, pkt + wq * 4096, wq == 3 ? kPktBytes - 3 * 4096 : 4096, full + 8 * sb);
-        bulk_commit_group();
+        bulk_copy_to_cluster(dst + sb * 2 * kPktStride + wq * 4096, pkt + wq * 4096, wq == 3 ? kPktBytes - 3 * 4096 : 4096, full + 16 * sb);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) l[i] = add2(l[i], ls[i]);
@@ -997,8 +1003,7 @@ __device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int par
     }
   }
 out:
-  if (lane == 0) bulk_wait_group<0>();   // copies land before the CTA may leave
-  __syncwarp();
+  __syncwarp();   // (the partner, which stays until what is on its way has landed, has this CTA stay as well)
 }
 
 // ------------------------------------------------------------------ O-CTA --
@@ -1083,17 +1088,21 @@ __device__ void o_mma(const Fp4Params& p, Shared& sh, uint32_t smem, int part) {
   const uint32_t tmem = uniform(sh.tmem_base);
   constexpr uint32_t idesc = idesc_f16_f32(128, 256, 1, 1);
   const uint64_t v0 = smem_desc_sw128(smem + kOffV, kVChunk, 1024);
+  // A packet is expected from when the one before it in its slot has come: it completes `p_full` whatever these MMAs are at.
+  if (lane < 4) mbar_arrive_expect_tx(AT(p_full) + 8 * lane, kPktBytes);
+  __syncwarp();
   while (w.next(s)) {
     if (seg > 0) warp_wait(smem, AT(o_free), (seg - 1) & 1);
 #pragma unroll 1
     for (int k = s.kb; k < s.ke; k += 2, ++T) {
-      const uint32_t slot = T & 1, pkt = smem + slot * 2 * kPktStride, full = AT(p_full) + 8 * slot;
+      const uint32_t slot = T & 1, pkt = smem + slot * 2 * kPktStride, full = AT(p_full) + 16 * slot;
       const bool last = k + 2 >= s.ke;
       const int ntok = tile_tokens(p, s, k);
-      if (lane == 0) mbar_arrive_expect_tx(full, 2 * kPktBytes);
-      __syncwarp();
       warp_wait(smem, full, (T >> 1) & 1);
+      warp_wait(smem, full + 8, (T >> 1) & 1);
       if (warp_told_to_leave(smem)) goto out;
+      if (lane < 2) mbar_arrive_expect_tx(full + 8 * lane, kPktBytes);
+      __syncwarp();
       if (k != s.kb && (ld_shared_s32(pkt + kPktFlag) | ld_shared_s32(pkt + kPktStride + kPktFlag))) {   // scale O before adding
         mma_commit_warp(AT(o_sync));
         warp_wait(smem, AT(o_sync), nresc & 1);
@@ -1141,6 +1150,11 @@ __device__ void o_mma(const Fp4Params& p, Shared& sh, uint32_t smem, int part) {
 out:
   mma_commit_warp(AT(drain));   // behind everything issued
   drain_bar(AT(drain), 0);
+  if (warp_told_to_leave(smem)) {   // packets of this tile and the next may be on their way (part of them, which costs the limit)
+    const uint32_t t0 = timer_lo();
+    for (uint32_t j = 2 * T; j < 2 * T + 4; ++j)
+      while (!mbar_test(AT(p_full) + 8 * (j & 3), (j >> 2) & 1) && timer_lo() - t0 <= kTimeoutNs) {}
+  }
   __syncwarp();
   if (lane == 0) {
     sh.cmd = 3;
@@ -1149,20 +1163,23 @@ out:
   }
 }
 
-// A lane of warp 2: gives packet slots back to the S-CTA once the MMAs are done with them.
+// A lane of warp 2: tells the S-CTA's warpgroups that their packets have landed (a copy to another CTA's shared memory is known to be
+// done by that CTA's barrier alone: no bulk group of the sender's counts it), and gives slots back once the MMAs are done with them.
+// It polls: one after the other a warpgroup would wait for the other's packet too (64 x 4096: 91.4 against 84.0 us), and its arrivals say
+// that something has been read and release nothing to the cluster (with such releases 97 against 91.9 us).
 __device__ void o_forward(const Fp4Params& p, uint32_t smem, int part, uint32_t peer) {
   SegmentWalker w;
   w.init(p, part);
   Segment s;
-  uint32_t T = 0;
-  const uint32_t credit = map_to_rank(AT(credit), peer);
-  while (w.next(s))
-#pragma unroll 1
-    for (int t = tiles_of(s); t > 0; --t, ++T) {
-      wait(smem, AT(p_free) + 8 * (T & 1), (T >> 1) & 1);
-      if (told_to_leave(smem)) return;
-      mbar_arrive_remote(credit + (T & 1) * 8);
-    }
+  uint32_t tiles = 0, n0 = 0, n1 = 0, nf = 0;   // tiles in all; landed packets of either warpgroup and free slots told of
+  while (w.next(s)) tiles += tiles_of(s);
+  const uint32_t sent = map_to_rank(AT(sent), peer), credit = map_to_rank(AT(credit), peer);
+  while (n0 < tiles || n1 < tiles || nf < tiles) {
+    if (n0 < tiles && mbar_poll(AT(p_full) + 16 * (n0 & 1), (n0 >> 1) & 1)) mbar_arrive_other(sent), ++n0;
+    if (n1 < tiles && mbar_poll(AT(p_full) + 16 * (n1 & 1) + 8, (n1 >> 1) & 1)) mbar_arrive_other(sent + 8), ++n1;
+    if (nf < tiles && mbar_poll(AT(p_free) + 8 * (nf & 1), (nf >> 1) & 1)) mbar_arrive_other(credit + 8 * (nf & 1)), ++nf;
+    if (told_to_leave(smem)) return;
+  }
 }
 
 // A lane of warp 3: the pair's limit on waiting.  No tile's MMAs for kTimeoutNs (every role's progress is needed for one), or the S-CTA's
@@ -1336,7 +1353,9 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_fp4_kernel(const __gri
       init(sh.s_full[i], 1);
       init(sh.s_empty[i], 8);
       init(sh.credit[i], 1);
-      init(sh.p_full[i], 1);
+      init(sh.sent[i], 1);
+      init(sh.p_full[i][0], 1);
+      init(sh.p_full[i][1], 1);
       init(sh.p_free[i], 1);
     }
     for (int i = 0; i < kItems; ++i) {

@@ -172,13 +172,6 @@ __device__ __noinline__ void w_drain(uint64_t& bar, uint32_t parity, uint64_t un
     if (global_timer_ns() > until) return;
 }
 
-// Arrival in another CTA that releases nothing beyond this CTA: it says that something has been read.  A release to
-// the cluster would wait for what the thread or its warp has on its way to L2 (over a microsecond: a page's sums
-// set the period with it, 145 us for two query positions over 8192 tokens; a request's q came back 5 us late).
-__device__ __forceinline__ void mbar_arrive_other(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_bar) : "memory");
-}
-
 // --------------------------------------------------------------- the walk --
 __device__ __forceinline__ int length_of(const WeightsParams& p, int b) {   // 0 where it is out of range
   const int n = __ldg(p.seqlens + b);

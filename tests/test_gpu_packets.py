@@ -1,0 +1,71 @@
+"""Decodes whose pairs hand over many tiles, while other work keeps the GPU's memory and shared memory busy: every run gives the bits
+of the first, whichever cache is read."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from mla_absorbed_decode_gb300 import build_lib
+    build_lib.build()
+    yield
+
+
+def _cache(kind, blocks, g):
+    if kind == "bf16":
+        return torch.randn((blocks, 64, 576), generator=g, device="cuda").to(BF)
+    if kind == "fp8":
+        return (torch.randn((blocks, 64, 576), generator=g, device="cuda") * 64).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    kv = torch.randint(0, 256, (blocks, 64, 352), generator=g, device="cuda", dtype=torch.uint8)
+    kv[..., 256:] &= 0xB7                                                 # no NaN, scales and rope codes below 1
+    return kv
+
+
+@pytest.mark.parametrize("kind", ["fp4"])
+@pytest.mark.parametrize("H,s_q", [(128, 1), (16, 1), (128, 2)])
+@pytest.mark.parametrize("lists", [False, True])
+def test_equal_bits_beside_other_work(kind, H, s_q, lists):
+    import mla_absorbed_decode_gb300 as mla
+    g = torch.Generator(device="cuda").manual_seed(H + s_q)
+    lens = [5000, 64, 2900, 129, 8192, 1, 700, 3333] * 4
+    B, pages = len(lens), 128
+    table = torch.randperm(B * pages, generator=g, device="cuda").to(torch.int32).view(B, pages)
+    kv = _cache(kind, B * pages, g)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q = torch.randn((B, s_q, H, 576), generator=g, device="cuda").to(BF)
+    scale = () if kind == "bf16" else (2.0 ** -6 if kind == "fp8" else 0.5,)
+    P = mla.num_sm_parts(s_q, H)
+    more = ()
+    if lists:
+        k = n.clamp(max=1500)
+        idx = torch.stack([(torch.rand(1500, generator=g, device="cuda") * m).int() for m in lens])
+        more = (idx, k)
+    meta = mla.decode_metadata(more[1] if lists else n, s_q, H, s_q > 1, P)
+    call = getattr(mla, "decode" + ("_sparse" if lists else "") + ("" if kind == "bf16" else "_" + kind))
+    run = lambda: call(q, kv, *scale, table, n, *more, 192 ** -0.5, s_q > 1, meta, P)
+    want = [t.clone() for t in run()]
+    assert mla.get_device_status() == 0 and not want[0].isnan().any()
+    side = torch.cuda.Stream()
+    a, b = torch.empty(1 << 28, dtype=torch.uint8, device="cuda"), torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    m = torch.randn((2048, 2048), device="cuda").to(BF)
+    torch.cuda.synchronize()
+    got = []
+    for i in range(40):
+        with torch.cuda.stream(side):
+            if i % 2:
+                b.copy_(a)
+            else:
+                torch.matmul(m, m)
+        out, lse = run()
+        got.append((out, lse))
+        if len(got) == 8:
+            torch.cuda.synchronize()
+            assert all(torch.equal(o, want[0]) and torch.equal(l, want[1]) for o, l in got), i
+            got = []
+    assert mla.get_device_status() == 0
