@@ -133,6 +133,7 @@ struct Bars {
   uint64_t s_empty[2];      // S-CTA: S read by the softmax warps (8 arrivals)
   uint64_t q_full;          // S-CTA: Q of the segment stored in TMEM
   uint64_t credit[kSlots];  // S-CTA: the partner's receive slot is free (remote arrival)
+  uint64_t sent[2];         // S-CTA: the packet of a staging slot has landed (remote arrival)
   uint64_t p_full[kSlots];  // O-CTA: packet bytes arrived (bulk copy from the partner)
   uint64_t p_free[kSlots];  // O-CTA: PV MMAs that read a packet slot are done
   uint64_t o_full;          // O-CTA: the segment's last PV MMAs are done
@@ -919,13 +920,14 @@ __device__ void s_cta_softmax(const DecodeParams& p, Shared& sh, uint32_t smem, 
     for (int k = s.kb; k < s.ke; ++k, ++T) {
       const uint32_t sb = T & 1, ph = (T >> 1) & 1;
       const uint32_t rs = T % kSlots, rph = (T / kSlots) & 1;
-      // S of this page; thread 0 also makes sure that staging slot sb is free (the bulk
-      // copy that used it two pages ago has read it) and that the partner's receive
+      // S of this page; thread 0 also makes sure that staging slot sb is free (the packet
+      // sent from it two pages ago has landed: no bulk group of the sender's counts a copy to
+      // another CTA, only that CTA's barrier does) and that the partner's receive
       // slot rs is free (its PV of the page that used it, kSlots pages ago, is done).
       bool ok_t = wait_bar(sh, smem_u32(&sh.bar.s_full[sb]), ph, p.status, cl);
       if (t == 0 && ok_t) {
-        bulk_wait_group_read<1>();
-        ok_t = wait_bar(sh, smem_u32(&sh.bar.credit[rs]), rph ^ 1, p.status, cl, true);
+        ok_t = wait_bar(sh, smem_u32(&sh.bar.sent[sb]), ph ^ 1, p.status, cl, true) &&
+               wait_bar(sh, smem_u32(&sh.bar.credit[rs]), rph ^ 1, p.status, cl, true);
       }
       tc_fence_after();
       float sv[32];
@@ -1039,10 +1041,7 @@ __device__ void s_cta_softmax(const DecodeParams& p, Shared& sh, uint32_t smem, 
       }
       fence_proxy_async_smem();
       named_bar_sync(1, kST);
-      if (t == 0) {
-        bulk_copy_to_cluster(peer_recv + rs * kPktStride, slot, kPktStride, peer_pfull0 + rs * 8);
-        bulk_commit_group();
-      }
+      if (t == 0) bulk_copy_to_cluster(peer_recv + rs * kPktStride, slot, kPktStride, peer_pfull0 + rs * 8);
     }
     if (!ok) break;
     if (row_valid && wg == 0) {
@@ -1055,7 +1054,6 @@ __device__ void s_cta_softmax(const DecodeParams& p, Shared& sh, uint32_t smem, 
         p.lse_part[static_cast<int64_t>(ns0 + s.split) * p.rows + g] = lse;
     }
   }
-  if (t == 0) bulk_wait_group<0>();   // copies land before the CTA may exit
 }
 
 // ------------------------------------------------------------------ O-CTA --
@@ -1075,6 +1073,9 @@ __device__ void o_cta_mma(const DecodeParams& p, Shared& sh, uint32_t smem, int 
   const uint32_t tmem = sh.tmem_base;
   constexpr uint32_t idesc = F8 ? idesc_e4m3_f32(128, 256, 0, 1) : idesc_bf16_f32(128, 256, 0, 1);
   bool ok = true, any = false;
+  // a slot's packet is expected from when the one before it has come, so that it completes p_full wherever these MMAs are
+  if (lane < kSlots) mbar_arrive_expect_tx(smem_u32(&sh.bar.p_full[lane]), kPktStride);
+  __syncwarp();
   while (ok && w.next(s)) {
     if (seg > 0 && !warp_wait(sh, smem_u32(&sh.bar.o_free), (seg - 1) & 1, p.status, cl)) break;
     const int L = __ldg(p.lens + s.b);
@@ -1083,10 +1084,10 @@ __device__ void o_cta_mma(const DecodeParams& p, Shared& sh, uint32_t smem, int 
       const uint32_t ps = T % kSlots, pph = (T / kSlots) & 1;
       const uint32_t vstage = smem + C::kOffStage + st * C::kVStageBytes;
       const uint32_t pkt = smem + C::kOffRecv + ps * kPktStride;
-      if (lane == 0) mbar_arrive_expect_tx(smem_u32(&sh.bar.p_full[ps]), kPktStride);
-      __syncwarp();
       if (!warp_wait(sh, smem_u32(&sh.bar.full[st]), ph, p.status, cl)) { ok = false; break; }
       if (!warp_wait(sh, smem_u32(&sh.bar.p_full[ps]), pph, p.status, cl, true)) { ok = false; break; }
+      if (lane == 0) mbar_arrive_expect_tx(smem_u32(&sh.bar.p_full[ps]), kPktStride);
+      __syncwarp();
       // tail page: zero the value rows past the sequence end up to the next MMA-step
       // boundary, so that P = 0 never meets a non-finite value in the MMA (per half)
       const int nvalid = min(64, L - k * 64);
@@ -1169,6 +1170,12 @@ __device__ void o_cta_mma(const DecodeParams& p, Shared& sh, uint32_t smem, int 
     mma_commit_warp(smem_u32(&sh.bar.drain));
     drain_bar(smem_u32(&sh.bar.drain), 0);
   }
+  // a call that gives up: packets that are on their way land before the CTAs may leave (one that was not sent costs the limit)
+  if (!ok || sh.abort) {
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t j = 0; j < kSlots; ++j)
+      while (!mbar_test(smem_u32(&sh.bar.p_full[(T + j) % kSlots]), ((T + j) / kSlots) & 1) && global_timer_ns() - t0 <= kTimeoutNs) {}
+  }
   __syncwarp();
   if (lane == 0) {
     sh.cmd = 3;
@@ -1177,17 +1184,21 @@ __device__ void o_cta_mma(const DecodeParams& p, Shared& sh, uint32_t smem, int 
   __syncwarp();
 }
 
-// Warp 2 of the O-CTA: returns each packet slot to the S-CTA once the MMAs reading it are done.
+// Warp 2 of the O-CTA: tells the S-CTA that a packet has landed, and returns each packet slot once the MMAs reading it are done
+// (page T's packet, then page T - 1's slot, which page T + 3 takes).
 __device__ void o_cta_forwarder(const DecodeParams& p, Shared& sh, int part, uint32_t cl, uint32_t peer) {
   SegmentWalker w;
   w.init(p, part);
   Segment s;
   uint32_t T = 0;
-  const uint32_t credit0 = map_to_rank(smem_u32(&sh.bar.credit[0]), peer);
+  const uint32_t credit0 = map_to_rank(smem_u32(&sh.bar.credit[0]), peer), sent0 = map_to_rank(smem_u32(&sh.bar.sent[0]), peer);
   bool ok = true;
   while (ok && w.next(s)) {
     for (int k = s.kb; k < s.ke; ++k, ++T) {
-      const uint32_t ps = T % kSlots, pph = (T / kSlots) & 1;
+      if (!wait_bar(sh, smem_u32(&sh.bar.p_full[T % kSlots]), (T / kSlots) & 1, p.status, cl, true)) { ok = false; break; }
+      mbar_arrive_other(sent0 + (T & 1) * 8);
+      if (T == 0) continue;
+      const uint32_t ps = (T - 1) % kSlots, pph = ((T - 1) / kSlots) & 1;
       if (!wait_bar(sh, smem_u32(&sh.bar.p_free[ps]), pph, p.status, cl)) { ok = false; break; }
       mbar_arrive_remote(credit0 + ps * 8);
     }
@@ -1374,6 +1385,7 @@ mla_decode_kernel(const __grid_constant__ KvMaps maps, const DecodeParams p) {
       mbar_init(smem_u32(&sh.bar.empty_b[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sh.bar.sent[i]), 1);
       mbar_init(smem_u32(&sh.bar.s_full[i]), 1);
       mbar_init(smem_u32(&sh.bar.s_empty[i]), kGroupWarps);   // one arrival per softmax warp
     }

@@ -27,7 +27,7 @@ def _cache(kind, blocks, g):
     return kv
 
 
-@pytest.mark.parametrize("kind", ["fp4"])
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "fp4"])
 @pytest.mark.parametrize("H,s_q", [(128, 1), (16, 1), (128, 2)])
 @pytest.mark.parametrize("lists", [False, True])
 def test_equal_bits_beside_other_work(kind, H, s_q, lists):
