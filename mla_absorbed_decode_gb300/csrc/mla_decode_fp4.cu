@@ -43,6 +43,7 @@
 #include <cudaTypedefs.h>
 #include <stdint.h>
 
+#include <cfloat>
 #include <climits>
 #include <cstddef>
 #include <cmath>
@@ -796,7 +797,7 @@ __device__ __forceinline__ void s_scale_q(const Fp4Params& p, Shared& sh, uint32
     for (int g = 0; g < 4; ++g) {
       uint32_t top = largest(largest(mine == g ? rope_top : 0u, v[g][0]), v[g][1]);
       top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
-      e[g] = max(top >> 7, 41u);   // the exponent: a factor of 2^100 at most
+      e[g] = max(top >> 7, 15u);   // the exponent: a factor of 2^126 at most, whose inverse is a normal number
       if (mine == g) rope_e = e[g];
     }
     __syncwarp();
@@ -805,8 +806,11 @@ __device__ __forceinline__ void s_scale_q(const Fp4Params& p, Shared& sh, uint32
       if (j + 4 * g >= blk.half) break;
 #pragma unroll
       for (int u = 0; u < 2; ++u) st_shared_v4(place(g, (lane >> 3) + 4 * u), scaled(v[g][u], e[g]));
-      // (the factor is never 0, so that scores of -inf stay what they are)
-      if (lane == 0) sh.q_scale[w * blk.half + j + 4 * g] = fmaxf(unit * __uint_as_float((min(e[g], 141u) - 14u) << 23), 0x1p-126f);
+      // what `scaled` took out of the row, into its scores (never 0 or infinite, so that scores of -inf and 0 stay what they are)
+      if (lane == 0) {
+        const float back = __uint_as_float(((e[g] < 255u ? e[g] : 141u) - 14u) << 23);
+        sh.q_scale[w * blk.half + j + 4 * g] = fminf(fmaxf(unit * back, 0x1p-126f), FLT_MAX);
+      }
     }
     if (j + 4 * mine < blk.half) st_shared_v4(place(mine, 8), scaled(rope, rope_e));
   }

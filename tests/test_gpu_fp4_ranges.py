@@ -1,0 +1,51 @@
+"""The calls on a 4-bit latent cache at the ends of what their arguments allow, against the float64 oracle: large and small
+queries, scales and rows, infinities, positions far out, NaN where a query position does not look.
+
+Tolerances are those of test_gpu_fp4 where nothing else is said: they are relative to sum |q_d k_d| and to the values, so
+powers of two on q, on the cache and on the scales leave them as they are.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import test_gpu_fp4 as base
+from test_gpu_fp4 import SCALE, _case, _compare, _ref, _run
+
+from _harness import to_np
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from mla_absorbed_decode_gb300 import build_lib
+    build_lib.build()
+    yield
+
+
+@pytest.fixture
+def softmax_scale(monkeypatch):
+    """Sets the softmax scale of test_gpu_fp4's calls, oracle and tolerances."""
+    return lambda scale: monkeypatch.setattr(base, "SCALE", scale)
+
+
+# -------------------------------------------------------------------------------------- queries --
+@pytest.mark.parametrize("factor", [2.0 ** 13, 2.0 ** 15, 2.0 ** 40, 2.0 ** 100, 2.0 ** -40, 2.0 ** -110])
+@pytest.mark.parametrize("s_q,H,topk", [(1, 128, None), (2, 24, None), (1, 128, [300, 129]), (2, 24, [300, 129])])
+def test_queries_of_any_size(s_q, H, topk, factor, softmax_scale):
+    """Rows of q far from size one, with a softmax scale that brings their scores back to it; every third head stays as it is."""
+    inp = _case([333, 190], s_q=s_q, H=H, topk=topk, seed=71, kv_scale=2.0 ** -6)
+    scaled = torch.arange(H) % 3 != 1
+    inp["q"][:, :, scaled] *= factor
+    if factor > 1:
+        assert float(inp["q"].float().abs().max()) >= 2.0 ** 15
+    else:                   # (the others' scores would pass float32's range)
+        inp["q"][:, :, ~scaled] *= factor
+    softmax_scale(SCALE / factor)
+    for parts in (1, 5):
+        _compare(inp, _run(inp, parts), _ref(inp), f"factor={factor} parts={parts}")
