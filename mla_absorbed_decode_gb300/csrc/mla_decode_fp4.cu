@@ -950,8 +950,9 @@ __device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int par
         named_bar_sync(bar, 128);
         leave |= !wait_done(smem, AT(sent) + 8 * w, (T & 1) ^ 1);   // (the factors below go into the packet too)
         if (t < blk.half) {   // a thread a head: its new reference, and what it makes of the sums so far
-          const float m = fmaxf(fmaxf(sh.part[w][0][t], sh.part[w][1][t]), fmaxf(sh.part[w][2][t], sh.part[w][3][t])) *
-                          sh.q_scale[w * blk.half + t];
+          float m = fmaxf(fmaxf(sh.part[w][0][t], sh.part[w][1][t]), fmaxf(sh.part[w][2][t], sh.part[w][3][t])) *
+                    sh.q_scale[w * blk.half + t];
+          if (m > FLT_MAX) m = FLT_MAX;   // a score past float32's range: its exponential is infinite, and the row NaN (not empty)
           const float old = sh.ref[w][t];
           float alpha = 1.f;
           if (old == -INFINITY ? m > -INFINITY : m + old > kTop) {

@@ -49,3 +49,19 @@ def test_queries_of_any_size(s_q, H, topk, factor, softmax_scale):
     softmax_scale(SCALE / factor)
     for parts in (1, 5):
         _compare(inp, _run(inp, parts), _ref(inp), f"factor={factor} parts={parts}")
+
+
+@pytest.mark.parametrize("topk", [None, [300, 64]])
+def test_scores_past_float32_are_not_empty_rows(topk, softmax_scale):
+    """Scores of some 1e39: NaN, as from an fp32 softmax, and not the 0 and -inf of a row that sees nothing.  Rows of zeros
+    (scores of 0) keep their result."""
+    inp = _case([400, 64], H=32, topk=topk, seed=72)
+    inp["q"][:, :, 3] = 0.0
+    softmax_scale(1e38)
+    want = _ref(dict(inp, q=inp["q"][:, :, 3:4].contiguous()))
+    for parts in (1, 4):
+        out, lse = _run(inp, parts)
+        rest = [h for h in range(32) if h != 3]
+        assert torch.all(out[:, :, rest].isnan()), parts
+        assert torch.all(lse[:, :, rest].isnan() | lse[:, :, rest].isposinf()), parts
+        _compare(dict(inp, q=inp["q"][:, :, 3:4]), (out[:, :, 3:4], lse[:, :, 3:4]), want, f"parts={parts}")
