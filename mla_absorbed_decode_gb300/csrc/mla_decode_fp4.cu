@@ -101,6 +101,7 @@ static_assert(kOffRows + kRowSlots * kRowBytes <= kOffShared, "O-CTA layout");
 constexpr uint32_t kDone = 0xffffffffu;
 
 struct Fp4Params : DecodeParams {
+  float unit;  // softmax_scale * kv_scale * log2(e): log2 units of a score of codes (scale_log2 alone may pass float32's range)
   int q_box;   // q rows of a TMA box
 };
 
@@ -766,7 +767,6 @@ out:
 // segment's first MMA waits for it: 9000 cycles for 128 rows one by one): of each 32 bytes a lane for the latent dims, of the four
 // RoPE parts 16 bytes a lane.  The largest element is found in the bits, whose order is that of the absolute values (a NaN's the highest).
 __device__ __forceinline__ void s_scale_q(const Fp4Params& p, Shared& sh, uint32_t smem, const Block& blk, int w, int wq, int lane) {
-  const float unit = p.scale_log2 * p.kv_scale;
 #pragma unroll 1
   for (int j = wq; j < blk.half; j += 16) {
     auto place = [&](int g, int chunk) {   // 16 bytes, lane % 8, of a chunk of row g
@@ -809,7 +809,7 @@ __device__ __forceinline__ void s_scale_q(const Fp4Params& p, Shared& sh, uint32
       // what `scaled` took out of the row, into its scores (never 0 or infinite, so that scores of -inf and 0 stay what they are)
       if (lane == 0) {
         const float back = __uint_as_float(((e[g] < 255u ? e[g] : 141u) - 14u) << 23);
-        sh.q_scale[w * blk.half + j + 4 * g] = fminf(fmaxf(unit * back, 0x1p-126f), FLT_MAX);
+        sh.q_scale[w * blk.half + j + 4 * g] = fminf(fmaxf(p.unit * back, 0x1p-126f), FLT_MAX);
       }
     }
     if (j + 4 * mine < blk.half) st_shared_v4(place(mine, 8), scaled(rope, rope_e));
@@ -1484,8 +1484,8 @@ mla_status_t decode_fp4_impl(const void* q, const uint8_t* kv_cache, float kv_sc
   if (indices && (!topk_lens || index_stride < 1 || !aligned(indices, 4) || !aligned(topk_lens, 4))) return MLA_ERR_INVALID_ARG;
   if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.f)) return MLA_ERR_INVALID_ARG;
   if (!std::isfinite(kv_scale) || !(kv_scale > 0.f) || !fp4_scale_ok(kv_scale)) return MLA_ERR_INVALID_ARG;
-  const double scale_log2 = static_cast<double>(softmax_scale) * 1.4426950408889634074;
-  if (!std::isnormal(static_cast<float>(scale_log2 * kv_scale))) return MLA_ERR_INVALID_ARG;
+  const float unit = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634074 * kv_scale);
+  if (!std::isnormal(unit)) return MLA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(s_q) * H > kMaxPairsPerCluster * kRowsPerPair || B > kScheduleMaxB) return MLA_ERR_UNSUPPORTED;
   if (num_blocks > ((int64_t(1) << 31) - kPageTokens) / kPageTokens) return MLA_ERR_UNSUPPORTED;
   const int rows = s_q * H;
@@ -1507,7 +1507,7 @@ mla_status_t decode_fp4_impl(const void* q, const uint8_t* kv_cache, float kv_sc
   p.H = H;
   p.rows = rows;
   p.n_rb = (rows + kRowsPerPair - 1) / kRowsPerPair;
-  p.scale_log2 = static_cast<float>(scale_log2);
+  p.unit = unit;
   p.causal = causal_s_q && s_q > 1 ? 1 : 0;   // (a single query position sees every token)
   p.kv_scale = kv_scale;
   p.meta = static_cast<const int32_t*>(metadata);

@@ -65,3 +65,17 @@ def test_scores_past_float32_are_not_empty_rows(topk, softmax_scale):
         assert torch.all(out[:, :, rest].isnan()), parts
         assert torch.all(lse[:, :, rest].isnan() | lse[:, :, rest].isposinf()), parts
         _compare(dict(inp, q=inp["q"][:, :, 3:4]), (out[:, :, 3:4], lse[:, :, 3:4]), want, f"parts={parts}")
+
+
+# --------------------------------------------------------------------------------------- scales --
+@pytest.mark.parametrize("topk", [None, [300, 64]])
+def test_a_softmax_scale_whose_log2_units_pass_float32(topk, softmax_scale):
+    """3e38 * log2(e) is past float32's range, its product with kv_scale is not: with rows of q of size 2^-116 and values of
+    size 2^-9 the scores come to some hundreds."""
+    inp = _case([400, 64], H=32, topk=topk, seed=73, values=lambda rng, pool: rng.normal(0, 2.0 ** -9, (pool, 64, 576)))
+    inp["q"] *= 2.0 ** -116
+    softmax_scale(3e38)
+    ref = _ref(inp)
+    assert np.all(np.abs(ref[2]) < 1000)
+    for parts in (1, 4):
+        _compare(inp, _run(inp, parts), ref, f"parts={parts}")
