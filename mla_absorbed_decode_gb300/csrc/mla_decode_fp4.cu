@@ -995,7 +995,7 @@ __device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int par
     if (t < 64) {
       const float sum = (sh.part[w][0][t] + sh.part[w][1][t]) + (sh.part[w][2][t] + sh.part[w][3][t]);
       const uint32_t inv = map_to_rank(smem + kOffInvL + ((seg - 1) % kInvSlots) * 512 + w * 256 + t * 4, peer);
-      st_cluster_u32(inv, __float_as_uint(sum == 0.f ? 0.f : __fdividef(p.kv_scale, sum)));
+      st_cluster_u32(inv, __float_as_uint(sum == 0.f ? 0.f : __fdividef(1.f, sum)));
       mbar_arrive_remote(map_to_rank(AT(inv_full) + 8 * ((seg - 1) % kInvSlots), peer));
       const int n = w * blk.half + t, g = blk.rb * kRowsPerPair + n;
       if (t < blk.half && n < blk.valid) {
@@ -1270,7 +1270,8 @@ __device__ void o_epilogue(const Fp4Params& p, Shared& sh, uint32_t smem, int pa
       const int x = 8 * j + (lane >> 2);
       return ld_shared_v4(stg + x * 64 + ((tq ^ ((x >> 1) & 3)) << 4));
     };
-    auto f = [&](uint32_t v) { return __uint_as_float(v) * inv_l; };
+    // kv_scale by itself: 2^-116 over a sum of up to 2^31 would be a subnormal factor with a bit or two
+    auto f = [&](uint32_t v) { return __uint_as_float(v) * inv_l * p.kv_scale; };
     auto emit = [&](int c, const uint32_t (&v)[32]) {
       if (final_out) {   // 32 bf16 columns: 64 B a row
 #pragma unroll

@@ -79,3 +79,26 @@ def test_a_softmax_scale_whose_log2_units_pass_float32(topk, softmax_scale):
     assert np.all(np.abs(ref[2]) < 1000)
     for parts in (1, 4):
         _compare(inp, _run(inp, parts), ref, f"parts={parts}")
+
+
+@pytest.mark.parametrize("kv_scale", [2.0 ** -116, 2.0 ** 115])
+@pytest.mark.parametrize("topk", [None, [32768]])
+def test_the_ends_of_kv_scale(topk, kv_scale, softmax_scale):
+    """A long context whose first tile sets references that the rest exceeds by almost what is allowed (7.9 of 8 in log2 units), so
+    that a row's sum of exponentials comes to 2^29, with the smallest and the largest scale of the cache."""
+    n, rope = 32768, 7.9 / (64 * SCALE * np.log2(np.e))
+
+    def values(rng, pool):
+        x = np.concatenate((1 + 0.1 * rng.normal(0, 1, (pool, 64, 512)), np.full((pool, 64, 64), rope)), axis=2)
+        return x
+    inp = _case([n], H=16, topk=topk, seed=74, values=values)
+    inp["q"][...] = 0.0
+    inp["q"][..., 512:] = 1.0
+    kv, table = inp["kv"].numpy(), inp["table"].numpy()[0]
+    for page in table[:2]:
+        kv[page, :, 288:] = 0                          # the first 128 tokens score 0
+    inp["kv_scale"] = kv_scale                          # (the bytes are those of 2^-6)
+    softmax_scale(SCALE * 2.0 ** -6 / kv_scale)
+    ref = _ref(inp)
+    for parts in (1, 5):
+        _compare(inp, _run(inp, parts), ref, f"parts={parts}")
