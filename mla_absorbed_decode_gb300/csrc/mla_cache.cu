@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 
@@ -61,9 +62,11 @@ __device__ __forceinline__ float quotient_for_rounding(Float2Sum v, Float2Sum d)
   if (!(rest != 0.f) || q == 0.f || !(fabsf(q) <= 3.4e38f)) return q;
   return __uint_as_float((__float_as_uint(q) - ((rest < 0.f) == (q > 0.f) ? 1u : 0u)) | 1u);
 }
-// x0 a + x1 b, the factors sums of two floats.
+// x0 a + x1 b, the factors sums of two floats.  One that is infinite (or passes float32's range) stays so: its low part, a difference
+// of infinities, is NaN.
 __device__ __forceinline__ Float2Sum dot2(float x0, Float2Sum a, float x1, Float2Sum b) {
   const Float2Sum s = add_exactly(times(x0, a), times(x1, b));
+  if (!(fabsf(s.hi) <= FLT_MAX)) return {s.hi, 0.f};
   const float hi = __fadd_rn(s.hi, s.lo);
   return {hi, __fsub_rn(s.lo, __fsub_rn(hi, s.hi))};
 }

@@ -102,3 +102,50 @@ def test_the_ends_of_kv_scale(topk, kv_scale, softmax_scale):
     ref = _ref(inp)
     for parts in (1, 5):
         _compare(inp, _run(inp, parts), ref, f"parts={parts}")
+
+
+# -------------------------------------------------------------------------------------- appends --
+def _append(rows, kv_scale, **more):
+    """The bytes [N, 352] that new rows of one request become."""
+    import mla_absorbed_decode_gb300 as mla
+    N = rows.shape[0]
+    blocks = (N + 63) // 64
+    kv = torch.full((blocks, 64, 352), 0x55, dtype=torch.uint8, device="cuda")
+    table = torch.arange(blocks, dtype=torch.int32, device="cuda").view(1, blocks)
+    d = rows.cuda()
+    mla.cache_append_fp4(d[:, :512], d[:, 512:], kv, kv_scale, table, torch.tensor([N], dtype=torch.int32, device="cuda"),
+                         **{k: v.cuda() if torch.is_tensor(v) else v for k, v in more.items()})
+    assert mla.get_device_status() == 0
+    return kv.view(-1, 352)[:N].cpu().numpy()
+
+
+@pytest.mark.parametrize("norm", [False, True])
+def test_infinities_of_k_pe_saturate_when_they_turn(norm):
+    """An infinite element, and pairs whose turned values pass float32's range, become +-448: never NaN but where an infinity is
+    taken from another."""
+    g = torch.Generator().manual_seed(75)
+    N, most = 64, float(torch.finfo(BF).max)
+    rows = torch.randn((N, 576), generator=g).to(BF)
+    pos = torch.randint(1, 131072, (N,), generator=g, dtype=torch.int32)
+    inf = float("inf")
+    odd = {0: (inf, None), 3: (None, -inf), 8: (-inf, None), 11: (inf, 0.0), 17: (most, most), 19: (most, -most), 24: (inf, most),
+           31: (-inf, inf)}
+    for j, pair in odd.items():
+        for i, v in enumerate(pair):
+            if v is not None:
+                rows[:, 512 + 2 * j + i] = v
+    got = _append(rows, 2.0 ** -6, positions=pos, norm_weight=torch.ones(512, dtype=BF) if norm else None)[:, 288:]
+    x = to_np(rows)[:, 512:]
+    for j in odd:
+        a = pos.numpy() * 10000.0 ** (-2.0 * j / 64)
+        with np.errstate(invalid="ignore"):
+            y0 = x[:, 2 * j] * np.cos(a) - x[:, 2 * j + 1] * np.sin(a)
+            y1 = x[:, 2 * j] * np.sin(a) + x[:, 2 * j + 1] * np.cos(a)
+        for i, y in enumerate((y0, y1)):
+            want = oracle.e4m3_round(y * 2.0 ** 6)
+            code = got[:, 2 * j + i]
+            none = np.isnan(y)
+            assert np.all((code[none] & 0x7F) == 0x7F), (j, i)
+            assert np.array_equal(code[~none], want[~none]), (j, i)
+    rest = np.setdiff1d(np.arange(64), [2 * j + i for j in odd for i in (0, 1)])
+    assert np.all((got[:, rest] & 0x7F) != 0x7F)
