@@ -317,12 +317,30 @@ __global__ void __launch_bounds__(128) mla_append_fp4_kernel(const __grid_consta
 #pragma unroll
   for (int i = 0; i < 8; ++i) y[2 * i] = bf16_lo(cw[i]), y[2 * i + 1] = bf16_hi(cw[i]);
   if constexpr (Norm) {
-    Float2Sum ss = {0.f, 0.f};
+    Float2Sum ss;
+    auto mean_square = [&](float eps) {   // of the warp's row, and eps (squares of bf16 are exact where they are normal)
+      ss = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 16; ++i) ss = add_exactly(ss, {__fmul_rn(y[i], y[i]), 0.f});   // (squares of bf16 are exact)
+      for (int i = 0; i < 16; ++i) ss = add_exactly(ss, {__fmul_rn(y[i], y[i]), 0.f});
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) ss = add_exactly(ss, {__shfl_xor_sync(0xffffffffu, ss.hi, o), __shfl_xor_sync(0xffffffffu, ss.lo, o)});
-    ss = add_exactly({ss.hi * (1.f / kDimV), ss.lo * (1.f / kDimV)}, {p.norm_eps, 0.f});
+      for (int o = 16; o >= 1; o >>= 1) ss = add_exactly(ss, {__shfl_xor_sync(0xffffffffu, ss.hi, o), __shfl_xor_sync(0xffffffffu, ss.lo, o)});
+      ss = add_exactly({ss.hi * (1.f / kDimV), ss.lo * (1.f / kDimV)}, {eps, 0.f});
+    };
+    mean_square(p.norm_eps);
+    if (!(ss.hi >= 0x1p-80f && ss.hi <= 0x1p120f)) {
+      // Squares that float32 has no room for (all lanes agree): the row, and eps with it, by a power of two that brings the larger of
+      // the row's largest element and sqrt(eps) to [1, 4), and the same result.  Not for rows of zeros, or with an infinity or NaN.
+      uint32_t top = __float_as_uint(sqrtf(p.norm_eps));
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+      top = __reduce_max_sync(0xffffffffu, top);
+      if (top > 0u && top < 0x7F800000u) {
+        const float by = __uint_as_float((254u - min(top >> 23, 253u)) << 23);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] *= by;
+        mean_square(p.norm_eps * by * by);
+      }
+    }
     // its inverse root: an approximation and one step of Newton's method for the rest, then a power of two times a number in [1, 2)
     const float r = rsqrtf(ss.hi);
     const Float2Sum rr = times(r, {r, 0.f}), one = times(ss.hi, rr);

@@ -149,3 +149,42 @@ def test_infinities_of_k_pe_saturate_when_they_turn(norm):
             assert np.array_equal(code[~none], want[~none]), (j, i)
     rest = np.setdiff1d(np.arange(64), [2 * j + i for j in odd for i in (0, 1)])
     assert np.all((got[:, rest] & 0x7F) != 0x7F)
+
+
+@pytest.mark.parametrize("eps,sizes", [(0.0, (-120, -100, -70, -64, -40, 0, 58, 63, 100, 120)), (1e-6, (0, 20, 59, 63, 100, 120)),
+                                        (1e-30, (-60, -50, -40, 0, 63, 120)), (1e30, (40, 50, 63, 100))])
+def test_norms_of_rows_of_any_size(eps, sizes):
+    """Rows whose squares, or their sum, float32 has no room for: the codes of 64 bits, as for rows of size one (those of a value
+    that lies within 2^-40 of itself of a halfway point might differ: expected 1e-6 of them)."""
+    g = torch.Generator().manual_seed(76)
+    rows = torch.randn((8 * len(sizes), 576), generator=g)
+    rows[:, :512] *= torch.tensor([2.0 ** s for s in sizes]).repeat_interleave(8)[:, None]
+    rows[::8, 5:300] = 0.0
+    rows[1::8, 7] *= 16.0
+    rows = rows.to(BF)
+    w = (1 + 0.3 * torch.randn(512, generator=g)).to(BF)
+    for kv_scale in (2.0 ** -6, 0.013):
+        got = _append(rows, kv_scale, norm_weight=w, norm_eps=eps)
+        x = to_np(rows)
+        x = np.concatenate((oracle.normed_latent(x[:, :512], to_np(w), float(np.float32(eps))), x[:, 512:]), axis=1)
+        want = oracle.pack_fp4(x, kv_scale)
+        bad = np.nonzero((got != want).any(axis=1))[0]
+        assert bad.size == 0, [sizes[r // 8] for r in bad]
+
+
+def test_norms_of_rows_that_have_none():
+    """A row of zeros stays one of zeros, or becomes NaN where eps is 0 too (0 times infinity); a NaN makes its row NaN, an infinity
+    its group, and the rest of its row 0."""
+    rows = torch.randn((5, 576), generator=torch.Generator().manual_seed(77)).to(BF)
+    rows[0, :512] = 0.0
+    rows[1, 100] = float("nan")
+    rows[2, 200] = float("-inf")
+    rows[3, 0], rows[3, 511] = float("inf"), float("nan")
+    w = torch.ones(512, dtype=BF)
+    for eps, zeros_are in ((1e-6, 0), (1e-45, 0), (0.0, 0x7F)):
+        got = _append(rows, 2.0 ** -6, norm_weight=w, norm_eps=eps)
+        assert np.all(got[0, :256] == 0) and np.all(got[0, 256:288] == zeros_are)
+        assert np.all(got[1, 256:288] == 0x7F) and np.all(got[3, 256:288] == 0x7F)
+        scales = got[2, 256:288]
+        assert scales[200 // 16] == 0x7F and np.all(np.delete(scales, 200 // 16) == 0)      # finite / infinite is 0
+        assert np.all((got[4, 256:288] & 0x7F) != 0x7F)
