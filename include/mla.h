@@ -407,8 +407,8 @@ mla_status_t mla_cache_append_fp8(const mla_bf16_t* c, int64_t c_row_stride, con
  *   scale = E4M3(max |y| over the 16 dims of a group / (6 kv_scale))
  *   code  = E2M1(y / (scale kv_scale))          (0 in a group whose scale is 0 or NaN)
  *   rope  = E4M3(turned k_pe / kv_scale)
- * every rounding to nearest even and saturating (infinities too), of values known to more than float32's 24 bits
- * (positions below 2^17; the rotation is within 2^-19 of the pair's norm up to 2^24).  A group with a NaN gets a NaN
+ * every rounding to nearest even and saturating (infinities too), of values known to more than float32's 24 bits; a
+ * turned value is within 2^-25 of its pair's norm (positions below 2^17; 2^-21 up to 2^24).  A group with a NaN gets a NaN
  * scale, so that its values read as NaN.
  *  kv_cache     [num_blocks, 64, 352] bytes, 16-byte aligned (the decodes read it 32-byte aligned)
  *  kv_scale     as for mla_decode_fp4

@@ -70,20 +70,27 @@ __device__ __forceinline__ Float2Sum dot2(float x0, Float2Sum a, float x1, Float
   const float hi = __fadd_rn(s.hi, s.lo);
   return {hi, __fsub_rn(s.lo, __fsub_rn(hi, s.hi))};
 }
-// The pair (x0, x1) turned by the angle pos * (hi + lo), for codes: a value is off by about 2^-26 of the pair's norm (positions
-// below 2^17; 2^-19 up to 2^24), where rope_turn's hardware sine, off by 2^-21, would move many times as many codes that lie
-// halfway.  The angle less k quarter turns (pi / 2 in three floats, products with their rounding errors) is a pair of floats in
-// [-pi / 4, pi / 4], its sine and cosine are Taylor polynomials whose leading terms are added up exactly.
+// The pair (x0, x1) turned by the angle pos * (hi + lo), for codes: a value is off by 2^-25.5 of the pair's norm at most (positions
+// below 2^17; 2^-21.8 up to 2^24, where half an ulp of the angle is 2^-1 and its low part carries 2^-25), where rope_turn's hardware
+// sine, off by 2^-21, would move many times as many codes that lie halfway.  The angle less k quarter turns (pi / 2 in three floats,
+// products with their rounding errors) is a pair of floats in [-pi / 4, pi / 4] or a little more, its sine and cosine are Taylor
+// polynomials whose leading terms are added up exactly.
 __device__ __forceinline__ void rope_turned(float hi, float lo, int pos, float x0, float x1, Float2Sum (&y)[2]) {
   constexpr float kQuarter1 = 0x1.921fb6p+0f, kQuarter2 = -0x1.777a5cp-25f, kQuarter3 = -0x1.ee59dap-50f;
   const float fp = static_cast<float>(pos);
   const float a = __fmul_rn(fp, hi), b = fmaf(fp, lo, fmaf(fp, hi, -a));
-  const float k = rintf(__fmul_rn(a, 0.636619772f));
+  float k = rintf(__fmul_rn(a, 0.636619772f));
   const float p1 = __fmul_rn(k, kQuarter1), p2 = __fmul_rn(k, kQuarter2);
   const float t = __fsub_rn(a, p1), u = __fsub_rn(t, p2), v = __fsub_rn(u, t);
   const float e = __fadd_rn(__fsub_rn(t, __fsub_rn(u, v)), __fsub_rn(-p2, v));   // (t - p2) - u
   const float l = e + ((b - fmaf(k, kQuarter1, -p1)) - fmaf(k, kQuarter3, fmaf(k, kQuarter2, -p2)));
-  const float r = __fadd_rn(u, l), rl = __fsub_rn(l, __fsub_rn(r, u));
+  float r = __fadd_rn(u, l), rl = __fsub_rn(l, __fsub_rn(r, u));
+  if (fabsf(r) > 1.f) {   // past 2^21 k comes out short by up to 1.1 quarter turns, too far for the polynomials (2^-18.4 at an angle of 2.4)
+    const float more = rintf(__fmul_rn(r, 0.636619772f)), w = fmaf(-more, kQuarter1, r), rest = fmaf(-more, kQuarter2, rl);
+    k += more;
+    r = __fadd_rn(w, rest);
+    rl = __fsub_rn(rest, __fsub_rn(r, w));
+  }
   const float z = __fmul_rn(r, r), zl = fmaf(r, r, -z) + 2.f * r * rl;
   const float s1 = r * z * fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, 1.f / 6227020800.f, -1.f / 39916800.f), 1.f / 362880.f), -1.f / 5040.f),
                                         1.f / 120.f), -1.f / 6.f);

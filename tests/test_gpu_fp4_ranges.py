@@ -188,3 +188,79 @@ def test_norms_of_rows_that_have_none():
         scales = got[2, 256:288]
         assert scales[200 // 16] == 0x7F and np.all(np.delete(scales, 200 // 16) == 0)      # finite / infinite is 0
         assert np.all((got[4, 256:288] & 0x7F) != 0x7F)
+
+
+def _quarter_turns(top):
+    """Positions at which pair 0, which turns by one radian a position, is nearest to a quarter turn: denominators of fractions close
+    to 2 / pi, and their neighbours."""
+    p = np.arange(1, top, dtype=np.float64)
+    off = np.abs(p * (2 / np.pi) - np.rint(p * (2 / np.pi)))
+    return p[np.argsort(off)[:400]].astype(np.int64)
+
+
+@pytest.mark.parametrize("theta", [10000.0, 500000.0])
+@pytest.mark.parametrize("low,top,bits", [(0, 2 ** 17, 25), (2 ** 17, 2 ** 24, 21)])
+@pytest.mark.parametrize("kv_scale", [2.0 ** -6, 0.013])
+def test_rope_codes_of_turned_pairs(low, top, bits, theta, kv_scale):
+    """Codes of values off by at most 2^-bits of their pair's norm: each lies between the codes of the 64-bit value less and plus that.
+    (A sine off by 2^-21 would put some 2^-21 / 2^-5 of 2.1 million values, a hundred, past the first bound.)"""
+    g = torch.Generator().manual_seed(78)
+    N = 32768
+    rows = torch.randn((N, 576), generator=g).to(BF)
+    pos = torch.randint(low, top, (N,), generator=g, dtype=torch.int32)
+    pos[::3] *= -1
+    if low == 0:
+        pos[:400] = torch.from_numpy(_quarter_turns(top)).int()
+        pos[400:410] = torch.tensor([0, 1, -1, 2, 11, 355, -355, 710, top - 1, 1 - top])
+    else:
+        pos[:4000] = torch.arange(top - 4000, top)
+        pos[4000:8000] = torch.arange(-(top - 1), -(top - 1) + 4000)
+    got = _append(rows, kv_scale, positions=pos, rope_theta=theta)[:, 288:]
+    x = to_np(rows)[:, 512:]
+    y = oracle.rope_axes(x[:, None], pos.numpy()[None], (32,), base=theta)[:, 0]
+    room = 2.0 ** -bits * np.repeat(np.hypot(x[:, 0::2], x[:, 1::2]), 2, axis=1)
+    unit = float(np.float32(kv_scale))
+    value = lambda code: oracle.dequantize_e4m3(code, 1.0)
+    code = value(got)
+    low_end, high_end = value(oracle.e4m3_round((y - room) / unit)), value(oracle.e4m3_round((y + room) / unit))
+    bad = (code < low_end) | (code > high_end)
+    assert not bad.any(), (int(bad.sum()), pos.numpy()[np.nonzero(bad)[0][:5]].tolist())
+
+
+def _next_to_halfway(pos, pair, theta, unit, room):
+    """(positions, first elements in [1, 2), their second is 0) for which the first or the second turned value lies between room and
+    8 room from halfway between two codes, relative to the pair's norm."""
+    x0 = 1 + np.arange(128) / 128
+    p, x = [], []
+    for part in np.array_split(pos, max(1, pos.size >> 16)):
+        a = part * theta ** (-2.0 * pair / 64)
+        for turned in (np.cos(a), np.sin(a)):
+            v = np.abs(turned[:, None] * x0) / unit
+            step = 2.0 ** (np.floor(np.log2(v)) - 3)
+            off = np.abs(v / step - np.floor(v / step) - 0.5) * step * unit / x0
+            i, k = np.nonzero((v > 2.0 ** -5) & (v < 440) & (off > room) & (off < 8 * room))
+            p.append(part[i])
+            x.append(x0[k])
+    return np.concatenate(p), np.concatenate(x)
+
+
+@pytest.mark.parametrize("low,top,bits", [(1, 2 ** 17, 25), (2 ** 24 - 2 ** 18, 2 ** 24, 21)])
+@pytest.mark.parametrize("pair,theta", [(0, 10000.0), (1, 500000.0), (5, 10000.0), (30, 10000.0)])
+def test_rope_codes_next_to_halfway(pair, theta, low, top, bits):
+    """Turned values that lie just further than the stated error from halfway between two codes: none may get the wrong one."""
+    kv_scale = 2.0 ** -6
+    p, x = _next_to_halfway(np.arange(low, top), pair, theta, kv_scale, 2.0 ** -bits)
+    keep = np.random.default_rng(79).permutation(p.size)[:65536]
+    p, x = p[keep], x[keep]
+    assert p.size > 50
+    rows = torch.zeros((p.size, 576))
+    rows[:, 512 + 2 * pair] = torch.from_numpy(x).float()
+    got = _append(rows.to(BF), kv_scale, positions=torch.from_numpy(p).int(), rope_theta=theta)
+    y = oracle.rope_axes(to_np(rows)[:, None, 512:], p[None], (32,), base=theta)[:, 0, 2 * pair:2 * pair + 2]
+    # The one of the two values that the row was picked for lies further than the error from halfway: one code is allowed.  The other may
+    # lie nearer (of 33181 rows two do: at 16775432 and 16701101, by 2^-27 and 2^-28.5 of the norm), and has two.
+    low_end, high_end = (oracle.dequantize_e4m3(oracle.e4m3_round((y + d * 2.0 ** -bits * x[:, None]) / kv_scale), 1.0) for d in (-1, 1))
+    assert np.all((low_end == high_end).any(axis=1))
+    code = oracle.dequantize_e4m3(got[:, 288 + 2 * pair:290 + 2 * pair], 1.0)
+    bad = np.nonzero(((code < low_end) | (code > high_end)).any(axis=1))[0]
+    assert bad.size == 0, (bad.size, p.size, p[bad[:5]].tolist())
