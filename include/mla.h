@@ -179,7 +179,8 @@ mla_status_t mla_decode_sparse_fp8(const mla_bf16_t* q, const uint8_t* kv_cache,
  *  kv_scale  one scale for the whole cache, in [2^-116, 2^115], and softmax_scale * kv_scale * log2(e) a normal
  *            float32 (else MLA_ERR_INVALID_ARG)
  * The attention is that of mla_decode over these values; q stays bf16.  A row with a score past float32's
- * range comes out as NaN, its lse as NaN or +inf.  Other arguments, results and
+ * range comes out as NaN, its lse as NaN or +inf; a NaN in a cached token reaches the rows that see the token, and
+ * no others.  Other arguments, results and
  * errors as for mla_decode, but B up to 16384 (more: MLA_ERR_UNSUPPORTED).  Async on stream. */
 mla_status_t mla_decode_fp4(const mla_bf16_t* q, const uint8_t* kv_cache, float kv_scale, int64_t num_blocks,
                             const int32_t* block_table, int max_blocks, const int32_t* seqlens, int B, int s_q, int H,

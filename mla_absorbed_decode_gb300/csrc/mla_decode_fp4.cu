@@ -337,6 +337,12 @@ __device__ __forceinline__ void values16(uint32_t w0, uint32_t w1, uint32_t scal
   v[7] = mul_f16x2(e2m1x2_to_f16x2<3>(w1), scale);
 }
 
+// Four E4M3 scales, 0 in place of NaN: a row that sees the token is NaN by its score, and a row that does not (P = 0) stays clean.
+__device__ __forceinline__ uint32_t without_nan(uint32_t scales) {
+  const uint32_t nan = ((scales & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+  return scales & ~(nan | (nan - (nan >> 7)));
+}
+
 // ------------------------------------------------------------------- walk --
 struct Segment {
   int b, kb, ke, split;   // request, page range, split index within the request
@@ -1057,7 +1063,7 @@ __device__ void o_convert(const Fp4Params& p, uint32_t smem) {
       for (int c = 0; c < 2; ++c) {
         uint32_t x[32];
         if (r < n) {
-          const uint32_t s01 = e4m3x2_to_f16x2<0>(scale[c]), s23 = e4m3x2_to_f16x2<1>(scale[c]);
+          const uint32_t sc = without_nan(scale[c]), s01 = e4m3x2_to_f16x2<0>(sc), s23 = e4m3x2_to_f16x2<1>(sc);
           values16(code[c][0].x, code[c][0].y, __byte_perm(s01, 0, 0x1010), x);
           values16(code[c][0].z, code[c][0].w, __byte_perm(s01, 0, 0x3232), x + 8);
           values16(code[c][1].x, code[c][1].y, __byte_perm(s23, 0, 0x1010), x + 16);

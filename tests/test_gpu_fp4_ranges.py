@@ -264,3 +264,25 @@ def test_rope_codes_next_to_halfway(pair, theta, low, top, bits):
     code = oracle.dequantize_e4m3(got[:, 288 + 2 * pair:290 + 2 * pair], 1.0)
     bad = np.nonzero(((code < low_end) | (code > high_end)).any(axis=1))[0]
     assert bad.size == 0, (bad.size, p.size, p[bad[:5]].tolist())
+
+
+# ----------------------------------------------------------------------------------------- masks --
+@pytest.mark.parametrize("s_q,H", [(2, 128), (3, 16), (4, 128)])
+@pytest.mark.parametrize("code", [0x7F, 0xFF])
+def test_a_nan_that_a_query_position_does_not_see(s_q, H, code):
+    """The newest tokens of a request with NaN in a scale or in the RoPE key: the query positions before them are what they were, the
+    others are NaN; dense and over lists."""
+    n = [300, 65, 513]
+    for topk in (None, [300, 40, 257]):
+        inp = _case(n, s_q=s_q, H=H, topk=topk, seed=80)
+        if topk:
+            for b in range(3):      # the newest tokens are on the lists
+                inp["indices"][b, :s_q] = torch.arange(n[b] - s_q, n[b])
+        dirty = dict(inp, kv=inp["kv"].clone())
+        for b, byte in enumerate((256 + 3, 288 + 20, 256 + 31)):
+            t = n[b] - 1
+            dirty["kv"][int(inp["table"][b, t // 64]), t % 64, byte] = code
+        for parts in (1, 4):
+            clean, got = _run(inp, parts), _run(dirty, parts)
+            assert torch.equal(got[0][:, : s_q - 1], clean[0][:, : s_q - 1]) and torch.equal(got[1][:, : s_q - 1], clean[1][:, : s_q - 1])
+            assert torch.all(got[0][:, -1].isnan()) and torch.all(got[1][:, -1].isnan())
