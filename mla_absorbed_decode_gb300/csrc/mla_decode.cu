@@ -1200,7 +1200,7 @@ __device__ void o_cta_forwarder(const DecodeParams& p, Shared& sh, int part, uin
       if (T == 0) continue;
       const uint32_t ps = (T - 1) % kSlots, pph = ((T - 1) / kSlots) & 1;
       if (!wait_bar(sh, smem_u32(&sh.bar.p_free[ps]), pph, p.status, cl)) { ok = false; break; }
-      mbar_arrive_remote(credit0 + ps * 8);
+      mbar_arrive_other(credit0 + ps * 8);   // (with a release to the cluster 64 x 2 x 8192 took 283 us instead of 261)
     }
   }
 }
