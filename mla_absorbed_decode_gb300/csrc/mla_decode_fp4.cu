@@ -18,12 +18,14 @@
 //     and accumulates O += P V, P^T and V both read by the MMA as they lie (tokens by rows: transposed operands).
 // Rows past 128 go to further pairs of the cluster, which walk the same pages.  A cluster is one part of the split schedule.
 //
-// Measured (GB300, 1.9 GHz; call with its merge, q and cache from HBM): 64 x 4096 tokens, 128 heads 81.6 us (895 TFLOP/s, 0.46 of a
-// library's bf16 product), 16 heads 70 us; 64 x 2 x 8192: 263 us (1110 TFLOP/s); 4 x 131072: 194 us; 64 lists of 2048 tokens: 65 us;
-// 2 x 300 tokens, 16 heads: 16 us.  A tile takes a pair 3800 cycles, of which S's MMAs are 2304 and O's 2048: what is between are the
-// waits of chains (keys converted -> MMA -> exponentials -> vote -> copy -> MMA) whose links take 100 to 300 cycles each however little
-// they do, with 20 warps on an SM that issue 0.57 of the time; TMEM, where MMAs without gaps hold up the others' loads and stores; and the
-// O-CTA's shared memory (V written once and read by the MMAs with P: 2800 cycles at 128 bytes each).
+// Measured (GB300, 1.9 GHz; call with its merge, q and cache from HBM): 64 x 4096 tokens, 128 heads 83.9 us (870 TFLOP/s, 0.45 of a
+// library's bf16 product), 16 heads 72 us; 64 x 2 x 8192: 267 us (1094 TFLOP/s); 4 x 131072: 136 us (202 us with 1% of the tokens eight
+// times as large, whose references move); 64 lists of 2048 tokens: 66 us; 2 x 300 tokens, 16 heads: 16 us.  A tile takes a pair some
+// 3900 cycles, of which S's MMAs are 2304 and O's 2048: what is between are the
+// waits of chains (keys converted -> MMA -> exponentials -> vote -> copy -> landed -> MMA) whose links take 100 to 300 cycles each however
+// little they do (the last packet's landing 400 to 800), with 20 warps on an SM that issue 0.59 of the time; TMEM, where MMAs without gaps
+// hold up the others' loads and stores; and the O-CTA's shared memory (V written once and read by the MMAs with P: 2800 cycles at 128
+// bytes each).
 //
 // The softmax is online, with the reference maximum of a head raised only where a score passes it by 2^8: the threads take the
 // exponentials against the old reference, and a vote (the barrier that ends a tile) tells whether one overflowed its room;
@@ -197,13 +199,13 @@ template <int R>
 __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(R)); }
 template <int R>
 __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(R)); }
-// `bytes` (a multiple of 16, both addresses 16-byte aligned) of global memory into shared memory.
 // 32 aligned bytes.
 __device__ __forceinline__ void load32(const void* at, uint4& a, uint4& b) {
   asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
       : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w) : "l"(at));
 }
 __device__ __forceinline__ void prefetch_line(const void* at) { asm volatile("prefetch.global.L2 [%0];" :: "l"(at) : "memory"); }
+// `bytes` (a multiple of 16, both addresses 16-byte aligned) of global memory into shared memory.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
@@ -875,7 +877,7 @@ __device__ void s_softmax(const Fp4Params& p, Shared& sh, uint32_t smem, int par
       __syncwarp();
       tc_fence_after();
       if (masked) {
-        if (Sparse && (key < 0 || key >= L_seq)) key = INT_MAX;   // (a bad entry is reported by the loads, and seen by nobody)
+        if (Sparse && (key < 0 || key >= L_seq)) key = INT_MAX;   // (a bad entry is reported by the loads; the result is undefined)
 #pragma unroll 1
         for (int c = 0; c < blk.half; c += 8) {
           uint32_t x[8];
